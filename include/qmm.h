@@ -517,6 +517,100 @@ qmm_status qmm_w8_dequant_packed(const void* A, int64_t M, int64_t K, int64_t N,
                                  const int32_t* zero_point, int64_t zp_count, void* C, int c_dtype, void* workspace,
                                  size_t workspace_bytes, void* stream);
 
+/*
+ * RMS norm with the residual's addition and an int8 output with one scale per
+ * row: the A and act_scale that qmm_a8w8 takes. One row of H elements:
+ *   h     = T(x + residual)           (T: x's type; without a residual h = x)
+ *   v     = h * w;   a = max |v|
+ *   rstd  = 1 / sqrt(mean(h^2) + eps)
+ *   q     = rne(v * (127 / a));       scale = a * rstd / 127
+ * each step fp32, so q * scale stands for the normalised row h * rstd * w
+ * within half a step; rstd cancels out of q. A row with a below 2^-100 is a row
+ * of zeros: q = 0 and scale 1; a row whose v holds a NaN or an infinity gets
+ * q = 0 and scale NaN.
+ *
+ *  x             [M] rows of H, x_dtype QMM_F32 or QMM_BF16, ldx >= H elements
+ *                between rows
+ *  residual      the same type, ldr elements between rows, or NULL
+ *  w             [H], w_dtype QMM_F32 or QMM_BF16
+ *  h             [M,H] of x's type, contiguous: receives x + residual (may be
+ *                NULL: not stored; may be x or residual where those are
+ *                contiguous: a row is read before it is written)
+ *  q             [M,H] int8;  scale, rstd  float[M] (rstd is what the gradient
+ *                takes)
+ * s8_dequantize_rows reads such rows back: y[m,i] = y_dtype(q[m,i] * scale[m]).
+ *
+ * The gradient, with the quantiser passed straight through (the gradient of
+ * h * rstd * w): n = h * rstd, g = dy * w,
+ *   dx[m]   = rstd * (g - n * mean(g * n)) (+ dh[m]);   dweight = sum_m dy * n
+ *  dy, h, dh     [M] rows of H of `dtype` (QMM_F32 or QMM_BF16); dh, the
+ *                gradient that reaches h past the norm, may be NULL. dx is the
+ *                gradient of x and of the residual alike.
+ *  dx            [M,H] of dtype, contiguous (may be dy or dh where contiguous)
+ *  dweight       float[H]; the sum over rows runs in a fixed order
+ *  workspace     qmm_rms_norm_backward_workspace_bytes(M, H) bytes, 16-byte aligned
+ * M = 0 launches nothing but a zero fill of dweight; H = 0 launches nothing.
+ */
+qmm_status qmm_rms_norm_s8(const void* x, int x_dtype, int64_t M, int64_t H, int64_t ldx, const void* residual,
+                           int64_t ldr, const void* w, int w_dtype, float eps, void* h, int8_t* q, float* scale,
+                           float* rstd, void* stream);
+qmm_status qmm_s8_dequantize_rows(const int8_t* q, const float* scale, int64_t M, int64_t H, void* y, int y_dtype,
+                                  void* stream);
+size_t qmm_rms_norm_backward_workspace_bytes(int64_t M, int64_t H);
+qmm_status qmm_rms_norm_backward(const void* dy, int64_t lddy, const void* h, int64_t ldh, const void* dh,
+                                 int64_t lddh, int dtype, int64_t M, int64_t H, const void* w, int w_dtype,
+                                 const float* rstd, void* dx, float* dweight, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/*
+ * 4-bit floats with block scales: e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives; nearest, ties to the even code, beyond 6 to 6), consecutive
+ * elements of a row sharing a scale:
+ *   block 32   scale 2^(floor(log2 b) - 2), at least 2^-127, b the block's
+ *              largest magnitude (MXFP4 of the OCP Microscaling Formats
+ *              specification); codes e2m1(x / scale)
+ *   block 16   an e4m3 scale under a float32 scale per row: g = rowmax / 2688
+ *              (1 where that is below 2^-100), u = 1 / g, s = e4m3(b * u / 6),
+ *              codes e2m1(x * (u / s))
+ * A block (32) or a row (16) that holds a NaN or an infinity gets a NaN scale,
+ * so that what is computed from it is NaN.
+ *
+ * A packed matrix is one caller-owned buffer of qmm_fp4_bytes(rows, cols,
+ * block) bytes (0: unsupported), 16-byte aligned: codes, scales and row scales
+ * in the order the tensor cores take them, rows and columns padded to 128. It
+ * is meant to be made by these calls; a weight is packed once and kept.
+ *
+ *  qmm_fp4_quantize       x (x_dtype QMM_F32 or QMM_BF16), stored as [rows]
+ *                         rows of cols elements ldx apart, to packed
+ *                         [rows,cols]; with trans = 1, x is stored as [cols]
+ *                         rows of `rows` elements (its transpose is packed, the
+ *                         blocks running down x's columns)
+ *  qmm_fp4_quantize_both  one read of x [rows,cols] to packed [rows,cols] and
+ *                         packed_t [cols,rows]
+ *  qmm_fp4_dequantize     y [rows,cols] contiguous, y_dtype QMM_F32 or QMM_BF16:
+ *                         y_dtype((code * s) * g)
+ *  qmm_fp4_matmul         C[m,n] = c_dtype(((sum_k a*sa * b*sb) * ga[m]) * gb[n]),
+ *                         A packed [M,K], B packed [N,K] of the same block, C [M,N]
+ *                         contiguous, QMM_F32 or QMM_BF16; one fp32 accumulation
+ *                         over K (split over CTAs and joined in a fixed order for
+ *                         small M). With operands packed along the right axes it
+ *                         is a linear layer's forward (x, w), input gradient
+ *                         (dy, w transposed) and weight gradient (dy and x
+ *                         transposed) alike.
+ * K = 0 gives zeros; M = 0 or N = 0 launches nothing. QMM_ERR_INVALID_ARG for a
+ * bad block, dtype, stride, null or unaligned pointer or short buffer.
+ */
+size_t qmm_fp4_bytes(int64_t rows, int64_t cols, int block);
+qmm_status qmm_fp4_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, int trans, int block,
+                            void* packed, size_t packed_bytes, void* stream);
+qmm_status qmm_fp4_quantize_both(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, int block,
+                                 void* packed, size_t packed_bytes, void* packed_t, size_t packed_t_bytes,
+                                 void* stream);
+qmm_status qmm_fp4_dequantize(const void* packed, size_t packed_bytes, int64_t rows, int64_t cols, int block, void* y,
+                              int y_dtype, void* stream);
+qmm_status qmm_fp4_matmul(const void* a_packed, size_t a_bytes, int64_t M, const void* b_packed, size_t b_bytes,
+                          int64_t N, int64_t K, int block, void* C, int c_dtype, void* stream);
+
 /* Human-readable name of a status. Never NULL. */
 const char* qmm_status_string(int status);
 

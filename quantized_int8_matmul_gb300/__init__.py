@@ -105,6 +105,21 @@ def _load() -> ctypes.CDLL:
     lib.qmm_w8_dequant_packed_workspace_bytes.restype = sz
     lib.qmm_w8_dequant_packed.argtypes = [vp, i64, i64, i64, vp, sz, vp, i64, vp, i64, vp, ci, vp, sz, vp]
     lib.qmm_w8_dequant_packed.restype = ci
+    cf = ctypes.c_float
+    lib.qmm_rms_norm_s8.argtypes = [vp, ci, i64, i64, i64, vp, i64, vp, ci, cf, vp, vp, vp, vp, vp]
+    lib.qmm_s8_dequantize_rows.argtypes = [vp, vp, i64, i64, vp, ci, vp]
+    lib.qmm_rms_norm_backward_workspace_bytes.argtypes = [i64, i64]
+    lib.qmm_rms_norm_backward_workspace_bytes.restype = sz
+    lib.qmm_rms_norm_backward.argtypes = [vp, i64, vp, i64, vp, i64, ci, i64, i64, vp, ci, vp, vp, vp, vp, sz, vp]
+    lib.qmm_fp4_bytes.argtypes = [i64, i64, ci]
+    lib.qmm_fp4_bytes.restype = sz
+    lib.qmm_fp4_quantize.argtypes = [vp, ci, i64, i64, i64, ci, ci, vp, sz, vp]
+    lib.qmm_fp4_quantize_both.argtypes = [vp, ci, i64, i64, i64, ci, vp, sz, vp, sz, vp]
+    lib.qmm_fp4_dequantize.argtypes = [vp, sz, i64, i64, ci, vp, ci, vp]
+    lib.qmm_fp4_matmul.argtypes = [vp, sz, i64, vp, sz, i64, i64, ci, vp, ci, vp]
+    for fn in ("qmm_rms_norm_s8", "qmm_s8_dequantize_rows", "qmm_rms_norm_backward", "qmm_fp4_quantize",
+               "qmm_fp4_quantize_both", "qmm_fp4_dequantize", "qmm_fp4_matmul"):
+        getattr(lib, fn).restype = ci
     lib.qmm_int8_mma_peak_launch.argtypes = [ci, ctypes.POINTER(ctypes.c_double), vp]
     lib.qmm_int8_mma_peak_launch.restype = ci
     return lib
@@ -683,6 +698,207 @@ def dynamic_quantize_linear(x, row_len=None, workspace=None, y=None, stream=None
     return y, y_scale, y_zp
 
 
+def _need_rows(t, dtypes, name, shape=None):
+    """A 2-D CUDA tensor whose rows are contiguous (any row stride >= its width);
+    returns the row stride in elements."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}")
+    rows, cols = t.shape
+    if rows <= 1 or cols == 0:      # the row stride is never used
+        if cols > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name}: rows must be contiguous")
+        return cols
+    if (cols > 1 and t.stride(1) != 1) or t.stride(0) < cols:
+        raise ValueError(f"{name}: rows must be contiguous and not overlap")
+    return t.stride(0)
+
+
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
+def _need_out(t, dtypes, name, shape):
+    _need(t, dtypes, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}")
+
+
+class RmsNormS8(NamedTuple):
+    """qmm_rms_norm_s8's outputs: the int8 rows and their scales (A and act_scale
+    of qmm_a8w8), the sum x + residual (x itself without a residual) and the
+    reciprocal root mean square, which qmm_rms_norm_backward takes."""
+    q: torch.Tensor
+    scale: torch.Tensor
+    h: torch.Tensor
+    rstd: torch.Tensor
+
+
+def qmm_rms_norm_s8(x, weight, residual=None, eps=1e-6, out=None, h_out=None, stream=None) -> RmsNormS8:
+    """h = x + residual (rounded to x's type), then h / rms(h) * weight as int8
+    rows with one float32 scale each: q = rne(v * (127 / max|v|)), v = h * weight.
+
+    x (and residual) float32 or bfloat16 [M, H], rows contiguous at any stride;
+    weight float32 or bfloat16 [H]. out: int8 [M, H]; h_out: [M, H] of x's type,
+    may be x or residual itself. A row that holds a NaN or an infinity gets a NaN
+    scale."""
+    ldx = _need_rows(x, _FLOATS, "x")
+    M, H = x.shape
+    _need_out(weight, _FLOATS, "weight", (H,))
+    ldr = H
+    if residual is not None:
+        ldr = _need_rows(residual, (x.dtype,), "residual", (M, H))
+    if out is None:
+        out = torch.empty((M, H), dtype=torch.int8, device=x.device)
+    _need_out(out, (torch.int8,), "out", (M, H))
+    if residual is None:
+        if h_out is not None:
+            raise ValueError("h_out without a residual: h is x")
+        h = x
+    else:
+        h = torch.empty((M, H), dtype=x.dtype, device=x.device) if h_out is None else h_out
+        _need_out(h, (x.dtype,), "h_out", (M, H))
+    stats = torch.empty((2, M), dtype=torch.float32, device=x.device)
+    scale, rstd = stats[0], stats[1]
+    st = _lib.qmm_rms_norm_s8(_ptr(x), _TORCH_TO_QMM[x.dtype], M, H, ldx, _ptr(residual), ldr, _ptr(weight),
+                              _TORCH_TO_QMM[weight.dtype], float(eps), None if residual is None else _ptr(h),
+                              _ptr(out), _ptr(scale), _ptr(rstd), _stream(stream))
+    _check("qmm_rms_norm_s8", st)
+    return RmsNormS8(out, scale, h, rstd)
+
+
+def qmm_s8_dequantize_rows(q, scale, out=None, out_dtype=torch.bfloat16, stream=None):
+    """int8 rows read back: out[m, i] = q[m, i] * scale[m], float32 or bfloat16."""
+    _need(q, (torch.int8,), "q")
+    if q.dim() != 2:
+        raise ValueError("q must be 2-D")
+    M, H = q.shape
+    _need_out(scale, (torch.float32,), "scale", (M,))
+    if out is None:
+        out = torch.empty((M, H), dtype=out_dtype, device=q.device)
+    _need_out(out, _FLOATS, "out", (M, H))
+    _check("qmm_s8_dequantize_rows",
+           _lib.qmm_s8_dequantize_rows(_ptr(q), _ptr(scale), M, H, _ptr(out), _TORCH_TO_QMM[out.dtype],
+                                       _stream(stream)))
+    return out
+
+
+def qmm_rms_norm_backward_workspace_bytes(M: int, H: int) -> int:
+    return int(_lib.qmm_rms_norm_backward_workspace_bytes(M, H))
+
+
+def qmm_rms_norm_backward(dy, h, weight, rstd, dh=None, out=None, dweight=None, stream=None, workspace="auto"):
+    """The gradient of qmm_rms_norm_s8 with the quantiser passed straight through:
+    (dx [M, H] of h's type, dweight float32 [H]) from dy, the gradient of the
+    normalised rows, and dh, the gradient that reaches h past the norm (or None).
+    h and rstd as the forward call returned them; dx is the gradient of x and of
+    the residual alike. dweight sums the rows in a fixed order."""
+    ldh = _need_rows(h, _FLOATS, "h")
+    M, H = h.shape
+    lddy = _need_rows(dy, (h.dtype,), "dy", (M, H))
+    lddh = H if dh is None else _need_rows(dh, (h.dtype,), "dh", (M, H))
+    _need_out(weight, _FLOATS, "weight", (H,))
+    _need_out(rstd, (torch.float32,), "rstd", (M,))
+    if out is None:
+        out = torch.empty((M, H), dtype=h.dtype, device=h.device)
+    _need_out(out, (h.dtype,), "out", (M, H))
+    if dweight is None:
+        dweight = torch.empty(H, dtype=torch.float32, device=h.device)
+    _need_out(dweight, (torch.float32,), "dweight", (H,))
+    ws, wsb = _workspace(workspace, qmm_rms_norm_backward_workspace_bytes(M, H), h.device)
+    st = _lib.qmm_rms_norm_backward(_ptr(dy), lddy, _ptr(h), ldh, _ptr(dh), lddh, _TORCH_TO_QMM[h.dtype], M, H,
+                                    _ptr(weight), _TORCH_TO_QMM[weight.dtype], _ptr(rstd), _ptr(out), _ptr(dweight),
+                                    _ptr(ws), wsb, _stream(stream))
+    _check("qmm_rms_norm_backward", st)
+    return out, dweight
+
+
+class Fp4Matrix(NamedTuple):
+    """A packed [rows, cols] matrix of 4-bit floats with block scales (32
+    elements to a power of two, or 16 to an e4m3 scale under a row scale)."""
+    buf: torch.Tensor
+    rows: int
+    cols: int
+    block: int
+
+
+def qmm_fp4_bytes(rows: int, cols: int, block: int) -> int:
+    return int(_lib.qmm_fp4_bytes(rows, cols, block))
+
+
+def _fp4_new(rows, cols, block, device, out, name):
+    if block not in (16, 32):
+        raise ValueError("block must be 16 or 32")
+    if out is None:
+        return Fp4Matrix(torch.empty(qmm_fp4_bytes(rows, cols, block), dtype=torch.uint8, device=device), rows, cols,
+                         block)
+    if (out.rows, out.cols, out.block) != (rows, cols, block):
+        raise ValueError(f"{name} must be a packed [{rows}, {cols}] matrix of block {block}")
+    _need(out.buf, (torch.uint8,), name)
+    return out
+
+
+def qmm_fp4_quantize(x, block=16, transpose=False, out=None, stream=None) -> Fp4Matrix:
+    """Pack x [R, C] (float32 or bfloat16, rows contiguous at any stride) to 4-bit
+    floats, blocks running along its rows; with transpose, the packed matrix is
+    x.T [C, R], blocks running down x's columns. out: an Fp4Matrix to reuse."""
+    ldx = _need_rows(x, _FLOATS, "x")
+    R, C = x.shape
+    rows, cols = (C, R) if transpose else (R, C)
+    m = _fp4_new(rows, cols, block, x.device, out, "out")
+    _check("qmm_fp4_quantize",
+           _lib.qmm_fp4_quantize(_ptr(x), _TORCH_TO_QMM[x.dtype], rows, cols, ldx, int(bool(transpose)), block,
+                                 _ptr(m.buf), m.buf.numel(), _stream(stream)))
+    return m
+
+
+def qmm_fp4_quantize_both(x, block=16, out=None, out_t=None, stream=None):
+    """(qmm_fp4_quantize(x), qmm_fp4_quantize(x, transpose=True)) from one read of x."""
+    ldx = _need_rows(x, _FLOATS, "x")
+    R, C = x.shape
+    m = _fp4_new(R, C, block, x.device, out, "out")
+    t = _fp4_new(C, R, block, x.device, out_t, "out_t")
+    _check("qmm_fp4_quantize_both",
+           _lib.qmm_fp4_quantize_both(_ptr(x), _TORCH_TO_QMM[x.dtype], R, C, ldx, block, _ptr(m.buf), m.buf.numel(),
+                                      _ptr(t.buf), t.buf.numel(), _stream(stream)))
+    return m, t
+
+
+def qmm_fp4_dequantize(m: Fp4Matrix, out=None, out_dtype=torch.bfloat16, stream=None):
+    """A packed matrix read back to float32 or bfloat16 [rows, cols]."""
+    _need(m.buf, (torch.uint8,), "m")
+    if out is None:
+        out = torch.empty((m.rows, m.cols), dtype=out_dtype, device=m.buf.device)
+    _need_out(out, _FLOATS, "out", (m.rows, m.cols))
+    _check("qmm_fp4_dequantize",
+           _lib.qmm_fp4_dequantize(_ptr(m.buf), m.buf.numel(), m.rows, m.cols, m.block, _ptr(out),
+                                   _TORCH_TO_QMM[out.dtype], _stream(stream)))
+    return out
+
+
+def qmm_fp4_matmul(a: Fp4Matrix, b: Fp4Matrix, out=None, out_dtype=torch.bfloat16, stream=None):
+    """a @ b.T of packed a [M, K] and b [N, K] (the same block), float32 or
+    bfloat16 [M, N]: the product of the values that the operands stand for, with
+    one fp32 accumulation."""
+    _need(a.buf, (torch.uint8,), "a")
+    _need(b.buf, (torch.uint8,), "b")
+    if a.cols != b.cols:
+        raise ValueError("inner dimensions differ")
+    if a.block != b.block:
+        raise ValueError("operands of different blocks")
+    if out is None:
+        out = torch.empty((a.rows, b.rows), dtype=out_dtype, device=a.buf.device)
+    _need_out(out, _FLOATS, "out", (a.rows, b.rows))
+    _check("qmm_fp4_matmul",
+           _lib.qmm_fp4_matmul(_ptr(a.buf), a.buf.numel(), a.rows, _ptr(b.buf), b.buf.numel(), b.rows, a.cols,
+                               a.block, _ptr(out), _TORCH_TO_QMM[out.dtype], _stream(stream)))
+    return out
+
+
 def num_sms() -> int:
     return int(_lib.qmm_num_sms())
 
@@ -691,6 +907,8 @@ __all__ = [
     "qmm_w8_dequant", "qmm_a8w8", "qmm_a8w8_acc", "matmul_integer", "conv_integer", "dynamic_quantize_matmul",
     "dynamic_quantize_matmul_pack_weight", "dynamic_quantize_matmul_packed", "DqmPackedWeight",
     "dynamic_quantize_linear",
+    "qmm_rms_norm_s8", "RmsNormS8", "qmm_s8_dequantize_rows", "qmm_rms_norm_backward", "qmm_fp4_quantize",
+    "qmm_fp4_quantize_both", "qmm_fp4_dequantize", "qmm_fp4_matmul", "qmm_fp4_bytes", "Fp4Matrix",
     "dynamic_quantize_linear_workspace_bytes", "last_kernel", "check_device_error", "QmmError", "lib",
     "num_sms", "LIB_PATH",
 ]

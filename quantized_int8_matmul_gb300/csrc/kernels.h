@@ -290,6 +290,66 @@ cudaError_t launch_dql(const float* x, long long n, uint8_t* y, float* y_scale, 
                        long long row_len, float* partials, int num_partials, cudaStream_t s,
                        const char** kernel_name);
 
+// ---------------------------------------------------------------------------
+// RMS norm with the residual's addition and int8 rows out, and its gradient
+// (norm.cu); int8 rows read back.
+// ---------------------------------------------------------------------------
+struct NormArgs {
+  const void* x;               // [M] rows of H, f32 or bf16, ldx elements apart
+  const void* residual;        // the same type, ldr apart, or null
+  const void* w; int w_f32;    // [H] f32 (1) or bf16 (0)
+  void* h;                     // [M][H] of x's type: x + residual, or null (not stored)
+  int8_t* q;                   // [M][H]
+  float* scale;                // [M]
+  float* rstd;                 // [M]
+  long long M, ldx, ldr;
+  int H;
+  float eps;
+};
+cudaError_t launch_rms_norm_s8(const NormArgs& a, bool bf16, cudaStream_t s, const char** kernel_name);
+// y[m][i] = q[m][i] * scale[m]
+cudaError_t launch_s8_dequantize_rows(const int8_t* q, const float* scale, long long M, int H, void* y, bool bf16,
+                                      cudaStream_t s, const char** kernel_name);
+struct NormBwdArgs {
+  const void* dy;              // [M] rows of H, lddy apart, f32 or bf16
+  const void* h;               // the same type, ldh apart
+  const void* dh;              // gradient arriving at h itself, the same type, lddh apart, or null
+  const void* w; int w_f32;
+  const float* rstd;           // [M]
+  void* dx;                    // [M][H]
+  float* dweight;              // [H]
+  float* partials;             // rms_norm_backward_partials(M, H) rows of H floats
+  long long M, lddy, ldh, lddh;
+  int H;
+};
+int rms_norm_backward_partials(long long M, int H);
+cudaError_t launch_rms_norm_backward(const NormBwdArgs& a, bool bf16, cudaStream_t s, const char** kernel_name);
+
+// ---------------------------------------------------------------------------
+// 4-bit floats with block scales (fp4.cu; layout in fp4.cuh) and their product
+// (gemm_fp4.cu).
+// ---------------------------------------------------------------------------
+size_t fp4_packed_bytes(long long rows, long long cols, int block);
+struct Fp4QuantArgs {
+  const void* x;               // [rows][cols], f32 or bf16, rows ld elements apart
+  long long rows, cols, ld;
+  int vec;                     // every row starts on 16 bytes
+  uint8_t* out;                // rows only: packed [rows][cols]; otherwise packed [cols][rows]
+  uint8_t* out_rows;           // not rows only: packed [rows][cols] as well, or null
+};
+cudaError_t launch_fp4_quantize(const Fp4QuantArgs& a, bool bf16, int block, bool rows_only, cudaStream_t s,
+                                const char** kernel_name);
+cudaError_t launch_fp4_dequantize(const void* packed, long long rows, long long cols, int block, void* y, bool bf16,
+                                  cudaStream_t s, const char** kernel_name);
+struct GemmFp4Args {
+  const uint8_t* A;            // packed [M][K]
+  const uint8_t* B;            // packed [N][K]
+  long long M, N, K;
+  void* C; int c_f32;          // [M][N]
+  unsigned* err;
+};
+cudaError_t launch_gemm_fp4(const GemmFp4Args& a, int block, cudaStream_t s, const char** kernel_name);
+
 int num_sms();
 // The unique id of the calling thread's current CUDA context; false when no
 // context is current (or the driver offers no such query).

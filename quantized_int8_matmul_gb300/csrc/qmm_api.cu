@@ -1617,4 +1617,203 @@ qmm_status dynamic_quantize_linear(const float* x, int64_t n, uint8_t* y, float*
                        name);
 }
 
+static bool float_type(int t) { return t == QMM_F32 || t == QMM_BF16; }
+
+qmm_status qmm_rms_norm_s8(const void* x, int x_dtype, int64_t M, int64_t H, int64_t ldx, const void* residual,
+                           int64_t ldr, const void* w, int w_dtype, float eps, void* h, int8_t* q, float* scale,
+                           float* rstd, void* stream) {
+  if (!float_type(x_dtype) || !float_type(w_dtype)) return QMM_ERR_INVALID_ARG;
+  if (!dim_ok(M) || !dim_ok(H) || ldx < H || (residual && ldr < H) || !(eps >= 0.f)) return QMM_ERR_INVALID_ARG;
+  if (M == 0 || H == 0) {
+    t_last_kernel = "none";
+    return QMM_OK;
+  }
+  if (!x || !w || !q || !scale || !rstd) return QMM_ERR_INVALID_ARG;
+  if (h && ((h == x && ldx != H) || (h == residual && ldr != H))) return QMM_ERR_INVALID_ARG;
+  cudaGetLastError();
+  NormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.w = w;
+  a.w_f32 = w_dtype == QMM_F32;
+  a.h = h;
+  a.q = q;
+  a.scale = scale;
+  a.rstd = rstd;
+  a.M = M;
+  a.ldx = ldx;
+  a.ldr = ldr;
+  a.H = (int)H;
+  a.eps = eps;
+  const char* name = "none";
+  return finish_launch(launch_rms_norm_s8(a, x_dtype == QMM_BF16, static_cast<cudaStream_t>(stream), &name), name);
+}
+
+qmm_status qmm_s8_dequantize_rows(const int8_t* q, const float* scale, int64_t M, int64_t H, void* y, int y_dtype,
+                                  void* stream) {
+  if (!float_type(y_dtype) || !dim_ok(M) || !dim_ok(H)) return QMM_ERR_INVALID_ARG;
+  if (M == 0 || H == 0) {
+    t_last_kernel = "none";
+    return QMM_OK;
+  }
+  if (!q || !scale || !y) return QMM_ERR_INVALID_ARG;
+  cudaGetLastError();
+  const char* name = "none";
+  return finish_launch(launch_s8_dequantize_rows(q, scale, M, (int)H, y, y_dtype == QMM_BF16,
+                                                 static_cast<cudaStream_t>(stream), &name),
+                       name);
+}
+
+size_t qmm_rms_norm_backward_workspace_bytes(int64_t M, int64_t H) {
+  if (!dim_ok(M) || !dim_ok(H) || M == 0) return 0;
+  return sizeof(float) * (size_t)rms_norm_backward_partials(M, (int)H) * (size_t)H;
+}
+
+qmm_status qmm_rms_norm_backward(const void* dy, int64_t lddy, const void* h, int64_t ldh, const void* dh,
+                                 int64_t lddh, int dtype, int64_t M, int64_t H, const void* w, int w_dtype,
+                                 const float* rstd, void* dx, float* dweight, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  if (!float_type(dtype) || !float_type(w_dtype)) return QMM_ERR_INVALID_ARG;
+  if (!dim_ok(M) || !dim_ok(H) || lddy < H || ldh < H || (dh && lddh < H)) return QMM_ERR_INVALID_ARG;
+  if (H == 0) {
+    t_last_kernel = "none";
+    return QMM_OK;
+  }
+  if (!dweight) return QMM_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M == 0) {
+    cudaGetLastError();
+    return finish_launch(cudaMemsetAsync(dweight, 0, (size_t)H * sizeof(float), s), "none");
+  }
+  if (!dy || !h || !w || !rstd || !dx) return QMM_ERR_INVALID_ARG;
+  if ((dx == dy && lddy != H) || (dx == dh && lddh != H) || dx == h) return QMM_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < qmm_rms_norm_backward_workspace_bytes(M, H))
+    return QMM_ERR_INVALID_ARG;
+  cudaGetLastError();
+  NormBwdArgs a{};
+  a.dy = dy;
+  a.h = h;
+  a.dh = dh;
+  a.w = w;
+  a.w_f32 = w_dtype == QMM_F32;
+  a.rstd = rstd;
+  a.dx = dx;
+  a.dweight = dweight;
+  a.partials = static_cast<float*>(workspace);
+  a.M = M;
+  a.lddy = lddy;
+  a.ldh = ldh;
+  a.lddh = lddh;
+  a.H = (int)H;
+  const char* name = "none";
+  return finish_launch(launch_rms_norm_backward(a, dtype == QMM_BF16, s, &name), name);
+}
+
+// Tiles are counted in int32 by the kernels' grids.
+static bool fp4_shape_ok(int64_t rows, int64_t cols, int block) {
+  return (block == 16 || block == 32) && dim_ok(rows) && dim_ok(cols) &&
+         ((rows + 127) / 128) * ((cols + 127) / 128) <= (int64_t)INT_MAX / 16;
+}
+
+size_t qmm_fp4_bytes(int64_t rows, int64_t cols, int block) {
+  return fp4_shape_ok(rows, cols, block) ? fp4_packed_bytes(rows, cols, block) : 0;
+}
+
+static qmm_status fp4_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, int block,
+                               void* packed, size_t packed_bytes, void* packed_t, size_t packed_t_bytes, int way,
+                               void* stream) {
+  // rows, cols, ldx of x as stored; way 0: packed only, 1: packed_t only, 2: both
+  if (!float_type(x_dtype) || (block != 16 && block != 32)) return QMM_ERR_INVALID_ARG;
+  if (!dim_ok(rows) || !dim_ok(cols) || ldx < cols) return QMM_ERR_INVALID_ARG;
+  if (!fp4_shape_ok(rows, cols, block)) return QMM_ERR_UNSUPPORTED;
+  if (rows == 0 || cols == 0) {
+    t_last_kernel = "none";
+    return QMM_OK;
+  }
+  if (!x) return QMM_ERR_INVALID_ARG;
+  if (way != 1 && (!packed || !aligned16(packed) || packed_bytes < fp4_packed_bytes(rows, cols, block)))
+    return QMM_ERR_INVALID_ARG;
+  if (way != 0 && (!packed_t || !aligned16(packed_t) || packed_t_bytes < fp4_packed_bytes(cols, rows, block)))
+    return QMM_ERR_INVALID_ARG;
+  cudaGetLastError();
+  const int es = x_dtype == QMM_BF16 ? 2 : 4;
+  Fp4QuantArgs a{};
+  a.x = x;
+  a.rows = rows;
+  a.cols = cols;
+  a.ld = ldx;
+  a.vec = aligned16(x) && (ldx * es) % 16 == 0;
+  a.out = static_cast<uint8_t*>(way == 0 ? packed : packed_t);
+  a.out_rows = way == 2 ? static_cast<uint8_t*>(packed) : nullptr;
+  const char* name = "none";
+  return finish_launch(launch_fp4_quantize(a, x_dtype == QMM_BF16, block, way == 0, static_cast<cudaStream_t>(stream),
+                                           &name),
+                       name);
+}
+
+qmm_status qmm_fp4_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, int trans, int block,
+                            void* packed, size_t packed_bytes, void* stream) {
+  if (trans != 0 && trans != 1) return QMM_ERR_INVALID_ARG;
+  if (trans) return fp4_quantize(x, x_dtype, cols, rows, ldx, block, nullptr, 0, packed, packed_bytes, 1, stream);
+  return fp4_quantize(x, x_dtype, rows, cols, ldx, block, packed, packed_bytes, nullptr, 0, 0, stream);
+}
+
+qmm_status qmm_fp4_quantize_both(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, int block,
+                                 void* packed, size_t packed_bytes, void* packed_t, size_t packed_t_bytes,
+                                 void* stream) {
+  return fp4_quantize(x, x_dtype, rows, cols, ldx, block, packed, packed_bytes, packed_t, packed_t_bytes, 2, stream);
+}
+
+qmm_status qmm_fp4_dequantize(const void* packed, size_t packed_bytes, int64_t rows, int64_t cols, int block, void* y,
+                              int y_dtype, void* stream) {
+  if (!float_type(y_dtype) || (block != 16 && block != 32)) return QMM_ERR_INVALID_ARG;
+  if (!dim_ok(rows) || !dim_ok(cols)) return QMM_ERR_INVALID_ARG;
+  if (!fp4_shape_ok(rows, cols, block)) return QMM_ERR_UNSUPPORTED;
+  if (rows == 0 || cols == 0) {
+    t_last_kernel = "none";
+    return QMM_OK;
+  }
+  if (!packed || !aligned16(packed) || packed_bytes < fp4_packed_bytes(rows, cols, block) || !y)
+    return QMM_ERR_INVALID_ARG;
+  cudaGetLastError();
+  const char* name = "none";
+  return finish_launch(launch_fp4_dequantize(packed, rows, cols, block, y, y_dtype == QMM_BF16,
+                                             static_cast<cudaStream_t>(stream), &name),
+                       name);
+}
+
+qmm_status qmm_fp4_matmul(const void* a_packed, size_t a_bytes, int64_t M, const void* b_packed, size_t b_bytes,
+                          int64_t N, int64_t K, int block, void* C, int c_dtype, void* stream) {
+  if (!float_type(c_dtype) || (block != 16 && block != 32)) return QMM_ERR_INVALID_ARG;
+  if (!dim_ok(M) || !dim_ok(N) || !dim_ok(K)) return QMM_ERR_INVALID_ARG;
+  if (!fp4_shape_ok(M, K, block) || !fp4_shape_ok(N, K, block) || !fp4_shape_ok(M, N, block))
+    return QMM_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) {
+    t_last_kernel = "none";
+    return QMM_OK;
+  }
+  if (!C) return QMM_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (K == 0) {
+    cudaGetLastError();
+    return finish_launch(cudaMemsetAsync(C, 0, (size_t)M * N * (c_dtype == QMM_F32 ? 4 : 2), s), "none");
+  }
+  if (!a_packed || !aligned16(a_packed) || a_bytes < fp4_packed_bytes(M, K, block)) return QMM_ERR_INVALID_ARG;
+  if (!b_packed || !aligned16(b_packed) || b_bytes < fp4_packed_bytes(N, K, block)) return QMM_ERR_INVALID_ARG;
+  unsigned* err = err_word();
+  if (!err) return QMM_ERR_CUDA;
+  cudaGetLastError();
+  GemmFp4Args a{};
+  a.A = static_cast<const uint8_t*>(a_packed);
+  a.B = static_cast<const uint8_t*>(b_packed);
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.C = C;
+  a.c_f32 = c_dtype == QMM_F32;
+  a.err = err;
+  const char* name = "none";
+  return finish_launch(launch_gemm_fp4(a, block, s, &name), name);
+}
+
 }  // extern "C"
