@@ -13,6 +13,7 @@ first import; if that fails the import fails loudly.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple
 
@@ -133,13 +134,17 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+# The entry points' pointer arguments are declared c_void_p, which takes plain
+# integers: a c_void_p object per argument, and a Stream object per call, would
+# cost more host time than a small call's launch (0.2 and 3 us each).
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _check(fn: str, status: int):
@@ -705,26 +710,29 @@ def _need_rows(t, dtypes, name, shape=None):
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {t.dtype} not in {dtypes}")
-    if t.dim() != 2:
+    size = t.shape
+    if len(size) != 2:
         raise ValueError(f"{name} must be 2-D")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and size != shape:
         raise ValueError(f"{name} must be {tuple(shape)}")
-    rows, cols = t.shape
-    if rows <= 1 or cols == 0:      # the row stride is never used
-        if cols > 1 and t.stride(1) != 1:
-            raise ValueError(f"{name}: rows must be contiguous")
+    rows, cols = size
+    if t.is_contiguous():
         return cols
-    if (cols > 1 and t.stride(1) != 1) or t.stride(0) < cols:
+    ld, step = t.stride()
+    if rows <= 1:                   # the row stride is never used
+        ld = cols
+    if (cols > 1 and step != 1) or ld < cols:
         raise ValueError(f"{name}: rows must be contiguous and not overlap")
-    return t.stride(0)
+    return ld
 
 
 _FLOATS = (torch.float32, torch.bfloat16)
+_F32, _S8, _U8 = (torch.float32,), (torch.int8,), (torch.uint8,)
 
 
 def _need_out(t, dtypes, name, shape):
     _need(t, dtypes, name)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}")
 
 
@@ -747,46 +755,54 @@ def qmm_rms_norm_s8(x, weight, residual=None, eps=1e-6, out=None, h_out=None, st
     may be x or residual itself. A row that holds a NaN or an infinity gets a NaN
     scale."""
     ldx = _need_rows(x, _FLOATS, "x")
-    M, H = x.shape
+    shape, dt, dev = x.shape, x.dtype, x.device
+    M, H = shape
     _need_out(weight, _FLOATS, "weight", (H,))
-    ldr = H
-    if residual is not None:
-        ldr = _need_rows(residual, (x.dtype,), "residual", (M, H))
     if out is None:
-        out = torch.empty((M, H), dtype=torch.int8, device=x.device)
-    _need_out(out, (torch.int8,), "out", (M, H))
+        out = torch.empty(shape, dtype=torch.int8, device=dev)
+    else:
+        _need_out(out, _S8, "out", shape)
     if residual is None:
         if h_out is not None:
             raise ValueError("h_out without a residual: h is x")
-        h = x
+        h, ldr, rp, hp = x, H, None, None
     else:
-        h = torch.empty((M, H), dtype=x.dtype, device=x.device) if h_out is None else h_out
-        _need_out(h, (x.dtype,), "h_out", (M, H))
-    stats = torch.empty((2, M), dtype=torch.float32, device=x.device)
-    scale, rstd = stats[0], stats[1]
-    st = _lib.qmm_rms_norm_s8(_ptr(x), _TORCH_TO_QMM[x.dtype], M, H, ldx, _ptr(residual), ldr, _ptr(weight),
-                              _TORCH_TO_QMM[weight.dtype], float(eps), None if residual is None else _ptr(h),
-                              _ptr(out), _ptr(scale), _ptr(rstd), _stream(stream))
-    _check("qmm_rms_norm_s8", st)
+        ldr = _need_rows(residual, (dt,), "residual", shape)
+        if h_out is None:
+            h = torch.empty(shape, dtype=dt, device=dev)
+        else:
+            h = h_out
+            _need_out(h, (dt,), "h_out", shape)
+        rp, hp = residual.data_ptr(), h.data_ptr()
+    scale = torch.empty(M, dtype=torch.float32, device=dev)
+    rstd = torch.empty(M, dtype=torch.float32, device=dev)
+    st = _lib.qmm_rms_norm_s8(x.data_ptr(), _TORCH_TO_QMM[dt], M, H, ldx, rp, ldr, weight.data_ptr(),
+                              _TORCH_TO_QMM[weight.dtype], eps, hp, out.data_ptr(), scale.data_ptr(),
+                              rstd.data_ptr(), _stream(stream))
+    if st:
+        _check("qmm_rms_norm_s8", st)
     return RmsNormS8(out, scale, h, rstd)
 
 
 def qmm_s8_dequantize_rows(q, scale, out=None, out_dtype=torch.bfloat16, stream=None):
     """int8 rows read back: out[m, i] = q[m, i] * scale[m], float32 or bfloat16."""
-    _need(q, (torch.int8,), "q")
-    if q.dim() != 2:
+    _need(q, _S8, "q")
+    shape = q.shape
+    if len(shape) != 2:
         raise ValueError("q must be 2-D")
-    M, H = q.shape
-    _need_out(scale, (torch.float32,), "scale", (M,))
+    M, H = shape
+    _need_out(scale, _F32, "scale", (M,))
     if out is None:
-        out = torch.empty((M, H), dtype=out_dtype, device=q.device)
-    _need_out(out, _FLOATS, "out", (M, H))
-    _check("qmm_s8_dequantize_rows",
-           _lib.qmm_s8_dequantize_rows(_ptr(q), _ptr(scale), M, H, _ptr(out), _TORCH_TO_QMM[out.dtype],
-                                       _stream(stream)))
+        out = torch.empty(shape, dtype=out_dtype, device=q.device)
+    _need_out(out, _FLOATS, "out", shape)
+    st = _lib.qmm_s8_dequantize_rows(q.data_ptr(), scale.data_ptr(), M, H, out.data_ptr(), _TORCH_TO_QMM[out.dtype],
+                                     _stream(stream))
+    if st:
+        _check("qmm_s8_dequantize_rows", st)
     return out
 
 
+@functools.lru_cache(maxsize=256)
 def qmm_rms_norm_backward_workspace_bytes(M: int, H: int) -> int:
     return int(_lib.qmm_rms_norm_backward_workspace_bytes(M, H))
 
@@ -798,22 +814,26 @@ def qmm_rms_norm_backward(dy, h, weight, rstd, dh=None, out=None, dweight=None, 
     h and rstd as the forward call returned them; dx is the gradient of x and of
     the residual alike. dweight sums the rows in a fixed order."""
     ldh = _need_rows(h, _FLOATS, "h")
-    M, H = h.shape
-    lddy = _need_rows(dy, (h.dtype,), "dy", (M, H))
-    lddh = H if dh is None else _need_rows(dh, (h.dtype,), "dh", (M, H))
+    shape, dt, dev = h.shape, h.dtype, h.device
+    M, H = shape
+    lddy = _need_rows(dy, (dt,), "dy", shape)
+    lddh = H if dh is None else _need_rows(dh, (dt,), "dh", shape)
     _need_out(weight, _FLOATS, "weight", (H,))
-    _need_out(rstd, (torch.float32,), "rstd", (M,))
+    _need_out(rstd, _F32, "rstd", (M,))
     if out is None:
-        out = torch.empty((M, H), dtype=h.dtype, device=h.device)
-    _need_out(out, (h.dtype,), "out", (M, H))
+        out = torch.empty(shape, dtype=dt, device=dev)
+    else:
+        _need_out(out, (dt,), "out", shape)
     if dweight is None:
-        dweight = torch.empty(H, dtype=torch.float32, device=h.device)
-    _need_out(dweight, (torch.float32,), "dweight", (H,))
-    ws, wsb = _workspace(workspace, qmm_rms_norm_backward_workspace_bytes(M, H), h.device)
-    st = _lib.qmm_rms_norm_backward(_ptr(dy), lddy, _ptr(h), ldh, _ptr(dh), lddh, _TORCH_TO_QMM[h.dtype], M, H,
-                                    _ptr(weight), _TORCH_TO_QMM[weight.dtype], _ptr(rstd), _ptr(out), _ptr(dweight),
-                                    _ptr(ws), wsb, _stream(stream))
-    _check("qmm_rms_norm_backward", st)
+        dweight = torch.empty(H, dtype=torch.float32, device=dev)
+    else:
+        _need_out(dweight, _F32, "dweight", (H,))
+    ws, wsb = _workspace(workspace, qmm_rms_norm_backward_workspace_bytes(M, H), dev)
+    st = _lib.qmm_rms_norm_backward(dy.data_ptr(), lddy, h.data_ptr(), ldh, _ptr(dh), lddh, _TORCH_TO_QMM[dt], M, H,
+                                    weight.data_ptr(), _TORCH_TO_QMM[weight.dtype], rstd.data_ptr(), out.data_ptr(),
+                                    dweight.data_ptr(), _ptr(ws), wsb, _stream(stream))
+    if st:
+        _check("qmm_rms_norm_backward", st)
     return out, dweight
 
 
@@ -826,6 +846,7 @@ class Fp4Matrix(NamedTuple):
     block: int
 
 
+@functools.lru_cache(maxsize=256)
 def qmm_fp4_bytes(rows: int, cols: int, block: int) -> int:
     return int(_lib.qmm_fp4_bytes(rows, cols, block))
 
@@ -850,9 +871,11 @@ def qmm_fp4_quantize(x, block=16, transpose=False, out=None, stream=None) -> Fp4
     R, C = x.shape
     rows, cols = (C, R) if transpose else (R, C)
     m = _fp4_new(rows, cols, block, x.device, out, "out")
-    _check("qmm_fp4_quantize",
-           _lib.qmm_fp4_quantize(_ptr(x), _TORCH_TO_QMM[x.dtype], rows, cols, ldx, int(bool(transpose)), block,
-                                 _ptr(m.buf), m.buf.numel(), _stream(stream)))
+    buf = m.buf
+    st = _lib.qmm_fp4_quantize(x.data_ptr(), _TORCH_TO_QMM[x.dtype], rows, cols, ldx, 1 if transpose else 0, block,
+                               buf.data_ptr(), buf.numel(), _stream(stream))
+    if st:
+        _check("qmm_fp4_quantize", st)
     return m
 
 
@@ -862,21 +885,25 @@ def qmm_fp4_quantize_both(x, block=16, out=None, out_t=None, stream=None):
     R, C = x.shape
     m = _fp4_new(R, C, block, x.device, out, "out")
     t = _fp4_new(C, R, block, x.device, out_t, "out_t")
-    _check("qmm_fp4_quantize_both",
-           _lib.qmm_fp4_quantize_both(_ptr(x), _TORCH_TO_QMM[x.dtype], R, C, ldx, block, _ptr(m.buf), m.buf.numel(),
-                                      _ptr(t.buf), t.buf.numel(), _stream(stream)))
+    a, b = m.buf, t.buf
+    st = _lib.qmm_fp4_quantize_both(x.data_ptr(), _TORCH_TO_QMM[x.dtype], R, C, ldx, block, a.data_ptr(), a.numel(),
+                                    b.data_ptr(), b.numel(), _stream(stream))
+    if st:
+        _check("qmm_fp4_quantize_both", st)
     return m, t
 
 
 def qmm_fp4_dequantize(m: Fp4Matrix, out=None, out_dtype=torch.bfloat16, stream=None):
     """A packed matrix read back to float32 or bfloat16 [rows, cols]."""
-    _need(m.buf, (torch.uint8,), "m")
+    buf, rows, cols, block = m
+    _need(buf, _U8, "m")
     if out is None:
-        out = torch.empty((m.rows, m.cols), dtype=out_dtype, device=m.buf.device)
-    _need_out(out, _FLOATS, "out", (m.rows, m.cols))
-    _check("qmm_fp4_dequantize",
-           _lib.qmm_fp4_dequantize(_ptr(m.buf), m.buf.numel(), m.rows, m.cols, m.block, _ptr(out),
-                                   _TORCH_TO_QMM[out.dtype], _stream(stream)))
+        out = torch.empty((rows, cols), dtype=out_dtype, device=buf.device)
+    _need_out(out, _FLOATS, "out", (rows, cols))
+    st = _lib.qmm_fp4_dequantize(buf.data_ptr(), buf.numel(), rows, cols, block, out.data_ptr(),
+                                 _TORCH_TO_QMM[out.dtype], _stream(stream))
+    if st:
+        _check("qmm_fp4_dequantize", st)
     return out
 
 
@@ -884,18 +911,21 @@ def qmm_fp4_matmul(a: Fp4Matrix, b: Fp4Matrix, out=None, out_dtype=torch.bfloat1
     """a @ b.T of packed a [M, K] and b [N, K] (the same block), float32 or
     bfloat16 [M, N]: the product of the values that the operands stand for, with
     one fp32 accumulation."""
-    _need(a.buf, (torch.uint8,), "a")
-    _need(b.buf, (torch.uint8,), "b")
-    if a.cols != b.cols:
+    abuf, M, K, block = a
+    bbuf, N, Kb, block_b = b
+    _need(abuf, _U8, "a")
+    _need(bbuf, _U8, "b")
+    if K != Kb:
         raise ValueError("inner dimensions differ")
-    if a.block != b.block:
+    if block != block_b:
         raise ValueError("operands of different blocks")
     if out is None:
-        out = torch.empty((a.rows, b.rows), dtype=out_dtype, device=a.buf.device)
-    _need_out(out, _FLOATS, "out", (a.rows, b.rows))
-    _check("qmm_fp4_matmul",
-           _lib.qmm_fp4_matmul(_ptr(a.buf), a.buf.numel(), a.rows, _ptr(b.buf), b.buf.numel(), b.rows, a.cols,
-                               a.block, _ptr(out), _TORCH_TO_QMM[out.dtype], _stream(stream)))
+        out = torch.empty((M, N), dtype=out_dtype, device=abuf.device)
+    _need_out(out, _FLOATS, "out", (M, N))
+    st = _lib.qmm_fp4_matmul(abuf.data_ptr(), abuf.numel(), M, bbuf.data_ptr(), bbuf.numel(), N, K, block,
+                             out.data_ptr(), _TORCH_TO_QMM[out.dtype], _stream(stream))
+    if st:
+        _check("qmm_fp4_matmul", st)
     return out
 
 

@@ -10,6 +10,7 @@
 // MMAs, four warps store the tile.
 #include "common.cuh"
 #include "fp4.cuh"
+#include "gemm_fp4.cuh"
 #include "kernels.h"
 
 #include <algorithm>
@@ -31,46 +32,6 @@ struct Shared {
 };
 
 enum : unsigned { SITE_EMPTY = 0x500, SITE_FULL = 0x501, SITE_DONE = 0x502 };
-
-// Shared-memory descriptor without swizzle (K-major): lbo bytes between core
-// matrices along K, sbo bytes between 8-row groups.
-__device__ __forceinline__ uint64_t sdesc_none(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
-  d |= (uint64_t)1 << 46;
-  return d;
-}
-
-// Instruction descriptor of the block-scaled 4-bit MMA: [4,6) B scale id,
-// [7,10) A format (1 = e2m1), [10,13) B format, [17,23) N >> 3, 23 scale type
-// (0 = ue4m3, 1 = ue8m0), [24,29) M >> 4, [29,31) A scale id; 31: K = 64.
-__host__ __device__ constexpr uint32_t idesc_fp4(int M, int N, bool e8m0, int sf_id) {
-  return ((uint32_t)sf_id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((e8m0 ? 1u : 0u) << 23) |
-         ((uint32_t)(M >> 4) << 24) | ((uint32_t)sf_id << 29);
-}
-
-template <int BLOCK>
-__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa,
-                                        uint32_t sfb, uint32_t acc) {
-  if (BLOCK == 16)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
-        : "memory");
-}
-// One atom of scales (512 bytes) into four tensor-memory columns, repeated in
-// the four 32-lane quarters.
-__device__ __forceinline__ void cp_scales(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
-}
 
 template <int BLOCK>
 __global__ void __launch_bounds__(NT, 1) gemm_fp4_kernel(const GemmFp4Args p) {
@@ -192,6 +153,10 @@ cudaError_t launch(const GemmFp4Args& a, cudaStream_t s) {
 }  // namespace gfp4
 
 cudaError_t launch_gemm_fp4(const GemmFp4Args& a, int block, cudaStream_t s, const char** kernel_name) {
+  if (a.M > 256) {
+    *kernel_name = "gemm_fp4_pair";
+    return launch_gemm_fp4_pair(a, block, s);
+  }
   *kernel_name = "gemm_fp4";
   return block == 16 ? gfp4::launch<16>(a, s) : gfp4::launch<32>(a, s);
 }

@@ -1,0 +1,350 @@
+// The product of two packed 4-bit matrices (fp4.cuh) on SM pairs, for more than
+// a few rows:
+//   C[m][n] = ((sum_k a*sa * b*sb) * ga[m]) * gb[n]
+// with the block scales applied by the block-scaled MMA (tcgen05.mma
+// kind::mxf4nvf4, K = 64 an instruction, fp32 accumulation in tensor memory) and
+// the row scales of block 16 in the epilogue.
+//
+// Cluster of 2 CTAs per 256 x 256 tile of C, persistent over the tiles, 320
+// threads each:
+//  * warp 9: copies this CTA's 128 rows of A and 128 rows of B (256 columns of K
+//    a stage: 16 KB of codes each) and the scales of its rows of A and of all 256
+//    rows of B into a ring. The packed layout is the MMA's own, so every copy is
+//    one contiguous run; a tensor map describes it as a plain matrix only because
+//    tensor copies can complete on the even CTA's barrier.
+//  * warp 8 of the even CTA: moves each 128 columns' scales to tensor memory
+//    (tcgen05.cp, both CTAs at once) and issues the pair MMAs.
+//  * warps 0-7: one row and 128 columns a thread; scale, round, stage 32 rows x
+//    128 bytes in shared memory and store the box by TMA (row pitches that TMA
+//    cannot take are stored from the staged rows by the warp).
+// Tensor memory: 512 columns cannot hold two 256-column accumulators and the
+// scales, so the accumulators of even and odd tiles overlap in 64 columns
+// (0..255 and 192..447; the scales at 448). The epilogue empties those 64 first
+// and the next tile's MMAs start then.
+// Every wait is bounded (common.cuh).
+#include "common.cuh"
+#include "fp4.cuh"
+#include "gemm_fp4.cuh"
+#include "kernels.h"
+#include "tma.h"
+
+#include <algorithm>
+#include <mutex>
+
+namespace qmm {
+namespace gfp4 {
+namespace pair {
+
+constexpr int NEW = 8;
+constexpr int NT = NEW * 32 + 64;
+constexpr int NS = 5;
+constexpr int STAGE_KT = 2;                       // 128-column tiles of K a stage
+constexpr int CODE_BYTES = STAGE_KT * 8192;       // one operand's codes a stage and CTA
+constexpr int STG_BYTES = 32 * 128;               // a warp's staged rows
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t ACC1 = 192;                    // first column of odd tiles' accumulator
+constexpr uint32_t SF_COL = 448;                  // two buffers of 24 columns: A's 8, B's 16
+
+struct Shared {
+  uint64_t full[NS], empty[NS];
+  uint64_t acc_full[2];   // the pair's commit, per tile parity
+  uint64_t acc_free;      // even CTA: one arrival per epilogue warp of both CTAs and tile
+  uint64_t teardown;
+  uint32_t tmem_base;
+  int abort_flag;
+  float gb[NEW][64];      // per epilogue warp, the column scales of the 64 columns it works on (block 16)
+};
+
+enum : unsigned {
+  SITE_EMPTY = 0x510, SITE_FULL = 0x511, SITE_ACC_FULL = 0x512, SITE_ACC_FREE = 0x513, SITE_TEARDOWN = 0x514,
+  SITE_FINAL = 0x515
+};
+
+__device__ __forceinline__ void load_pair(uint32_t dst, const void* tmap, int row, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(dst),
+      "l"(tmap), "r"(0), "r"(row), "r"(bar)
+      : "memory");
+}
+
+template <int BLOCK>
+struct Cfg {
+  static constexpr int ATOMS = BLOCK == 16 ? 2 : 1;            // scale atoms per 128 columns
+  static constexpr int SF_BYTES = STAGE_KT * ATOMS * 512;      // 128 rows' scales a stage
+  static constexpr int STAGE = 2 * CODE_BYTES + 3 * SF_BYTES;  // A, B, A's scales, B's two halves
+  static constexpr size_t SMEM = (size_t)NS * STAGE + NEW * STG_BYTES + sizeof(Shared) + 1024;
+};
+static_assert(Cfg<16>::SMEM <= 232448, "shared memory per CTA");
+
+template <int BLOCK>
+__global__ void __launch_bounds__(NT, 1)
+    gemm_fp4_pair_kernel(const GemmFp4Args p, const int tma_c, const __grid_constant__ CUtensorMap tmA,
+                         const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmSA,
+                         const __grid_constant__ CUtensorMap tmSB, const __grid_constant__ CUtensorMap tmC) {
+  using C = Cfg<BLOCK>;
+  constexpr int ATOMS = C::ATOMS;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  const uint32_t stg_base = sbase + NS * C::STAGE;
+  Shared& sm = *reinterpret_cast<Shared*>(smem_raw + (sbase - raw) + NS * C::STAGE + NEW * STG_BYTES);
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int cid = (int)cluster_id_x(), ncl = (int)nclusters_x();
+  const Fp4Layout LA(p.M, p.K, BLOCK), LB(p.N, p.K, BLOCK);
+  const int m_tiles = (int)((p.M + 255) / 256), n_tiles = (int)((p.N + 255) / 256);
+  const int tiles = m_tiles * n_tiles;
+  const int my_tiles = cid < tiles ? (tiles - cid + ncl - 1) / ncl : 0;
+  const int kt = (int)LA.kt, spt = (kt + STAGE_KT - 1) / STAGE_KT;
+
+  if (t == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], 1);
+    }
+    mbar_init(&sm.acc_full[0], 1);
+    mbar_init(&sm.acc_full[1], 1);
+    mbar_init(&sm.acc_free, 2 * NEW);
+    mbar_init(&sm.teardown, 1);
+    sm.abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == NEW) {
+    tmem_alloc_pair(&sm.tmem_base, TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tbase = sm.tmem_base;
+
+  if (warp == NEW) {
+    // ---------------- pair MMA issuer (even CTA) ----------------
+    if (rank == 0 && lane == 0) {
+      constexpr uint32_t id0 = idesc_fp4(256, 256, BLOCK == 32, 0), id1 = idesc_fp4(256, 256, BLOCK == 32, 2);
+      int g = 0;
+      uint32_t sfb_i = 0;
+      bool ok = true;
+      for (int tl = 0; tl < my_tiles && ok; ++tl) {
+        // the columns shared with the previous tile's accumulator are drained, and
+        // with them (the epilogue works in order) all of this one's last tile
+        if (tl > 0) {
+          ok = mbar_wait_cluster(&sm.acc_free, (uint32_t)((tl - 1) & 1), &sm.abort_flag, p.err, SITE_ACC_FREE);
+          if (!ok) break;
+        }
+        tc_fence_after();
+        const uint32_t tacc = tbase + ((tl & 1) ? ACC1 : 0u);
+        for (int s = 0; s < spt; ++s, ++g) {
+          const int slot = g % NS;
+          ok = mbar_wait_cluster(&sm.full[slot], (uint32_t)((g / NS) & 1), &sm.abort_flag, p.err, SITE_FULL);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a = sbase + (uint32_t)slot * C::STAGE, b = a + CODE_BYTES;
+          const uint32_t fa = b + CODE_BYTES, fb = fa + C::SF_BYTES;
+          const int n = min(STAGE_KT, kt - s * STAGE_KT);
+          for (int k = 0; k < n; ++k, ++sfb_i) {
+            const uint32_t sa = tbase + SF_COL + (sfb_i & 1u) * 24u, sb = sa + 8u;
+#pragma unroll
+            for (int i = 0; i < ATOMS; ++i) {
+              cp_scales_pair(sa + i * 4, sdesc_none(fa + (k * ATOMS + i) * 512, 16u, 128u));
+              cp_scales_pair(sb + i * 8, sdesc_none(fb + (k * ATOMS + i) * 512, 16u, 128u));
+              cp_scales_pair(sb + i * 8 + 4, sdesc_none(fb + C::SF_BYTES + (k * ATOMS + i) * 512, 16u, 128u));
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {   // 64 columns of K each
+              const uint32_t off = (uint32_t)(k * 8192 + j * 4096);
+              mma_fp4_pair<BLOCK>(tacc, sdesc_none(a + off, 2048u, 128u), sdesc_none(b + off, 2048u, 128u),
+                                  (BLOCK == 32 && j) ? id1 : id0, sa + (BLOCK == 16 ? j * 4 : 0),
+                                  sb + (BLOCK == 16 ? j * 8 : 0), (s > 0 || k > 0 || j > 0) ? 1u : 0u);
+            }
+          }
+          tc_commit_pair_mc(&sm.empty[slot], 0x3);
+        }
+        if (!ok) break;
+        tc_commit_pair_mc(&sm.acc_full[tl & 1], 0x3);
+      }
+    }
+    __syncwarp();
+  } else if (warp == NEW + 1) {
+    // ---------------- producer (both CTAs) ----------------
+    if (lane == 0) {
+      prefetch_tmap(&tmA);
+      prefetch_tmap(&tmB);
+      prefetch_tmap(&tmSA);
+      prefetch_tmap(&tmSB);
+      const uint32_t full0 = mapa_shared(smem_u32(&sm.full[0]), 0);
+      int g = 0;
+      bool ok = true;
+      for (int tl = 0; tl < my_tiles && ok; ++tl) {
+        const int tile = cid + tl * ncl, mt = tile / n_tiles, nt = tile - mt * n_tiles;
+        // row tiles of this CTA (past the matrix: the last one again; its results are not stored)
+        const int ra = min(2 * mt + (int)rank, (int)LA.rt - 1), rb = min(2 * nt + (int)rank, (int)LB.rt - 1);
+        const int rb0 = 2 * nt, rb1 = min(2 * nt + 1, (int)LB.rt - 1);
+        for (int s = 0; s < spt; ++s, ++g) {
+          const int slot = g % NS;
+          if (g >= NS &&
+              !mbar_wait(&sm.empty[slot], (uint32_t)((g / NS - 1) & 1), &sm.abort_flag, p.err, SITE_EMPTY)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar = full0 + (uint32_t)slot * 8u;
+          if (rank == 0) mbar_arrive_expect_tx(&sm.full[slot], 2u * C::STAGE);
+          const uint32_t dst = sbase + (uint32_t)slot * C::STAGE;
+          // a stage that reaches past its row tile copies bytes that no MMA reads
+          load_pair(dst, &tmA, (ra * kt + s * STAGE_KT) * 8, bar);
+          load_pair(dst + CODE_BYTES, &tmB, (rb * kt + s * STAGE_KT) * 8, bar);
+          load_pair(dst + 2 * CODE_BYTES, &tmSA, (ra * kt + s * STAGE_KT) * ATOMS, bar);
+          load_pair(dst + 2 * CODE_BYTES + C::SF_BYTES, &tmSB, (rb0 * kt + s * STAGE_KT) * ATOMS, bar);
+          load_pair(dst + 2 * CODE_BYTES + 2 * C::SF_BYTES, &tmSB, (rb1 * kt + s * STAGE_KT) * ATOMS, bar);
+        }
+      }
+      // the even CTA's barriers count both CTAs' bytes: once the last stages'
+      // phases complete, no copy of either CTA is in flight
+      if (rank == 0)
+        for (int j = (g > NS ? g - NS : 0); j < g; ++j)
+          mbar_wait_cluster(&sm.full[j % NS], (uint32_t)((j / NS) & 1), nullptr, p.err, SITE_FINAL);
+    }
+    __syncwarp();
+  } else {
+    // ---------------- epilogue ----------------
+    const int q = warp & 3, h = warp >> 2;
+    const uint32_t free0 = mapa_shared(smem_u32(&sm.acc_free), 0);
+    const uint32_t stg = stg_base + (uint32_t)warp * STG_BYTES;
+    const float* rows_a = reinterpret_cast<const float*>(p.A + LA.row_off());
+    const float* rows_b = reinterpret_cast<const float*>(p.B + LB.row_off());
+    for (int tl = 0; tl < my_tiles; ++tl) {
+      const int tile = cid + tl * ncl, mt = tile / n_tiles, nt = tile - mt * n_tiles;
+      const long long row0 = (long long)mt * 256 + rank * 128 + q * 32;
+      const long long col0 = (long long)nt * 256 + h * 128;
+      float ga = 1.f, gb[4] = {};   // this lane's row scale; column scales lane, lane + 32, ...
+      if (BLOCK == 16) {
+        if (row0 + lane < p.M) ga = __ldg(rows_a + row0 + lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (col0 + i * 32 + lane < p.N) gb[i] = __ldg(rows_b + col0 + i * 32 + lane);
+      }
+      if (!mbar_wait_cluster(&sm.acc_full[tl & 1], (uint32_t)((tl >> 1) & 1), &sm.abort_flag, p.err, SITE_ACC_FULL))
+        break;
+      tc_fence_after();
+      const uint32_t tacc = tbase + ((uint32_t)(q * 32) << 16) + ((tl & 1) ? ACC1 : 0u) + (uint32_t)(h * 128);
+      // even tiles share columns 192..255 with the next accumulator, odd ones 0..63
+      const int first = (tl & 1) ? 0 : 1;
+      const bool shares = h == ((tl & 1) ? 0 : 1);
+      if (!shares) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote_cta(free0);
+      }
+#pragma unroll 1
+      for (int u = 0; u < 2; ++u) {
+        const int unit = u ^ first;   // 64 columns
+        uint32_t acc[2][32];
+        tmem_ld32x2(tacc + unit * 64, acc[0], tacc + unit * 64 + 32, acc[1]);
+        if (shares && u == 0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote_cta(free0);
+        }
+        const long long n0 = col0 + unit * 64;
+        if (row0 >= p.M || n0 >= p.N) continue;
+        if (BLOCK == 16) {
+          __syncwarp();   // the last unit's scales are read
+          sm.gb[warp][lane] = unit ? gb[2] : gb[0];
+          sm.gb[warp][lane + 32] = unit ? gb[3] : gb[1];
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            acc[i >> 5][i & 31] = __float_as_uint(
+                __fmul_rn(__fmul_rn(__uint_as_float(acc[i >> 5][i & 31]), ga), sm.gb[warp][i]));
+        }
+        store_unit(p, &tmC, tma_c, stg, acc, row0, n0, lane);
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+    tc_fence_before();
+  }
+
+  __syncthreads();
+  if (t == 0 && sm.abort_flag) st_shared_cluster_u32(mapa_shared(smem_u32(&sm.abort_flag), rank ^ 1u), 1u);
+  if (warp == NEW && rank == 0) {
+    tc_fence_after();
+    if (lane == 0) {
+      tc_commit_pair_mc(&sm.teardown, 0x1);
+      mbar_wait(&sm.teardown, 0u, nullptr, p.err, SITE_TEARDOWN);
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  if (warp == NEW) {
+    tc_fence_after();
+    tmem_dealloc_pair(tbase, TMEM_COLS);
+  }
+}
+
+template <int BLOCK>
+cudaError_t launch(const GemmFp4Args& a, cudaStream_t s) {
+  using C = Cfg<BLOCK>;
+  auto kern = gemm_fp4_pair_kernel<BLOCK>;
+  static std::mutex mu;
+  static int max_clusters[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(NT, 1, 1);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!max_clusters[dev]) {
+      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+      if (e != cudaSuccess) return e;
+      cfg.gridDim = dim3(2 * 64, 1, 1);
+      e = cudaOccupancyMaxActiveClusters(&max_clusters[dev], kern, &cfg);
+      if (e != cudaSuccess) return e;
+      if (max_clusters[dev] < 1) return cudaErrorInvalidConfiguration;
+    }
+    clusters = max_clusters[dev];
+  }
+  const Fp4Layout LA(a.M, a.K, BLOCK), LB(a.N, a.K, BLOCK);
+  CUtensorMap ta{}, tb{}, tsa{}, tsb{}, tc{};
+  // codes as rows of 1 KB (8 to a 128 x 128 tile), scales as rows of one atom
+  auto codes = [](CUtensorMap* m, const uint8_t* base, const Fp4Layout& L) {
+    return make_tmap_2d(m, base, CU_TENSOR_MAP_DATA_TYPE_INT32, 256, L.code_bytes() / 1024, 1024, 256, STAGE_KT * 8,
+                        CU_TENSOR_MAP_SWIZZLE_NONE);
+  };
+  auto scales = [](CUtensorMap* m, const uint8_t* base, const Fp4Layout& L) {
+    return make_tmap_2d(m, base + L.scale_off(), CU_TENSOR_MAP_DATA_TYPE_INT32, 128, L.scale_bytes() / 512, 512, 128,
+                        STAGE_KT * C::ATOMS, CU_TENSOR_MAP_SWIZZLE_NONE);
+  };
+  cudaError_t e = codes(&ta, a.A, LA);
+  if (e == cudaSuccess) e = codes(&tb, a.B, LB);
+  if (e == cudaSuccess) e = scales(&tsa, a.A, LA);
+  if (e == cudaSuccess) e = scales(&tsb, a.B, LB);
+  int tma_c = 0;
+  if (e == cudaSuccess) e = make_c_map(a, &tc, &tma_c);
+  if (e != cudaSuccess) return e;
+  const long long tiles = ((a.M + 255) / 256) * ((a.N + 255) / 256);
+  cfg.gridDim = dim3(2 * (unsigned)std::min<long long>(tiles, clusters), 1, 1);
+  e = cudaLaunchKernelEx(&cfg, kern, a, tma_c, ta, tb, tsa, tsb, tc);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+}  // namespace pair
+}  // namespace gfp4
+
+cudaError_t launch_gemm_fp4_pair(const GemmFp4Args& a, int block, cudaStream_t s) {
+  return block == 16 ? gfp4::pair::launch<16>(a, s) : gfp4::pair::launch<32>(a, s);
+}
+
+}  // namespace qmm

@@ -348,6 +348,7 @@ struct GemmFp4Args {
   void* C; int c_f32;          // [M][N]
   unsigned* err;
 };
+cudaError_t launch_gemm_fp4_pair(const GemmFp4Args& a, int block, cudaStream_t s);
 cudaError_t launch_gemm_fp4(const GemmFp4Args& a, int block, cudaStream_t s, const char** kernel_name);
 
 int num_sms();
