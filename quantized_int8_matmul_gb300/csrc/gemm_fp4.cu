@@ -89,28 +89,32 @@ __global__ void __launch_bounds__(NT, 1) gemm_fp4_kernel(const GemmFp4Args p) {
     }
     __syncwarp();
   } else if (warp == 4) {
-    if (lane == 0) {
-      for (int s = 0; s < stages; ++s) {
-        const int slot = s % NS;
-        if (!mbar_wait(&sm.full[slot], (uint32_t)((s / NS) & 1), &sm.abort_flag, p.err, SITE_FULL)) break;
-        tc_fence_after();
-        const int n = min(STAGE_KT, kt - s * STAGE_KT);
-        const uint32_t a = sbase + (uint32_t)slot * STAGE, b = a + CODE_BYTES;
-        const uint32_t fa = a + 2 * CODE_BYTES, fb = fa + SF_BYTES;
-        for (int i = 0; i < n * ATOMS; ++i) {
-          cp_scales(tbase + SFA_COL + i * 4, sdesc_none(fa + i * 512, 16u, 128u));
-          cp_scales(tbase + SFB_COL + i * 4, sdesc_none(fb + i * 512, 16u, 128u));
-        }
-        for (int j = 0; j < 2 * n; ++j) {   // 64 columns of K each
-          const uint64_t ad = sdesc_none(a + j * 4096, 2048u, 128u), bd = sdesc_none(b + j * 4096, 2048u, 128u);
-          const uint32_t col = BLOCK == 16 ? j * 4 : (j >> 1) * 4;
-          mma_fp4<BLOCK>(tbase, ad, bd, idesc_fp4(128, 128, BLOCK == 32, BLOCK == 32 ? (j & 1) * 2 : 0),
-                         tbase + SFA_COL + col, tbase + SFB_COL + col, (s > 0 || j > 0) ? 1u : 0u);
-        }
-        tc_commit(&sm.empty[slot]);
+    const uint32_t on = elect_one();
+    const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
+    uint32_t acc = 0u;
+    for (int s = 0; s < stages; ++s) {
+      const int slot = s % NS;
+      if (!__all_sync(0xffffffffu,
+                      mbar_wait(&sm.full[slot], (uint32_t)((s / NS) & 1), &sm.abort_flag, p.err, SITE_FULL)))
+        break;
+      tc_fence_after();
+      const int n = min(STAGE_KT, kt - s * STAGE_KT);
+      const uint32_t a = (sbase + (uint32_t)slot * STAGE) >> 4, b = a + (CODE_BYTES >> 4);
+      const uint32_t fa = b + (CODE_BYTES >> 4), fb = fa + (SF_BYTES >> 4);
+      for (int i = 0; i < n * ATOMS; ++i) {
+        cp_scales(tb + SFA_COL + i * 4, fa + i * 32, on);
+        cp_scales(tb + SFB_COL + i * 4, fb + i * 32, on);
       }
-      tc_commit(&sm.done);   // also after a wait that ran out: every MMA issued so far
+      for (int j = 0; j < 2 * n; ++j) {   // 64 columns of K each
+        const uint32_t col = BLOCK == 16 ? j * 4 : (j >> 1) * 4;
+        mma_fp4<BLOCK>(tb, a + j * 256 + kDescLo, b + j * 256 + kDescLo,
+                       idesc_fp4(128, 128, BLOCK == 32, BLOCK == 32 ? (j & 1) * 2 : 0), tb + SFA_COL + col,
+                       tb + SFB_COL + col, acc, on);
+        acc = 1u;
+      }
+      commit_on(&sm.empty[slot], on);
     }
+    commit_on(&sm.done, on);   // also after a wait that ran out: every MMA issued so far
     __syncwarp();
   } else {
     const long long row = mt * 128 + warp * 32 + lane;

@@ -9,16 +9,6 @@
 namespace qmm {
 namespace gfp4 {
 
-// Shared-memory descriptor without swizzle (K-major): lbo bytes between core
-// matrices (8 rows x 16 bytes) along K, sbo bytes between 8-row groups.
-__device__ __forceinline__ uint64_t sdesc_none(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
-  d |= (uint64_t)1 << 46;
-  return d;
-}
-
 // Instruction descriptor of the block-scaled 4-bit MMA: [4,6) B scale id,
 // [7,10) A format (1 = e2m1), [10,13) B format, [17,23) N >> 3, 23 scale type
 // (0 = ue4m3, 1 = ue8m0), [24,29) M >> 4, [29,31) A scale id; 31: K = 64. The
@@ -28,47 +18,79 @@ __host__ __device__ constexpr uint32_t idesc_fp4(int M, int N, bool e8m0, int sf
          ((uint32_t)(M >> 4) << 24) | ((uint32_t)sf_id << 29);
 }
 
+// Shared-memory descriptor without swizzle (K-major): [0,14) address / 16,
+// [16,30) bytes between core matrices along K / 16, [32,46) bytes between 8-row
+// groups / 16, 46 version. Here always 2 KB between core matrices along K and 128
+// bytes between 8-row groups (the packed layout), so the low word is
+// address / 16 + kDescLo. (The scale copies use the 8-row groups alone.)
+constexpr uint32_t kDescLo = (2048u >> 4) << 16;
+constexpr uint32_t kDescHi = (128u >> 4) | (1u << 14);
+
+// The MMA warp runs converged and one lane issues (`on` is that lane's flag):
+// addresses and descriptors then stay in uniform registers, where the
+// instructions take them from. Issued from inside a one-lane branch, every
+// operand is moved there first, and that thread's own instructions, not the
+// tensor core, set the rate.
+//
 // D[tmem] (+)= (A scaled) x (B scaled): 16 (4 scales a K step) or 32 (2) elements to a scale.
+#define QMM_FP4_MMA(GROUP, VEC)                                                                                    \
+  asm volatile(                                                                                                    \
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\t"                                                               \
+      "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 e, %7, 0;\n\t"                                                         \
+      "mov.b64 a, {%1, %8};\n\tmov.b64 b, {%2, %8};\n\t"                                                           \
+      "@e tcgen05.mma.cta_group::" GROUP ".kind::mxf4nvf4.block_scale.scale_vec::" VEC                             \
+      " [%0], a, b, %3, [%4], [%5], p;\n\t}" ::"r"(d),                                                             \
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc), "r"(on), "r"(kDescHi)                        \
+      : "memory")
 template <int BLOCK>
-__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa,
-                                        uint32_t sfb, uint32_t acc) {
-  if (BLOCK == 16)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
-        : "memory");
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t sfa,
+                                        uint32_t sfb, uint32_t acc, uint32_t on) {
+  if (BLOCK == 16) QMM_FP4_MMA("1", "4X");
+  else QMM_FP4_MMA("1", "2X");
 }
 template <int BLOCK>
-__device__ __forceinline__ void mma_fp4_pair(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa,
-                                             uint32_t sfb, uint32_t acc) {
-  if (BLOCK == 16)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
-        : "memory");
+__device__ __forceinline__ void mma_fp4_pair(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t sfa,
+                                             uint32_t sfb, uint32_t acc, uint32_t on) {
+  if (BLOCK == 16) QMM_FP4_MMA("2", "4X");
+  else QMM_FP4_MMA("2", "2X");
 }
 
-// One atom of scales (512 bytes) into four tensor-memory columns, repeated in
-// the four 32-lane quarters. Executes in order with the MMAs of the same thread.
-__device__ __forceinline__ void cp_scales(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+// One atom of scales (512 bytes at 16 * addr16) into four tensor-memory columns,
+// repeated in the four 32-lane quarters. Executes in order with the MMAs of the
+// same thread.
+__device__ __forceinline__ void cp_scales(uint32_t taddr, uint32_t addr16, uint32_t on) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .b64 a;\n\tsetp.ne.b32 e, %2, 0;\n\tmov.b64 a, {%1, %3};\n\t"
+      "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], a;\n\t}" ::"r"(taddr),
+      "r"(addr16), "r"(on), "r"(kDescHi)
+      : "memory");
 }
-__device__ __forceinline__ void cp_scales_pair(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+__device__ __forceinline__ void cp_scales_pair(uint32_t taddr, uint32_t addr16, uint32_t on) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .b64 a;\n\tsetp.ne.b32 e, %2, 0;\n\tmov.b64 a, {%1, %3};\n\t"
+      "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], a;\n\t}" ::"r"(taddr),
+      "r"(addr16), "r"(on), "r"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void commit_on(uint64_t* bar, uint32_t on) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void commit_pair_on(uint64_t* bar, uint32_t on) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %2, 0;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t on;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(on));
+  return on;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(uint32_t a, uint32_t b) {

@@ -120,49 +120,60 @@ __global__ void __launch_bounds__(NT, 1)
   const uint32_t tbase = sm.tmem_base;
 
   if (warp == NEW) {
-    // ---------------- pair MMA issuer (even CTA) ----------------
-    if (rank == 0 && lane == 0) {
+    // ---------------- pair MMA issuer (even CTA, the warp converged) ----------------
+    if (rank == 0) {
       constexpr uint32_t id0 = idesc_fp4(256, 256, BLOCK == 32, 0), id1 = idesc_fp4(256, 256, BLOCK == 32, 2);
-      int g = 0;
-      uint32_t sfb_i = 0;
+      const uint32_t on = elect_one();
+      const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
+      const uint32_t s16 = sbase >> 4;
+      int slot = 0;
+      uint32_t phase = 0u, buf = 0u;
       bool ok = true;
       for (int tl = 0; tl < my_tiles && ok; ++tl) {
         // the columns shared with the previous tile's accumulator are drained, and
         // with them (the epilogue works in order) all of this one's last tile
         if (tl > 0) {
           ok = mbar_wait_cluster(&sm.acc_free, (uint32_t)((tl - 1) & 1), &sm.abort_flag, p.err, SITE_ACC_FREE);
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
         }
         tc_fence_after();
-        const uint32_t tacc = tbase + ((tl & 1) ? ACC1 : 0u);
-        for (int s = 0; s < spt; ++s, ++g) {
-          const int slot = g % NS;
-          ok = mbar_wait_cluster(&sm.full[slot], (uint32_t)((g / NS) & 1), &sm.abort_flag, p.err, SITE_FULL);
+        const uint32_t tacc = tb + ((tl & 1) ? ACC1 : 0u);
+        uint32_t acc = 0u;
+        for (int s = 0; s < spt; ++s) {
+          ok = mbar_wait_cluster(&sm.full[slot], phase, &sm.abort_flag, p.err, SITE_FULL);
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t a = sbase + (uint32_t)slot * C::STAGE, b = a + CODE_BYTES;
-          const uint32_t fa = b + CODE_BYTES, fb = fa + C::SF_BYTES;
-          const int n = min(STAGE_KT, kt - s * STAGE_KT);
-          for (int k = 0; k < n; ++k, ++sfb_i) {
-            const uint32_t sa = tbase + SF_COL + (sfb_i & 1u) * 24u, sb = sa + 8u;
+          const uint32_t a = s16 + (uint32_t)slot * (C::STAGE >> 4), b = a + (CODE_BYTES >> 4);
+          const uint32_t fa = b + (CODE_BYTES >> 4), fb = fa + (C::SF_BYTES >> 4);
+#pragma unroll
+          for (int k = 0; k < STAGE_KT; ++k) {
+            if (k > 0 && s * STAGE_KT + k >= kt) break;
+            const uint32_t sa = tb + SF_COL + buf, sb = sa + 8u;
+            buf ^= 24u;
 #pragma unroll
             for (int i = 0; i < ATOMS; ++i) {
-              cp_scales_pair(sa + i * 4, sdesc_none(fa + (k * ATOMS + i) * 512, 16u, 128u));
-              cp_scales_pair(sb + i * 8, sdesc_none(fb + (k * ATOMS + i) * 512, 16u, 128u));
-              cp_scales_pair(sb + i * 8 + 4, sdesc_none(fb + C::SF_BYTES + (k * ATOMS + i) * 512, 16u, 128u));
+              cp_scales_pair(sa + i * 4, fa + (k * ATOMS + i) * 32, on);
+              cp_scales_pair(sb + i * 8, fb + (k * ATOMS + i) * 32, on);
+              cp_scales_pair(sb + i * 8 + 4, fb + (C::SF_BYTES >> 4) + (k * ATOMS + i) * 32, on);
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {   // 64 columns of K each
-              const uint32_t off = (uint32_t)(k * 8192 + j * 4096);
-              mma_fp4_pair<BLOCK>(tacc, sdesc_none(a + off, 2048u, 128u), sdesc_none(b + off, 2048u, 128u),
-                                  (BLOCK == 32 && j) ? id1 : id0, sa + (BLOCK == 16 ? j * 4 : 0),
-                                  sb + (BLOCK == 16 ? j * 8 : 0), (s > 0 || k > 0 || j > 0) ? 1u : 0u);
+              const uint32_t off = (uint32_t)(k * 512 + j * 256) + kDescLo;
+              mma_fp4_pair<BLOCK>(tacc, a + off, b + off, (BLOCK == 32 && j) ? id1 : id0,
+                                  sa + (BLOCK == 16 ? j * 4 : 0), sb + (BLOCK == 16 ? j * 8 : 0), acc, on);
+              acc = 1u;
             }
           }
-          tc_commit_pair_mc(&sm.empty[slot], 0x3);
+          commit_pair_on(&sm.empty[slot], on);
+          if (++slot == NS) {
+            slot = 0;
+            phase ^= 1u;
+          }
         }
         if (!ok) break;
-        tc_commit_pair_mc(&sm.acc_full[tl & 1], 0x3);
+        commit_pair_on(&sm.acc_full[tl & 1], on);
       }
     }
     __syncwarp();
