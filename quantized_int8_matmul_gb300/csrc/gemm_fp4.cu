@@ -1,53 +1,88 @@
-// The product of two packed 4-bit matrices (fp4.cuh) on the tensor cores:
+// The product of two packed 4-bit matrices (fp4.cuh) for up to 256 rows of A:
 //   C[m][n] = ((sum_k a*sa * b*sb) * ga[m]) * gb[n]
-// with codes a, b (e2m1), block scales sa, sb applied by the block-scaled MMA
-// (tcgen05.mma kind::mxf4nvf4, fp32 accumulation in tensor memory) and the row
-// scales of block 16 applied once in the epilogue (block 32 has none).
+// (the MMA and its operands as in gemm_fp4_pair.cu). A few rows of activations
+// against a weight read 0.53 or 0.56 bytes an element of the weight from HBM and
+// do little else, so the roles are swapped: 128 rows of B (columns of C) are the
+// MMA's M side, and all rows of A, rounded up to 16, its N side. Every byte of
+// the weight is read by exactly one CTA.
 //
-// One CTA per 128 x 128 tile of C: a producer warp copies each operand's codes
-// and scales with bulk copies into a ring (the packed layout is the MMA's own),
-// one thread moves the scales into tensor memory (tcgen05.cp) and issues the
-// MMAs, four warps store the tile.
+// A cluster of S CTAs shares 128 columns of C, each taking a run of K: S is
+// chosen so that about two CTAs an SM are there to stream the weight. Each CTA
+// (192 threads): warp 5 copies the weight's codes and scales (256 columns of K a
+// stage, one contiguous run each) and the rows' chunks into a ring with bulk
+// copies; warp 4 moves the scales to tensor memory and issues the MMAs; warps
+// 0-3 put the fp32 partial sums in shared memory, and after a cluster barrier
+// each CTA adds up its share of the rows over the cluster in rank order (so the
+// result does not depend on timing), scales and stores them.
+// Every wait is bounded (common.cuh).
 #include "common.cuh"
 #include "fp4.cuh"
 #include "gemm_fp4.cuh"
 #include "kernels.h"
 
 #include <algorithm>
+#include <mutex>
 
 namespace qmm {
 namespace gfp4 {
+namespace rows {
 
 constexpr int STAGE_KT = 2;                       // 128-column tiles of K per stage
-constexpr int CODE_BYTES = STAGE_KT * 8192;       // per operand
-constexpr int NS = 4;
+constexpr int CODE_BYTES = STAGE_KT * 8192;       // the weight's codes per stage
+constexpr int NS_MAX = 8;
 constexpr int NT = 192;                           // 4 epilogue warps, MMA, producer
-constexpr uint32_t TMEM_COLS = 256;
-constexpr uint32_t SFA_COL = 128, SFB_COL = 160;
 
 struct Shared {
-  uint64_t full[NS], empty[NS], done;
+  uint64_t full[NS_MAX], empty[NS_MAX], done;
   uint32_t tmem_base;
   int abort_flag;
 };
 
 enum : unsigned { SITE_EMPTY = 0x500, SITE_FULL = 0x501, SITE_DONE = 0x502 };
 
+// What the host chose for a problem.
+struct Plan {
+  int mp;        // rows of A rounded up to 16
+  int ns;        // ring stages
+  int split;     // CTAs of a cluster (each a run of K)
+  int stage;     // bytes of a stage
+  int tmem;      // tensor memory columns
+  size_t smem;
+};
+
 template <int BLOCK>
-__global__ void __launch_bounds__(NT, 1) gemm_fp4_kernel(const GemmFp4Args p) {
-  constexpr int ATOMS = BLOCK == 16 ? 2 : 1;      // scale atoms per 128 columns of K
-  constexpr int SF_BYTES = STAGE_KT * ATOMS * 512;
-  constexpr int STAGE = 2 * CODE_BYTES + 2 * SF_BYTES;
+struct Cfg {
+  static constexpr int ATOMS = BLOCK == 16 ? 2 : 1;
+  static constexpr int SF_BYTES = STAGE_KT * ATOMS * 512;
+};
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
+  return v;
+}
+
+template <int BLOCK>
+__global__ void __launch_bounds__(NT) gemm_fp4_rows_kernel(const GemmFp4Args p, const Plan pl) {
+  constexpr int ATOMS = Cfg<BLOCK>::ATOMS, SF_BYTES = Cfg<BLOCK>::SF_BYTES;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t sbase = (raw + 1023u) & ~1023u;
-  Shared& sm = *reinterpret_cast<Shared*>(smem_raw + (sbase - raw) + NS * STAGE);
+  const uint32_t sbase = (raw + 127u) & ~127u;
+  uint8_t* sptr = smem_raw + (sbase - raw);
+  Shared& sm = *reinterpret_cast<Shared*>(sptr + (size_t)pl.ns * pl.stage);
   const Fp4Layout LA(p.M, p.K, BLOCK), LB(p.N, p.K, BLOCK);
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  const long long mt = blockIdx.x / LB.rt, nt = blockIdx.x - mt * LB.rt;
-  const int kt = (int)LA.kt, stages = (kt + STAGE_KT - 1) / STAGE_KT;
+  const int rank = pl.split > 1 ? (int)cluster_ctarank() : 0;
+  const long long nt = blockIdx.x / pl.split;
+  const int kt = (int)LA.kt, stages_all = (kt + STAGE_KT - 1) / STAGE_KT;
+  const int s0 = (int)((long long)stages_all * rank / pl.split);
+  const int s1 = (int)((long long)stages_all * (rank + 1) / pl.split);
+  const int mp = pl.mp, mt = (mp + 127) >> 7;      // row tiles of A
+  const uint32_t sf_col = (uint32_t)(mp + 31) & ~31u;
   if (t == 0) {
-    for (int i = 0; i < NS; ++i) {
+    for (int i = 0; i < pl.ns; ++i) {
       mbar_init(&sm.full[i], 1);
       mbar_init(&sm.empty[i], 1);
     }
@@ -56,104 +91,235 @@ __global__ void __launch_bounds__(NT, 1) gemm_fp4_kernel(const GemmFp4Args p) {
     fence_mbarrier_init();
   }
   if (warp == 4) {
-    tmem_alloc(&sm.tmem_base, TMEM_COLS);
+    tmem_alloc(&sm.tmem_base, (uint32_t)pl.tmem);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = sm.tmem_base;
+  // launched as a programmatic dependent: what is above ran under the call before
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
   if (warp == 5) {
+    // ---------------- producer ----------------
     if (lane == 0) {
-      const uint8_t* ca = p.A + (size_t)mt * kt * 8192;
-      const uint8_t* cb = p.B + (size_t)nt * kt * 8192;
-      const uint8_t* fa = p.A + LA.scale_off() + (size_t)mt * kt * ATOMS * 512;
-      const uint8_t* fb = p.B + LB.scale_off() + (size_t)nt * kt * ATOMS * 512;
-      int s = 0;
-      for (; s < stages; ++s) {
-        const int slot = s % NS;
-        if (s >= NS &&
-            !mbar_wait(&sm.empty[slot], (uint32_t)((s / NS - 1) & 1), &sm.abort_flag, p.err, SITE_EMPTY))
-          break;
+      const uint8_t* wc = p.B + (size_t)nt * kt * 8192;
+      const uint8_t* wf = p.B + LB.scale_off() + (size_t)nt * kt * ATOMS * 512;
+      const uint8_t* xf = p.A + LA.scale_off();
+      int slot = 0;
+      uint32_t phase = 1u;   // a fresh ring slot is empty
+      int s = s0;
+      for (; s < s1; ++s) {
+        if (s - s0 >= pl.ns && !mbar_wait(&sm.empty[slot], phase, &sm.abort_flag, p.err, SITE_EMPTY)) break;
         const int n = min(STAGE_KT, kt - s * STAGE_KT);
-        const uint32_t dst = sbase + (uint32_t)slot * STAGE;
-        mbar_arrive_expect_tx(&sm.full[slot], (uint32_t)n * 2u * (8192u + ATOMS * 512u));
-        bulk_load(dst, ca + (size_t)s * CODE_BYTES, n * 8192, &sm.full[slot]);
-        bulk_load(dst + CODE_BYTES, cb + (size_t)s * CODE_BYTES, n * 8192, &sm.full[slot]);
-        bulk_load(dst + 2 * CODE_BYTES, fa + (size_t)s * SF_BYTES, n * ATOMS * 512, &sm.full[slot]);
-        bulk_load(dst + 2 * CODE_BYTES + SF_BYTES, fb + (size_t)s * SF_BYTES, n * ATOMS * 512, &sm.full[slot]);
+        const uint32_t dst = sbase + (uint32_t)(slot * pl.stage);
+        uint64_t* bar = &sm.full[slot];
+        mbar_arrive_expect_tx(bar, (uint32_t)n * (8192u + (uint32_t)mp * 64u + (uint32_t)((1 + mt) * ATOMS * 512)));
+        bulk_load(dst, wc + (size_t)s * CODE_BYTES, n * 8192, bar);
+        bulk_load(dst + CODE_BYTES, wf + (size_t)s * SF_BYTES, n * ATOMS * 512, bar);
+        const uint32_t df = dst + CODE_BYTES + SF_BYTES, dx = df + (uint32_t)(mt * SF_BYTES);
+        for (int i = 0; i < mt; ++i) {
+          const size_t tile = (size_t)i * kt + (size_t)s * STAGE_KT;
+          bulk_load(df + i * SF_BYTES, xf + tile * ATOMS * 512, n * ATOMS * 512, bar);
+          const uint32_t bytes = (uint32_t)min(128, mp - i * 128) * 16u;
+          for (int c = 0; c < 4 * n; ++c)
+            bulk_load(dx + (uint32_t)(c * mp * 16 + i * 2048), p.A + tile * 8192 + c * 2048, bytes, bar);
+        }
+        if (++slot == pl.ns) {
+          slot = 0;
+          phase ^= 1u;
+        }
       }
       // no copy is left in flight when the CTA ends
-      for (int j = (s > NS ? s - NS : 0); j < s; ++j)
-        mbar_wait(&sm.full[j % NS], (uint32_t)((j / NS) & 1), nullptr, p.err, SITE_FULL);
+      for (int j = (s - s0 > pl.ns ? s - pl.ns : s0); j < s; ++j)
+        mbar_wait(&sm.full[(j - s0) % pl.ns], (uint32_t)(((j - s0) / pl.ns) & 1), nullptr, p.err, SITE_FULL);
     }
     __syncwarp();
   } else if (warp == 4) {
+    // ---------------- MMA issuer (the warp converged) ----------------
     const uint32_t on = elect_one();
     const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
-    uint32_t acc = 0u;
-    for (int s = 0; s < stages; ++s) {
-      const int slot = s % NS;
-      if (!__all_sync(0xffffffffu,
-                      mbar_wait(&sm.full[slot], (uint32_t)((s / NS) & 1), &sm.abort_flag, p.err, SITE_FULL)))
-        break;
+    const uint32_t id0 = idesc_fp4(128, 0, BLOCK == 32, 0) | ((uint32_t)(mp >> 3) << 17);
+    const uint32_t id1 = idesc_fp4(128, 0, BLOCK == 32, 2) | ((uint32_t)(mp >> 3) << 17);
+    const uint32_t s16 = desc_addr(sbase);
+    const uint32_t x_lbo = (uint32_t)mp << 16;      // bytes between A's chunks / 16
+    const uint32_t sa0 = tb + sf_col, sb0 = sa0 + STAGE_KT * ATOMS * 4;
+    int slot = 0;
+    uint32_t phase = 0u, acc = 0u;
+    for (int s = s0; s < s1; ++s) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&sm.full[slot], phase, &sm.abort_flag, p.err, SITE_FULL))) break;
       tc_fence_after();
+      const uint32_t w = s16 + (uint32_t)(slot * pl.stage >> 4), wf = w + (CODE_BYTES >> 4);
+      const uint32_t xf = wf + (SF_BYTES >> 4), x = xf + (uint32_t)(mt * SF_BYTES >> 4);
       const int n = min(STAGE_KT, kt - s * STAGE_KT);
-      const uint32_t a = (sbase + (uint32_t)slot * STAGE) >> 4, b = a + (CODE_BYTES >> 4);
-      const uint32_t fa = b + (CODE_BYTES >> 4), fb = fa + (SF_BYTES >> 4);
-      for (int i = 0; i < n * ATOMS; ++i) {
-        cp_scales(tb + SFA_COL + i * 4, fa + i * 32, on);
-        cp_scales(tb + SFB_COL + i * 4, fb + i * 32, on);
-      }
-      for (int j = 0; j < 2 * n; ++j) {   // 64 columns of K each
-        const uint32_t col = BLOCK == 16 ? j * 4 : (j >> 1) * 4;
-        mma_fp4<BLOCK>(tb, a + j * 256 + kDescLo, b + j * 256 + kDescLo,
-                       idesc_fp4(128, 128, BLOCK == 32, BLOCK == 32 ? (j & 1) * 2 : 0), tb + SFA_COL + col,
-                       tb + SFB_COL + col, acc, on);
-        acc = 1u;
+#pragma unroll
+      for (int k = 0; k < STAGE_KT; ++k) {
+        if (k >= n) break;
+#pragma unroll
+        for (int i = 0; i < ATOMS; ++i) {
+          const int q = k * ATOMS + i;
+          cp_scales(sa0 + q * 4, wf + q * 32, on);
+          cp_scales(sb0 + q * mt * 4, xf + q * 32, on);
+          if (mt > 1) cp_scales(sb0 + q * mt * 4 + 4, xf + (SF_BYTES >> 4) + q * 32, on);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {   // 64 columns of K each: two chunks
+          const int q = BLOCK == 16 ? k * 2 + j : k;
+          mma_fp4<BLOCK>(tb, w + (uint32_t)(k * 512 + j * 256) + kDescLo, x + (uint32_t)((k * 4 + j * 2) * mp) + x_lbo,
+                         (BLOCK == 32 && j) ? id1 : id0, sa0 + q * 4, sb0 + q * mt * 4, acc, on);
+          acc = 1u;
+        }
       }
       commit_on(&sm.empty[slot], on);
+      if (++slot == pl.ns) {
+        slot = 0;
+        phase ^= 1u;
+      }
     }
     commit_on(&sm.done, on);   // also after a wait that ran out: every MMA issued so far
     __syncwarp();
-  } else {
-    const long long row = mt * 128 + warp * 32 + lane;
-    const bool ok = mbar_wait(&sm.done, 0u, nullptr, p.err, SITE_DONE, 4 * kWaitLimitNs);
-    tc_fence_after();
-    const float ga = (BLOCK == 16 && row < p.M) ? reinterpret_cast<const float*>(p.A + LA.row_off())[row] : 1.f;
-    for (int g = 0; g < 4; ++g) {
-      uint32_t acc[32];
-      tmem_ld32(tbase + ((uint32_t)(warp * 32) << 16) + g * 32, acc);
-      for (int i = 0; i < 32; ++i) {
-        const long long n = nt * 128 + g * 32 + i;
-        if (!ok || sm.abort_flag || row >= p.M || n >= p.N) continue;
-        float v = __uint_as_float(acc[i]);
-        if (BLOCK == 16)
-          v = __fmul_rn(__fmul_rn(v, ga), __ldg(reinterpret_cast<const float*>(p.B + LB.row_off()) + n));
-        if (p.c_f32) static_cast<float*>(p.C)[row * p.N + n] = v;
-        else static_cast<__nv_bfloat16*>(p.C)[row * p.N + n] = __float2bfloat16_rn(v);
-      }
+  }
+  // ---------------- partial sums to shared memory: part[m][128] ----------------
+  const bool ok = mbar_wait(&sm.done, 0u, nullptr, p.err, SITE_DONE, 4 * kWaitLimitNs);
+  tc_fence_after();
+  // the ring is free: every copy has landed (the MMAs that completed waited for
+  // them all, or the producer did before this barrier)
+  __syncthreads();
+  float* part = reinterpret_cast<float*>(sptr);
+  if (warp < 4 && ok) {
+    for (int g = 0; g < mp; g += 16) {
+      uint32_t acc[16];
+      tmem_ld16(tbase + ((uint32_t)(warp * 32) << 16) + g, acc);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) part[(g + i) * 128 + warp * 32 + lane] = __uint_as_float(acc[i]);
     }
     tc_fence_before();
   }
-  __syncthreads();
+  if (pl.split > 1) cluster_sync_all();
+  else __syncthreads();
+  // ---------------- this CTA's rows: sum over the cluster, scale, store ----------------
+  const long long n0 = nt * 128 + lane * 4;
+  float gb[4] = {1.f, 1.f, 1.f, 1.f};
+  if (BLOCK == 16) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n0 + e < p.N) gb[e] = __ldg(reinterpret_cast<const float*>(p.B + LB.row_off()) + n0 + e);
+  }
+  const bool v4 = (p.N & 3) == 0 && (reinterpret_cast<uintptr_t>(p.C) & 15) == 0;
+  if (ok && !sm.abort_flag) {
+    for (int m = rank + warp * pl.split; m < p.M; m += (NT / 32) * pl.split) {
+      const uint32_t local = sbase + (uint32_t)(m * 512 + lane * 16);
+      float4 v = pl.split > 1 ? ld_cluster_f4(mapa_shared(local, 0)) : *reinterpret_cast<const float4*>(part + m * 128 + lane * 4);
+      for (int r = 1; r < pl.split; ++r) {
+        const float4 o = ld_cluster_f4(mapa_shared(local, (uint32_t)r));
+        v.x += o.x;
+        v.y += o.y;
+        v.z += o.z;
+        v.w += o.w;
+      }
+      if (BLOCK == 16) {
+        const float ga = __ldg(reinterpret_cast<const float*>(p.A + LA.row_off()) + m);
+        v.x = __fmul_rn(__fmul_rn(v.x, ga), gb[0]);
+        v.y = __fmul_rn(__fmul_rn(v.y, ga), gb[1]);
+        v.z = __fmul_rn(__fmul_rn(v.z, ga), gb[2]);
+        v.w = __fmul_rn(__fmul_rn(v.w, ga), gb[3]);
+      }
+      if (n0 >= p.N) continue;
+      if (p.c_f32) {
+        float* c = static_cast<float*>(p.C) + (long long)m * p.N + n0;
+        if (v4) {
+          *reinterpret_cast<float4*>(c) = v;
+        } else {
+          const float e[4] = {v.x, v.y, v.z, v.w};
+          for (int i = 0; i < 4 && n0 + i < p.N; ++i) c[i] = e[i];
+        }
+      } else {
+        __nv_bfloat16* c = static_cast<__nv_bfloat16*>(p.C) + (long long)m * p.N + n0;
+        const uint32_t lo = pack_bf16(__float_as_uint(v.x), __float_as_uint(v.y));
+        const uint32_t hi = pack_bf16(__float_as_uint(v.z), __float_as_uint(v.w));
+        if (v4) {
+          *reinterpret_cast<uint2*>(c) = make_uint2(lo, hi);
+        } else {
+          const uint32_t w[2] = {lo, hi};
+          for (int i = 0; i < 4 && n0 + i < p.N; ++i)
+            reinterpret_cast<uint16_t*>(c)[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+        }
+      }
+    }
+  }
+  if (pl.split > 1) cluster_sync_all();   // the others have read this CTA's sums
+  else __syncthreads();
   if (warp == 4) {
     tc_fence_after();
-    tmem_dealloc(tbase, TMEM_COLS);
+    tmem_dealloc(tbase, (uint32_t)pl.tmem);
   }
+}
+
+// Ring and split for a problem. Up to 128 rows leave room for two CTAs an SM
+// (their rings and tensor memory); more take one. The split is the smallest of
+// 1, 2, 4, 8 that puts two CTAs on every SM (one, above 128 rows), as long as
+// every CTA keeps two stages.
+template <int BLOCK>
+Plan make_plan(const GemmFp4Args& a) {
+  Plan pl;
+  const Fp4Layout LB(a.N, a.K, BLOCK);
+  pl.mp = (int)((a.M + 15) / 16 * 16);
+  const int mt = (pl.mp + 127) / 128;
+  const int sf = Cfg<BLOCK>::SF_BYTES;
+  pl.stage = CODE_BYTES + sf * (1 + mt) + pl.mp * 16 * 4 * STAGE_KT;
+  const int per_sm = pl.mp <= 128 ? 2 : 1;
+  const int budget = per_sm == 2 ? 110 * 1024 : 222 * 1024;
+  pl.ns = std::max(2, std::min(NS_MAX, budget / pl.stage));
+  const int part = pl.mp * 512;   // the partial sums take the ring's place
+  while (pl.ns * pl.stage < part) ++pl.ns;
+  const int cols = ((pl.mp + 31) & ~31) + STAGE_KT * Cfg<BLOCK>::ATOMS * 4 * (1 + mt);
+  pl.tmem = cols <= 64 ? 64 : cols <= 128 ? 128 : cols <= 256 ? 256 : 512;
+  const long long stages = (LB.kt + STAGE_KT - 1) / STAGE_KT;
+  pl.split = 1;
+  while (pl.split < 8 && LB.rt * pl.split < (long long)per_sm * num_sms() && stages >= 4 * pl.split) pl.split *= 2;
+  pl.smem = (size_t)pl.ns * pl.stage + sizeof(Shared) + 128;
+  return pl;
 }
 
 template <int BLOCK>
 cudaError_t launch(const GemmFp4Args& a, cudaStream_t s) {
-  constexpr int ATOMS = BLOCK == 16 ? 2 : 1;
-  const size_t smem = NS * (2 * CODE_BYTES + 2 * STAGE_KT * ATOMS * 512) + sizeof(Shared) + 1024;
-  cudaError_t e = cudaFuncSetAttribute(gemm_fp4_kernel<BLOCK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  auto kern = gemm_fp4_rows_kernel<BLOCK>;
+  static std::mutex mu;
+  static bool ready[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!ready[dev]) {
+      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+      if (e != cudaSuccess) return e;
+      ready[dev] = true;
+    }
+  }
+  const Plan pl = make_plan<BLOCK>(a);
+  const Fp4Layout LB(a.N, a.K, BLOCK);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)pl.split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(LB.rt * pl.split), 1, 1);
+  cfg.blockDim = dim3(NT, 1, 1);
+  cfg.dynamicSmemBytes = pl.smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, pl);
   if (e != cudaSuccess) return e;
-  const Fp4Layout LA(a.M, a.K, BLOCK), LB(a.N, a.K, BLOCK);
-  gemm_fp4_kernel<BLOCK><<<(unsigned)(LA.rt * LB.rt), NT, smem, s>>>(a);
   return cudaGetLastError();
 }
 
+}  // namespace rows
 }  // namespace gfp4
 
 cudaError_t launch_gemm_fp4(const GemmFp4Args& a, int block, cudaStream_t s, const char** kernel_name) {
@@ -161,8 +327,8 @@ cudaError_t launch_gemm_fp4(const GemmFp4Args& a, int block, cudaStream_t s, con
     *kernel_name = "gemm_fp4_pair";
     return launch_gemm_fp4_pair(a, block, s);
   }
-  *kernel_name = "gemm_fp4";
-  return block == 16 ? gfp4::launch<16>(a, s) : gfp4::launch<32>(a, s);
+  *kernel_name = "gemm_fp4_rows";
+  return block == 16 ? gfp4::rows::launch<16>(a, s) : gfp4::rows::launch<32>(a, s);
 }
 
 }  // namespace qmm

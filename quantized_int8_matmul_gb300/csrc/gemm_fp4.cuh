@@ -23,6 +23,9 @@ __host__ __device__ constexpr uint32_t idesc_fp4(int M, int N, bool e8m0, int sf
 // groups / 16, 46 version. Here always 2 KB between core matrices along K and 128
 // bytes between 8-row groups (the packed layout), so the low word is
 // address / 16 + kDescLo. (The scale copies use the 8-row groups alone.)
+// A shared address as a descriptor holds it. In a cluster the addresses of CTAs
+// past the first have higher bits set, which would land in the next field.
+__device__ __forceinline__ uint32_t desc_addr(uint32_t saddr) { return (saddr >> 4) & 0x3FFFu; }
 constexpr uint32_t kDescLo = (2048u >> 4) << 16;
 constexpr uint32_t kDescHi = (128u >> 4) | (1u << 14);
 

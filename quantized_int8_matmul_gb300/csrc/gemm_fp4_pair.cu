@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(NT, 1)
       constexpr uint32_t id0 = idesc_fp4(256, 256, BLOCK == 32, 0), id1 = idesc_fp4(256, 256, BLOCK == 32, 2);
       const uint32_t on = elect_one();
       const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
-      const uint32_t s16 = sbase >> 4;
+      const uint32_t s16 = desc_addr(sbase);
       int slot = 0;
       uint32_t phase = 0u, buf = 0u;
       bool ok = true;
