@@ -20,6 +20,7 @@
 
 #include <algorithm>
 #include <cuda_fp8.h>
+#include <mutex>
 
 namespace qmm {
 namespace fp4 {
@@ -77,42 +78,74 @@ __device__ __forceinline__ uint8_t block_scale(unsigned max_bits, float u, float
 }
 
 template <typename T>
-__device__ __forceinline__ float ld1(const T* p);
-template <>
-__device__ __forceinline__ float ld1<float>(const float* p) { return __ldg(p); }
-template <>
-__device__ __forceinline__ float ld1<__nv_bfloat16>(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float ld1(const T* p) { return (float)*p; }
 
-// Elements [k, k + 8) of a row of n (k a multiple of 8; past the end: 0).
+// Eight consecutive elements as they lie in memory.
 template <typename T>
-__device__ __forceinline__ void load8(const T* row, long long k, long long n, bool vec, float (&v)[8]) {
-  if (vec && k + 8 <= n) {
-    if (sizeof(T) == 2) {
-      const uint4 r = *reinterpret_cast<const uint4*>(row + k);
-      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 r;
+  // elements [k, k + 8) of a row of n (k a multiple of 8; past the end: 0)
+  __device__ __forceinline__ void load(const __nv_bfloat16* row, long long k, long long n, bool vec) {
+    if (vec && k + 8 <= n) {
+      r = *reinterpret_cast<const uint4*>(row + k);
+    } else {
+      uint32_t w[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        const uint16_t* s = reinterpret_cast<const uint16_t*>(row) + k + 2 * i;
+        w[i] = (k + 2 * i < n ? (uint32_t)s[0] : 0u) | (k + 2 * i + 1 < n ? (uint32_t)s[1] << 16 : 0u);
       }
-    } else {
-      const float4 a = *reinterpret_cast<const float4*>(row + k);
-      const float4 b = *(reinterpret_cast<const float4*>(row + k) + 1);
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+      r = make_uint4(w[0], w[1], w[2], w[3]);
     }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = k + e < n ? ld1(row + k + e) : 0.f;
   }
-}
-
-__device__ __forceinline__ unsigned max8(const float (&v)[8]) {
-  unsigned m = 0u;
+  __device__ __forceinline__ void floats(float (&v)[8]) const {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-  for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7fffffffu);
-  return m;
-}
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  // bits of the largest magnitude as a float (a NaN is above infinity)
+  __device__ __forceinline__ unsigned max_bits() const {
+    const unsigned a = pair_max(pair_max(r.x, r.y), pair_max(r.z, r.w));
+    return max(a << 16, a & 0x7fff0000u);
+  }
+  static __device__ __forceinline__ uint32_t pair_max(uint32_t a, uint32_t b) {
+    // magnitudes of finite bf16 values, infinities and NaNs are ordered as integers
+    return __vmaxu2(a & 0x7fff7fffu, b & 0x7fff7fffu);
+  }
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* row, long long k, long long n, bool vec) {
+    if (vec && k + 8 <= n) {
+      a = *reinterpret_cast<const float4*>(row + k);
+      b = *(reinterpret_cast<const float4*>(row + k) + 1);
+    } else {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = k + e < n ? row[k + e] : 0.f;
+      a = make_float4(v[0], v[1], v[2], v[3]);
+      b = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  }
+  __device__ __forceinline__ void floats(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+  __device__ __forceinline__ unsigned max_bits() const {
+    float v[8];
+    floats(v);
+    unsigned m = 0u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7fffffffu);
+    return m;
+  }
+};
 
 // The maximum over the lanes that share a block: 4 lanes of 8 elements for 32,
 // 2 for 16.
@@ -124,260 +157,405 @@ __device__ __forceinline__ unsigned block_max(unsigned m) {
 }
 
 // ---------------------------------------------------------------------------
-// Along the rows. A CTA takes eight rows of a tile, {2c, 2c + 1} + {0, 32, 64,
-// 96}, a warp 32 columns of them at a time: lane l holds 8 columns of row l / 4.
-// Rows chosen so make every 32-byte sector of codes (two neighbouring rows'
-// 16 bytes) and of scales (two rows' 16-byte lines of an atom, whose 4-byte
-// parts are rows 32 apart) the work of one CTA.
+// Along the rows. A CTA takes the rows {2c, 2c + 1} + {0, 32, 64, 96} of a tile
+// (J = 4: a warp step is 32 columns of eight rows, 8 columns a lane) or, for
+// matrices of up to 32 rows, {2c, 2c + 1} (J = 1: 128 columns of two rows). Rows
+// chosen so make every 32-byte sector of codes (two neighbouring rows' 16 bytes)
+// and of scales (two rows' 16-byte lines of an atom, whose 4-byte parts are rows
+// 32 apart) the work of one CTA. A warp's steps of a batch (ITER) are loaded
+// together; with block 16 a row whose steps are one batch stays in registers
+// between its maximum and its codes, longer rows are read again.
 // ---------------------------------------------------------------------------
-template <typename T, int BLOCK>
-__global__ void quantize_rows_kernel(const Fp4QuantArgs p) {
+template <typename T, int BLOCK, int J, int ITER>
+__global__ void __launch_bounds__(1024) quantize_rows_kernel(const Fp4QuantArgs p, const int staged) {
+  constexpr int ATOMS = BLOCK == 16 ? 2 : 1;
   constexpr int SPC = 32 / BLOCK;   // scales per 32-column chunk
+  constexpr int UC = J == 4 ? 1 : 4;   // chunks a warp step
   __shared__ unsigned rowmax[8];
+  extern __shared__ __align__(16) uint8_t sfs[];   // [atom][2 rows][4 rows 32 apart][4] (staged)
   const Fp4Layout L(p.rows, p.cols, BLOCK);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const long long tile = blockIdx.x >> 4;
-  const int rin = 2 * (blockIdx.x & 15) + ((lane >> 2) & 1) + 32 * (lane >> 3);
+  const int c2 = 2 * (blockIdx.x & 15);
+  const int ra = J == 4 ? (lane >> 2) & 1 : lane >> 4, rj = J == 4 ? lane >> 3 : 0;
+  const int piece = J == 4 ? lane & 3 : lane & 15;
+  const int rin = c2 + ra + 32 * rj;
   const long long row = tile * 128 + rin;
-  if (tile * 128 + 2 * (blockIdx.x & 15) >= p.rows) return;
+  if (tile * 128 + c2 >= p.rows) return;
   const bool rv = row < p.rows;
   const T* x = static_cast<const T*>(p.x) + (rv ? row : 0) * p.ld;
   const long long n = rv ? p.cols : 0;
   const bool vec = p.vec;
-  const int chunks = (int)(L.kt * 4);
+  const int units = (int)(L.kt * 4 / UC);
+  const int batches = (units + nw * ITER - 1) / (nw * ITER);
+  Raw8<T> v[ITER];
+  auto load = [&](int b) {
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+      const int u = (b * ITER + i) * nw + warp;   // past the end: columns past n, zeros
+      v[i].load(x, (long long)u * (32 * UC) + piece * 8, n, vec);
+    }
+  };
   float u = 1.f;
   if (BLOCK == 16) {
     if (threadIdx.x < 8) rowmax[threadIdx.x] = 0u;
     __syncthreads();
     unsigned m = 0u;
-    for (int c = warp; c < chunks; c += nw) {
-      float v[8];
-      load8(x, (long long)c * 32 + (lane & 3) * 8, n, vec, v);
-      m = max(m, max8(v));
-    }
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    if ((lane & 3) == 0) atomicMax(&rowmax[lane >> 2], m);
-    __syncthreads();
-    const float g = row_scale(rowmax[lane >> 2]);
-    u = __fdiv_rn(1.f, g);
-    if (warp == 0 && (lane & 3) == 0 && rv) reinterpret_cast<float*>(p.out + L.row_off())[row] = g;
-  }
-  uint8_t* codes = p.out + (size_t)tile * L.kt * 8192 + rin * 16 + (lane & 3) * 4;
-  uint8_t* sf = p.out + L.scale_off() + (size_t)tile * L.kt * 512 * L.atoms() + (rin & 31) * 16 + (rin >> 5) * 4;
-  for (int c = warp; c < chunks; c += nw) {
-    float v[8];
-    load8(x, (long long)c * 32 + (lane & 3) * 8, n, vec, v);
-    float mul = 0.f;
-    bool zero;
-    const uint8_t s = block_scale<BLOCK>(block_max<BLOCK>(max8(v)), u, mul, zero);
+    for (int b = 0; b < batches; ++b) {
+      load(b);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(v[e], mul);
-    const uint32_t code = zero ? 0u : e2m1x8(v);
-    if (rv) {
-      *reinterpret_cast<uint32_t*>(codes + (size_t)c * 2048) = code;
-      const int k = c * SPC + (BLOCK == 16 ? (lane & 3) >> 1 : 0);
-      if ((lane & (BLOCK == 16 ? 1 : 3)) == 0) sf[(size_t)(k >> 2) * 512 + (k & 3)] = s;
+      for (int i = 0; i < ITER; ++i) m = max(m, v[i].max_bits());
     }
+#pragma unroll
+    for (int o = 1; o < 4 * UC; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (piece == 0) atomicMax(&rowmax[rj * 2 + ra], m);
+    __syncthreads();
+    const float g = row_scale(rowmax[rj * 2 + ra]);
+    u = __fdiv_rn(1.f, g);
+    if (warp == 0 && piece == 0 && rv) reinterpret_cast<float*>(p.out + L.row_off())[row] = g;
+  }
+  uint8_t* codes = p.out + (size_t)tile * L.kt * 8192 + rin * 16 + (piece & 3) * 4;
+  uint8_t* sf = p.out + L.scale_off() + (size_t)tile * L.kt * 512 * ATOMS + c2 * 16;
+  for (int b = 0; b < batches; ++b) {
+    if (BLOCK == 32 || batches > 1) load(b);
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+      const int un = (b * ITER + i) * nw + warp;
+      float mul = 0.f, f[8];
+      bool zero;
+      const uint8_t s = block_scale<BLOCK>(block_max<BLOCK>(v[i].max_bits()), u, mul, zero);
+      v[i].floats(f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(f[e], mul);
+      const uint32_t code = zero ? 0u : e2m1x8(f);
+      const int ch = un * UC + (piece >> 2);
+      if (un < units) {
+        const int k = ch * SPC + (BLOCK == 16 ? (piece & 3) >> 1 : 0);
+        const int off = ra * 16 + rj * 4 + (k & 3);
+        const bool mine = (piece & (BLOCK == 16 ? 1 : 3)) == 0;
+        if (rv) *reinterpret_cast<uint32_t*>(codes + (size_t)ch * 2048) = code;
+        if (mine && staged) sfs[(k >> 2) * 32 + off] = s;
+        if (mine && !staged && rv) sf[(size_t)(k >> 2) * 512 + off] = s;
+      }
+    }
+  }
+  if (staged) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < (int)L.kt * ATOMS * 2; i += blockDim.x)
+      *reinterpret_cast<uint4*>(sf + (size_t)(i >> 1) * 512 + (i & 1) * 16) = reinterpret_cast<const uint4*>(sfs)[i];
   }
 }
 
 // ---------------------------------------------------------------------------
 // Along the columns, or both ways: x is [rows][cols] in memory; the packed
-// matrix along the columns is its transpose [cols][rows]. A CTA takes a tile of
-// 128 x 128 of x through shared memory.
+// matrix along the columns is its transpose [cols][rows].
 // ---------------------------------------------------------------------------
-// Largest magnitudes of the columns (and the rows) into the packed buffers' max words.
+// Largest magnitudes of the columns (and the rows) into the packed buffers' max
+// words: 64 rows x 256 columns a CTA, eight columns a lane.
 template <typename T>
-__global__ void absmax_kernel(const Fp4QuantArgs p, unsigned* colmax, unsigned* rowmax) {
+__global__ void __launch_bounds__(256) absmax_kernel(const Fp4QuantArgs p, unsigned* colmax, unsigned* rowmax) {
+  __shared__ unsigned cm[256];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int kt = (int)((p.cols + 127) / 128), ty = blockIdx.x / kt, tx = blockIdx.x - ty * kt;
-  const long long c0 = (long long)tx * 128, r0 = (long long)ty * 128;
-  unsigned cm[4] = {0u, 0u, 0u, 0u};
-  for (int i = warp; i < 128; i += 8) {
-    const long long r = r0 + i;
-    if (r >= p.rows) break;
-    unsigned rm = 0u;
+  const int ct = (int)((p.cols + 255) / 256), ty = blockIdx.x / ct, tx = blockIdx.x - ty * ct;
+  const long long c = (long long)tx * 256, r0 = (long long)ty * 64 + warp;
+  cm[threadIdx.x] = 0u;
+  __syncthreads();
+  if (p.vec) {
+    unsigned m[8] = {};
+    Raw8<T> v[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const long long c = c0 + j * 32 + lane;
-      const unsigned b =
-          c < p.cols ? __float_as_uint(ld1(static_cast<const T*>(p.x) + r * p.ld + c)) & 0x7fffffffu : 0u;
-      cm[j] = max(cm[j], b);
-      rm = max(rm, b);
+    for (int i = 0; i < 8; ++i) {
+      const long long r = r0 + 8 * i;
+      v[i].load(static_cast<const T*>(p.x) + (r < p.rows ? r : 0) * p.ld, c + lane * 8, r < p.rows ? p.cols : 0, true);
     }
-    if (rowmax) {
-      rm = __reduce_max_sync(0xffffffffu, rm);
-      if (lane == 0) atomicMax(rowmax + r, rm);
-    }
-  }
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const long long c = c0 + j * 32 + lane;
-    if (c < p.cols) atomicMax(colmax + c, cm[j]);
+    for (int i = 0; i < 8; ++i) {
+      float f[8];
+      v[i].floats(f);
+      unsigned rm = 0u;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const unsigned b = __float_as_uint(f[e]) & 0x7fffffffu;
+        m[e] = max(m[e], b);
+        rm = max(rm, b);
+      }
+      if (rowmax) {
+        rm = __reduce_max_sync(0xffffffffu, rm);
+        if (lane == 0 && r0 + 8 * i < p.rows) atomicMax(rowmax + r0 + 8 * i, rm);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) atomicMax(&cm[lane * 8 + e], m[e]);
+  } else {   // rows that no vector load can take: neighbouring lanes, neighbouring columns
+    unsigned m[8] = {};
+    for (int i = 0; i < 8; ++i) {
+      const long long r = r0 + 8 * i;
+      if (r >= p.rows) break;
+      unsigned rm = 0u;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const long long k = c + e * 32 + lane;
+        const unsigned b =
+            k < p.cols ? __float_as_uint(ld1(static_cast<const T*>(p.x) + r * p.ld + k)) & 0x7fffffffu : 0u;
+        m[e] = max(m[e], b);
+        rm = max(rm, b);
+      }
+      if (rowmax) {
+        rm = __reduce_max_sync(0xffffffffu, rm);
+        if (lane == 0) atomicMax(rowmax + r, rm);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) atomicMax(&cm[e * 32 + lane], m[e]);
   }
+  __syncthreads();
+  if (c + threadIdx.x < p.cols) atomicMax(colmax + c + threadIdx.x, cm[threadIdx.x]);
 }
+
+// One tile of 128 x 128 of x a CTA: its rows are quantised as they are loaded
+// (ROWS), all of it goes to shared memory, and its columns are quantised from
+// there. Codes and scales leave as whole tiles by bulk copies.
+template <typename T>
+struct TileSmem {
+  static constexpr int PITCH = 128 * (int)sizeof(T) + 16;   // bytes; 16 more keep row accesses off each other's banks
+  static constexpr int CODES = 128 * PITCH;                 // two tiles of codes, then of scales
+  static constexpr int SCALES = CODES + 2 * 8192;
+  static constexpr int BYTES = SCALES + 2 * 1024;
+};
 
 template <typename T, int BLOCK, bool ROWS>
 __global__ void __launch_bounds__(256) quantize_tile_kernel(const Fp4QuantArgs p) {
+  using S = TileSmem<T>;
+  constexpr int ATOMS = BLOCK == 16 ? 2 : 1;
   constexpr int SPC = 32 / BLOCK;
-  extern __shared__ __align__(16) uint8_t smem[];
-  T* tile = reinterpret_cast<T*>(smem);   // [128][128]
-  __shared__ __align__(16) uint8_t sfs[1024];
+  constexpr int CW = 4 / sizeof(T);   // columns in a 32-bit word
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint8_t* codes_c = smem + S::CODES;
+  uint8_t* codes_r = codes_c + 8192;
+  uint8_t* sf_c = smem + S::SCALES;
+  uint8_t* sf_r = sf_c + 1024;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const Fp4Layout Lr(p.rows, p.cols, BLOCK), Lc(p.cols, p.rows, BLOCK);
   const int ty = blockIdx.x / (int)Lr.kt, tx = blockIdx.x - ty * (int)Lr.kt;
   const long long c0 = (long long)tx * 128, r0 = (long long)ty * 128;
   const size_t ti = blockIdx.x;                       // this tile in the packed rows
   const size_t tc = (size_t)tx * Lc.kt + ty;          // and in the packed columns
-  // rows of x: quantised as they are loaded
-#pragma unroll 2
-  for (int it = 0; it < 8; ++it) {
-    const int item = it * 8 + warp, ch = item & 3, grp = item >> 2;
-    const int rin = 2 * grp + ((lane >> 2) & 1) + 32 * (lane >> 3);
-    const long long row = r0 + rin;
-    const bool rv = row < p.rows;
-    const int k = ch * 32 + (lane & 3) * 8;
-    float v[8];
-    load8(static_cast<const T*>(p.x) + (rv ? row : 0) * p.ld, c0 + k, rv ? p.cols : 0, p.vec, v);
-    T* d = tile + rin * 128 + k;
+  // a warp step: 8 rows x 32 columns; warp w takes rows 8w .. 8w + 7 of each 64
+  Raw8<T> v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) d[e] = (T)v[e];
+  for (int i = 0; i < 8; ++i) {
+    const int rin = (i >> 2) * 64 + warp * 8 + (lane >> 2), k = (i & 3) * 32 + (lane & 3) * 8;
+    const bool rv = r0 + rin < p.rows;
+    v[i].load(static_cast<const T*>(p.x) + (rv ? r0 + rin : 0) * p.ld, c0 + k, rv ? p.cols : 0, p.vec);
+  }
+  float u = 1.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int ch = i & 3, rin = (i >> 2) * 64 + warp * 8 + (lane >> 2), k = ch * 32 + (lane & 3) * 8;
+    *reinterpret_cast<Raw8<T>*>(smem + rin * S::PITCH + k * sizeof(T)) = v[i];
     if (ROWS) {
-      float u = 1.f, mul = 0.f;
-      if (BLOCK == 16) {
-        const float g = row_scale(rv ? reinterpret_cast<const unsigned*>(p.out_rows + Lr.max_off())[row] : 0u);
+      if (BLOCK == 16 && ch == 0) {
+        const bool rv = r0 + rin < p.rows;
+        const float g = row_scale(rv ? reinterpret_cast<const unsigned*>(p.out_rows + Lr.max_off())[r0 + rin] : 0u);
         u = __fdiv_rn(1.f, g);
-        if (c0 == 0 && ch == 0 && (lane & 3) == 0 && rv) reinterpret_cast<float*>(p.out_rows + Lr.row_off())[row] = g;
+        if (c0 == 0 && (lane & 3) == 0 && rv) reinterpret_cast<float*>(p.out_rows + Lr.row_off())[r0 + rin] = g;
       }
+      float mul = 0.f, f[8];
       bool zero;
-      const uint8_t s = block_scale<BLOCK>(block_max<BLOCK>(max8(v)), u, mul, zero);
+      const uint8_t s = block_scale<BLOCK>(block_max<BLOCK>(v[i].max_bits()), u, mul, zero);
+      v[i].floats(f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(v[e], mul);
-      const uint32_t code = zero ? 0u : e2m1x8(v);
-      *reinterpret_cast<uint32_t*>(p.out_rows + ti * 8192 + ch * 2048 + rin * 16 + (lane & 3) * 4) = code;
+      for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(f[e], mul);
+      *reinterpret_cast<uint32_t*>(codes_r + ch * 2048 + rin * 16 + (lane & 3) * 4) = zero ? 0u : e2m1x8(f);
       const int ks = ch * SPC + (BLOCK == 16 ? (lane & 3) >> 1 : 0);
       if ((lane & (BLOCK == 16 ? 1 : 3)) == 0)
-        sfs[(ks >> 2) * 512 + (rin & 31) * 16 + (rin >> 5) * 4 + (ks & 3)] = s;
+        sf_r[(ks >> 2) * 512 + (rin & 31) * 16 + (rin >> 5) * 4 + (ks & 3)] = s;
     }
   }
   __syncthreads();
-  if (ROWS) {
-    if (t < 32 * Lr.atoms())
-      reinterpret_cast<uint4*>(p.out_rows + Lr.scale_off() + ti * 512 * Lr.atoms())[t] =
-          reinterpret_cast<const uint4*>(sfs)[t];
-    __syncthreads();
-  }
-  // columns: one column and 32 rows at a time
-  for (int item = t; item < 512; item += 256) {
-    const int c = item & 127, ch = item >> 7;
-    const bool cv = c0 + c < p.cols;
-    float u = 1.f;
-    if (BLOCK == 16) {
-      const float g = row_scale(cv ? reinterpret_cast<const unsigned*>(p.out + Lc.max_off())[c0 + c] : 0u);
-      u = __fdiv_rn(1.f, g);
-      if (r0 == 0 && ch == 0 && cv) reinterpret_cast<float*>(p.out + Lc.row_off())[c0 + c] = g;
+  // a work item: 32 rows of the column(s) in one 32-bit word
+#pragma unroll 1
+  for (int item = t; item < 4 * 128 / CW; item += 256) {
+    const int cw = item % (128 / CW), ch = item / (128 / CW);
+    float uc[CW];
+#pragma unroll
+    for (int w = 0; w < CW; ++w) {
+      uc[w] = 1.f;
+      if (BLOCK == 16) {
+        const long long c = c0 + cw * CW + w;
+        const float g = row_scale(c < p.cols ? reinterpret_cast<const unsigned*>(p.out + Lc.max_off())[c] : 0u);
+        uc[w] = __fdiv_rn(1.f, g);
+        if (r0 == 0 && ch == 0 && c < p.cols) reinterpret_cast<float*>(p.out + Lc.row_off())[c] = g;
+      }
     }
-    uint32_t code[4];
+    uint32_t code[CW][4];
 #pragma unroll
     for (int b = 0; b < SPC; ++b) {
-      float v[BLOCK];
-      unsigned m = 0u;
+      uint32_t x[BLOCK], m = 0u;
 #pragma unroll
       for (int e = 0; e < BLOCK; ++e) {
-        v[e] = (float)tile[(ch * 32 + b * BLOCK + e) * 128 + c];
-        m = max(m, __float_as_uint(v[e]) & 0x7fffffffu);
+        x[e] = *reinterpret_cast<const uint32_t*>(smem + (ch * 32 + b * BLOCK + e) * S::PITCH + cw * 4);
+        m = CW == 2 ? __vmaxu2(m, x[e] & 0x7fff7fffu) : max(m, x[e] & 0x7fffffffu);
       }
-      float mul = 0.f;
-      bool zero;
-      const uint8_t s = block_scale<BLOCK>(m, u, mul, zero);
-      const int ks = ch * SPC + b;
-      sfs[(ks >> 2) * 512 + (c & 31) * 16 + (c >> 5) * 4 + (ks & 3)] = s;
 #pragma unroll
-      for (int q = 0; q < BLOCK / 8; ++q) {
-        float w[8];
+      for (int w = 0; w < CW; ++w) {
+        const unsigned mb = CW == 1 ? m : w == 0 ? m << 16 : m & 0x7fff0000u;
+        float mul = 0.f;
+        bool zero;
+        const uint8_t s = block_scale<BLOCK>(mb, uc[w], mul, zero);
+        const int ks = ch * SPC + b, c = cw * CW + w;
+        sf_c[(ks >> 2) * 512 + (c & 31) * 16 + (c >> 5) * 4 + (ks & 3)] = s;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = __fmul_rn(v[q * 8 + e], mul);
-        code[b * (BLOCK / 8) + q] = zero ? 0u : e2m1x8(w);
+        for (int q = 0; q < BLOCK / 8; ++q) {
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t xe = x[q * 8 + e];
+            f[e] = __fmul_rn(__uint_as_float(CW == 1 ? xe : w == 0 ? xe << 16 : xe & 0xffff0000u), mul);
+          }
+          code[w][b * (BLOCK / 8) + q] = zero ? 0u : e2m1x8(f);
+        }
       }
     }
-    *reinterpret_cast<uint4*>(p.out + tc * 8192 + ch * 2048 + c * 16) =
-        make_uint4(code[0], code[1], code[2], code[3]);
+#pragma unroll
+    for (int w = 0; w < CW; ++w)
+      *reinterpret_cast<uint4*>(codes_c + ch * 2048 + (cw * CW + w) * 16) =
+          make_uint4(code[w][0], code[w][1], code[w][2], code[w][3]);
   }
+  fence_proxy_async_smem();   // this thread's writes, visible to the copy engine
   __syncthreads();
-  if (t < 32 * Lc.atoms())
-    reinterpret_cast<uint4*>(p.out + Lc.scale_off() + tc * 512 * Lc.atoms())[t] =
-        reinterpret_cast<const uint4*>(sfs)[t];
+  if (t == 0) {
+    bulk_store(p.out + tc * 8192, smem_u32(codes_c), 8192);
+    bulk_store(p.out + Lc.scale_off() + tc * (512 * ATOMS), smem_u32(sf_c), 512 * ATOMS);
+    if (ROWS) {
+      bulk_store(p.out_rows + ti * 8192, smem_u32(codes_r), 8192);
+      bulk_store(p.out_rows + Lr.scale_off() + ti * (512 * ATOMS), smem_u32(sf_r), 512 * ATOMS);
+    }
+    bulk_commit();
+    bulk_wait_all();
+  }
 }
 
 // ---------------------------------------------------------------------------
 // Reading back: y[r][c] = code * block scale (* row scale), one CTA per tile.
 // ---------------------------------------------------------------------------
-// Eight codes to floats: code c is the fp16 value whose bits are the sign and
-// c's three low bits moved to exponent and mantissa, times 2^14.
-__device__ __forceinline__ void decode8(uint32_t w, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t c = (w >> (4 * i)) & 15u;
-    const float m = __half2float(__ushort_as_half((unsigned short)((c & 7u) << 9))) * 16384.f;
-    v[i] = (c & 8u) ? -m : m;
-  }
+// A code as a float: its three low bits moved to the exponent and mantissa of an
+// fp16 value are that value times 2^-14.
+__device__ __forceinline__ float decode(uint32_t c) {
+  const float m = __half2float(__ushort_as_half((unsigned short)((c & 7u) << 9))) * 16384.f;
+  return (c & 8u) ? -m : m;
 }
 
-template <typename T, int BLOCK>
-__global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* packed, long long rows, long long cols, T* y,
-                                                         int vec) {
+template <typename T, int BLOCK, bool VEC>
+__global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* packed, long long rows, long long cols, T* y) {
+  constexpr int ATOMS = BLOCK == 16 ? 2 : 1;
   const Fp4Layout L(rows, cols, BLOCK);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const size_t ti = blockIdx.x;
   const int ty = blockIdx.x / (int)L.kt, tx = blockIdx.x - ty * (int)L.kt;
-  const uint8_t* sf = packed + L.scale_off() + ti * 512 * L.atoms();
-  for (int it = 0; it < 8; ++it) {
-    const int item = it * 8 + warp, ch = item & 3, grp = item >> 2;
-    const int rin = 8 * grp + (lane >> 2);
-    const long long row = (long long)ty * 128 + rin;
-    const long long k = (long long)tx * 128 + ch * 32 + (lane & 3) * 8;
-    if (row >= rows || k >= cols) continue;
-    const uint32_t w =
-        *reinterpret_cast<const uint32_t*>(packed + ti * 8192 + ch * 2048 + rin * 16 + (lane & 3) * 4);
-    const int ks = ch * (32 / BLOCK) + (BLOCK == 16 ? (lane & 3) >> 1 : 0);
-    const uint8_t sb = sf[(ks >> 2) * 512 + (rin & 31) * 16 + (rin >> 5) * 4 + (ks & 3)];
-    const float s = BLOCK == 16 ? e4m3_to_f(sb) : e8m0_to_f(sb);
-    const float g = BLOCK == 16 ? reinterpret_cast<const float*>(packed + L.row_off())[row] : 1.f;
-    float v[8];
-    decode8(w, v);
+  const uint8_t* codes = packed + ti * 8192;
+  const uint8_t* sf = packed + L.scale_off() + ti * (512 * ATOMS);
+  const float* gs = reinterpret_cast<const float*>(packed + L.row_off()) + (long long)ty * 128;
+  const long long r0 = (long long)ty * 128, c0 = (long long)tx * 128;
+  if (VEC) {   // 8 rows x 32 columns a warp step, eight columns a lane
+    uint32_t w[8];
+    uint8_t sb[8];
+    float g[2] = {1.f, 1.f};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      v[e] = __fmul_rn(v[e], s);
-      if (BLOCK == 16) v[e] = __fmul_rn(v[e], g);
+    for (int i = 0; i < 8; ++i) {
+      const int ch = i & 3, rin = (i >> 2) * 64 + warp * 8 + (lane >> 2);
+      const int ks = ch * (32 / BLOCK) + (BLOCK == 16 ? (lane & 3) >> 1 : 0);
+      w[i] = *reinterpret_cast<const uint32_t*>(codes + ch * 2048 + rin * 16 + (lane & 3) * 4);
+      sb[i] = sf[(ks >> 2) * 512 + (rin & 31) * 16 + (rin >> 5) * 4 + (ks & 3)];
+      if (BLOCK == 16 && ch == 0 && r0 + rin < rows) g[i >> 2] = gs[rin];
     }
-    T* out = y + row * cols + k;
-    if (vec && k + 8 <= cols) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int ch = i & 3, rin = (i >> 2) * 64 + warp * 8 + (lane >> 2);
+      const long long row = r0 + rin, k = c0 + ch * 32 + (lane & 3) * 8;
+      if (row >= rows || k >= cols) continue;
+      const float s = BLOCK == 16 ? e4m3_to_f(sb[i]) : e8m0_to_f(sb[i]);
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[e] = __fmul_rn(decode(w[i] >> (4 * e)), s);
+        if (BLOCK == 16) v[e] = __fmul_rn(v[e], g[i >> 2]);
+      }
+      T* out = y + row * cols + k;   // cols is a multiple of 16 bytes: 8 columns lie inside, or 4 of float32
       if (sizeof(T) == 2) {
         uint32_t o[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-          o[i] = *reinterpret_cast<uint32_t*>(&b);
+        for (int e = 0; e < 4; ++e) {
+          __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+          o[e] = *reinterpret_cast<uint32_t*>(&b);
         }
         *reinterpret_cast<uint4*>(out) = make_uint4(o[0], o[1], o[2], o[3]);
       } else {
         reinterpret_cast<float4*>(out)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(out)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        if (k + 4 < cols) reinterpret_cast<float4*>(out)[1] = make_float4(v[4], v[5], v[6], v[7]);
       }
-    } else {
+    }
+  } else {   // one row a warp step, neighbouring lanes neighbouring columns
+    for (int i = 0; i < 16; ++i) {
+      const int rin = warp * 16 + i;
+      if (r0 + rin >= rows) break;
+      const float g = BLOCK == 16 ? gs[rin] : 1.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (k + e < cols) out[e] = (T)v[e];
+      for (int ch = 0; ch < 4; ++ch) {
+        const long long k = c0 + ch * 32 + lane;
+        if (k >= cols) continue;
+        const uint32_t c = codes[ch * 2048 + rin * 16 + (lane >> 1)] >> (4 * (lane & 1));
+        const int ks = ch * (32 / BLOCK) + (BLOCK == 16 ? lane >> 4 : 0);
+        const uint8_t sb = sf[(ks >> 2) * 512 + (rin & 31) * 16 + (rin >> 5) * 4 + (ks & 3)];
+        float v = __fmul_rn(decode(c), BLOCK == 16 ? e4m3_to_f(sb) : e8m0_to_f(sb));
+        if (BLOCK == 16) v = __fmul_rn(v, g);
+        y[(r0 + rin) * cols + k] = (T)v;
+      }
     }
   }
 }
 
+// Steps a warp loads together and warps a CTA: about 16 warps, eight steps of
+// bf16 or four of float32 at most (the registers of 1024 threads).
+template <typename T, int BLOCK, int J>
+cudaError_t launch_rows_j(const Fp4QuantArgs& a, cudaStream_t s) {
+  const Fp4Layout L(a.rows, a.cols, BLOCK);
+  const long long units = L.kt * (J == 4 ? 4 : 1);
+  constexpr int MOST = sizeof(T) == 2 ? 8 : 4;
+  int iter = 1;
+  while (iter < MOST && units > 16 * iter) iter *= 2;
+  const int nw = (int)std::min<long long>(32, std::max<long long>(4, (units + iter - 1) / iter));
+  size_t smem = (size_t)L.kt * L.atoms() * 32;
+  const int staged = smem <= 40 * 1024;
+  if (!staged) smem = 0;
+  const unsigned grid = (unsigned)(L.rt * 16);
+  switch (iter) {
+    case 1: quantize_rows_kernel<T, BLOCK, J, 1><<<grid, nw * 32, smem, s>>>(a, staged); break;
+    case 2: quantize_rows_kernel<T, BLOCK, J, 2><<<grid, nw * 32, smem, s>>>(a, staged); break;
+    case 4: quantize_rows_kernel<T, BLOCK, J, 4><<<grid, nw * 32, smem, s>>>(a, staged); break;
+    default: quantize_rows_kernel<T, BLOCK, J, MOST><<<grid, nw * 32, smem, s>>>(a, staged); break;
+  }
+  return cudaGetLastError();
+}
+
 template <typename T, int BLOCK>
 cudaError_t launch_rows(const Fp4QuantArgs& a, cudaStream_t s) {
-  const Fp4Layout L(a.rows, a.cols, BLOCK);
-  const int threads = (int)std::min<long long>(512, std::max<long long>(128, L.kt * 4 * 32));
-  quantize_rows_kernel<T, BLOCK><<<(unsigned)(L.rt * 16), threads, 0, s>>>(a);
+  return a.rows <= 32 ? launch_rows_j<T, BLOCK, 1>(a, s) : launch_rows_j<T, BLOCK, 4>(a, s);
+}
+
+template <typename T, int BLOCK, bool ROWS>
+cudaError_t launch_tile(const Fp4QuantArgs& a, unsigned grid, cudaStream_t s) {
+  static std::once_flag once[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  auto kern = quantize_tile_kernel<T, BLOCK, ROWS>;
+  std::call_once(once[dev], [&] {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TileSmem<T>::BYTES);
+  });
+  if (e != cudaSuccess) return e;
+  kern<<<grid, 256, TileSmem<T>::BYTES, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -385,29 +563,27 @@ template <typename T, int BLOCK>
 cudaError_t launch_tiles(const Fp4QuantArgs& a, cudaStream_t s) {
   const Fp4Layout Lr(a.rows, a.cols, BLOCK), Lc(a.cols, a.rows, BLOCK);
   const unsigned grid = (unsigned)(Lr.kt * Lr.rt);
-  cudaError_t e = cudaSuccess;
   if (BLOCK == 16) {
     unsigned* cm = reinterpret_cast<unsigned*>(a.out + Lc.max_off());
     unsigned* rm = a.out_rows ? reinterpret_cast<unsigned*>(a.out_rows + Lr.max_off()) : nullptr;
-    e = cudaMemsetAsync(cm, 0, (size_t)Lc.rt * 512, s);
+    cudaError_t e = cudaMemsetAsync(cm, 0, (size_t)Lc.rt * 512, s);
     if (e == cudaSuccess && rm) e = cudaMemsetAsync(rm, 0, (size_t)Lr.rt * 512, s);
     if (e != cudaSuccess) return e;
-    absmax_kernel<T><<<grid, 256, 0, s>>>(a, cm, rm);
+    const long long ctas = ((a.cols + 255) / 256) * ((a.rows + 63) / 64);
+    absmax_kernel<T><<<(unsigned)ctas, 256, 0, s>>>(a, cm, rm);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  const size_t smem = 128 * 128 * sizeof(T);
-  if (a.out_rows) {
-    e = cudaFuncSetAttribute(quantize_tile_kernel<T, BLOCK, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem);
-    if (e != cudaSuccess) return e;
-    quantize_tile_kernel<T, BLOCK, true><<<grid, 256, smem, s>>>(a);
-  } else {
-    e = cudaFuncSetAttribute(quantize_tile_kernel<T, BLOCK, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem);
-    if (e != cudaSuccess) return e;
-    quantize_tile_kernel<T, BLOCK, false><<<grid, 256, smem, s>>>(a);
-  }
+  return a.out_rows ? launch_tile<T, BLOCK, true>(a, grid, s) : launch_tile<T, BLOCK, false>(a, grid, s);
+}
+
+template <typename T, int BLOCK>
+cudaError_t launch_dequantize(const uint8_t* in, long long rows, long long cols, void* y, cudaStream_t s) {
+  const Fp4Layout L(rows, cols, BLOCK);
+  const unsigned grid = (unsigned)(L.kt * L.rt);
+  const bool vec = (reinterpret_cast<uintptr_t>(y) % 16) == 0 && (cols * (long long)sizeof(T)) % 16 == 0;
+  if (vec) dequantize_kernel<T, BLOCK, true><<<grid, 256, 0, s>>>(in, rows, cols, static_cast<T*>(y));
+  else dequantize_kernel<T, BLOCK, false><<<grid, 256, 0, s>>>(in, rows, cols, static_cast<T*>(y));
   return cudaGetLastError();
 }
 
@@ -433,20 +609,12 @@ cudaError_t launch_fp4_dequantize(const void* packed, long long rows, long long 
                                   cudaStream_t s, const char** kernel_name) {
   using namespace fp4;
   *kernel_name = "fp4_dequantize";
-  const Fp4Layout L(rows, cols, block);
-  const unsigned grid = (unsigned)(L.kt * L.rt);
   const uint8_t* in = static_cast<const uint8_t*>(packed);
-  const int vec = (reinterpret_cast<uintptr_t>(y) % 16) == 0 && (cols * (bf16 ? 2 : 4)) % 16 == 0;
-  if (bf16) {
-    auto* o = static_cast<__nv_bfloat16*>(y);
-    if (block == 16) dequantize_kernel<__nv_bfloat16, 16><<<grid, 256, 0, s>>>(in, rows, cols, o, vec);
-    else dequantize_kernel<__nv_bfloat16, 32><<<grid, 256, 0, s>>>(in, rows, cols, o, vec);
-  } else {
-    auto* o = static_cast<float*>(y);
-    if (block == 16) dequantize_kernel<float, 16><<<grid, 256, 0, s>>>(in, rows, cols, o, vec);
-    else dequantize_kernel<float, 32><<<grid, 256, 0, s>>>(in, rows, cols, o, vec);
-  }
-  return cudaGetLastError();
+  if (bf16)
+    return block == 16 ? launch_dequantize<__nv_bfloat16, 16>(in, rows, cols, y, s)
+                       : launch_dequantize<__nv_bfloat16, 32>(in, rows, cols, y, s);
+  return block == 16 ? launch_dequantize<float, 16>(in, rows, cols, y, s)
+                     : launch_dequantize<float, 32>(in, rows, cols, y, s);
 }
 
 }  // namespace qmm

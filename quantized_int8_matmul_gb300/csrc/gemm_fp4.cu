@@ -1,4 +1,4 @@
-// The product of two packed 4-bit matrices (fp4.cuh) for up to 256 rows of A:
+// The product of two packed 4-bit matrices (fp4.cuh) for up to 64 rows of A:
 //   C[m][n] = ((sum_k a*sa * b*sb) * ga[m]) * gb[n]
 // (the MMA and its operands as in gemm_fp4_pair.cu). A few rows of activations
 // against a weight read 0.53 or 0.56 bytes an element of the weight from HBM and
@@ -6,8 +6,8 @@
 // MMA's M side, and all rows of A, rounded up to 16, its N side. Every byte of
 // the weight is read by exactly one CTA.
 //
-// A cluster of S CTAs shares 128 columns of C, each taking a run of K: S is
-// chosen so that about two CTAs an SM are there to stream the weight. Each CTA
+// A cluster of S CTAs shares 128 columns of C, each taking a run of K: S is the
+// largest (up to 8) that keeps all CTAs resident at once, two an SM. Each CTA
 // (192 threads): warp 5 copies the weight's codes and scales (256 columns of K a
 // stage, one contiguous run each) and the rows' chunks into a ring with bulk
 // copies; warp 4 moves the scales to tensor memory and issues the MMAs; warps
@@ -65,7 +65,7 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
 }
 
 template <int BLOCK>
-__global__ void __launch_bounds__(NT) gemm_fp4_rows_kernel(const GemmFp4Args p, const Plan pl) {
+__global__ void __launch_bounds__(NT, 2) gemm_fp4_rows_kernel(const GemmFp4Args p, const Plan pl) {
   constexpr int ATOMS = Cfg<BLOCK>::ATOMS, SF_BYTES = Cfg<BLOCK>::SF_BYTES;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(NT) gemm_fp4_rows_kernel(const GemmFp4Args p, 
   const int kt = (int)LA.kt, stages_all = (kt + STAGE_KT - 1) / STAGE_KT;
   const int s0 = (int)((long long)stages_all * rank / pl.split);
   const int s1 = (int)((long long)stages_all * (rank + 1) / pl.split);
-  const int mp = pl.mp, mt = (mp + 127) >> 7;      // row tiles of A
+  const int mp = pl.mp;
   const uint32_t sf_col = (uint32_t)(mp + 31) & ~31u;
   if (t == 0) {
     for (int i = 0; i < pl.ns; ++i) {
@@ -115,17 +115,13 @@ __global__ void __launch_bounds__(NT) gemm_fp4_rows_kernel(const GemmFp4Args p, 
         const int n = min(STAGE_KT, kt - s * STAGE_KT);
         const uint32_t dst = sbase + (uint32_t)(slot * pl.stage);
         uint64_t* bar = &sm.full[slot];
-        mbar_arrive_expect_tx(bar, (uint32_t)n * (8192u + (uint32_t)mp * 64u + (uint32_t)((1 + mt) * ATOMS * 512)));
+        mbar_arrive_expect_tx(bar, (uint32_t)n * (8192u + (uint32_t)mp * 64u + 2u * ATOMS * 512u));
         bulk_load(dst, wc + (size_t)s * CODE_BYTES, n * 8192, bar);
         bulk_load(dst + CODE_BYTES, wf + (size_t)s * SF_BYTES, n * ATOMS * 512, bar);
-        const uint32_t df = dst + CODE_BYTES + SF_BYTES, dx = df + (uint32_t)(mt * SF_BYTES);
-        for (int i = 0; i < mt; ++i) {
-          const size_t tile = (size_t)i * kt + (size_t)s * STAGE_KT;
-          bulk_load(df + i * SF_BYTES, xf + tile * ATOMS * 512, n * ATOMS * 512, bar);
-          const uint32_t bytes = (uint32_t)min(128, mp - i * 128) * 16u;
-          for (int c = 0; c < 4 * n; ++c)
-            bulk_load(dx + (uint32_t)(c * mp * 16 + i * 2048), p.A + tile * 8192 + c * 2048, bytes, bar);
-        }
+        bulk_load(dst + CODE_BYTES + SF_BYTES, xf + (size_t)s * SF_BYTES, n * ATOMS * 512, bar);
+        for (int c = 0; c < 4 * n; ++c)
+          bulk_load(dst + CODE_BYTES + 2 * SF_BYTES + (uint32_t)(c * mp * 16),
+                    p.A + (size_t)s * CODE_BYTES + c * 2048, (uint32_t)mp * 16u, bar);
         if (++slot == pl.ns) {
           slot = 0;
           phase ^= 1u;
@@ -151,7 +147,7 @@ __global__ void __launch_bounds__(NT) gemm_fp4_rows_kernel(const GemmFp4Args p, 
       if (!__all_sync(0xffffffffu, mbar_wait(&sm.full[slot], phase, &sm.abort_flag, p.err, SITE_FULL))) break;
       tc_fence_after();
       const uint32_t w = s16 + (uint32_t)(slot * pl.stage >> 4), wf = w + (CODE_BYTES >> 4);
-      const uint32_t xf = wf + (SF_BYTES >> 4), x = xf + (uint32_t)(mt * SF_BYTES >> 4);
+      const uint32_t xf = wf + (SF_BYTES >> 4), x = xf + (SF_BYTES >> 4);
       const int n = min(STAGE_KT, kt - s * STAGE_KT);
 #pragma unroll
       for (int k = 0; k < STAGE_KT; ++k) {
@@ -160,14 +156,13 @@ __global__ void __launch_bounds__(NT) gemm_fp4_rows_kernel(const GemmFp4Args p, 
         for (int i = 0; i < ATOMS; ++i) {
           const int q = k * ATOMS + i;
           cp_scales(sa0 + q * 4, wf + q * 32, on);
-          cp_scales(sb0 + q * mt * 4, xf + q * 32, on);
-          if (mt > 1) cp_scales(sb0 + q * mt * 4 + 4, xf + (SF_BYTES >> 4) + q * 32, on);
+          cp_scales(sb0 + q * 4, xf + q * 32, on);
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {   // 64 columns of K each: two chunks
           const int q = BLOCK == 16 ? k * 2 + j : k;
           mma_fp4<BLOCK>(tb, w + (uint32_t)(k * 512 + j * 256) + kDescLo, x + (uint32_t)((k * 4 + j * 2) * mp) + x_lbo,
-                         (BLOCK == 32 && j) ? id1 : id0, sa0 + q * 4, sb0 + q * mt * 4, acc, on);
+                         (BLOCK == 32 && j) ? id1 : id0, sa0 + q * 4, sb0 + q * 4, acc, on);
           acc = 1u;
         }
       }
@@ -256,28 +251,23 @@ __global__ void __launch_bounds__(NT) gemm_fp4_rows_kernel(const GemmFp4Args p, 
   }
 }
 
-// Ring and split for a problem. Up to 128 rows leave room for two CTAs an SM
-// (their rings and tensor memory); more take one. The split is the smallest of
-// 1, 2, 4, 8 that puts two CTAs on every SM (one, above 128 rows), as long as
-// every CTA keeps two stages.
+// Ring and split for a problem: two CTAs an SM (their rings and tensor memory),
+// and the largest split that keeps every CTA resident at once, each with two
+// stages at least. 1 x 28672 x 8192 (224 column tiles): 22.3 us with a split of
+// 1, 29.8 with 2 (448 CTAs, a second wave); 1 x 4096 x 4096 (32 tiles): 12.0
+// with 1, 6.6 with 4, 6.9 with 8.
 template <int BLOCK>
 Plan make_plan(const GemmFp4Args& a) {
   Plan pl;
   const Fp4Layout LB(a.N, a.K, BLOCK);
   pl.mp = (int)((a.M + 15) / 16 * 16);
-  const int mt = (pl.mp + 127) / 128;
   const int sf = Cfg<BLOCK>::SF_BYTES;
-  pl.stage = CODE_BYTES + sf * (1 + mt) + pl.mp * 16 * 4 * STAGE_KT;
-  const int per_sm = pl.mp <= 128 ? 2 : 1;
-  const int budget = per_sm == 2 ? 110 * 1024 : 222 * 1024;
-  pl.ns = std::max(2, std::min(NS_MAX, budget / pl.stage));
-  const int part = pl.mp * 512;   // the partial sums take the ring's place
-  while (pl.ns * pl.stage < part) ++pl.ns;
-  const int cols = ((pl.mp + 31) & ~31) + STAGE_KT * Cfg<BLOCK>::ATOMS * 4 * (1 + mt);
-  pl.tmem = cols <= 64 ? 64 : cols <= 128 ? 128 : cols <= 256 ? 256 : 512;
+  pl.stage = CODE_BYTES + 2 * sf + pl.mp * 16 * 4 * STAGE_KT;
+  pl.ns = std::min(NS_MAX, 110 * 1024 / pl.stage);   // at least 3; the partial sums (mp * 512) fit in one stage or two
+  const int cols = ((pl.mp + 31) & ~31) + 2 * STAGE_KT * Cfg<BLOCK>::ATOMS * 4;
+  pl.tmem = cols <= 64 ? 64 : 128;
   const long long stages = (LB.kt + STAGE_KT - 1) / STAGE_KT;
-  pl.split = 1;
-  while (pl.split < 8 && LB.rt * pl.split < (long long)per_sm * num_sms() && stages >= 4 * pl.split) pl.split *= 2;
+  pl.split = (int)std::max<long long>(1, std::min({8ll, 2ll * num_sms() / LB.rt, stages / 2}));
   pl.smem = (size_t)pl.ns * pl.stage + sizeof(Shared) + 128;
   return pl;
 }
@@ -323,7 +313,10 @@ cudaError_t launch(const GemmFp4Args& a, cudaStream_t s) {
 }  // namespace gfp4
 
 cudaError_t launch_gemm_fp4(const GemmFp4Args& a, int block, cudaStream_t s, const char** kernel_name) {
-  if (a.M > 256) {
+  // Above 64 rows the pair kernel's 256 x 256 tiles win although they may be
+  // mostly padding: 128 x 11008 x 4096 takes 12.1 us there and 14.3 here, 64 rows
+  // 11.6 and 11.6, 64 x 28672 x 8192 30.0 and 26.1.
+  if (a.M > 64) {
     *kernel_name = "gemm_fp4_pair";
     return launch_gemm_fp4_pair(a, block, s);
   }

@@ -11,7 +11,8 @@
 // Backward, one row, the quantiser passed straight through: n = h * rstd,
 //   g = dy * w;  dx = rstd * (g - n * mean(g * n)) (+ dh);  dw = sum over rows of dy * n.
 // Sums and statistics are fp32. Both are bound by HBM: every tensor is read or
-// written once, the row held in registers between its reduction and its output.
+// written once, the row held in registers between its reduction and its output
+// (rows too long for that are read twice).
 #include "common.cuh"
 #include "kernels.h"
 
@@ -59,8 +60,6 @@ struct Vec<__nv_bfloat16> {
   }
 };
 
-__device__ __forceinline__ float to_f(float v) { return v; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 template <typename T>
 __device__ __forceinline__ T from_f(float v);
 template <>
@@ -68,52 +67,114 @@ __device__ __forceinline__ float from_f<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// E consecutive elements of a row starting at element i (VEC: one 16-byte
-// access; otherwise element by element, those at or past n read as 0).
+// The elements a thread holds, NV vectors of E: vector j of thread t of a row of
+// G threads is elements (j * G + t) * E + e (VEC: one 16-byte access), or, where
+// rows are not all 16-byte aligned, (j * E + e) * G + t (neighbouring threads,
+// neighbouring elements).
 template <typename T, bool VEC>
-__device__ __forceinline__ void load_e(const T* row, int i, int n, float* v) {
+__device__ __forceinline__ int elem(int j, int e, int t, int G) {
   constexpr int E = Vec<T>::E;
+  return VEC ? (j * G + t) * E + e : (j * E + e) * G + t;
+}
+// Vector j of a row of n elements, as 16 bytes of T; elements past the end are 0.
+template <typename T, bool VEC>
+__device__ __forceinline__ uint4 load_vec(const T* row, int j, int t, int G, int n) {
+  constexpr int E = Vec<T>::E;
+  uint4 r = make_uint4(0u, 0u, 0u, 0u);
   if (VEC) {
-    Vec<T>::unpack(*reinterpret_cast<const uint4*>(row + i), v);
+    const int i = elem<T, VEC>(j, 0, t, G);
+    if (i < n) r = *reinterpret_cast<const uint4*>(row + i);
   } else {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = i + e < n ? to_f(row[i + e]) : 0.f;
+    for (int e = 0; e < E; ++e) {
+      const int i = elem<T, VEC>(j, e, t, G);
+      if (sizeof(T) == 4) {
+        if (i < n) w[e & 3] = reinterpret_cast<const uint32_t*>(row)[i];
+      } else if (i < n) {
+        w[(e >> 1) & 3] |= (uint32_t)reinterpret_cast<const uint16_t*>(row)[i] << (16 * (e & 1));
+      }
+    }
+    r = make_uint4(w[0], w[1], w[2], w[3]);
   }
+  return r;
 }
 template <typename T, bool VEC>
-__device__ __forceinline__ void store_e(T* row, int i, int n, const float* v) {
+__device__ __forceinline__ void store_vec(T* row, int j, int t, int G, int n, const uint4& r) {
   constexpr int E = Vec<T>::E;
   if (VEC) {
-    *reinterpret_cast<uint4*>(row + i) = Vec<T>::pack(v);
+    const int i = elem<T, VEC>(j, 0, t, G);
+    if (i < n) *reinterpret_cast<uint4*>(row + i) = r;
   } else {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (i + e < n) row[i + e] = from_f<T>(v[e]);
+    for (int e = 0; e < E; ++e) {
+      const int i = elem<T, VEC>(j, e, t, G);
+      if (i >= n) continue;
+      if (sizeof(T) == 4) reinterpret_cast<uint32_t*>(row)[i] = w[e & 3];
+      else reinterpret_cast<uint16_t*>(row)[i] = (uint16_t)(w[(e >> 1) & 3] >> (16 * (e & 1)));
+    }
   }
 }
-template <typename T, bool VEC>
-__device__ __forceinline__ void load_w(const void* w, int w_f32, int i, int n, float* v) {
+// x + residual rounded to T, element by element.
+template <typename T>
+__device__ __forceinline__ uint4 add_vec(const uint4& x, const uint4& r) {
   constexpr int E = Vec<T>::E;
-  if (w_f32) {
+  float a[E], b[E];
+  Vec<T>::unpack(x, a);
+  Vec<T>::unpack(r, b);
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = (VEC || i + e < n) ? __ldg(static_cast<const float*>(w) + i + e) : 0.f;
+  for (int e = 0; e < E; ++e) a[e] = __fadd_rn(a[e], b[e]);
+  return Vec<T>::pack(a);
+}
+// The weight's elements at the same places (either type; VEC: 16-byte aligned).
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_w(const void* w, int w_f32, int j, int t, int G, int n, float* v) {
+  constexpr int E = Vec<T>::E;
+  if (VEC) {
+    const int i = elem<T, VEC>(j, 0, t, G);
+    if (i >= n) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = 0.f;
+    } else if (w_f32) {
+      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(w) + i);
+#pragma unroll
+      for (int q = 0; q < E / 4; ++q) {
+        const float4 f = __ldg(p + q);
+        v[4 * q] = f.x;
+        v[4 * q + 1] = f.y;
+        v[4 * q + 2] = f.z;
+        v[4 * q + 3] = f.w;
+      }
+    } else {
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(w) + i);
+#pragma unroll
+      for (int q = 0; q < E / 2; ++q) {   // E / 2 words: merged into 8- or 16-byte loads
+        const uint32_t f = __ldg(p + q);
+        v[2 * q] = __uint_as_float(f << 16);
+        v[2 * q + 1] = __uint_as_float(f & 0xffff0000u);
+      }
+    }
   } else {
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      v[e] = (VEC || i + e < n) ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i + e]) : 0.f;
+    for (int e = 0; e < E; ++e) {
+      const int i = elem<T, VEC>(j, e, t, G);
+      v[e] = i >= n ? 0.f
+             : w_f32 ? __ldg(static_cast<const float*>(w) + i)
+                     : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i]);
+    }
   }
 }
 
-// Sum of a and maximum of b over the CTA (every thread gets both).
-__device__ __forceinline__ void block_sum_max(float& a, unsigned& b) {
-  __shared__ float sa[32];
-  __shared__ unsigned sb[32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = (blockDim.x + 31) >> 5;
+// Sum of a and maximum of b over the threads of a row: a warp, or the CTA
+// through sa / sb (one entry a warp). One barrier: two calls in a row use
+// different arrays.
+__device__ __forceinline__ void row_sum_max(float& a, unsigned& b, int G, float* sa, unsigned* sb) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
   b = __reduce_max_sync(0xffffffffu, b);
-  if (nw == 1) return;
-  __syncthreads();   // an earlier use of the arrays is over
+  if (G == 32) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = G >> 5;
   if (lane == 0) {
     sa[warp] = a;
     sb[warp] = b;
@@ -124,6 +185,18 @@ __device__ __forceinline__ void block_sum_max(float& a, unsigned& b) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
   b = __reduce_max_sync(0xffffffffu, b);
+}
+__device__ __forceinline__ float row_sum(float a, int G, float* sa) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  if (G == 32) return a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = G >> 5;
+  if (lane == 0) sa[warp] = a;
+  __syncthreads();
+  a = lane < nw ? sa[lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  return a;
 }
 
 // The row's scale and the multiplier of v. A row that holds a NaN or an
@@ -151,122 +224,410 @@ __device__ __forceinline__ int quant1(float v, float inv) {
   return __float2int_rn(p);
 }
 
-template <typename T, bool VEC>
-__global__ void rms_norm_s8_kernel(const NormArgs p) {
+// One row per G = blockDim.x threads (blockDim.y rows a CTA where G is a warp),
+// NV vectors a thread. NV = 0: rows of any length, read twice.
+template <typename T, bool VEC, int NV>
+__global__ void __launch_bounds__(1024) rms_norm_s8_kernel(const NormArgs p) {
   constexpr int E = Vec<T>::E;
-  const int n = p.H, nt = blockDim.x;
-  for (long long m = blockIdx.x; m < p.M; m += gridDim.x) {
-    const T* x = static_cast<const T*>(p.x) + m * p.ldx;
-    const T* r = p.residual ? static_cast<const T*>(p.residual) + m * p.ldr : nullptr;
-    T* ho = p.h ? static_cast<T*>(p.h) + m * (long long)n : nullptr;
-    int8_t* q = p.q + m * (long long)n;
-    float ss = 0.f;
-    unsigned am = 0u;
-    for (int i = threadIdx.x * E; i < n; i += nt * E) {
-      float h[E], w[E];
-      load_e<T, VEC>(x, i, n, h);
-      if (r) {
-        float b[E];
-        load_e<T, VEC>(r, i, n, b);
+  __shared__ float sa[32];
+  __shared__ unsigned sb[32];
+  const int n = p.H, G = blockDim.x, t = threadIdx.x;
+  const long long m = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+  if (m >= p.M) return;   // whole warps (G a warp), or nobody
+  const T* x = static_cast<const T*>(p.x) + m * p.ldx;
+  const T* r = p.residual ? static_cast<const T*>(p.residual) + m * p.ldr : nullptr;
+  T* ho = p.h ? static_cast<T*>(p.h) + m * (long long)n : nullptr;
+  int8_t* q = p.q + m * (long long)n;
+  float ss = 0.f;
+  unsigned am = 0u;
+  // v = h * w of a vector, and its share of the statistics
+  auto stats = [&](const uint4& hr, const float* w, float* v) {
+    Vec<T>::unpack(hr, v);
 #pragma unroll
-        for (int e = 0; e < E; ++e) h[e] = to_f(from_f<T>(__fadd_rn(h[e], b[e])));
-      }
-      if (ho) store_e<T, VEC>(ho, i, n, h);
-      load_w<T, VEC>(p.w, p.w_f32, i, n, w);
+    for (int e = 0; e < E; ++e) {
+      ss = __fmaf_rn(v[e], v[e], ss);
+      v[e] = __fmul_rn(v[e], w[e]);
+      am = max(am, __float_as_uint(v[e]) & 0x7fffffffu);
+    }
+  };
+  auto quantise = [&](int j, const float* v, float inv, bool zero) {
+    int8_t o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = zero ? 0 : (int8_t)quant1(v[e], inv);
+    if (VEC) {
+      const int i = elem<T, VEC>(j, 0, t, G);
+      if (i >= n) return;
+      if (E == 8) *reinterpret_cast<uint2*>(q + i) = *reinterpret_cast<const uint2*>(o);
+      else *reinterpret_cast<uint32_t*>(q + i) = *reinterpret_cast<const uint32_t*>(o);
+    } else {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        ss = __fmaf_rn(h[e], h[e], ss);
-        am = max(am, __float_as_uint(__fmul_rn(h[e], w[e])) & 0x7fffffffu);
+        const int i = elem<T, VEC>(j, e, t, G);
+        if (i < n) q[i] = o[e];
       }
     }
-    block_sum_max(ss, am);
+  };
+  if (NV > 0) {
+    constexpr int K = NV > 0 ? NV : 1;
+    uint4 h[K];
+    float v[K][E];
+#pragma unroll
+    for (int j = 0; j < K; ++j) h[j] = load_vec<T, VEC>(x, j, t, G, n);
+    if (r) {
+      uint4 b[K];
+#pragma unroll
+      for (int j = 0; j < K; ++j) b[j] = load_vec<T, VEC>(r, j, t, G, n);
+#pragma unroll
+      for (int j = 0; j < K; ++j) h[j] = add_vec<T>(h[j], b[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      if (ho) store_vec<T, VEC>(ho, j, t, G, n, h[j]);
+      float w[E];
+      load_w<T, VEC>(p.w, p.w_f32, j, t, G, n, w);
+      stats(h[j], w, v[j]);
+    }
+    row_sum_max(ss, am, G, sa, sb);
     const RowScale s = row_scale(ss, am, n, p.eps);
-    if (threadIdx.x == 0) {
+    if (t == 0) {
       p.scale[m] = s.scale;
       p.rstd[m] = s.rstd;
     }
-    for (int i = threadIdx.x * E; i < n; i += nt * E) {
-      float h[E], w[E];
-      // a stored h is read back (it may lie over x or the residual)
-      load_e<T, VEC>(ho ? ho : x, i, n, h);
-      if (r && !ho) {
-        float b[E];
-        load_e<T, VEC>(r, i, n, b);
 #pragma unroll
-        for (int e = 0; e < E; ++e) h[e] = to_f(from_f<T>(__fadd_rn(h[e], b[e])));
+    for (int j = 0; j < K; ++j) quantise(j, v[j], s.inv, am >= kInfBits);
+  } else {
+    const int steps = (n + G * E - 1) / (G * E);
+    for (int j = 0; j < steps; ++j) {
+      uint4 h = load_vec<T, VEC>(x, j, t, G, n);
+      if (r) h = add_vec<T>(h, load_vec<T, VEC>(r, j, t, G, n));
+      if (ho) store_vec<T, VEC>(ho, j, t, G, n, h);
+      float v[E], w[E];
+      load_w<T, VEC>(p.w, p.w_f32, j, t, G, n, w);
+      stats(h, w, v);
+    }
+    row_sum_max(ss, am, G, sa, sb);
+    const RowScale s = row_scale(ss, am, n, p.eps);
+    if (t == 0) {
+      p.scale[m] = s.scale;
+      p.rstd[m] = s.rstd;
+    }
+    for (int j = 0; j < steps; ++j) {
+      // a stored h is read back (by the thread that wrote it: it may lie over x or the residual)
+      uint4 h = load_vec<T, VEC>(ho ? ho : x, j, t, G, n);
+      if (r && !ho) h = add_vec<T>(h, load_vec<T, VEC>(r, j, t, G, n));
+      float v[E], w[E];
+      load_w<T, VEC>(p.w, p.w_f32, j, t, G, n, w);
+      Vec<T>::unpack(h, v);
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = __fmul_rn(v[e], w[e]);
+      quantise(j, v, s.inv, am >= kInfBits);
+    }
+  }
+}
+
+// y[i] = q[i] * scale[i / H] over the flat [M * H] array, eight elements a step
+// (both arrays are contiguous, so no width is unaligned).
+template <typename T, typename I, bool VEC>
+__global__ void __launch_bounds__(256) s8_dequantize_rows_kernel(const int8_t* q, const float* scale, I total, I H,
+                                                                 T* y) {
+  constexpr int STEPS = 4;
+  uint2 raw[STEPS];
+  const I base = (I)blockIdx.x * (256 * 8 * STEPS) + threadIdx.x * 8;
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    const I i = base + (I)s * (256 * 8);
+    if (VEC && i < total && total - i >= 8) raw[s] = *reinterpret_cast<const uint2*>(q + i);
+  }
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    const I i = base + (I)s * (256 * 8);
+    if (i >= total) return;
+    const I m = i / H, c = i - m * H;
+    if (VEC && total - i >= 8) {
+      float f[8];
+      const uint32_t w[2] = {raw[s].x, raw[s].y};
+      const float s0 = __ldg(scale + m);
+      if (H - c >= 8) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = __fmul_rn((float)(int8_t)(w[e >> 2] >> (8 * (e & 3))), s0);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          f[e] = __fmul_rn((float)(int8_t)(w[e >> 2] >> (8 * (e & 3))), __ldg(scale + (i + e) / H));
       }
-      load_w<T, VEC>(p.w, p.w_f32, i, n, w);
+#pragma unroll
+      for (int e = 0; e < 8; e += Vec<T>::E) *reinterpret_cast<uint4*>(y + i + e) = Vec<T>::pack(f + e);
+    } else {
+      for (int e = 0; e < 8 && total - i > (I)e; ++e)
+        y[i + e] = from_f<T>(__fmul_rn((float)q[i + e], __ldg(scale + (i + e) / H)));
+    }
+  }
+}
+
+// Backward. A CTA takes rows blockIdx.x, blockIdx.x + gridDim.x, ... (blockDim.y
+// of them at a time where a row is one warp's) and keeps its columns' share of
+// dweight in registers; the shares go to partials and sum_partials adds them in
+// order. The next rows are prefetched to L2 by bulk copies (PF of them ahead), so
+// that HBM stays busy through a row's reduction. NV = 0: rows of any length,
+// read twice, the shares of dweight accumulated in partials itself.
+constexpr int PF = 2;
+template <typename T>
+constexpr int backward_threads(int nv) {   // at most, so that a thread's registers suffice
+  return nv == 0 ? 1024 : nv == 4 ? (sizeof(T) == 4 ? 704 : 576) : 512;
+}
+template <typename T, bool VEC, int NV>
+__global__ void __launch_bounds__(backward_threads<T>(NV), NV == 1 ? 3 : NV == 2 ? 2 : 1)
+    rms_norm_backward_kernel(const NormBwdArgs p) {
+  constexpr int E = Vec<T>::E;
+  constexpr int K = NV > 0 ? NV : 1;
+  __shared__ float sa[2][32];
+  __shared__ float sw[NV == 1 ? 8 * 32 * E : 1];
+  const int n = p.H, G = blockDim.x, t = threadIdx.x;
+  const long long step = (long long)gridDim.x * blockDim.y;
+  const T* h0 = static_cast<const T*>(p.h);
+  const T* dy0 = static_cast<const T*>(p.dy);
+  const T* dh0 = static_cast<const T*>(p.dh);
+  float* part = p.partials + (long long)blockIdx.x * n;
+  auto prefetch = [&](long long m) {
+    if (!VEC || t >= 3 || m >= p.M) return;
+    const T* row = t == 0 ? h0 + m * p.ldh : t == 1 ? dy0 + m * p.lddy : dh0 ? dh0 + m * p.lddh : nullptr;
+    if (row)
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(row), "r"((uint32_t)(n * sizeof(T))) : "memory");
+  };
+  long long m = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+  int par = 0;
+  if (NV > 0) {
+    float dw[K][E];
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+#pragma unroll
+      for (int e = 0; e < E; ++e) dw[j][e] = 0.f;
+    for (int i = 1; i < PF; ++i) prefetch(m + i * step);
+    for (; m < p.M; m += step) {
+      prefetch(m + PF * step);
+      const float rstd = __ldg(p.rstd + m);
+      uint4 h[K], dy[K], dh[K];
+#pragma unroll
+      for (int j = 0; j < K; ++j) h[j] = load_vec<T, VEC>(h0 + m * p.ldh, j, t, G, n);
+#pragma unroll
+      for (int j = 0; j < K; ++j) dy[j] = load_vec<T, VEC>(dy0 + m * p.lddy, j, t, G, n);
+      if (dh0) {
+#pragma unroll
+        for (int j = 0; j < K; ++j) dh[j] = load_vec<T, VEC>(dh0 + m * p.lddh, j, t, G, n);
+      }
+      float dot = 0.f;
+#pragma unroll
+      for (int j = 0; j < K; ++j) {
+        float w[E], nn[E], g[E];
+        load_w<T, VEC>(p.w, p.w_f32, j, t, G, n, w);
+        Vec<T>::unpack(h[j], nn);
+        Vec<T>::unpack(dy[j], g);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          nn[e] *= rstd;
+          dw[j][e] = __fmaf_rn(g[e], nn[e], dw[j][e]);
+          dot = __fmaf_rn(g[e] * w[e], nn[e], dot);
+        }
+      }
+      const float mean = row_sum(dot, G, sa[par]) / (float)n;
+      par ^= 1;
+#pragma unroll
+      for (int j = 0; j < K; ++j) {
+        float w[E], v[E], g[E];
+        load_w<T, VEC>(p.w, p.w_f32, j, t, G, n, w);
+        Vec<T>::unpack(h[j], v);
+        Vec<T>::unpack(dy[j], g);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = __fmaf_rn(-(v[e] * rstd), mean, g[e] * w[e]) * rstd;
+        if (dh0) {
+          Vec<T>::unpack(dh[j], g);
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[e] += g[e];
+        }
+        store_vec<T, VEC>(static_cast<T*>(p.dx) + m * (long long)n, j, t, G, n, Vec<T>::pack(v));
+      }
+    }
+    if (NV == 1 && blockDim.y > 1) {   // the CTA's warps, each with rows of its own: added in order
+#pragma unroll
+      for (int e = 0; e < E; ++e) sw[(threadIdx.y * 32 + t) * E + e] = dw[0][e];
+      __syncthreads();
+      if (threadIdx.y > 0) return;
+      for (int y = 1; y < (int)blockDim.y; ++y)
+#pragma unroll
+        for (int e = 0; e < E; ++e) dw[0][e] += sw[(y * 32 + t) * E + e];
+    }
+#pragma unroll
+    for (int j = 0; j < K; ++j)
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        if (VEC || i + e < n) q[i + e] = am >= kInfBits ? 0 : (int8_t)quant1(__fmul_rn(h[e], w[e]), s.inv);
+        const int i = elem<T, VEC>(j, e, t, G);
+        if (i < n) part[i] = dw[j][e];
       }
+  } else {
+    const int steps = (n + G * E - 1) / (G * E);
+    bool fresh = true;
+    for (; m < p.M; m += step) {
+      const float rstd = __ldg(p.rstd + m);
+      float dot = 0.f;
+      for (int j = 0; j < steps; ++j) {
+        float h[E], dy[E], w[E];
+        Vec<T>::unpack(load_vec<T, VEC>(h0 + m * p.ldh, j, t, G, n), h);
+        Vec<T>::unpack(load_vec<T, VEC>(dy0 + m * p.lddy, j, t, G, n), dy);
+        load_w<T, VEC>(p.w, p.w_f32, j, t, G, n, w);
+#pragma unroll
+        for (int e = 0; e < E; ++e) dot = __fmaf_rn(dy[e] * w[e], h[e] * rstd, dot);
+      }
+      const float mean = row_sum(dot, G, sa[par]) / (float)n;
+      par ^= 1;
+      for (int j = 0; j < steps; ++j) {
+        float h[E], dy[E], dh[E], w[E];
+        Vec<T>::unpack(load_vec<T, VEC>(h0 + m * p.ldh, j, t, G, n), h);
+        Vec<T>::unpack(load_vec<T, VEC>(dy0 + m * p.lddy, j, t, G, n), dy);
+        if (dh0) Vec<T>::unpack(load_vec<T, VEC>(dh0 + m * p.lddh, j, t, G, n), dh);
+        load_w<T, VEC>(p.w, p.w_f32, j, t, G, n, w);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float nn = h[e] * rstd;
+          const int i = elem<T, VEC>(j, e, t, G);
+          if (i < n) part[i] = __fmaf_rn(dy[e], nn, fresh ? 0.f : part[i]);
+          h[e] = __fmaf_rn(-nn, mean, dy[e] * w[e]) * rstd;
+          if (dh0) h[e] += dh[e];
+        }
+        store_vec<T, VEC>(static_cast<T*>(p.dx) + m * (long long)n, j, t, G, n, Vec<T>::pack(h));
+      }
+      fresh = false;
     }
   }
 }
 
-template <typename T>
-__global__ void s8_dequantize_rows_kernel(const int8_t* q, const float* scale, long long M, int H, T* y) {
-  const long long m = blockIdx.x;
-  const float s = scale[m];
-  for (int i = threadIdx.x; i < H; i += blockDim.x)
-    y[m * H + i] = from_f<T>(__fmul_rn((float)q[m * H + i], s));
-}
-
-template <typename T>
-__global__ void rms_norm_backward_kernel(const NormBwdArgs p) {
-  const int n = p.H, nt = blockDim.x;
-  float* part = p.partials + (long long)blockIdx.x * n;
-  for (int i = threadIdx.x; i < n; i += nt) part[i] = 0.f;
-  for (long long m = blockIdx.x; m < p.M; m += gridDim.x) {
-    const T* h = static_cast<const T*>(p.h) + m * p.ldh;
-    const T* dy = static_cast<const T*>(p.dy) + m * p.lddy;
-    const T* dh = p.dh ? static_cast<const T*>(p.dh) + m * p.lddh : nullptr;
-    T* dx = static_cast<T*>(p.dx) + m * (long long)n;
-    const float rstd = p.rstd[m];
-    float dot = 0.f;
-    unsigned unused = 0u;
-    for (int i = threadIdx.x; i < n; i += nt) {
-      float w[1];
-      w[0] = p.w_f32 ? static_cast<const float*>(p.w)[i] : __bfloat162float(static_cast<const __nv_bfloat16*>(p.w)[i]);
-      dot = __fmaf_rn(to_f(dy[i]) * w[0], to_f(h[i]) * rstd, dot);
-    }
-    block_sum_max(dot, unused);
-    const float mean = dot / (float)n;
-    for (int i = threadIdx.x; i < n; i += nt) {
-      const float w = p.w_f32 ? static_cast<const float*>(p.w)[i]
-                              : __bfloat162float(static_cast<const __nv_bfloat16*>(p.w)[i]);
-      const float d = to_f(dy[i]), nn = to_f(h[i]) * rstd;
-      float v = rstd * (d * w - nn * mean);
-      if (dh) v += to_f(dh[i]);
-      dx[i] = from_f<T>(v);
-      part[i] += d * nn;
-    }
+// out[i] = the sum of column i of part [count][n], in a fixed order: 32 columns
+// a CTA, 16 interleaved runs of rows, then the runs.
+__global__ void __launch_bounds__(512) sum_partials_kernel(const float* part, int count, int n, float* out) {
+  __shared__ float s[16][32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int i = blockIdx.x * 32 + threadIdx.x;
+  float a = 0.f;
+  if (i < n) {
+#pragma unroll 4
+    for (int c = threadIdx.y; c < count; c += 16) a += part[(long long)c * n + i];
   }
-}
-
-__global__ void sum_partials_kernel(const float* part, int count, int n, float* out) {
-  const int i = blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= n) return;
-  float s = 0.f;
-  for (int c = 0; c < count; ++c) s += part[(long long)c * n + i];
-  out[i] = s;
+  s[threadIdx.y][threadIdx.x] = a;
+  __syncthreads();
+  if (threadIdx.y == 0 && i < n) {
+#pragma unroll
+    for (int y = 1; y < 16; ++y) a += s[y][threadIdx.x];
+    out[i] = a;
+  }
 }
 
 template <typename T>
 bool rows_vec(const void* p, long long ld) {
-  return (reinterpret_cast<uintptr_t>(p) % 16) == 0 && (ld * (long long)sizeof(T)) % 16 == 0;
+  return !p || ((reinterpret_cast<uintptr_t>(p) % 16) == 0 && (ld * (long long)sizeof(T)) % 16 == 0);
 }
 
+int round32(int v) { return (v + 31) / 32 * 32; }
+
+// Vectors a thread and threads a row. With rows enough to fill the GPU, two or
+// four vectors a thread (more loads in flight, fewer warps in the reduction);
+// with few rows one (the row's latency). Rows of one warp share a CTA.
 template <typename T>
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
   constexpr int E = Vec<T>::E;
-  const bool vec = a.H % E == 0 && rows_vec<T>(a.x, a.ldx) && (!a.residual || rows_vec<T>(a.residual, a.ldr)) &&
-                   (!a.h || rows_vec<T>(a.h, a.H));
-  const int threads = std::min(512, std::max(32, ((a.H + E - 1) / E + 31) / 32 * 32));
-  const unsigned grid = (unsigned)std::min<long long>(a.M, 1 << 30);
-  if (vec) rms_norm_s8_kernel<T, true><<<grid, threads, 0, s>>>(a);
-  else rms_norm_s8_kernel<T, false><<<grid, threads, 0, s>>>(a);
+  const bool vec = a.H % E == 0 && rows_vec<T>(a.x, a.ldx) && rows_vec<T>(a.residual, a.ldr) &&
+                   rows_vec<T>(a.h, a.H) && (reinterpret_cast<uintptr_t>(a.w) % 16) == 0 &&
+                   (reinterpret_cast<uintptr_t>(a.q) % 8) == 0;
+  const int nvec = (a.H + E - 1) / E;
+  const bool many = a.M >= 2 * num_sms();
+  int nv = nvec <= 32 ? 1 : many ? (nvec <= 256 ? 1 : nvec <= 1024 ? 2 : 4) : (nvec <= 1024 ? 1 : nvec <= 2048 ? 2 : 4);
+  if (nvec > 4096) nv = 0;
+  const int G = nv ? std::max(32, round32((nvec + nv - 1) / nv)) : 1024;
+  const int R = G == 32 ? (many ? 8 : 1) : 1;
+  const dim3 block(G, R);
+  const unsigned grid = (unsigned)((a.M + R - 1) / R);
+#define QMM_NORM(V)                                                                         \
+  switch (nv) {                                                                             \
+    case 1: rms_norm_s8_kernel<T, V, 1><<<grid, block, 0, s>>>(a); break;                   \
+    case 2: rms_norm_s8_kernel<T, V, 2><<<grid, block, 0, s>>>(a); break;                   \
+    case 4: rms_norm_s8_kernel<T, V, 4><<<grid, block, 0, s>>>(a); break;                   \
+    default: rms_norm_s8_kernel<T, V, 0><<<grid, block, 0, s>>>(a); break;                  \
+  }
+  if (vec) {
+    QMM_NORM(true)
+  } else {
+    QMM_NORM(false)
+  }
+#undef QMM_NORM
   return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_dequantize(const int8_t* q, const float* scale, long long M, int H, T* y, cudaStream_t s) {
+  const long long total = M * H;
+  const unsigned grid = (unsigned)((total + 8191) / 8192);
+  const bool vec = (reinterpret_cast<uintptr_t>(q) % 8) == 0 && (reinterpret_cast<uintptr_t>(y) % 16) == 0;
+  const bool small = total + 8192 < (1ll << 32);
+  if (small) {
+    if (vec) s8_dequantize_rows_kernel<T, uint32_t, true><<<grid, 256, 0, s>>>(q, scale, (uint32_t)total, (uint32_t)H, y);
+    else s8_dequantize_rows_kernel<T, uint32_t, false><<<grid, 256, 0, s>>>(q, scale, (uint32_t)total, (uint32_t)H, y);
+  } else {
+    if (vec) s8_dequantize_rows_kernel<T, uint64_t, true><<<grid, 256, 0, s>>>(q, scale, (uint64_t)total, (uint64_t)H, y);
+    else s8_dequantize_rows_kernel<T, uint64_t, false><<<grid, 256, 0, s>>>(q, scale, (uint64_t)total, (uint64_t)H, y);
+  }
+  return cudaGetLastError();
+}
+
+// Launch shape of the backward pass: vectors a thread, threads a row, rows of a
+// CTA at a time, CTAs (= rows of partials). The CTAs are those that fit at once,
+// at most 8 an SM for narrow rows (each adds a row to sum_partials' work).
+struct BwdShape {
+  int nv, G, R, parts;
+};
+template <typename T>
+BwdShape backward_shape(long long M, int H) {
+  constexpr int E = Vec<T>::E;
+  BwdShape b;
+  const int nvec = (H + E - 1) / E;
+  b.nv = nvec <= 512 ? 1 : nvec <= 1024 ? 2 : nvec <= 4 * backward_threads<T>(4) ? 4 : 0;
+  b.G = b.nv ? std::max(32, round32((nvec + b.nv - 1) / b.nv)) : 1024;
+  b.R = b.G == 32 ? 8 : 1;
+  const int per_sm = b.nv == 1 ? std::min(8, 1536 / (b.G * b.R)) : b.nv == 2 ? 2 : 1;
+  b.parts = (int)std::min<long long>((M + b.R - 1) / b.R, 152ll * std::max(1, per_sm));
+  return b;
+}
+
+template <typename T>
+cudaError_t launch_backward(const NormBwdArgs& a, cudaStream_t s) {
+  constexpr int E = Vec<T>::E;
+  const bool vec = a.H % E == 0 && rows_vec<T>(a.h, a.ldh) && rows_vec<T>(a.dy, a.lddy) &&
+                   rows_vec<T>(a.dh, a.lddh) && rows_vec<T>(a.dx, a.H) && (reinterpret_cast<uintptr_t>(a.w) % 16) == 0;
+  const BwdShape b = backward_shape<T>(a.M, a.H);
+  const dim3 block(b.G, b.R);
+#define QMM_NORM(V)                                                                           \
+  switch (b.nv) {                                                                             \
+    case 1: rms_norm_backward_kernel<T, V, 1><<<b.parts, block, 0, s>>>(a); break;            \
+    case 2: rms_norm_backward_kernel<T, V, 2><<<b.parts, block, 0, s>>>(a); break;            \
+    case 4: rms_norm_backward_kernel<T, V, 4><<<b.parts, block, 0, s>>>(a); break;            \
+    default: rms_norm_backward_kernel<T, V, 0><<<b.parts, block, 0, s>>>(a); break;           \
+  }
+  if (vec) {
+    QMM_NORM(true)
+  } else {
+    QMM_NORM(false)
+  }
+#undef QMM_NORM
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((a.H + 31) / 32));
+  cfg.blockDim = dim3(32, 16);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, sum_partials_kernel, (const float*)a.partials, b.parts, a.H, a.dweight);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace norm
@@ -279,25 +640,18 @@ cudaError_t launch_rms_norm_s8(const NormArgs& a, bool bf16, cudaStream_t s, con
 cudaError_t launch_s8_dequantize_rows(const int8_t* q, const float* scale, long long M, int H, void* y, bool bf16,
                                       cudaStream_t s, const char** kernel_name) {
   *kernel_name = "s8_dequantize_rows";
-  if (bf16)
-    norm::s8_dequantize_rows_kernel<<<(unsigned)M, 256, 0, s>>>(q, scale, M, H, static_cast<__nv_bfloat16*>(y));
-  else
-    norm::s8_dequantize_rows_kernel<<<(unsigned)M, 256, 0, s>>>(q, scale, M, H, static_cast<float*>(y));
-  return cudaGetLastError();
+  return bf16 ? norm::launch_dequantize(q, scale, M, H, static_cast<__nv_bfloat16*>(y), s)
+              : norm::launch_dequantize(q, scale, M, H, static_cast<float*>(y), s);
 }
 
-int rms_norm_backward_partials(long long M, int H) { return (int)std::min<long long>(M, 2 * 152); }
+// The larger of the two types' counts (the size query does not know the type).
+int rms_norm_backward_partials(long long M, int H) {
+  return std::max(norm::backward_shape<float>(M, H).parts, norm::backward_shape<__nv_bfloat16>(M, H).parts);
+}
 
 cudaError_t launch_rms_norm_backward(const NormBwdArgs& a, bool bf16, cudaStream_t s, const char** kernel_name) {
   *kernel_name = "rms_norm_backward+sum_partials";
-  const int parts = rms_norm_backward_partials(a.M, a.H);
-  const int threads = std::min(512, std::max(32, (a.H + 31) / 32 * 32));
-  if (bf16) norm::rms_norm_backward_kernel<__nv_bfloat16><<<parts, threads, 0, s>>>(a);
-  else norm::rms_norm_backward_kernel<float><<<parts, threads, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  norm::sum_partials_kernel<<<(a.H + 127) / 128, 128, 0, s>>>(a.partials, parts, a.H, a.dweight);
-  return cudaGetLastError();
+  return bf16 ? norm::launch_backward<__nv_bfloat16>(a, s) : norm::launch_backward<float>(a, s);
 }
 
 }  // namespace qmm
