@@ -147,19 +147,41 @@ struct Raw8<float> {
   }
 };
 
-// The maximum over the lanes that share a block: 4 lanes of 8 elements for 32,
-// 2 for 16.
-template <int BLOCK>
-__device__ __forceinline__ unsigned block_max(unsigned m) {
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  if (BLOCK == 32) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  return m;
-}
+// Sixteen consecutive elements, a lane's share of a row: a block of 16, or half a
+// block of 32 (the other half in the neighbouring lane).
+template <typename T>
+struct Raw16 {
+  Raw8<T> lo, hi;
+  __device__ __forceinline__ void load(const T* row, long long k, long long n, bool vec) {
+    lo.load(row, k, n, vec);
+    hi.load(row, k + 8, n, vec);
+  }
+  __device__ __forceinline__ unsigned max_bits() const { return max(lo.max_bits(), hi.max_bits()); }
+  // the block's scale, and the elements' codes, the first in the lowest bits
+  template <int BLOCK>
+  __device__ __forceinline__ uint2 codes(float u, uint8_t& scale) const {
+    unsigned m = max_bits();
+    if (BLOCK == 32) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    float mul = 0.f, f[8];
+    bool zero;
+    scale = block_scale<BLOCK>(m, u, mul, zero);
+    uint2 c;
+    lo.floats(f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(f[e], mul);
+    c.x = e2m1x8(f);
+    hi.floats(f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(f[e], mul);
+    c.y = e2m1x8(f);
+    return zero ? make_uint2(0u, 0u) : c;
+  }
+};
 
 // ---------------------------------------------------------------------------
 // Along the rows. A CTA takes the rows {2c, 2c + 1} + {0, 32, 64, 96} of a tile
-// (J = 4: a warp step is 32 columns of eight rows, 8 columns a lane) or, for
-// matrices of up to 32 rows, {2c, 2c + 1} (J = 1: 128 columns of two rows). Rows
+// (J = 4: a warp step is 64 columns of eight rows, 16 columns a lane) or, for
+// matrices of up to 32 rows, {2c, 2c + 1} (J = 1: 256 columns of two rows). Rows
 // chosen so make every 32-byte sector of codes (two neighbouring rows' 16 bytes)
 // and of scales (two rows' 16-byte lines of an atom, whose 4-byte parts are rows
 // 32 apart) the work of one CTA. A warp's steps of a batch (ITER) are loaded
@@ -169,32 +191,30 @@ __device__ __forceinline__ unsigned block_max(unsigned m) {
 template <typename T, int BLOCK, int J, int ITER>
 __global__ void __launch_bounds__(1024) quantize_rows_kernel(const Fp4QuantArgs p, const int staged) {
   constexpr int ATOMS = BLOCK == 16 ? 2 : 1;
-  constexpr int SPC = 32 / BLOCK;   // scales per 32-column chunk
-  constexpr int UC = J == 4 ? 1 : 4;   // chunks a warp step
+  constexpr int SPC = 32 / BLOCK;      // scales per 32-column chunk
+  constexpr int LANES = J == 4 ? 4 : 16;   // lanes a row
+  constexpr int UC = LANES / 2;        // chunks a warp step
   __shared__ unsigned rowmax[8];
   extern __shared__ __align__(16) uint8_t sfs[];   // [atom][2 rows][4 rows 32 apart][4] (staged)
   const Fp4Layout L(p.rows, p.cols, BLOCK);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  const long long tile = blockIdx.x >> 4;
-  const int c2 = 2 * (blockIdx.x & 15);
+  const int tile = blockIdx.x >> 4, c2 = 2 * (blockIdx.x & 15);
   const int ra = J == 4 ? (lane >> 2) & 1 : lane >> 4, rj = J == 4 ? lane >> 3 : 0;
-  const int piece = J == 4 ? lane & 3 : lane & 15;
+  const int piece = lane & (LANES - 1), half = piece & 1;
   const int rin = c2 + ra + 32 * rj;
-  const long long row = tile * 128 + rin;
-  if (tile * 128 + c2 >= p.rows) return;
+  const long long row = (long long)tile * 128 + rin;
+  if ((long long)tile * 128 + c2 >= p.rows) return;
   const bool rv = row < p.rows;
   const T* x = static_cast<const T*>(p.x) + (rv ? row : 0) * p.ld;
-  const long long n = rv ? p.cols : 0;
+  const int n = rv ? (int)p.cols : 0;
   const bool vec = p.vec;
-  const int units = (int)(L.kt * 4 / UC);
+  const int chunks = (int)L.kt * 4, units = (chunks + UC - 1) / UC;
   const int batches = (units + nw * ITER - 1) / (nw * ITER);
-  Raw8<T> v[ITER];
+  Raw16<T> v[ITER];
   auto load = [&](int b) {
 #pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-      const int u = (b * ITER + i) * nw + warp;   // past the end: columns past n, zeros
-      v[i].load(x, (long long)u * (32 * UC) + piece * 8, n, vec);
-    }
+    for (int i = 0; i < ITER; ++i)   // past the end: columns past n, zeros
+      v[i].load(x, (long long)((b * ITER + i) * nw + warp) * (32 * UC) + piece * 16, n, vec);
   };
   float u = 1.f;
   if (BLOCK == 16) {
@@ -207,33 +227,27 @@ __global__ void __launch_bounds__(1024) quantize_rows_kernel(const Fp4QuantArgs 
       for (int i = 0; i < ITER; ++i) m = max(m, v[i].max_bits());
     }
 #pragma unroll
-    for (int o = 1; o < 4 * UC; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 1; o < LANES; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (piece == 0) atomicMax(&rowmax[rj * 2 + ra], m);
     __syncthreads();
     const float g = row_scale(rowmax[rj * 2 + ra]);
     u = __fdiv_rn(1.f, g);
     if (warp == 0 && piece == 0 && rv) reinterpret_cast<float*>(p.out + L.row_off())[row] = g;
   }
-  uint8_t* codes = p.out + (size_t)tile * L.kt * 8192 + rin * 16 + (piece & 3) * 4;
+  uint8_t* codes = p.out + (size_t)tile * L.kt * 8192 + rin * 16 + half * 8;
   uint8_t* sf = p.out + L.scale_off() + (size_t)tile * L.kt * 512 * ATOMS + c2 * 16;
   for (int b = 0; b < batches; ++b) {
     if (BLOCK == 32 || batches > 1) load(b);
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
-      const int un = (b * ITER + i) * nw + warp;
-      float mul = 0.f, f[8];
-      bool zero;
-      const uint8_t s = block_scale<BLOCK>(block_max<BLOCK>(v[i].max_bits()), u, mul, zero);
-      v[i].floats(f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(f[e], mul);
-      const uint32_t code = zero ? 0u : e2m1x8(f);
-      const int ch = un * UC + (piece >> 2);
-      if (un < units) {
-        const int k = ch * SPC + (BLOCK == 16 ? (piece & 3) >> 1 : 0);
+      uint8_t s;
+      const uint2 code = v[i].template codes<BLOCK>(u, s);
+      const int ch = ((b * ITER + i) * nw + warp) * UC + (piece >> 1);
+      if (ch < chunks) {
+        const int k = ch * SPC + (BLOCK == 16 ? half : 0);
         const int off = ra * 16 + rj * 4 + (k & 3);
-        const bool mine = (piece & (BLOCK == 16 ? 1 : 3)) == 0;
-        if (rv) *reinterpret_cast<uint32_t*>(codes + (size_t)ch * 2048) = code;
+        const bool mine = BLOCK == 16 || half == 0;
+        if (rv) *reinterpret_cast<uint2*>(codes + (size_t)ch * 2048) = code;
         if (mine && staged) sfs[(k >> 2) * 32 + off] = s;
         if (mine && !staged && rv) sf[(size_t)(k >> 2) * 512 + off] = s;
       }
@@ -340,36 +354,32 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const Fp4QuantArgs p
   const long long c0 = (long long)tx * 128, r0 = (long long)ty * 128;
   const size_t ti = blockIdx.x;                       // this tile in the packed rows
   const size_t tc = (size_t)tx * Lc.kt + ty;          // and in the packed columns
-  // a warp step: 8 rows x 32 columns; warp w takes rows 8w .. 8w + 7 of each 64
-  Raw8<T> v[8];
+  // a warp step: 8 rows x 64 columns; warp w takes rows 8w .. 8w + 7 of each 64
+  Raw16<T> v[4];
+  const int half = lane & 1;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int rin = (i >> 2) * 64 + warp * 8 + (lane >> 2), k = (i & 3) * 32 + (lane & 3) * 8;
+  for (int i = 0; i < 4; ++i) {
+    const int rin = (i >> 1) * 64 + warp * 8 + (lane >> 2), k = (i & 1) * 64 + (lane & 3) * 16;
     const bool rv = r0 + rin < p.rows;
     v[i].load(static_cast<const T*>(p.x) + (rv ? r0 + rin : 0) * p.ld, c0 + k, rv ? p.cols : 0, p.vec);
   }
   float u = 1.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int ch = i & 3, rin = (i >> 2) * 64 + warp * 8 + (lane >> 2), k = ch * 32 + (lane & 3) * 8;
-    *reinterpret_cast<Raw8<T>*>(smem + rin * S::PITCH + k * sizeof(T)) = v[i];
+  for (int i = 0; i < 4; ++i) {
+    const int rin = (i >> 1) * 64 + warp * 8 + (lane >> 2), k = (i & 1) * 64 + (lane & 3) * 16;
+    *reinterpret_cast<Raw16<T>*>(smem + rin * S::PITCH + k * sizeof(T)) = v[i];
     if (ROWS) {
-      if (BLOCK == 16 && ch == 0) {
+      if (BLOCK == 16 && (i & 1) == 0) {
         const bool rv = r0 + rin < p.rows;
         const float g = row_scale(rv ? reinterpret_cast<const unsigned*>(p.out_rows + Lr.max_off())[r0 + rin] : 0u);
         u = __fdiv_rn(1.f, g);
         if (c0 == 0 && (lane & 3) == 0 && rv) reinterpret_cast<float*>(p.out_rows + Lr.row_off())[r0 + rin] = g;
       }
-      float mul = 0.f, f[8];
-      bool zero;
-      const uint8_t s = block_scale<BLOCK>(block_max<BLOCK>(v[i].max_bits()), u, mul, zero);
-      v[i].floats(f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(f[e], mul);
-      *reinterpret_cast<uint32_t*>(codes_r + ch * 2048 + rin * 16 + (lane & 3) * 4) = zero ? 0u : e2m1x8(f);
-      const int ks = ch * SPC + (BLOCK == 16 ? (lane & 3) >> 1 : 0);
-      if ((lane & (BLOCK == 16 ? 1 : 3)) == 0)
-        sf_r[(ks >> 2) * 512 + (rin & 31) * 16 + (rin >> 5) * 4 + (ks & 3)] = s;
+      uint8_t s;
+      const uint2 code = v[i].template codes<BLOCK>(u, s);
+      const int ch = k >> 5, ks = ch * SPC + (BLOCK == 16 ? half : 0);
+      *reinterpret_cast<uint2*>(codes_r + ch * 2048 + rin * 16 + half * 8) = code;
+      if (BLOCK == 16 || half == 0) sf_r[(ks >> 2) * 512 + (rin & 31) * 16 + (rin >> 5) * 4 + (ks & 3)] = s;
     }
   }
   __syncthreads();
@@ -515,13 +525,13 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* packed, 
   }
 }
 
-// Steps a warp loads together and warps a CTA: about 16 warps, eight steps of
-// bf16 or four of float32 at most (the registers of 1024 threads).
+// Steps a warp loads together and warps a CTA: about 16 warps, four steps of
+// bf16 or two of float32 at most (the registers of 1024 threads).
 template <typename T, int BLOCK, int J>
 cudaError_t launch_rows_j(const Fp4QuantArgs& a, cudaStream_t s) {
   const Fp4Layout L(a.rows, a.cols, BLOCK);
-  const long long units = L.kt * (J == 4 ? 4 : 1);
-  constexpr int MOST = sizeof(T) == 2 ? 8 : 4;
+  const long long units = J == 4 ? L.kt * 2 : (L.kt + 1) / 2;
+  constexpr int MOST = sizeof(T) == 2 ? 4 : 2;
   int iter = 1;
   while (iter < MOST && units > 16 * iter) iter *= 2;
   const int nw = (int)std::min<long long>(32, std::max<long long>(4, (units + iter - 1) / iter));
@@ -532,7 +542,6 @@ cudaError_t launch_rows_j(const Fp4QuantArgs& a, cudaStream_t s) {
   switch (iter) {
     case 1: quantize_rows_kernel<T, BLOCK, J, 1><<<grid, nw * 32, smem, s>>>(a, staged); break;
     case 2: quantize_rows_kernel<T, BLOCK, J, 2><<<grid, nw * 32, smem, s>>>(a, staged); break;
-    case 4: quantize_rows_kernel<T, BLOCK, J, 4><<<grid, nw * 32, smem, s>>>(a, staged); break;
     default: quantize_rows_kernel<T, BLOCK, J, MOST><<<grid, nw * 32, smem, s>>>(a, staged); break;
   }
   return cudaGetLastError();

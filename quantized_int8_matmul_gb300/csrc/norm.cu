@@ -61,7 +61,7 @@ struct Vec<__nv_bfloat16> {
 };
 
 template <typename T>
-__device__ __forceinline__ T from_f(float v);
+__device__ __forceinline__ T from_f(float v);   // rounded to nearest even
 template <>
 __device__ __forceinline__ float from_f<float>(float v) { return v; }
 template <>
@@ -147,12 +147,22 @@ __device__ __forceinline__ void load_w(const void* w, int w_f32, int j, int t, i
         v[4 * q + 3] = f.w;
       }
     } else {
-      const uint32_t* p = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(w) + i);
+      uint32_t f[4];
+      if (E == 8) {
+        const uint4 r = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(w) + i));
+        f[0] = r.x;
+        f[1] = r.y;
+        f[2] = r.z;
+        f[3] = r.w;
+      } else {
+        const uint2 r = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(w) + i));
+        f[0] = r.x;
+        f[1] = r.y;
+      }
 #pragma unroll
-      for (int q = 0; q < E / 2; ++q) {   // E / 2 words: merged into 8- or 16-byte loads
-        const uint32_t f = __ldg(p + q);
-        v[2 * q] = __uint_as_float(f << 16);
-        v[2 * q + 1] = __uint_as_float(f & 0xffff0000u);
+      for (int q = 0; q < E / 2; ++q) {
+        v[2 * q] = __uint_as_float(f[q] << 16);
+        v[2 * q + 1] = __uint_as_float(f[q] & 0xffff0000u);
       }
     }
   } else {
@@ -219,9 +229,25 @@ __device__ __forceinline__ RowScale row_scale(float ss, unsigned amax_bits, int 
   }
   return r;
 }
-__device__ __forceinline__ int quant1(float v, float inv) {
-  const float p = fminf(fmaxf(__fmul_rn(v, inv), -127.f), 127.f);
-  return __float2int_rn(p);
+// E quantised values as bytes, the first in the lowest. |v * inv| is at most
+// 127 (1 + 2^-23), and adding 1.5 * 2^23 rounds such a value to the nearest
+// integer (ties to even) and leaves it in the low bits of the sum: one addition
+// where a conversion runs at an eighth of its rate.
+template <int E>
+__device__ __forceinline__ void quantise(const float* v, float inv, bool zero, uint32_t (&o)[E / 4]) {
+#pragma unroll
+  for (int q = 0; q < E / 4; ++q) {
+    uint32_t b[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) b[e] = __float_as_uint(__fadd_rn(__fmul_rn(v[4 * q + e], inv), 12582912.f));
+    o[q] = zero ? 0u : prmt(prmt(b[0], b[1], 0x0040u), prmt(b[2], b[3], 0x0040u), 0x5410u);
+  }
+}
+// max(a, |b|) that keeps a NaN
+__device__ __forceinline__ float max_abs(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+  return r;
 }
 
 // One row per G = blockDim.x threads (blockDim.y rows a CTA where G is a warp),
@@ -238,8 +264,7 @@ __global__ void __launch_bounds__(1024) rms_norm_s8_kernel(const NormArgs p) {
   const T* r = p.residual ? static_cast<const T*>(p.residual) + m * p.ldr : nullptr;
   T* ho = p.h ? static_cast<T*>(p.h) + m * (long long)n : nullptr;
   int8_t* q = p.q + m * (long long)n;
-  float ss = 0.f;
-  unsigned am = 0u;
+  float ss = 0.f, amax = 0.f;
   // v = h * w of a vector, and its share of the statistics
   auto stats = [&](const uint4& hr, const float* w, float* v) {
     Vec<T>::unpack(hr, v);
@@ -247,23 +272,22 @@ __global__ void __launch_bounds__(1024) rms_norm_s8_kernel(const NormArgs p) {
     for (int e = 0; e < E; ++e) {
       ss = __fmaf_rn(v[e], v[e], ss);
       v[e] = __fmul_rn(v[e], w[e]);
-      am = max(am, __float_as_uint(v[e]) & 0x7fffffffu);
+      amax = max_abs(amax, v[e]);
     }
   };
-  auto quantise = [&](int j, const float* v, float inv, bool zero) {
-    int8_t o[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = zero ? 0 : (int8_t)quant1(v[e], inv);
+  auto put = [&](int j, const float* v, float inv, bool zero) {
+    uint32_t o[E / 4];
+    quantise<E>(v, inv, zero, o);
     if (VEC) {
       const int i = elem<T, VEC>(j, 0, t, G);
       if (i >= n) return;
-      if (E == 8) *reinterpret_cast<uint2*>(q + i) = *reinterpret_cast<const uint2*>(o);
-      else *reinterpret_cast<uint32_t*>(q + i) = *reinterpret_cast<const uint32_t*>(o);
+      if (E == 8) *reinterpret_cast<uint2*>(q + i) = make_uint2(o[0], o[E / 4 - 1]);
+      else *reinterpret_cast<uint32_t*>(q + i) = o[0];
     } else {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const int i = elem<T, VEC>(j, e, t, G);
-        if (i < n) q[i] = o[e];
+        if (i < n) q[i] = (int8_t)(o[e >> 2] >> (8 * (e & 3)));
       }
     }
   };
@@ -287,6 +311,7 @@ __global__ void __launch_bounds__(1024) rms_norm_s8_kernel(const NormArgs p) {
       load_w<T, VEC>(p.w, p.w_f32, j, t, G, n, w);
       stats(h[j], w, v[j]);
     }
+    unsigned am = __float_as_uint(amax);
     row_sum_max(ss, am, G, sa, sb);
     const RowScale s = row_scale(ss, am, n, p.eps);
     if (t == 0) {
@@ -294,7 +319,7 @@ __global__ void __launch_bounds__(1024) rms_norm_s8_kernel(const NormArgs p) {
       p.rstd[m] = s.rstd;
     }
 #pragma unroll
-    for (int j = 0; j < K; ++j) quantise(j, v[j], s.inv, am >= kInfBits);
+    for (int j = 0; j < K; ++j) put(j, v[j], s.inv, am >= kInfBits);
   } else {
     const int steps = (n + G * E - 1) / (G * E);
     for (int j = 0; j < steps; ++j) {
@@ -305,6 +330,7 @@ __global__ void __launch_bounds__(1024) rms_norm_s8_kernel(const NormArgs p) {
       load_w<T, VEC>(p.w, p.w_f32, j, t, G, n, w);
       stats(h, w, v);
     }
+    unsigned am = __float_as_uint(amax);
     row_sum_max(ss, am, G, sa, sb);
     const RowScale s = row_scale(ss, am, n, p.eps);
     if (t == 0) {
@@ -320,7 +346,7 @@ __global__ void __launch_bounds__(1024) rms_norm_s8_kernel(const NormArgs p) {
       Vec<T>::unpack(h, v);
 #pragma unroll
       for (int e = 0; e < E; ++e) v[e] = __fmul_rn(v[e], w[e]);
-      quantise(j, v, s.inv, am >= kInfBits);
+      put(j, v, s.inv, am >= kInfBits);
     }
   }
 }
@@ -371,12 +397,8 @@ __global__ void __launch_bounds__(256) s8_dequantize_rows_kernel(const int8_t* q
 // that HBM stays busy through a row's reduction. NV = 0: rows of any length,
 // read twice, the shares of dweight accumulated in partials itself.
 constexpr int PF = 2;
-template <typename T>
-constexpr int backward_threads(int nv) {   // at most, so that a thread's registers suffice
-  return nv == 0 ? 1024 : nv == 4 ? (sizeof(T) == 4 ? 704 : 576) : 512;
-}
-template <typename T, bool VEC, int NV>
-__global__ void __launch_bounds__(backward_threads<T>(NV), NV == 1 ? 3 : NV == 2 ? 2 : 1)
+template <typename T, bool VEC, int NV, bool DH>
+__global__ void __launch_bounds__(1024)
     rms_norm_backward_kernel(const NormBwdArgs p) {
   constexpr int E = Vec<T>::E;
   constexpr int K = NV > 0 ? NV : 1;
@@ -386,7 +408,7 @@ __global__ void __launch_bounds__(backward_threads<T>(NV), NV == 1 ? 3 : NV == 2
   const long long step = (long long)gridDim.x * blockDim.y;
   const T* h0 = static_cast<const T*>(p.h);
   const T* dy0 = static_cast<const T*>(p.dy);
-  const T* dh0 = static_cast<const T*>(p.dh);
+  const T* dh0 = DH ? static_cast<const T*>(p.dh) : nullptr;
   float* part = p.partials + (long long)blockIdx.x * n;
   auto prefetch = [&](long long m) {
     if (!VEC || t >= 3 || m >= p.M) return;
@@ -397,29 +419,31 @@ __global__ void __launch_bounds__(backward_threads<T>(NV), NV == 1 ? 3 : NV == 2
   long long m = (long long)blockIdx.x * blockDim.y + threadIdx.y;
   int par = 0;
   if (NV > 0) {
-    float dw[K][E];
+    constexpr bool HELD = NV == 1;   // the weight in registers too
+    float dw[K][E], w[E];
 #pragma unroll
     for (int j = 0; j < K; ++j)
 #pragma unroll
       for (int e = 0; e < E; ++e) dw[j][e] = 0.f;
+    if (HELD) load_w<T, VEC>(p.w, p.w_f32, 0, t, G, n, w);
     for (int i = 1; i < PF; ++i) prefetch(m + i * step);
     for (; m < p.M; m += step) {
       prefetch(m + PF * step);
       const float rstd = __ldg(p.rstd + m);
-      uint4 h[K], dy[K], dh[K];
+      uint4 h[K], dy[K], dh[DH ? K : 1];
 #pragma unroll
       for (int j = 0; j < K; ++j) h[j] = load_vec<T, VEC>(h0 + m * p.ldh, j, t, G, n);
 #pragma unroll
       for (int j = 0; j < K; ++j) dy[j] = load_vec<T, VEC>(dy0 + m * p.lddy, j, t, G, n);
-      if (dh0) {
+      if (DH) {
 #pragma unroll
-        for (int j = 0; j < K; ++j) dh[j] = load_vec<T, VEC>(dh0 + m * p.lddh, j, t, G, n);
+        for (int j = 0; j < K; ++j) dh[DH ? j : 0] = load_vec<T, VEC>(dh0 + m * p.lddh, j, t, G, n);
       }
       float dot = 0.f;
 #pragma unroll
       for (int j = 0; j < K; ++j) {
-        float w[E], nn[E], g[E];
-        load_w<T, VEC>(p.w, p.w_f32, j, t, G, n, w);
+        float nn[E], g[E];
+        if (!HELD) load_w<T, VEC>(p.w, p.w_f32, j, t, G, n, w);
         Vec<T>::unpack(h[j], nn);
         Vec<T>::unpack(dy[j], g);
 #pragma unroll
@@ -429,18 +453,18 @@ __global__ void __launch_bounds__(backward_threads<T>(NV), NV == 1 ? 3 : NV == 2
           dot = __fmaf_rn(g[e] * w[e], nn[e], dot);
         }
       }
-      const float mean = row_sum(dot, G, sa[par]) / (float)n;
+      const float c = -(row_sum(dot, G, sa[par]) / (float)n) * rstd;   // dx = g * rstd + n * c
       par ^= 1;
 #pragma unroll
       for (int j = 0; j < K; ++j) {
-        float w[E], v[E], g[E];
-        load_w<T, VEC>(p.w, p.w_f32, j, t, G, n, w);
+        float v[E], g[E];
+        if (!HELD) load_w<T, VEC>(p.w, p.w_f32, j, t, G, n, w);
         Vec<T>::unpack(h[j], v);
         Vec<T>::unpack(dy[j], g);
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = __fmaf_rn(-(v[e] * rstd), mean, g[e] * w[e]) * rstd;
-        if (dh0) {
-          Vec<T>::unpack(dh[j], g);
+        for (int e = 0; e < E; ++e) v[e] = __fmaf_rn(v[e] * rstd, c, g[e] * w[e] * rstd);
+        if (DH) {
+          Vec<T>::unpack(dh[DH ? j : 0], g);
 #pragma unroll
           for (int e = 0; e < E; ++e) v[e] += g[e];
         }
@@ -483,7 +507,7 @@ __global__ void __launch_bounds__(backward_threads<T>(NV), NV == 1 ? 3 : NV == 2
         float h[E], dy[E], dh[E], w[E];
         Vec<T>::unpack(load_vec<T, VEC>(h0 + m * p.ldh, j, t, G, n), h);
         Vec<T>::unpack(load_vec<T, VEC>(dy0 + m * p.lddy, j, t, G, n), dy);
-        if (dh0) Vec<T>::unpack(load_vec<T, VEC>(dh0 + m * p.lddh, j, t, G, n), dh);
+        if (DH) Vec<T>::unpack(load_vec<T, VEC>(dh0 + m * p.lddh, j, t, G, n), dh);
         load_w<T, VEC>(p.w, p.w_f32, j, t, G, n, w);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
@@ -491,7 +515,7 @@ __global__ void __launch_bounds__(backward_threads<T>(NV), NV == 1 ? 3 : NV == 2
           const int i = elem<T, VEC>(j, e, t, G);
           if (i < n) part[i] = __fmaf_rn(dy[e], nn, fresh ? 0.f : part[i]);
           h[e] = __fmaf_rn(-nn, mean, dy[e] * w[e]) * rstd;
-          if (dh0) h[e] += dh[e];
+          if (DH) h[e] += dh[e];
         }
         store_vec<T, VEC>(static_cast<T*>(p.dx) + m * (long long)n, j, t, G, n, Vec<T>::pack(h));
       }
@@ -527,9 +551,11 @@ bool rows_vec(const void* p, long long ld) {
 
 int round32(int v) { return (v + 31) / 32 * 32; }
 
-// Vectors a thread and threads a row. With rows enough to fill the GPU, two or
-// four vectors a thread (more loads in flight, fewer warps in the reduction);
-// with few rows one (the row's latency). Rows of one warp share a CTA.
+// Vectors a thread and threads a row. With rows enough to fill the GPU, four
+// vectors a thread (fewer warps to run the per-row steps); with few rows one (the
+// row's latency). Rows of one warp share a CTA. Long rows are read twice, by CTAs
+// small enough that several share an SM: held in registers, a row leaves no room
+// for the next one's loads (4096 x 11008 float32: 105 us read twice, 144 held).
 template <typename T>
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
   constexpr int E = Vec<T>::E;
@@ -538,9 +564,9 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
                    (reinterpret_cast<uintptr_t>(a.q) % 8) == 0;
   const int nvec = (a.H + E - 1) / E;
   const bool many = a.M >= 2 * num_sms();
-  int nv = nvec <= 32 ? 1 : many ? (nvec <= 256 ? 1 : nvec <= 1024 ? 2 : 4) : (nvec <= 1024 ? 1 : nvec <= 2048 ? 2 : 4);
-  if (nvec > 4096) nv = 0;
-  const int G = nv ? std::max(32, round32((nvec + nv - 1) / nv)) : 1024;
+  int nv = many ? (nvec <= 32 ? 1 : nvec <= 128 ? 2 : 4) : (nvec <= 1024 ? 1 : nvec <= 2048 ? 2 : 4);
+  if (nvec > (many ? 2048 : 4096)) nv = 0;
+  const int G = nv ? std::max(32, round32((nvec + nv - 1) / nv)) : many ? 512 : 1024;
   const int R = G == 32 ? (many ? 8 : 1) : 1;
   const dim3 block(G, R);
   const unsigned grid = (unsigned)((a.M + R - 1) / R);
@@ -577,8 +603,10 @@ cudaError_t launch_dequantize(const int8_t* q, const float* scale, long long M, 
 }
 
 // Launch shape of the backward pass: vectors a thread, threads a row, rows of a
-// CTA at a time, CTAs (= rows of partials). The CTAs are those that fit at once,
-// at most 8 an SM for narrow rows (each adds a row to sum_partials' work).
+// CTA at a time, CTAs (= rows of partials). 64 registers hold one vector of each
+// tensor with its weight and sums, two, or three of float32; longer rows are
+// read twice. The CTAs are those that fit at once (1024 threads an SM), at most 8
+// an SM for narrow rows (each adds a row to sum_partials' work).
 struct BwdShape {
   int nv, G, R, parts;
 };
@@ -587,27 +615,27 @@ BwdShape backward_shape(long long M, int H) {
   constexpr int E = Vec<T>::E;
   BwdShape b;
   const int nvec = (H + E - 1) / E;
-  b.nv = nvec <= 512 ? 1 : nvec <= 1024 ? 2 : nvec <= 4 * backward_threads<T>(4) ? 4 : 0;
+  b.nv = nvec <= 1024 ? 1 : nvec <= 2048 ? 2 : sizeof(T) == 4 && nvec <= 3072 ? 3 : 0;
   b.G = b.nv ? std::max(32, round32((nvec + b.nv - 1) / b.nv)) : 1024;
   b.R = b.G == 32 ? 8 : 1;
-  const int per_sm = b.nv == 1 ? std::min(8, 1536 / (b.G * b.R)) : b.nv == 2 ? 2 : 1;
-  b.parts = (int)std::min<long long>((M + b.R - 1) / b.R, 152ll * std::max(1, per_sm));
+  const int per_sm = std::max(1, std::min(8, 1024 / (b.G * b.R)));
+  b.parts = (int)std::min<long long>((M + b.R - 1) / b.R, 152ll * per_sm);
   return b;
 }
 
-template <typename T>
+template <typename T, bool DH>
 cudaError_t launch_backward(const NormBwdArgs& a, cudaStream_t s) {
   constexpr int E = Vec<T>::E;
   const bool vec = a.H % E == 0 && rows_vec<T>(a.h, a.ldh) && rows_vec<T>(a.dy, a.lddy) &&
                    rows_vec<T>(a.dh, a.lddh) && rows_vec<T>(a.dx, a.H) && (reinterpret_cast<uintptr_t>(a.w) % 16) == 0;
   const BwdShape b = backward_shape<T>(a.M, a.H);
   const dim3 block(b.G, b.R);
-#define QMM_NORM(V)                                                                           \
-  switch (b.nv) {                                                                             \
-    case 1: rms_norm_backward_kernel<T, V, 1><<<b.parts, block, 0, s>>>(a); break;            \
-    case 2: rms_norm_backward_kernel<T, V, 2><<<b.parts, block, 0, s>>>(a); break;            \
-    case 4: rms_norm_backward_kernel<T, V, 4><<<b.parts, block, 0, s>>>(a); break;            \
-    default: rms_norm_backward_kernel<T, V, 0><<<b.parts, block, 0, s>>>(a); break;           \
+#define QMM_NORM(V)                                                                               \
+  switch (b.nv) {                                                                                 \
+    case 1: rms_norm_backward_kernel<T, V, 1, DH><<<b.parts, block, 0, s>>>(a); break;            \
+    case 2: rms_norm_backward_kernel<T, V, 2, DH><<<b.parts, block, 0, s>>>(a); break;            \
+    case 3: rms_norm_backward_kernel<T, V, sizeof(T) == 4 ? 3 : 0, DH><<<b.parts, block, 0, s>>>(a); break; \
+    default: rms_norm_backward_kernel<T, V, 0, DH><<<b.parts, block, 0, s>>>(a); break;           \
   }
   if (vec) {
     QMM_NORM(true)
@@ -651,7 +679,9 @@ int rms_norm_backward_partials(long long M, int H) {
 
 cudaError_t launch_rms_norm_backward(const NormBwdArgs& a, bool bf16, cudaStream_t s, const char** kernel_name) {
   *kernel_name = "rms_norm_backward+sum_partials";
-  return bf16 ? norm::launch_backward<__nv_bfloat16>(a, s) : norm::launch_backward<float>(a, s);
+  if (bf16)
+    return a.dh ? norm::launch_backward<__nv_bfloat16, true>(a, s) : norm::launch_backward<__nv_bfloat16, false>(a, s);
+  return a.dh ? norm::launch_backward<float, true>(a, s) : norm::launch_backward<float, false>(a, s);
 }
 
 }  // namespace qmm
