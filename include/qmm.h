@@ -536,8 +536,8 @@ qmm_status qmm_w8_dequant_packed(const void* A, int64_t M, int64_t K, int64_t N,
  *  h             [M,H] of x's type, contiguous: receives x + residual (may be
  *                NULL: not stored; may be x or residual where those are
  *                contiguous: a row is read before it is written)
- *  q             [M,H] int8;  scale, rstd  float[M] (rstd is what the gradient
- *                takes)
+ *  q             [M,H] int8;  scale  float[M];  rstd  float[M] or NULL (not
+ *                stored): what the gradient takes
  * s8_dequantize_rows reads such rows back: y[m,i] = y_dtype(q[m,i] * scale[m]).
  *
  * The gradient, with the quantiser passed straight through (the gradient of

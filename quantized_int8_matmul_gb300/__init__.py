@@ -5,7 +5,9 @@ tensors, passes raw device pointers, sizes and the current CUDA stream to the
 C ABI of the same name (include/qmm.h), and raises ``QmmError`` on a non-OK
 status. Every step of the computation runs in the library's CUDA kernels;
 there is no CPU or PyTorch fallback. Output tensors are allocated with torch
-when the caller does not pass one (device memory is PyTorch's job here).
+when the caller does not pass one (device memory is PyTorch's job here). The
+marshalling of the calls that are often shorter than their marshalling (the norm,
+4-bit floats) is native, in the ``_binding`` module; the others use ctypes.
 
 If the shared library is missing it is built from ``csrc/`` with nvcc on
 first import; if that fails the import fails loudly.
@@ -13,7 +15,6 @@ first import; if that fails the import fails loudly.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from typing import NamedTuple
 
@@ -106,21 +107,10 @@ def _load() -> ctypes.CDLL:
     lib.qmm_w8_dequant_packed_workspace_bytes.restype = sz
     lib.qmm_w8_dequant_packed.argtypes = [vp, i64, i64, i64, vp, sz, vp, i64, vp, i64, vp, ci, vp, sz, vp]
     lib.qmm_w8_dequant_packed.restype = ci
-    cf = ctypes.c_float
-    lib.qmm_rms_norm_s8.argtypes = [vp, ci, i64, i64, i64, vp, i64, vp, ci, cf, vp, vp, vp, vp, vp]
-    lib.qmm_s8_dequantize_rows.argtypes = [vp, vp, i64, i64, vp, ci, vp]
     lib.qmm_rms_norm_backward_workspace_bytes.argtypes = [i64, i64]
     lib.qmm_rms_norm_backward_workspace_bytes.restype = sz
-    lib.qmm_rms_norm_backward.argtypes = [vp, i64, vp, i64, vp, i64, ci, i64, i64, vp, ci, vp, vp, vp, vp, sz, vp]
     lib.qmm_fp4_bytes.argtypes = [i64, i64, ci]
     lib.qmm_fp4_bytes.restype = sz
-    lib.qmm_fp4_quantize.argtypes = [vp, ci, i64, i64, i64, ci, ci, vp, sz, vp]
-    lib.qmm_fp4_quantize_both.argtypes = [vp, ci, i64, i64, i64, ci, vp, sz, vp, sz, vp]
-    lib.qmm_fp4_dequantize.argtypes = [vp, sz, i64, i64, ci, vp, ci, vp]
-    lib.qmm_fp4_matmul.argtypes = [vp, sz, i64, vp, sz, i64, i64, ci, vp, ci, vp]
-    for fn in ("qmm_rms_norm_s8", "qmm_s8_dequantize_rows", "qmm_rms_norm_backward", "qmm_fp4_quantize",
-               "qmm_fp4_quantize_both", "qmm_fp4_dequantize", "qmm_fp4_matmul"):
-        getattr(lib, fn).restype = ci
     lib.qmm_int8_mma_peak_launch.argtypes = [ci, ctypes.POINTER(ctypes.c_double), vp]
     lib.qmm_int8_mma_peak_launch.restype = ci
     return lib
@@ -128,6 +118,8 @@ def _load() -> ctypes.CDLL:
 
 _lib = _load()
 LIB_PATH = _build.LIB_PATH
+
+from . import _binding  # noqa: E402  (built beside libqmm.so, which it links)
 
 
 def lib() -> ctypes.CDLL:
@@ -703,106 +695,39 @@ def dynamic_quantize_linear(x, row_len=None, workspace=None, y=None, stream=None
     return y, y_scale, y_zp
 
 
-def _need_rows(t, dtypes, name, shape=None):
-    """A 2-D CUDA tensor whose rows are contiguous (any row stride >= its width);
-    returns the row stride in elements."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: dtype {t.dtype} not in {dtypes}")
-    size = t.shape
-    if len(size) != 2:
-        raise ValueError(f"{name} must be 2-D")
-    if shape is not None and size != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}")
-    rows, cols = size
-    if t.is_contiguous():
-        return cols
-    ld, step = t.stride()
-    if rows <= 1:                   # the row stride is never used
-        ld = cols
-    if (cols > 1 and step != 1) or ld < cols:
-        raise ValueError(f"{name}: rows must be contiguous and not overlap")
-    return ld
-
-
-_FLOATS = (torch.float32, torch.bfloat16)
-_F32, _S8, _U8 = (torch.float32,), (torch.int8,), (torch.uint8,)
-
-
-def _need_out(t, dtypes, name, shape):
-    _need(t, dtypes, name)
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}")
-
-
 class RmsNormS8(NamedTuple):
     """qmm_rms_norm_s8's outputs: the int8 rows and their scales (A and act_scale
-    of qmm_a8w8), the sum x + residual (x itself without a residual) and the
-    reciprocal root mean square, which qmm_rms_norm_backward takes."""
+    of qmm_a8w8), the sum x + residual (x itself without a residual) and, where
+    asked for, the reciprocal root mean square that qmm_rms_norm_backward takes."""
     q: torch.Tensor
     scale: torch.Tensor
     h: torch.Tensor
-    rstd: torch.Tensor
+    rstd: torch.Tensor | None
 
 
-def qmm_rms_norm_s8(x, weight, residual=None, eps=1e-6, out=None, h_out=None, stream=None) -> RmsNormS8:
+def qmm_rms_norm_s8(x, weight, residual=None, eps=1e-6, out=None, h_out=None, save_rstd=False,
+                    stream=None) -> RmsNormS8:
     """h = x + residual (rounded to x's type), then h / rms(h) * weight as int8
     rows with one float32 scale each: q = rne(v * (127 / max|v|)), v = h * weight.
 
     x (and residual) float32 or bfloat16 [M, H], rows contiguous at any stride;
     weight float32 or bfloat16 [H]. out: int8 [M, H]; h_out: [M, H] of x's type,
-    may be x or residual itself. A row that holds a NaN or an infinity gets a NaN
-    scale."""
-    ldx = _need_rows(x, _FLOATS, "x")
-    shape, dt, dev = x.shape, x.dtype, x.device
-    M, H = shape
-    _need_out(weight, _FLOATS, "weight", (H,))
-    if out is None:
-        out = torch.empty(shape, dtype=torch.int8, device=dev)
-    else:
-        _need_out(out, _S8, "out", shape)
-    if residual is None:
-        if h_out is not None:
-            raise ValueError("h_out without a residual: h is x")
-        h, ldr, rp, hp = x, H, None, None
-    else:
-        ldr = _need_rows(residual, (dt,), "residual", shape)
-        if h_out is None:
-            h = torch.empty(shape, dtype=dt, device=dev)
-        else:
-            h = h_out
-            _need_out(h, (dt,), "h_out", shape)
-        rp, hp = residual.data_ptr(), h.data_ptr()
-    scale = torch.empty(M, dtype=torch.float32, device=dev)
-    rstd = torch.empty(M, dtype=torch.float32, device=dev)
-    st = _lib.qmm_rms_norm_s8(x.data_ptr(), _TORCH_TO_QMM[dt], M, H, ldx, rp, ldr, weight.data_ptr(),
-                              _TORCH_TO_QMM[weight.dtype], eps, hp, out.data_ptr(), scale.data_ptr(),
-                              rstd.data_ptr(), _stream(stream))
-    if st:
-        _check("qmm_rms_norm_s8", st)
-    return RmsNormS8(out, scale, h, rstd)
+    may be x or residual itself. save_rstd: return rstd [M] for the gradient. A row
+    that holds a NaN or an infinity gets a NaN scale."""
+    r = _binding.rms_norm_s8(x, weight, residual, eps, out, h_out, save_rstd, stream)
+    if type(r) is int:
+        raise QmmError("qmm_rms_norm_s8", r)
+    return RmsNormS8._make(r)
 
 
 def qmm_s8_dequantize_rows(q, scale, out=None, out_dtype=torch.bfloat16, stream=None):
     """int8 rows read back: out[m, i] = q[m, i] * scale[m], float32 or bfloat16."""
-    _need(q, _S8, "q")
-    shape = q.shape
-    if len(shape) != 2:
-        raise ValueError("q must be 2-D")
-    M, H = shape
-    _need_out(scale, _F32, "scale", (M,))
-    if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=q.device)
-    _need_out(out, _FLOATS, "out", shape)
-    st = _lib.qmm_s8_dequantize_rows(q.data_ptr(), scale.data_ptr(), M, H, out.data_ptr(), _TORCH_TO_QMM[out.dtype],
-                                     _stream(stream))
-    if st:
-        _check("qmm_s8_dequantize_rows", st)
-    return out
+    r = _binding.s8_dequantize_rows(q, scale, out, out_dtype, stream)
+    if type(r) is int:
+        raise QmmError("qmm_s8_dequantize_rows", r)
+    return r
 
 
-@functools.lru_cache(maxsize=256)
 def qmm_rms_norm_backward_workspace_bytes(M: int, H: int) -> int:
     return int(_lib.qmm_rms_norm_backward_workspace_bytes(M, H))
 
@@ -812,29 +737,12 @@ def qmm_rms_norm_backward(dy, h, weight, rstd, dh=None, out=None, dweight=None, 
     (dx [M, H] of h's type, dweight float32 [H]) from dy, the gradient of the
     normalised rows, and dh, the gradient that reaches h past the norm (or None).
     h and rstd as the forward call returned them; dx is the gradient of x and of
-    the residual alike. dweight sums the rows in a fixed order."""
-    ldh = _need_rows(h, _FLOATS, "h")
-    shape, dt, dev = h.shape, h.dtype, h.device
-    M, H = shape
-    lddy = _need_rows(dy, (dt,), "dy", shape)
-    lddh = H if dh is None else _need_rows(dh, (dt,), "dh", shape)
-    _need_out(weight, _FLOATS, "weight", (H,))
-    _need_out(rstd, _F32, "rstd", (M,))
-    if out is None:
-        out = torch.empty(shape, dtype=dt, device=dev)
-    else:
-        _need_out(out, (dt,), "out", shape)
-    if dweight is None:
-        dweight = torch.empty(H, dtype=torch.float32, device=dev)
-    else:
-        _need_out(dweight, _F32, "dweight", (H,))
-    ws, wsb = _workspace(workspace, qmm_rms_norm_backward_workspace_bytes(M, H), dev)
-    st = _lib.qmm_rms_norm_backward(dy.data_ptr(), lddy, h.data_ptr(), ldh, _ptr(dh), lddh, _TORCH_TO_QMM[dt], M, H,
-                                    weight.data_ptr(), _TORCH_TO_QMM[weight.dtype], rstd.data_ptr(), out.data_ptr(),
-                                    dweight.data_ptr(), _ptr(ws), wsb, _stream(stream))
-    if st:
-        _check("qmm_rms_norm_backward", st)
-    return out, dweight
+    the residual alike. dweight sums the rows in a fixed order. workspace: "auto"
+    or a device tensor of qmm_rms_norm_backward_workspace_bytes(M, H) bytes."""
+    r = _binding.rms_norm_backward(dy, h, weight, rstd, dh, out, dweight, stream, workspace)
+    if type(r) is int:
+        raise QmmError("qmm_rms_norm_backward", r)
+    return r
 
 
 class Fp4Matrix(NamedTuple):
@@ -846,65 +754,57 @@ class Fp4Matrix(NamedTuple):
     block: int
 
 
-@functools.lru_cache(maxsize=256)
 def qmm_fp4_bytes(rows: int, cols: int, block: int) -> int:
     return int(_lib.qmm_fp4_bytes(rows, cols, block))
 
 
-def _fp4_new(rows, cols, block, device, out, name):
-    if block not in (16, 32):
-        raise ValueError("block must be 16 or 32")
-    if out is None:
-        return Fp4Matrix(torch.empty(qmm_fp4_bytes(rows, cols, block), dtype=torch.uint8, device=device), rows, cols,
-                         block)
-    if (out.rows, out.cols, out.block) != (rows, cols, block):
+def _fp4_buf(m, rows, cols, block, name):
+    """The buffer of an Fp4Matrix that the caller wants filled."""
+    if (m.rows, m.cols, m.block) != (rows, cols, block):
         raise ValueError(f"{name} must be a packed [{rows}, {cols}] matrix of block {block}")
-    _need(out.buf, (torch.uint8,), name)
-    return out
+    return m.buf
+
+
+def _fp4_extents(x, block):
+    if block != 16 and block != 32:
+        raise ValueError("block must be 16 or 32")
+    size = x.shape
+    if len(size) != 2:
+        raise ValueError("x must be 2-D")
+    return size
 
 
 def qmm_fp4_quantize(x, block=16, transpose=False, out=None, stream=None) -> Fp4Matrix:
     """Pack x [R, C] (float32 or bfloat16, rows contiguous at any stride) to 4-bit
     floats, blocks running along its rows; with transpose, the packed matrix is
     x.T [C, R], blocks running down x's columns. out: an Fp4Matrix to reuse."""
-    ldx = _need_rows(x, _FLOATS, "x")
-    R, C = x.shape
-    rows, cols = (C, R) if transpose else (R, C)
-    m = _fp4_new(rows, cols, block, x.device, out, "out")
-    buf = m.buf
-    st = _lib.qmm_fp4_quantize(x.data_ptr(), _TORCH_TO_QMM[x.dtype], rows, cols, ldx, 1 if transpose else 0, block,
-                               buf.data_ptr(), buf.numel(), _stream(stream))
-    if st:
-        _check("qmm_fp4_quantize", st)
-    return m
+    rows, cols = _fp4_extents(x, block)
+    if transpose:
+        rows, cols = cols, rows
+    buf = None if out is None else _fp4_buf(out, rows, cols, block, "out")
+    r = _binding.fp4_quantize(x, block, transpose, buf, stream)
+    if type(r) is int:
+        raise QmmError("qmm_fp4_quantize", r)
+    return Fp4Matrix(r, rows, cols, block)
 
 
 def qmm_fp4_quantize_both(x, block=16, out=None, out_t=None, stream=None):
     """(qmm_fp4_quantize(x), qmm_fp4_quantize(x, transpose=True)) from one read of x."""
-    ldx = _need_rows(x, _FLOATS, "x")
-    R, C = x.shape
-    m = _fp4_new(R, C, block, x.device, out, "out")
-    t = _fp4_new(C, R, block, x.device, out_t, "out_t")
-    a, b = m.buf, t.buf
-    st = _lib.qmm_fp4_quantize_both(x.data_ptr(), _TORCH_TO_QMM[x.dtype], R, C, ldx, block, a.data_ptr(), a.numel(),
-                                    b.data_ptr(), b.numel(), _stream(stream))
-    if st:
-        _check("qmm_fp4_quantize_both", st)
-    return m, t
+    R, C = _fp4_extents(x, block)
+    buf = None if out is None else _fp4_buf(out, R, C, block, "out")
+    buf_t = None if out_t is None else _fp4_buf(out_t, C, R, block, "out_t")
+    r = _binding.fp4_quantize_both(x, block, buf, buf_t, stream)
+    if type(r) is int:
+        raise QmmError("qmm_fp4_quantize_both", r)
+    return Fp4Matrix(r[0], R, C, block), Fp4Matrix(r[1], C, R, block)
 
 
 def qmm_fp4_dequantize(m: Fp4Matrix, out=None, out_dtype=torch.bfloat16, stream=None):
     """A packed matrix read back to float32 or bfloat16 [rows, cols]."""
-    buf, rows, cols, block = m
-    _need(buf, _U8, "m")
-    if out is None:
-        out = torch.empty((rows, cols), dtype=out_dtype, device=buf.device)
-    _need_out(out, _FLOATS, "out", (rows, cols))
-    st = _lib.qmm_fp4_dequantize(buf.data_ptr(), buf.numel(), rows, cols, block, out.data_ptr(),
-                                 _TORCH_TO_QMM[out.dtype], _stream(stream))
-    if st:
-        _check("qmm_fp4_dequantize", st)
-    return out
+    r = _binding.fp4_dequantize(*m, out, out_dtype, stream)
+    if type(r) is int:
+        raise QmmError("qmm_fp4_dequantize", r)
+    return r
 
 
 def qmm_fp4_matmul(a: Fp4Matrix, b: Fp4Matrix, out=None, out_dtype=torch.bfloat16, stream=None):
@@ -913,20 +813,14 @@ def qmm_fp4_matmul(a: Fp4Matrix, b: Fp4Matrix, out=None, out_dtype=torch.bfloat1
     one fp32 accumulation."""
     abuf, M, K, block = a
     bbuf, N, Kb, block_b = b
-    _need(abuf, _U8, "a")
-    _need(bbuf, _U8, "b")
     if K != Kb:
         raise ValueError("inner dimensions differ")
     if block != block_b:
         raise ValueError("operands of different blocks")
-    if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=abuf.device)
-    _need_out(out, _FLOATS, "out", (M, N))
-    st = _lib.qmm_fp4_matmul(abuf.data_ptr(), abuf.numel(), M, bbuf.data_ptr(), bbuf.numel(), N, K, block,
-                             out.data_ptr(), _TORCH_TO_QMM[out.dtype], _stream(stream))
-    if st:
-        _check("qmm_fp4_matmul", st)
-    return out
+    r = _binding.fp4_matmul(abuf, M, bbuf, N, K, block, out, out_dtype, stream)
+    if type(r) is int:
+        raise QmmError("qmm_fp4_matmul", r)
+    return r
 
 
 def num_sms() -> int:

@@ -3,21 +3,27 @@
 Each translation unit under ``csrc/`` is compiled in parallel to an object in
 ``_build/`` and the objects are linked into ``libqmm.so`` next to this file,
 with the CUDA runtime linked statically so the library loads on a host that
-has the toolkit but no driver (the exported-symbol checks run there).
-A rebuild happens only when a source or header is newer than the library.
+has the toolkit but no driver (the exported-symbol checks run there). The
+host-only ``csrc/binding.cpp`` becomes the Python module ``_binding`` (argument
+marshalling against torch's headers), linked to ``libqmm.so``.
+A rebuild happens only when a source or header is newer than the libraries.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 REPO_DIR = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libqmm.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING_PATH = os.path.join(PKG_DIR, "_binding.so")
 HEADERS = [os.path.join(REPO_DIR, "include", "qmm.h")]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -38,23 +44,44 @@ def sources() -> list[str]:
 
 def _inputs() -> list[str]:
     hdrs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    return sources() + hdrs + HEADERS + [__file__]
+    return sources() + hdrs + HEADERS + [BINDING_SRC, __file__]
 
 
 def needs_build() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
         return True
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
     return any(os.path.getmtime(p) > t for p in _inputs())
 
 
+def _torch_dir() -> str:
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def _cxx() -> str:
+    return os.environ.get("CXX") or shutil.which("g++") or "c++"
+
+
 def _compile(src: str) -> str:
-    obj = os.path.join(BUILD_DIR, os.path.basename(src)[:-3] + ".o")
-    cmd = [nvcc_path(), *ARCH_FLAGS, *NVCC_FLAGS, "-c", src, "-o", obj]
+    obj = os.path.join(BUILD_DIR, os.path.splitext(os.path.basename(src))[0] + ".o")
+    if src == BINDING_SRC:
+        cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+        cmd = [_cxx(), "-O2", "-std=c++17", "-fPIC", "-Wall", "-I" + os.path.join(_torch_dir(), "include"),
+               "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(cuda, "include"), "-c", src, "-o", obj]
+    else:
+        cmd = [nvcc_path(), *ARCH_FLAGS, *NVCC_FLAGS, "-c", src, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"compiling {os.path.basename(src)} failed:\n{r.stdout}\n{r.stderr}")
     return obj
+
+
+def _link(cmd: list[str], path: str) -> None:
+    tmp = path + ".tmp"
+    r = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"linking {os.path.basename(path)} failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, path)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -62,15 +89,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not needs_build():
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
-    srcs = sources()
+    srcs = [BINDING_SRC, *sources()]
     with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
-        objs = list(ex.map(_compile, srcs))
-    tmp = LIB_PATH + ".tmp"
-    cmd = [nvcc_path(), *ARCH_FLAGS, "-shared", "-cudart", "static", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB_PATH)
+        binding, *objs = ex.map(_compile, srcs)
+    _link([nvcc_path(), *ARCH_FLAGS, "-shared", "-cudart", "static", *objs], LIB_PATH)
+    tlib = os.path.join(_torch_dir(), "lib")
+    _link([_cxx(), "-shared", binding, "-L" + PKG_DIR, "-l:libqmm.so", "-Wl,-rpath,$ORIGIN", "-L" + tlib,
+           "-Wl,-rpath," + tlib, "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"], BINDING_PATH)
     if verbose:
         print(f"built {LIB_PATH}")
     return LIB_PATH

@@ -1,0 +1,340 @@
+// Native argument marshalling for the entry points whose calls are often a few
+// microseconds of GPU time: checks torch tensors, allocates outputs, passes
+// pointers, sizes and the stream to the C ABI (include/qmm.h) -- what the package's
+// Python functions do through ctypes, without their interpreter time (a norm of
+// one 4096-wide row: 17.7 us a call marshalled in Python, of which the launch is 3).
+// A function returns its tensors, or the C ABI's status as an int if that is not
+// QMM_OK; malformed tensors raise ValueError.
+#define PY_SSIZE_T_CLEAN
+#include <Python.h>
+
+#include <ATen/core/Tensor.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Dtype.h>
+#include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <exception>
+#include <initializer_list>
+#include <optional>
+#include <string>
+
+#include "../../include/qmm.h"
+
+namespace {
+
+struct Error : std::exception {   // a Python exception is set
+  const char* what() const noexcept override { return "python error"; }
+};
+[[noreturn]] void fail(const std::string& msg) {
+  PyErr_SetString(PyExc_ValueError, msg.c_str());
+  throw Error();
+}
+
+using at::ScalarType;
+using at::Tensor;
+using Types = std::initializer_list<ScalarType>;
+
+int qmm_type(ScalarType t) {
+  return t == ScalarType::Float ? QMM_F32 : t == ScalarType::BFloat16 ? QMM_BF16 : t == ScalarType::Char ? QMM_S8
+         : t == ScalarType::Byte ? QMM_U8 : QMM_S32;
+}
+
+std::string shape_text(at::IntArrayRef s) {
+  std::string r = "(";
+  for (size_t i = 0; i < s.size(); ++i) r += (i ? ", " : "") + std::to_string(s[i]);
+  return r + (s.size() == 1 ? ",)" : ")");
+}
+
+const Tensor& tensor(PyObject* o, const char* name) {
+  if (!THPVariable_Check(o)) {
+    PyErr_Format(PyExc_TypeError, "%s must be a tensor", name);
+    throw Error();
+  }
+  return THPVariable_Unpack(o);
+}
+
+void check_type(const Tensor& t, Types types, const char* name) {
+  if (!t.is_cuda()) fail(std::string(name) + " must be a CUDA tensor");
+  for (ScalarType s : types)
+    if (t.scalar_type() == s) return;
+  fail(std::string(name) + ": dtype " + at::toString(t.scalar_type()) + " is not accepted");
+}
+
+// A contiguous CUDA tensor of one of the types (and, where given, of a shape).
+const Tensor& need(PyObject* o, Types types, const char* name) {
+  const Tensor& t = tensor(o, name);
+  check_type(t, types, name);
+  if (!t.is_contiguous()) fail(std::string(name) + " must be contiguous");
+  return t;
+}
+const Tensor& need(PyObject* o, Types types, const char* name, at::IntArrayRef shape) {
+  const Tensor& t = need(o, types, name);
+  if (t.sizes() != shape) fail(std::string(name) + " must be " + shape_text(shape));
+  return t;
+}
+
+// A 2-D CUDA tensor whose rows are contiguous, at any row stride of its width or
+// more; ld receives the stride.
+const Tensor& need_rows(PyObject* o, Types types, const char* name, int64_t& ld) {
+  const Tensor& t = tensor(o, name);
+  check_type(t, types, name);
+  if (t.dim() != 2) fail(std::string(name) + " must be 2-D");
+  ld = t.size(1);
+  if (t.is_contiguous()) return t;
+  if (t.size(0) > 1) ld = t.stride(0);
+  if ((t.size(1) > 1 && t.stride(1) != 1) || ld < t.size(1))
+    fail(std::string(name) + ": rows must be contiguous and not overlap");
+  return t;
+}
+const Tensor& need_rows(PyObject* o, Types types, const char* name, int64_t& ld, at::IntArrayRef shape) {
+  const Tensor& t = need_rows(o, types, name, ld);
+  if (t.sizes() != shape) fail(std::string(name) + " must be " + shape_text(shape));
+  return t;
+}
+
+constexpr ScalarType F32 = ScalarType::Float, BF16 = ScalarType::BFloat16, S8 = ScalarType::Char, U8 = ScalarType::Byte;
+#define FLOATS {F32, BF16}
+
+Tensor empty(at::IntArrayRef shape, ScalarType type, const Tensor& like) {
+  return Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
+}
+
+// `out` checked, or a new tensor where it is None.
+Tensor output(PyObject* out, at::IntArrayRef shape, ScalarType type, Types types, const char* name,
+              const Tensor& like) {
+  return out == Py_None ? empty(shape, type, like) : need(out, types, name, shape);
+}
+
+ScalarType float_type(PyObject* o) {
+  if (!THPDtype_Check(o)) fail("out_dtype must be a torch dtype");
+  const ScalarType t = reinterpret_cast<THPDtype*>(o)->scalar_type;
+  if (t != F32 && t != BF16) fail("out_dtype must be float32 or bfloat16");
+  return t;
+}
+
+void* stream(PyObject* o) {
+  if (o == Py_None) return c10::cuda::getCurrentCUDAStream().stream();
+  PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
+  if (!h) throw Error();
+  void* s = PyLong_AsVoidPtr(h);
+  Py_DECREF(h);
+  if (PyErr_Occurred()) throw Error();
+  return s;
+}
+
+int64_t integer(PyObject* o) {
+  const long long v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw Error();
+  return v;
+}
+
+void* ptr(const Tensor& t) { return t.data_ptr(); }
+
+PyObject* wrap(const Tensor& t) { return THPVariable_Wrap(t); }
+
+PyObject* pair(PyObject* a, PyObject* b) {
+  PyObject* r = PyTuple_New(2);
+  PyTuple_SET_ITEM(r, 0, a);
+  PyTuple_SET_ITEM(r, 1, b);
+  return r;
+}
+
+// A call of the C ABI without the interpreter lock (a launch waits where the
+// stream's queue is full).
+template <typename F>
+qmm_status unlocked(F f) {
+  qmm_status st;
+  Py_BEGIN_ALLOW_THREADS;
+  st = f();
+  Py_END_ALLOW_THREADS;
+  return st;
+}
+
+// x, weight, residual, eps, out, h_out, save_rstd, stream -> (q, scale, h, rstd)
+PyObject* rms_norm_s8(PyObject* const* a) {
+  int64_t ldx, ldr = 0;
+  const Tensor& x = need_rows(a[0], FLOATS, "x", ldx);
+  const auto shape = x.sizes();
+  const int64_t M = shape[0], H = shape[1];
+  const ScalarType t = x.scalar_type();
+  const Tensor& w = need(a[1], FLOATS, "weight", {H});
+  const bool res = a[2] != Py_None;
+  const double eps = PyFloat_AsDouble(a[3]);
+  if (PyErr_Occurred()) throw Error();
+  const Tensor q = output(a[4], shape, S8, {S8}, "out", x);
+  Tensor h = x;
+  const void* rp = nullptr;
+  if (res) {
+    rp = ptr(need_rows(a[2], {t}, "residual", ldr, shape));
+    h = output(a[5], shape, t, {t}, "h_out", x);
+  } else if (a[5] != Py_None) {
+    fail("h_out without a residual: h is x");
+  }
+  const bool save = PyObject_IsTrue(a[6]) == 1;
+  const Tensor scale = empty({M}, F32, x);
+  Tensor rstd;
+  if (save) rstd = empty({M}, F32, x);
+  void* s = stream(a[7]);
+  const qmm_status st = unlocked([&] {
+    return qmm_rms_norm_s8(ptr(x), qmm_type(t), M, H, ldx, rp, ldr, ptr(w), qmm_type(w.scalar_type()), (float)eps,
+                           res ? ptr(h) : nullptr, static_cast<int8_t*>(ptr(q)), static_cast<float*>(ptr(scale)),
+                           save ? static_cast<float*>(ptr(rstd)) : nullptr, s);
+  });
+  if (st != QMM_OK) return PyLong_FromLong(st);
+  PyObject* r = PyTuple_New(4);
+  PyTuple_SET_ITEM(r, 0, wrap(q));
+  PyTuple_SET_ITEM(r, 1, wrap(scale));
+  if (res) {
+    PyTuple_SET_ITEM(r, 2, wrap(h));
+  } else {
+    Py_INCREF(a[0]);
+    PyTuple_SET_ITEM(r, 2, a[0]);
+  }
+  if (save) {
+    PyTuple_SET_ITEM(r, 3, wrap(rstd));
+  } else {
+    Py_INCREF(Py_None);
+    PyTuple_SET_ITEM(r, 3, Py_None);
+  }
+  return r;
+}
+
+// q, scale, out, out_dtype, stream -> out
+PyObject* s8_dequantize_rows(PyObject* const* a) {
+  const Tensor& q = need(a[0], {S8}, "q");
+  if (q.dim() != 2) fail("q must be 2-D");
+  const int64_t M = q.size(0), H = q.size(1);
+  const Tensor& scale = need(a[1], {F32}, "scale", {M});
+  const Tensor y = output(a[2], q.sizes(), float_type(a[3]), FLOATS, "out", q);
+  void* s = stream(a[4]);
+  const qmm_status st = unlocked([&] {
+    return qmm_s8_dequantize_rows(static_cast<const int8_t*>(ptr(q)), static_cast<const float*>(ptr(scale)), M, H,
+                                  ptr(y), qmm_type(y.scalar_type()), s);
+  });
+  return st != QMM_OK ? PyLong_FromLong(st) : wrap(y);
+}
+
+// dy, h, weight, rstd, dh, out, dweight, stream, workspace -> (dx, dweight)
+PyObject* rms_norm_backward(PyObject* const* a) {
+  int64_t ldh, lddy, lddh = 0;
+  const Tensor& h = need_rows(a[1], FLOATS, "h", ldh);
+  const auto shape = h.sizes();
+  const int64_t M = shape[0], H = shape[1];
+  const ScalarType t = h.scalar_type();
+  const Tensor& dy = need_rows(a[0], {t}, "dy", lddy, shape);
+  const Tensor& w = need(a[2], FLOATS, "weight", {H});
+  const Tensor& rstd = need(a[3], {F32}, "rstd", {M});
+  const void* dh = a[4] == Py_None ? nullptr : ptr(need_rows(a[4], {t}, "dh", lddh, shape));
+  const Tensor dx = output(a[5], shape, t, {t}, "out", h);
+  const Tensor dw = output(a[6], {H}, F32, {F32}, "dweight", h);
+  const size_t bytes = qmm_rms_norm_backward_workspace_bytes(M, H);
+  Tensor ws;
+  size_t have = 0;
+  if (THPVariable_Check(a[8])) {
+    ws = tensor(a[8], "workspace");
+    if (!ws.is_cuda()) fail("workspace must be a CUDA tensor");
+    have = ws.nbytes();
+  } else if (bytes) {
+    if (!PyUnicode_Check(a[8]) || PyUnicode_CompareWithASCIIString(a[8], "auto") != 0)
+      fail("workspace must be 'auto' or a device tensor");
+    ws = empty({(int64_t)bytes}, U8, h);
+    have = bytes;
+  }
+  void* s = stream(a[7]);
+  const qmm_status st = unlocked([&] {
+    return qmm_rms_norm_backward(ptr(dy), lddy, ptr(h), ldh, dh, lddh, qmm_type(t), M, H, ptr(w),
+                                 qmm_type(w.scalar_type()), static_cast<const float*>(ptr(rstd)), ptr(dx),
+                                 static_cast<float*>(ptr(dw)), ws.defined() ? ptr(ws) : nullptr, have, s);
+  });
+  return st != QMM_OK ? PyLong_FromLong(st) : pair(wrap(dx), wrap(dw));
+}
+
+Tensor packed(PyObject* out, int64_t rows, int64_t cols, int block, const char* name, const Tensor& like) {
+  if (out != Py_None) return need(out, {U8}, name);
+  return empty({(int64_t)qmm_fp4_bytes(rows, cols, block)}, U8, like);
+}
+
+// x, block, transpose, out, stream -> buffer
+PyObject* fp4_quantize(PyObject* const* a) {
+  int64_t ld;
+  const Tensor& x = need_rows(a[0], FLOATS, "x", ld);
+  const int block = (int)integer(a[1]);
+  const int trans = PyObject_IsTrue(a[2]) == 1;
+  const int64_t rows = x.size(trans ? 1 : 0), cols = x.size(trans ? 0 : 1);
+  const Tensor b = packed(a[3], rows, cols, block, "out", x);
+  void* s = stream(a[4]);
+  const qmm_status st = unlocked([&] {
+    return qmm_fp4_quantize(ptr(x), qmm_type(x.scalar_type()), rows, cols, ld, trans, block, ptr(b), b.nbytes(), s);
+  });
+  return st != QMM_OK ? PyLong_FromLong(st) : wrap(b);
+}
+
+// x, block, out, out_t, stream -> (buffer, buffer of the transpose)
+PyObject* fp4_quantize_both(PyObject* const* a) {
+  int64_t ld;
+  const Tensor& x = need_rows(a[0], FLOATS, "x", ld);
+  const int block = (int)integer(a[1]);
+  const int64_t R = x.size(0), C = x.size(1);
+  const Tensor b = packed(a[2], R, C, block, "out", x), bt = packed(a[3], C, R, block, "out_t", x);
+  void* s = stream(a[4]);
+  const qmm_status st = unlocked([&] {
+    return qmm_fp4_quantize_both(ptr(x), qmm_type(x.scalar_type()), R, C, ld, block, ptr(b), b.nbytes(), ptr(bt),
+                                 bt.nbytes(), s);
+  });
+  return st != QMM_OK ? PyLong_FromLong(st) : pair(wrap(b), wrap(bt));
+}
+
+// buffer, rows, cols, block, out, out_dtype, stream -> out
+PyObject* fp4_dequantize(PyObject* const* a) {
+  const Tensor& b = need(a[0], {U8}, "m");
+  const int64_t rows = integer(a[1]), cols = integer(a[2]);
+  const int block = (int)integer(a[3]);
+  const Tensor y = output(a[4], {rows, cols}, float_type(a[5]), FLOATS, "out", b);
+  void* s = stream(a[6]);
+  const qmm_status st = unlocked(
+      [&] { return qmm_fp4_dequantize(ptr(b), b.nbytes(), rows, cols, block, ptr(y), qmm_type(y.scalar_type()), s); });
+  return st != QMM_OK ? PyLong_FromLong(st) : wrap(y);
+}
+
+// a, M, b, N, K, block, out, out_dtype, stream -> out
+PyObject* fp4_matmul(PyObject* const* a) {
+  const Tensor &A = need(a[0], {U8}, "a"), &B = need(a[2], {U8}, "b");
+  const int64_t M = integer(a[1]), N = integer(a[3]), K = integer(a[4]);
+  const int block = (int)integer(a[5]);
+  const Tensor y = output(a[6], {M, N}, float_type(a[7]), FLOATS, "out", A);
+  void* s = stream(a[8]);
+  const qmm_status st = unlocked([&] {
+    return qmm_fp4_matmul(ptr(A), A.nbytes(), M, ptr(B), B.nbytes(), N, K, block, ptr(y), qmm_type(y.scalar_type()),
+                          s);
+  });
+  return st != QMM_OK ? PyLong_FromLong(st) : wrap(y);
+}
+
+template <PyObject* (*F)(PyObject* const*), int N>
+PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != N) {
+    PyErr_Format(PyExc_TypeError, "%d arguments expected", N);
+    return nullptr;
+  }
+  try {
+    return F(args);
+  } catch (const Error&) {
+    return nullptr;
+  } catch (const std::exception& e) {   // an allocation that failed, for instance
+    torch::translate_exception_to_python(std::current_exception());
+    return nullptr;
+  }
+}
+
+#define ENTRY(f, n) \
+  { #f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<f, n>)), METH_FASTCALL, nullptr }
+PyMethodDef methods[] = {ENTRY(rms_norm_s8, 8),   ENTRY(s8_dequantize_rows, 5), ENTRY(rms_norm_backward, 9),
+                         ENTRY(fp4_quantize, 5),  ENTRY(fp4_quantize_both, 5),  ENTRY(fp4_dequantize, 7),
+                         ENTRY(fp4_matmul, 9),    {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "Argument marshalling of the C ABI.", -1, methods};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__binding(void) { return PyModule_Create(&module); }

@@ -301,7 +301,7 @@ struct NormArgs {
   void* h;                     // [M][H] of x's type: x + residual, or null (not stored)
   int8_t* q;                   // [M][H]
   float* scale;                // [M]
-  float* rstd;                 // [M]
+  float* rstd;                 // [M] or null (not stored)
   long long M, ldx, ldr;
   int H;
   float eps;

@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(1024) rms_norm_s8_kernel(const NormArgs p) {
     const RowScale s = row_scale(ss, am, n, p.eps);
     if (t == 0) {
       p.scale[m] = s.scale;
-      p.rstd[m] = s.rstd;
+      if (p.rstd) p.rstd[m] = s.rstd;
     }
 #pragma unroll
     for (int j = 0; j < K; ++j) put(j, v[j], s.inv, am >= kInfBits);
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(1024) rms_norm_s8_kernel(const NormArgs p) {
     const RowScale s = row_scale(ss, am, n, p.eps);
     if (t == 0) {
       p.scale[m] = s.scale;
-      p.rstd[m] = s.rstd;
+      if (p.rstd) p.rstd[m] = s.rstd;
     }
     for (int j = 0; j < steps; ++j) {
       // a stored h is read back (by the thread that wrote it: it may lie over x or the residual)

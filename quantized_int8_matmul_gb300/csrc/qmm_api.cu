@@ -1628,7 +1628,7 @@ qmm_status qmm_rms_norm_s8(const void* x, int x_dtype, int64_t M, int64_t H, int
     t_last_kernel = "none";
     return QMM_OK;
   }
-  if (!x || !w || !q || !scale || !rstd) return QMM_ERR_INVALID_ARG;
+  if (!x || !w || !q || !scale) return QMM_ERR_INVALID_ARG;
   if (h && ((h == x && ldx != H) || (h == residual && ldr != H))) return QMM_ERR_INVALID_ARG;
   cudaGetLastError();
   NormArgs a{};

@@ -11,6 +11,15 @@ ODD = ctypes.c_void_p(260)
 @pytest.fixture(scope="module")
 def qmm():
     import quantized_int8_matmul_gb300 as q
+    lib = q.lib()
+    i64, vp, ci, sz, cf = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
+    lib.qmm_rms_norm_s8.argtypes = [vp, ci, i64, i64, i64, vp, i64, vp, ci, cf, vp, vp, vp, vp, vp]
+    lib.qmm_s8_dequantize_rows.argtypes = [vp, vp, i64, i64, vp, ci, vp]
+    lib.qmm_rms_norm_backward.argtypes = [vp, i64, vp, i64, vp, i64, ci, i64, i64, vp, ci, vp, vp, vp, vp, sz, vp]
+    lib.qmm_fp4_quantize.argtypes = [vp, ci, i64, i64, i64, ci, ci, vp, sz, vp]
+    lib.qmm_fp4_quantize_both.argtypes = [vp, ci, i64, i64, i64, ci, vp, sz, vp, sz, vp]
+    lib.qmm_fp4_dequantize.argtypes = [vp, sz, i64, i64, ci, vp, ci, vp]
+    lib.qmm_fp4_matmul.argtypes = [vp, sz, i64, vp, sz, i64, i64, ci, vp, ci, vp]
     return q
 
 
@@ -22,7 +31,7 @@ def test_rms_norm_refusals(qmm):
         return lib.qmm_rms_norm_s8(x, xd, M, H, ldx, r, ldr, w, wd, eps, h, q, s, rs, None)
     for kw in (dict(xd=qmm.QMM_S8), dict(wd=qmm.QMM_S32), dict(M=-1), dict(H=2 ** 31), dict(ldx=63), dict(ldr=63),
                dict(eps=-1.0), dict(eps=float("nan")), dict(x=None), dict(w=None), dict(q=None), dict(s=None),
-               dict(rs=None), dict(h=P, x=P, ldx=65)):
+               dict(h=P, x=P, ldx=65)):
         assert call(**kw) == bad, kw
     assert call(M=0, x=None) == qmm.QMM_OK and call(H=0, ldx=0, ldr=0) == qmm.QMM_OK
     assert lib.qmm_s8_dequantize_rows(P, P, 4, 4, P, qmm.QMM_S8, None) == bad
