@@ -5,13 +5,19 @@
 // kind::mxf4nvf4, K = 64 an instruction, fp32 accumulation in tensor memory) and
 // the row scales of block 16 in the epilogue.
 //
-// Cluster of 2 CTAs per 256 x 256 tile of C, persistent over the tiles, 320
+// Tiles that do not fill a last round of all pairs are cut into pieces 128 or 64
+// columns wide where that gives every pair one (4096 x 4096 x 11008: 256 tiles on
+// 76 pairs are 3 rounds and 28 tiles, run as 56 pieces).
+//
+// Cluster of 2 CTAs per 256 x 256 tile of C, persistent over the tiles, 352
 // threads each:
-//  * warp 9: copies this CTA's 128 rows of A and 128 rows of B (256 columns of K
-//    a stage: 16 KB of codes each) and the scales of its rows of A and of all 256
-//    rows of B into a ring. The packed layout is the MMA's own, so every copy is
-//    one contiguous run; a tensor map describes it as a plain matrix only because
-//    tensor copies can complete on the even CTA's barrier.
+//  * warps 9 and 10: copy this CTA's 128 rows of A and 128 rows of B (256 columns
+//    of K a stage: 16 KB of codes each), the scales of its rows of A and those of
+//    all 256 rows of B into a ring, a warp for each operand: one warp issuing all
+//    five copies of a stage was late with them (4096 x 4096 x 11008, block 32:
+//    58.5 us with one, 53.2 with two). The packed layout is the MMA's own, so
+//    every copy is one contiguous run; a tensor map describes it as a plain matrix
+//    only because tensor copies can complete on the even CTA's barrier.
 //  * warp 8 of the even CTA: moves each 128 columns' scales to tensor memory
 //    (tcgen05.cp, both CTAs at once) and issues the pair MMAs.
 //  * warps 0-7: one row and 128 columns a thread; scale, round, stage 32 rows x
@@ -36,7 +42,7 @@ namespace gfp4 {
 namespace pair {
 
 constexpr int NEW = 8;
-constexpr int NT = NEW * 32 + 64;
+constexpr int NT = NEW * 32 + 96;   // + MMA warp + two producer warps
 constexpr int NS = 5;
 constexpr int STAGE_KT = 2;                       // 128-column tiles of K a stage
 constexpr int CODE_BYTES = STAGE_KT * 8192;       // one operand's codes a stage and CTA
@@ -55,16 +61,67 @@ struct Shared {
   float gb[NEW][64];      // per epilogue warp, the column scales of the 64 columns it works on (block 16)
 };
 
+// The tiles of a launch: `full` of them 256 columns wide, dealt out in turn, then
+// the rest in pieces of 256 / cut columns, one to a cluster.
+constexpr int kBand = 8;
+struct Sched {
+  int full, cut, pieces, m_tiles;
+};
+struct Work {
+  int mt, nt;    // tile
+  int piece;     // of the tile's columns (0 for a whole tile)
+  int width;     // columns: 256, 128 or 64
+};
+__device__ __forceinline__ int work_count(const Sched& sc, int cid, int ncl) {
+  return (cid < sc.full ? (sc.full - cid + ncl - 1) / ncl : 0) + (cid < sc.pieces ? 1 : 0);
+}
+__device__ __forceinline__ Work work_at(const Sched& sc, int i, int cid, int ncl, int n_tiles) {
+  Work w;
+  int tile = cid + i * ncl;
+  w.piece = 0;
+  w.width = 256;
+  if (tile >= sc.full) {
+    tile = sc.full + cid / sc.cut;
+    w.piece = cid - cid / sc.cut * sc.cut;
+    w.width = 256 / sc.cut;
+  }
+  // bands of kBand rows of tiles, down the columns of a band
+  const int band = tile / (kBand * n_tiles), in = tile - band * kBand * n_tiles;
+  const int rows = min(kBand, sc.m_tiles - band * kBand);
+  w.nt = in / rows;
+  w.mt = band * kBand + in - w.nt * rows;
+  return w;
+}
+
 enum : unsigned {
   SITE_EMPTY = 0x510, SITE_FULL = 0x511, SITE_ACC_FULL = 0x512, SITE_ACC_FREE = 0x513, SITE_TEARDOWN = 0x514,
   SITE_FINAL = 0x515
 };
 
-__device__ __forceinline__ void load_pair(uint32_t dst, const void* tmap, int row, uint32_t bar) {
+// Tensor copies that complete on the even CTA's barrier, issued by the lane whose
+// `on` is set (the producer warps run converged, as the issuer does).
+__device__ __forceinline__ void load_pair(uint32_t dst, const void* tmap, int row, uint32_t bar, uint32_t on) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-      "[%4];" ::"r"(dst),
-      "l"(tmap), "r"(0), "r"(row), "r"(bar)
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+      "@e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3}], [%4];\n\t}" ::"r"(dst),
+      "l"(tmap), "r"(0), "r"(row), "r"(bar), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void load_pair_3d(uint32_t dst, const void* tmap, int chunk, int part, uint32_t bar,
+                                             uint32_t on) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %6, 0;\n\t"
+      "@e cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3, %4}], [%5];\n\t}" ::"r"(dst),
+      "l"(tmap), "r"(0), "r"(chunk), "r"(part), "r"(bar), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void expect_on(uint64_t* bar, uint32_t bytes, uint32_t on) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %2, 0;\n\t"
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+      "r"(bytes), "r"(on)
       : "memory");
 }
 
@@ -77,10 +134,65 @@ struct Cfg {
 };
 static_assert(Cfg<16>::SMEM <= 232448, "shared memory per CTA");
 
+// The issuing warp's place in the ring of stages and scale buffers.
+struct Issuer {
+  uint32_t s16, tb, on;   // ring base / 16, tensor memory base, this lane issues
+  int slot;
+  uint32_t phase, buf;
+
+  // All of K for one tile (WIDTH 256) or piece; odd: tensor memory columns by
+  // which a piece's scales of B start after their atom (an odd piece of 64 columns
+  // is the second half of its 128 rows). False if a wait ran out.
+  template <int BLOCK, int WIDTH>
+  __device__ __forceinline__ bool tile(Shared& sm, unsigned* err, int kt, uint32_t tacc, uint32_t odd) {
+    using C = Cfg<BLOCK>;
+    constexpr int ATOMS = C::ATOMS;
+    constexpr uint32_t id0 = idesc_fp4(256, WIDTH, BLOCK == 32, 0), id1 = idesc_fp4(256, WIDTH, BLOCK == 32, 2);
+    constexpr uint32_t b_ch = WIDTH / 2;              // a CTA's rows of B: a chunk's bytes / 16
+    constexpr uint32_t b_lo = b_ch << 16;
+    constexpr uint32_t sb_at = WIDTH == 256 ? 8 : 4;  // tensor memory columns of B's scales an atom
+    uint32_t acc = 0u;
+    for (int left = kt; left > 0; left -= STAGE_KT) {
+      const bool ok = mbar_wait_cluster(&sm.full[slot], phase, &sm.abort_flag, err, SITE_FULL);
+      if (!__all_sync(0xffffffffu, ok)) return false;
+      tc_fence_after();
+      const uint32_t a = s16 + (uint32_t)slot * (C::STAGE >> 4), b = a + (CODE_BYTES >> 4);
+      const uint32_t fa = b + (CODE_BYTES >> 4), fb = fa + (C::SF_BYTES >> 4);
+#pragma unroll
+      for (int k = 0; k < STAGE_KT; ++k) {
+        if (k > 0 && left == 1) break;
+        const uint32_t sa = tb + SF_COL + buf, sb = sa + 8u;
+        buf ^= 24u;
+#pragma unroll
+        for (int i = 0; i < ATOMS; ++i) {
+          cp_scales_pair(sa + i * 4, fa + (k * ATOMS + i) * 32, on);
+          cp_scales_pair(sb + i * sb_at, fb + (k * ATOMS + i) * 32, on);
+          if (WIDTH == 256) cp_scales_pair(sb + i * 8 + 4, fb + (C::SF_BYTES >> 4) + (k * ATOMS + i) * 32, on);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {   // 64 columns of K each
+          mma_fp4_pair<BLOCK>(tacc, a + (uint32_t)(k * 512 + j * 256) + kDescLo,
+                              b + (uint32_t)(k * 4 + j * 2) * b_ch + b_lo, (BLOCK == 32 && j) ? id1 : id0,
+                              sa + (BLOCK == 16 ? j * 4 : 0),
+                              sb + (BLOCK == 16 ? j * sb_at : 0u) + (WIDTH == 64 ? odd : 0u), acc, on);
+          acc = 1u;
+        }
+      }
+      commit_pair_on(&sm.empty[slot], on);
+      if (++slot == NS) {
+        slot = 0;
+        phase ^= 1u;
+      }
+    }
+    return true;
+  }
+};
+
 template <int BLOCK>
 __global__ void __launch_bounds__(NT, 1)
-    gemm_fp4_pair_kernel(const GemmFp4Args p, const int tma_c, const __grid_constant__ CUtensorMap tmA,
-                         const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmSA,
+    gemm_fp4_pair_kernel(const GemmFp4Args p, const int tma_c, const Sched sc, const __grid_constant__ CUtensorMap tmA,
+                         const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmBP,
+                         const __grid_constant__ CUtensorMap tmSA,
                          const __grid_constant__ CUtensorMap tmSB, const __grid_constant__ CUtensorMap tmC) {
   using C = Cfg<BLOCK>;
   constexpr int ATOMS = C::ATOMS;
@@ -93,10 +205,9 @@ __global__ void __launch_bounds__(NT, 1)
   const uint32_t rank = cluster_ctarank();
   const int cid = (int)cluster_id_x(), ncl = (int)nclusters_x();
   const Fp4Layout LA(p.M, p.K, BLOCK), LB(p.N, p.K, BLOCK);
-  const int m_tiles = (int)((p.M + 255) / 256), n_tiles = (int)((p.N + 255) / 256);
-  const int tiles = m_tiles * n_tiles;
-  const int my_tiles = cid < tiles ? (tiles - cid + ncl - 1) / ncl : 0;
-  const int kt = (int)LA.kt, spt = (kt + STAGE_KT - 1) / STAGE_KT;
+  const int n_tiles = (int)((p.N + 255) / 256);
+  const int my_tiles = work_count(sc, cid, ncl);
+  const int kt = (int)LA.kt;
 
   if (t == 0) {
     for (int i = 0; i < NS; ++i) {
@@ -122,14 +233,13 @@ __global__ void __launch_bounds__(NT, 1)
   if (warp == NEW) {
     // ---------------- pair MMA issuer (even CTA, the warp converged) ----------------
     if (rank == 0) {
-      constexpr uint32_t id0 = idesc_fp4(256, 256, BLOCK == 32, 0), id1 = idesc_fp4(256, 256, BLOCK == 32, 2);
       const uint32_t on = elect_one();
       const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
-      const uint32_t s16 = desc_addr(sbase);
-      int slot = 0;
-      uint32_t phase = 0u, buf = 0u;
+      Issuer ring{desc_addr(sbase), tb, on, 0, 0u, 0u};
+      // broadcast from one lane, so that the compiler sees the warp's control flow is uniform
+      const int cid_u = __shfl_sync(0xffffffffu, cid, 0), tiles_u = __shfl_sync(0xffffffffu, my_tiles, 0);
       bool ok = true;
-      for (int tl = 0; tl < my_tiles && ok; ++tl) {
+      for (int tl = 0; tl < tiles_u && ok; ++tl) {
         // the columns shared with the previous tile's accumulator are drained, and
         // with them (the epilogue works in order) all of this one's last tile
         if (tl > 0) {
@@ -139,83 +249,77 @@ __global__ void __launch_bounds__(NT, 1)
         }
         tc_fence_after();
         const uint32_t tacc = tb + ((tl & 1) ? ACC1 : 0u);
-        uint32_t acc = 0u;
-        for (int s = 0; s < spt; ++s) {
-          ok = mbar_wait_cluster(&sm.full[slot], phase, &sm.abort_flag, p.err, SITE_FULL);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t a = s16 + (uint32_t)slot * (C::STAGE >> 4), b = a + (CODE_BYTES >> 4);
-          const uint32_t fa = b + (CODE_BYTES >> 4), fb = fa + (C::SF_BYTES >> 4);
-#pragma unroll
-          for (int k = 0; k < STAGE_KT; ++k) {
-            if (k > 0 && s * STAGE_KT + k >= kt) break;
-            const uint32_t sa = tb + SF_COL + buf, sb = sa + 8u;
-            buf ^= 24u;
-#pragma unroll
-            for (int i = 0; i < ATOMS; ++i) {
-              cp_scales_pair(sa + i * 4, fa + (k * ATOMS + i) * 32, on);
-              cp_scales_pair(sb + i * 8, fb + (k * ATOMS + i) * 32, on);
-              cp_scales_pair(sb + i * 8 + 4, fb + (C::SF_BYTES >> 4) + (k * ATOMS + i) * 32, on);
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {   // 64 columns of K each
-              const uint32_t off = (uint32_t)(k * 512 + j * 256) + kDescLo;
-              mma_fp4_pair<BLOCK>(tacc, a + off, b + off, (BLOCK == 32 && j) ? id1 : id0,
-                                  sa + (BLOCK == 16 ? j * 4 : 0), sb + (BLOCK == 16 ? j * 8 : 0), acc, on);
-              acc = 1u;
-            }
-          }
-          commit_pair_on(&sm.empty[slot], on);
-          if (++slot == NS) {
-            slot = 0;
-            phase ^= 1u;
-          }
-        }
+        const Work wk = work_at(sc, tl, cid_u, ncl, n_tiles);
+        const int width = __shfl_sync(0xffffffffu, wk.width, 0);
+        const uint32_t odd = __shfl_sync(0xffffffffu, wk.piece & 1, 0) ? 2u : 0u;
+        if (width == 256) ok = ring.template tile<BLOCK, 256>(sm, p.err, kt, tacc, odd);
+        else if (width == 128) ok = ring.template tile<BLOCK, 128>(sm, p.err, kt, tacc, odd);
+        else ok = ring.template tile<BLOCK, 64>(sm, p.err, kt, tacc, odd);
         if (!ok) break;
         commit_pair_on(&sm.acc_full[tl & 1], on);
       }
     }
     __syncwarp();
-  } else if (warp == NEW + 1) {
-    // ---------------- producer (both CTAs) ----------------
-    if (lane == 0) {
-      prefetch_tmap(&tmA);
-      prefetch_tmap(&tmB);
-      prefetch_tmap(&tmSA);
-      prefetch_tmap(&tmSB);
-      const uint32_t full0 = mapa_shared(smem_u32(&sm.full[0]), 0);
-      int g = 0;
-      bool ok = true;
-      for (int tl = 0; tl < my_tiles && ok; ++tl) {
-        const int tile = cid + tl * ncl, mt = tile / n_tiles, nt = tile - mt * n_tiles;
-        // row tiles of this CTA (past the matrix: the last one again; its results are not stored)
-        const int ra = min(2 * mt + (int)rank, (int)LA.rt - 1), rb = min(2 * nt + (int)rank, (int)LB.rt - 1);
-        const int rb0 = 2 * nt, rb1 = min(2 * nt + 1, (int)LB.rt - 1);
-        for (int s = 0; s < spt; ++s, ++g) {
-          const int slot = g % NS;
-          if (g >= NS &&
-              !mbar_wait(&sm.empty[slot], (uint32_t)((g / NS - 1) & 1), &sm.abort_flag, p.err, SITE_EMPTY)) {
-            ok = false;
-            break;
-          }
-          const uint32_t bar = full0 + (uint32_t)slot * 8u;
-          if (rank == 0) mbar_arrive_expect_tx(&sm.full[slot], 2u * C::STAGE);
-          const uint32_t dst = sbase + (uint32_t)slot * C::STAGE;
-          // a stage that reaches past its row tile copies bytes that no MMA reads
-          load_pair(dst, &tmA, (ra * kt + s * STAGE_KT) * 8, bar);
-          load_pair(dst + CODE_BYTES, &tmB, (rb * kt + s * STAGE_KT) * 8, bar);
-          load_pair(dst + 2 * CODE_BYTES, &tmSA, (ra * kt + s * STAGE_KT) * ATOMS, bar);
-          load_pair(dst + 2 * CODE_BYTES + C::SF_BYTES, &tmSB, (rb0 * kt + s * STAGE_KT) * ATOMS, bar);
-          load_pair(dst + 2 * CODE_BYTES + 2 * C::SF_BYTES, &tmSB, (rb1 * kt + s * STAGE_KT) * ATOMS, bar);
+  } else if (warp > NEW) {
+    // ---------------- producers (both CTAs): warp 9 A, warp 10 B ----------------
+    const bool is_a = warp == NEW + 1;
+    const uint32_t on = elect_one();
+    if (on) {
+      prefetch_tmap(is_a ? &tmA : &tmB);
+      prefetch_tmap(is_a ? &tmSA : &tmSB);
+      if (!is_a && sc.cut > 1) prefetch_tmap(&tmBP);
+    }
+    const uint32_t full0 = mapa_shared(smem_u32(&sm.full[0]), 0);
+    const int cid_u = __shfl_sync(0xffffffffu, cid, 0), tiles_u = __shfl_sync(0xffffffffu, my_tiles, 0);
+    const int rank_u = __shfl_sync(0xffffffffu, (int)rank, 0);
+    const uint32_t expect = rank_u == 0 && is_a ? on : 0u;
+    int g = 0, slot = 0;
+    uint32_t phase = 1u;   // a fresh slot is empty: the first round's waits pass
+    bool ok = true;
+    for (int tl = 0; tl < tiles_u && ok; ++tl) {
+      const Work wk = work_at(sc, tl, cid_u, ncl, n_tiles);
+      const int width = __shfl_sync(0xffffffffu, wk.width, 0);
+      const bool whole = width == 256;
+      // row tiles of this CTA (past the matrix: the last one again; its results are not stored)
+      const int last = (int)LB.rt - 1;
+      const int ra = min(2 * wk.mt + rank_u, (int)LA.rt - 1), rb = min(2 * wk.nt + rank_u, last);
+      // B's scales: both row tiles of a whole tile, a piece's one
+      const int rb0 = min(2 * wk.nt + (width == 64 ? wk.piece >> 1 : wk.piece), last);
+      const int rb1 = min(2 * wk.nt + 1, last);
+      // a piece's part of its row tile: the CTAs' halves of it
+      const int part = width == 128 ? rank_u : 2 * (wk.piece & 1) + rank_u;
+      const uint32_t bytes =
+          2u * (whole ? (uint32_t)C::STAGE : (uint32_t)(CODE_BYTES + width * 64 + 2 * C::SF_BYTES));
+      const int r0 = is_a ? ra * kt : rb * kt, f0 = is_a ? ra * kt : rb0 * kt, f1 = rb1 * kt;
+      for (int s = 0; s < kt; s += STAGE_KT, ++g) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.empty[slot], phase, &sm.abort_flag, p.err, SITE_EMPTY));
+        if (!ok) break;
+        const uint32_t bar = full0 + (uint32_t)slot * 8u;
+        const uint32_t dst = sbase + (uint32_t)slot * C::STAGE, sf = dst + 2 * CODE_BYTES;
+        expect_on(&sm.full[slot], bytes, expect);
+        // a stage that reaches past its row tile copies bytes that no MMA reads
+        if (is_a) {
+          load_pair(dst, &tmA, (r0 + s) * 8, bar, on);
+          load_pair(sf, &tmSA, (f0 + s) * ATOMS, bar, on);
+        } else if (whole) {
+          load_pair(dst + CODE_BYTES, &tmB, (r0 + s) * 8, bar, on);
+          load_pair(sf + C::SF_BYTES, &tmSB, (f0 + s) * ATOMS, bar, on);
+          load_pair(sf + 2 * C::SF_BYTES, &tmSB, (f1 + s) * ATOMS, bar, on);
+        } else {
+          load_pair_3d(dst + CODE_BYTES, &tmBP, (f0 + s) * 4, part, bar, on);
+          load_pair(sf + C::SF_BYTES, &tmSB, (f0 + s) * ATOMS, bar, on);
+        }
+        if (++slot == NS) {
+          slot = 0;
+          phase ^= 1u;
         }
       }
-      // the even CTA's barriers count both CTAs' bytes: once the last stages'
-      // phases complete, no copy of either CTA is in flight
-      if (rank == 0)
-        for (int j = (g > NS ? g - NS : 0); j < g; ++j)
-          mbar_wait_cluster(&sm.full[j % NS], (uint32_t)((j / NS) & 1), nullptr, p.err, SITE_FINAL);
     }
+    // the even CTA's barriers count both CTAs' bytes: once the last stages'
+    // phases complete, no copy of either CTA is in flight
+    if (rank == 0 && is_a)
+      for (int j = (g > NS ? g - NS : 0); j < g; ++j)
+        mbar_wait_cluster(&sm.full[j % NS], (uint32_t)((j / NS) & 1), nullptr, p.err, SITE_FINAL);
     __syncwarp();
   } else {
     // ---------------- epilogue ----------------
@@ -225,9 +329,12 @@ __global__ void __launch_bounds__(NT, 1)
     const float* rows_a = reinterpret_cast<const float*>(p.A + LA.row_off());
     const float* rows_b = reinterpret_cast<const float*>(p.B + LB.row_off());
     for (int tl = 0; tl < my_tiles; ++tl) {
-      const int tile = cid + tl * ncl, mt = tile / n_tiles, nt = tile - mt * n_tiles;
-      const long long row0 = (long long)mt * 256 + rank * 128 + q * 32;
-      const long long col0 = (long long)nt * 256 + h * 128;
+      const Work wk = work_at(sc, tl, cid, ncl, n_tiles);
+      const long long row0 = (long long)wk.mt * 256 + rank * 128 + q * 32;
+      // this warp's columns: half of a whole tile's or of 128; all 64 of the narrowest
+      const int hc = wk.width == 256 ? 128 : 64;
+      const long long col0 = (long long)wk.nt * 256 + wk.piece * wk.width + h * hc;
+      const int units = wk.width == 256 ? 2 : (wk.width == 128 || h == 0) ? 1 : 0;
       float ga = 1.f, gb[4] = {};   // this lane's row scale; column scales lane, lane + 32, ...
       if (BLOCK == 16) {
         if (row0 + lane < p.M) ga = __ldg(rows_a + row0 + lane);
@@ -238,16 +345,16 @@ __global__ void __launch_bounds__(NT, 1)
       if (!mbar_wait_cluster(&sm.acc_full[tl & 1], (uint32_t)((tl >> 1) & 1), &sm.abort_flag, p.err, SITE_ACC_FULL))
         break;
       tc_fence_after();
-      const uint32_t tacc = tbase + ((uint32_t)(q * 32) << 16) + ((tl & 1) ? ACC1 : 0u) + (uint32_t)(h * 128);
+      const uint32_t tacc = tbase + ((uint32_t)(q * 32) << 16) + ((tl & 1) ? ACC1 : 0u) + (uint32_t)(h * hc);
       // even tiles share columns 192..255 with the next accumulator, odd ones 0..63
-      const int first = (tl & 1) ? 0 : 1;
-      const bool shares = h == ((tl & 1) ? 0 : 1);
+      const int first = (tl & 1) || units < 2 ? 0 : 1;
+      const bool shares = units == 2 && h == ((tl & 1) ? 0 : 1);   // (a piece is the last of its cluster)
       if (!shares) {
         __syncwarp();
         if (lane == 0) mbar_arrive_remote_cta(free0);
       }
 #pragma unroll 1
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < units; ++u) {
         const int unit = u ^ first;   // 64 columns
         uint32_t acc[2][32];
         tmem_ld32x2(tacc + unit * 64, acc[0], tacc + unit * 64 + 32, acc[1]);
@@ -327,7 +434,7 @@ cudaError_t launch(const GemmFp4Args& a, cudaStream_t s) {
     clusters = max_clusters[dev];
   }
   const Fp4Layout LA(a.M, a.K, BLOCK), LB(a.N, a.K, BLOCK);
-  CUtensorMap ta{}, tb{}, tsa{}, tsb{}, tc{};
+  CUtensorMap ta{}, tb{}, tbp{}, tsa{}, tsb{}, tc{};
   // codes as rows of 1 KB (8 to a 128 x 128 tile), scales as rows of one atom
   auto codes = [](CUtensorMap* m, const uint8_t* base, const Fp4Layout& L) {
     return make_tmap_2d(m, base, CU_TENSOR_MAP_DATA_TYPE_INT32, 256, L.code_bytes() / 1024, 1024, 256, STAGE_KT * 8,
@@ -344,9 +451,21 @@ cudaError_t launch(const GemmFp4Args& a, cudaStream_t s) {
   int tma_c = 0;
   if (e == cudaSuccess) e = make_c_map(a, &tc, &tma_c);
   if (e != cudaSuccess) return e;
-  const long long tiles = ((a.M + 255) / 256) * ((a.N + 255) / 256);
-  cfg.gridDim = dim3(2 * (unsigned)std::min<long long>(tiles, clusters), 1, 1);
-  e = cudaLaunchKernelEx(&cfg, kern, a, tma_c, ta, tb, tsa, tsb, tc);
+  const int tiles = (int)(((a.M + 255) / 256) * ((a.N + 255) / 256));
+  Sched sc{tiles, 1, 0, (int)((a.M + 255) / 256)};
+  const int rest = tiles % clusters;
+  if (rest > 0 && 2 * rest <= clusters) {
+    sc.cut = 4 * rest <= clusters ? 4 : 2;
+    sc.full = tiles - rest;
+    sc.pieces = rest * sc.cut;
+    // B's codes by chunk (32 columns) and part of its 128 rows
+    const uint32_t part = 512u / sc.cut;   // 32-bit words: 128 / cut rows of 16 bytes, half of a piece's
+    e = make_tmap_3d(&tbp, a.B, CU_TENSOR_MAP_DATA_TYPE_INT32, part, LB.code_bytes() / 2048, sc.cut, 2048, part * 4,
+                     part, STAGE_KT * 4, CU_TENSOR_MAP_SWIZZLE_NONE);
+  }
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(2 * (unsigned)std::min(std::max(tiles, sc.pieces), clusters), 1, 1);
+  e = cudaLaunchKernelEx(&cfg, kern, a, tma_c, sc, ta, tb, tbp, tsa, tsb, tc);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

@@ -525,23 +525,29 @@ __global__ void __launch_bounds__(1024)
 }
 
 // out[i] = the sum of column i of part [count][n], in a fixed order: 32 columns
-// a CTA, 16 interleaved runs of rows, then the runs.
-__global__ void __launch_bounds__(512) sum_partials_kernel(const float* part, int count, int n, float* out) {
-  __shared__ float s[16][32];
+// a CTA, 32 interleaved runs of rows (eight loads of each in flight), then the
+// runs.
+__global__ void __launch_bounds__(1024) sum_partials_kernel(const float* part, int count, int n, float* out) {
+  __shared__ float s[32][33];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int i = blockIdx.x * 32 + threadIdx.x;
   float a = 0.f;
   if (i < n) {
-#pragma unroll 4
-    for (int c = threadIdx.y; c < count; c += 16) a += part[(long long)c * n + i];
+    for (int c = threadIdx.y; c < count; c += 32 * 8) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = c + 32 * k < count ? part[(long long)(c + 32 * k) * n + i] : 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) a += v[k];
+    }
   }
   s[threadIdx.y][threadIdx.x] = a;
   __syncthreads();
-  if (threadIdx.y == 0 && i < n) {
+  a = s[threadIdx.x][threadIdx.y];   // one column a warp
 #pragma unroll
-    for (int y = 1; y < 16; ++y) a += s[y][threadIdx.x];
-    out[i] = a;
-  }
+  for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  const int c = blockIdx.x * 32 + threadIdx.y;
+  if (threadIdx.x == 0 && c < n) out[c] = a;
 }
 
 template <typename T>
@@ -650,7 +656,7 @@ cudaError_t launch_backward(const NormBwdArgs& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((a.H + 31) / 32));
-  cfg.blockDim = dim3(32, 16);
+  cfg.blockDim = dim3(32, 32);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
