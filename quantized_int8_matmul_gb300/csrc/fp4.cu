@@ -178,6 +178,14 @@ struct Raw16 {
   }
 };
 
+// A warp step's elements in shared memory, filled by neighbouring lanes from
+// neighbouring columns; 16 bytes a row more keep the rows off each other's banks.
+template <typename T, int ROWS, int COLS>
+struct RowStage {
+  static constexpr int PITCH = COLS + 16 / (int)sizeof(T);
+  static constexpr int BYTES = ROWS * PITCH * (int)sizeof(T);
+};
+
 // ---------------------------------------------------------------------------
 // Along the rows. A CTA takes the rows {2c, 2c + 1} + {0, 32, 64, 96} of a tile
 // (J = 4: a warp step is 64 columns of eight rows, 16 columns a lane) or, for
@@ -188,14 +196,18 @@ struct Raw16 {
 // together; with block 16 a row whose steps are one batch stays in registers
 // between its maximum and its codes, longer rows are read again.
 // ---------------------------------------------------------------------------
-template <typename T, int BLOCK, int J, int ITER>
-__global__ void __launch_bounds__(1024) quantize_rows_kernel(const Fp4QuantArgs p, const int staged) {
+template <typename T, int BLOCK, int J, int ITER, bool VEC>
+__global__ void __launch_bounds__(VEC ? 1024 : 384) quantize_rows_kernel(const Fp4QuantArgs p, const int staged) {
+  constexpr int WROWS = J == 4 ? 8 : 2, WCOLS = J == 4 ? 64 : 256;   // a warp step
   constexpr int ATOMS = BLOCK == 16 ? 2 : 1;
   constexpr int SPC = 32 / BLOCK;      // scales per 32-column chunk
   constexpr int LANES = J == 4 ? 4 : 16;   // lanes a row
   constexpr int UC = LANES / 2;        // chunks a warp step
   __shared__ unsigned rowmax[8];
-  extern __shared__ __align__(16) uint8_t sfs[];   // [atom][2 rows][4 rows 32 apart][4] (staged)
+  // rows that no vector load can take: a buffer a warp; then the scales (staged),
+  // [atom][2 rows][4 rows 32 apart][4]
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint8_t* sfs = smem + (VEC ? 0 : (blockDim.x >> 5) * RowStage<T, WROWS, WCOLS>::BYTES);
   const Fp4Layout L(p.rows, p.cols, BLOCK);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const int tile = blockIdx.x >> 4, c2 = 2 * (blockIdx.x & 15);
@@ -207,14 +219,31 @@ __global__ void __launch_bounds__(1024) quantize_rows_kernel(const Fp4QuantArgs 
   const bool rv = row < p.rows;
   const T* x = static_cast<const T*>(p.x) + (rv ? row : 0) * p.ld;
   const int n = rv ? (int)p.cols : 0;
-  const bool vec = p.vec;
   const int chunks = (int)L.kt * 4, units = (chunks + UC - 1) / UC;
   const int batches = (units + nw * ITER - 1) / (nw * ITER);
   Raw16<T> v[ITER];
   auto load = [&](int b) {
 #pragma unroll
-    for (int i = 0; i < ITER; ++i)   // past the end: columns past n, zeros
-      v[i].load(x, (long long)((b * ITER + i) * nw + warp) * (32 * UC) + piece * 16, n, vec);
+    for (int i = 0; i < ITER; ++i) {   // past the end: columns past n, zeros
+      const long long k0 = (long long)((b * ITER + i) * nw + warp) * WCOLS;
+      if (VEC) {
+        v[i].load(x, k0 + piece * 16, n, true);
+      } else {
+        using S = RowStage<T, WROWS, WCOLS>;
+        T* buf = reinterpret_cast<T*>(smem + warp * S::BYTES);
+        __syncwarp();
+#pragma unroll
+        for (int r = 0; r < WROWS; ++r) {
+          const long long rr = (long long)tile * 128 + c2 + (r & 1) + 32 * (r >> 1);
+          const T* xr = static_cast<const T*>(p.x) + (rr < p.rows ? rr : 0) * p.ld;
+#pragma unroll
+          for (int c = lane; c < WCOLS; c += 32)
+            buf[r * S::PITCH + c] = rr < p.rows && k0 + c < p.cols ? xr[k0 + c] : (T)0.f;
+        }
+        __syncwarp();
+        v[i] = *reinterpret_cast<const Raw16<T>*>(buf + (J == 4 ? rj * 2 + ra : ra) * S::PITCH + piece * 16);
+      }
+    }
   };
   float u = 1.f;
   if (BLOCK == 16) {
@@ -302,21 +331,33 @@ __global__ void __launch_bounds__(256) absmax_kernel(const Fp4QuantArgs p, unsig
     for (int e = 0; e < 8; ++e) atomicMax(&cm[lane * 8 + e], m[e]);
   } else {   // rows that no vector load can take: neighbouring lanes, neighbouring columns
     unsigned m[8] = {};
-    for (int i = 0; i < 8; ++i) {
-      const long long r = r0 + 8 * i;
-      if (r >= p.rows) break;
-      unsigned rm = 0u;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const long long k = c + e * 32 + lane;
-        const unsigned b =
-            k < p.cols ? __float_as_uint(ld1(static_cast<const T*>(p.x) + r * p.ld + k)) & 0x7fffffffu : 0u;
-        m[e] = max(m[e], b);
-        rm = max(rm, b);
+    for (int h = 0; h < 2; ++h) {   // four rows' loads together
+      T v[4][8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const long long r = r0 + 8 * (4 * h + i);
+        const T* x = static_cast<const T*>(p.x) + (r < p.rows ? r : 0) * p.ld;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const long long k = c + e * 32 + lane;
+          v[i][e] = r < p.rows && k < p.cols ? x[k] : (T)0.f;
+        }
       }
-      if (rowmax) {
-        rm = __reduce_max_sync(0xffffffffu, rm);
-        if (lane == 0) atomicMax(rowmax + r, rm);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const long long r = r0 + 8 * (4 * h + i);
+        unsigned rm = 0u;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const unsigned b = __float_as_uint((float)v[i][e]) & 0x7fffffffu;
+          m[e] = max(m[e], b);
+          rm = max(rm, b);
+        }
+        if (rowmax) {
+          rm = __reduce_max_sync(0xffffffffu, rm);
+          if (lane == 0 && r < p.rows) atomicMax(rowmax + r, rm);
+        }
       }
     }
 #pragma unroll
@@ -328,7 +369,10 @@ __global__ void __launch_bounds__(256) absmax_kernel(const Fp4QuantArgs p, unsig
 
 // One tile of 128 x 128 of x a CTA: its rows are quantised as they are loaded
 // (ROWS), all of it goes to shared memory, and its columns are quantised from
-// there. Codes and scales leave as whole tiles by bulk copies.
+// there. Codes and scales leave as whole tiles by bulk copies. CLUSTER (block 16,
+// x of up to 8 tiles down): the tiles above each other are one cluster, and the
+// columns' maxima are taken over it -- one launch in place of a fill, a pass for
+// the maxima and this.
 template <typename T>
 struct TileSmem {
   static constexpr int PITCH = 128 * (int)sizeof(T) + 16;   // bytes; 16 more keep row accesses off each other's banks
@@ -337,7 +381,7 @@ struct TileSmem {
   static constexpr int BYTES = SCALES + 2 * 1024;
 };
 
-template <typename T, int BLOCK, bool ROWS>
+template <typename T, int BLOCK, bool ROWS, bool CLUSTER>
 __global__ void __launch_bounds__(256) quantize_tile_kernel(const Fp4QuantArgs p) {
   using S = TileSmem<T>;
   constexpr int ATOMS = BLOCK == 16 ? 2 : 1;
@@ -350,24 +394,43 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const Fp4QuantArgs p
   uint8_t* sf_r = sf_c + 1024;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const Fp4Layout Lr(p.rows, p.cols, BLOCK), Lc(p.cols, p.rows, BLOCK);
-  const int ty = blockIdx.x / (int)Lr.kt, tx = blockIdx.x - ty * (int)Lr.kt;
+  const int across = CLUSTER ? (int)Lr.rt : (int)Lr.kt;
+  const int b1 = blockIdx.x / across, b0 = blockIdx.x - b1 * across;
+  const int ty = CLUSTER ? b0 : b1, tx = CLUSTER ? b1 : b0;
   const long long c0 = (long long)tx * 128, r0 = (long long)ty * 128;
-  const size_t ti = blockIdx.x;                       // this tile in the packed rows
+  const size_t ti = (size_t)ty * Lr.kt + tx;          // this tile in the packed rows
   const size_t tc = (size_t)tx * Lc.kt + ty;          // and in the packed columns
   // a warp step: 8 rows x 64 columns; warp w takes rows 8w .. 8w + 7 of each 64
   Raw16<T> v[4];
   const int half = lane & 1;
+  if (!p.vec) {   // neighbouring lanes, neighbouring columns, into shared memory first
+#pragma unroll 4
+    for (int i = 0; i < 16; ++i) {
+      const long long r = r0 + i * 8 + warp;
+      const T* x = static_cast<const T*>(p.x) + (r < p.rows ? r : 0) * p.ld;
+      T* d = reinterpret_cast<T*>(smem + (i * 8 + warp) * S::PITCH);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const long long c = c0 + j * 32 + lane;
+        d[j * 32 + lane] = r < p.rows && c < p.cols ? x[c] : (T)0.f;
+      }
+    }
+    __syncthreads();
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int rin = (i >> 1) * 64 + warp * 8 + (lane >> 2), k = (i & 1) * 64 + (lane & 3) * 16;
     const bool rv = r0 + rin < p.rows;
-    v[i].load(static_cast<const T*>(p.x) + (rv ? r0 + rin : 0) * p.ld, c0 + k, rv ? p.cols : 0, p.vec);
+    if (p.vec)
+      v[i].load(static_cast<const T*>(p.x) + (rv ? r0 + rin : 0) * p.ld, c0 + k, rv ? p.cols : 0, true);
+    else if (ROWS)
+      v[i] = *reinterpret_cast<const Raw16<T>*>(smem + rin * S::PITCH + k * sizeof(T));
   }
   float u = 1.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int rin = (i >> 1) * 64 + warp * 8 + (lane >> 2), k = (i & 1) * 64 + (lane & 3) * 16;
-    *reinterpret_cast<Raw16<T>*>(smem + rin * S::PITCH + k * sizeof(T)) = v[i];
+    if (p.vec) *reinterpret_cast<Raw16<T>*>(smem + rin * S::PITCH + k * sizeof(T)) = v[i];
     if (ROWS) {
       if (BLOCK == 16 && (i & 1) == 0) {
         const bool rv = r0 + rin < p.rows;
@@ -383,6 +446,38 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const Fp4QuantArgs p
     }
   }
   __syncthreads();
+  __shared__ unsigned cmax[CLUSTER ? 128 : 1];   // this tile's, then read by the cluster
+  unsigned* call = reinterpret_cast<unsigned*>(sf_r);   // the whole columns'
+  if (CLUSTER) {
+    if (t < 128) cmax[t] = 0u;
+    __syncthreads();
+    for (int item = t; item < 4 * 128 / CW; item += 256) {
+      const int cw = item % (128 / CW), ch = item / (128 / CW);
+      uint32_t m = 0u;
+#pragma unroll 8
+      for (int e = 0; e < 32; ++e) {
+        const uint32_t x = *reinterpret_cast<const uint32_t*>(smem + (ch * 32 + e) * S::PITCH + cw * 4);
+        m = CW == 2 ? __vmaxu2(m, x & 0x7fff7fffu) : max(m, x & 0x7fffffffu);
+      }
+      if (CW == 2) {
+        atomicMax(&cmax[2 * cw], m << 16);
+        atomicMax(&cmax[2 * cw + 1], m & 0x7fff0000u);
+      } else {
+        atomicMax(&cmax[cw], m);
+      }
+    }
+    cluster_sync_all();
+    if (t < 128) {
+      unsigned m = 0u;
+      for (int r = 0; r < (int)Lr.rt; ++r) {
+        uint32_t x;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(mapa_shared(smem_u32(&cmax[t]), (uint32_t)r)));
+        m = max(m, x);
+      }
+      call[t] = m;
+    }
+    cluster_sync_all();   // (the others have read cmax)
+  }
   // a work item: 32 rows of the column(s) in one 32-bit word
 #pragma unroll 1
   for (int item = t; item < 4 * 128 / CW; item += 256) {
@@ -393,7 +488,8 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const Fp4QuantArgs p
       uc[w] = 1.f;
       if (BLOCK == 16) {
         const long long c = c0 + cw * CW + w;
-        const float g = row_scale(c < p.cols ? reinterpret_cast<const unsigned*>(p.out + Lc.max_off())[c] : 0u);
+        const float g = row_scale(CLUSTER ? call[cw * CW + w]
+                                  : c < p.cols ? reinterpret_cast<const unsigned*>(p.out + Lc.max_off())[c] : 0u);
         uc[w] = __fdiv_rn(1.f, g);
         if (r0 == 0 && ch == 0 && c < p.cols) reinterpret_cast<float*>(p.out + Lc.row_off())[c] = g;
       }
@@ -505,21 +601,26 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* packed, 
         if (k + 4 < cols) reinterpret_cast<float4*>(out)[1] = make_float4(v[4], v[5], v[6], v[7]);
       }
     }
-  } else {   // one row a warp step, neighbouring lanes neighbouring columns
+  } else {   // the tile through shared memory; one row a warp step, neighbouring lanes neighbouring columns
+    __shared__ __align__(16) uint8_t cs[8192 + 1024];
+    for (int i = threadIdx.x; i < 512; i += 256) reinterpret_cast<uint4*>(cs)[i] = reinterpret_cast<const uint4*>(codes)[i];
+    if (threadIdx.x < 32 * ATOMS)
+      reinterpret_cast<uint4*>(cs + 8192)[threadIdx.x] = reinterpret_cast<const uint4*>(sf)[threadIdx.x];
+    __syncthreads();
+#pragma unroll 4
     for (int i = 0; i < 16; ++i) {
-      const int rin = warp * 16 + i;
+      const int rin = i * 8 + warp;
       if (r0 + rin >= rows) break;
       const float g = BLOCK == 16 ? gs[rin] : 1.f;
 #pragma unroll
       for (int ch = 0; ch < 4; ++ch) {
         const long long k = c0 + ch * 32 + lane;
-        if (k >= cols) continue;
-        const uint32_t c = codes[ch * 2048 + rin * 16 + (lane >> 1)] >> (4 * (lane & 1));
+        const uint32_t c = cs[ch * 2048 + rin * 16 + (lane >> 1)] >> (4 * (lane & 1));
         const int ks = ch * (32 / BLOCK) + (BLOCK == 16 ? lane >> 4 : 0);
-        const uint8_t sb = sf[(ks >> 2) * 512 + (rin & 31) * 16 + (rin >> 5) * 4 + (ks & 3)];
+        const uint8_t sb = cs[8192 + (ks >> 2) * 512 + (rin & 31) * 16 + (rin >> 5) * 4 + (ks & 3)];
         float v = __fmul_rn(decode(c), BLOCK == 16 ? e4m3_to_f(sb) : e8m0_to_f(sb));
         if (BLOCK == 16) v = __fmul_rn(v, g);
-        y[(r0 + rin) * cols + k] = (T)v;
+        if (k < cols) y[(r0 + rin) * cols + k] = (T)v;
       }
     }
   }
@@ -532,17 +633,23 @@ cudaError_t launch_rows_j(const Fp4QuantArgs& a, cudaStream_t s) {
   const Fp4Layout L(a.rows, a.cols, BLOCK);
   const long long units = J == 4 ? L.kt * 2 : (L.kt + 1) / 2;
   constexpr int MOST = sizeof(T) == 2 ? 4 : 2;
+  const unsigned grid = (unsigned)(L.rt * 16);
+  size_t smem = (size_t)L.kt * L.atoms() * 32;
+  int staged = smem <= (a.vec ? 40 : 16) * 1024;
+  if (!staged) smem = 0;
+  if (!a.vec) {   // 12 warps' buffers and the scales stay within 48 KB
+    const int nw = (int)std::min<long long>(12, std::max<long long>(4, (units + 1) / 2));
+    smem += (size_t)nw * (J == 4 ? RowStage<T, 8, 64>::BYTES : RowStage<T, 2, 256>::BYTES);
+    quantize_rows_kernel<T, BLOCK, J, 2, false><<<grid, nw * 32, smem, s>>>(a, staged);
+    return cudaGetLastError();
+  }
   int iter = 1;
   while (iter < MOST && units > 16 * iter) iter *= 2;
   const int nw = (int)std::min<long long>(32, std::max<long long>(4, (units + iter - 1) / iter));
-  size_t smem = (size_t)L.kt * L.atoms() * 32;
-  const int staged = smem <= 40 * 1024;
-  if (!staged) smem = 0;
-  const unsigned grid = (unsigned)(L.rt * 16);
   switch (iter) {
-    case 1: quantize_rows_kernel<T, BLOCK, J, 1><<<grid, nw * 32, smem, s>>>(a, staged); break;
-    case 2: quantize_rows_kernel<T, BLOCK, J, 2><<<grid, nw * 32, smem, s>>>(a, staged); break;
-    default: quantize_rows_kernel<T, BLOCK, J, MOST><<<grid, nw * 32, smem, s>>>(a, staged); break;
+    case 1: quantize_rows_kernel<T, BLOCK, J, 1, true><<<grid, nw * 32, smem, s>>>(a, staged); break;
+    case 2: quantize_rows_kernel<T, BLOCK, J, 2, true><<<grid, nw * 32, smem, s>>>(a, staged); break;
+    default: quantize_rows_kernel<T, BLOCK, J, MOST, true><<<grid, nw * 32, smem, s>>>(a, staged); break;
   }
   return cudaGetLastError();
 }
@@ -552,26 +659,52 @@ cudaError_t launch_rows(const Fp4QuantArgs& a, cudaStream_t s) {
   return a.rows <= 32 ? launch_rows_j<T, BLOCK, 1>(a, s) : launch_rows_j<T, BLOCK, 4>(a, s);
 }
 
-template <typename T, int BLOCK, bool ROWS>
-cudaError_t launch_tile(const Fp4QuantArgs& a, unsigned grid, cudaStream_t s) {
+template <typename T, int BLOCK, bool ROWS, bool CLUSTER>
+cudaError_t launch_tile(const Fp4QuantArgs& a, unsigned grid, unsigned cluster, cudaStream_t s) {
   static std::once_flag once[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  auto kern = quantize_tile_kernel<T, BLOCK, ROWS>;
+  auto kern = quantize_tile_kernel<T, BLOCK, ROWS, CLUSTER>;
   std::call_once(once[dev], [&] {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TileSmem<T>::BYTES);
   });
   if (e != cudaSuccess) return e;
-  kern<<<grid, 256, TileSmem<T>::BYTES, s>>>(a);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = TileSmem<T>::BYTES;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = CLUSTER ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, kern, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
+
+// Block 16, x of up to 8 tiles down: the columns by clusters, the rows (both ways)
+// by their own kernel.
+inline bool by_clusters(const Fp4QuantArgs& a, int block) { return block == 16 && a.rows <= 8 * 128; }
 
 template <typename T, int BLOCK>
 cudaError_t launch_tiles(const Fp4QuantArgs& a, cudaStream_t s) {
   const Fp4Layout Lr(a.rows, a.cols, BLOCK), Lc(a.cols, a.rows, BLOCK);
   const unsigned grid = (unsigned)(Lr.kt * Lr.rt);
+  if (BLOCK == 16 && by_clusters(a, BLOCK)) {
+    if (a.out_rows) {
+      Fp4QuantArgs r = a;
+      r.out = a.out_rows;
+      r.out_rows = nullptr;
+      const cudaError_t e = launch_rows<T, BLOCK>(r, s);
+      if (e != cudaSuccess) return e;
+    }
+    return launch_tile<T, BLOCK, false, BLOCK == 16>(a, grid, (unsigned)Lr.rt, s);
+  }
   if (BLOCK == 16) {
     unsigned* cm = reinterpret_cast<unsigned*>(a.out + Lc.max_off());
     unsigned* rm = a.out_rows ? reinterpret_cast<unsigned*>(a.out_rows + Lr.max_off()) : nullptr;
@@ -583,7 +716,8 @@ cudaError_t launch_tiles(const Fp4QuantArgs& a, cudaStream_t s) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  return a.out_rows ? launch_tile<T, BLOCK, true>(a, grid, s) : launch_tile<T, BLOCK, false>(a, grid, s);
+  return a.out_rows ? launch_tile<T, BLOCK, true, false>(a, grid, 1, s)
+                    : launch_tile<T, BLOCK, false, false>(a, grid, 1, s);
 }
 
 template <typename T, int BLOCK>
@@ -608,8 +742,11 @@ cudaError_t launch_fp4_quantize(const Fp4QuantArgs& a, bool bf16, int block, boo
     if (bf16) return block == 16 ? launch_rows<__nv_bfloat16, 16>(a, s) : launch_rows<__nv_bfloat16, 32>(a, s);
     return block == 16 ? launch_rows<float, 16>(a, s) : launch_rows<float, 32>(a, s);
   }
-  *kernel_name = a.out_rows ? (block == 16 ? "fp4_absmax+fp4_quantize_both" : "fp4_quantize_both")
-                            : (block == 16 ? "fp4_absmax+fp4_quantize_columns" : "fp4_quantize_columns");
+  if (by_clusters(a, block))
+    *kernel_name = a.out_rows ? "fp4_quantize_rows+fp4_quantize_columns_cluster" : "fp4_quantize_columns_cluster";
+  else
+    *kernel_name = a.out_rows ? (block == 16 ? "fp4_absmax+fp4_quantize_both" : "fp4_quantize_both")
+                              : (block == 16 ? "fp4_absmax+fp4_quantize_columns" : "fp4_quantize_columns");
   if (bf16) return block == 16 ? launch_tiles<__nv_bfloat16, 16>(a, s) : launch_tiles<__nv_bfloat16, 32>(a, s);
   return block == 16 ? launch_tiles<float, 16>(a, s) : launch_tiles<float, 32>(a, s);
 }

@@ -67,28 +67,45 @@ __device__ __forceinline__ float from_f<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// The elements a thread holds, NV vectors of E: vector j of thread t of a row of
-// G threads is elements (j * G + t) * E + e (VEC: one 16-byte access), or, where
-// rows are not all 16-byte aligned, (j * E + e) * G + t (neighbouring threads,
-// neighbouring elements).
-template <typename T, bool VEC>
-__device__ __forceinline__ int elem(int j, int e, int t, int G) {
+// The elements a thread holds, NV vectors of E; where vector j of thread t of a row
+// of G threads lies (W):
+//   kAligned   elements (j * G + t) * E + e, one 16-byte access: every row starts
+//              on 16 bytes and holds whole vectors
+//   kShifted   the same s elements earlier, s the row's start past a 16-byte
+//              boundary: the vectors are aligned, the first and the last of a row
+//              are taken element by element (widths that are no multiple of 16
+//              bytes: all tensors of a row then start equally far past one)
+//   kScalar    (j * E + e) * G + t, element by element (neighbouring threads,
+//              neighbouring elements): tensors aligned unlike each other
+enum Access { kScalar, kAligned, kShifted };
+template <typename T, int W>
+__device__ __forceinline__ int elem(int j, int e, int t, int G, int s) {
   constexpr int E = Vec<T>::E;
-  return VEC ? (j * G + t) * E + e : (j * E + e) * G + t;
+  return W == kScalar ? (j * E + e) * G + t : (j * G + t) * E + e - (W == kShifted ? s : 0);
+}
+template <typename T, int W>
+__device__ __forceinline__ int row_shift(long long m, int n) {
+  return W == kShifted ? (int)((m * n) & (Vec<T>::E - 1)) : 0;
+}
+// Vector j is one access (which may lie past the end of the row).
+template <typename T, int W>
+__device__ __forceinline__ bool whole(int i, int n) {
+  return W == kAligned || (W == kShifted && i >= 0 && i + Vec<T>::E <= n);
 }
 // Vector j of a row of n elements, as 16 bytes of T; elements past the end are 0.
-template <typename T, bool VEC>
-__device__ __forceinline__ uint4 load_vec(const T* row, int j, int t, int G, int n) {
+template <typename T, int W>
+__device__ __forceinline__ uint4 load_vec(const T* row, int j, int t, int G, int s, int n) {
   constexpr int E = Vec<T>::E;
   uint4 r = make_uint4(0u, 0u, 0u, 0u);
-  if (VEC) {
-    const int i = elem<T, VEC>(j, 0, t, G);
-    if (i < n) r = *reinterpret_cast<const uint4*>(row + i);
-  } else {
+  const int i0 = elem<T, W>(j, 0, t, G, s);
+  if (whole<T, W>(i0, n)) {
+    if (i0 < n) r = *reinterpret_cast<const uint4*>(row + i0);
+  } else if (W == kScalar || i0 < n) {
     uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const int i = elem<T, VEC>(j, e, t, G);
+      const int i = elem<T, W>(j, e, t, G, s);
+      if (W == kShifted && i < 0) continue;
       if (sizeof(T) == 4) {
         if (i < n) w[e & 3] = reinterpret_cast<const uint32_t*>(row)[i];
       } else if (i < n) {
@@ -99,18 +116,18 @@ __device__ __forceinline__ uint4 load_vec(const T* row, int j, int t, int G, int
   }
   return r;
 }
-template <typename T, bool VEC>
-__device__ __forceinline__ void store_vec(T* row, int j, int t, int G, int n, const uint4& r) {
+template <typename T, int W>
+__device__ __forceinline__ void store_vec(T* row, int j, int t, int G, int s, int n, const uint4& r) {
   constexpr int E = Vec<T>::E;
-  if (VEC) {
-    const int i = elem<T, VEC>(j, 0, t, G);
-    if (i < n) *reinterpret_cast<uint4*>(row + i) = r;
-  } else {
+  const int i0 = elem<T, W>(j, 0, t, G, s);
+  if (whole<T, W>(i0, n)) {
+    if (i0 < n) *reinterpret_cast<uint4*>(row + i0) = r;
+  } else if (W == kScalar || i0 < n) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const int i = elem<T, VEC>(j, e, t, G);
-      if (i >= n) continue;
+      const int i = elem<T, W>(j, e, t, G, s);
+      if (i >= n || i < 0) continue;
       if (sizeof(T) == 4) reinterpret_cast<uint32_t*>(row)[i] = w[e & 3];
       else reinterpret_cast<uint16_t*>(row)[i] = (uint16_t)(w[(e >> 1) & 3] >> (16 * (e & 1)));
     }
@@ -127,12 +144,12 @@ __device__ __forceinline__ uint4 add_vec(const uint4& x, const uint4& r) {
   for (int e = 0; e < E; ++e) a[e] = __fadd_rn(a[e], b[e]);
   return Vec<T>::pack(a);
 }
-// The weight's elements at the same places (either type; VEC: 16-byte aligned).
-template <typename T, bool VEC>
-__device__ __forceinline__ void load_w(const void* w, int w_f32, int j, int t, int G, int n, float* v) {
+// The weight's elements at the same places (either type; kAligned: 16-byte aligned).
+template <typename T, int W>
+__device__ __forceinline__ void load_w(const void* w, int w_f32, int j, int t, int G, int s, int n, float* v) {
   constexpr int E = Vec<T>::E;
-  if (VEC) {
-    const int i = elem<T, VEC>(j, 0, t, G);
+  if (W == kAligned) {
+    const int i = elem<T, W>(j, 0, t, G, s);
     if (i >= n) {
 #pragma unroll
       for (int e = 0; e < E; ++e) v[e] = 0.f;
@@ -168,8 +185,8 @@ __device__ __forceinline__ void load_w(const void* w, int w_f32, int j, int t, i
   } else {
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const int i = elem<T, VEC>(j, e, t, G);
-      v[e] = i >= n ? 0.f
+      const int i = elem<T, W>(j, e, t, G, s);
+      v[e] = i >= n || i < 0 ? 0.f
              : w_f32 ? __ldg(static_cast<const float*>(w) + i)
                      : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i]);
     }
@@ -252,7 +269,7 @@ __device__ __forceinline__ float max_abs(float a, float b) {
 
 // One row per G = blockDim.x threads (blockDim.y rows a CTA where G is a warp),
 // NV vectors a thread. NV = 0: rows of any length, read twice.
-template <typename T, bool VEC, int NV>
+template <typename T, int W, int NV>
 __global__ void __launch_bounds__(1024) rms_norm_s8_kernel(const NormArgs p) {
   constexpr int E = Vec<T>::E;
   __shared__ float sa[32];
@@ -260,6 +277,7 @@ __global__ void __launch_bounds__(1024) rms_norm_s8_kernel(const NormArgs p) {
   const int n = p.H, G = blockDim.x, t = threadIdx.x;
   const long long m = (long long)blockIdx.x * blockDim.y + threadIdx.y;
   if (m >= p.M) return;   // whole warps (G a warp), or nobody
+  const int s = row_shift<T, W>(m, n);
   const T* x = static_cast<const T*>(p.x) + m * p.ldx;
   const T* r = p.residual ? static_cast<const T*>(p.residual) + m * p.ldr : nullptr;
   T* ho = p.h ? static_cast<T*>(p.h) + m * (long long)n : nullptr;
@@ -278,16 +296,16 @@ __global__ void __launch_bounds__(1024) rms_norm_s8_kernel(const NormArgs p) {
   auto put = [&](int j, const float* v, float inv, bool zero) {
     uint32_t o[E / 4];
     quantise<E>(v, inv, zero, o);
-    if (VEC) {
-      const int i = elem<T, VEC>(j, 0, t, G);
-      if (i >= n) return;
-      if (E == 8) *reinterpret_cast<uint2*>(q + i) = make_uint2(o[0], o[E / 4 - 1]);
-      else *reinterpret_cast<uint32_t*>(q + i) = o[0];
+    const int i0 = elem<T, W>(j, 0, t, G, s);
+    if (whole<T, W>(i0, n)) {
+      if (i0 >= n) return;
+      if (E == 8) *reinterpret_cast<uint2*>(q + i0) = make_uint2(o[0], o[E / 4 - 1]);
+      else *reinterpret_cast<uint32_t*>(q + i0) = o[0];
     } else {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const int i = elem<T, VEC>(j, e, t, G);
-        if (i < n) q[i] = (int8_t)(o[e >> 2] >> (8 * (e & 3)));
+        const int i = elem<T, W>(j, e, t, G, s);
+        if (i < n && i >= 0) q[i] = (int8_t)(o[e >> 2] >> (8 * (e & 3)));
       }
     }
   };
@@ -296,57 +314,57 @@ __global__ void __launch_bounds__(1024) rms_norm_s8_kernel(const NormArgs p) {
     uint4 h[K];
     float v[K][E];
 #pragma unroll
-    for (int j = 0; j < K; ++j) h[j] = load_vec<T, VEC>(x, j, t, G, n);
+    for (int j = 0; j < K; ++j) h[j] = load_vec<T, W>(x, j, t, G, s, n);
     if (r) {
       uint4 b[K];
 #pragma unroll
-      for (int j = 0; j < K; ++j) b[j] = load_vec<T, VEC>(r, j, t, G, n);
+      for (int j = 0; j < K; ++j) b[j] = load_vec<T, W>(r, j, t, G, s, n);
 #pragma unroll
       for (int j = 0; j < K; ++j) h[j] = add_vec<T>(h[j], b[j]);
     }
 #pragma unroll
     for (int j = 0; j < K; ++j) {
-      if (ho) store_vec<T, VEC>(ho, j, t, G, n, h[j]);
+      if (ho) store_vec<T, W>(ho, j, t, G, s, n, h[j]);
       float w[E];
-      load_w<T, VEC>(p.w, p.w_f32, j, t, G, n, w);
+      load_w<T, W>(p.w, p.w_f32, j, t, G, s, n, w);
       stats(h[j], w, v[j]);
     }
     unsigned am = __float_as_uint(amax);
     row_sum_max(ss, am, G, sa, sb);
-    const RowScale s = row_scale(ss, am, n, p.eps);
+    const RowScale rs = row_scale(ss, am, n, p.eps);
     if (t == 0) {
-      p.scale[m] = s.scale;
-      if (p.rstd) p.rstd[m] = s.rstd;
+      p.scale[m] = rs.scale;
+      if (p.rstd) p.rstd[m] = rs.rstd;
     }
 #pragma unroll
-    for (int j = 0; j < K; ++j) put(j, v[j], s.inv, am >= kInfBits);
+    for (int j = 0; j < K; ++j) put(j, v[j], rs.inv, am >= kInfBits);
   } else {
-    const int steps = (n + G * E - 1) / (G * E);
+    const int steps = (n + s + G * E - 1) / (G * E);
     for (int j = 0; j < steps; ++j) {
-      uint4 h = load_vec<T, VEC>(x, j, t, G, n);
-      if (r) h = add_vec<T>(h, load_vec<T, VEC>(r, j, t, G, n));
-      if (ho) store_vec<T, VEC>(ho, j, t, G, n, h);
+      uint4 h = load_vec<T, W>(x, j, t, G, s, n);
+      if (r) h = add_vec<T>(h, load_vec<T, W>(r, j, t, G, s, n));
+      if (ho) store_vec<T, W>(ho, j, t, G, s, n, h);
       float v[E], w[E];
-      load_w<T, VEC>(p.w, p.w_f32, j, t, G, n, w);
+      load_w<T, W>(p.w, p.w_f32, j, t, G, s, n, w);
       stats(h, w, v);
     }
     unsigned am = __float_as_uint(amax);
     row_sum_max(ss, am, G, sa, sb);
-    const RowScale s = row_scale(ss, am, n, p.eps);
+    const RowScale rs = row_scale(ss, am, n, p.eps);
     if (t == 0) {
-      p.scale[m] = s.scale;
-      if (p.rstd) p.rstd[m] = s.rstd;
+      p.scale[m] = rs.scale;
+      if (p.rstd) p.rstd[m] = rs.rstd;
     }
     for (int j = 0; j < steps; ++j) {
       // a stored h is read back (by the thread that wrote it: it may lie over x or the residual)
-      uint4 h = load_vec<T, VEC>(ho ? ho : x, j, t, G, n);
-      if (r && !ho) h = add_vec<T>(h, load_vec<T, VEC>(r, j, t, G, n));
+      uint4 h = load_vec<T, W>(ho ? ho : x, j, t, G, s, n);
+      if (r && !ho) h = add_vec<T>(h, load_vec<T, W>(r, j, t, G, s, n));
       float v[E], w[E];
-      load_w<T, VEC>(p.w, p.w_f32, j, t, G, n, w);
+      load_w<T, W>(p.w, p.w_f32, j, t, G, s, n, w);
       Vec<T>::unpack(h, v);
 #pragma unroll
       for (int e = 0; e < E; ++e) v[e] = __fmul_rn(v[e], w[e]);
-      put(j, v, s.inv, am >= kInfBits);
+      put(j, v, rs.inv, am >= kInfBits);
     }
   }
 }
@@ -397,7 +415,7 @@ __global__ void __launch_bounds__(256) s8_dequantize_rows_kernel(const int8_t* q
 // that HBM stays busy through a row's reduction. NV = 0: rows of any length,
 // read twice, the shares of dweight accumulated in partials itself.
 constexpr int PF = 2;
-template <typename T, bool VEC, int NV, bool DH>
+template <typename T, int W, int NV, bool DH>
 __global__ void __launch_bounds__(1024)
     rms_norm_backward_kernel(const NormBwdArgs p) {
   constexpr int E = Vec<T>::E;
@@ -410,13 +428,16 @@ __global__ void __launch_bounds__(1024)
   const T* dy0 = static_cast<const T*>(p.dy);
   const T* dh0 = DH ? static_cast<const T*>(p.dh) : nullptr;
   float* part = p.partials + (long long)blockIdx.x * n;
-  auto prefetch = [&](long long m) {
-    if (!VEC || t >= 3 || m >= p.M) return;
-    const T* row = t == 0 ? h0 + m * p.ldh : t == 1 ? dy0 + m * p.lddy : dh0 ? dh0 + m * p.lddh : nullptr;
-    if (row)
-      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(row), "r"((uint32_t)(n * sizeof(T))) : "memory");
-  };
   long long m = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+  // the same for all rows of a thread: their distance is a multiple of E rows (or
+  // there is one row), so its columns stay the same
+  const int s = row_shift<T, W>(m, n);
+  auto prefetch = [&](long long m) {
+    if (W == kScalar || t >= 3 || m >= p.M) return;
+    const T* row = t == 0 ? h0 + m * p.ldh : t == 1 ? dy0 + m * p.lddy : dh0 ? dh0 + m * p.lddh : nullptr;
+    const uint32_t bytes = ((uint32_t)(n + s) * (uint32_t)sizeof(T) + 15u) & ~15u;   // whole 16-byte lines
+    if (row) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(row - s), "r"(bytes) : "memory");
+  };
   int par = 0;
   if (NV > 0) {
     constexpr bool HELD = NV == 1;   // the weight in registers too
@@ -425,25 +446,25 @@ __global__ void __launch_bounds__(1024)
     for (int j = 0; j < K; ++j)
 #pragma unroll
       for (int e = 0; e < E; ++e) dw[j][e] = 0.f;
-    if (HELD) load_w<T, VEC>(p.w, p.w_f32, 0, t, G, n, w);
+    if (HELD) load_w<T, W>(p.w, p.w_f32, 0, t, G, s, n, w);
     for (int i = 1; i < PF; ++i) prefetch(m + i * step);
     for (; m < p.M; m += step) {
       prefetch(m + PF * step);
       const float rstd = __ldg(p.rstd + m);
       uint4 h[K], dy[K], dh[DH ? K : 1];
 #pragma unroll
-      for (int j = 0; j < K; ++j) h[j] = load_vec<T, VEC>(h0 + m * p.ldh, j, t, G, n);
+      for (int j = 0; j < K; ++j) h[j] = load_vec<T, W>(h0 + m * p.ldh, j, t, G, s, n);
 #pragma unroll
-      for (int j = 0; j < K; ++j) dy[j] = load_vec<T, VEC>(dy0 + m * p.lddy, j, t, G, n);
+      for (int j = 0; j < K; ++j) dy[j] = load_vec<T, W>(dy0 + m * p.lddy, j, t, G, s, n);
       if (DH) {
 #pragma unroll
-        for (int j = 0; j < K; ++j) dh[DH ? j : 0] = load_vec<T, VEC>(dh0 + m * p.lddh, j, t, G, n);
+        for (int j = 0; j < K; ++j) dh[DH ? j : 0] = load_vec<T, W>(dh0 + m * p.lddh, j, t, G, s, n);
       }
       float dot = 0.f;
 #pragma unroll
       for (int j = 0; j < K; ++j) {
         float nn[E], g[E];
-        if (!HELD) load_w<T, VEC>(p.w, p.w_f32, j, t, G, n, w);
+        if (!HELD) load_w<T, W>(p.w, p.w_f32, j, t, G, s, n, w);
         Vec<T>::unpack(h[j], nn);
         Vec<T>::unpack(dy[j], g);
 #pragma unroll
@@ -458,7 +479,7 @@ __global__ void __launch_bounds__(1024)
 #pragma unroll
       for (int j = 0; j < K; ++j) {
         float v[E], g[E];
-        if (!HELD) load_w<T, VEC>(p.w, p.w_f32, j, t, G, n, w);
+        if (!HELD) load_w<T, W>(p.w, p.w_f32, j, t, G, s, n, w);
         Vec<T>::unpack(h[j], v);
         Vec<T>::unpack(dy[j], g);
 #pragma unroll
@@ -468,36 +489,41 @@ __global__ void __launch_bounds__(1024)
 #pragma unroll
           for (int e = 0; e < E; ++e) v[e] += g[e];
         }
-        store_vec<T, VEC>(static_cast<T*>(p.dx) + m * (long long)n, j, t, G, n, Vec<T>::pack(v));
+        store_vec<T, W>(static_cast<T*>(p.dx) + m * (long long)n, j, t, G, s, n, Vec<T>::pack(v));
       }
     }
     if (NV == 1 && blockDim.y > 1) {   // the CTA's warps, each with rows of its own: added in order
 #pragma unroll
-      for (int e = 0; e < E; ++e) sw[(threadIdx.y * 32 + t) * E + e] = dw[0][e];
+      for (int e = 0; e < E; ++e) {
+        const int i = elem<T, W>(0, e, t, G, s);
+        if (i >= 0 && i < n) sw[threadIdx.y * 32 * E + i] = dw[0][e];
+      }
       __syncthreads();
-      if (threadIdx.y > 0) return;
-      for (int y = 1; y < (int)blockDim.y; ++y)
-#pragma unroll
-        for (int e = 0; e < E; ++e) dw[0][e] += sw[(y * 32 + t) * E + e];
+      for (int i = threadIdx.y * 32 + t; i < n; i += 32 * blockDim.y) {
+        float a = sw[i];
+        for (int y = 1; y < (int)blockDim.y; ++y) a += sw[y * 32 * E + i];
+        part[i] = a;
+      }
+      return;
     }
 #pragma unroll
     for (int j = 0; j < K; ++j)
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const int i = elem<T, VEC>(j, e, t, G);
-        if (i < n) part[i] = dw[j][e];
+        const int i = elem<T, W>(j, e, t, G, s);
+        if (i < n && i >= 0) part[i] = dw[j][e];
       }
   } else {
-    const int steps = (n + G * E - 1) / (G * E);
+    const int steps = (n + s + G * E - 1) / (G * E);
     bool fresh = true;
     for (; m < p.M; m += step) {
       const float rstd = __ldg(p.rstd + m);
       float dot = 0.f;
       for (int j = 0; j < steps; ++j) {
         float h[E], dy[E], w[E];
-        Vec<T>::unpack(load_vec<T, VEC>(h0 + m * p.ldh, j, t, G, n), h);
-        Vec<T>::unpack(load_vec<T, VEC>(dy0 + m * p.lddy, j, t, G, n), dy);
-        load_w<T, VEC>(p.w, p.w_f32, j, t, G, n, w);
+        Vec<T>::unpack(load_vec<T, W>(h0 + m * p.ldh, j, t, G, s, n), h);
+        Vec<T>::unpack(load_vec<T, W>(dy0 + m * p.lddy, j, t, G, s, n), dy);
+        load_w<T, W>(p.w, p.w_f32, j, t, G, s, n, w);
 #pragma unroll
         for (int e = 0; e < E; ++e) dot = __fmaf_rn(dy[e] * w[e], h[e] * rstd, dot);
       }
@@ -505,19 +531,19 @@ __global__ void __launch_bounds__(1024)
       par ^= 1;
       for (int j = 0; j < steps; ++j) {
         float h[E], dy[E], dh[E], w[E];
-        Vec<T>::unpack(load_vec<T, VEC>(h0 + m * p.ldh, j, t, G, n), h);
-        Vec<T>::unpack(load_vec<T, VEC>(dy0 + m * p.lddy, j, t, G, n), dy);
-        if (DH) Vec<T>::unpack(load_vec<T, VEC>(dh0 + m * p.lddh, j, t, G, n), dh);
-        load_w<T, VEC>(p.w, p.w_f32, j, t, G, n, w);
+        Vec<T>::unpack(load_vec<T, W>(h0 + m * p.ldh, j, t, G, s, n), h);
+        Vec<T>::unpack(load_vec<T, W>(dy0 + m * p.lddy, j, t, G, s, n), dy);
+        if (DH) Vec<T>::unpack(load_vec<T, W>(dh0 + m * p.lddh, j, t, G, s, n), dh);
+        load_w<T, W>(p.w, p.w_f32, j, t, G, s, n, w);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           const float nn = h[e] * rstd;
-          const int i = elem<T, VEC>(j, e, t, G);
-          if (i < n) part[i] = __fmaf_rn(dy[e], nn, fresh ? 0.f : part[i]);
+          const int i = elem<T, W>(j, e, t, G, s);
+          if (i < n && i >= 0) part[i] = __fmaf_rn(dy[e], nn, fresh ? 0.f : part[i]);
           h[e] = __fmaf_rn(-nn, mean, dy[e] * w[e]) * rstd;
           if (DH) h[e] += dh[e];
         }
-        store_vec<T, VEC>(static_cast<T*>(p.dx) + m * (long long)n, j, t, G, n, Vec<T>::pack(h));
+        store_vec<T, W>(static_cast<T*>(p.dx) + m * (long long)n, j, t, G, s, n, Vec<T>::pack(h));
       }
       fresh = false;
     }
@@ -550,9 +576,17 @@ __global__ void __launch_bounds__(1024) sum_partials_kernel(const float* part, i
   if (threadIdx.x == 0 && c < n) out[c] = a;
 }
 
+// A tensor of rows ld apart whose row m starts as far past a 16-byte boundary as
+// element m * H of an aligned array.
 template <typename T>
-bool rows_vec(const void* p, long long ld) {
-  return !p || ((reinterpret_cast<uintptr_t>(p) % 16) == 0 && (ld * (long long)sizeof(T)) % 16 == 0);
+bool rows_like(const void* p, long long ld, int H) {
+  return !p || ((reinterpret_cast<uintptr_t>(p) % 16) == 0 && (ld - H) % Vec<T>::E == 0);
+}
+// Vectors of a row, shifted if it has to be.
+template <typename T>
+int row_vectors(int H) {
+  constexpr int E = Vec<T>::E;
+  return H % E == 0 ? H / E : (H + 2 * (E - 1)) / E;
 }
 
 int round32(int v) { return (v + 31) / 32 * 32; }
@@ -565,10 +599,11 @@ int round32(int v) { return (v + 31) / 32 * 32; }
 template <typename T>
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
   constexpr int E = Vec<T>::E;
-  const bool vec = a.H % E == 0 && rows_vec<T>(a.x, a.ldx) && rows_vec<T>(a.residual, a.ldr) &&
-                   rows_vec<T>(a.h, a.H) && (reinterpret_cast<uintptr_t>(a.w) % 16) == 0 &&
-                   (reinterpret_cast<uintptr_t>(a.q) % 8) == 0;
-  const int nvec = (a.H + E - 1) / E;
+  const bool like = rows_like<T>(a.x, a.ldx, a.H) && rows_like<T>(a.residual, a.ldr, a.H) &&
+                    rows_like<T>(a.h, a.H, a.H) && (reinterpret_cast<uintptr_t>(a.q) % 8) == 0;
+  const Access acc = !like ? kScalar
+                     : a.H % E == 0 && (reinterpret_cast<uintptr_t>(a.w) % 16) == 0 ? kAligned : kShifted;
+  const int nvec = row_vectors<T>(a.H);
   const bool many = a.M >= 2 * num_sms();
   int nv = many ? (nvec <= 32 ? 1 : nvec <= 128 ? 2 : 4) : (nvec <= 1024 ? 1 : nvec <= 2048 ? 2 : 4);
   if (nvec > (many ? 2048 : 4096)) nv = 0;
@@ -583,10 +618,12 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
     case 4: rms_norm_s8_kernel<T, V, 4><<<grid, block, 0, s>>>(a); break;                   \
     default: rms_norm_s8_kernel<T, V, 0><<<grid, block, 0, s>>>(a); break;                  \
   }
-  if (vec) {
-    QMM_NORM(true)
+  if (acc == kAligned) {
+    QMM_NORM(kAligned)
+  } else if (acc == kShifted) {
+    QMM_NORM(kShifted)
   } else {
-    QMM_NORM(false)
+    QMM_NORM(kScalar)
   }
 #undef QMM_NORM
   return cudaGetLastError();
@@ -612,15 +649,15 @@ cudaError_t launch_dequantize(const int8_t* q, const float* scale, long long M, 
 // CTA at a time, CTAs (= rows of partials). 64 registers hold one vector of each
 // tensor with its weight and sums, two, or three of float32; longer rows are
 // read twice. The CTAs are those that fit at once (1024 threads an SM), at most 8
-// an SM for narrow rows (each adds a row to sum_partials' work).
+// an SM for narrow rows (each adds a row to sum_partials' work); more CTAs than
+// rows, or a multiple of 8 (row_shift).
 struct BwdShape {
   int nv, G, R, parts;
 };
 template <typename T>
 BwdShape backward_shape(long long M, int H) {
-  constexpr int E = Vec<T>::E;
   BwdShape b;
-  const int nvec = (H + E - 1) / E;
+  const int nvec = row_vectors<T>(H);
   b.nv = nvec <= 1024 ? 1 : nvec <= 2048 ? 2 : sizeof(T) == 4 && nvec <= 3072 ? 3 : 0;
   b.G = b.nv ? std::max(32, round32((nvec + b.nv - 1) / b.nv)) : 1024;
   b.R = b.G == 32 ? 8 : 1;
@@ -632,8 +669,10 @@ BwdShape backward_shape(long long M, int H) {
 template <typename T, bool DH>
 cudaError_t launch_backward(const NormBwdArgs& a, cudaStream_t s) {
   constexpr int E = Vec<T>::E;
-  const bool vec = a.H % E == 0 && rows_vec<T>(a.h, a.ldh) && rows_vec<T>(a.dy, a.lddy) &&
-                   rows_vec<T>(a.dh, a.lddh) && rows_vec<T>(a.dx, a.H) && (reinterpret_cast<uintptr_t>(a.w) % 16) == 0;
+  const bool like = rows_like<T>(a.h, a.ldh, a.H) && rows_like<T>(a.dy, a.lddy, a.H) &&
+                    rows_like<T>(a.dh, a.lddh, a.H) && rows_like<T>(a.dx, a.H, a.H);
+  const Access acc = !like ? kScalar
+                     : a.H % E == 0 && (reinterpret_cast<uintptr_t>(a.w) % 16) == 0 ? kAligned : kShifted;
   const BwdShape b = backward_shape<T>(a.M, a.H);
   const dim3 block(b.G, b.R);
 #define QMM_NORM(V)                                                                               \
@@ -643,10 +682,12 @@ cudaError_t launch_backward(const NormBwdArgs& a, cudaStream_t s) {
     case 3: rms_norm_backward_kernel<T, V, sizeof(T) == 4 ? 3 : 0, DH><<<b.parts, block, 0, s>>>(a); break; \
     default: rms_norm_backward_kernel<T, V, 0, DH><<<b.parts, block, 0, s>>>(a); break;           \
   }
-  if (vec) {
-    QMM_NORM(true)
+  if (acc == kAligned) {
+    QMM_NORM(kAligned)
+  } else if (acc == kShifted) {
+    QMM_NORM(kShifted)
   } else {
-    QMM_NORM(false)
+    QMM_NORM(kScalar)
   }
 #undef QMM_NORM
   cudaError_t e = cudaGetLastError();

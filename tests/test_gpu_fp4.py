@@ -36,7 +36,8 @@ def check_values(m, x, bf16_out=False):
 
 
 SHAPES = [(1, 1), (1, 16), (2, 31), (3, 33), (1, 4096), (16, 8192), (127, 128), (128, 129), (129, 127), (130, 257),
-          (64, 100), (300, 1000), (33, 4100), (257, 515), (5, 20000), (1, 70000)]
+          (64, 100), (300, 1000), (33, 4100), (257, 515), (5, 20000), (1, 70000), (1024, 200), (1025, 200),
+          (200, 1024), (201, 1027), (2, 200001), (1100, 2055)]
 
 
 @pytest.mark.parametrize("block", [16, 32])

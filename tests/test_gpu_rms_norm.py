@@ -53,7 +53,7 @@ def check_forward(x, r, w, out, eps):
 @pytest.mark.parametrize("residual", [True, False])
 @pytest.mark.parametrize("M,H", [(1, 1), (3, 7), (5, 8), (2, 33), (9, 64), (4, 100), (17, 255), (8, 256), (3, 1000),
                                  (1, 4096), (33, 4096), (7, 5003), (5, 8192), (2, 11008), (3, 16384), (2, 40000),
-                                 (1, 131072), (2, 70001)])
+                                 (1, 131072), (2, 70001), (700, 251), (701, 4099), (900, 13), (400, 8190), (40, 4097)])
 def test_forward(M, H, dt, residual):
     x, r, w = make(M, H, TYPES[dt], M * 1000 + H, residual)
     out = q.qmm_rms_norm_s8(x, w, residual=r, eps=1e-5, save_rstd=True)
@@ -169,7 +169,8 @@ def check_backward(dy, h, w, rstd, dh, dx, dw):
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("with_dh", [True, False])
 @pytest.mark.parametrize("M,H", [(1, 1), (3, 5), (1, 4096), (40, 33), (300, 256), (5, 1000), (1000, 4096), (33, 5003),
-                                 (777, 64), (20, 11008), (9, 16384), (3, 40000), (2, 100001)])
+                                 (777, 64), (20, 11008), (9, 16384), (3, 40000), (2, 100001), (2000, 251), (3000, 13), (1500, 4099), (700, 8190),
+                                 (310, 1025), (161, 12285)])
 def test_backward(M, H, dt, with_dh):
     t = TYPES[dt]
     g = torch.Generator(device="cuda").manual_seed(M + H)
