@@ -156,6 +156,9 @@ struct Raw16 {
     lo.load(row, k, n, vec);
     hi.load(row, k + 8, n, vec);
   }
+  __device__ __forceinline__ void load_whole(const T* p) {
+    *this = *reinterpret_cast<const Raw16<T>*>(p);
+  }
   __device__ __forceinline__ unsigned max_bits() const { return max(lo.max_bits(), hi.max_bits()); }
   // the block's scale, and the elements' codes, the first in the lowest bits
   template <int BLOCK>
@@ -223,6 +226,11 @@ __global__ void __launch_bounds__(VEC ? 1024 : 384) quantize_rows_kernel(const F
   const int batches = (units + nw * ITER - 1) / (nw * ITER);
   Raw16<T> v[ITER];
   auto load = [&](int b) {
+    if (VEC && (long long)(b + 1) * ITER * nw * WCOLS <= p.cols) {   // the whole batch lies inside
+#pragma unroll
+      for (int i = 0; i < ITER; ++i) v[i].load_whole(x + ((b * ITER + i) * nw + warp) * WCOLS + piece * 16);
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {   // past the end: columns past n, zeros
       const long long k0 = (long long)((b * ITER + i) * nw + warp) * WCOLS;
@@ -303,14 +311,14 @@ __global__ void __launch_bounds__(256) absmax_kernel(const Fp4QuantArgs p, unsig
   const long long c = (long long)tx * 256, r0 = (long long)ty * 64 + warp;
   cm[threadIdx.x] = 0u;
   __syncthreads();
-  if (p.vec) {
+  // rows past the end read the last one again: no maximum changes
+  const T* x = static_cast<const T*>(p.x);
+  if (p.vec && c + 256 <= p.cols) {
     unsigned m[8] = {};
     Raw8<T> v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const long long r = r0 + 8 * i;
-      v[i].load(static_cast<const T*>(p.x) + (r < p.rows ? r : 0) * p.ld, c + lane * 8, r < p.rows ? p.cols : 0, true);
-    }
+    for (int i = 0; i < 8; ++i)
+      v[i] = *reinterpret_cast<const Raw8<T>*>(x + min(r0 + 8 * i, p.rows - 1) * p.ld + c + lane * 8);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float f[8];
@@ -329,35 +337,27 @@ __global__ void __launch_bounds__(256) absmax_kernel(const Fp4QuantArgs p, unsig
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) atomicMax(&cm[lane * 8 + e], m[e]);
-  } else {   // rows that no vector load can take: neighbouring lanes, neighbouring columns
+  } else {   // neighbouring lanes, neighbouring columns (past the end the last one again)
     unsigned m[8] = {};
+    T v[8][8];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {   // four rows' loads together
-      T v[4][8];
+    for (int i = 0; i < 8; ++i) {
+      const T* row = x + min(r0 + 8 * i, p.rows - 1) * p.ld;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const long long r = r0 + 8 * (4 * h + i);
-        const T* x = static_cast<const T*>(p.x) + (r < p.rows ? r : 0) * p.ld;
+      for (int e = 0; e < 8; ++e) v[i][e] = row[min(c + e * 32 + lane, p.cols - 1)];
+    }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const long long k = c + e * 32 + lane;
-          v[i][e] = r < p.rows && k < p.cols ? x[k] : (T)0.f;
-        }
+    for (int i = 0; i < 8; ++i) {
+      unsigned rm = 0u;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const unsigned b = __float_as_uint((float)v[i][e]) & 0x7fffffffu;
+        m[e] = max(m[e], b);
+        rm = max(rm, b);
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const long long r = r0 + 8 * (4 * h + i);
-        unsigned rm = 0u;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const unsigned b = __float_as_uint((float)v[i][e]) & 0x7fffffffu;
-          m[e] = max(m[e], b);
-          rm = max(rm, b);
-        }
-        if (rowmax) {
-          rm = __reduce_max_sync(0xffffffffu, rm);
-          if (lane == 0 && r < p.rows) atomicMax(rowmax + r, rm);
-        }
+      if (rowmax) {
+        rm = __reduce_max_sync(0xffffffffu, rm);
+        if (lane == 0 && r0 + 8 * i < p.rows) atomicMax(rowmax + r0 + 8 * i, rm);
       }
     }
 #pragma unroll
@@ -417,8 +417,15 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const Fp4QuantArgs p
     }
     __syncthreads();
   }
+  const bool inside = p.vec && r0 + 128 <= p.rows && c0 + 128 <= p.cols;
+  if (inside) {
+    const T* x = static_cast<const T*>(p.x) + (r0 + warp * 8 + (lane >> 2)) * p.ld + c0 + (lane & 3) * 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i].load_whole(x + (i >> 1) * 64 * p.ld + (i & 1) * 64);
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
+    if (inside) break;
     const int rin = (i >> 1) * 64 + warp * 8 + (lane >> 2), k = (i & 1) * 64 + (lane & 3) * 16;
     const bool rv = r0 + rin < p.rows;
     if (p.vec)

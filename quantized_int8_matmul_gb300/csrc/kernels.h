@@ -321,6 +321,7 @@ struct NormBwdArgs {
   float* partials;             // rms_norm_backward_partials(M, H) rows of H floats
   long long M, lddy, ldh, lddh;
   int H;
+  unsigned* err;               // device error word
 };
 int rms_norm_backward_partials(long long M, int H);
 cudaError_t launch_rms_norm_backward(const NormBwdArgs& a, bool bf16, cudaStream_t s, const char** kernel_name);

@@ -17,6 +17,7 @@
 #include "kernels.h"
 
 #include <algorithm>
+#include <mutex>
 
 namespace qmm {
 namespace norm {
@@ -411,10 +412,9 @@ __global__ void __launch_bounds__(256) s8_dequantize_rows_kernel(const int8_t* q
 // Backward. A CTA takes rows blockIdx.x, blockIdx.x + gridDim.x, ... (blockDim.y
 // of them at a time where a row is one warp's) and keeps its columns' share of
 // dweight in registers; the shares go to partials and sum_partials adds them in
-// order. The next rows are prefetched to L2 by bulk copies (PF of them ahead), so
-// that HBM stays busy through a row's reduction. NV = 0: rows of any length,
-// read twice, the shares of dweight accumulated in partials itself.
-constexpr int PF = 2;
+// order. This one loads rows directly: rows of one warp, tensors aligned unlike
+// each other, and (NV = 0) rows too long for registers, which are read twice, the
+// shares of dweight accumulated in partials itself.
 template <typename T, int W, int NV, bool DH>
 __global__ void __launch_bounds__(1024)
     rms_norm_backward_kernel(const NormBwdArgs p) {
@@ -432,12 +432,6 @@ __global__ void __launch_bounds__(1024)
   // the same for all rows of a thread: their distance is a multiple of E rows (or
   // there is one row), so its columns stay the same
   const int s = row_shift<T, W>(m, n);
-  auto prefetch = [&](long long m) {
-    if (W == kScalar || t >= 3 || m >= p.M) return;
-    const T* row = t == 0 ? h0 + m * p.ldh : t == 1 ? dy0 + m * p.lddy : dh0 ? dh0 + m * p.lddh : nullptr;
-    const uint32_t bytes = ((uint32_t)(n + s) * (uint32_t)sizeof(T) + 15u) & ~15u;   // whole 16-byte lines
-    if (row) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(row - s), "r"(bytes) : "memory");
-  };
   int par = 0;
   if (NV > 0) {
     constexpr bool HELD = NV == 1;   // the weight in registers too
@@ -447,9 +441,7 @@ __global__ void __launch_bounds__(1024)
 #pragma unroll
       for (int e = 0; e < E; ++e) dw[j][e] = 0.f;
     if (HELD) load_w<T, W>(p.w, p.w_f32, 0, t, G, s, n, w);
-    for (int i = 1; i < PF; ++i) prefetch(m + i * step);
     for (; m < p.M; m += step) {
-      prefetch(m + PF * step);
       const float rstd = __ldg(p.rstd + m);
       uint4 h[K], dy[K], dh[DH ? K : 1];
 #pragma unroll
@@ -550,19 +542,143 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-// out[i] = the sum of column i of part [count][n], in a fixed order: 32 columns
-// a CTA, 32 interleaved runs of rows (eight loads of each in flight), then the
-// runs.
-__global__ void __launch_bounds__(1024) sum_partials_kernel(const float* part, int count, int n, float* out) {
+// The same for rows that come by bulk copies: a ring of `slots` rows (h, dy and dh
+// each in 16-byte lines; of rows too long for two slots of all three, h and dy) in
+// shared memory, refilled once a row's reduction has passed, so that the next rows
+// are on their way through the whole of this one's work. Waits are bounded (common.cuh).
+constexpr int RING_MAX = 8;
+constexpr unsigned SITE_ROW = 0x520;
+template <typename T, int W, int NV, bool DH>
+__global__ void __launch_bounds__(1024) rms_norm_backward_ring_kernel(const NormBwdArgs p, const int slots,
+                                                                      const int tensors) {
+  constexpr int E = Vec<T>::E;
+  constexpr bool HELD = NV == 1;   // the weight in registers too
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ float sa[2][32];
+  __shared__ uint64_t full[RING_MAX];
+  const int n = p.H, G = blockDim.x, t = threadIdx.x;
+  const long long m0 = blockIdx.x, step = gridDim.x;
+  const int rows = (int)((p.M - m0 + step - 1) / step);
+  const int s = row_shift<T, W>(m0, n);   // the same for all of the CTA's rows
+  const uint32_t line = ((uint32_t)(n + s) * (uint32_t)sizeof(T) + 15u) & ~15u;   // a row's bytes
+  const uint32_t pitch = (uint32_t)(n + E) * (uint32_t)sizeof(T) / 16u * 16u + 16u;
+  auto fill = [&](int r) {   // one thread
+    const long long m = m0 + r * step;
+    uint64_t* bar = &full[r % slots];
+    const uint32_t dst = smem_u32(ring) + (uint32_t)(r % slots) * (uint32_t)tensors * pitch;
+    mbar_arrive_expect_tx(bar, (uint32_t)tensors * line);
+    bulk_load(dst, static_cast<const T*>(p.h) + m * p.ldh - s, line, bar);
+    bulk_load(dst + pitch, static_cast<const T*>(p.dy) + m * p.lddy - s, line, bar);
+    if (DH && tensors == 3) bulk_load(dst + 2 * pitch, static_cast<const T*>(p.dh) + m * p.lddh - s, line, bar);
+  };
+  if (t == 0) {
+    for (int i = 0; i < slots; ++i) mbar_init(&full[i], 1);
+    fence_mbarrier_init();
+    for (int r = 0; r < slots && r < rows; ++r) fill(r);
+  }
+  float dw[NV][E], w[E];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int e = 0; e < E; ++e) dw[j][e] = 0.f;
+  if (HELD) load_w<T, W>(p.w, p.w_f32, 0, t, G, s, n, w);
+  __syncthreads();
+  // vector j of a row in the ring, with zeros outside the row
+  auto get = [&](const uint8_t* row, int j) {
+    const int i0 = elem<T, W>(j, 0, t, G, s);
+    uint4 r = make_uint4(0u, 0u, 0u, 0u);
+    if (i0 < n) r = *reinterpret_cast<const uint4*>(row + (size_t)(j * G + t) * 16);
+    if (W == kShifted && i0 < n && !whole<T, W>(i0, n)) {
+      float f[E];
+      Vec<T>::unpack(r, f);
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (i0 + e < 0 || i0 + e >= n) f[e] = 0.f;
+      r = Vec<T>::pack(f);
+    }
+    return r;
+  };
+  float next = __ldg(p.rstd + m0);
+  for (int r = 0; r < rows; ++r) {
+    const long long m = m0 + r * step;
+    const float rstd = next;
+    if (r + 1 < rows) next = __ldg(p.rstd + m + step);
+    if (!mbar_wait(&full[r % slots], (uint32_t)((r / slots) & 1), nullptr, p.err, SITE_ROW)) {
+      // (the copies of the later slots are waited for, with the same limit, before the CTA ends)
+      for (int i = 1; i < slots && r + i < rows; ++i)
+        mbar_wait(&full[(r + i) % slots], (uint32_t)(((r + i) / slots) & 1), nullptr, p.err, SITE_ROW);
+      break;
+    }
+    const uint8_t* in = ring + (size_t)(r % slots) * (uint32_t)tensors * pitch;
+    uint4 h[NV], dy[NV], dh[DH ? NV : 1];
+    float dot = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      h[j] = get(in, j);
+      dy[j] = get(in + pitch, j);
+      if (DH && tensors == 3) dh[DH ? j : 0] = get(in + 2 * pitch, j);
+      if (DH && tensors == 2)   // not in the ring: too long
+        dh[DH ? j : 0] = load_vec<T, W>(static_cast<const T*>(p.dh) + m * p.lddh, j, t, G, s, n);
+      float nn[E], g[E];
+      if (!HELD) load_w<T, W>(p.w, p.w_f32, j, t, G, s, n, w);
+      Vec<T>::unpack(h[j], nn);
+      Vec<T>::unpack(dy[j], g);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        nn[e] *= rstd;
+        dw[j][e] = __fmaf_rn(g[e], nn[e], dw[j][e]);
+        dot = __fmaf_rn(g[e] * w[e], nn[e], dot);
+      }
+    }
+    // past the barrier in row_sum the row is in registers and its slot free
+    const float c = -(row_sum(dot, G, sa[r & 1]) / (float)n) * rstd;   // dx = g * rstd + n * c
+    if (t == 0 && r + slots < rows) {
+      fence_proxy_async_smem();   // the slot was read through the generic proxy
+      fill(r + slots);
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float v[E], g[E];
+      if (!HELD) load_w<T, W>(p.w, p.w_f32, j, t, G, s, n, w);
+      Vec<T>::unpack(h[j], v);
+      Vec<T>::unpack(dy[j], g);
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = __fmaf_rn(v[e] * rstd, c, g[e] * w[e] * rstd);
+      if (DH) {
+        Vec<T>::unpack(dh[DH ? j : 0], g);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] += g[e];
+      }
+      store_vec<T, W>(static_cast<T*>(p.dx) + m * (long long)n, j, t, G, s, n, Vec<T>::pack(v));
+    }
+  }
+  float* part = p.partials + m0 * n;
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int i = elem<T, W>(j, e, t, G, s);
+      if (i < n && i >= 0) part[i] = dw[j][e];
+    }
+}
+
+// out[i] = the sum of column i of part [count][n], in a fixed order: a cluster for
+// 32 columns, each CTA a run of the rows as 32 interleaved ones (eight loads of
+// each in flight), joined in rank order.
+__global__ void __launch_bounds__(1024) sum_partials_kernel(const float* part, int count, int n, int split,
+                                                            float* out) {
   __shared__ float s[32][33];
+  __shared__ float sum[32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int i = blockIdx.x * 32 + threadIdx.x;
+  const int rank = split > 1 ? (int)cluster_ctarank() : 0, c0 = blockIdx.x / split * 32;
+  const int beg = (int)((long long)count * rank / split), end = (int)((long long)count * (rank + 1) / split);
+  const int i = c0 + threadIdx.x;
   float a = 0.f;
   if (i < n) {
-    for (int c = threadIdx.y; c < count; c += 32 * 8) {
+    for (int c = beg + threadIdx.y; c < end; c += 32 * 8) {
       float v[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = c + 32 * k < count ? part[(long long)(c + 32 * k) * n + i] : 0.f;
+      for (int k = 0; k < 8; ++k) v[k] = c + 32 * k < end ? part[(long long)(c + 32 * k) * n + i] : 0.f;
 #pragma unroll
       for (int k = 0; k < 8; ++k) a += v[k];
     }
@@ -572,8 +688,21 @@ __global__ void __launch_bounds__(1024) sum_partials_kernel(const float* part, i
   a = s[threadIdx.x][threadIdx.y];   // one column a warp
 #pragma unroll
   for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-  const int c = blockIdx.x * 32 + threadIdx.y;
-  if (threadIdx.x == 0 && c < n) out[c] = a;
+  if (threadIdx.x == 0) sum[threadIdx.y] = a;
+  if (split > 1) cluster_sync_all();
+  else __syncthreads();
+  if (rank == 0 && threadIdx.y == 0 && i < n) {
+    float r = sum[threadIdx.x];
+    for (int k = 1; k < split; ++k) {
+      float x;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                   : "=f"(x)
+                   : "r"(mapa_shared(smem_u32(&sum[threadIdx.x]), (uint32_t)k)));
+      r += x;
+    }
+    out[i] = r;
+  }
+  if (split > 1) cluster_sync_all();   // rank 0 has read the others' sums
 }
 
 // A tensor of rows ld apart whose row m starts as far past a 16-byte boundary as
@@ -646,24 +775,98 @@ cudaError_t launch_dequantize(const int8_t* q, const float* scale, long long M, 
 }
 
 // Launch shape of the backward pass: vectors a thread, threads a row, rows of a
-// CTA at a time, CTAs (= rows of partials). 64 registers hold one vector of each
-// tensor with its weight and sums, two, or three of float32; longer rows are
-// read twice. The CTAs are those that fit at once (1024 threads an SM), at most 8
-// an SM for narrow rows (each adds a row to sum_partials' work); more CTAs than
-// rows, or a multiple of 8 (row_shift).
+// CTA at a time, CTAs (= rows of partials), slots of a CTA's ring (0: direct).
+// 64 registers hold one vector of each tensor with its weight and sums, or two, or
+// three of float32; longer rows are read twice. CTAs are as many as fit at once
+// (1024 threads and the rings' two slots or more an SM, at most 8 an SM), no more
+// than rows, or a multiple of 8 (row_shift).
 struct BwdShape {
-  int nv, G, R, parts;
+  int nv, G, R, parts, slots, tensors;
+  size_t slot;   // bytes: a row of each of `tensors`
 };
 template <typename T>
-BwdShape backward_shape(long long M, int H) {
+BwdShape backward_shape(long long M, int H, bool dh, Access acc) {
+  constexpr int MOST = sizeof(T) == 4 ? 3 : 2;   // vectors a thread
+  constexpr int E = Vec<T>::E;
   BwdShape b;
   const int nvec = row_vectors<T>(H);
-  b.nv = nvec <= 1024 ? 1 : nvec <= 2048 ? 2 : sizeof(T) == 4 && nvec <= 3072 ? 3 : 0;
+  const size_t row = (size_t)(H + E) * sizeof(T) / 16 * 16 + 16, room = 212 * 1024;
+  b.tensors = dh && 2 * 3 * row <= room ? 3 : 2;
+  b.slot = b.tensors * row;
+  b.R = 1;
+  b.slots = 0;
+  b.nv = std::max(1, (nvec + 1023) / 1024);
+  if (b.nv > MOST) b.nv = 0;
   b.G = b.nv ? std::max(32, round32((nvec + b.nv - 1) / b.nv)) : 1024;
-  b.R = b.G == 32 ? 8 : 1;
-  const int per_sm = std::max(1, std::min(8, 1024 / (b.G * b.R)));
+  const int fit = (int)std::min<size_t>(64, room / b.slot);
+  int per_sm = std::min(8, 1024 / b.G);
+  if (acc != kScalar && b.nv > 0 && b.G > 32 && fit >= 2) {
+    per_sm = std::min(per_sm, fit / 2);
+    b.slots = std::min(RING_MAX, fit / per_sm);
+  } else {
+    if (acc == kScalar && b.nv == 3) b.nv = 0, b.G = 1024;
+    b.R = b.G == 32 ? 8 : 1;
+    per_sm = std::max(1, std::min(8, 1024 / (b.G * b.R)));
+  }
   b.parts = (int)std::min<long long>((M + b.R - 1) / b.R, 152ll * per_sm);
   return b;
+}
+
+// dweight from the partials, launched as a programmatic dependent.
+cudaError_t launch_sum(const NormBwdArgs& a, int parts, cudaStream_t s) {
+  const int groups = (a.H + 31) / 32;
+  int split = 1;   // up to 8, while that leaves every thread a load and every SM at most one CTA
+  while (split < 8 && parts >= 64 * split && groups * split * 2 <= num_sms()) split *= 2;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(groups * split));
+  cfg.blockDim = dim3(32, 32);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = split > 1 ? 2 : 1;
+  const cudaError_t e =
+      cudaLaunchKernelEx(&cfg, sum_partials_kernel, (const float*)a.partials, parts, a.H, split, a.dweight);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <typename T, int W, int NV, bool DH>
+cudaError_t launch_ring_nv(const NormBwdArgs& a, const BwdShape& b, int slots, size_t smem, cudaStream_t s) {
+  auto kern = rms_norm_backward_ring_kernel<T, W, NV, DH>;
+  static std::once_flag once[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::call_once(once[dev], [&] {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 222 * 1024);
+  });
+  if (e != cudaSuccess) return e;
+  kern<<<b.parts, b.G, smem, s>>>(a, slots, b.tensors);
+  return cudaGetLastError();
+}
+template <typename T, int W, bool DH>
+cudaError_t launch_ring(const NormBwdArgs& a, const BwdShape& b, cudaStream_t s) {
+  const size_t smem = b.slots * b.slot;
+  if (b.nv == 1) return launch_ring_nv<T, W, 1, DH>(a, b, b.slots, smem, s);
+  if (b.nv == 2) return launch_ring_nv<T, W, 2, DH>(a, b, b.slots, smem, s);
+  return launch_ring_nv<T, W, sizeof(T) == 4 ? 3 : 2, DH>(a, b, b.slots, smem, s);
+}
+
+// (of aligned tensors only rows of one warp and rows too long come here)
+template <typename T, int W, bool DH>
+void launch_direct(const NormBwdArgs& a, const BwdShape& b, dim3 block, cudaStream_t s) {
+  constexpr int NV2 = W == kScalar ? 2 : 0;
+  switch (b.nv) {
+    case 1: rms_norm_backward_kernel<T, W, 1, DH><<<b.parts, block, 0, s>>>(a); break;
+    case 2: rms_norm_backward_kernel<T, W, NV2, DH><<<b.parts, block, 0, s>>>(a); break;
+    default: rms_norm_backward_kernel<T, W, 0, DH><<<b.parts, block, 0, s>>>(a); break;
+  }
 }
 
 template <typename T, bool DH>
@@ -673,36 +876,17 @@ cudaError_t launch_backward(const NormBwdArgs& a, cudaStream_t s) {
                     rows_like<T>(a.dh, a.lddh, a.H) && rows_like<T>(a.dx, a.H, a.H);
   const Access acc = !like ? kScalar
                      : a.H % E == 0 && (reinterpret_cast<uintptr_t>(a.w) % 16) == 0 ? kAligned : kShifted;
-  const BwdShape b = backward_shape<T>(a.M, a.H);
+  const BwdShape b = backward_shape<T>(a.M, a.H, DH, acc);
   const dim3 block(b.G, b.R);
-#define QMM_NORM(V)                                                                               \
-  switch (b.nv) {                                                                                 \
-    case 1: rms_norm_backward_kernel<T, V, 1, DH><<<b.parts, block, 0, s>>>(a); break;            \
-    case 2: rms_norm_backward_kernel<T, V, 2, DH><<<b.parts, block, 0, s>>>(a); break;            \
-    case 3: rms_norm_backward_kernel<T, V, sizeof(T) == 4 ? 3 : 0, DH><<<b.parts, block, 0, s>>>(a); break; \
-    default: rms_norm_backward_kernel<T, V, 0, DH><<<b.parts, block, 0, s>>>(a); break;           \
+  if (b.slots > 0) {
+    const cudaError_t e = acc == kAligned ? launch_ring<T, kAligned, DH>(a, b, s) : launch_ring<T, kShifted, DH>(a, b, s);
+    return e != cudaSuccess ? e : launch_sum(a, b.parts, s);
   }
-  if (acc == kAligned) {
-    QMM_NORM(kAligned)
-  } else if (acc == kShifted) {
-    QMM_NORM(kShifted)
-  } else {
-    QMM_NORM(kScalar)
-  }
-#undef QMM_NORM
+  if (acc == kAligned) launch_direct<T, kAligned, DH>(a, b, block, s);
+  else if (acc == kShifted) launch_direct<T, kShifted, DH>(a, b, block, s);
+  else launch_direct<T, kScalar, DH>(a, b, block, s);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.H + 31) / 32));
-  cfg.blockDim = dim3(32, 32);
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, sum_partials_kernel, (const float*)a.partials, b.parts, a.H, a.dweight);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return e != cudaSuccess ? e : launch_sum(a, b.parts, s);
 }
 
 }  // namespace norm
@@ -719,9 +903,14 @@ cudaError_t launch_s8_dequantize_rows(const int8_t* q, const float* scale, long 
               : norm::launch_dequantize(q, scale, M, H, static_cast<float*>(y), s);
 }
 
-// The larger of the two types' counts (the size query does not know the type).
+// The largest count over what the size query does not know: type, dh, alignment.
 int rms_norm_backward_partials(long long M, int H) {
-  return std::max(norm::backward_shape<float>(M, H).parts, norm::backward_shape<__nv_bfloat16>(M, H).parts);
+  int most = 0;
+  for (const norm::Access acc : {norm::kScalar, norm::kAligned})
+    for (const bool dh : {false, true})
+      most = std::max({most, norm::backward_shape<float>(M, H, dh, acc).parts,
+                       norm::backward_shape<__nv_bfloat16>(M, H, dh, acc).parts});
+  return most;
 }
 
 cudaError_t launch_rms_norm_backward(const NormBwdArgs& a, bool bf16, cudaStream_t s, const char** kernel_name) {

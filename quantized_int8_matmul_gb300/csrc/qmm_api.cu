@@ -1689,8 +1689,11 @@ qmm_status qmm_rms_norm_backward(const void* dy, int64_t lddy, const void* h, in
   if ((dx == dy && lddy != H) || (dx == dh && lddh != H) || dx == h) return QMM_ERR_INVALID_ARG;
   if (!workspace || !aligned16(workspace) || workspace_bytes < qmm_rms_norm_backward_workspace_bytes(M, H))
     return QMM_ERR_INVALID_ARG;
+  unsigned* err = err_word();
+  if (!err) return QMM_ERR_CUDA;
   cudaGetLastError();
   NormBwdArgs a{};
+  a.err = err;
   a.dy = dy;
   a.h = h;
   a.dh = dh;
