@@ -14,6 +14,7 @@
 // A block (32) or row (16) that holds a NaN or an infinity gets a NaN scale.
 //
 // Bound by HBM: x is read once, 0.53 or 0.56 bytes an element are written.
+#include "chain.cuh"
 #include "common.cuh"
 #include "fp4.cuh"
 #include "kernels.h"
@@ -200,19 +201,23 @@ struct RowStage {
 // between its maximum and its codes, longer rows are read again.
 // ---------------------------------------------------------------------------
 template <typename T, int BLOCK, int J, int ITER, bool VEC>
-__global__ void __launch_bounds__(VEC ? 1024 : 384) quantize_rows_kernel(const Fp4QuantArgs p, const int staged) {
+__global__ void __launch_bounds__(VEC ? 1024 : 896) quantize_rows_kernel(const Fp4QuantArgs p, const int staged,
+                                                                                const int whole) {
   constexpr int WROWS = J == 4 ? 8 : 2, WCOLS = J == 4 ? 64 : 256;   // a warp step
+  const int nw = blockDim.x >> 5;
+  chain_wait();
   constexpr int ATOMS = BLOCK == 16 ? 2 : 1;
   constexpr int SPC = 32 / BLOCK;      // scales per 32-column chunk
   constexpr int LANES = J == 4 ? 4 : 16;   // lanes a row
   constexpr int UC = LANES / 2;        // chunks a warp step
   __shared__ unsigned rowmax[8];
-  // rows that no vector load can take: a buffer a warp; then the scales (staged),
-  // [atom][2 rows][4 rows 32 apart][4]
+  // rows that no vector load can take: all of the CTA's rows (whole > 0: elements
+  // between them), or a buffer a warp; then the scales (staged), [atom][2 rows][4
+  // rows 32 apart][4]
   extern __shared__ __align__(128) uint8_t smem[];
-  uint8_t* sfs = smem + (VEC ? 0 : (blockDim.x >> 5) * RowStage<T, WROWS, WCOLS>::BYTES);
+  uint8_t* sfs = smem + (VEC ? 0 : whole ? WROWS * whole * (int)sizeof(T) : nw * RowStage<T, WROWS, WCOLS>::BYTES);
   const Fp4Layout L(p.rows, p.cols, BLOCK);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int tile = blockIdx.x >> 4, c2 = 2 * (blockIdx.x & 15);
   const int ra = J == 4 ? (lane >> 2) & 1 : lane >> 4, rj = J == 4 ? lane >> 3 : 0;
   const int piece = lane & (LANES - 1), half = piece & 1;
@@ -224,8 +229,49 @@ __global__ void __launch_bounds__(VEC ? 1024 : 384) quantize_rows_kernel(const F
   const int n = rv ? (int)p.cols : 0;
   const int chunks = (int)L.kt * 4, units = (chunks + UC - 1) / UC;
   const int batches = (units + nw * ITER - 1) / (nw * ITER);
+  if (!VEC && whole) {
+    T* all = reinterpret_cast<T*>(smem);
+    constexpr int CB = 16 / WROWS;   // 16 loads in flight: all rows, CB columns apart
+    const T* xr[WROWS];
+    int m[WROWS];
+#pragma unroll
+    for (int r = 0; r < WROWS; ++r) {
+      const long long rr = (long long)tile * 128 + c2 + (r & 1) + 32 * (r >> 1);
+      xr[r] = static_cast<const T*>(p.x) + (rr < p.rows ? rr : 0) * p.ld;
+      m[r] = rr < p.rows ? (int)p.cols : 0;
+    }
+    for (int c = threadIdx.x; c < units * WCOLS; c += CB * blockDim.x) {
+      T e[CB][WROWS];
+#pragma unroll
+      for (int k = 0; k < CB; ++k)
+#pragma unroll
+        for (int r = 0; r < WROWS; ++r) {
+          const int i = c + k * blockDim.x;
+          e[k][r] = xr[r][min(i, (int)p.cols - 1)];
+          if (i >= m[r]) e[k][r] = (T)0.f;
+        }
+#pragma unroll
+      for (int k = 0; k < CB; ++k)
+#pragma unroll
+        for (int r = 0; r < WROWS; ++r) {
+          const int i = c + k * blockDim.x;
+          if (i < units * WCOLS) all[r * whole + i] = e[k][r];
+        }
+    }
+    __syncthreads();
+  }
   Raw16<T> v[ITER];
   auto load = [&](int b) {
+    if (!VEC && whole) {
+      const T* all = reinterpret_cast<const T*>(smem) + (J == 4 ? rj * 2 + ra : ra) * whole + piece * 16;
+#pragma unroll
+      for (int i = 0; i < ITER; ++i) {
+        const int un = (b * ITER + i) * nw + warp;
+        if (un < units) v[i].load_whole(all + un * WCOLS);
+        else v[i] = Raw16<T>{};
+      }
+      return;
+    }
     if (VEC && (long long)(b + 1) * ITER * nw * WCOLS <= p.cols) {   // the whole batch lies inside
 #pragma unroll
       for (int i = 0; i < ITER; ++i) v[i].load_whole(x + ((b * ITER + i) * nw + warp) * WCOLS + piece * 16);
@@ -290,6 +336,7 @@ __global__ void __launch_bounds__(VEC ? 1024 : 384) quantize_rows_kernel(const F
       }
     }
   }
+  chain_release();
   if (staged) {
     __syncthreads();
     for (int i = threadIdx.x; i < (int)L.kt * ATOMS * 2; i += blockDim.x)
@@ -306,6 +353,7 @@ __global__ void __launch_bounds__(VEC ? 1024 : 384) quantize_rows_kernel(const F
 template <typename T>
 __global__ void __launch_bounds__(256) absmax_kernel(const Fp4QuantArgs p, unsigned* colmax, unsigned* rowmax) {
   __shared__ unsigned cm[256];
+  chain_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int ct = (int)((p.cols + 255) / 256), ty = blockIdx.x / ct, tx = blockIdx.x - ty * ct;
   const long long c = (long long)tx * 256, r0 = (long long)ty * 64 + warp;
@@ -363,6 +411,7 @@ __global__ void __launch_bounds__(256) absmax_kernel(const Fp4QuantArgs p, unsig
 #pragma unroll
     for (int e = 0; e < 8; ++e) atomicMax(&cm[e * 32 + lane], m[e]);
   }
+  chain_release();
   __syncthreads();
   if (c + threadIdx.x < p.cols) atomicMax(colmax + c + threadIdx.x, cm[threadIdx.x]);
 }
@@ -383,6 +432,7 @@ struct TileSmem {
 
 template <typename T, int BLOCK, bool ROWS, bool CLUSTER>
 __global__ void __launch_bounds__(256) quantize_tile_kernel(const Fp4QuantArgs p) {
+  chain_wait();
   using S = TileSmem<T>;
   constexpr int ATOMS = BLOCK == 16 ? 2 : 1;
   constexpr int SPC = 32 / BLOCK;
@@ -535,6 +585,7 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const Fp4QuantArgs p
       *reinterpret_cast<uint4*>(codes_c + ch * 2048 + (cw * CW + w) * 16) =
           make_uint4(code[w][0], code[w][1], code[w][2], code[w][3]);
   }
+  chain_release();
   fence_proxy_async_smem();   // this thread's writes, visible to the copy engine
   __syncthreads();
   if (t == 0) {
@@ -561,6 +612,7 @@ __device__ __forceinline__ float decode(uint32_t c) {
 
 template <typename T, int BLOCK, bool VEC>
 __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* packed, long long rows, long long cols, T* y) {
+  chain_wait();
   constexpr int ATOMS = BLOCK == 16 ? 2 : 1;
   const Fp4Layout L(rows, cols, BLOCK);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -582,6 +634,7 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* packed, 
       sb[i] = sf[(ks >> 2) * 512 + (rin & 31) * 16 + (rin >> 5) * 4 + (ks & 3)];
       if (BLOCK == 16 && ch == 0 && r0 + rin < rows) g[i >> 2] = gs[rin];
     }
+    chain_release();
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int ch = i & 3, rin = (i >> 2) * 64 + warp * 8 + (lane >> 2);
@@ -613,6 +666,7 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* packed, 
     for (int i = threadIdx.x; i < 512; i += 256) reinterpret_cast<uint4*>(cs)[i] = reinterpret_cast<const uint4*>(codes)[i];
     if (threadIdx.x < 32 * ATOMS)
       reinterpret_cast<uint4*>(cs + 8192)[threadIdx.x] = reinterpret_cast<const uint4*>(sf)[threadIdx.x];
+    chain_release();
     __syncthreads();
 #pragma unroll 4
     for (int i = 0; i < 16; ++i) {
@@ -644,21 +698,34 @@ cudaError_t launch_rows_j(const Fp4QuantArgs& a, cudaStream_t s) {
   size_t smem = (size_t)L.kt * L.atoms() * 32;
   int staged = smem <= (a.vec ? 40 : 16) * 1024;
   if (!staged) smem = 0;
-  if (!a.vec) {   // 12 warps' buffers and the scales stay within 48 KB
-    const int nw = (int)std::min<long long>(12, std::max<long long>(4, (units + 1) / 2));
-    smem += (size_t)nw * (J == 4 ? RowStage<T, 8, 64>::BYTES : RowStage<T, 2, 256>::BYTES);
-    quantize_rows_kernel<T, BLOCK, J, 2, false><<<grid, nw * 32, smem, s>>>(a, staged);
-    return cudaGetLastError();
+  if (!a.vec) {
+    constexpr int WROWS = J == 4 ? 8 : 2, WCOLS = J == 4 ? 64 : 256;
+    auto kern = quantize_rows_kernel<T, BLOCK, J, 2, false>;
+    static std::once_flag once[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::call_once(once[dev],
+                   [&] { e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024); });
+    if (e != cudaSuccess) return e;
+    // all rows in shared memory (16 bytes a row more keep them off each other's
+    // banks), or, where they are too long, the warps' buffers
+    const long long whole = units * WCOLS + 16 / (long long)sizeof(T);
+    if (whole * WROWS * (long long)sizeof(T) + (long long)smem <= 200 * 1024) {
+      const int nw = (int)std::min<long long>(16, std::max<long long>(8, (units + 1) / 2));
+      return launch_chained(kern, grid, nw * 32, smem + (size_t)whole * WROWS * sizeof(T), 1, s, a, staged, (int)whole);
+    }
+    const int nw = 28;
+    return launch_chained(kern, grid, nw * 32, smem + (size_t)nw * RowStage<T, WROWS, WCOLS>::BYTES, 1, s, a, staged, 0);
   }
   int iter = 1;
   while (iter < MOST && units > 16 * iter) iter *= 2;
   const int nw = (int)std::min<long long>(32, std::max<long long>(4, (units + iter - 1) / iter));
-  switch (iter) {
-    case 1: quantize_rows_kernel<T, BLOCK, J, 1, true><<<grid, nw * 32, smem, s>>>(a, staged); break;
-    case 2: quantize_rows_kernel<T, BLOCK, J, 2, true><<<grid, nw * 32, smem, s>>>(a, staged); break;
-    default: quantize_rows_kernel<T, BLOCK, J, MOST, true><<<grid, nw * 32, smem, s>>>(a, staged); break;
-  }
-  return cudaGetLastError();
+  auto kern = iter == 1   ? quantize_rows_kernel<T, BLOCK, J, 1, true>
+              : iter == 2 ? quantize_rows_kernel<T, BLOCK, J, 2, true>
+                          : quantize_rows_kernel<T, BLOCK, J, MOST, true>;
+  return launch_chained(kern, grid, nw * 32, smem, 1, s, a, staged, 0);
 }
 
 template <typename T, int BLOCK>
@@ -678,20 +745,7 @@ cudaError_t launch_tile(const Fp4QuantArgs& a, unsigned grid, unsigned cluster, 
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TileSmem<T>::BYTES);
   });
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = TileSmem<T>::BYTES;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = CLUSTER ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, kern, a);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return launch_chained(kern, grid, 256, TileSmem<T>::BYTES, cluster, s, a);
 }
 
 // Block 16, x of up to 8 tiles down: the columns by clusters, the rows (both ways)
@@ -719,8 +773,7 @@ cudaError_t launch_tiles(const Fp4QuantArgs& a, cudaStream_t s) {
     if (e == cudaSuccess && rm) e = cudaMemsetAsync(rm, 0, (size_t)Lr.rt * 512, s);
     if (e != cudaSuccess) return e;
     const long long ctas = ((a.cols + 255) / 256) * ((a.rows + 63) / 64);
-    absmax_kernel<T><<<(unsigned)ctas, 256, 0, s>>>(a, cm, rm);
-    e = cudaGetLastError();
+    e = launch_chained(absmax_kernel<T>, (unsigned)ctas, 256, 0, 1, s, a, cm, rm);
     if (e != cudaSuccess) return e;
   }
   return a.out_rows ? launch_tile<T, BLOCK, true, false>(a, grid, 1, s)
@@ -732,9 +785,8 @@ cudaError_t launch_dequantize(const uint8_t* in, long long rows, long long cols,
   const Fp4Layout L(rows, cols, BLOCK);
   const unsigned grid = (unsigned)(L.kt * L.rt);
   const bool vec = (reinterpret_cast<uintptr_t>(y) % 16) == 0 && (cols * (long long)sizeof(T)) % 16 == 0;
-  if (vec) dequantize_kernel<T, BLOCK, true><<<grid, 256, 0, s>>>(in, rows, cols, static_cast<T*>(y));
-  else dequantize_kernel<T, BLOCK, false><<<grid, 256, 0, s>>>(in, rows, cols, static_cast<T*>(y));
-  return cudaGetLastError();
+  auto kern = vec ? dequantize_kernel<T, BLOCK, true> : dequantize_kernel<T, BLOCK, false>;
+  return launch_chained(kern, grid, 256, 0, 1, s, in, rows, cols, static_cast<T*>(y));
 }
 
 }  // namespace fp4

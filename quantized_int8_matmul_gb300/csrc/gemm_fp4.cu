@@ -15,6 +15,7 @@
 // each CTA adds up its share of the rows over the cluster in rank order (so the
 // result does not depend on timing), scales and stores them.
 // Every wait is bounded (common.cuh).
+#include "chain.cuh"
 #include "common.cuh"
 #include "fp4.cuh"
 #include "gemm_fp4.cuh"
@@ -98,8 +99,7 @@ __global__ void __launch_bounds__(NT, 2) gemm_fp4_rows_kernel(const GemmFp4Args 
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = sm.tmem_base;
-  // launched as a programmatic dependent: what is above ran under the call before
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  chain_wait();   // what is above ran under the call before
 
   if (warp == 5) {
     // ---------------- producer ----------------
@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(NT, 2) gemm_fp4_rows_kernel(const GemmFp4Args 
   }
   // ---------------- partial sums to shared memory: part[m][128] ----------------
   const bool ok = mbar_wait(&sm.done, 0u, nullptr, p.err, SITE_DONE, 4 * kWaitLimitNs);
+  chain_release();
   tc_fence_after();
   // the ring is free: every copy has landed (the MMAs that completed waited for
   // them all, or the producer did before this barrier)
@@ -290,23 +291,7 @@ cudaError_t launch(const GemmFp4Args& a, cudaStream_t s) {
   }
   const Plan pl = make_plan<BLOCK>(a);
   const Fp4Layout LB(a.N, a.K, BLOCK);
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)pl.split;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(LB.rt * pl.split), 1, 1);
-  cfg.blockDim = dim3(NT, 1, 1);
-  cfg.dynamicSmemBytes = pl.smem;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, pl);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  return launch_chained(kern, (unsigned)(LB.rt * pl.split), NT, pl.smem, (unsigned)pl.split, s, a, pl);
 }
 
 }  // namespace rows

@@ -28,6 +28,7 @@
 // (0..255 and 192..447; the scales at 448). The epilogue empties those 64 first
 // and the next tile's MMAs start then.
 // Every wait is bounded (common.cuh).
+#include "chain.cuh"
 #include "common.cuh"
 #include "fp4.cuh"
 #include "gemm_fp4.cuh"
@@ -229,6 +230,7 @@ __global__ void __launch_bounds__(NT, 1)
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tbase = sm.tmem_base;
+  chain_wait();   // what is above ran under the call before
 
   if (warp == NEW) {
     // ---------------- pair MMA issuer (even CTA, the warp converged) ----------------
@@ -349,6 +351,7 @@ __global__ void __launch_bounds__(NT, 1)
       // even tiles share columns 192..255 with the next accumulator, odd ones 0..63
       const int first = (tl & 1) || units < 2 ? 0 : 1;
       const bool shares = units == 2 && h == ((tl & 1) ? 0 : 1);   // (a piece is the last of its cluster)
+      if (tl == my_tiles - 1) chain_release();
       if (!shares) {
         __syncwarp();
         if (lane == 0) mbar_arrive_remote_cta(free0);
@@ -382,6 +385,7 @@ __global__ void __launch_bounds__(NT, 1)
     tc_fence_before();
   }
 
+  chain_release();
   __syncthreads();
   if (t == 0 && sm.abort_flag) st_shared_cluster_u32(mapa_shared(smem_u32(&sm.abort_flag), rank ^ 1u), 1u);
   if (warp == NEW && rank == 0) {
@@ -409,7 +413,9 @@ cudaError_t launch(const GemmFp4Args& a, cudaStream_t s) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
@@ -419,7 +425,7 @@ cudaError_t launch(const GemmFp4Args& a, cudaStream_t s) {
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 1;   // (the occupancy query; the launch is chained)
   int clusters = 0;
   {
     std::lock_guard<std::mutex> lock(mu);
@@ -465,6 +471,7 @@ cudaError_t launch(const GemmFp4Args& a, cudaStream_t s) {
   }
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(2 * (unsigned)std::min(std::max(tiles, sc.pieces), clusters), 1, 1);
+  cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, kern, a, tma_c, sc, ta, tb, tbp, tsa, tsb, tc);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();

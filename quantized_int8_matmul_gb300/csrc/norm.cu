@@ -13,6 +13,7 @@
 // Sums and statistics are fp32. Both are bound by HBM: every tensor is read or
 // written once, the row held in registers between its reduction and its output
 // (rows too long for that are read twice).
+#include "chain.cuh"
 #include "common.cuh"
 #include "kernels.h"
 
@@ -275,6 +276,7 @@ __global__ void __launch_bounds__(1024) rms_norm_s8_kernel(const NormArgs p) {
   constexpr int E = Vec<T>::E;
   __shared__ float sa[32];
   __shared__ unsigned sb[32];
+  chain_wait();
   const int n = p.H, G = blockDim.x, t = threadIdx.x;
   const long long m = (long long)blockIdx.x * blockDim.y + threadIdx.y;
   if (m >= p.M) return;   // whole warps (G a warp), or nobody
@@ -333,6 +335,7 @@ __global__ void __launch_bounds__(1024) rms_norm_s8_kernel(const NormArgs p) {
     unsigned am = __float_as_uint(amax);
     row_sum_max(ss, am, G, sa, sb);
     const RowScale rs = row_scale(ss, am, n, p.eps);
+    chain_release();
     if (t == 0) {
       p.scale[m] = rs.scale;
       if (p.rstd) p.rstd[m] = rs.rstd;
@@ -352,6 +355,7 @@ __global__ void __launch_bounds__(1024) rms_norm_s8_kernel(const NormArgs p) {
     unsigned am = __float_as_uint(amax);
     row_sum_max(ss, am, G, sa, sb);
     const RowScale rs = row_scale(ss, am, n, p.eps);
+    chain_release();
     if (t == 0) {
       p.scale[m] = rs.scale;
       if (p.rstd) p.rstd[m] = rs.rstd;
@@ -375,6 +379,7 @@ __global__ void __launch_bounds__(1024) rms_norm_s8_kernel(const NormArgs p) {
 template <typename T, typename I, bool VEC>
 __global__ void __launch_bounds__(256) s8_dequantize_rows_kernel(const int8_t* q, const float* scale, I total, I H,
                                                                  T* y) {
+  chain_wait();
   constexpr int STEPS = 4;
   uint2 raw[STEPS];
   const I base = (I)blockIdx.x * (256 * 8 * STEPS) + threadIdx.x * 8;
@@ -383,6 +388,7 @@ __global__ void __launch_bounds__(256) s8_dequantize_rows_kernel(const int8_t* q
     const I i = base + (I)s * (256 * 8);
     if (VEC && i < total && total - i >= 8) raw[s] = *reinterpret_cast<const uint2*>(q + i);
   }
+  chain_release();
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {
     const I i = base + (I)s * (256 * 8);
@@ -422,6 +428,7 @@ __global__ void __launch_bounds__(1024)
   constexpr int K = NV > 0 ? NV : 1;
   __shared__ float sa[2][32];
   __shared__ float sw[NV == 1 ? 8 * 32 * E : 1];
+  chain_wait();
   const int n = p.H, G = blockDim.x, t = threadIdx.x;
   const long long step = (long long)gridDim.x * blockDim.y;
   const T* h0 = static_cast<const T*>(p.h);
@@ -484,6 +491,7 @@ __global__ void __launch_bounds__(1024)
         store_vec<T, W>(static_cast<T*>(p.dx) + m * (long long)n, j, t, G, s, n, Vec<T>::pack(v));
       }
     }
+    chain_release();
     if (NV == 1 && blockDim.y > 1) {   // the CTA's warps, each with rows of its own: added in order
 #pragma unroll
       for (int e = 0; e < E; ++e) {
@@ -556,6 +564,7 @@ __global__ void __launch_bounds__(1024) rms_norm_backward_ring_kernel(const Norm
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ float sa[2][32];
   __shared__ uint64_t full[RING_MAX];
+  chain_wait();
   const int n = p.H, G = blockDim.x, t = threadIdx.x;
   const long long m0 = blockIdx.x, step = gridDim.x;
   const int rows = (int)((p.M - m0 + step - 1) / step);
@@ -652,6 +661,7 @@ __global__ void __launch_bounds__(1024) rms_norm_backward_ring_kernel(const Norm
       store_vec<T, W>(static_cast<T*>(p.dx) + m * (long long)n, j, t, G, s, n, Vec<T>::pack(v));
     }
   }
+  chain_release();
   float* part = p.partials + m0 * n;
 #pragma unroll
   for (int j = 0; j < NV; ++j)
@@ -669,7 +679,7 @@ __global__ void __launch_bounds__(1024) sum_partials_kernel(const float* part, i
                                                             float* out) {
   __shared__ float s[32][33];
   __shared__ float sum[32];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  chain_wait();
   const int rank = split > 1 ? (int)cluster_ctarank() : 0, c0 = blockIdx.x / split * 32;
   const int beg = (int)((long long)count * rank / split), end = (int)((long long)count * (rank + 1) / split);
   const int i = c0 + threadIdx.x;
@@ -683,6 +693,7 @@ __global__ void __launch_bounds__(1024) sum_partials_kernel(const float* part, i
       for (int k = 0; k < 8; ++k) a += v[k];
     }
   }
+  chain_release();
   s[threadIdx.y][threadIdx.x] = a;
   __syncthreads();
   a = s[threadIdx.x][threadIdx.y];   // one column a warp
@@ -740,38 +751,31 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
   const int R = G == 32 ? (many ? 8 : 1) : 1;
   const dim3 block(G, R);
   const unsigned grid = (unsigned)((a.M + R - 1) / R);
-#define QMM_NORM(V)                                                                         \
-  switch (nv) {                                                                             \
-    case 1: rms_norm_s8_kernel<T, V, 1><<<grid, block, 0, s>>>(a); break;                   \
-    case 2: rms_norm_s8_kernel<T, V, 2><<<grid, block, 0, s>>>(a); break;                   \
-    case 4: rms_norm_s8_kernel<T, V, 4><<<grid, block, 0, s>>>(a); break;                   \
-    default: rms_norm_s8_kernel<T, V, 0><<<grid, block, 0, s>>>(a); break;                  \
+#define QMM_NORM(V)                                                                                     \
+  switch (nv) {                                                                                         \
+    case 1: return launch_chained(rms_norm_s8_kernel<T, V, 1>, grid, block, 0, 1, s, a);                \
+    case 2: return launch_chained(rms_norm_s8_kernel<T, V, 2>, grid, block, 0, 1, s, a);                \
+    case 4: return launch_chained(rms_norm_s8_kernel<T, V, 4>, grid, block, 0, 1, s, a);                \
+    default: return launch_chained(rms_norm_s8_kernel<T, V, 0>, grid, block, 0, 1, s, a);               \
   }
-  if (acc == kAligned) {
-    QMM_NORM(kAligned)
-  } else if (acc == kShifted) {
-    QMM_NORM(kShifted)
-  } else {
-    QMM_NORM(kScalar)
-  }
+  if (acc == kAligned) QMM_NORM(kAligned)
+  if (acc == kShifted) QMM_NORM(kShifted)
+  QMM_NORM(kScalar)
 #undef QMM_NORM
-  return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t launch_dequantize(const int8_t* q, const float* scale, long long M, int H, T* y, cudaStream_t s) {
+template <typename T, typename I>
+cudaError_t launch_dequantize_i(const int8_t* q, const float* scale, long long M, int H, T* y, cudaStream_t s) {
   const long long total = M * H;
   const unsigned grid = (unsigned)((total + 8191) / 8192);
   const bool vec = (reinterpret_cast<uintptr_t>(q) % 8) == 0 && (reinterpret_cast<uintptr_t>(y) % 16) == 0;
-  const bool small = total + 8192 < (1ll << 32);
-  if (small) {
-    if (vec) s8_dequantize_rows_kernel<T, uint32_t, true><<<grid, 256, 0, s>>>(q, scale, (uint32_t)total, (uint32_t)H, y);
-    else s8_dequantize_rows_kernel<T, uint32_t, false><<<grid, 256, 0, s>>>(q, scale, (uint32_t)total, (uint32_t)H, y);
-  } else {
-    if (vec) s8_dequantize_rows_kernel<T, uint64_t, true><<<grid, 256, 0, s>>>(q, scale, (uint64_t)total, (uint64_t)H, y);
-    else s8_dequantize_rows_kernel<T, uint64_t, false><<<grid, 256, 0, s>>>(q, scale, (uint64_t)total, (uint64_t)H, y);
-  }
-  return cudaGetLastError();
+  auto kern = vec ? s8_dequantize_rows_kernel<T, I, true> : s8_dequantize_rows_kernel<T, I, false>;
+  return launch_chained(kern, grid, 256, 0, 1, s, q, scale, (I)total, (I)H, y);
+}
+template <typename T>
+cudaError_t launch_dequantize(const int8_t* q, const float* scale, long long M, int H, T* y, cudaStream_t s) {
+  return M * H + 8192 < (1ll << 32) ? launch_dequantize_i<T, uint32_t>(q, scale, M, H, y, s)
+                                    : launch_dequantize_i<T, uint64_t>(q, scale, M, H, y, s);
 }
 
 // Launch shape of the backward pass: vectors a thread, threads a row, rows of a
@@ -812,27 +816,13 @@ BwdShape backward_shape(long long M, int H, bool dh, Access acc) {
   return b;
 }
 
-// dweight from the partials, launched as a programmatic dependent.
+// dweight from the partials.
 cudaError_t launch_sum(const NormBwdArgs& a, int parts, cudaStream_t s) {
   const int groups = (a.H + 31) / 32;
   int split = 1;   // up to 8, while that leaves every thread a load and every SM at most one CTA
   while (split < 8 && parts >= 64 * split && groups * split * 2 <= num_sms()) split *= 2;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)split;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(groups * split));
-  cfg.blockDim = dim3(32, 32);
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = split > 1 ? 2 : 1;
-  const cudaError_t e =
-      cudaLaunchKernelEx(&cfg, sum_partials_kernel, (const float*)a.partials, parts, a.H, split, a.dweight);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return launch_chained(sum_partials_kernel, (unsigned)(groups * split), dim3(32, 32), 0, (unsigned)split, s,
+                        a.partials, parts, a.H, split, a.dweight);
 }
 
 template <typename T, int W, int NV, bool DH>
@@ -847,8 +837,7 @@ cudaError_t launch_ring_nv(const NormBwdArgs& a, const BwdShape& b, int slots, s
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 222 * 1024);
   });
   if (e != cudaSuccess) return e;
-  kern<<<b.parts, b.G, smem, s>>>(a, slots, b.tensors);
-  return cudaGetLastError();
+  return launch_chained(kern, b.parts, b.G, smem, 1, s, a, slots, b.tensors);
 }
 template <typename T, int W, bool DH>
 cudaError_t launch_ring(const NormBwdArgs& a, const BwdShape& b, cudaStream_t s) {
@@ -860,13 +849,12 @@ cudaError_t launch_ring(const NormBwdArgs& a, const BwdShape& b, cudaStream_t s)
 
 // (of aligned tensors only rows of one warp and rows too long come here)
 template <typename T, int W, bool DH>
-void launch_direct(const NormBwdArgs& a, const BwdShape& b, dim3 block, cudaStream_t s) {
+cudaError_t launch_direct(const NormBwdArgs& a, const BwdShape& b, cudaStream_t s) {
   constexpr int NV2 = W == kScalar ? 2 : 0;
-  switch (b.nv) {
-    case 1: rms_norm_backward_kernel<T, W, 1, DH><<<b.parts, block, 0, s>>>(a); break;
-    case 2: rms_norm_backward_kernel<T, W, NV2, DH><<<b.parts, block, 0, s>>>(a); break;
-    default: rms_norm_backward_kernel<T, W, 0, DH><<<b.parts, block, 0, s>>>(a); break;
-  }
+  auto kern = b.nv == 1   ? rms_norm_backward_kernel<T, W, 1, DH>
+              : b.nv == 2 ? rms_norm_backward_kernel<T, W, NV2, DH>
+                          : rms_norm_backward_kernel<T, W, 0, DH>;
+  return launch_chained(kern, b.parts, dim3(b.G, b.R), 0, 1, s, a);
 }
 
 template <typename T, bool DH>
@@ -877,15 +865,13 @@ cudaError_t launch_backward(const NormBwdArgs& a, cudaStream_t s) {
   const Access acc = !like ? kScalar
                      : a.H % E == 0 && (reinterpret_cast<uintptr_t>(a.w) % 16) == 0 ? kAligned : kShifted;
   const BwdShape b = backward_shape<T>(a.M, a.H, DH, acc);
-  const dim3 block(b.G, b.R);
-  if (b.slots > 0) {
-    const cudaError_t e = acc == kAligned ? launch_ring<T, kAligned, DH>(a, b, s) : launch_ring<T, kShifted, DH>(a, b, s);
-    return e != cudaSuccess ? e : launch_sum(a, b.parts, s);
-  }
-  if (acc == kAligned) launch_direct<T, kAligned, DH>(a, b, block, s);
-  else if (acc == kShifted) launch_direct<T, kShifted, DH>(a, b, block, s);
-  else launch_direct<T, kScalar, DH>(a, b, block, s);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e;
+  if (b.slots > 0)
+    e = acc == kAligned ? launch_ring<T, kAligned, DH>(a, b, s) : launch_ring<T, kShifted, DH>(a, b, s);
+  else
+    e = acc == kAligned   ? launch_direct<T, kAligned, DH>(a, b, s)
+        : acc == kShifted ? launch_direct<T, kShifted, DH>(a, b, s)
+                          : launch_direct<T, kScalar, DH>(a, b, s);
   return e != cudaSuccess ? e : launch_sum(a, b.parts, s);
 }
 
