@@ -81,6 +81,25 @@ __device__ __forceinline__ uint8_t block_scale(unsigned max_bits, float u, float
 template <typename T>
 __device__ __forceinline__ float ld1(const T* p) { return (float)*p; }
 
+// Larger of each of two non-negative bf16 (a NaN wins), in one instruction.
+constexpr uint32_t kMag = 0x7fff7fffu;   // magnitudes of two bf16
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// (a * m, b * m), each rounded once, in one instruction.
+__device__ __forceinline__ void mul_pair(float& a, float& b, float m) {
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmul.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(m));
+}
+__device__ __forceinline__ void mul8(float (&v)[8], float m) {
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) mul_pair(v[e], v[e + 1], m);
+}
+
 // Eight consecutive elements as they lie in memory.
 template <typename T>
 struct Raw8;
@@ -110,14 +129,12 @@ struct Raw8<__nv_bfloat16> {
     }
   }
   // bits of the largest magnitude as a float (a NaN is above infinity)
-  __device__ __forceinline__ unsigned max_bits() const {
-    const unsigned a = pair_max(pair_max(r.x, r.y), pair_max(r.z, r.w));
-    return max(a << 16, a & 0x7fff0000u);
+  __device__ __forceinline__ unsigned max_bits() const { return bits(pair()); }
+  // the larger magnitudes of the even and of the odd elements, two bf16
+  __device__ __forceinline__ uint32_t pair() const {
+    return max_pair(max_pair(r.x & kMag, r.y & kMag), max_pair(r.z & kMag, r.w & kMag));
   }
-  static __device__ __forceinline__ uint32_t pair_max(uint32_t a, uint32_t b) {
-    // magnitudes of finite bf16 values, infinities and NaNs are ordered as integers
-    return __vmaxu2(a & 0x7fff7fffu, b & 0x7fff7fffu);
-  }
+  static __device__ __forceinline__ unsigned bits(uint32_t p) { return max(p << 16, p & 0xffff0000u); }
 };
 template <>
 struct Raw8<float> {
@@ -160,23 +177,23 @@ struct Raw16 {
   __device__ __forceinline__ void load_whole(const T* p) {
     *this = *reinterpret_cast<const Raw16<T>*>(p);
   }
-  __device__ __forceinline__ unsigned max_bits() const { return max(lo.max_bits(), hi.max_bits()); }
-  // the block's scale, and the elements' codes, the first in the lowest bits
+  __device__ __forceinline__ unsigned max_bits() const {
+    if constexpr (sizeof(T) == 2) return Raw8<T>::bits(max_pair(lo.pair(), hi.pair()));
+    else return max(lo.max_bits(), hi.max_bits());
+  }
+  // the block's scale, and the elements' codes, the first in the lowest bits; m: max_bits()
   template <int BLOCK>
-  __device__ __forceinline__ uint2 codes(float u, uint8_t& scale) const {
-    unsigned m = max_bits();
+  __device__ __forceinline__ uint2 codes(unsigned m, float u, uint8_t& scale) const {
     if (BLOCK == 32) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     float mul = 0.f, f[8];
     bool zero;
     scale = block_scale<BLOCK>(m, u, mul, zero);
     uint2 c;
     lo.floats(f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(f[e], mul);
+    mul8(f, mul);
     c.x = e2m1x8(f);
     hi.floats(f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(f[e], mul);
+    mul8(f, mul);
     c.y = e2m1x8(f);
     return zero ? make_uint2(0u, 0u) : c;
   }
@@ -300,6 +317,7 @@ __global__ void __launch_bounds__(VEC ? 1024 : 896) quantize_rows_kernel(const F
     }
   };
   float u = 1.f;
+  unsigned vm[ITER];
   if (BLOCK == 16) {
     if (threadIdx.x < 8) rowmax[threadIdx.x] = 0u;
     __syncthreads();
@@ -307,7 +325,10 @@ __global__ void __launch_bounds__(VEC ? 1024 : 896) quantize_rows_kernel(const F
     for (int b = 0; b < batches; ++b) {
       load(b);
 #pragma unroll
-      for (int i = 0; i < ITER; ++i) m = max(m, v[i].max_bits());
+      for (int i = 0; i < ITER; ++i) {
+        vm[i] = v[i].max_bits();
+        m = max(m, vm[i]);
+      }
     }
 #pragma unroll
     for (int o = 1; o < LANES; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -320,11 +341,15 @@ __global__ void __launch_bounds__(VEC ? 1024 : 896) quantize_rows_kernel(const F
   uint8_t* codes = p.out + (size_t)tile * L.kt * 8192 + rin * 16 + half * 8;
   uint8_t* sf = p.out + L.scale_off() + (size_t)tile * L.kt * 512 * ATOMS + c2 * 16;
   for (int b = 0; b < batches; ++b) {
-    if (BLOCK == 32 || batches > 1) load(b);
+    if (BLOCK == 32 || batches > 1) {
+      load(b);
+#pragma unroll
+      for (int i = 0; i < ITER; ++i) vm[i] = v[i].max_bits();
+    }
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
       uint8_t s;
-      const uint2 code = v[i].template codes<BLOCK>(u, s);
+      const uint2 code = v[i].template codes<BLOCK>(vm[i], u, s);
       const int ch = ((b * ITER + i) * nw + warp) * UC + (piece >> 1);
       if (ch < chunks) {
         const int k = ch * SPC + (BLOCK == 16 ? half : 0);
@@ -496,7 +521,7 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const Fp4QuantArgs p
         if (c0 == 0 && (lane & 3) == 0 && rv) reinterpret_cast<float*>(p.out_rows + Lr.row_off())[r0 + rin] = g;
       }
       uint8_t s;
-      const uint2 code = v[i].template codes<BLOCK>(u, s);
+      const uint2 code = v[i].template codes<BLOCK>(v[i].max_bits(), u, s);
       const int ch = k >> 5, ks = ch * SPC + (BLOCK == 16 ? half : 0);
       *reinterpret_cast<uint2*>(codes_r + ch * 2048 + rin * 16 + half * 8) = code;
       if (BLOCK == 16 || half == 0) sf_r[(ks >> 2) * 512 + (rin & 31) * 16 + (rin >> 5) * 4 + (ks & 3)] = s;
@@ -514,11 +539,11 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const Fp4QuantArgs p
 #pragma unroll 8
       for (int e = 0; e < 32; ++e) {
         const uint32_t x = *reinterpret_cast<const uint32_t*>(smem + (ch * 32 + e) * S::PITCH + cw * 4);
-        m = CW == 2 ? __vmaxu2(m, x & 0x7fff7fffu) : max(m, x & 0x7fffffffu);
+        m = CW == 2 ? max_pair(m, x & kMag) : max(m, x & 0x7fffffffu);
       }
       if (CW == 2) {
         atomicMax(&cmax[2 * cw], m << 16);
-        atomicMax(&cmax[2 * cw + 1], m & 0x7fff0000u);
+        atomicMax(&cmax[2 * cw + 1], m & 0xffff0000u);
       } else {
         atomicMax(&cmax[cw], m);
       }
@@ -558,11 +583,11 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const Fp4QuantArgs p
 #pragma unroll
       for (int e = 0; e < BLOCK; ++e) {
         x[e] = *reinterpret_cast<const uint32_t*>(smem + (ch * 32 + b * BLOCK + e) * S::PITCH + cw * 4);
-        m = CW == 2 ? __vmaxu2(m, x[e] & 0x7fff7fffu) : max(m, x[e] & 0x7fffffffu);
+        m = CW == 2 ? max_pair(m, x[e] & kMag) : max(m, x[e] & 0x7fffffffu);
       }
 #pragma unroll
       for (int w = 0; w < CW; ++w) {
-        const unsigned mb = CW == 1 ? m : w == 0 ? m << 16 : m & 0x7fff0000u;
+        const unsigned mb = CW == 1 ? m : w == 0 ? m << 16 : m & 0xffff0000u;
         float mul = 0.f;
         bool zero;
         const uint8_t s = block_scale<BLOCK>(mb, uc[w], mul, zero);
@@ -574,8 +599,9 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const Fp4QuantArgs p
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const uint32_t xe = x[q * 8 + e];
-            f[e] = __fmul_rn(__uint_as_float(CW == 1 ? xe : w == 0 ? xe << 16 : xe & 0xffff0000u), mul);
+            f[e] = __uint_as_float(CW == 1 ? xe : w == 0 ? xe << 16 : xe & 0xffff0000u);
           }
+          mul8(f, mul);
           code[w][b * (BLOCK / 8) + q] = zero ? 0u : e2m1x8(f);
         }
       }

@@ -79,7 +79,9 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return
 //              bytes: all tensors of a row then start equally far past one)
 //   kScalar    (j * E + e) * G + t, element by element (neighbouring threads,
 //              neighbouring elements): tensors aligned unlike each other
-enum Access { kScalar, kAligned, kShifted };
+//   kExact     kAligned where the threads' vectors are the row exactly and the
+//              weight has the rows' type: no bound is checked
+enum Access { kScalar, kAligned, kShifted, kExact };
 template <typename T, int W>
 __device__ __forceinline__ int elem(int j, int e, int t, int G, int s) {
   constexpr int E = Vec<T>::E;
@@ -92,7 +94,7 @@ __device__ __forceinline__ int row_shift(long long m, int n) {
 // Vector j is one access (which may lie past the end of the row).
 template <typename T, int W>
 __device__ __forceinline__ bool whole(int i, int n) {
-  return W == kAligned || (W == kShifted && i >= 0 && i + Vec<T>::E <= n);
+  return W == kAligned || W == kExact || (W == kShifted && i >= 0 && i + Vec<T>::E <= n);
 }
 // Vector j of a row of n elements, as 16 bytes of T; elements past the end are 0.
 template <typename T, int W>
@@ -101,7 +103,7 @@ __device__ __forceinline__ uint4 load_vec(const T* row, int j, int t, int G, int
   uint4 r = make_uint4(0u, 0u, 0u, 0u);
   const int i0 = elem<T, W>(j, 0, t, G, s);
   if (whole<T, W>(i0, n)) {
-    if (i0 < n) r = *reinterpret_cast<const uint4*>(row + i0);
+    if (W == kExact || i0 < n) r = *reinterpret_cast<const uint4*>(row + i0);
   } else if (W == kScalar || i0 < n) {
     uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
@@ -123,7 +125,7 @@ __device__ __forceinline__ void store_vec(T* row, int j, int t, int G, int s, in
   constexpr int E = Vec<T>::E;
   const int i0 = elem<T, W>(j, 0, t, G, s);
   if (whole<T, W>(i0, n)) {
-    if (i0 < n) *reinterpret_cast<uint4*>(row + i0) = r;
+    if (W == kExact || i0 < n) *reinterpret_cast<uint4*>(row + i0) = r;
   } else if (W == kScalar || i0 < n) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -150,7 +152,9 @@ __device__ __forceinline__ uint4 add_vec(const uint4& x, const uint4& r) {
 template <typename T, int W>
 __device__ __forceinline__ void load_w(const void* w, int w_f32, int j, int t, int G, int s, int n, float* v) {
   constexpr int E = Vec<T>::E;
-  if (W == kAligned) {
+  if (W == kExact) {
+    Vec<T>::unpack(__ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(w) + elem<T, W>(j, 0, t, G, s))), v);
+  } else if (W == kAligned) {
     const int i = elem<T, W>(j, 0, t, G, s);
     if (i >= n) {
 #pragma unroll
@@ -248,6 +252,21 @@ __device__ __forceinline__ RowScale row_scale(float ss, unsigned amax_bits, int 
   }
   return r;
 }
+// Two float32 operations in one instruction, each rounded once.
+__device__ __forceinline__ void mul_pair(float& a, float& b, float x, float y) {
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tmul.rn.f32x2 p, p, q;\n\t"
+      "mov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(x), "f"(y));
+}
+// (c, d) += (a * a, b * b)
+__device__ __forceinline__ void square_pair(float a, float b, float& c, float& d) {
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%0, %1};\n\tfma.rn.f32x2 q, p, p, q;\n\t"
+      "mov.b64 {%0, %1}, q;\n\t}"
+      : "+f"(c), "+f"(d)
+      : "f"(a), "f"(b));
+}
+
 // E quantised values as bytes, the first in the lowest. |v * inv| is at most
 // 127 (1 + 2^-23), and adding 1.5 * 2^23 rounds such a value to the nearest
 // integer (ties to even) and leaves it in the low bits of the sum: one addition
@@ -256,10 +275,17 @@ template <int E>
 __device__ __forceinline__ void quantise(const float* v, float inv, bool zero, uint32_t (&o)[E / 4]) {
 #pragma unroll
   for (int q = 0; q < E / 4; ++q) {
-    uint32_t b[4];
+    float b[4];
+    uint32_t i[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) b[e] = __float_as_uint(__fadd_rn(__fmul_rn(v[4 * q + e], inv), 12582912.f));
-    o[q] = zero ? 0u : prmt(prmt(b[0], b[1], 0x0040u), prmt(b[2], b[3], 0x0040u), 0x5410u);
+    for (int e = 0; e < 4; ++e) b[e] = v[4 * q + e];
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) mul_pair(b[e], b[e + 1], inv, inv);
+    // (one by one: paired, the addition would be fused with the product, whose own
+    // rounding the definition has)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) i[e] = __float_as_uint(__fadd_rn(b[e], 12582912.f));
+    o[q] = zero ? 0u : prmt(prmt(i[0], i[1], 0x0040u), prmt(i[2], i[3], 0x0040u), 0x5410u);
   }
 }
 // max(a, |b|) that keeps a NaN
@@ -285,15 +311,15 @@ __global__ void __launch_bounds__(1024) rms_norm_s8_kernel(const NormArgs p) {
   const T* r = p.residual ? static_cast<const T*>(p.residual) + m * p.ldr : nullptr;
   T* ho = p.h ? static_cast<T*>(p.h) + m * (long long)n : nullptr;
   int8_t* q = p.q + m * (long long)n;
-  float ss = 0.f, amax = 0.f;
+  float ss = 0.f, ss2 = 0.f, amax = 0.f;   // the even and the odd elements' squares
   // v = h * w of a vector, and its share of the statistics
   auto stats = [&](const uint4& hr, const float* w, float* v) {
     Vec<T>::unpack(hr, v);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      ss = __fmaf_rn(v[e], v[e], ss);
-      v[e] = __fmul_rn(v[e], w[e]);
-      amax = max_abs(amax, v[e]);
+    for (int e = 0; e < E; e += 2) {
+      square_pair(v[e], v[e + 1], ss, ss2);
+      mul_pair(v[e], v[e + 1], w[e], w[e + 1]);
+      amax = max_abs(max_abs(amax, v[e]), v[e + 1]);
     }
   };
   auto put = [&](int j, const float* v, float inv, bool zero) {
@@ -301,7 +327,7 @@ __global__ void __launch_bounds__(1024) rms_norm_s8_kernel(const NormArgs p) {
     quantise<E>(v, inv, zero, o);
     const int i0 = elem<T, W>(j, 0, t, G, s);
     if (whole<T, W>(i0, n)) {
-      if (i0 >= n) return;
+      if (W != kExact && i0 >= n) return;
       if (E == 8) *reinterpret_cast<uint2*>(q + i0) = make_uint2(o[0], o[E / 4 - 1]);
       else *reinterpret_cast<uint32_t*>(q + i0) = o[0];
     } else {
@@ -333,6 +359,7 @@ __global__ void __launch_bounds__(1024) rms_norm_s8_kernel(const NormArgs p) {
       stats(h[j], w, v[j]);
     }
     unsigned am = __float_as_uint(amax);
+    ss += ss2;
     row_sum_max(ss, am, G, sa, sb);
     const RowScale rs = row_scale(ss, am, n, p.eps);
     chain_release();
@@ -353,6 +380,7 @@ __global__ void __launch_bounds__(1024) rms_norm_s8_kernel(const NormArgs p) {
       stats(h, w, v);
     }
     unsigned am = __float_as_uint(amax);
+    ss += ss2;
     row_sum_max(ss, am, G, sa, sb);
     const RowScale rs = row_scale(ss, am, n, p.eps);
     chain_release();
@@ -596,7 +624,7 @@ __global__ void __launch_bounds__(1024) rms_norm_backward_ring_kernel(const Norm
   auto get = [&](const uint8_t* row, int j) {
     const int i0 = elem<T, W>(j, 0, t, G, s);
     uint4 r = make_uint4(0u, 0u, 0u, 0u);
-    if (i0 < n) r = *reinterpret_cast<const uint4*>(row + (size_t)(j * G + t) * 16);
+    if (W == kExact || i0 < n) r = *reinterpret_cast<const uint4*>(row + (size_t)(j * G + t) * 16);
     if (W == kShifted && i0 < n && !whole<T, W>(i0, n)) {
       float f[E];
       Vec<T>::unpack(r, f);
@@ -758,6 +786,7 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
     case 4: return launch_chained(rms_norm_s8_kernel<T, V, 4>, grid, block, 0, 1, s, a);                \
     default: return launch_chained(rms_norm_s8_kernel<T, V, 0>, grid, block, 0, 1, s, a);               \
   }
+  if (acc == kAligned && nv > 0 && nv * G * E == a.H && (a.w_f32 != 0) == (sizeof(T) == 4)) QMM_NORM(kExact)
   if (acc == kAligned) QMM_NORM(kAligned)
   if (acc == kShifted) QMM_NORM(kShifted)
   QMM_NORM(kScalar)
@@ -867,7 +896,9 @@ cudaError_t launch_backward(const NormBwdArgs& a, cudaStream_t s) {
   const BwdShape b = backward_shape<T>(a.M, a.H, DH, acc);
   cudaError_t e;
   if (b.slots > 0)
-    e = acc == kAligned ? launch_ring<T, kAligned, DH>(a, b, s) : launch_ring<T, kShifted, DH>(a, b, s);
+    e = acc == kShifted ? launch_ring<T, kShifted, DH>(a, b, s)
+        : b.nv * b.G * E == a.H && (a.w_f32 != 0) == (sizeof(T) == 4) ? launch_ring<T, kExact, DH>(a, b, s)
+                                                                       : launch_ring<T, kAligned, DH>(a, b, s);
   else
     e = acc == kAligned   ? launch_direct<T, kAligned, DH>(a, b, s)
         : acc == kShifted ? launch_direct<T, kShifted, DH>(a, b, s)
