@@ -207,45 +207,60 @@ struct RowStage {
   static constexpr int BYTES = ROWS * PITCH * (int)sizeof(T);
 };
 
+template <int J>
+struct ScaleWord;   // J scale words of four
+template <>
+struct ScaleWord<4> { using type = uint4; };
+template <>
+struct ScaleWord<2> { using type = uint2; };
+template <>
+struct ScaleWord<1> { using type = uint32_t; };
+
 // ---------------------------------------------------------------------------
-// Along the rows. A CTA takes the rows {2c, 2c + 1} + {0, 32, 64, 96} of a tile
-// (J = 4: a warp step is 64 columns of eight rows, 16 columns a lane) or, for
-// matrices of up to 32 rows, {2c, 2c + 1} (J = 1: 256 columns of two rows). Rows
-// chosen so make every 32-byte sector of codes (two neighbouring rows' 16 bytes)
-// and of scales (two rows' 16-byte lines of an atom, whose 4-byte parts are rows
-// 32 apart) the work of one CTA. A warp's steps of a batch (ITER) are loaded
+// Along the rows. A CTA takes the rows {2c, 2c + 1} + 32 j of a tile, all four j
+// (J = 4: a warp step is 64 columns of eight rows, 16 columns a lane), two of them
+// (J = 2: 128 columns of four rows) or, for matrices of up to 32 rows, one (J = 1:
+// 256 columns of two rows). Rows chosen so make every 32-byte sector of codes (two
+// neighbouring rows' 16 bytes) the work of one CTA, and of scales (two rows'
+// 16-byte lines of an atom, whose 4-byte parts are rows 32 apart) of one or two.
+// Block 32 takes a segment of the columns a CTA (blockIdx.y). A warp's steps of a batch (ITER) are loaded
 // together; with block 16 a row whose steps are one batch stays in registers
 // between its maximum and its codes, longer rows are read again.
 // ---------------------------------------------------------------------------
 template <typename T, int BLOCK, int J, int ITER, bool VEC>
 __global__ void __launch_bounds__(VEC ? 1024 : 896) quantize_rows_kernel(const Fp4QuantArgs p, const int staged,
                                                                                 const int whole) {
-  constexpr int WROWS = J == 4 ? 8 : 2, WCOLS = J == 4 ? 64 : 256;   // a warp step
-  const int nw = blockDim.x >> 5;
-  chain_wait();
+  constexpr int WROWS = 2 * J, WCOLS = 512 / WROWS;   // a warp step
   constexpr int ATOMS = BLOCK == 16 ? 2 : 1;
-  constexpr int SPC = 32 / BLOCK;      // scales per 32-column chunk
-  constexpr int LANES = J == 4 ? 4 : 16;   // lanes a row
-  constexpr int UC = LANES / 2;        // chunks a warp step
+  constexpr int SPC = 32 / BLOCK;          // scales per 32-column chunk
+  constexpr int LANES = 32 / WROWS;        // lanes a row
+  constexpr int UC = LANES / 2;            // chunks a warp step
   __shared__ unsigned rowmax[8];
+  const int nw = blockDim.x >> 5;
   // rows that no vector load can take: all of the CTA's rows (whole > 0: elements
-  // between them), or a buffer a warp; then the scales (staged), [atom][2 rows][4
+  // between them), or a buffer a warp; then the scales (staged), [atom][2 rows][J
   // rows 32 apart][4]
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* sfs = smem + (VEC ? 0 : whole ? WROWS * whole * (int)sizeof(T) : nw * RowStage<T, WROWS, WCOLS>::BYTES);
+  chain_wait();
   const Fp4Layout L(p.rows, p.cols, BLOCK);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tile = blockIdx.x >> 4, c2 = 2 * (blockIdx.x & 15);
-  const int ra = J == 4 ? (lane >> 2) & 1 : lane >> 4, rj = J == 4 ? lane >> 3 : 0;
+  constexpr int PER_TILE = J == 2 ? 32 : 16;
+  const int tile = blockIdx.x / PER_TILE, in_tile = blockIdx.x % PER_TILE;
+  const int c2 = 2 * (in_tile & 15), j0 = J == 2 ? 2 * (in_tile >> 4) : 0;
+  const int ri = lane / LANES, ra = ri & 1, rj = ri >> 1;
   const int piece = lane & (LANES - 1), half = piece & 1;
-  const int rin = c2 + ra + 32 * rj;
-  const long long row = (long long)tile * 128 + rin;
-  if ((long long)tile * 128 + c2 >= p.rows) return;
+  const int rin = c2 + ra + 32 * (j0 + rj);
+  const long long row = (long long)tile * 128 + rin, row_first = (long long)tile * 128 + c2 + 32 * j0;
+  if (row_first >= p.rows) return;
   const bool rv = row < p.rows;
   const T* x = static_cast<const T*>(p.x) + (rv ? row : 0) * p.ld;
   const int n = rv ? (int)p.cols : 0;
-  const int chunks = (int)L.kt * 4, units = (chunks + UC - 1) / UC;
-  const int batches = (units + nw * ITER - 1) / (nw * ITER);
+  const int chunks = (int)L.kt * 4, units_all = (chunks + UC - 1) / UC;
+  // this CTA's steps: all, or (block 32) as many as its warps take in one batch
+  const int u0 = BLOCK == 32 && gridDim.y > 1 ? blockIdx.y * nw * ITER : 0;
+  const int units = BLOCK == 32 && gridDim.y > 1 ? min(units_all, u0 + nw * ITER) : units_all;
+  const int batches = (units - u0 + nw * ITER - 1) / (nw * ITER);
   if (!VEC && whole) {
     T* all = reinterpret_cast<T*>(smem);
     constexpr int CB = 16 / WROWS;   // 16 loads in flight: all rows, CB columns apart
@@ -253,7 +268,7 @@ __global__ void __launch_bounds__(VEC ? 1024 : 896) quantize_rows_kernel(const F
     int m[WROWS];
 #pragma unroll
     for (int r = 0; r < WROWS; ++r) {
-      const long long rr = (long long)tile * 128 + c2 + (r & 1) + 32 * (r >> 1);
+      const long long rr = row_first + (r & 1) + 32 * (r >> 1);
       xr[r] = static_cast<const T*>(p.x) + (rr < p.rows ? rr : 0) * p.ld;
       m[r] = rr < p.rows ? (int)p.cols : 0;
     }
@@ -280,7 +295,7 @@ __global__ void __launch_bounds__(VEC ? 1024 : 896) quantize_rows_kernel(const F
   Raw16<T> v[ITER];
   auto load = [&](int b) {
     if (!VEC && whole) {
-      const T* all = reinterpret_cast<const T*>(smem) + (J == 4 ? rj * 2 + ra : ra) * whole + piece * 16;
+      const T* all = reinterpret_cast<const T*>(smem) + ri * whole + piece * 16;
 #pragma unroll
       for (int i = 0; i < ITER; ++i) {
         const int un = (b * ITER + i) * nw + warp;
@@ -289,14 +304,14 @@ __global__ void __launch_bounds__(VEC ? 1024 : 896) quantize_rows_kernel(const F
       }
       return;
     }
-    if (VEC && (long long)(b + 1) * ITER * nw * WCOLS <= p.cols) {   // the whole batch lies inside
+    if (VEC && (long long)(u0 + (b + 1) * ITER * nw) * WCOLS <= p.cols) {   // the whole batch lies inside
 #pragma unroll
-      for (int i = 0; i < ITER; ++i) v[i].load_whole(x + ((b * ITER + i) * nw + warp) * WCOLS + piece * 16);
+      for (int i = 0; i < ITER; ++i) v[i].load_whole(x + (u0 + (b * ITER + i) * nw + warp) * WCOLS + piece * 16);
       return;
     }
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {   // past the end: columns past n, zeros
-      const long long k0 = (long long)((b * ITER + i) * nw + warp) * WCOLS;
+      const long long k0 = (long long)(u0 + (b * ITER + i) * nw + warp) * WCOLS;
       if (VEC) {
         v[i].load(x, k0 + piece * 16, n, true);
       } else {
@@ -305,14 +320,14 @@ __global__ void __launch_bounds__(VEC ? 1024 : 896) quantize_rows_kernel(const F
         __syncwarp();
 #pragma unroll
         for (int r = 0; r < WROWS; ++r) {
-          const long long rr = (long long)tile * 128 + c2 + (r & 1) + 32 * (r >> 1);
+          const long long rr = row_first + (r & 1) + 32 * (r >> 1);
           const T* xr = static_cast<const T*>(p.x) + (rr < p.rows ? rr : 0) * p.ld;
 #pragma unroll
           for (int c = lane; c < WCOLS; c += 32)
             buf[r * S::PITCH + c] = rr < p.rows && k0 + c < p.cols ? xr[k0 + c] : (T)0.f;
         }
         __syncwarp();
-        v[i] = *reinterpret_cast<const Raw16<T>*>(buf + (J == 4 ? rj * 2 + ra : ra) * S::PITCH + piece * 16);
+        v[i] = *reinterpret_cast<const Raw16<T>*>(buf + ri * S::PITCH + piece * 16);
       }
     }
   };
@@ -332,14 +347,15 @@ __global__ void __launch_bounds__(VEC ? 1024 : 896) quantize_rows_kernel(const F
     }
 #pragma unroll
     for (int o = 1; o < LANES; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (piece == 0) atomicMax(&rowmax[rj * 2 + ra], m);
+    if (piece == 0) atomicMax(&rowmax[ri], m);
     __syncthreads();
-    const float g = row_scale(rowmax[rj * 2 + ra]);
+    const float g = row_scale(rowmax[ri]);
     u = __fdiv_rn(1.f, g);
     if (warp == 0 && piece == 0 && rv) reinterpret_cast<float*>(p.out + L.row_off())[row] = g;
   }
   uint8_t* codes = p.out + (size_t)tile * L.kt * 8192 + rin * 16 + half * 8;
-  uint8_t* sf = p.out + L.scale_off() + (size_t)tile * L.kt * 512 * ATOMS + c2 * 16;
+  uint8_t* sf = p.out + L.scale_off() + (size_t)tile * L.kt * 512 * ATOMS + c2 * 16 + j0 * 4;
+  const int atom0 = u0 * UC * SPC / 4;   // the segment's first atom
   for (int b = 0; b < batches; ++b) {
     if (BLOCK == 32 || batches > 1) {
       load(b);
@@ -350,22 +366,24 @@ __global__ void __launch_bounds__(VEC ? 1024 : 896) quantize_rows_kernel(const F
     for (int i = 0; i < ITER; ++i) {
       uint8_t s;
       const uint2 code = v[i].template codes<BLOCK>(vm[i], u, s);
-      const int ch = ((b * ITER + i) * nw + warp) * UC + (piece >> 1);
+      const int ch = (u0 + (b * ITER + i) * nw + warp) * UC + (piece >> 1);
       if (ch < chunks) {
         const int k = ch * SPC + (BLOCK == 16 ? half : 0);
-        const int off = ra * 16 + rj * 4 + (k & 3);
         const bool mine = BLOCK == 16 || half == 0;
         if (rv) *reinterpret_cast<uint2*>(codes + (size_t)ch * 2048) = code;
-        if (mine && staged) sfs[(k >> 2) * 32 + off] = s;
-        if (mine && !staged && rv) sf[(size_t)(k >> 2) * 512 + off] = s;
+        if (mine && staged) sfs[((k >> 2) - atom0) * (8 * J) + ra * 4 * J + rj * 4 + (k & 3)] = s;
+        if (mine && !staged && rv) sf[(size_t)(k >> 2) * 512 + ra * 16 + rj * 4 + (k & 3)] = s;
       }
     }
   }
   chain_release();
-  if (staged) {
+  if (staged) {   // a row's J scale words of an atom at a time
     __syncthreads();
-    for (int i = threadIdx.x; i < (int)L.kt * ATOMS * 2; i += blockDim.x)
-      *reinterpret_cast<uint4*>(sf + (size_t)(i >> 1) * 512 + (i & 1) * 16) = reinterpret_cast<const uint4*>(sfs)[i];
+    using Word = typename ScaleWord<J>::type;
+    const int atoms = (min(chunks, units * UC) * SPC + 3) / 4 - atom0;
+    for (int i = threadIdx.x; i < atoms * 2; i += blockDim.x)
+      *reinterpret_cast<Word*>(sf + (size_t)(atom0 + (i >> 1)) * 512 + (i & 1) * 16) =
+          reinterpret_cast<const Word*>(sfs)[i];
   }
 }
 
@@ -387,29 +405,27 @@ __global__ void __launch_bounds__(256) absmax_kernel(const Fp4QuantArgs p, unsig
   // rows past the end read the last one again: no maximum changes
   const T* x = static_cast<const T*>(p.x);
   if (p.vec && c + 256 <= p.cols) {
-    unsigned m[8] = {};
+    constexpr int CW = 4 / sizeof(T), NWORD = 8 / CW;   // 32-bit words of a lane's eight columns
+    uint32_t m[NWORD] = {};
     Raw8<T> v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       v[i] = *reinterpret_cast<const Raw8<T>*>(x + min(r0 + 8 * i, p.rows - 1) * p.ld + c + lane * 8);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float f[8];
-      v[i].floats(f);
-      unsigned rm = 0u;
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(&v[i]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const unsigned b = __float_as_uint(f[e]) & 0x7fffffffu;
-        m[e] = max(m[e], b);
-        rm = max(rm, b);
-      }
+      for (int e = 0; e < NWORD; ++e) m[e] = CW == 2 ? max_pair(m[e], w[e] & kMag) : max(m[e], w[e] & 0x7fffffffu);
       if (rowmax) {
-        rm = __reduce_max_sync(0xffffffffu, rm);
+        const unsigned rm = __reduce_max_sync(0xffffffffu, v[i].max_bits());
         if (lane == 0 && r0 + 8 * i < p.rows) atomicMax(rowmax + r0 + 8 * i, rm);
       }
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) atomicMax(&cm[lane * 8 + e], m[e]);
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t w = m[e / CW];
+      atomicMax(&cm[lane * 8 + e], CW == 1 ? w : (e & 1) ? w & 0xffff0000u : w << 16);
+    }
   } else {   // neighbouring lanes, neighbouring columns (past the end the last one again)
     unsigned m[8] = {};
     T v[8][8];
@@ -443,15 +459,15 @@ __global__ void __launch_bounds__(256) absmax_kernel(const Fp4QuantArgs p, unsig
 
 // One tile of 128 x 128 of x a CTA: its rows are quantised as they are loaded
 // (ROWS), all of it goes to shared memory, and its columns are quantised from
-// there. Codes and scales leave as whole tiles by bulk copies. CLUSTER (block 16,
+// there. The columns' codes and all scales leave as whole tiles by bulk copies. CLUSTER (block 16,
 // x of up to 8 tiles down): the tiles above each other are one cluster, and the
 // columns' maxima are taken over it -- one launch in place of a fill, a pass for
 // the maxima and this.
 template <typename T>
 struct TileSmem {
   static constexpr int PITCH = 128 * (int)sizeof(T) + 16;   // bytes; 16 more keep row accesses off each other's banks
-  static constexpr int CODES = 128 * PITCH;                 // two tiles of codes, then of scales
-  static constexpr int SCALES = CODES + 2 * 8192;
+  static constexpr int CODES = 128 * PITCH;                 // the columns' codes, then two tiles of scales
+  static constexpr int SCALES = CODES + 8192;
   static constexpr int BYTES = SCALES + 2 * 1024;
 };
 
@@ -464,7 +480,6 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const Fp4QuantArgs p
   constexpr int CW = 4 / sizeof(T);   // columns in a 32-bit word
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* codes_c = smem + S::CODES;
-  uint8_t* codes_r = codes_c + 8192;
   uint8_t* sf_c = smem + S::SCALES;
   uint8_t* sf_r = sf_c + 1024;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -523,7 +538,8 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const Fp4QuantArgs p
       uint8_t s;
       const uint2 code = v[i].template codes<BLOCK>(v[i].max_bits(), u, s);
       const int ch = k >> 5, ks = ch * SPC + (BLOCK == 16 ? half : 0);
-      *reinterpret_cast<uint2*>(codes_r + ch * 2048 + rin * 16 + half * 8) = code;
+      // (8 rows of a chunk: 128 bytes of the packed tile)
+      *reinterpret_cast<uint2*>(p.out_rows + ti * 8192 + ch * 2048 + rin * 16 + half * 8) = code;
       if (BLOCK == 16 || half == 0) sf_r[(ks >> 2) * 512 + (rin & 31) * 16 + (rin >> 5) * 4 + (ks & 3)] = s;
     }
   }
@@ -618,7 +634,6 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const Fp4QuantArgs p
     bulk_store(p.out + tc * 8192, smem_u32(codes_c), 8192);
     bulk_store(p.out + Lc.scale_off() + tc * (512 * ATOMS), smem_u32(sf_c), 512 * ATOMS);
     if (ROWS) {
-      bulk_store(p.out_rows + ti * 8192, smem_u32(codes_r), 8192);
       bulk_store(p.out_rows + Lr.scale_off() + ti * (512 * ATOMS), smem_u32(sf_r), 512 * ATOMS);
     }
     bulk_commit();
@@ -713,19 +728,19 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* packed, 
   }
 }
 
-// Steps a warp loads together and warps a CTA: about 16 warps, four steps of
-// bf16 or two of float32 at most (the registers of 1024 threads).
+// Steps a warp loads together and warps a CTA. Block 16: as few CTAs' rows as fill
+// the registers of one batch, four steps of bf16 or two of float32 (64 registers a
+// thread); block 32: four warps of them, the columns over as many CTAs as it takes.
 template <typename T, int BLOCK, int J>
 cudaError_t launch_rows_j(const Fp4QuantArgs& a, cudaStream_t s) {
+  constexpr int WROWS = 2 * J, WCOLS = 512 / WROWS, MOST = sizeof(T) == 2 ? 4 : 2;
   const Fp4Layout L(a.rows, a.cols, BLOCK);
-  const long long units = J == 4 ? L.kt * 2 : (L.kt + 1) / 2;
-  constexpr int MOST = sizeof(T) == 2 ? 4 : 2;
-  const unsigned grid = (unsigned)(L.rt * 16);
-  size_t smem = (size_t)L.kt * L.atoms() * 32;
+  const long long units = (L.kt * 128 + WCOLS - 1) / WCOLS;
+  const unsigned grid = (unsigned)(L.rt * (J == 2 ? 32 : 16));
+  size_t smem = (size_t)L.kt * L.atoms() * 8 * J;
   int staged = smem <= (a.vec ? 40 : 16) * 1024;
   if (!staged) smem = 0;
   if (!a.vec) {
-    constexpr int WROWS = J == 4 ? 8 : 2, WCOLS = J == 4 ? 64 : 256;
     auto kern = quantize_rows_kernel<T, BLOCK, J, 2, false>;
     static std::once_flag once[64];
     int dev = 0;
@@ -746,17 +761,25 @@ cudaError_t launch_rows_j(const Fp4QuantArgs& a, cudaStream_t s) {
     return launch_chained(kern, grid, nw * 32, smem + (size_t)nw * RowStage<T, WROWS, WCOLS>::BYTES, 1, s, a, staged, 0);
   }
   int iter = 1;
-  while (iter < MOST && units > 16 * iter) iter *= 2;
-  const int nw = (int)std::min<long long>(32, std::max<long long>(4, (units + iter - 1) / iter));
+  while (iter < MOST && units > (BLOCK == 32 ? 4 : 8) * iter) iter *= 2;
+  int nw = (int)std::min<long long>(32, std::max<long long>(4, (units + iter - 1) / iter));
+  unsigned segments = 1;
+  if (BLOCK == 32 && units > 4 * iter) {
+    nw = 4;
+    segments = (unsigned)((units + 4 * iter - 1) / (4 * iter));
+    smem = (size_t)(4 * iter * WCOLS / 128) * 8 * J;
+    staged = 1;
+  }
   auto kern = iter == 1   ? quantize_rows_kernel<T, BLOCK, J, 1, true>
               : iter == 2 ? quantize_rows_kernel<T, BLOCK, J, 2, true>
                           : quantize_rows_kernel<T, BLOCK, J, MOST, true>;
-  return launch_chained(kern, grid, nw * 32, smem, 1, s, a, staged, 0);
+  return launch_chained(kern, dim3(grid, segments), nw * 32, smem, 1, s, a, staged, 0);
 }
 
 template <typename T, int BLOCK>
 cudaError_t launch_rows(const Fp4QuantArgs& a, cudaStream_t s) {
-  return a.rows <= 32 ? launch_rows_j<T, BLOCK, 1>(a, s) : launch_rows_j<T, BLOCK, 4>(a, s);
+  if (a.rows <= 32) return launch_rows_j<T, BLOCK, 1>(a, s);
+  return BLOCK == 16 ? launch_rows_j<T, BLOCK, 2>(a, s) : launch_rows_j<T, BLOCK, 4>(a, s);
 }
 
 template <typename T, int BLOCK, bool ROWS, bool CLUSTER>
