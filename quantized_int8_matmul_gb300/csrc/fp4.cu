@@ -387,14 +387,26 @@ __global__ void __launch_bounds__(VEC ? 1024 : 896) quantize_rows_kernel(const F
   }
 }
 
+// a[0 .. na) and b[0 .. n - na) to zero, before the maxima: two fills of the
+// library's took 2 us longer, as they do not start on the heels of what precedes them.
+__global__ void __launch_bounds__(256) zero_kernel(unsigned* a, int na, unsigned* b, int n) {
+  chain_wait();
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i < na) a[i] = 0u;
+  else if (i < n) b[i - na] = 0u;
+  chain_release();
+}
+
+
 // ---------------------------------------------------------------------------
 // Along the columns, or both ways: x is [rows][cols] in memory; the packed
 // matrix along the columns is its transpose [cols][rows].
 // ---------------------------------------------------------------------------
 // Largest magnitudes of the columns (and the rows) into the packed buffers' max
 // words: 64 rows x 256 columns a CTA, eight columns a lane.
-template <typename T>
-__global__ void __launch_bounds__(256) absmax_kernel(const Fp4QuantArgs p, unsigned* colmax, unsigned* rowmax) {
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256, VEC ? 4 : 2) absmax_kernel(const Fp4QuantArgs p, unsigned* colmax,
+                                                                  unsigned* rowmax) {
   __shared__ unsigned cm[256];
   chain_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -404,21 +416,25 @@ __global__ void __launch_bounds__(256) absmax_kernel(const Fp4QuantArgs p, unsig
   __syncthreads();
   // rows past the end read the last one again: no maximum changes
   const T* x = static_cast<const T*>(p.x);
-  if (p.vec && c + 256 <= p.cols) {
+  if (VEC && c + 256 <= p.cols) {
     constexpr int CW = 4 / sizeof(T), NWORD = 8 / CW;   // 32-bit words of a lane's eight columns
+    constexpr int NB = 16 / (int)sizeof(T);               // rows in flight
     uint32_t m[NWORD] = {};
-    Raw8<T> v[8];
+#pragma unroll 1
+    for (int i0 = 0; i0 < 8; i0 += NB) {
+      Raw8<T> v[NB];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      v[i] = *reinterpret_cast<const Raw8<T>*>(x + min(r0 + 8 * i, p.rows - 1) * p.ld + c + lane * 8);
+      for (int i = 0; i < NB; ++i)
+        v[i] = *reinterpret_cast<const Raw8<T>*>(x + min(r0 + 8 * (i0 + i), p.rows - 1) * p.ld + c + lane * 8);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(&v[i]);
+      for (int i = 0; i < NB; ++i) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&v[i]);
 #pragma unroll
-      for (int e = 0; e < NWORD; ++e) m[e] = CW == 2 ? max_pair(m[e], w[e] & kMag) : max(m[e], w[e] & 0x7fffffffu);
-      if (rowmax) {
-        const unsigned rm = __reduce_max_sync(0xffffffffu, v[i].max_bits());
-        if (lane == 0 && r0 + 8 * i < p.rows) atomicMax(rowmax + r0 + 8 * i, rm);
+        for (int e = 0; e < NWORD; ++e) m[e] = CW == 2 ? max_pair(m[e], w[e] & kMag) : max(m[e], w[e] & 0x7fffffffu);
+        if (rowmax) {
+          const unsigned rm = __reduce_max_sync(0xffffffffu, v[i].max_bits());
+          if (lane == 0 && r0 + 8 * (i0 + i) < p.rows) atomicMax(rowmax + r0 + 8 * (i0 + i), rm);
+        }
       }
     }
 #pragma unroll
@@ -428,25 +444,29 @@ __global__ void __launch_bounds__(256) absmax_kernel(const Fp4QuantArgs p, unsig
     }
   } else {   // neighbouring lanes, neighbouring columns (past the end the last one again)
     unsigned m[8] = {};
-    T v[8][8];
+    constexpr int NB = VEC ? 2 : 8;   // (VEC: the last columns alone)
+#pragma unroll 1
+    for (int i0 = 0; i0 < 8; i0 += NB) {
+      T v[NB][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const T* row = x + min(r0 + 8 * i, p.rows - 1) * p.ld;
+      for (int i = 0; i < NB; ++i) {
+        const T* row = x + min(r0 + 8 * (i0 + i), p.rows - 1) * p.ld;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = row[min(c + e * 32 + lane, p.cols - 1)];
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      unsigned rm = 0u;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const unsigned b = __float_as_uint((float)v[i][e]) & 0x7fffffffu;
-        m[e] = max(m[e], b);
-        rm = max(rm, b);
+        for (int e = 0; e < 8; ++e) v[i][e] = row[min(c + e * 32 + lane, p.cols - 1)];
       }
-      if (rowmax) {
-        rm = __reduce_max_sync(0xffffffffu, rm);
-        if (lane == 0 && r0 + 8 * i < p.rows) atomicMax(rowmax + r0 + 8 * i, rm);
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        unsigned rm = 0u;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const unsigned b = __float_as_uint((float)v[i][e]) & 0x7fffffffu;
+          m[e] = max(m[e], b);
+          rm = max(rm, b);
+        }
+        if (rowmax) {
+          rm = __reduce_max_sync(0xffffffffu, rm);
+          if (lane == 0 && r0 + 8 * (i0 + i) < p.rows) atomicMax(rowmax + r0 + 8 * (i0 + i), rm);
+        }
       }
     }
 #pragma unroll
@@ -459,27 +479,25 @@ __global__ void __launch_bounds__(256) absmax_kernel(const Fp4QuantArgs p, unsig
 
 // One tile of 128 x 128 of x a CTA: its rows are quantised as they are loaded
 // (ROWS), all of it goes to shared memory, and its columns are quantised from
-// there. The columns' codes and all scales leave as whole tiles by bulk copies. CLUSTER (block 16,
+// there. The scales leave as whole tiles by bulk copies. CLUSTER (block 16,
 // x of up to 8 tiles down): the tiles above each other are one cluster, and the
 // columns' maxima are taken over it -- one launch in place of a fill, a pass for
 // the maxima and this.
 template <typename T>
 struct TileSmem {
   static constexpr int PITCH = 128 * (int)sizeof(T) + 16;   // bytes; 16 more keep row accesses off each other's banks
-  static constexpr int CODES = 128 * PITCH;                 // the columns' codes, then two tiles of scales
-  static constexpr int SCALES = CODES + 8192;
+  static constexpr int SCALES = 128 * PITCH;                // two tiles of scales
   static constexpr int BYTES = SCALES + 2 * 1024;
 };
 
 template <typename T, int BLOCK, bool ROWS, bool CLUSTER>
-__global__ void __launch_bounds__(256) quantize_tile_kernel(const Fp4QuantArgs p) {
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 5 : 3) quantize_tile_kernel(const Fp4QuantArgs p) {
   chain_wait();
   using S = TileSmem<T>;
   constexpr int ATOMS = BLOCK == 16 ? 2 : 1;
   constexpr int SPC = 32 / BLOCK;
   constexpr int CW = 4 / sizeof(T);   // columns in a 32-bit word
   extern __shared__ __align__(128) uint8_t smem[];
-  uint8_t* codes_c = smem + S::CODES;
   uint8_t* sf_c = smem + S::SCALES;
   uint8_t* sf_r = sf_c + 1024;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -576,6 +594,7 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const Fp4QuantArgs p
     }
     cluster_sync_all();   // (the others have read cmax)
   }
+  const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;   // (16-byte alignment is all that is asked)
   // a work item: 32 rows of the column(s) in one 32-bit word
 #pragma unroll 1
   for (int item = t; item < 4 * 128 / CW; item += 256) {
@@ -622,16 +641,22 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const Fp4QuantArgs p
         }
       }
     }
+    uint8_t* d = p.out + tc * 8192 + ch * 2048 + cw * CW * 16;
+    if (CW == 2 && wide) {   // two columns' codes as one store
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d), "r"(code[0][0]),
+                   "r"(code[0][1]), "r"(code[0][2]), "r"(code[0][3]), "r"(code[CW - 1][0]), "r"(code[CW - 1][1]),
+                   "r"(code[CW - 1][2]), "r"(code[CW - 1][3])
+                   : "memory");
+    } else {
 #pragma unroll
-    for (int w = 0; w < CW; ++w)
-      *reinterpret_cast<uint4*>(codes_c + ch * 2048 + (cw * CW + w) * 16) =
-          make_uint4(code[w][0], code[w][1], code[w][2], code[w][3]);
+      for (int w = 0; w < CW; ++w)
+        reinterpret_cast<uint4*>(d)[w] = make_uint4(code[w][0], code[w][1], code[w][2], code[w][3]);
+    }
   }
   chain_release();
   fence_proxy_async_smem();   // this thread's writes, visible to the copy engine
   __syncthreads();
   if (t == 0) {
-    bulk_store(p.out + tc * 8192, smem_u32(codes_c), 8192);
     bulk_store(p.out + Lc.scale_off() + tc * (512 * ATOMS), smem_u32(sf_c), 512 * ATOMS);
     if (ROWS) {
       bulk_store(p.out_rows + Lr.scale_off() + ti * (512 * ATOMS), smem_u32(sf_r), 512 * ATOMS);
@@ -818,11 +843,12 @@ cudaError_t launch_tiles(const Fp4QuantArgs& a, cudaStream_t s) {
   if (BLOCK == 16) {
     unsigned* cm = reinterpret_cast<unsigned*>(a.out + Lc.max_off());
     unsigned* rm = a.out_rows ? reinterpret_cast<unsigned*>(a.out_rows + Lr.max_off()) : nullptr;
-    cudaError_t e = cudaMemsetAsync(cm, 0, (size_t)Lc.rt * 512, s);
-    if (e == cudaSuccess && rm) e = cudaMemsetAsync(rm, 0, (size_t)Lr.rt * 512, s);
+    const int words = (int)(Lc.rt * 128 + (rm ? Lr.rt * 128 : 0));
+    cudaError_t e = launch_chained(zero_kernel, (unsigned)((words + 255) / 256), 256, 0, 1, s, cm, (int)(Lc.rt * 128),
+                                   rm, words);
     if (e != cudaSuccess) return e;
     const long long ctas = ((a.cols + 255) / 256) * ((a.rows + 63) / 64);
-    e = launch_chained(absmax_kernel<T>, (unsigned)ctas, 256, 0, 1, s, a, cm, rm);
+    e = launch_chained(a.vec ? absmax_kernel<T, true> : absmax_kernel<T, false>, (unsigned)ctas, 256, 0, 1, s, a, cm, rm);
     if (e != cudaSuccess) return e;
   }
   return a.out_rows ? launch_tile<T, BLOCK, true, false>(a, grid, 1, s)

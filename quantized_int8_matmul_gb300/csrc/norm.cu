@@ -259,6 +259,19 @@ __device__ __forceinline__ void mul_pair(float& a, float& b, float x, float y) {
       : "+f"(a), "+f"(b)
       : "f"(x), "f"(y));
 }
+__device__ __forceinline__ void add_pair(float& a, float& b, float x, float y) {
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tadd.rn.f32x2 p, p, q;\n\t"
+      "mov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(x), "f"(y));
+}
+// (a, b) += (x * z, y * w)
+__device__ __forceinline__ void fma_pair(float& a, float& b, float x, float y, float z, float w) {
+  asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmov.b64 r, {%0, %1};\n\t"
+      "fma.rn.f32x2 r, p, q, r;\n\tmov.b64 {%0, %1}, r;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(x), "f"(y), "f"(z), "f"(w));
+}
 // (c, d) += (a * a, b * b)
 __device__ __forceinline__ void square_pair(float a, float b, float& c, float& d) {
   asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%0, %1};\n\tfma.rn.f32x2 q, p, p, q;\n\t"
@@ -581,16 +594,41 @@ __global__ void __launch_bounds__(1024)
 // The same for rows that come by bulk copies: a ring of `slots` rows (h, dy and dh
 // each in 16-byte lines; of rows too long for two slots of all three, h and dy) in
 // shared memory, refilled once a row's reduction has passed, so that the next rows
-// are on their way through the whole of this one's work. Waits are bounded (common.cuh).
+// are on their way through the whole of this one's work. Rows of one vector a
+// thread go in pairs (RB = 2): one barrier and one reduction for both. Waits are
+// bounded (common.cuh).
 constexpr int RING_MAX = 8;
 constexpr unsigned SITE_ROW = 0x520;
-template <typename T, int W, int NV, bool DH>
+
+// sums of RB values over the CTA's threads; sa: [RB][32]
+template <int RB>
+__device__ __forceinline__ void row_sums(float (&a)[RB], int G, float* sa) {
+  if constexpr (RB == 1) {
+    a[0] = row_sum(a[0], G, sa);
+  } else {   // the halves of a warp take a row each
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = G >> 5, hi = lane >> 4, l = lane & 15;
+    float v = (hi ? a[1] : a[0]) + __shfl_xor_sync(0xffffffffu, hi ? a[0] : a[1], 16);
+#pragma unroll
+    for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (G > 32) {
+      if (l == 0) sa[hi * 32 + warp] = v;
+      __syncthreads();
+      v = (l < nw ? sa[hi * 32 + l] : 0.f) + (l + 16 < nw ? sa[hi * 32 + l + 16] : 0.f);
+#pragma unroll
+      for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    }
+    a[0] = __shfl_sync(0xffffffffu, v, 0);
+    a[1] = __shfl_sync(0xffffffffu, v, 16);
+  }
+}
+
+template <typename T, int W, int NV, bool DH, int RB>
 __global__ void __launch_bounds__(1024) rms_norm_backward_ring_kernel(const NormBwdArgs p, const int slots,
                                                                       const int tensors) {
   constexpr int E = Vec<T>::E;
   constexpr bool HELD = NV == 1;   // the weight in registers too
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ float sa[2][32];
+  __shared__ float sa[2][RB * 32];
   __shared__ uint64_t full[RING_MAX];
   chain_wait();
   const int n = p.H, G = blockDim.x, t = threadIdx.x;
@@ -635,58 +673,90 @@ __global__ void __launch_bounds__(1024) rms_norm_backward_ring_kernel(const Norm
     }
     return r;
   };
-  float next = __ldg(p.rstd + m0);
-  for (int r = 0; r < rows; ++r) {
+  float next[RB];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) next[b] = b < rows ? __ldg(p.rstd + m0 + b * step) : 0.f;
+  int slot = 0, seen = 0, got = 0;   // the next row's slot, how often the ring went round, rows that came
+  for (int r = 0; r < rows; r += RB) {
     const long long m = m0 + r * step;
-    const float rstd = next;
-    if (r + 1 < rows) next = __ldg(p.rstd + m + step);
-    if (!mbar_wait(&full[r % slots], (uint32_t)((r / slots) & 1), nullptr, p.err, SITE_ROW)) {
-      // (the copies of the later slots are waited for, with the same limit, before the CTA ends)
-      for (int i = 1; i < slots && r + i < rows; ++i)
-        mbar_wait(&full[(r + i) % slots], (uint32_t)(((r + i) / slots) & 1), nullptr, p.err, SITE_ROW);
+    float rstd[RB], dot[RB];
+    uint4 h[RB][NV], dy[RB][NV], dh[RB][DH ? NV : 1];
+    bool ok = true;
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      rstd[b] = next[b];
+      next[b] = r + RB + b < rows ? __ldg(p.rstd + m + (RB + b) * step) : 0.f;
+      dot[b] = 0.f;
+      if (b > 0 && r + b >= rows) {   // a row of zeros (rstd 0)
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          h[b][j] = dy[b][j] = make_uint4(0u, 0u, 0u, 0u);
+          if (DH) dh[b][j] = h[b][j];
+        }
+        continue;
+      }
+      ok = ok && mbar_wait(&full[slot], (uint32_t)(seen & 1), nullptr, p.err, SITE_ROW);
+      if (!ok) break;
+      const uint8_t* in = ring + (size_t)slot * (uint32_t)tensors * pitch;
+      if (++slot == slots) slot = 0, ++seen;
+      ++got;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        h[b][j] = get(in, j);
+        dy[b][j] = get(in + pitch, j);
+        if (DH && tensors == 3) dh[b][DH ? j : 0] = get(in + 2 * pitch, j);
+        if (DH && tensors == 2)   // not in the ring: too long
+          dh[b][DH ? j : 0] = load_vec<T, W>(static_cast<const T*>(p.dh) + (m + b * step) * p.lddh, j, t, G, s, n);
+        float nn[E], g[E], d2[2] = {0.f, 0.f};
+        if (!HELD) load_w<T, W>(p.w, p.w_f32, j, t, G, s, n, w);
+        Vec<T>::unpack(h[b][j], nn);
+        Vec<T>::unpack(dy[b][j], g);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          mul_pair(nn[e], nn[e + 1], rstd[b], rstd[b]);
+          fma_pair(dw[j][e], dw[j][e + 1], g[e], g[e + 1], nn[e], nn[e + 1]);
+          mul_pair(g[e], g[e + 1], w[e], w[e + 1]);
+          fma_pair(d2[0], d2[1], g[e], g[e + 1], nn[e], nn[e + 1]);
+        }
+        dot[b] += d2[0] + d2[1];
+      }
+    }
+    if (!ok) {   // the copies of the later slots are waited for, with the same limit, before the CTA ends
+      for (++got; got < rows && got < r + slots; ++got) {
+        if (++slot == slots) slot = 0, ++seen;
+        mbar_wait(&full[slot], (uint32_t)(seen & 1), nullptr, p.err, SITE_ROW);
+      }
       break;
     }
-    const uint8_t* in = ring + (size_t)(r % slots) * (uint32_t)tensors * pitch;
-    uint4 h[NV], dy[NV], dh[DH ? NV : 1];
-    float dot = 0.f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      h[j] = get(in, j);
-      dy[j] = get(in + pitch, j);
-      if (DH && tensors == 3) dh[DH ? j : 0] = get(in + 2 * pitch, j);
-      if (DH && tensors == 2)   // not in the ring: too long
-        dh[DH ? j : 0] = load_vec<T, W>(static_cast<const T*>(p.dh) + m * p.lddh, j, t, G, s, n);
-      float nn[E], g[E];
-      if (!HELD) load_w<T, W>(p.w, p.w_f32, j, t, G, s, n, w);
-      Vec<T>::unpack(h[j], nn);
-      Vec<T>::unpack(dy[j], g);
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        nn[e] *= rstd;
-        dw[j][e] = __fmaf_rn(g[e], nn[e], dw[j][e]);
-        dot = __fmaf_rn(g[e] * w[e], nn[e], dot);
-      }
-    }
-    // past the barrier in row_sum the row is in registers and its slot free
-    const float c = -(row_sum(dot, G, sa[r & 1]) / (float)n) * rstd;   // dx = g * rstd + n * c
+    // past the barrier in row_sums the rows are in registers and their slots free
+    row_sums<RB>(dot, G, sa[(r / RB) & 1]);
     if (t == 0 && r + slots < rows) {
-      fence_proxy_async_smem();   // the slot was read through the generic proxy
-      fill(r + slots);
+      fence_proxy_async_smem();   // the slots were read through the generic proxy
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+        if (r + b + slots < rows) fill(r + b + slots);
     }
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      float v[E], g[E];
-      if (!HELD) load_w<T, W>(p.w, p.w_f32, j, t, G, s, n, w);
-      Vec<T>::unpack(h[j], v);
-      Vec<T>::unpack(dy[j], g);
+    for (int b = 0; b < RB; ++b) {
+      if (b > 0 && r + b >= rows) break;
+      const float c = -(dot[b] / (float)n) * rstd[b];   // dx = g * rstd + n * c
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = __fmaf_rn(v[e] * rstd, c, g[e] * w[e] * rstd);
-      if (DH) {
-        Vec<T>::unpack(dh[DH ? j : 0], g);
+      for (int j = 0; j < NV; ++j) {
+        float v[E], g[E], d[E];
+        if (!HELD) load_w<T, W>(p.w, p.w_f32, j, t, G, s, n, w);
+        Vec<T>::unpack(h[b][j], v);
+        Vec<T>::unpack(dy[b][j], g);
+        if (DH) Vec<T>::unpack(dh[b][DH ? j : 0], d);
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] += g[e];
+        for (int e = 0; e < E; e += 2) {
+          mul_pair(v[e], v[e + 1], rstd[b], rstd[b]);
+          mul_pair(g[e], g[e + 1], w[e], w[e + 1]);
+          mul_pair(g[e], g[e + 1], rstd[b], rstd[b]);
+          fma_pair(g[e], g[e + 1], v[e], v[e + 1], c, c);
+          if (DH) add_pair(g[e], g[e + 1], d[e], d[e + 1]);
+        }
+        store_vec<T, W>(static_cast<T*>(p.dx) + (m + b * step) * (long long)n, j, t, G, s, n, Vec<T>::pack(g));
       }
-      store_vec<T, W>(static_cast<T*>(p.dx) + m * (long long)n, j, t, G, s, n, Vec<T>::pack(v));
     }
   }
   chain_release();
@@ -854,9 +924,9 @@ cudaError_t launch_sum(const NormBwdArgs& a, int parts, cudaStream_t s) {
                         a.partials, parts, a.H, split, a.dweight);
 }
 
-template <typename T, int W, int NV, bool DH>
+template <typename T, int W, int NV, bool DH, int RB>
 cudaError_t launch_ring_nv(const NormBwdArgs& a, const BwdShape& b, int slots, size_t smem, cudaStream_t s) {
-  auto kern = rms_norm_backward_ring_kernel<T, W, NV, DH>;
+  auto kern = rms_norm_backward_ring_kernel<T, W, NV, DH, RB>;
   static std::once_flag once[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -871,9 +941,11 @@ cudaError_t launch_ring_nv(const NormBwdArgs& a, const BwdShape& b, int slots, s
 template <typename T, int W, bool DH>
 cudaError_t launch_ring(const NormBwdArgs& a, const BwdShape& b, cudaStream_t s) {
   const size_t smem = b.slots * b.slot;
-  if (b.nv == 1) return launch_ring_nv<T, W, 1, DH>(a, b, b.slots, smem, s);
-  if (b.nv == 2) return launch_ring_nv<T, W, 2, DH>(a, b, b.slots, smem, s);
-  return launch_ring_nv<T, W, sizeof(T) == 4 ? 3 : 2, DH>(a, b, b.slots, smem, s);
+  // (pairs of rows leave two slots on their way)
+  if (b.nv == 1 && b.slots >= 4) return launch_ring_nv<T, W, 1, DH, 2>(a, b, b.slots, smem, s);
+  if (b.nv == 1) return launch_ring_nv<T, W, 1, DH, 1>(a, b, b.slots, smem, s);
+  if (b.nv == 2) return launch_ring_nv<T, W, 2, DH, 1>(a, b, b.slots, smem, s);
+  return launch_ring_nv<T, W, sizeof(T) == 4 ? 3 : 2, DH, 1>(a, b, b.slots, smem, s);
 }
 
 // (of aligned tensors only rows of one warp and rows too long come here)
