@@ -245,9 +245,9 @@ __global__ void __launch_bounds__(VEC ? 1024 : 896) quantize_rows_kernel(const F
   chain_wait();
   const Fp4Layout L(p.rows, p.cols, BLOCK);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int PER_TILE = J == 2 ? 32 : 16;
-  const int tile = blockIdx.x / PER_TILE, in_tile = blockIdx.x % PER_TILE;
-  const int c2 = 2 * (in_tile & 15), j0 = J == 2 ? 2 * (in_tile >> 4) : 0;
+  const int per_tile = J == 1 && p.rows <= 32 ? 16 : 64 / J;
+  const int tile = blockIdx.x / per_tile, in_tile = blockIdx.x - tile * per_tile;
+  const int c2 = 2 * (in_tile & 15), j0 = J * (in_tile >> 4);
   const int ri = lane / LANES, ra = ri & 1, rj = ri >> 1;
   const int piece = lane & (LANES - 1), half = piece & 1;
   const int rin = c2 + ra + 32 * (j0 + rj);
@@ -761,7 +761,7 @@ cudaError_t launch_rows_j(const Fp4QuantArgs& a, cudaStream_t s) {
   constexpr int WROWS = 2 * J, WCOLS = 512 / WROWS, MOST = sizeof(T) == 2 ? 4 : 2;
   const Fp4Layout L(a.rows, a.cols, BLOCK);
   const long long units = (L.kt * 128 + WCOLS - 1) / WCOLS;
-  const unsigned grid = (unsigned)(L.rt * (J == 2 ? 32 : 16));
+  const unsigned grid = (unsigned)(J == 1 && a.rows <= 32 ? 16 : L.rt * (64 / J));
   size_t smem = (size_t)L.kt * L.atoms() * 8 * J;
   int staged = smem <= (a.vec ? 40 : 16) * 1024;
   if (!staged) smem = 0;
@@ -785,8 +785,8 @@ cudaError_t launch_rows_j(const Fp4QuantArgs& a, cudaStream_t s) {
     const int nw = 28;
     return launch_chained(kern, grid, nw * 32, smem + (size_t)nw * RowStage<T, WROWS, WCOLS>::BYTES, 1, s, a, staged, 0);
   }
-  int iter = 1;
-  while (iter < MOST && units > (BLOCK == 32 ? 4 : 8) * iter) iter *= 2;
+  int iter = 1;   // (a CTA alone on its SM takes more warps)
+  while (iter < MOST && units > (BLOCK == 32 ? 4 : (int)grid < num_sms() ? 16 : 8) * iter) iter *= 2;
   int nw = (int)std::min<long long>(32, std::max<long long>(4, (units + iter - 1) / iter));
   unsigned segments = 1;
   if (BLOCK == 32 && units > 4 * iter) {
@@ -803,8 +803,14 @@ cudaError_t launch_rows_j(const Fp4QuantArgs& a, cudaStream_t s) {
 
 template <typename T, int BLOCK>
 cudaError_t launch_rows(const Fp4QuantArgs& a, cudaStream_t s) {
-  if (a.rows <= 32) return launch_rows_j<T, BLOCK, 1>(a, s);
-  return BLOCK == 16 ? launch_rows_j<T, BLOCK, 2>(a, s) : launch_rows_j<T, BLOCK, 4>(a, s);
+  // Two rows a CTA where more would not give every SM one (137 x 4100 bf16, block 16:
+  // 5.2 us with four, 3.8 with two; block 32 of aligned rows has its segments
+  // instead), or where four would be too long for two CTAs' registers on an SM
+  // (4096 x 11008: 38.8 and 35.4; 8192 x 4096: 20.4 and 22.0).
+  const bool few = (a.rows + 127) / 128 * 32 < num_sms();
+  if (BLOCK == 32) return a.rows <= 32 || (few && !a.vec) ? launch_rows_j<T, BLOCK, 1>(a, s)
+                                                            : launch_rows_j<T, BLOCK, 4>(a, s);
+  return few || (a.vec && a.cols > 8192) ? launch_rows_j<T, BLOCK, 1>(a, s) : launch_rows_j<T, BLOCK, 2>(a, s);
 }
 
 template <typename T, int BLOCK, bool ROWS, bool CLUSTER>
