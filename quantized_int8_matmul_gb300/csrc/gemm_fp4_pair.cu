@@ -10,14 +10,17 @@
 // 76 pairs are 3 rounds and 28 tiles, run as 56 pieces).
 //
 // Cluster of 2 CTAs per 256 x 256 tile of C, persistent over the tiles, 352
-// threads each:
-//  * warps 9 and 10: copy this CTA's 128 rows of A and 128 rows of B (256 columns
-//    of K a stage: 16 KB of codes each), the scales of its rows of A and those of
-//    all 256 rows of B into a ring, a warp for each operand: one warp issuing all
-//    five copies of a stage was late with them (4096 x 4096 x 11008, block 32:
-//    58.5 us with one, 53.2 with two). The packed layout is the MMA's own, so
-//    every copy is one contiguous run; a tensor map describes it as a plain matrix
-//    only because tensor copies can complete on the even CTA's barrier.
+// threads each. A tile's columns are two parts of 128, each one 128-row tile of B
+// of which either CTA holds 64 rows (twice as many MMAs of half the width run at
+// the same rate, and a part can start by itself).
+//  * warps 9 and 10: copy this CTA's 128 rows of A and its halves of B's two row
+//    tiles (256 columns of K a stage: 16 KB of codes each), the scales of its rows
+//    of A and those of all 256 rows of B into a ring, a warp for each operand: one
+//    warp issuing all six copies of a stage was late with them (4096 x 4096 x
+//    11008, block 32: 58.5 us with one, 53.2 with two). The packed layout is the
+//    MMA's own, so every copy is one contiguous run or eight; a tensor map
+//    describes it as a plain matrix only because tensor copies can complete on the
+//    even CTA's barrier.
 //  * warp 8 of the even CTA: moves each 128 columns' scales to tensor memory
 //    (tcgen05.cp, both CTAs at once) and issues the pair MMAs.
 //  * warps 0-7: one row and 128 columns a thread; scale, round, stage 32 rows x
@@ -25,8 +28,17 @@
 //    cannot take are stored from the staged rows by the warp).
 // Tensor memory: 512 columns cannot hold two 256-column accumulators and the
 // scales, so the accumulators of even and odd tiles overlap in 64 columns
-// (0..255 and 192..447; the scales at 448). The epilogue empties those 64 first
-// and the next tile's MMAs start then.
+// (0..255 and 192..447; the scales at 448). The epilogue empties those 64 first;
+// until then the next tile runs its first stages on the part that is free.
+//
+// What bounds it: the MMA with K = 64 alone sustains about 9.6 PFLOP/s here
+// (124 cycles for 256 x 256 x 64). 8192 x 11008 x 4096 bf16 output, block 32: 106 us
+// (7.0 PFLOP/s), of which the stores of C cost 15 us (91 us without them): their
+// bursts delay the loads, and five stages (2500 cycles) cannot ride that out. So
+// the stores are spread over the next tile's time (118.5 us before this and the
+// early start, 112.5 with block 32; now 112 and 106). B shared by two pairs through
+// multicast in clusters of four made no pair faster and leaves 8 of 152 SMs idle
+// (121 us); smaller stages are bound by the issuing warp (145 us).
 // Every wait is bounded (common.cuh).
 #include "chain.cuh"
 #include "common.cuh"
@@ -47,6 +59,9 @@ constexpr int NT = NEW * 32 + 96;   // + MMA warp + two producer warps
 constexpr int NS = 5;
 constexpr int STAGE_KT = 2;                       // 128-column tiles of K a stage
 constexpr int CODE_BYTES = STAGE_KT * 8192;       // one operand's codes a stage and CTA
+constexpr int PART_BYTES = CODE_BYTES / 2;        // a CTA's codes of 128 columns of C a stage: 64 rows of B
+constexpr long long kPaceLimit = 100000;          // cycles that the stores of a tile may be spread over
+constexpr int AHEAD = 3;                          // stages that a tile may start on half its columns
 constexpr int STG_BYTES = 32 * 128;               // a warp's staged rows
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t ACC1 = 192;                    // first column of odd tiles' accumulator
@@ -55,7 +70,8 @@ constexpr uint32_t SF_COL = 448;                  // two buffers of 24 columns: 
 struct Shared {
   uint64_t full[NS], empty[NS];
   uint64_t acc_full[2];   // the pair's commit, per tile parity
-  uint64_t acc_free;      // even CTA: one arrival per epilogue warp of both CTAs and tile
+  uint64_t acc_free;      // even CTA: the columns shared with the next tile are read; one arrival per epilogue warp
+  uint64_t acc_done[2];   // of both CTAs and tile. All columns are, per tile parity
   uint64_t teardown;
   uint32_t tmem_base;
   int abort_flag;
@@ -96,7 +112,7 @@ __device__ __forceinline__ Work work_at(const Sched& sc, int i, int cid, int ncl
 
 enum : unsigned {
   SITE_EMPTY = 0x510, SITE_FULL = 0x511, SITE_ACC_FULL = 0x512, SITE_ACC_FREE = 0x513, SITE_TEARDOWN = 0x514,
-  SITE_FINAL = 0x515
+  SITE_FINAL = 0x515, SITE_ACC_DONE = 0x516
 };
 
 // Tensor copies that complete on the even CTA's barrier, issued by the lane whose
@@ -126,6 +142,18 @@ __device__ __forceinline__ void expect_on(uint64_t* bar, uint32_t bytes, uint32_
       : "memory");
 }
 
+// whether the phase has completed, without waiting
+__device__ __forceinline__ bool mbar_test_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 template <int BLOCK>
 struct Cfg {
   static constexpr int ATOMS = BLOCK == 16 ? 2 : 1;            // scale atoms per 128 columns
@@ -141,51 +169,93 @@ struct Issuer {
   int slot;
   uint32_t phase, buf;
 
-  // All of K for one tile (WIDTH 256) or piece; odd: tensor memory columns by
-  // which a piece's scales of B start after their atom (an odd piece of 64 columns
-  // is the second half of its 128 rows). False if a wait ran out.
-  template <int BLOCK, int WIDTH>
-  __device__ __forceinline__ bool tile(Shared& sm, unsigned* err, int kt, uint32_t tacc, uint32_t odd) {
+  __device__ __forceinline__ void advance() {
+    if (++slot == NS) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+  __device__ __forceinline__ bool wait_full(Shared& sm, unsigned* err) {
+    const bool ok = mbar_wait(&sm.full[slot], phase, &sm.abort_flag, err, SITE_FULL);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    tc_fence_after();
+    return true;
+  }
+
+  // The stage at `slot` (n tiles of 128 columns of K) for parts P0 .. P1 - 1 of the
+  // tile's columns: a tile of 256 has two parts of 128, a piece is one part of
+  // WIDTH. odd: tensor memory columns by which a piece's scales of B start after
+  // their atom (an odd piece of 64 columns is the second half of its 128 rows).
+  template <int BLOCK, int WIDTH, int P0, int P1>
+  __device__ __forceinline__ void stage(int n, uint32_t tacc, uint32_t odd, uint32_t accumulate) {
     using C = Cfg<BLOCK>;
-    constexpr int ATOMS = C::ATOMS;
-    constexpr uint32_t id0 = idesc_fp4(256, WIDTH, BLOCK == 32, 0), id1 = idesc_fp4(256, WIDTH, BLOCK == 32, 2);
-    constexpr uint32_t b_ch = WIDTH / 2;              // a CTA's rows of B: a chunk's bytes / 16
+    constexpr int ATOMS = C::ATOMS, PW = WIDTH == 64 ? 64 : 128;   // a part's columns
+    constexpr uint32_t id0 = idesc_fp4(256, PW, BLOCK == 32, 0), id1 = idesc_fp4(256, PW, BLOCK == 32, 2);
+    constexpr uint32_t b_ch = PW / 2;                 // a CTA's rows of a part of B: a chunk's bytes / 16
     constexpr uint32_t b_lo = b_ch << 16;
-    constexpr uint32_t sb_at = WIDTH == 256 ? 8 : 4;  // tensor memory columns of B's scales an atom
-    uint32_t acc = 0u;
-    for (int left = kt; left > 0; left -= STAGE_KT) {
-      const bool ok = mbar_wait_cluster(&sm.full[slot], phase, &sm.abort_flag, err, SITE_FULL);
-      if (!__all_sync(0xffffffffu, ok)) return false;
-      tc_fence_after();
-      const uint32_t a = s16 + (uint32_t)slot * (C::STAGE >> 4), b = a + (CODE_BYTES >> 4);
-      const uint32_t fa = b + (CODE_BYTES >> 4), fb = fa + (C::SF_BYTES >> 4);
+    const uint32_t a = s16 + (uint32_t)slot * (C::STAGE >> 4), b = a + (CODE_BYTES >> 4);
+    const uint32_t fa = b + (CODE_BYTES >> 4), fb = fa + (C::SF_BYTES >> 4);
 #pragma unroll
-      for (int k = 0; k < STAGE_KT; ++k) {
-        if (k > 0 && left == 1) break;
-        const uint32_t sa = tb + SF_COL + buf, sb = sa + 8u;
-        buf ^= 24u;
+    for (int k = 0; k < STAGE_KT; ++k) {
+      if (k > 0 && n == 1) break;
+      const uint32_t sa = tb + SF_COL + buf, sb = sa + 8u;
+      buf ^= 24u;
 #pragma unroll
-        for (int i = 0; i < ATOMS; ++i) {
-          cp_scales_pair(sa + i * 4, fa + (k * ATOMS + i) * 32, on);
-          cp_scales_pair(sb + i * sb_at, fb + (k * ATOMS + i) * 32, on);
-          if (WIDTH == 256) cp_scales_pair(sb + i * 8 + 4, fb + (C::SF_BYTES >> 4) + (k * ATOMS + i) * 32, on);
-        }
+      for (int i = 0; i < ATOMS; ++i) {
+        cp_scales_pair(sa + i * 4, fa + (k * ATOMS + i) * 32, on);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {   // 64 columns of K each
-          mma_fp4_pair<BLOCK>(tacc, a + (uint32_t)(k * 512 + j * 256) + kDescLo,
-                              b + (uint32_t)(k * 4 + j * 2) * b_ch + b_lo, (BLOCK == 32 && j) ? id1 : id0,
-                              sa + (BLOCK == 16 ? j * 4 : 0),
-                              sb + (BLOCK == 16 ? j * sb_at : 0u) + (WIDTH == 64 ? odd : 0u), acc, on);
-          acc = 1u;
-        }
+        for (int h = P0; h < P1; ++h)
+          cp_scales_pair(sb + (h * ATOMS + i) * 4, fb + h * (C::SF_BYTES >> 4) + (k * ATOMS + i) * 32, on);
       }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)   // 64 columns of K each
+#pragma unroll
+        for (int h = P0; h < P1; ++h)
+          mma_fp4_pair<BLOCK>(tacc + h * 128, a + (uint32_t)(k * 512 + j * 256) + kDescLo,
+                              b + h * (PART_BYTES >> 4) + (uint32_t)(k * 4 + j * 2) * b_ch + b_lo,
+                              (BLOCK == 32 && j) ? id1 : id0, sa + (BLOCK == 16 ? j * 4 : 0),
+                              sb + (h * ATOMS + (BLOCK == 16 ? j : 0)) * 4 + (WIDTH == 64 ? odd : 0u),
+                              (k > 0 || j > 0) ? 1u : accumulate, on);
+    }
+  }
+
+  // Stages [from, stages) of a tile or piece. False if a wait ran out.
+  template <int BLOCK, int WIDTH>
+  __device__ __forceinline__ bool run(Shared& sm, unsigned* err, int kt, int from, uint32_t tacc, uint32_t odd) {
+    for (int left = kt - from * STAGE_KT; left > 0; left -= STAGE_KT) {
+      if (!wait_full(sm, err)) return false;
+      stage<BLOCK, WIDTH, 0, WIDTH == 256 ? 2 : 1>(left, tacc, odd, left == kt ? 0u : 1u);
       commit_pair_on(&sm.empty[slot], on);
-      if (++slot == NS) {
-        slot = 0;
-        phase ^= 1u;
-      }
+      advance();
     }
     return true;
+  }
+
+  // Part FREE of up to AHEAD first stages, until the previous tile's columns are
+  // drained; then the other part of the same stages. Returns their number, -1 if a
+  // wait ran out.
+  template <int BLOCK, int FREE>
+  __device__ __forceinline__ int start(Shared& sm, unsigned* err, int kt, uint32_t tacc, uint32_t parity) {
+    const int slot0 = slot;
+    const uint32_t phase0 = phase;
+    int ahead = 0;
+    while (ahead < AHEAD && ahead * STAGE_KT < kt) {
+      if (__all_sync(0xffffffffu, mbar_test_cluster(&sm.acc_free, parity))) break;
+      if (!wait_full(sm, err)) return -1;
+      stage<BLOCK, 256, FREE, FREE + 1>(kt - ahead * STAGE_KT, tacc, 0u, ahead ? 1u : 0u);
+      advance();
+      ++ahead;
+    }
+    if (!__all_sync(0xffffffffu, mbar_wait_cluster(&sm.acc_free, parity, &sm.abort_flag, err, SITE_ACC_FREE))) return -1;
+    tc_fence_after();
+    slot = slot0;
+    phase = phase0;
+    for (int i = 0; i < ahead; ++i) {
+      stage<BLOCK, 256, 1 - FREE, 2 - FREE>(kt - i * STAGE_KT, tacc, 0u, i ? 1u : 0u);
+      commit_pair_on(&sm.empty[slot], on);
+      advance();
+    }
+    return ahead;
   }
 };
 
@@ -218,6 +288,8 @@ __global__ void __launch_bounds__(NT, 1)
     mbar_init(&sm.acc_full[0], 1);
     mbar_init(&sm.acc_full[1], 1);
     mbar_init(&sm.acc_free, 2 * NEW);
+    mbar_init(&sm.acc_done[0], 2 * NEW);
+    mbar_init(&sm.acc_done[1], 2 * NEW);
     mbar_init(&sm.teardown, 1);
     sm.abort_flag = 0;
     fence_mbarrier_init();
@@ -242,21 +314,34 @@ __global__ void __launch_bounds__(NT, 1)
       const int cid_u = __shfl_sync(0xffffffffu, cid, 0), tiles_u = __shfl_sync(0xffffffffu, my_tiles, 0);
       bool ok = true;
       for (int tl = 0; tl < tiles_u && ok; ++tl) {
-        // the columns shared with the previous tile's accumulator are drained, and
-        // with them (the epilogue works in order) all of this one's last tile
-        if (tl > 0) {
-          ok = mbar_wait_cluster(&sm.acc_free, (uint32_t)((tl - 1) & 1), &sm.abort_flag, p.err, SITE_ACC_FREE);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-        }
-        tc_fence_after();
         const uint32_t tacc = tb + ((tl & 1) ? ACC1 : 0u);
         const Work wk = work_at(sc, tl, cid_u, ncl, n_tiles);
         const int width = __shfl_sync(0xffffffffu, wk.width, 0);
         const uint32_t odd = __shfl_sync(0xffffffffu, wk.piece & 1, 0) ? 2u : 0u;
-        if (width == 256) ok = ring.template tile<BLOCK, 256>(sm, p.err, kt, tacc, odd);
-        else if (width == 128) ok = ring.template tile<BLOCK, 128>(sm, p.err, kt, tacc, odd);
-        else ok = ring.template tile<BLOCK, 64>(sm, p.err, kt, tacc, odd);
+        // this accumulator's last tile is drained; the previous tile's columns
+        // (shared by an odd tile's first part, an even tile's second) are soon
+        int begun = 0;
+        if (tl > 1) {
+          ok = mbar_wait_cluster(&sm.acc_done[tl & 1], (uint32_t)(((tl >> 1) - 1) & 1), &sm.abort_flag, p.err,
+                                 SITE_ACC_DONE);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
+        tc_fence_after();
+        if (tl > 0 && width == 256) {
+          begun = (tl & 1) ? ring.template start<BLOCK, 1>(sm, p.err, kt, tacc, 0u)
+                           : ring.template start<BLOCK, 0>(sm, p.err, kt, tacc, 1u);
+          ok = begun >= 0;
+          if (!ok) break;
+        } else if (tl > 0) {
+          ok = mbar_wait_cluster(&sm.acc_free, (uint32_t)((tl - 1) & 1), &sm.abort_flag, p.err, SITE_ACC_FREE);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        if (width == 256) ok = ring.template run<BLOCK, 256>(sm, p.err, kt, begun, tacc, odd);
+        else if (width == 128) ok = ring.template run<BLOCK, 128>(sm, p.err, kt, 0, tacc, odd);
+        else ok = ring.template run<BLOCK, 64>(sm, p.err, kt, 0, tacc, odd);
         if (!ok) break;
         commit_pair_on(&sm.acc_full[tl & 1], on);
       }
@@ -269,7 +354,7 @@ __global__ void __launch_bounds__(NT, 1)
     if (on) {
       prefetch_tmap(is_a ? &tmA : &tmB);
       prefetch_tmap(is_a ? &tmSA : &tmSB);
-      if (!is_a && sc.cut > 1) prefetch_tmap(&tmBP);
+      if (!is_a && sc.cut > 2) prefetch_tmap(&tmBP);
     }
     const uint32_t full0 = mapa_shared(smem_u32(&sm.full[0]), 0);
     const int cid_u = __shfl_sync(0xffffffffu, cid, 0), tiles_u = __shfl_sync(0xffffffffu, my_tiles, 0);
@@ -284,15 +369,15 @@ __global__ void __launch_bounds__(NT, 1)
       const bool whole = width == 256;
       // row tiles of this CTA (past the matrix: the last one again; its results are not stored)
       const int last = (int)LB.rt - 1;
-      const int ra = min(2 * wk.mt + rank_u, (int)LA.rt - 1), rb = min(2 * wk.nt + rank_u, last);
-      // B's scales: both row tiles of a whole tile, a piece's one
+      const int ra = min(2 * wk.mt + rank_u, (int)LA.rt - 1);
+      // row tiles of B: both of a whole tile, a piece's one
       const int rb0 = min(2 * wk.nt + (width == 64 ? wk.piece >> 1 : wk.piece), last);
       const int rb1 = min(2 * wk.nt + 1, last);
-      // a piece's part of its row tile: the CTAs' halves of it
-      const int part = width == 128 ? rank_u : 2 * (wk.piece & 1) + rank_u;
+      // the CTA's part of a row tile: a half, of a piece of 64 columns a quarter
+      const int part = width >= 128 ? rank_u : 2 * (wk.piece & 1) + rank_u;
       const uint32_t bytes =
-          2u * (whole ? (uint32_t)C::STAGE : (uint32_t)(CODE_BYTES + width * 64 + 2 * C::SF_BYTES));
-      const int r0 = is_a ? ra * kt : rb * kt, f0 = is_a ? ra * kt : rb0 * kt, f1 = rb1 * kt;
+          2u * (whole ? (uint32_t)C::STAGE : (uint32_t)(CODE_BYTES + width * 32 * STAGE_KT + 2 * C::SF_BYTES));
+      const int f0 = is_a ? ra * kt : rb0 * kt, f1 = rb1 * kt;
       for (int s = 0; s < kt; s += STAGE_KT, ++g) {
         ok = __all_sync(0xffffffffu, mbar_wait(&sm.empty[slot], phase, &sm.abort_flag, p.err, SITE_EMPTY));
         if (!ok) break;
@@ -301,14 +386,15 @@ __global__ void __launch_bounds__(NT, 1)
         expect_on(&sm.full[slot], bytes, expect);
         // a stage that reaches past its row tile copies bytes that no MMA reads
         if (is_a) {
-          load_pair(dst, &tmA, (r0 + s) * 8, bar, on);
+          load_pair(dst, &tmA, (f0 + s) * 8, bar, on);
           load_pair(sf, &tmSA, (f0 + s) * ATOMS, bar, on);
         } else if (whole) {
-          load_pair(dst + CODE_BYTES, &tmB, (r0 + s) * 8, bar, on);
+          load_pair_3d(dst + CODE_BYTES, &tmB, (f0 + s) * 4, part, bar, on);
+          load_pair_3d(dst + CODE_BYTES + PART_BYTES, &tmB, (f1 + s) * 4, part, bar, on);
           load_pair(sf + C::SF_BYTES, &tmSB, (f0 + s) * ATOMS, bar, on);
           load_pair(sf + 2 * C::SF_BYTES, &tmSB, (f1 + s) * ATOMS, bar, on);
         } else {
-          load_pair_3d(dst + CODE_BYTES, &tmBP, (f0 + s) * 4, part, bar, on);
+          load_pair_3d(dst + CODE_BYTES, width == 128 ? &tmB : &tmBP, (f0 + s) * 4, part, bar, on);
           load_pair(sf + C::SF_BYTES, &tmSB, (f0 + s) * ATOMS, bar, on);
         }
         if (++slot == NS) {
@@ -327,9 +413,11 @@ __global__ void __launch_bounds__(NT, 1)
     // ---------------- epilogue ----------------
     const int q = warp & 3, h = warp >> 2;
     const uint32_t free0 = mapa_shared(smem_u32(&sm.acc_free), 0);
+    const uint32_t done0 = mapa_shared(smem_u32(&sm.acc_done[0]), 0);
     const uint32_t stg = stg_base + (uint32_t)warp * STG_BYTES;
     const float* rows_a = reinterpret_cast<const float*>(p.A + LA.row_off());
     const float* rows_b = reinterpret_cast<const float*>(p.B + LB.row_off());
+    long long last = 0;
     for (int tl = 0; tl < my_tiles; ++tl) {
       const Work wk = work_at(sc, tl, cid, ncl, n_tiles);
       const long long row0 = (long long)wk.mt * 256 + rank * 128 + q * 32;
@@ -346,25 +434,35 @@ __global__ void __launch_bounds__(NT, 1)
       }
       if (!mbar_wait_cluster(&sm.acc_full[tl & 1], (uint32_t)((tl >> 1) & 1), &sm.abort_flag, p.err, SITE_ACC_FULL))
         break;
+      // the time that the next tile will take, if that is a whole one too: as this one did
+      const long long now = clock64();
+      const bool paced = tl > 0 && tl + 1 < my_tiles && work_at(sc, tl + 1, cid, ncl, n_tiles).width == 256;
+      const long long period = paced ? min(now - last, kPaceLimit) : 0;
+      last = now;
       tc_fence_after();
       const uint32_t tacc = tbase + ((uint32_t)(q * 32) << 16) + ((tl & 1) ? ACC1 : 0u) + (uint32_t)(h * hc);
       // even tiles share columns 192..255 with the next accumulator, odd ones 0..63
       const int first = (tl & 1) || units < 2 ? 0 : 1;
+      const uint32_t done = done0 + (uint32_t)(tl & 1) * 8u;
       const bool shares = units == 2 && h == ((tl & 1) ? 0 : 1);   // (a piece is the last of its cluster)
       if (tl == my_tiles - 1) chain_release();
       if (!shares) {
         __syncwarp();
         if (lane == 0) mbar_arrive_remote_cta(free0);
+        if (lane == 0 && units == 0) mbar_arrive_remote_cta(done);
       }
 #pragma unroll 1
       for (int u = 0; u < units; ++u) {
         const int unit = u ^ first;   // 64 columns
         uint32_t acc[2][32];
         tmem_ld32x2(tacc + unit * 64, acc[0], tacc + unit * 64 + 32, acc[1]);
-        if (shares && u == 0) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_remote_cta(free0);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && shares && u == 0) mbar_arrive_remote_cta(free0);
+        if (lane == 0 && u == units - 1) mbar_arrive_remote_cta(done);
+        if (period > 0) {   // quarters of the next tile's time, each for 64 of its 256 columns
+          const long long until = now + (period >> 2) * (2 * u + (shares ? 0 : 1));
+          while (clock64() < until) __nanosleep(64);
         }
         const long long n0 = col0 + unit * 64;
         if (row0 >= p.M || n0 >= p.N) continue;
@@ -441,33 +539,33 @@ cudaError_t launch(const GemmFp4Args& a, cudaStream_t s) {
   }
   const Fp4Layout LA(a.M, a.K, BLOCK), LB(a.N, a.K, BLOCK);
   CUtensorMap ta{}, tb{}, tbp{}, tsa{}, tsb{}, tc{};
-  // codes as rows of 1 KB (8 to a 128 x 128 tile), scales as rows of one atom
-  auto codes = [](CUtensorMap* m, const uint8_t* base, const Fp4Layout& L) {
-    return make_tmap_2d(m, base, CU_TENSOR_MAP_DATA_TYPE_INT32, 256, L.code_bytes() / 1024, 1024, 256, STAGE_KT * 8,
-                        CU_TENSOR_MAP_SWIZZLE_NONE);
+  // A's codes as rows of 1 KB (8 to a 128 x 128 tile), scales as rows of one atom, B's
+  // codes by chunk (32 columns of K) and part (half or quarter) of their 128 rows
+  auto parts = [](CUtensorMap* m, const uint8_t* base, const Fp4Layout& L, unsigned n) {
+    const uint32_t words = 512u / n;   // 32-bit words: 128 / n rows of 16 bytes
+    return make_tmap_3d(m, base, CU_TENSOR_MAP_DATA_TYPE_INT32, words, L.code_bytes() / 2048, n, 2048, words * 4, words,
+                        STAGE_KT * 4, CU_TENSOR_MAP_SWIZZLE_NONE);
   };
   auto scales = [](CUtensorMap* m, const uint8_t* base, const Fp4Layout& L) {
     return make_tmap_2d(m, base + L.scale_off(), CU_TENSOR_MAP_DATA_TYPE_INT32, 128, L.scale_bytes() / 512, 512, 128,
                         STAGE_KT * C::ATOMS, CU_TENSOR_MAP_SWIZZLE_NONE);
   };
-  cudaError_t e = codes(&ta, a.A, LA);
-  if (e == cudaSuccess) e = codes(&tb, a.B, LB);
+  cudaError_t e = make_tmap_2d(&ta, a.A, CU_TENSOR_MAP_DATA_TYPE_INT32, 256, LA.code_bytes() / 1024, 1024, 256,
+                               STAGE_KT * 8, CU_TENSOR_MAP_SWIZZLE_NONE);
+  if (e == cudaSuccess) e = parts(&tb, a.B, LB, 2);
   if (e == cudaSuccess) e = scales(&tsa, a.A, LA);
   if (e == cudaSuccess) e = scales(&tsb, a.B, LB);
   int tma_c = 0;
   if (e == cudaSuccess) e = make_c_map(a, &tc, &tma_c);
   if (e != cudaSuccess) return e;
-  const int tiles = (int)(((a.M + 255) / 256) * ((a.N + 255) / 256));
-  Sched sc{tiles, 1, 0, (int)((a.M + 255) / 256)};
+  const int m_tiles = (int)((a.M + 255) / 256), tiles = m_tiles * (int)((a.N + 255) / 256);
+  Sched sc{tiles, 1, 0, m_tiles};
   const int rest = tiles % clusters;
   if (rest > 0 && 2 * rest <= clusters) {
     sc.cut = 4 * rest <= clusters ? 4 : 2;
     sc.full = tiles - rest;
     sc.pieces = rest * sc.cut;
-    // B's codes by chunk (32 columns) and part of its 128 rows
-    const uint32_t part = 512u / sc.cut;   // 32-bit words: 128 / cut rows of 16 bytes, half of a piece's
-    e = make_tmap_3d(&tbp, a.B, CU_TENSOR_MAP_DATA_TYPE_INT32, part, LB.code_bytes() / 2048, sc.cut, 2048, part * 4,
-                     part, STAGE_KT * 4, CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (sc.cut == 4) e = parts(&tbp, a.B, LB, 4);
   }
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(2 * (unsigned)std::min(std::max(tiles, sc.pieces), clusters), 1, 1);
