@@ -676,6 +676,21 @@ __device__ __forceinline__ float decode(uint32_t c) {
   return (c & 8u) ? -m : m;
 }
 
+// Eight codes, the first in the lowest bits, by the conversion to fp16 pairs.
+__device__ __forceinline__ void decode8(uint32_t w, float (&v)[8]) {
+  uint32_t h[4];
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\tcvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\tcvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[e]));
+    v[2 * e] = f.x;
+    v[2 * e + 1] = f.y;
+  }
+}
+
 template <typename T, int BLOCK, bool VEC>
 __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* packed, long long rows, long long cols, T* y) {
   chain_wait();
@@ -708,11 +723,9 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* packed, 
       if (row >= rows || k >= cols) continue;
       const float s = BLOCK == 16 ? e4m3_to_f(sb[i]) : e8m0_to_f(sb[i]);
       float v[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        v[e] = __fmul_rn(decode(w[i] >> (4 * e)), s);
-        if (BLOCK == 16) v[e] = __fmul_rn(v[e], g[i >> 2]);
-      }
+      decode8(w[i], v);
+      mul8(v, s);
+      if (BLOCK == 16) mul8(v, g[i >> 2]);
       T* out = y + row * cols + k;   // cols is a multiple of 16 bytes: 8 columns lie inside, or 4 of float32
       if (sizeof(T) == 2) {
         uint32_t o[4];
