@@ -8,6 +8,11 @@
  *   qmm_a8w8                 int8 x int8 -> exact int32 -> row/column scales
  *   matmul_integer           ONNX MatMulInteger with zero points, shared B
  *   dynamic_quantize_linear  ONNX DynamicQuantizeLinear to uint8
+ * and the operators around a quantised layer:
+ *   qmm_rms_norm_s8, qmm_rms_norm_backward, qmm_s8_dequantize_rows
+ *                            root-mean-square norm to int8 rows, its gradient
+ *   qmm_fp4_quantize, qmm_fp4_quantize_both, qmm_fp4_dequantize, qmm_fp4_matmul
+ *                            4-bit floats with block scales, and their product
  *
  * Conventions for every entry point:
  *  - Tensors are caller-owned DEVICE pointers, row-major and contiguous in the

@@ -223,7 +223,10 @@ struct ScaleWord<1> { using type = uint32_t; };
 // 256 columns of two rows). Rows chosen so make every 32-byte sector of codes (two
 // neighbouring rows' 16 bytes) the work of one CTA, and of scales (two rows'
 // 16-byte lines of an atom, whose 4-byte parts are rows 32 apart) of one or two.
-// Block 32 takes a segment of the columns a CTA (blockIdx.y). A warp's steps of a batch (ITER) are loaded
+// Block 32 takes a segment of the columns a CTA (blockIdx.y). 8192 x 4096 bf16: block
+// 32 14.9 us (5.7 TB/s, 85 % of a copy's rate), block 16 20.4 (63 %: a row has to be
+// whole before its first code, so its loads, maximum and codes do not overlap within
+// a CTA; the registers that hold it limit an SM to 32 warps). A warp's steps of a batch (ITER) are loaded
 // together; with block 16 a row whose steps are one batch stays in registers
 // between its maximum and its codes, longer rows are read again.
 // ---------------------------------------------------------------------------
@@ -403,7 +406,9 @@ __global__ void __launch_bounds__(256) zero_kernel(unsigned* a, int na, unsigned
 // matrix along the columns is its transpose [cols][rows].
 // ---------------------------------------------------------------------------
 // Largest magnitudes of the columns (and the rows) into the packed buffers' max
-// words: 64 rows x 256 columns a CTA, eight columns a lane.
+// words: 64 rows x 256 columns a CTA, eight columns a lane. 8192 x 4096 bf16: 11 of
+// the 27.8 us that block 16 takes along the columns (the second reading of x is
+// largely from L2).
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256, VEC ? 4 : 2) absmax_kernel(const Fp4QuantArgs p, unsigned* colmax,
                                                                   unsigned* rowmax) {
@@ -482,7 +487,9 @@ __global__ void __launch_bounds__(256, VEC ? 4 : 2) absmax_kernel(const Fp4Quant
 // there. The scales leave as whole tiles by bulk copies. CLUSTER (block 16,
 // x of up to 8 tiles down): the tiles above each other are one cluster, and the
 // columns' maxima are taken over it -- one launch in place of a fill, a pass for
-// the maxima and this.
+// the maxima and this. 8192 x 4096 bf16: block 32 both ways 19.6 us (5.3 TB/s, 79 %
+// of a copy's rate; issue slots 56 % busy), columns alone 15.5; block 16 with its
+// maxima 36.5 and 27.8. 4099 x 1021 float32, block 16, columns: 8.6 us.
 template <typename T>
 struct TileSmem {
   static constexpr int PITCH = 128 * (int)sizeof(T) + 16;   // bytes; 16 more keep row accesses off each other's banks
@@ -668,6 +675,8 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 5 : 3) quantize_tile_ker
 
 // ---------------------------------------------------------------------------
 // Reading back: y[r][c] = code * block scale (* row scale), one CTA per tile.
+// 8192 x 4096 to bf16 14.2 us (6.0 TB/s, 90 % of a copy's rate); 4099 x 1021 to
+// float32, element by element from the tile in shared memory, 7.4 us (2.6 TB/s).
 // ---------------------------------------------------------------------------
 // A code as a float: its three low bits moved to the exponent and mantissa of an
 // fp16 value are that value times 2^-14.
@@ -742,7 +751,8 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* packed, 
     }
   } else {   // the tile through shared memory; one row a warp step, neighbouring lanes neighbouring columns
     __shared__ __align__(16) uint8_t cs[8192 + 1024];
-    for (int i = threadIdx.x; i < 512; i += 256) reinterpret_cast<uint4*>(cs)[i] = reinterpret_cast<const uint4*>(codes)[i];
+    for (int i = threadIdx.x; i < 512; i += 256)
+      reinterpret_cast<uint4*>(cs)[i] = reinterpret_cast<const uint4*>(codes)[i];
     if (threadIdx.x < 32 * ATOMS)
       reinterpret_cast<uint4*>(cs + 8192)[threadIdx.x] = reinterpret_cast<const uint4*>(sf)[threadIdx.x];
     chain_release();
@@ -867,7 +877,8 @@ cudaError_t launch_tiles(const Fp4QuantArgs& a, cudaStream_t s) {
                                    rm, words);
     if (e != cudaSuccess) return e;
     const long long ctas = ((a.cols + 255) / 256) * ((a.rows + 63) / 64);
-    e = launch_chained(a.vec ? absmax_kernel<T, true> : absmax_kernel<T, false>, (unsigned)ctas, 256, 0, 1, s, a, cm, rm);
+    e = launch_chained(a.vec ? absmax_kernel<T, true> : absmax_kernel<T, false>, (unsigned)ctas, 256, 0, 1, s, a, cm,
+                       rm);
     if (e != cudaSuccess) return e;
   }
   return a.out_rows ? launch_tile<T, BLOCK, true, false>(a, grid, 1, s)

@@ -14,6 +14,10 @@
 // 0-3 put the fp32 partial sums in shared memory, and after a cluster barrier
 // each CTA adds up its share of the rows over the cluster in rank order (so the
 // result does not depend on timing), scales and stores them.
+// 1 x 28672 x 8192: block 16 21.7 us, block 32 20.1 (6.1 and 6.2 TB/s of weight and
+// scales, 91 and 93 % of a copy's rate); 64 x 28672 x 8192 25.6 and 23.1. 1 x 4096 x
+// 4096 5.5 and 5.1 us, of which the weight's bytes are 1.4: the launch, the first
+// bytes' way and the join over the cluster (0.9 us) are the rest.
 // Every wait is bounded (common.cuh).
 #include "chain.cuh"
 #include "common.cuh"
@@ -206,7 +210,8 @@ __global__ void __launch_bounds__(NT, 2) gemm_fp4_rows_kernel(const GemmFp4Args 
   if (ok && !sm.abort_flag) {
     for (int m = rank + warp * pl.split; m < p.M; m += (NT / 32) * pl.split) {
       const uint32_t local = sbase + (uint32_t)(m * 512 + lane * 16);
-      float4 v = pl.split > 1 ? ld_cluster_f4(mapa_shared(local, 0)) : *reinterpret_cast<const float4*>(part + m * 128 + lane * 4);
+      float4 v = pl.split > 1 ? ld_cluster_f4(mapa_shared(local, 0))
+                              : *reinterpret_cast<const float4*>(part + m * 128 + lane * 4);
       for (int r = 1; r < pl.split; ++r) {
         const float4 o = ld_cluster_f4(mapa_shared(local, (uint32_t)r));
         v.x += o.x;
@@ -254,7 +259,7 @@ __global__ void __launch_bounds__(NT, 2) gemm_fp4_rows_kernel(const GemmFp4Args 
 
 // Ring and split for a problem: two CTAs an SM (their rings and tensor memory),
 // and the largest split that keeps every CTA resident at once, each with two
-// stages at least. 1 x 28672 x 8192 (224 column tiles): 22.3 us with a split of
+// stages at least. 1 x 28672 x 8192 (224 column tiles): 21.7 us with a split of
 // 1, 29.8 with 2 (448 CTAs, a second wave); 1 x 4096 x 4096 (32 tiles): 12.0
 // with 1, 6.6 with 4, 6.9 with 8.
 template <int BLOCK>
@@ -299,8 +304,8 @@ cudaError_t launch(const GemmFp4Args& a, cudaStream_t s) {
 
 cudaError_t launch_gemm_fp4(const GemmFp4Args& a, int block, cudaStream_t s, const char** kernel_name) {
   // Above 64 rows the pair kernel's 256 x 256 tiles win although they may be
-  // mostly padding: 128 x 11008 x 4096 takes 12.1 us there and 14.3 here, 64 rows
-  // 11.6 and 11.6, 64 x 28672 x 8192 30.0 and 26.1.
+  // mostly padding: 128 x 11008 x 4096 takes 11.1 us there and 14.3 here, 64 rows
+  // 10.5 and 10.2, 64 x 28672 x 8192 30.0 and 25.6.
   if (a.M > 64) {
     *kernel_name = "gemm_fp4_pair";
     return launch_gemm_fp4_pair(a, block, s);

@@ -32,11 +32,12 @@
 // until then the next tile runs its first stages on the part that is free.
 //
 // What bounds it: the MMA with K = 64 alone sustains about 9.6 PFLOP/s here
-// (124 cycles for 256 x 256 x 64). 8192 x 11008 x 4096 bf16 output, block 32: 106 us
-// (7.0 PFLOP/s), of which the stores of C cost 15 us (91 us without them): their
-// bursts delay the loads, and five stages (2500 cycles) cannot ride that out. So
-// the stores are spread over the next tile's time (118.5 us before this and the
-// early start, 112.5 with block 32; now 112 and 106). B shared by two pairs through
+// (124 cycles for 256 x 256 x 64). 8192 x 11008 x 4096 bf16 output, block 32: 106 to
+// 112 us from run to run (7.0 to 6.6 PFLOP/s), of which the stores of C cost 15 us
+// or more (91 us without them): their bursts delay the loads, and five stages (2500
+// cycles) cannot ride that out. So the stores are spread over the next tile's time
+// (4096 x 11008 x 4096 without this and the early start 62.8 us in blocks of 16 and
+// 59.4 in blocks of 32; now 60.3 and 56.0). B shared by two pairs through
 // multicast in clusters of four made no pair faster and leaves 8 of 152 SMs idle
 // (121 us); smaller stages are bound by the issuing warp (145 us).
 // Every wait is bounded (common.cuh).
