@@ -177,6 +177,19 @@ struct Raw16 {
   __device__ __forceinline__ void load_whole(const T* p) {
     *this = *reinterpret_cast<const Raw16<T>*>(p);
   }
+  // The same of global memory, where 32-byte alignment allows a whole sector a load
+  // (half of one a load costs twice the requests).
+  __device__ __forceinline__ void load_whole(const T* p, bool wide) {
+    if (!wide) return load_whole(p);
+    uint32_t* w = reinterpret_cast<uint32_t*>(this);
+    const uint32_t* g = reinterpret_cast<const uint32_t*>(p);
+#pragma unroll
+    for (int i = 0; i < 4 * (int)sizeof(T); i += 8)
+      asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]), "=r"(w[i + 4]), "=r"(w[i + 5]),
+                     "=r"(w[i + 6]), "=r"(w[i + 7])
+                   : "l"(g + i));
+  }
   __device__ __forceinline__ unsigned max_bits() const {
     if constexpr (sizeof(T) == 2) return Raw8<T>::bits(max_pair(lo.pair(), hi.pair()));
     else return max(lo.max_bits(), hi.max_bits());
@@ -226,9 +239,9 @@ struct ScaleWord<1> { using type = uint32_t; };
 // Block 32 takes a segment of the columns a CTA (blockIdx.y). 8192 x 4096 bf16: block
 // 32 14.9 us (5.7 TB/s, 85 % of a copy's rate), block 16 20.4 (63 %: a row has to be
 // whole before its first code, so its loads, maximum and codes do not overlap within
-// a CTA; the registers that hold it limit an SM to 32 warps). A warp's steps of a batch (ITER) are loaded
-// together; with block 16 a row whose steps are one batch stays in registers
-// between its maximum and its codes, longer rows are read again.
+// a CTA; the registers that hold it limit an SM to 32 warps). A warp's steps of a
+// batch (ITER) are loaded together; with block 16 a row whose steps are one batch
+// stays in registers between its maximum and its codes, longer rows are read again.
 // ---------------------------------------------------------------------------
 template <typename T, int BLOCK, int J, int ITER, bool VEC>
 __global__ void __launch_bounds__(VEC ? 1024 : 896) quantize_rows_kernel(const Fp4QuantArgs p, const int staged,
@@ -259,6 +272,7 @@ __global__ void __launch_bounds__(VEC ? 1024 : 896) quantize_rows_kernel(const F
   const bool rv = row < p.rows;
   const T* x = static_cast<const T*>(p.x) + (rv ? row : 0) * p.ld;
   const int n = rv ? (int)p.cols : 0;
+  const bool wide = ((reinterpret_cast<uintptr_t>(p.x) | (size_t)p.ld * sizeof(T)) & 31) == 0;
   const int chunks = (int)L.kt * 4, units_all = (chunks + UC - 1) / UC;
   // this CTA's steps: all, or (block 32) as many as its warps take in one batch
   const int u0 = BLOCK == 32 && gridDim.y > 1 ? blockIdx.y * nw * ITER : 0;
@@ -309,7 +323,7 @@ __global__ void __launch_bounds__(VEC ? 1024 : 896) quantize_rows_kernel(const F
     }
     if (VEC && (long long)(u0 + (b + 1) * ITER * nw) * WCOLS <= p.cols) {   // the whole batch lies inside
 #pragma unroll
-      for (int i = 0; i < ITER; ++i) v[i].load_whole(x + (u0 + (b * ITER + i) * nw + warp) * WCOLS + piece * 16);
+      for (int i = 0; i < ITER; ++i) v[i].load_whole(x + (u0 + (b * ITER + i) * nw + warp) * WCOLS + piece * 16, wide);
       return;
     }
 #pragma unroll
@@ -532,11 +546,12 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 5 : 3) quantize_tile_ker
     }
     __syncthreads();
   }
+  const bool wide = ((reinterpret_cast<uintptr_t>(p.x) | (size_t)p.ld * sizeof(T)) & 31) == 0;
   const bool inside = p.vec && r0 + 128 <= p.rows && c0 + 128 <= p.cols;
   if (inside) {
     const T* x = static_cast<const T*>(p.x) + (r0 + warp * 8 + (lane >> 2)) * p.ld + c0 + (lane & 3) * 16;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i].load_whole(x + (i >> 1) * 64 * p.ld + (i & 1) * 64);
+    for (int i = 0; i < 4; ++i) v[i].load_whole(x + (i >> 1) * 64 * p.ld + (i & 1) * 64, wide);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -601,7 +616,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 5 : 3) quantize_tile_ker
     }
     cluster_sync_all();   // (the others have read cmax)
   }
-  const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;   // (16-byte alignment is all that is asked)
+  const bool wide_out = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;   // (16-byte alignment is all that is asked)
   // a work item: 32 rows of the column(s) in one 32-bit word
 #pragma unroll 1
   for (int item = t; item < 4 * 128 / CW; item += 256) {
@@ -649,7 +664,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 5 : 3) quantize_tile_ker
       }
     }
     uint8_t* d = p.out + tc * 8192 + ch * 2048 + cw * CW * 16;
-    if (CW == 2 && wide) {   // two columns' codes as one store
+    if (CW == 2 && wide_out) {   // two columns' codes as one store
       asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d), "r"(code[0][0]),
                    "r"(code[0][1]), "r"(code[0][2]), "r"(code[0][3]), "r"(code[CW - 1][0]), "r"(code[CW - 1][1]),
                    "r"(code[CW - 1][2]), "r"(code[CW - 1][3])
@@ -713,6 +728,7 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* packed, 
   const float* gs = reinterpret_cast<const float*>(packed + L.row_off()) + (long long)ty * 128;
   const long long r0 = (long long)ty * 128, c0 = (long long)tx * 128;
   if (VEC) {   // 8 rows x 32 columns a warp step, eight columns a lane
+    const bool wide = ((reinterpret_cast<uintptr_t>(y) | (size_t)cols * sizeof(T)) & 31) == 0;
     uint32_t w[8];
     uint8_t sb[8];
     float g[2] = {1.f, 1.f};
@@ -745,6 +761,12 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* packed, 
         }
         *reinterpret_cast<uint4*>(out) = make_uint4(o[0], o[1], o[2], o[3]);
       } else {
+        if (wide && k + 4 < cols) {
+          asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out), "f"(v[0]), "f"(v[1]),
+                       "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                       : "memory");
+          continue;
+        }
         reinterpret_cast<float4*>(out)[0] = make_float4(v[0], v[1], v[2], v[3]);
         if (k + 4 < cols) reinterpret_cast<float4*>(out)[1] = make_float4(v[4], v[5], v[6], v[7]);
       }

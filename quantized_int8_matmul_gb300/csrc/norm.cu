@@ -427,7 +427,7 @@ template <typename T, typename I, bool VEC>
 __global__ void __launch_bounds__(256) s8_dequantize_rows_kernel(const int8_t* q, const float* scale, I total, I H,
                                                                  T* y) {
   chain_wait();
-  constexpr int STEPS = 4;
+  constexpr int STEPS = 2;
   uint2 raw[STEPS];
   const I base = (I)blockIdx.x * (256 * 8 * STEPS) + threadIdx.x * 8;
 #pragma unroll
@@ -436,6 +436,7 @@ __global__ void __launch_bounds__(256) s8_dequantize_rows_kernel(const int8_t* q
     if (VEC && i < total && total - i >= 8) raw[s] = *reinterpret_cast<const uint2*>(q + i);
   }
   chain_release();
+  const bool wide = (reinterpret_cast<uintptr_t>(y) & 31) == 0;
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {
     const I i = base + (I)s * (256 * 8);
@@ -453,8 +454,14 @@ __global__ void __launch_bounds__(256) s8_dequantize_rows_kernel(const int8_t* q
         for (int e = 0; e < 8; ++e)
           f[e] = __fmul_rn((float)(int8_t)(w[e >> 2] >> (8 * (e & 3))), __ldg(scale + (i + e) / H));
       }
+      if (sizeof(T) == 4 && wide) {   // a whole 32-byte sector a lane
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(y + i), "f"(f[0]), "f"(f[1]),
+                     "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+                     : "memory");
+      } else {
 #pragma unroll
-      for (int e = 0; e < 8; e += Vec<T>::E) *reinterpret_cast<uint4*>(y + i + e) = Vec<T>::pack(f + e);
+        for (int e = 0; e < 8; e += Vec<T>::E) *reinterpret_cast<uint4*>(y + i + e) = Vec<T>::pack(f + e);
+      }
     } else {
       for (int e = 0; e < 8 && total - i > (I)e; ++e)
         y[i + e] = from_f<T>(__fmul_rn((float)q[i + e], __ldg(scale + (i + e) / H)));
@@ -877,7 +884,7 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
 template <typename T, typename I>
 cudaError_t launch_dequantize_i(const int8_t* q, const float* scale, long long M, int H, T* y, cudaStream_t s) {
   const long long total = M * H;
-  const unsigned grid = (unsigned)((total + 8191) / 8192);
+  const unsigned grid = (unsigned)((total + 4095) / 4096);
   const bool vec = (reinterpret_cast<uintptr_t>(q) % 8) == 0 && (reinterpret_cast<uintptr_t>(y) % 16) == 0;
   auto kern = vec ? s8_dequantize_rows_kernel<T, I, true> : s8_dequantize_rows_kernel<T, I, false>;
   return launch_chained(kern, grid, 256, 0, 1, s, q, scale, (I)total, (I)H, y);
