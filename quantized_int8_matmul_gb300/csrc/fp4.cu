@@ -693,13 +693,6 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 5 : 3) quantize_tile_ker
 // 8192 x 4096 to bf16 14.2 us (6.0 TB/s, 90 % of a copy's rate); 4099 x 1021 to
 // float32, element by element from the tile in shared memory, 7.4 us (2.6 TB/s).
 // ---------------------------------------------------------------------------
-// A code as a float: its three low bits moved to the exponent and mantissa of an
-// fp16 value are that value times 2^-14.
-__device__ __forceinline__ float decode(uint32_t c) {
-  const float m = __half2float(__ushort_as_half((unsigned short)((c & 7u) << 9))) * 16384.f;
-  return (c & 8u) ? -m : m;
-}
-
 // Eight codes, the first in the lowest bits, by the conversion to fp16 pairs.
 __device__ __forceinline__ void decode8(uint32_t w, float (&v)[8]) {
   uint32_t h[4];
@@ -727,31 +720,38 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* packed, 
   const uint8_t* sf = packed + L.scale_off() + ti * (512 * ATOMS);
   const float* gs = reinterpret_cast<const float*>(packed + L.row_off()) + (long long)ty * 128;
   const long long r0 = (long long)ty * 128, c0 = (long long)tx * 128;
-  if (VEC) {   // 8 rows x 32 columns a warp step, eight columns a lane
-    const bool wide = ((reinterpret_cast<uintptr_t>(y) | (size_t)cols * sizeof(T)) & 31) == 0;
-    uint32_t w[8];
-    uint8_t sb[8];
-    float g[2] = {1.f, 1.f};
+  // 8 rows x 32 columns a warp step, eight columns a lane
+  const bool wide = ((reinterpret_cast<uintptr_t>(y) | (size_t)cols * sizeof(T)) & 31) == 0;
+  uint32_t w[8];
+  uint8_t sb[8];
+  float g[2] = {1.f, 1.f};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int ch = i & 3, rin = (i >> 2) * 64 + warp * 8 + (lane >> 2);
-      const int ks = ch * (32 / BLOCK) + (BLOCK == 16 ? (lane & 3) >> 1 : 0);
-      w[i] = *reinterpret_cast<const uint32_t*>(codes + ch * 2048 + rin * 16 + (lane & 3) * 4);
-      sb[i] = sf[(ks >> 2) * 512 + (rin & 31) * 16 + (rin >> 5) * 4 + (ks & 3)];
-      if (BLOCK == 16 && ch == 0 && r0 + rin < rows) g[i >> 2] = gs[rin];
-    }
-    chain_release();
+  for (int i = 0; i < 8; ++i) {
+    const int ch = i & 3, rin = (i >> 2) * 64 + warp * 8 + (lane >> 2);
+    const int ks = ch * (32 / BLOCK) + (BLOCK == 16 ? (lane & 3) >> 1 : 0);
+    w[i] = *reinterpret_cast<const uint32_t*>(codes + ch * 2048 + rin * 16 + (lane & 3) * 4);
+    sb[i] = sf[(ks >> 2) * 512 + (rin & 31) * 16 + (rin >> 5) * 4 + (ks & 3)];
+    if (BLOCK == 16 && ch == 0 && r0 + rin < rows) g[i >> 2] = gs[rin];
+  }
+  chain_release();
+  // rows that start off 16 bytes: a warp's eight rows through shared memory, then a
+  // row at a time, neighbouring lanes neighbouring elements
+  constexpr int PITCH = 128 + 16 / (int)sizeof(T);
+  __shared__ __align__(16) T rows_s[VEC ? 1 : 8 * 8 * PITCH];
+  T* buf = rows_s + (VEC ? 0 : warp * 8 * PITCH);
+  const int n = (int)min(128ll, cols - c0);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int ch = i & 3, rin = (i >> 2) * 64 + warp * 8 + (lane >> 2);
-      const long long row = r0 + rin, k = c0 + ch * 32 + (lane & 3) * 8;
-      if (row >= rows || k >= cols) continue;
-      const float s = BLOCK == 16 ? e4m3_to_f(sb[i]) : e8m0_to_f(sb[i]);
-      float v[8];
-      decode8(w[i], v);
-      mul8(v, s);
-      if (BLOCK == 16) mul8(v, g[i >> 2]);
-      T* out = y + row * cols + k;   // cols is a multiple of 16 bytes: 8 columns lie inside, or 4 of float32
+  for (int i = 0; i < 8; ++i) {
+    const int ch = i & 3, rin = (i >> 2) * 64 + warp * 8 + (lane >> 2);
+    const long long row = r0 + rin, k = c0 + ch * 32 + (lane & 3) * 8;
+    const float s = BLOCK == 16 ? e4m3_to_f(sb[i]) : e8m0_to_f(sb[i]);
+    float v[8];
+    decode8(w[i], v);
+    mul8(v, s);
+    if (BLOCK == 16) mul8(v, g[i >> 2]);
+    // cols is a multiple of 16 bytes (VEC): 8 columns lie inside, or 4 of float32
+    T* out = VEC ? y + row * cols + k : buf + (lane >> 2) * PITCH + ch * 32 + (lane & 3) * 8;
+    if (!VEC || (row < rows && k < cols)) {
       if (sizeof(T) == 2) {
         uint32_t o[4];
 #pragma unroll
@@ -760,41 +760,44 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* packed, 
           o[e] = *reinterpret_cast<uint32_t*>(&b);
         }
         *reinterpret_cast<uint4*>(out) = make_uint4(o[0], o[1], o[2], o[3]);
+      } else if (VEC && wide && k + 4 < cols) {
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out), "f"(v[0]), "f"(v[1]),
+                     "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                     : "memory");
       } else {
-        if (wide && k + 4 < cols) {
-          asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out), "f"(v[0]), "f"(v[1]),
-                       "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-                       : "memory");
-          continue;
-        }
         reinterpret_cast<float4*>(out)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        if (k + 4 < cols) reinterpret_cast<float4*>(out)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        if (!VEC || k + 4 < cols) reinterpret_cast<float4*>(out)[1] = make_float4(v[4], v[5], v[6], v[7]);
       }
     }
-  } else {   // the tile through shared memory; one row a warp step, neighbouring lanes neighbouring columns
-    __shared__ __align__(16) uint8_t cs[8192 + 1024];
-    for (int i = threadIdx.x; i < 512; i += 256)
-      reinterpret_cast<uint4*>(cs)[i] = reinterpret_cast<const uint4*>(codes)[i];
-    if (threadIdx.x < 32 * ATOMS)
-      reinterpret_cast<uint4*>(cs + 8192)[threadIdx.x] = reinterpret_cast<const uint4*>(sf)[threadIdx.x];
-    chain_release();
-    __syncthreads();
+    if (VEC || ch < 3) continue;
+    __syncwarp();
+    const long long first = r0 + (i >> 2) * 64 + warp * 8;
+    const int some = (int)max(0ll, min(8ll, rows - first));
 #pragma unroll 4
-    for (int i = 0; i < 16; ++i) {
-      const int rin = i * 8 + warp;
-      if (r0 + rin >= rows) break;
-      const float g = BLOCK == 16 ? gs[rin] : 1.f;
+    for (int r = 0; r < some; ++r) {
+      T* d = y + (first + r) * cols + c0;
+      const T* from = buf + r * PITCH;
+      if (sizeof(T) == 4) {
 #pragma unroll
-      for (int ch = 0; ch < 4; ++ch) {
-        const long long k = c0 + ch * 32 + lane;
-        const uint32_t c = cs[ch * 2048 + rin * 16 + (lane >> 1)] >> (4 * (lane & 1));
-        const int ks = ch * (32 / BLOCK) + (BLOCK == 16 ? lane >> 4 : 0);
-        const uint8_t sb = cs[8192 + (ks >> 2) * 512 + (rin & 31) * 16 + (rin >> 5) * 4 + (ks & 3)];
-        float v = __fmul_rn(decode(c), BLOCK == 16 ? e4m3_to_f(sb) : e8m0_to_f(sb));
-        if (BLOCK == 16) v = __fmul_rn(v, g);
-        if (k < cols) y[(r0 + rin) * cols + k] = (T)v;
+        for (int j = 0; j < 4; ++j)
+          if (j * 32 + lane < n) d[j * 32 + lane] = from[j * 32 + lane];
+      } else {   // pairs of bf16 from the first 4-byte boundary on
+        const int odd = (int)(reinterpret_cast<uintptr_t>(d) >> 1) & 1;
+        if (odd && lane == 0) d[0] = from[0];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int e = odd + j * 64 + 2 * lane;
+          if (e + 1 < n) {
+            const uint32_t lo = reinterpret_cast<const uint16_t*>(from)[e];
+            const uint32_t hi = reinterpret_cast<const uint16_t*>(from)[e + 1];
+            *reinterpret_cast<uint32_t*>(d + e) = lo | hi << 16;
+          } else if (e < n) {
+            d[e] = from[e];
+          }
+        }
       }
     }
+    __syncwarp();
   }
 }
 
