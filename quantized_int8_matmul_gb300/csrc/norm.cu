@@ -148,6 +148,27 @@ __device__ __forceinline__ uint4 add_vec(const uint4& x, const uint4& r) {
   for (int e = 0; e < E; ++e) a[e] = __fadd_rn(a[e], b[e]);
   return Vec<T>::pack(a);
 }
+// The E elements that start s before vector v of a 16-byte aligned array (s the
+// same for the whole warp; v > 0 unless s is 0), from the two vectors they lie in.
+template <typename T>
+__device__ __forceinline__ uint4 load_back(const void* base, int v, int s) {
+  const uint4* p = static_cast<const uint4*>(base) + v;
+  const uint4 b = __ldg(p);
+  if (s == 0) return b;
+  const uint4 a = __ldg(p - 1);
+  uint32_t c[5];
+  switch (sizeof(T) == 4 ? s : (s + 1) >> 1) {   // words that a gives
+    case 1: c[0] = a.w, c[1] = b.x, c[2] = b.y, c[3] = b.z, c[4] = b.w; break;
+    case 2: c[0] = a.z, c[1] = a.w, c[2] = b.x, c[3] = b.y, c[4] = b.z; break;
+    case 3: c[0] = a.y, c[1] = a.z, c[2] = a.w, c[3] = b.x, c[4] = b.y; break;
+    default: c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w, c[4] = b.x; break;
+  }
+  if (sizeof(T) == 2 && (s & 1)) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) c[k] = c[k] >> 16 | c[k + 1] << 16;
+  }
+  return make_uint4(c[0], c[1], c[2], c[3]);
+}
 // The weight's elements at the same places (either type; kAligned: 16-byte aligned).
 template <typename T, int W>
 __device__ __forceinline__ void load_w(const void* w, int w_f32, int j, int t, int G, int s, int n, float* v) {
@@ -189,6 +210,12 @@ __device__ __forceinline__ void load_w(const void* w, int w_f32, int j, int t, i
       }
     }
   } else {
+    const int i0 = elem<T, W>(j, 0, t, G, s);
+    if (W == kShifted && i0 >= 0 && i0 + s + E <= n && (w_f32 != 0) == (sizeof(T) == 4) &&
+        (reinterpret_cast<uintptr_t>(w) & 15) == 0) {
+      Vec<T>::unpack(load_back<T>(w, (i0 + s) / E, s), v);
+      return;
+    }
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const int i = elem<T, W>(j, e, t, G, s);
