@@ -70,12 +70,10 @@ __device__ __forceinline__ uint8_t block_scale(unsigned max_bits, float u, float
     return zero ? 255 : (uint8_t)byte;
   }
   const float t = __fmul_rn(__fmul_rn(__uint_as_float(max_bits), u), kR6);
-  zero = !(t > 0.f) || !(u > 0.f);
-  if (zero) return 0;
   const uint8_t b = __nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3);
-  zero = b == 0;
-  mul = zero ? 0.f : __fdiv_rn(u, e4m3_to_f(b));
-  return b;
+  zero = !(t > 0.f) || !(u > 0.f) || b == 0;
+  mul = __fdiv_rn(u, zero ? 1.f : e4m3_to_f(b));
+  return zero ? 0 : b;
 }
 
 template <typename T>
@@ -401,6 +399,120 @@ __global__ void __launch_bounds__(VEC ? 1024 : 896) quantize_rows_kernel(const F
     for (int i = threadIdx.x; i < atoms * 2; i += blockDim.x)
       *reinterpret_cast<Word*>(sf + (size_t)(atom0 + (i >> 1)) * 512 + (i & 1) * 16) =
           reinterpret_cast<const Word*>(sfs)[i];
+  }
+}
+
+// The same for block 16 and many long rows: a ring of groups of rows (J = 1: two
+// rows each) filled by bulk copies, so that the next groups are on their way while
+// one waits for its rows' maxima and is turned into codes. A group is read from
+// shared memory twice, its blocks' maxima stay in registers. 4096 x 11008 bf16:
+// 26.8 us (4.3 TB/s, 64 % of a copy's rate).
+// Waits are bounded (common.cuh).
+constexpr int RING_THREADS = 512, RING_STEPS = 4, RING_MAX = 8;
+constexpr unsigned SITE_ROWS = 0x530;
+__global__ void __launch_bounds__(RING_THREADS, 2) quantize_rows_ring_kernel(const Fp4QuantArgs p, const int groups,
+                                                                            const int slots, const uint32_t pitch) {
+  using T = __nv_bfloat16;
+  constexpr int J = 1, WROWS = 2 * J, WCOLS = 512 / WROWS, LANES = 32 / WROWS, UC = LANES / 2, NW = RING_THREADS / 32;
+  constexpr int PER_TILE = 64 / J;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ unsigned rowmax[2][8];
+  __shared__ uint64_t full[RING_MAX];
+  chain_wait();
+  const Fp4Layout L(p.rows, p.cols, 16);
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int ri = lane / LANES, ra = ri & 1, rj = ri >> 1, piece = lane & (LANES - 1), half = piece & 1;
+  const int chunks = (int)L.kt * 4, units = (chunks + UC - 1) / UC, atoms = (int)L.kt * 2;
+  const uint32_t line = (uint32_t)p.cols * (uint32_t)sizeof(T);   // a row's bytes
+  uint8_t* sfs = smem + (size_t)slots * WROWS * pitch;   // two groups' scales
+  auto first_row = [&](int g) {
+    const int tile = g / PER_TILE, in = g - tile * PER_TILE;
+    return (long long)tile * 128 + 2 * (in & 15) + 32 * J * (in >> 4);
+  };
+  auto fill = [&](int k) {   // one thread: the CTA's k-th group
+    const long long r0 = first_row(blockIdx.x + k * gridDim.x);
+    uint64_t* bar = &full[k % slots];
+    uint32_t bytes = 0u;
+#pragma unroll
+    for (int r = 0; r < WROWS; ++r)
+      if (r0 + (r & 1) + 32 * (r >> 1) < p.rows) bytes += line;
+    mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+    for (int r = 0; r < WROWS; ++r) {
+      const long long row = r0 + (r & 1) + 32 * (r >> 1);
+      if (row < p.rows)
+        bulk_load(smem_u32(smem) + (uint32_t)((k % slots) * WROWS + r) * pitch, static_cast<const T*>(p.x) + row * p.ld,
+                  line, bar);
+    }
+  };
+  const int mine = (groups - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+  if (t < 8) rowmax[0][t] = 0u;
+  if (t == 0) {
+    for (int i = 0; i < slots; ++i) mbar_init(&full[i], 1);
+    fence_mbarrier_init();
+    for (int k = 0; k < slots && k < mine; ++k) fill(k);
+  }
+  __syncthreads();
+  for (int k = 0; k < mine; ++k) {
+    const int slot = k % slots;
+    if (!mbar_wait(&full[slot], (uint32_t)((k / slots) & 1), nullptr, p.err, SITE_ROWS)) {
+      // (the copies of the later slots are waited for, with the same limit, before the CTA ends)
+      for (int i = 1; i < slots && k + i < mine; ++i)
+        mbar_wait(&full[(k + i) % slots], (uint32_t)(((k + i) / slots) & 1), nullptr, p.err, SITE_ROWS);
+      break;
+    }
+    const int g = blockIdx.x + k * gridDim.x, tile = g / PER_TILE, in = g - tile * PER_TILE;
+    const int c2 = 2 * (in & 15), j0 = J * (in >> 4), rin = c2 + ra + 32 * (j0 + rj);
+    const long long row = (long long)tile * 128 + rin;
+    const bool rv = row < p.rows;
+    const T* x = reinterpret_cast<const T*>(smem + (size_t)(slot * WROWS + ri) * pitch);
+    const int n = rv ? (int)p.cols : 0;
+    auto get = [&](int un) {   // zeros past the end
+      const int c = un * WCOLS + piece * 16;
+      Raw16<T> v;
+      if (c + 16 <= n) v.load_whole(x + c);
+      else v.load(x, c, n, true);
+      return v;
+    };
+    unsigned m = 0u, vm[RING_STEPS];
+#pragma unroll
+    for (int i = 0; i < RING_STEPS; ++i) {
+      vm[i] = 0u;
+      if (warp + i * NW < units) vm[i] = get(warp + i * NW).max_bits();
+      m = max(m, vm[i]);
+    }
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (piece == 0) atomicMax(&rowmax[k & 1][ri], m);
+    __syncthreads();
+    const float gs = row_scale(rowmax[k & 1][ri]), u = __fdiv_rn(1.f, gs);
+    if (warp == 0 && piece == 0 && rv) reinterpret_cast<float*>(p.out + L.row_off())[row] = gs;
+    if (t < 8) rowmax[(k + 1) & 1][t] = 0u;
+    uint8_t* codes = p.out + (size_t)tile * L.kt * 8192 + rin * 16 + half * 8;
+    uint8_t* ss = sfs + (size_t)(k & 1) * atoms * 8 * J + ra * 4 * J + rj * 4;
+#pragma unroll
+    for (int i = 0; i < RING_STEPS; ++i) {
+      const int un = warp + i * NW, ch = un * UC + (piece >> 1);
+      if (un < units) {
+        uint8_t sc;
+        const uint2 code = get(un).template codes<16>(vm[i], u, sc);
+        if (ch < chunks) {
+          const int ks = ch * 2 + half;
+          if (rv) *reinterpret_cast<uint2*>(codes + (size_t)ch * 2048) = code;
+          ss[(ks >> 2) * (8 * J) + (ks & 3)] = sc;
+        }
+      }
+    }
+    __syncthreads();
+    if (t == 0 && k + slots < mine) {
+      fence_proxy_async_smem();   // the slot was read through the generic proxy
+      fill(k + slots);
+    }
+    using Word = typename ScaleWord<J>::type;   // a row's J scale words of an atom at a time
+    uint8_t* sf = p.out + L.scale_off() + (size_t)tile * L.kt * 1024 + c2 * 16 + j0 * 4;
+    const Word* from = reinterpret_cast<const Word*>(sfs + (size_t)(k & 1) * atoms * 8 * J);
+    for (int i = t; i < atoms * 2; i += RING_THREADS)
+      *reinterpret_cast<Word*>(sf + (size_t)(i >> 1) * 512 + (i & 1) * 16) = from[i];
   }
 }
 
@@ -849,12 +961,44 @@ cudaError_t launch_rows_j(const Fp4QuantArgs& a, cudaStream_t s) {
   return launch_chained(kern, dim3(grid, segments), nw * 32, smem, 1, s, a, staged, 0);
 }
 
+// Long bf16 rows by the ring, where two groups of two rows leave room for a second
+// CTA on the SM and there are groups for two rounds. 4096 x 11008: 35.0 us without,
+// 26.9 with; 2000 x 12288 19.4 and 17.9. The two barriers a group cost shorter rows
+// more than they gain (4096 x 8192: 22.9 and 22.5; 8192 x 4096: 20.0 and 21.8 at
+// best), and float32 rows, half as many elements a slot (1531 x 6144: 14.7 and 16.6).
+bool launch_rows_ring(const Fp4QuantArgs& a, cudaStream_t s, cudaError_t& e) {
+  using T = __nv_bfloat16;
+  const Fp4Layout L(a.rows, a.cols, 16);
+  const long long row = a.cols * (long long)sizeof(T);
+  if (!a.vec || row % 16 != 0 || row <= 16 * 1024 || a.rows < 8 * num_sms()) return false;
+  const uint32_t pitch = (uint32_t)row + 16;   // (keeps the rows off each other's banks)
+  const int slots = (int)std::min<long long>(RING_MAX, (106 * 1024 - L.kt * 32) / (2ll * pitch));
+  if (slots < 2 || L.kt * 128 > RING_STEPS * (RING_THREADS / 32) * 256) return false;
+  auto kern = quantize_rows_ring_kernel;
+  static std::once_flag once[64];
+  int dev = 0;
+  e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && (dev < 0 || dev >= 64)) e = cudaErrorInvalidDevice;
+  if (e != cudaSuccess) return true;
+  std::call_once(once[dev],
+                 [&] { e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 112 * 1024); });
+  if (e != cudaSuccess) return true;
+  const int groups = (int)(L.rt * 64);
+  e = launch_chained(kern, (unsigned)std::min(groups, 2 * num_sms()), RING_THREADS,
+                     (size_t)slots * 2 * pitch + (size_t)L.kt * 32, 1, s, a, groups, slots, pitch);
+  return true;
+}
+
 template <typename T, int BLOCK>
 cudaError_t launch_rows(const Fp4QuantArgs& a, cudaStream_t s) {
+  if (BLOCK == 16 && sizeof(T) == 2) {
+    cudaError_t e = cudaSuccess;
+    if (launch_rows_ring(a, s, e)) return e;
+  }
   // Two rows a CTA where more would not give every SM one (137 x 4100 bf16, block 16:
   // 5.2 us with four, 3.8 with two; block 32 of aligned rows has its segments
-  // instead), or where four would be too long for two CTAs' registers on an SM
-  // (4096 x 11008: 38.8 and 35.4; 8192 x 4096: 20.4 and 22.0).
+  // instead), or where four would be too long for two CTAs' registers on an SM and the
+  // ring does not apply (1000 x 11008 and the like; 4096 x 11008 38.8 and 35.4).
   const bool few = (a.rows + 127) / 128 * 32 < num_sms();
   if (BLOCK == 32) return a.rows <= 32 || (few && !a.vec) ? launch_rows_j<T, BLOCK, 1>(a, s)
                                                             : launch_rows_j<T, BLOCK, 4>(a, s);

@@ -337,6 +337,7 @@ struct Fp4QuantArgs {
   int vec;                     // every row starts on 16 bytes
   uint8_t* out;                // rows only: packed [rows][cols]; otherwise packed [cols][rows]
   uint8_t* out_rows;           // not rows only: packed [rows][cols] as well, or null
+  unsigned* err;               // device error word
 };
 cudaError_t launch_fp4_quantize(const Fp4QuantArgs& a, bool bf16, int block, bool rows_only, cudaStream_t s,
                                 const char** kernel_name);

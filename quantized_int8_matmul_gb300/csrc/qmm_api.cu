@@ -1738,9 +1738,12 @@ static qmm_status fp4_quantize(const void* x, int x_dtype, int64_t rows, int64_t
     return QMM_ERR_INVALID_ARG;
   if (way != 0 && (!packed_t || !aligned16(packed_t) || packed_t_bytes < fp4_packed_bytes(cols, rows, block)))
     return QMM_ERR_INVALID_ARG;
+  unsigned* err = err_word();
+  if (!err) return QMM_ERR_CUDA;
   cudaGetLastError();
   const int es = x_dtype == QMM_BF16 ? 2 : 4;
   Fp4QuantArgs a{};
+  a.err = err;
   a.x = x;
   a.rows = rows;
   a.cols = cols;

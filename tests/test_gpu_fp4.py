@@ -73,6 +73,26 @@ def test_quantise_strides_and_alignment(dt, block, ld, off):
     check_values(b, xt)
 
 
+@pytest.mark.parametrize("R,C,ld", [(1217, 8208, 8208), (1300, 11008, 11016), (1400, 13200, 13200)])
+def test_quantise_many_long_rows(R, C, ld):
+    """Rows that go through shared memory: the values, a row of zeros, non-finite ones, and the bytes of the
+    same rows packed a few at a time."""
+    x = make(R, ld, torch.bfloat16, C)
+    x[7] = 0
+    x[64, 5], x[R - 1, C - 1] = float("nan"), float("inf")
+    x = x[:, :C]
+    m = q.qmm_fp4_quantize(x, block=16)
+    q.check_device_error()
+    y = q.qmm_fp4_dequantize(m, out_dtype=torch.float32)
+    for r in (0, 128, 1152):
+        part = q.qmm_fp4_dequantize(q.qmm_fp4_quantize(x[r:r + 60], block=16), out_dtype=torch.float32)
+        assert torch.equal(torch.nan_to_num(y[r:r + 60], nan=-7.0), torch.nan_to_num(part, nan=-7.0))
+    assert (y[7] == 0).all() and torch.isnan(y[64]).all() and torch.isnan(y[R - 1]).all()
+    rows = [0, 1, 31, 32, 63, 65, 127, 128, 777, R - 2]
+    want = O.fp4_values(f32(x[rows]), 16, False)
+    assert np.array_equal(y[rows].cpu().numpy(), want)
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("block", [16, 32])
 def test_zeros_extremes_and_non_finite(dt, block):
