@@ -235,7 +235,7 @@ struct ScaleWord<1> { using type = uint32_t; };
 // neighbouring rows' 16 bytes) the work of one CTA, and of scales (two rows'
 // 16-byte lines of an atom, whose 4-byte parts are rows 32 apart) of one or two.
 // Block 32 takes a segment of the columns a CTA (blockIdx.y). 8192 x 4096 bf16: block
-// 32 14.9 us (5.7 TB/s, 85 % of a copy's rate), block 16 20.4 (63 %: a row has to be
+// 32 14.9 us (5.7 TB/s, 85 % of a copy's rate), block 16 20.0 (64 %: a row has to be
 // whole before its first code, so its loads, maximum and codes do not overlap within
 // a CTA; the registers that hold it limit an SM to 32 warps). A warp's steps of a
 // batch (ITER) are loaded together; with block 16 a row whose steps are one batch
@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(256) zero_kernel(unsigned* a, int na, unsigned
 // ---------------------------------------------------------------------------
 // Largest magnitudes of the columns (and the rows) into the packed buffers' max
 // words: 64 rows x 256 columns a CTA, eight columns a lane. 8192 x 4096 bf16: 11 of
-// the 27.8 us that block 16 takes along the columns (the second reading of x is
+// the 27.0 us that block 16 takes along the columns (the second reading of x is
 // largely from L2).
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256, VEC ? 4 : 2) absmax_kernel(const Fp4QuantArgs p, unsigned* colmax,
@@ -614,8 +614,8 @@ __global__ void __launch_bounds__(256, VEC ? 4 : 2) absmax_kernel(const Fp4Quant
 // x of up to 8 tiles down): the tiles above each other are one cluster, and the
 // columns' maxima are taken over it -- one launch in place of a fill, a pass for
 // the maxima and this. 8192 x 4096 bf16: block 32 both ways 19.6 us (5.3 TB/s, 79 %
-// of a copy's rate; issue slots 56 % busy), columns alone 15.5; block 16 with its
-// maxima 36.5 and 27.8. 4099 x 1021 float32, block 16, columns: 8.6 us.
+// of a copy's rate; issue slots 56 % busy), columns alone 15.1; block 16 with its
+// maxima 36.4 and 27.0. 4099 x 1021 float32, block 16, columns: 8.6 us.
 template <typename T>
 struct TileSmem {
   static constexpr int PITCH = 128 * (int)sizeof(T) + 16;   // bytes; 16 more keep row accesses off each other's banks
@@ -803,7 +803,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 5 : 3) quantize_tile_ker
 // ---------------------------------------------------------------------------
 // Reading back: y[r][c] = code * block scale (* row scale), one CTA per tile.
 // 8192 x 4096 to bf16 14.2 us (6.0 TB/s, 90 % of a copy's rate); 4099 x 1021 to
-// float32, element by element from the tile in shared memory, 7.4 us (2.6 TB/s).
+// float32, whose rows start off 16 bytes, 5.2 us (3.7 TB/s).
 // ---------------------------------------------------------------------------
 // Eight codes, the first in the lowest bits, by the conversion to fp16 pairs.
 __device__ __forceinline__ void decode8(uint32_t w, float (&v)[8]) {

@@ -339,9 +339,9 @@ __device__ __forceinline__ float max_abs(float a, float b) {
 // NV vectors a thread. NV = 0: rows of any length, read twice.
 // 8192 x 4096 bf16: 36.2 us with a residual (6.5 TB/s, 97 % of a copy's rate), 18.9
 // without (5.3 TB/s: then a CTA's two barriers a row show); 4096 x 11008 float32
-// with one 103 us (85 %). 1009 x 5003 float32, whose rows start off 16 bytes: 9.6 us
-// (2.6 TB/s; the neighbours' words are exchanged through shuffles, and the first
-// and last vectors of a row go element by element).
+// with one 103 us (85 %). Rows that start off 16 bytes: 8192 x 4095 bf16 57 us,
+// 1009 x 5003 float32 8.9 us (2.8 TB/s; the weight comes by two vectors and a shift,
+// 9.6 us element by element; a row's first and last vectors go element by element).
 template <typename T, int W, int NV>
 __global__ void __launch_bounds__(1024) rms_norm_s8_kernel(const NormArgs p) {
   constexpr int E = Vec<T>::E;
@@ -448,8 +448,9 @@ __global__ void __launch_bounds__(1024) rms_norm_s8_kernel(const NormArgs p) {
 }
 
 // y[i] = q[i] * scale[i / H] over the flat [M * H] array, eight elements a step
-// (both arrays are contiguous, so no width is unaligned). 8192 x 4096 to bf16:
-// 16.5 us, 6.1 TB/s, 91 % of a copy's rate.
+// (both arrays are contiguous, so no width is unaligned). 8192 x 4096 to bf16: 16.3
+// us, 6.2 TB/s, 92 % of a copy's rate; 4096 x 11008 to float32 33.9 us, 99 % (42.8
+// with a lane's 32 bytes in two stores).
 template <typename T, typename I, bool VEC>
 __global__ void __launch_bounds__(256) s8_dequantize_rows_kernel(const int8_t* q, const float* scale, I total, I H,
                                                                  T* y) {
