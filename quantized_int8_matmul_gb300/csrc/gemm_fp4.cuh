@@ -6,6 +6,8 @@
 #include "kernels.h"
 #include "tma.h"
 
+#include <climits>
+
 namespace qmm {
 namespace gfp4 {
 
@@ -129,19 +131,28 @@ __device__ __forceinline__ void store_box(const GemmFp4Args& p, const CUtensorMa
   }
   __syncwarp();
   const int rows = (int)min(32ll, p.M - row0);
-  for (int r = 0; r < rows; ++r) {
-    uint32_t v;   // this lane's 4 bytes of the row
-    const uint32_t a = stg + (uint32_t)r * 128u + (uint32_t)((((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-    const long long row = row0 + r;
-    if (p.c_f32) {
-      const long long n = n0 + lane;
-      if (n < p.N) static_cast<uint32_t*>(p.C)[row * p.N + n] = v;
-    } else {
-      const long long n = n0 + 2 * lane;
-      uint16_t* c = static_cast<uint16_t*>(p.C) + row * p.N + n;
-      if (n < p.N) c[0] = (uint16_t)v;
-      if (n + 1 < p.N) c[1] = (uint16_t)(v >> 16);
+  const int n = (int)min((long long)INT_MAX, p.N - n0);   // columns from n0 on
+  uint8_t* c = static_cast<uint8_t*>(p.C) + (row0 * p.N + n0) * (p.c_f32 ? 4 : 2);
+  const long long pitch = p.N * (p.c_f32 ? 4 : 2);
+  for (int r0 = 0; r0 < rows; r0 += 8) {   // eight rows at a time: each waits for its words
+    uint32_t v[8];   // this lane's 4 bytes of the rows
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t a =
+          stg + (uint32_t)(r0 + i) * 128u + (uint32_t)((((lane >> 2) ^ ((r0 + i) & 7)) << 4) + (lane & 3) * 4);
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[i]) : "r"(a));
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (r0 + i >= rows) break;
+      if (p.c_f32) {
+        if (lane < n) reinterpret_cast<uint32_t*>(c)[lane] = v[i];
+      } else {   // (shifting pairs to 4-byte boundaries through shuffles was slower)
+        uint16_t* h = reinterpret_cast<uint16_t*>(c) + 2 * lane;
+        if (2 * lane < n) h[0] = (uint16_t)v[i];
+        if (2 * lane + 1 < n) h[1] = (uint16_t)(v[i] >> 16);
+      }
+      c += pitch;
     }
   }
   __syncwarp();

@@ -435,9 +435,10 @@ __global__ void __launch_bounds__(NT, 1)
       }
       if (!mbar_wait_cluster(&sm.acc_full[tl & 1], (uint32_t)((tl >> 1) & 1), &sm.abort_flag, p.err, SITE_ACC_FULL))
         break;
-      // the time that the next tile will take, if that is a whole one too: as this one did
+      // the time that the next tile will take, if that is a whole one too: as this one
+      // did (rows stored by the warps are spread as it is)
       const long long now = clock64();
-      const bool paced = tl > 0 && tl + 1 < my_tiles && work_at(sc, tl + 1, cid, ncl, n_tiles).width == 256;
+      const bool paced = tma_c && tl > 0 && tl + 1 < my_tiles && work_at(sc, tl + 1, cid, ncl, n_tiles).width == 256;
       const long long period = paced ? min(now - last, kPaceLimit) : 0;
       last = now;
       tc_fence_after();
