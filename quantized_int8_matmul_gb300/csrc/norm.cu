@@ -817,7 +817,7 @@ __global__ void __launch_bounds__(1024) rms_norm_backward_ring_kernel(const Norm
 }
 
 // out[i] = the sum of column i of part [count][n], in a fixed order: a cluster for
-// 32 columns, each CTA a run of the rows as 32 interleaved ones (eight loads of
+// 32 columns, each CTA a run of the rows as 32 interleaved ones (twelve loads of
 // each in flight), joined in rank order. 304 x 4096 shares: about 4 us, all latency.
 __global__ void __launch_bounds__(1024) sum_partials_kernel(const float* part, int count, int n, int split,
                                                             float* out) {
@@ -829,12 +829,12 @@ __global__ void __launch_bounds__(1024) sum_partials_kernel(const float* part, i
   const int i = c0 + threadIdx.x;
   float a = 0.f;
   if (i < n) {
-    for (int c = beg + threadIdx.y; c < end; c += 32 * 8) {
-      float v[8];
+    for (int c = beg + threadIdx.y; c < end; c += 32 * 12) {
+      float v[12];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = c + 32 * k < end ? part[(long long)(c + 32 * k) * n + i] : 0.f;
+      for (int k = 0; k < 12; ++k) v[k] = c + 32 * k < end ? part[(long long)(c + 32 * k) * n + i] : 0.f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) a += v[k];
+      for (int k = 0; k < 12; ++k) a += v[k];
     }
   }
   chain_release();
