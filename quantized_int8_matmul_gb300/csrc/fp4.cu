@@ -76,9 +76,6 @@ __device__ __forceinline__ uint8_t block_scale(unsigned max_bits, float u, float
   return zero ? 0 : b;
 }
 
-template <typename T>
-__device__ __forceinline__ float ld1(const T* p) { return (float)*p; }
-
 // Larger of each of two non-negative bf16 (a NaN wins), in one instruction.
 constexpr uint32_t kMag = 0x7fff7fffu;   // magnitudes of two bf16
 __device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
@@ -1000,9 +997,13 @@ cudaError_t launch_rows(const Fp4QuantArgs& a, cudaStream_t s) {
   // instead), or where four would be too long for two CTAs' registers on an SM and the
   // ring does not apply (1000 x 11008 and the like; 4096 x 11008 38.8 and 35.4).
   const bool few = (a.rows + 127) / 128 * 32 < num_sms();
-  if (BLOCK == 32) return a.rows <= 32 || (few && !a.vec) ? launch_rows_j<T, BLOCK, 1>(a, s)
-                                                            : launch_rows_j<T, BLOCK, 4>(a, s);
-  return few || (a.vec && a.cols > 8192) ? launch_rows_j<T, BLOCK, 1>(a, s) : launch_rows_j<T, BLOCK, 2>(a, s);
+  if constexpr (BLOCK == 32) {
+    if (a.rows <= 32 || (few && !a.vec)) return launch_rows_j<T, BLOCK, 1>(a, s);
+    return launch_rows_j<T, BLOCK, 4>(a, s);
+  } else {
+    if (few || (a.vec && a.cols > 8192)) return launch_rows_j<T, BLOCK, 1>(a, s);
+    return launch_rows_j<T, BLOCK, 2>(a, s);
+  }
 }
 
 template <typename T, int BLOCK, bool ROWS, bool CLUSTER>
