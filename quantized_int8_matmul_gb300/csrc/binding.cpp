@@ -141,15 +141,25 @@ PyObject* pair(PyObject* a, PyObject* b) {
   return r;
 }
 
-// A call of the C ABI without the interpreter lock (a launch waits where the
-// stream's queue is full).
-template <typename F>
-qmm_status unlocked(F f) {
-  qmm_status st;
-  Py_BEGIN_ALLOW_THREADS;
-  st = f();
-  Py_END_ALLOW_THREADS;
-  return st;
+// The interpreter lock let go for a call of the C ABI (a launch waits where the
+// stream's queue is full), and taken back however the scope is left.
+class Unlocked {
+ public:
+  Unlocked() : state_(PyEval_SaveThread()) {}
+  ~Unlocked() { PyEval_RestoreThread(state_); }
+  Unlocked(const Unlocked&) = delete;
+  Unlocked& operator=(const Unlocked&) = delete;
+
+ private:
+  PyThreadState* state_;
+};
+
+// fn(args...) without the lock. The pointers are arguments, so all of them are taken
+// while it is still held: a tensor without storage (inside a transform) raises there.
+template <typename... P, typename... A>
+qmm_status unlocked(qmm_status (*fn)(P...), A... args) {
+  Unlocked u;
+  return fn(static_cast<P>(args)...);
 }
 
 // x, weight, residual, eps, out, h_out, save_rstd, stream -> (q, scale, h, rstd)
@@ -177,11 +187,9 @@ PyObject* rms_norm_s8(PyObject* const* a) {
   Tensor rstd;
   if (save) rstd = empty({M}, F32, x);
   void* s = stream(a[7]);
-  const qmm_status st = unlocked([&] {
-    return qmm_rms_norm_s8(ptr(x), qmm_type(t), M, H, ldx, rp, ldr, ptr(w), qmm_type(w.scalar_type()), (float)eps,
-                           res ? ptr(h) : nullptr, static_cast<int8_t*>(ptr(q)), static_cast<float*>(ptr(scale)),
-                           save ? static_cast<float*>(ptr(rstd)) : nullptr, s);
-  });
+  const qmm_status st =
+      unlocked(qmm_rms_norm_s8, ptr(x), qmm_type(t), M, H, ldx, rp, ldr, ptr(w), qmm_type(w.scalar_type()), eps,
+               res ? ptr(h) : nullptr, ptr(q), ptr(scale), save ? ptr(rstd) : nullptr, s);
   if (st != QMM_OK) return PyLong_FromLong(st);
   PyObject* r = PyTuple_New(4);
   PyTuple_SET_ITEM(r, 0, wrap(q));
@@ -209,10 +217,8 @@ PyObject* s8_dequantize_rows(PyObject* const* a) {
   const Tensor& scale = need(a[1], {F32}, "scale", {M});
   const Tensor y = output(a[2], q.sizes(), float_type(a[3]), FLOATS, "out", q);
   void* s = stream(a[4]);
-  const qmm_status st = unlocked([&] {
-    return qmm_s8_dequantize_rows(static_cast<const int8_t*>(ptr(q)), static_cast<const float*>(ptr(scale)), M, H,
-                                  ptr(y), qmm_type(y.scalar_type()), s);
-  });
+  const qmm_status st =
+      unlocked(qmm_s8_dequantize_rows, ptr(q), ptr(scale), M, H, ptr(y), qmm_type(y.scalar_type()), s);
   return st != QMM_OK ? PyLong_FromLong(st) : wrap(y);
 }
 
@@ -243,11 +249,9 @@ PyObject* rms_norm_backward(PyObject* const* a) {
     have = bytes;
   }
   void* s = stream(a[7]);
-  const qmm_status st = unlocked([&] {
-    return qmm_rms_norm_backward(ptr(dy), lddy, ptr(h), ldh, dh, lddh, qmm_type(t), M, H, ptr(w),
-                                 qmm_type(w.scalar_type()), static_cast<const float*>(ptr(rstd)), ptr(dx),
-                                 static_cast<float*>(ptr(dw)), ws.defined() ? ptr(ws) : nullptr, have, s);
-  });
+  const qmm_status st = unlocked(qmm_rms_norm_backward, ptr(dy), lddy, ptr(h), ldh, dh, lddh, qmm_type(t), M, H, ptr(w),
+                                 qmm_type(w.scalar_type()), ptr(rstd), ptr(dx), ptr(dw),
+                                 ws.defined() ? ptr(ws) : nullptr, have, s);
   return st != QMM_OK ? PyLong_FromLong(st) : pair(wrap(dx), wrap(dw));
 }
 
@@ -265,9 +269,8 @@ PyObject* fp4_quantize(PyObject* const* a) {
   const int64_t rows = x.size(trans ? 1 : 0), cols = x.size(trans ? 0 : 1);
   const Tensor b = packed(a[3], rows, cols, block, "out", x);
   void* s = stream(a[4]);
-  const qmm_status st = unlocked([&] {
-    return qmm_fp4_quantize(ptr(x), qmm_type(x.scalar_type()), rows, cols, ld, trans, block, ptr(b), b.nbytes(), s);
-  });
+  const qmm_status st = unlocked(qmm_fp4_quantize, ptr(x), qmm_type(x.scalar_type()), rows, cols, ld, trans, block,
+                                 ptr(b), b.nbytes(), s);
   return st != QMM_OK ? PyLong_FromLong(st) : wrap(b);
 }
 
@@ -279,10 +282,8 @@ PyObject* fp4_quantize_both(PyObject* const* a) {
   const int64_t R = x.size(0), C = x.size(1);
   const Tensor b = packed(a[2], R, C, block, "out", x), bt = packed(a[3], C, R, block, "out_t", x);
   void* s = stream(a[4]);
-  const qmm_status st = unlocked([&] {
-    return qmm_fp4_quantize_both(ptr(x), qmm_type(x.scalar_type()), R, C, ld, block, ptr(b), b.nbytes(), ptr(bt),
-                                 bt.nbytes(), s);
-  });
+  const qmm_status st = unlocked(qmm_fp4_quantize_both, ptr(x), qmm_type(x.scalar_type()), R, C, ld, block, ptr(b),
+                                 b.nbytes(), ptr(bt), bt.nbytes(), s);
   return st != QMM_OK ? PyLong_FromLong(st) : pair(wrap(b), wrap(bt));
 }
 
@@ -293,8 +294,8 @@ PyObject* fp4_dequantize(PyObject* const* a) {
   const int block = (int)integer(a[3]);
   const Tensor y = output(a[4], {rows, cols}, float_type(a[5]), FLOATS, "out", b);
   void* s = stream(a[6]);
-  const qmm_status st = unlocked(
-      [&] { return qmm_fp4_dequantize(ptr(b), b.nbytes(), rows, cols, block, ptr(y), qmm_type(y.scalar_type()), s); });
+  const qmm_status st =
+      unlocked(qmm_fp4_dequantize, ptr(b), b.nbytes(), rows, cols, block, ptr(y), qmm_type(y.scalar_type()), s);
   return st != QMM_OK ? PyLong_FromLong(st) : wrap(y);
 }
 
@@ -305,10 +306,8 @@ PyObject* fp4_matmul(PyObject* const* a) {
   const int block = (int)integer(a[5]);
   const Tensor y = output(a[6], {M, N}, float_type(a[7]), FLOATS, "out", A);
   void* s = stream(a[8]);
-  const qmm_status st = unlocked([&] {
-    return qmm_fp4_matmul(ptr(A), A.nbytes(), M, ptr(B), B.nbytes(), N, K, block, ptr(y), qmm_type(y.scalar_type()),
-                          s);
-  });
+  const qmm_status st = unlocked(qmm_fp4_matmul, ptr(A), A.nbytes(), M, ptr(B), B.nbytes(), N, K, block, ptr(y),
+                                 qmm_type(y.scalar_type()), s);
   return st != QMM_OK ? PyLong_FromLong(st) : wrap(y);
 }
 

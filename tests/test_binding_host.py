@@ -1,0 +1,71 @@
+"""The native marshalling of the norm's and the 4-bit calls on a host without a GPU:
+what it raises for tensors that have no memory behind them. Fake CUDA tensors
+(extents, type and device, no storage) stand in for real ones. What could end the
+process runs in one of its own."""
+import os
+import subprocess
+import sys
+import textwrap
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+PRELUDE = """
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+import quantized_int8_matmul_gb300 as q
+
+class Stream:
+    cuda_stream = 0
+
+S, F32, U8, S8 = Stream(), torch.float32, torch.uint8, torch.int8
+
+def outcome(f, *a):
+    try:
+        f(*a)
+        return "returned"
+    except Exception as e:
+        return type(e).__name__ + ": " + str(e)
+
+def fake(*shape, dtype=F32, device="cuda:0"):
+    return torch.empty(*shape, dtype=dtype, device=device)
+"""
+
+
+def child(body):
+    """The lines that `body` prints, run under fake tensors in a process of its own."""
+    code = PRELUDE + "with FakeTensorMode(allow_non_fake_inputs=True):\n" + textwrap.indent(textwrap.dedent(body), "    ")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, f"exit code {r.returncode}\n{r.stdout}\n{r.stderr[-2000:]}"
+    return r.stdout.splitlines()
+
+
+def test_batched_tensors_raise():
+    """Inside torch.vmap a tensor has no pointer of its own: an error, as the ctypes calls give, not the
+    end of the process."""
+    lines = child("""
+    B, M, N, H = 3, 4, 5, 128
+    rows, scale = fake(B, M, H, dtype=S8), fake(B, M)
+    x, y, w, dw = fake(B, M, H), fake(B, M, H), fake(H), fake(B, H)
+    ws = fake(q.qmm_rms_norm_backward_workspace_bytes(M, H), dtype=U8)
+    p = fake(B, q.qmm_fp4_bytes(M, H, 16), dtype=U8)
+    pt, pn = fake(B, q.qmm_fp4_bytes(H, M, 16), dtype=U8), fake(q.qmm_fp4_bytes(N, H, 16), dtype=U8)
+    C = fake(B, M, N)
+    mat = lambda b, r=M, c=H: q.Fp4Matrix(b, r, c, 16)
+    calls = {
+        "s8": (lambda a, s, o: q.qmm_s8_dequantize_rows(a, s, out=o, out_dtype=F32, stream=S), rows, scale, y),
+        "grad": (lambda d, h, r, o, g: q.qmm_rms_norm_backward(d, h, w, r, out=o, dweight=g, stream=S, workspace=ws),
+                 x, x, scale, y, dw),
+        "quantise": (lambda t, o: q.qmm_fp4_quantize(t, out=mat(o), stream=S), x, p),
+        "both": (lambda t, o, r: q.qmm_fp4_quantize_both(t, out=mat(o), out_t=mat(r, H, M), stream=S), x, p, pt),
+        "read": (lambda b, o: q.qmm_fp4_dequantize(mat(b), out=o, out_dtype=F32, stream=S), p, y),
+        "matmul": (lambda b, o: q.qmm_fp4_matmul(mat(b), mat(pn, N), out=o, out_dtype=F32, stream=S), p, C),
+        "norm": (lambda t, o: q.qmm_rms_norm_s8(t, w, out=o, stream=S), x, rows),
+    }
+    for name, (f, *args) in calls.items():
+        print(name, outcome(torch.vmap(f), *args))
+    """)
+    assert len(lines) == 7
+    for line in lines:
+        assert line.split()[1] == "RuntimeError:", line
+    for line in lines[:6]:   # (the norm allocates its scales first, which fails without a GPU)
+        assert "data pointer" in line, line
