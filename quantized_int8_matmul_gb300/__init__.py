@@ -9,6 +9,10 @@ when the caller does not pass one (device memory is PyTorch's job here). The
 marshalling of the calls that are often shorter than their marshalling (the norm,
 4-bit floats) is native, in the ``_binding`` module; the others use ctypes.
 
+``stream``: the norm's and the 4-bit calls run on it and allocate from its memory, as
+under ``torch.cuda.stream(stream)``: what such a call returns is ready, and its
+memory free for others, in that stream's order.
+
 If the shared library is missing it is built from ``csrc/`` with nvcc on
 first import; if that fails the import fails loudly.
 """

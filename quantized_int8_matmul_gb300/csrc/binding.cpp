@@ -10,6 +10,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
@@ -114,15 +115,30 @@ ScalarType float_type(PyObject* o) {
   return t;
 }
 
-void* stream(PyObject* o) {
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream().stream();
-  PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
-  if (!h) throw Error();
-  void* s = PyLong_AsVoidPtr(h);
-  Py_DECREF(h);
-  if (PyErr_Occurred()) throw Error();
-  return s;
-}
+// The stream of a call: the current one, or one that the caller gives. That one is
+// current while this lives, so that outputs and workspaces come from its own memory:
+// a block goes to the stream that allocated it when it is dropped, and to its next
+// user on that stream only behind the kernels of this call.
+class OnStream {
+ public:
+  OnStream(PyObject* o, const Tensor& like) {
+    if (o == Py_None) {
+      raw_ = c10::cuda::getCurrentCUDAStream().stream();
+      return;
+    }
+    PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
+    if (!h) throw Error();
+    raw_ = PyLong_AsVoidPtr(h);
+    Py_DECREF(h);
+    if (PyErr_Occurred()) throw Error();
+    guard_.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(raw_), like.device().index()));
+  }
+  void* raw() const { return raw_; }
+
+ private:
+  c10::cuda::OptionalCUDAStreamGuard guard_;
+  void* raw_;
+};
 
 int64_t integer(PyObject* o) {
   const long long v = PyLong_AsLongLong(o);
@@ -173,11 +189,11 @@ PyObject* rms_norm_s8(PyObject* const* a) {
   const bool res = a[2] != Py_None;
   const double eps = PyFloat_AsDouble(a[3]);
   if (PyErr_Occurred()) throw Error();
+  const void *xp = ptr(x), *wp = ptr(w), *rp = res ? ptr(need_rows(a[2], {t}, "residual", ldr, shape)) : nullptr;
+  const OnStream on(a[7], x);
   const Tensor q = output(a[4], shape, S8, {S8}, "out", x);
   Tensor h = x;
-  const void* rp = nullptr;
   if (res) {
-    rp = ptr(need_rows(a[2], {t}, "residual", ldr, shape));
     h = output(a[5], shape, t, {t}, "h_out", x);
   } else if (a[5] != Py_None) {
     fail("h_out without a residual: h is x");
@@ -186,10 +202,9 @@ PyObject* rms_norm_s8(PyObject* const* a) {
   const Tensor scale = empty({M}, F32, x);
   Tensor rstd;
   if (save) rstd = empty({M}, F32, x);
-  void* s = stream(a[7]);
   const qmm_status st =
-      unlocked(qmm_rms_norm_s8, ptr(x), qmm_type(t), M, H, ldx, rp, ldr, ptr(w), qmm_type(w.scalar_type()), eps,
-               res ? ptr(h) : nullptr, ptr(q), ptr(scale), save ? ptr(rstd) : nullptr, s);
+      unlocked(qmm_rms_norm_s8, xp, qmm_type(t), M, H, ldx, rp, ldr, wp, qmm_type(w.scalar_type()), eps,
+               res ? ptr(h) : nullptr, ptr(q), ptr(scale), save ? ptr(rstd) : nullptr, on.raw());
   if (st != QMM_OK) return PyLong_FromLong(st);
   PyObject* r = PyTuple_New(4);
   PyTuple_SET_ITEM(r, 0, wrap(q));
@@ -215,10 +230,11 @@ PyObject* s8_dequantize_rows(PyObject* const* a) {
   if (q.dim() != 2) fail("q must be 2-D");
   const int64_t M = q.size(0), H = q.size(1);
   const Tensor& scale = need(a[1], {F32}, "scale", {M});
+  const void *qp = ptr(q), *sp = ptr(scale);
+  const OnStream on(a[4], q);
   const Tensor y = output(a[2], q.sizes(), float_type(a[3]), FLOATS, "out", q);
-  void* s = stream(a[4]);
   const qmm_status st =
-      unlocked(qmm_s8_dequantize_rows, ptr(q), ptr(scale), M, H, ptr(y), qmm_type(y.scalar_type()), s);
+      unlocked(qmm_s8_dequantize_rows, qp, sp, M, H, ptr(y), qmm_type(y.scalar_type()), on.raw());
   return st != QMM_OK ? PyLong_FromLong(st) : wrap(y);
 }
 
@@ -233,6 +249,8 @@ PyObject* rms_norm_backward(PyObject* const* a) {
   const Tensor& w = need(a[2], FLOATS, "weight", {H});
   const Tensor& rstd = need(a[3], {F32}, "rstd", {M});
   const void* dh = a[4] == Py_None ? nullptr : ptr(need_rows(a[4], {t}, "dh", lddh, shape));
+  const void *dyp = ptr(dy), *hp = ptr(h), *wp = ptr(w), *rp = ptr(rstd);
+  const OnStream on(a[7], h);
   const Tensor dx = output(a[5], shape, t, {t}, "out", h);
   const Tensor dw = output(a[6], {H}, F32, {F32}, "dweight", h);
   const size_t bytes = qmm_rms_norm_backward_workspace_bytes(M, H);
@@ -248,10 +266,9 @@ PyObject* rms_norm_backward(PyObject* const* a) {
     ws = empty({(int64_t)bytes}, U8, h);
     have = bytes;
   }
-  void* s = stream(a[7]);
-  const qmm_status st = unlocked(qmm_rms_norm_backward, ptr(dy), lddy, ptr(h), ldh, dh, lddh, qmm_type(t), M, H, ptr(w),
-                                 qmm_type(w.scalar_type()), ptr(rstd), ptr(dx), ptr(dw),
-                                 ws.defined() ? ptr(ws) : nullptr, have, s);
+  const qmm_status st =
+      unlocked(qmm_rms_norm_backward, dyp, lddy, hp, ldh, dh, lddh, qmm_type(t), M, H, wp, qmm_type(w.scalar_type()),
+               rp, ptr(dx), ptr(dw), ws.defined() ? ptr(ws) : nullptr, have, on.raw());
   return st != QMM_OK ? PyLong_FromLong(st) : pair(wrap(dx), wrap(dw));
 }
 
@@ -267,10 +284,11 @@ PyObject* fp4_quantize(PyObject* const* a) {
   const int block = (int)integer(a[1]);
   const int trans = PyObject_IsTrue(a[2]) == 1;
   const int64_t rows = x.size(trans ? 1 : 0), cols = x.size(trans ? 0 : 1);
+  const void* xp = ptr(x);
+  const OnStream on(a[4], x);
   const Tensor b = packed(a[3], rows, cols, block, "out", x);
-  void* s = stream(a[4]);
-  const qmm_status st = unlocked(qmm_fp4_quantize, ptr(x), qmm_type(x.scalar_type()), rows, cols, ld, trans, block,
-                                 ptr(b), b.nbytes(), s);
+  const qmm_status st = unlocked(qmm_fp4_quantize, xp, qmm_type(x.scalar_type()), rows, cols, ld, trans, block, ptr(b),
+                                 b.nbytes(), on.raw());
   return st != QMM_OK ? PyLong_FromLong(st) : wrap(b);
 }
 
@@ -280,10 +298,11 @@ PyObject* fp4_quantize_both(PyObject* const* a) {
   const Tensor& x = need_rows(a[0], FLOATS, "x", ld);
   const int block = (int)integer(a[1]);
   const int64_t R = x.size(0), C = x.size(1);
+  const void* xp = ptr(x);
+  const OnStream on(a[4], x);
   const Tensor b = packed(a[2], R, C, block, "out", x), bt = packed(a[3], C, R, block, "out_t", x);
-  void* s = stream(a[4]);
-  const qmm_status st = unlocked(qmm_fp4_quantize_both, ptr(x), qmm_type(x.scalar_type()), R, C, ld, block, ptr(b),
-                                 b.nbytes(), ptr(bt), bt.nbytes(), s);
+  const qmm_status st = unlocked(qmm_fp4_quantize_both, xp, qmm_type(x.scalar_type()), R, C, ld, block, ptr(b),
+                                 b.nbytes(), ptr(bt), bt.nbytes(), on.raw());
   return st != QMM_OK ? PyLong_FromLong(st) : pair(wrap(b), wrap(bt));
 }
 
@@ -292,10 +311,11 @@ PyObject* fp4_dequantize(PyObject* const* a) {
   const Tensor& b = need(a[0], {U8}, "m");
   const int64_t rows = integer(a[1]), cols = integer(a[2]);
   const int block = (int)integer(a[3]);
+  const void* bp = ptr(b);
+  const OnStream on(a[6], b);
   const Tensor y = output(a[4], {rows, cols}, float_type(a[5]), FLOATS, "out", b);
-  void* s = stream(a[6]);
   const qmm_status st =
-      unlocked(qmm_fp4_dequantize, ptr(b), b.nbytes(), rows, cols, block, ptr(y), qmm_type(y.scalar_type()), s);
+      unlocked(qmm_fp4_dequantize, bp, b.nbytes(), rows, cols, block, ptr(y), qmm_type(y.scalar_type()), on.raw());
   return st != QMM_OK ? PyLong_FromLong(st) : wrap(y);
 }
 
@@ -304,10 +324,11 @@ PyObject* fp4_matmul(PyObject* const* a) {
   const Tensor &A = need(a[0], {U8}, "a"), &B = need(a[2], {U8}, "b");
   const int64_t M = integer(a[1]), N = integer(a[3]), K = integer(a[4]);
   const int block = (int)integer(a[5]);
+  const void *ap = ptr(A), *bp = ptr(B);
+  const OnStream on(a[8], A);
   const Tensor y = output(a[6], {M, N}, float_type(a[7]), FLOATS, "out", A);
-  void* s = stream(a[8]);
-  const qmm_status st = unlocked(qmm_fp4_matmul, ptr(A), A.nbytes(), M, ptr(B), B.nbytes(), N, K, block, ptr(y),
-                                 qmm_type(y.scalar_type()), s);
+  const qmm_status st = unlocked(qmm_fp4_matmul, ap, A.nbytes(), M, bp, B.nbytes(), N, K, block, ptr(y),
+                                 qmm_type(y.scalar_type()), on.raw());
   return st != QMM_OK ? PyLong_FromLong(st) : wrap(y);
 }
 
