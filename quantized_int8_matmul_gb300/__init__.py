@@ -9,8 +9,8 @@ when the caller does not pass one (device memory is PyTorch's job here). The
 marshalling of the calls that are often shorter than their marshalling (the norm,
 4-bit floats) is native, in the ``_binding`` module; the others use ctypes.
 
-``stream``: the norm's and the 4-bit calls run on it and allocate from its memory, as
-under ``torch.cuda.stream(stream)``: what such a call returns is ready, and its
+``stream``: a call that is given one runs on it and allocates device memory from its
+memory, as under ``torch.cuda.stream(stream)``: what it returns is ready, and its
 memory free for others, in that stream's order.
 
 If the shared library is missing it is built from ``csrc/`` with nvcc on
@@ -143,6 +143,18 @@ def _stream(stream=None):
     return stream.cuda_stream
 
 
+def _empty(size, dtype, device, stream):
+    """torch.empty from the memory of the call's stream (None: the current one). A block
+    goes back to the stream that allocated it, so one of another stream's would be
+    handed out again while this call's kernels still use it."""
+    if stream is None:
+        return torch.empty(size, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
+    with torch.cuda.stream(stream):
+        return torch.empty(size, dtype=dtype, device=device)
+
+
 def _check(fn: str, status: int):
     if status != QMM_OK:
         raise QmmError(fn, status)
@@ -165,7 +177,7 @@ def qmm_w8_pack_decode_weight(W, packed=None, stream=None):
     if nbytes == 0:
         raise QmmError("qmm_w8_pack_decode_weight", QMM_ERR_UNSUPPORTED)
     if packed is None:
-        packed = torch.empty(nbytes, dtype=torch.uint8, device=W.device)
+        packed = _empty(nbytes, torch.uint8, W.device, stream)
     _check("qmm_w8_pack_decode_weight",
            _lib.qmm_w8_pack_decode_weight(_ptr(W), K, N, _ptr(packed), packed.numel(), _stream(stream)))
     return packed
@@ -183,11 +195,11 @@ def qmm_w8_dequant_packed(A, packed, N, scale, zero_point=None, out=None, out_dt
         _need(zero_point, (torch.int32,), "zero_point")
         zc = zero_point.numel()
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=A.device)
+        out = _empty((M, N), out_dtype, A.device, stream)
     _need(out, (torch.float32, torch.bfloat16), "out")
     nbytes = int(_lib.qmm_w8_dequant_packed_workspace_bytes(M, K))
     if workspace is None:
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=A.device)
+        workspace = _empty(max(nbytes, 1), torch.uint8, A.device, stream)
     st = _lib.qmm_w8_dequant_packed(_ptr(A), M, K, N, _ptr(packed), packed.numel(), _ptr(scale), scale.numel(),
                                     _ptr(zero_point), zc, _ptr(out), _TORCH_TO_QMM[out.dtype], _ptr(workspace),
                                     workspace.numel(), _stream(stream))
@@ -240,9 +252,9 @@ def qmm_w8_dequant(A, B, scale, zero_point=None, out=None, out_dtype=torch.float
         _need(zero_point, (torch.int32,), "zero_point")
         zp_count = zero_point.numel()
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=A.device)
+        out = _empty((M, N), out_dtype, A.device, stream)
     _need(out, (torch.float32, torch.bfloat16), "out")
-    ws, wsb = _workspace(workspace, qmm_w8_dequant_workspace_bytes(A.dtype, M, K, N), A.device)
+    ws, wsb = _workspace(workspace, qmm_w8_dequant_workspace_bytes(A.dtype, M, K, N), A.device, stream)
     if ws is None:
         st = _lib.qmm_w8_dequant(_ptr(A), _TORCH_TO_QMM[A.dtype], _ptr(B), M, K, N, _ptr(scale), scale.numel(),
                                  _ptr(zero_point), zp_count, _ptr(out), _TORCH_TO_QMM[out.dtype], _stream(stream))
@@ -255,15 +267,15 @@ def qmm_w8_dequant(A, B, scale, zero_point=None, out=None, out_dtype=torch.float
     return out
 
 
-def _workspace(ws, nbytes, device):
-    """None -> no workspace; "auto" -> a fresh uint8 buffer of nbytes (torch's
-    caching allocator); a tensor -> used as is. Returns (tensor or None, bytes)."""
+def _workspace(ws, nbytes, device, stream):
+    """None -> no workspace; "auto" -> a fresh uint8 buffer of nbytes from the memory of
+    the call's stream; a tensor -> used as is. Returns (tensor or None, bytes)."""
     if ws is None or nbytes == 0:
         return None, 0
     if isinstance(ws, str):
         if ws != "auto":
             raise ValueError("workspace must be None, 'auto' or a device tensor")
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        ws = _empty(nbytes, torch.uint8, device, stream)
     return ws, ws.numel() * ws.element_size()
 
 
@@ -291,9 +303,9 @@ def qmm_a8w8(A, B, act_scale, weight_scale, out=None, out_dtype=torch.bfloat16, 
     if K2 != K:
         raise ValueError("inner dimensions differ")
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=A.device)
+        out = _empty((M, N), out_dtype, A.device, stream)
     _need(out, (torch.float32, torch.bfloat16), "out")
-    ws, wsb = _workspace(workspace, qmm_a8w8_workspace_bytes(M, K, N), A.device)
+    ws, wsb = _workspace(workspace, qmm_a8w8_workspace_bytes(M, K, N), A.device, stream)
     if ws is None:
         st = _lib.qmm_a8w8(_ptr(A), _ptr(B), M, K, N, _ptr(act_scale), act_scale.numel(), _ptr(weight_scale),
                            weight_scale.numel(), _ptr(out), _TORCH_TO_QMM[out.dtype], _stream(stream))
@@ -349,7 +361,7 @@ def qmm_a8w8_host(A, B, act_scale, weight_scale, out=None, out_dtype=torch.bfloa
         out = torch.empty((M, N), dtype=out_dtype, pin_memory=True)
     _need_host(out, (torch.float32, torch.bfloat16), "out")
     nbytes = qmm_a8w8_host_workspace_bytes(M, K, N, act_scale.numel(), weight_scale.numel(), out.dtype)
-    ws, wsb = _workspace(workspace, nbytes, torch.device("cuda", torch.cuda.current_device()))
+    ws, wsb = _workspace(workspace, nbytes, torch.device("cuda", torch.cuda.current_device()), stream)
     st = _lib.qmm_a8w8_host(_ptr(A), _ptr(B), M, K, N, _ptr(act_scale), act_scale.numel(), _ptr(weight_scale),
                             weight_scale.numel(), _ptr(out), _TORCH_TO_QMM[out.dtype], _ptr(ws), wsb,
                             _stream(stream))
@@ -362,7 +374,7 @@ def qmm_a8w8_packed(M, K, N, act_scale, weight_scale, workspace, out=None, out_d
     _need(act_scale, (torch.float32,), "act_scale")
     _need(weight_scale, (torch.float32,), "weight_scale")
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=workspace.device)
+        out = _empty((M, N), out_dtype, workspace.device, stream)
     _need(out, (torch.float32, torch.bfloat16), "out")
     st = _lib.qmm_a8w8_packed(M, K, N, _ptr(act_scale), act_scale.numel(), _ptr(weight_scale), weight_scale.numel(),
                               _ptr(out), _TORCH_TO_QMM[out.dtype], _ptr(workspace),
@@ -397,14 +409,14 @@ def qmm_a8w8_acc(A, B, act_scale=None, weight_scale=None, acc_in=None, acc_out=N
             if tuple(t.shape) != (M, N):
                 raise ValueError(f"{name} must be [{M}, {N}]")
     if out is None and out_dtype is not None:
-        out = torch.empty((M, N), dtype=out_dtype, device=A.device)
+        out = _empty((M, N), out_dtype, A.device, stream)
     if out is not None:
         _need(out, (torch.float32, torch.bfloat16), "out")
         _need(act_scale, (torch.float32,), "act_scale")
         _need(weight_scale, (torch.float32,), "weight_scale")
     elif acc_out is None:
         raise ValueError("nothing to write: give out_dtype/out or acc_out")
-    ws, wsb = _workspace(workspace, qmm_a8w8_acc_workspace_bytes(M, K, N), A.device)
+    ws, wsb = _workspace(workspace, qmm_a8w8_acc_workspace_bytes(M, K, N), A.device, stream)
     st = _lib.qmm_a8w8_acc(_ptr(A), int(bool(a_trans)), _ptr(B), int(bool(b_trans)), M, K, N, _ptr(acc_in),
                            _ptr(acc_out), _ptr(act_scale) if out is not None else None,
                            act_scale.numel() if out is not None else 0,
@@ -481,12 +493,12 @@ def conv_integer(x, w, x_zero_point=None, w_zero_point=None, pads=None, strides=
         oH = oW = 0   # the library rejects the geometry
     shape = (N, M, oW) if x.dim() == 3 else (N, M, oH, oW)
     if out is None:
-        out = torch.empty(shape, dtype=torch.int32, device=x.device)
+        out = _empty(shape, torch.int32, x.device, stream)
     _need(out, (torch.int32,), "out")
     if tuple(out.shape) != shape:
         raise ValueError(f"out must be {shape}")
     ws, wsb = _workspace(workspace, conv_integer_workspace_bytes(tuple(x.shape), tuple(w.shape), pads, strides,
-                                                                 dilations, group), x.device)
+                                                                 dilations, group), x.device, stream)
     st_ = _lib.conv_integer(_ptr(x), _TORCH_TO_QMM[x.dtype], _ptr(w), _TORCH_TO_QMM[w.dtype], N, C, H, Wd, M, kH, kW,
                             p, st, dl, group, _ptr(xzp), _ptr(wzp), 0 if wzp is None else wzp.numel(), _ptr(out),
                             _ptr(ws), wsb, _stream(stream))
@@ -520,11 +532,11 @@ def dynamic_quantize_matmul(x, W, w_scale, w_zero_point=None, bias=None, out=Non
         if bias.numel() != N:
             raise ValueError("bias must have N values")
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float32, device=x.device)
+        out = _empty((M, N), torch.float32, x.device, stream)
     _need(out, (torch.float32,), "out")
-    ys = torch.empty(1, dtype=torch.float32, device=x.device)
-    yz = torch.empty(1, dtype=torch.uint8, device=x.device)
-    ws, wsb = _workspace(workspace, dynamic_quantize_matmul_workspace_bytes(M, K, N), x.device)
+    ys = _empty(1, torch.float32, x.device, stream)
+    yz = _empty(1, torch.uint8, x.device, stream)
+    ws, wsb = _workspace(workspace, dynamic_quantize_matmul_workspace_bytes(M, K, N), x.device, stream)
     st = _lib.dynamic_quantize_matmul(_ptr(x), M, K, _ptr(W), _TORCH_TO_QMM[W.dtype], N, _ptr(w_scale),
                                       w_scale.numel(), _ptr(w_zero_point),
                                       0 if w_zero_point is None else w_zero_point.numel(), _ptr(bias), _ptr(out),
@@ -561,7 +573,7 @@ def dynamic_quantize_matmul_pack_weight(W, packed=None, stream=None) -> DqmPacke
     if nbytes == 0:
         raise QmmError("dynamic_quantize_matmul_pack_weight", QMM_ERR_INVALID_ARG)
     if packed is None:
-        packed = torch.empty(nbytes, dtype=torch.uint8, device=W.device)
+        packed = _empty(nbytes, torch.uint8, W.device, stream)
     _check("dynamic_quantize_matmul_pack_weight",
            _lib.dynamic_quantize_matmul_pack_weight(_ptr(W), _TORCH_TO_QMM[W.dtype], K, N, _ptr(packed),
                                                     packed.numel() * packed.element_size(), _stream(stream)))
@@ -589,13 +601,13 @@ def dynamic_quantize_matmul_packed(x, weight: DqmPackedWeight, w_scale, w_zero_p
         if bias.numel() != N:
             raise ValueError("bias must have N values")
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float32, device=x.device)
+        out = _empty((M, N), torch.float32, x.device, stream)
     _need(out, (torch.float32,), "out")
-    ys = torch.empty(1, dtype=torch.float32, device=x.device)
-    yz = torch.empty(1, dtype=torch.uint8, device=x.device)
+    ys = _empty(1, torch.float32, x.device, stream)
+    yz = _empty(1, torch.uint8, x.device, stream)
     nbytes = dynamic_quantize_matmul_packed_workspace_bytes(M, K)
     if isinstance(workspace, str) and workspace == "auto":
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=x.device)
+        workspace = _empty(max(nbytes, 1), torch.uint8, x.device, stream)
     if workspace is None:
         raise ValueError("the packed chain needs a workspace")
     buf = weight.buf
@@ -651,9 +663,10 @@ def matmul_integer(A, B, a_zero_point=None, b_zero_point=None, out=None, stream=
         _need(b_zero_point, (B.dtype,), "b_zero_point")
         bz = b_zero_point.numel()
     if out is None:
-        out = torch.empty((*batch_shape, M, N), dtype=torch.int32, device=A.device)
+        out = _empty((*batch_shape, M, N), torch.int32, A.device, stream)
     _need(out, (torch.int32,), "out")
-    ws, wsb = _workspace(workspace, matmul_integer_workspace_bytes(batch, M, K, N, a_stride, b_stride), A.device)
+    ws, wsb = _workspace(workspace, matmul_integer_workspace_bytes(batch, M, K, N, a_stride, b_stride), A.device,
+                         stream)
     if ws is None:
         st = _lib.matmul_integer(_ptr(A), _TORCH_TO_QMM[A.dtype], _ptr(B), _TORCH_TO_QMM[B.dtype], batch, M, K, N,
                                  a_stride, b_stride, _ptr(a_zero_point), az, _ptr(b_zero_point), bz, _ptr(out),
@@ -679,17 +692,17 @@ def dynamic_quantize_linear(x, row_len=None, workspace=None, y=None, stream=None
     n = x.numel()
     dev = x.device
     if y is None:
-        y = torch.empty(x.shape, dtype=torch.uint8, device=dev)
-    y_scale = torch.empty(1, dtype=torch.float32, device=dev)
-    y_zp = torch.empty(1, dtype=torch.uint8, device=dev)
+        y = _empty(x.shape, torch.uint8, dev, stream)
+    y_scale = _empty(1, torch.float32, dev, stream)
+    y_zp = _empty(1, torch.uint8, dev, stream)
     ws_bytes = dynamic_quantize_linear_workspace_bytes(n)
     if workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        workspace = _empty(ws_bytes, torch.uint8, dev, stream)
     row_sums = None
     rl = 0
     if row_len is not None:
         rl = int(row_len)
-        row_sums = torch.empty(n // rl if rl > 0 else 0, dtype=torch.int32, device=dev)
+        row_sums = _empty(n // rl if rl > 0 else 0, torch.int32, dev, stream)
     st = _lib.dynamic_quantize_linear(_ptr(x), n, _ptr(y), _ptr(y_scale), _ptr(y_zp), _ptr(row_sums), rl,
                                       _ptr(workspace), workspace.numel() * workspace.element_size(),
                                       _stream(stream))
