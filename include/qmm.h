@@ -530,9 +530,11 @@ qmm_status qmm_w8_dequant_packed(const void* A, int64_t M, int64_t K, int64_t N,
  *   rstd  = 1 / sqrt(mean(h^2) + eps)
  *   q     = rne(v * (127 / a));       scale = a * rstd / 127
  * each step fp32, so q * scale stands for the normalised row h * rstd * w
- * within half a step; rstd cancels out of q. A row with a below 2^-100 is a row
- * of zeros: q = 0 and scale 1; a row whose v holds a NaN or an infinity gets
- * q = 0 and scale NaN.
+ * within half a step; rstd cancels out of q. Squares that leave float32's range
+ * are taken of scaled elements, so rstd and scale hold for every finite h (rstd
+ * is infinite where its value is beyond float32's largest). A row with a below
+ * 2^-100 is a row of zeros: q = 0 and scale 1; a row whose v holds a NaN or an
+ * infinity gets q = 0 and scale NaN.
  *
  *  x             [M] rows of H, x_dtype QMM_F32 or QMM_BF16, ldx >= H elements
  *                between rows

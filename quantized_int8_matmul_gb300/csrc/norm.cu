@@ -259,9 +259,9 @@ __device__ __forceinline__ float row_sum(float a, int G, float* sa) {
   return a;
 }
 
-// The row's scale and the multiplier of v. A row that holds a NaN or an
-// infinity gets a NaN scale (and zeros); a row with a below 2^-100 (whose
-// 127 / a could overflow, and whose squares underflow) is stored as zeros, scale 1.
+// The row's scale and the multiplier of v. A row whose v holds a NaN or an
+// infinity gets a NaN scale (and zeros); a row with a below 2^-100 (whose 127 / a
+// could overflow) is stored as zeros, scale 1.
 struct RowScale {
   float inv, scale, rstd;
 };
@@ -278,6 +278,18 @@ __device__ __forceinline__ RowScale row_scale(float ss, unsigned amax_bits, int 
     r.scale = __fmul_rn(__fmul_rn(a, r.rstd), 1.f / 127.f);
   }
   return r;
+}
+// The power of two that brings a row's h into range where the sum of its squares has
+// left float32's (1: it has not), the same for all threads of the row.
+//   ss infinite: |h| up to 2^128; times 2^-80 the sum of 2^31 squares is below 2^127,
+//     and the largest |h|, above 2^48, keeps a square above 2^-64.
+//   ss below 2^-90: squares may have lost bits below 2^-126 (a mean wrong by up to
+//     2^-149), which shows unless eps covers it: 2^-120 does. Times 2^100 the sum is
+//     below 2^110, the smallest |h|, 2^-149, has a square of 2^-98, and eps * 2^200 is
+//     below 2^80.
+__device__ __forceinline__ float rescale(float ss, float eps) {
+  if (__float_as_uint(ss) == kInfBits) return 0x1p-80f;
+  return ss < 0x1p-90f && eps < 0x1p-120f ? 0x1p100f : 1.f;
 }
 // Two float32 operations in one instruction, each rounded once.
 __device__ __forceinline__ void mul_pair(float& a, float& b, float x, float y) {
@@ -335,12 +347,46 @@ __device__ __forceinline__ float max_abs(float a, float b) {
   return r;
 }
 
+// rstd and the scale, once more, of a row whose squares have left float32's range: the
+// sum of (f * h)^2, the row of h (a stored one, which may lie over x or the residual,
+// else T(x + residual)) read again element by element, and f undone in both. Its int8
+// values are right as they are (no sum is in them), so this comes last, when the row's
+// registers are free, as a call of its own with the kernel's arguments one by one: ahead
+// of the int8 values it held 12 registers more of every row's threads, inlined it cost
+// rows that never come here up to 5 % (so 1 %). What the row's threads stored of h is
+// visible to all of them: a barrier lies between.
+template <typename T>
+__device__ __noinline__ void rescaled_row(const void* x, long long ldx, const void* residual, long long ldr,
+                                          const void* stored, int n, float eps, float* scale, float* rstd, float* sa,
+                                          unsigned amax_bits, float f) {
+  const int G = blockDim.x, t = threadIdx.x;
+  const long long m = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+  const T* h = stored ? static_cast<const T*>(stored) + m * n : static_cast<const T*>(x) + m * ldx;
+  const T* r = residual && !stored ? static_cast<const T*>(residual) + m * ldr : nullptr;
+  if (G == 32) __syncwarp();
+  float ss = 0.f;
+#pragma unroll 1
+  for (int i = t; i < n; i += G) {
+    float a = (float)h[i];
+    if (r) a = (float)from_f<T>(__fadd_rn(a, (float)r[i]));
+    a = __fmul_rn(a, f);
+    ss = __fmaf_rn(a, a, ss);
+  }
+  if (G > 32) __syncthreads();   // sa has been read
+  ss = row_sum(ss, G, sa);
+  if (t != 0) return;
+  const float root = rsqrtf(__fadd_rn(__fdiv_rn(ss, (float)n), __fmul_rn(__fmul_rn(eps, f), f)));
+  if (rstd) rstd[m] = __fmul_rn(f, root);
+  const float a = __uint_as_float(amax_bits);
+  if (amax_bits < kInfBits && a >= 0x1p-100f) scale[m] = __fmul_rn(__fmul_rn(__fmul_rn(a, f), root), 1.f / 127.f);
+}
+
 // One row per G = blockDim.x threads (blockDim.y rows a CTA where G is a warp),
 // NV vectors a thread. NV = 0: rows of any length, read twice.
-// 8192 x 4096 bf16: 36.2 us with a residual (6.5 TB/s, 97 % of a copy's rate), 18.9
+// 8192 x 4096 bf16: 36.1 us with a residual (6.5 TB/s, 97 % of a copy's rate), 19.0
 // without (5.3 TB/s: then a CTA's two barriers a row show); 4096 x 11008 float32
 // with one 103 us (85 %). Rows that start off 16 bytes: 8192 x 4095 bf16 57 us,
-// 1009 x 5003 float32 8.9 us (2.8 TB/s; the weight comes by two vectors and a shift,
+// 1009 x 5003 float32 9.1 us (2.8 TB/s; the weight comes by two vectors and a shift,
 // 9.6 us element by element; a row's first and last vectors go element by element).
 template <typename T, int W, int NV>
 __global__ void __launch_bounds__(1024) rms_norm_s8_kernel(const NormArgs p) {
@@ -366,6 +412,11 @@ __global__ void __launch_bounds__(1024) rms_norm_s8_kernel(const NormArgs p) {
       mul_pair(v[e], v[e + 1], w[e], w[e + 1]);
       amax = max_abs(max_abs(amax, v[e]), v[e + 1]);
     }
+  };
+  auto rescaled = [&](unsigned am) {
+    const float f = rescale(ss, p.eps);
+    if (__builtin_expect(f != 1.f, 0))
+      rescaled_row<T>(p.x, p.ldx, p.residual, p.ldr, p.h, n, p.eps, p.scale, p.rstd, sa, am, f);
   };
   auto put = [&](int j, const float* v, float inv, bool zero) {
     uint32_t o[E / 4];
@@ -414,6 +465,7 @@ __global__ void __launch_bounds__(1024) rms_norm_s8_kernel(const NormArgs p) {
     }
 #pragma unroll
     for (int j = 0; j < K; ++j) put(j, v[j], rs.inv, am >= kInfBits);
+    rescaled(am);
   } else {
     const int steps = (n + s + G * E - 1) / (G * E);
     for (int j = 0; j < steps; ++j) {
@@ -444,6 +496,7 @@ __global__ void __launch_bounds__(1024) rms_norm_s8_kernel(const NormArgs p) {
       for (int e = 0; e < E; ++e) v[e] = __fmul_rn(v[e], w[e]);
       put(j, v, rs.inv, am >= kInfBits);
     }
+    rescaled(am);
   }
 }
 
