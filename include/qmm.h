@@ -557,6 +557,7 @@ qmm_status qmm_w8_dequant_packed(const void* A, int64_t M, int64_t K, int64_t N,
  *  dweight       float[H]; the sum over rows runs in a fixed order
  *  workspace     qmm_rms_norm_backward_workspace_bytes(M, H) bytes, 16-byte aligned
  * M = 0 launches nothing but a zero fill of dweight; H = 0 launches nothing.
+ * QMM_ERR_UNSUPPORTED for the norm and its gradient where H is above 2^31 - 1 - 2^14.
  */
 qmm_status qmm_rms_norm_s8(const void* x, int x_dtype, int64_t M, int64_t H, int64_t ldx, const void* residual,
                            int64_t ldr, const void* w, int w_dtype, float eps, void* h, int8_t* q, float* scale,

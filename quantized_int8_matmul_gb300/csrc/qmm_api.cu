@@ -1619,11 +1619,16 @@ qmm_status dynamic_quantize_linear(const float* x, int64_t n, uint8_t* y, float*
 
 static bool float_type(int t) { return t == QMM_F32 || t == QMM_BF16; }
 
+// The norm's kernels index a row in 32 bits, and the last vectors of a CTA's threads
+// (1024 of 8 elements) and a row's shift reach past its end.
+constexpr int64_t kNormMaxWidth = (int64_t)INT_MAX - (1 << 14);
+
 qmm_status qmm_rms_norm_s8(const void* x, int x_dtype, int64_t M, int64_t H, int64_t ldx, const void* residual,
                            int64_t ldr, const void* w, int w_dtype, float eps, void* h, int8_t* q, float* scale,
                            float* rstd, void* stream) {
   if (!float_type(x_dtype) || !float_type(w_dtype)) return QMM_ERR_INVALID_ARG;
   if (!dim_ok(M) || !dim_ok(H) || ldx < H || (residual && ldr < H) || !(eps >= 0.f)) return QMM_ERR_INVALID_ARG;
+  if (H > kNormMaxWidth) return QMM_ERR_UNSUPPORTED;
   if (M == 0 || H == 0) {
     t_last_kernel = "none";
     return QMM_OK;
@@ -1665,7 +1670,7 @@ qmm_status qmm_s8_dequantize_rows(const int8_t* q, const float* scale, int64_t M
 }
 
 size_t qmm_rms_norm_backward_workspace_bytes(int64_t M, int64_t H) {
-  if (!dim_ok(M) || !dim_ok(H) || M == 0) return 0;
+  if (!dim_ok(M) || !dim_ok(H) || M == 0 || H > kNormMaxWidth) return 0;
   return sizeof(float) * (size_t)rms_norm_backward_partials(M, (int)H) * (size_t)H;
 }
 
@@ -1675,6 +1680,7 @@ qmm_status qmm_rms_norm_backward(const void* dy, int64_t lddy, const void* h, in
                                  size_t workspace_bytes, void* stream) {
   if (!float_type(dtype) || !float_type(w_dtype)) return QMM_ERR_INVALID_ARG;
   if (!dim_ok(M) || !dim_ok(H) || lddy < H || ldh < H || (dh && lddh < H)) return QMM_ERR_INVALID_ARG;
+  if (H > kNormMaxWidth) return QMM_ERR_UNSUPPORTED;
   if (H == 0) {
     t_last_kernel = "none";
     return QMM_OK;
