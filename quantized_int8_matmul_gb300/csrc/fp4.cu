@@ -240,7 +240,7 @@ struct ScaleWord<1> { using type = uint32_t; };
 // ---------------------------------------------------------------------------
 template <typename T, int BLOCK, int J, int ITER, bool VEC>
 __global__ void __launch_bounds__(VEC ? 1024 : 896) quantize_rows_kernel(const Fp4QuantArgs p, const int staged,
-                                                                                const int whole) {
+                                                                                const int whole, const int turns) {
   constexpr int WROWS = 2 * J, WCOLS = 512 / WROWS;   // a warp step
   constexpr int ATOMS = BLOCK == 16 ? 2 : 1;
   constexpr int SPC = 32 / BLOCK;          // scales per 32-column chunk
@@ -269,9 +269,9 @@ __global__ void __launch_bounds__(VEC ? 1024 : 896) quantize_rows_kernel(const F
   const int n = rv ? (int)p.cols : 0;
   const bool wide = ((reinterpret_cast<uintptr_t>(p.x) | (size_t)p.ld * sizeof(T)) & 31) == 0;
   const int chunks = (int)L.kt * 4, units_all = (chunks + UC - 1) / UC;
-  // this CTA's steps: all, or (block 32) as many as its warps take in one batch
-  const int u0 = BLOCK == 32 && gridDim.y > 1 ? blockIdx.y * nw * ITER : 0;
-  const int units = BLOCK == 32 && gridDim.y > 1 ? min(units_all, u0 + nw * ITER) : units_all;
+  // this CTA's steps: all, or (block 32) as many as its warps take in `turns` batches
+  const int u0 = BLOCK == 32 && gridDim.y > 1 ? blockIdx.y * (nw * ITER * turns) : 0;
+  const int units = BLOCK == 32 && gridDim.y > 1 ? min(units_all, u0 + nw * ITER * turns) : units_all;
   const int batches = (units - u0 + nw * ITER - 1) / (nw * ITER);
   if (!VEC && whole) {
     T* all = reinterpret_cast<T*>(smem);
@@ -937,25 +937,32 @@ cudaError_t launch_rows_j(const Fp4QuantArgs& a, cudaStream_t s) {
     const long long whole = units * WCOLS + 16 / (long long)sizeof(T);
     if (whole * WROWS * (long long)sizeof(T) + (long long)smem <= 200 * 1024) {
       const int nw = (int)std::min<long long>(16, std::max<long long>(8, (units + 1) / 2));
-      return launch_chained(kern, grid, nw * 32, smem + (size_t)whole * WROWS * sizeof(T), 1, s, a, staged, (int)whole);
+      return launch_chained(kern, grid, nw * 32, smem + (size_t)whole * WROWS * sizeof(T), 1, s, a, staged, (int)whole,
+                            1);
     }
     const int nw = 28;
-    return launch_chained(kern, grid, nw * 32, smem + (size_t)nw * RowStage<T, WROWS, WCOLS>::BYTES, 1, s, a, staged, 0);
+    return launch_chained(kern, grid, nw * 32, smem + (size_t)nw * RowStage<T, WROWS, WCOLS>::BYTES, 1, s, a, staged, 0,
+                          1);
   }
   int iter = 1;   // (a CTA alone on its SM takes more warps)
   while (iter < MOST && units > (BLOCK == 32 ? 4 : (int)grid < num_sms() ? 16 : 8) * iter) iter *= 2;
   int nw = (int)std::min<long long>(32, std::max<long long>(4, (units + iter - 1) / iter));
+  // a segment is one batch, or as many as keep the segments on their grid axis (65,535:
+  // above 33 million columns of float32 in more than 32 rows, 67 of bf16)
+  constexpr long long AXIS = 65535;
   unsigned segments = 1;
+  int turns = 1;
   if (BLOCK == 32 && units > 4 * iter) {
     nw = 4;
-    segments = (unsigned)((units + 4 * iter - 1) / (4 * iter));
-    smem = (size_t)(4 * iter * WCOLS / 128) * 8 * J;
+    turns = (int)((units + 4 * iter * AXIS - 1) / (4 * iter * AXIS));
+    segments = (unsigned)((units + 4 * iter * turns - 1) / (4 * iter * turns));
+    smem = (size_t)(4 * iter * turns * WCOLS / 128) * 8 * J;
     staged = 1;
   }
   auto kern = iter == 1   ? quantize_rows_kernel<T, BLOCK, J, 1, true>
               : iter == 2 ? quantize_rows_kernel<T, BLOCK, J, 2, true>
                           : quantize_rows_kernel<T, BLOCK, J, MOST, true>;
-  return launch_chained(kern, dim3(grid, segments), nw * 32, smem, 1, s, a, staged, 0);
+  return launch_chained(kern, dim3(grid, segments), nw * 32, smem, 1, s, a, staged, 0, turns);
 }
 
 // Long bf16 rows by the ring, where two groups of two rows leave room for a second
