@@ -515,9 +515,9 @@ __global__ void __launch_bounds__(RING_THREADS, 2) quantize_rows_ring_kernel(con
 
 // a[0 .. na) and b[0 .. n - na) to zero, before the maxima: two fills of the
 // library's took 2 us longer, as they do not start on the heels of what precedes them.
-__global__ void __launch_bounds__(256) zero_kernel(unsigned* a, int na, unsigned* b, int n) {
+__global__ void __launch_bounds__(256) zero_kernel(unsigned* a, long long na, unsigned* b, long long n) {
   chain_wait();
-  const int i = blockIdx.x * 256 + threadIdx.x;
+  const long long i = blockIdx.x * 256ll + threadIdx.x;
   if (i < na) a[i] = 0u;
   else if (i < n) b[i - na] = 0u;
   chain_release();
@@ -1049,9 +1049,8 @@ cudaError_t launch_tiles(const Fp4QuantArgs& a, cudaStream_t s) {
   if (BLOCK == 16) {
     unsigned* cm = reinterpret_cast<unsigned*>(a.out + Lc.max_off());
     unsigned* rm = a.out_rows ? reinterpret_cast<unsigned*>(a.out_rows + Lr.max_off()) : nullptr;
-    const int words = (int)(Lc.rt * 128 + (rm ? Lr.rt * 128 : 0));
-    cudaError_t e = launch_chained(zero_kernel, (unsigned)((words + 255) / 256), 256, 0, 1, s, cm, (int)(Lc.rt * 128),
-                                   rm, words);
+    const long long cols = Lc.rt * 128, words = cols + (rm ? Lr.rt * 128 : 0);   // (together past 2^31)
+    cudaError_t e = launch_chained(zero_kernel, (unsigned)((words + 255) / 256), 256, 0, 1, s, cm, cols, rm, words);
     if (e != cudaSuccess) return e;
     const long long ctas = ((a.cols + 255) / 256) * ((a.rows + 63) / 64);
     e = launch_chained(a.vec ? absmax_kernel<T, true> : absmax_kernel<T, false>, (unsigned)ctas, 256, 0, 1, s, a, cm,
