@@ -16,6 +16,7 @@
 #include "chain.cuh"
 #include "common.cuh"
 #include "kernels.h"
+#include "row_copy.h"
 
 #include <algorithm>
 #include <mutex>
@@ -689,7 +690,8 @@ __global__ void __launch_bounds__(1024)
 // The same for rows that come by bulk copies: a ring of `slots` rows (h, dy and dh
 // each in 16-byte lines; of rows too long for two slots of all three, h and dy) in
 // shared memory, refilled once a row's reduction has passed, so that the next rows
-// are on their way through the whole of this one's work. Rows of one vector a
+// are on their way through the whole of this one's work. No copy reaches past the last
+// row of a tensor (4096 x 4095 bf16 with dh 49.1 us; 47.2 if the last one might). Rows of one vector a
 // thread go in pairs (RB = 2): one barrier and one reduction for both (8192 x 1024
 // bf16 21.1 -> 19.8 us). With sum_partials: 4096 x 4096 bf16 with dh 30.7 us (4.4
 // TB/s, 65 %), 4096 x 8192 49.6 (81 %), 1531 x 11008 float32 44.0 (69 %; 1531 rows
@@ -734,21 +736,46 @@ __global__ void __launch_bounds__(1024) rms_norm_backward_ring_kernel(const Norm
   const long long m0 = blockIdx.x, step = gridDim.x;
   const int rows = (int)((p.M - m0 + step - 1) / step);
   const int s = row_shift<T, W>(m0, n);   // the same for all of the CTA's rows
-  const uint32_t line = ((uint32_t)(n + s) * (uint32_t)sizeof(T) + 15u) & ~15u;   // a row's bytes
   const uint32_t pitch = (uint32_t)(n + E) * (uint32_t)sizeof(T) / 16u * 16u + 16u;
+  // The end of the tensors' last row is not copied (row_copy.h). The CTA that has the row
+  // reads it element by element: into the row's slot where that is filled at the start,
+  // else into its own row of partials, which it needs at its end only, from where a copy
+  // takes it to the slot behind the row before it.
+  auto tails = [&] {   // 16 bytes a tensor
+    return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p.partials + m0 * n) + 15) & ~(uintptr_t)15);
+  };
   auto fill = [&](int r) {   // one thread
     const long long m = m0 + r * step;
     uint64_t* bar = &full[r % slots];
     const uint32_t dst = smem_u32(ring) + (uint32_t)(r % slots) * (uint32_t)tensors * pitch;
-    mbar_arrive_expect_tx(bar, (uint32_t)tensors * line);
-    bulk_load(dst, static_cast<const T*>(p.h) + m * p.ldh - s, line, bar);
-    bulk_load(dst + pitch, static_cast<const T*>(p.dy) + m * p.lddy - s, line, bar);
-    if (DH && tensors == 3) bulk_load(dst + 2 * pitch, static_cast<const T*>(p.dh) + m * p.lddh - s, line, bar);
+    const bool last = W == kShifted && m == p.M - 1;
+    const uint32_t bytes = row_copy_bytes(n, s, (int)sizeof(T), last);
+    const uint32_t end = last && r >= slots ? row_copy_bytes(n, s, (int)sizeof(T), false) - bytes : 0u;   // 0 or 16
+    mbar_arrive_expect_tx(bar, (uint32_t)tensors * (bytes + end));
+    if (end)
+#pragma unroll 1
+      for (int i = 0; i < tensors; ++i) bulk_load(dst + i * pitch + bytes, tails() + 16 * i, end, bar);
+    bulk_load(dst, static_cast<const T*>(p.h) + m * p.ldh - s, bytes, bar);
+    bulk_load(dst + pitch, static_cast<const T*>(p.dy) + m * p.lddy - s, bytes, bar);
+    if (DH && tensors == 3) bulk_load(dst + 2 * pitch, static_cast<const T*>(p.dh) + m * p.lddh - s, bytes, bar);
   };
   if (t == 0) {
     for (int i = 0; i < slots; ++i) mbar_init(&full[i], 1);
     fence_mbarrier_init();
     for (int r = 0; r < slots && r < rows; ++r) fill(r);
+  }
+  if (W == kShifted && m0 + (rows - 1) * step == p.M - 1) {
+    const int last = rows - 1;
+    const uint32_t last_line = row_copy_bytes(n, s, (int)sizeof(T), true);
+    const int left = (n + s) & (E - 1), which = t / E, k = t & (E - 1);
+    if (which < tensors && k < left) {
+      const T* end = static_cast<const T*>(which == 0 ? p.h : which == 1 ? p.dy : p.dh) +
+                     (p.M - 1) * (which == 0 ? p.ldh : which == 1 ? p.lddy : p.lddh) + n - left;
+      uint8_t* to = last < slots ? ring + ((size_t)last * (uint32_t)tensors + which) * pitch + last_line
+                                 : tails() + 16 * which;
+      reinterpret_cast<T*>(to)[k] = end[k];
+    }
+    asm volatile("fence.proxy.async.global;" ::: "memory");   // for the copy engine (then the barrier)
   }
   float dw[NV][E], w[E];
 #pragma unroll
