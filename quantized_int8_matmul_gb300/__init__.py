@@ -14,7 +14,9 @@ memory, as under ``torch.cuda.stream(stream)``: what it returns is ready, and it
 memory free for others, in that stream's order.
 
 If the shared library is missing it is built from ``csrc/`` with nvcc on
-first import; if that fails the import fails loudly.
+first import; if that fails the import fails loudly. ``_binding`` belongs to one
+Python and one torch and is built again for others; where it cannot be (a torch
+without CUDA, no compiler) the calls that need it raise, and the others work.
 """
 from __future__ import annotations
 
@@ -50,7 +52,7 @@ class QmmError(RuntimeError):
 
 
 def _load() -> ctypes.CDLL:
-    path = _build.build()
+    path = _build.build_library()
     lib = ctypes.CDLL(path)
     i64, vp, ci = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int
     lib.qmm_w8_dequant.argtypes = [vp, ci, vp, i64, i64, i64, vp, i64, vp, i64, vp, ci, vp]
@@ -123,7 +125,28 @@ def _load() -> ctypes.CDLL:
 _lib = _load()
 LIB_PATH = _build.LIB_PATH
 
-from . import _binding  # noqa: E402  (built beside libqmm.so, which it links)
+
+class _NoBinding:
+    """Stands in for the native module where it cannot be built or loaded."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise RuntimeError(f"{name} needs the native module _binding, which could not be loaded: "
+                           f"{self._why}") from self._why
+
+
+def _load_binding():
+    try:
+        _build.build_binding()
+        from . import _binding   # (built beside libqmm.so, which it links)
+        return _binding
+    except (ImportError, OSError, RuntimeError) as e:
+        return _NoBinding(e)
+
+
+_binding = _load_binding()
 
 
 def lib() -> ctypes.CDLL:

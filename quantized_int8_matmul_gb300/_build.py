@@ -6,7 +6,8 @@ with the CUDA runtime linked statically so the library loads on a host that
 has the toolkit but no driver (the exported-symbol checks run there). The
 host-only ``csrc/binding.cpp`` becomes the Python module ``_binding`` (argument
 marshalling against torch's headers), linked to ``libqmm.so``.
-A rebuild happens only when a source or header is newer than the libraries.
+A rebuild happens only when a source or header is newer than the library made of it,
+or, of ``_binding``, when Python or torch is another one than it was built for.
 """
 from __future__ import annotations
 
@@ -24,6 +25,7 @@ BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libqmm.so")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 BINDING_PATH = os.path.join(PKG_DIR, "_binding.so")
+BINDING_TAG = os.path.join(BUILD_DIR, "binding.tag")   # what BINDING_PATH was built for
 HEADERS = [os.path.join(REPO_DIR, "include", "qmm.h")]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -42,16 +44,35 @@ def sources() -> list[str]:
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
-def _inputs() -> list[str]:
+def _newer(inputs: list[str], path: str) -> bool:
+    """path is missing or older than one of the inputs."""
+    if not os.path.exists(path):
+        return True
+    t = os.path.getmtime(path)
+    return any(os.path.getmtime(p) > t for p in inputs)
+
+
+def library_stale() -> bool:
     hdrs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    return sources() + hdrs + HEADERS + [BINDING_SRC, __file__]
+    return _newer(sources() + hdrs + HEADERS + [__file__], LIB_PATH)
+
+
+def binding_stale() -> bool:
+    if _newer(HEADERS + [BINDING_SRC, __file__], BINDING_PATH) or not os.path.exists(BINDING_TAG):
+        return True
+    with open(BINDING_TAG) as f:
+        return f.read() != binding_tag()
 
 
 def needs_build() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
-        return True
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
-    return any(os.path.getmtime(p) > t for p in _inputs())
+    return library_stale() or binding_stale()
+
+
+def binding_tag() -> str:
+    """The Python and the torch that a _binding built now is for: their binary interfaces
+    differ from version to version."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return f"{sysconfig.get_config_var('SOABI')}\n{_torch_dir()}\n{f.read()}"
 
 
 def _torch_dir() -> str:
@@ -84,18 +105,42 @@ def _link(cmd: list[str], path: str) -> None:
     os.replace(tmp, path)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libqmm.so if needed; return its path."""
-    if not force and not needs_build():
-        return LIB_PATH
-    os.makedirs(BUILD_DIR, exist_ok=True)
-    srcs = [BINDING_SRC, *sources()]
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
-        binding, *objs = ex.map(_compile, srcs)
-    _link([nvcc_path(), *ARCH_FLAGS, "-shared", "-cudart", "static", *objs], LIB_PATH)
+def _make(library: bool, binding: bool) -> None:
+    """Compile and link the two, each if asked for."""
+    if not library and not binding:
+        return
     tlib = os.path.join(_torch_dir(), "lib")
-    _link([_cxx(), "-shared", binding, "-L" + PKG_DIR, "-l:libqmm.so", "-Wl,-rpath,$ORIGIN", "-L" + tlib,
-           "-Wl,-rpath," + tlib, "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"], BINDING_PATH)
+    if binding and not os.path.exists(os.path.join(tlib, "libtorch_cuda.so")):
+        raise RuntimeError("this torch has no CUDA libraries to link _binding to")
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    srcs = ([BINDING_SRC] if binding else []) + (sources() if library else [])
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+        objs = list(ex.map(_compile, srcs))
+    bobj = objs.pop(0) if binding else None
+    if library:
+        _link([nvcc_path(), *ARCH_FLAGS, "-shared", "-cudart", "static", *objs], LIB_PATH)
+    if binding:
+        _link([_cxx(), "-shared", bobj, "-L" + PKG_DIR, "-l:libqmm.so", "-Wl,-rpath,$ORIGIN", "-L" + tlib,
+               "-Wl,-rpath," + tlib, "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"],
+              BINDING_PATH)
+        with open(BINDING_TAG, "w") as f:
+            f.write(binding_tag())
+
+
+def build_library() -> str:
+    """Compile and link libqmm.so if needed; return its path."""
+    _make(library_stale(), False)
+    return LIB_PATH
+
+
+def build_binding() -> None:
+    """Compile and link _binding.so if needed (libqmm.so is there)."""
+    _make(False, binding_stale())
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Compile and link both if needed; return libqmm.so's path."""
+    _make(force or library_stale(), force or binding_stale())
     if verbose:
         print(f"built {LIB_PATH}")
     return LIB_PATH
