@@ -146,6 +146,18 @@ int64_t integer(PyObject* o) {
   return v;
 }
 
+int block_size(PyObject* o) {
+  const int64_t v = integer(o);
+  if (v != 16 && v != 32) fail("block must be 16 or 32");
+  return (int)v;
+}
+
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Error();
+  return v != 0;
+}
+
 void* ptr(const Tensor& t) { return t.data_ptr(); }
 
 PyObject* wrap(const Tensor& t) { return THPVariable_Wrap(t); }
@@ -189,6 +201,7 @@ PyObject* rms_norm_s8(PyObject* const* a) {
   const bool res = a[2] != Py_None;
   const double eps = PyFloat_AsDouble(a[3]);
   if (PyErr_Occurred()) throw Error();
+  const bool save = truth(a[6]);
   const void *xp = ptr(x), *wp = ptr(w), *rp = res ? ptr(need_rows(a[2], {t}, "residual", ldr, shape)) : nullptr;
   const OnStream on(a[7], x);
   const Tensor q = output(a[4], shape, S8, {S8}, "out", x);
@@ -198,7 +211,6 @@ PyObject* rms_norm_s8(PyObject* const* a) {
   } else if (a[5] != Py_None) {
     fail("h_out without a residual: h is x");
   }
-  const bool save = PyObject_IsTrue(a[6]) == 1;
   const Tensor scale = empty({M}, F32, x);
   Tensor rstd;
   if (save) rstd = empty({M}, F32, x);
@@ -281,8 +293,8 @@ Tensor packed(PyObject* out, int64_t rows, int64_t cols, int block, const char* 
 PyObject* fp4_quantize(PyObject* const* a) {
   int64_t ld;
   const Tensor& x = need_rows(a[0], FLOATS, "x", ld);
-  const int block = (int)integer(a[1]);
-  const int trans = PyObject_IsTrue(a[2]) == 1;
+  const int block = block_size(a[1]);
+  const int trans = truth(a[2]);
   const int64_t rows = x.size(trans ? 1 : 0), cols = x.size(trans ? 0 : 1);
   const void* xp = ptr(x);
   const OnStream on(a[4], x);
@@ -296,7 +308,7 @@ PyObject* fp4_quantize(PyObject* const* a) {
 PyObject* fp4_quantize_both(PyObject* const* a) {
   int64_t ld;
   const Tensor& x = need_rows(a[0], FLOATS, "x", ld);
-  const int block = (int)integer(a[1]);
+  const int block = block_size(a[1]);
   const int64_t R = x.size(0), C = x.size(1);
   const void* xp = ptr(x);
   const OnStream on(a[4], x);
@@ -310,7 +322,7 @@ PyObject* fp4_quantize_both(PyObject* const* a) {
 PyObject* fp4_dequantize(PyObject* const* a) {
   const Tensor& b = need(a[0], {U8}, "m");
   const int64_t rows = integer(a[1]), cols = integer(a[2]);
-  const int block = (int)integer(a[3]);
+  const int block = block_size(a[3]);
   const void* bp = ptr(b);
   const OnStream on(a[6], b);
   const Tensor y = output(a[4], {rows, cols}, float_type(a[5]), FLOATS, "out", b);
@@ -323,7 +335,7 @@ PyObject* fp4_dequantize(PyObject* const* a) {
 PyObject* fp4_matmul(PyObject* const* a) {
   const Tensor &A = need(a[0], {U8}, "a"), &B = need(a[2], {U8}, "b");
   const int64_t M = integer(a[1]), N = integer(a[3]), K = integer(a[4]);
-  const int block = (int)integer(a[5]);
+  const int block = block_size(a[5]);
   const void *ap = ptr(A), *bp = ptr(B);
   const OnStream on(a[8], A);
   const Tensor y = output(a[6], {M, N}, float_type(a[7]), FLOATS, "out", A);

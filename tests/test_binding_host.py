@@ -69,3 +69,22 @@ def test_batched_tensors_raise():
         assert line.split()[1] == "RuntimeError:", line
     for line in lines[:6]:   # (the norm allocates its scales first, which fails without a GPU)
         assert "data pointer" in line, line
+
+
+def test_errors_inside_arguments_are_raised():
+    """A truth value that raises is that error, not a result with an error pending; a block that is no
+    int is refused, not cut to its low bits."""
+    lines = child("""
+    class Bad:
+        def __bool__(self):
+            raise ZeroDivisionError("no truth value")
+
+    x, w = fake(4, 64), fake(64)
+    print(outcome(lambda: q.qmm_rms_norm_s8(x, w, save_rstd=Bad(), stream=S)))
+    m = q.Fp4Matrix(fake(q.qmm_fp4_bytes(4, 64, 16), dtype=U8), 4, 64, 2 ** 32 + 16)
+    print(outcome(lambda: q.qmm_fp4_dequantize(m, out=x, out_dtype=F32, stream=S)))
+    print(outcome(lambda: q.qmm_fp4_matmul(m, m, out=fake(4, 4), out_dtype=F32, stream=S)))
+    print(outcome(lambda: q.qmm_fp4_quantize(x, block=2 ** 32 + 16, stream=S)))
+    """)
+    assert lines[0] == "ZeroDivisionError: no truth value"
+    assert len(lines) == 4 and all(line == "ValueError: block must be 16 or 32" for line in lines[1:]), lines
