@@ -70,9 +70,15 @@ const Tensor& need(PyObject* o, Types types, const char* name) {
   if (!t.is_contiguous()) fail(std::string(name) + " must be contiguous");
   return t;
 }
-const Tensor& need(PyObject* o, Types types, const char* name, at::IntArrayRef shape) {
+// Operands lie on one device.
+void check_device(const Tensor& t, const char* name, const Tensor& first) {
+  if (t.device() != first.device())
+    fail(std::string(name) + " is on " + t.device().str() + ", the first operand on " + first.device().str());
+}
+const Tensor& need(PyObject* o, Types types, const char* name, at::IntArrayRef shape, const Tensor& first) {
   const Tensor& t = need(o, types, name);
   if (t.sizes() != shape) fail(std::string(name) + " must be " + shape_text(shape));
+  check_device(t, name, first);
   return t;
 }
 
@@ -89,24 +95,16 @@ const Tensor& need_rows(PyObject* o, Types types, const char* name, int64_t& ld)
     fail(std::string(name) + ": rows must be contiguous and not overlap");
   return t;
 }
-const Tensor& need_rows(PyObject* o, Types types, const char* name, int64_t& ld, at::IntArrayRef shape) {
+const Tensor& need_rows(PyObject* o, Types types, const char* name, int64_t& ld, at::IntArrayRef shape,
+                        const Tensor& first) {
   const Tensor& t = need_rows(o, types, name, ld);
   if (t.sizes() != shape) fail(std::string(name) + " must be " + shape_text(shape));
+  check_device(t, name, first);
   return t;
 }
 
 constexpr ScalarType F32 = ScalarType::Float, BF16 = ScalarType::BFloat16, S8 = ScalarType::Char, U8 = ScalarType::Byte;
 #define FLOATS {F32, BF16}
-
-Tensor empty(at::IntArrayRef shape, ScalarType type, const Tensor& like) {
-  return Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
-}
-
-// `out` checked, or a new tensor where it is None.
-Tensor output(PyObject* out, at::IntArrayRef shape, ScalarType type, Types types, const char* name,
-              const Tensor& like) {
-  return out == Py_None ? empty(shape, type, like) : need(out, types, name, shape);
-}
 
 ScalarType float_type(PyObject* o) {
   if (!THPDtype_Check(o)) fail("out_dtype must be a torch dtype");
@@ -115,29 +113,44 @@ ScalarType float_type(PyObject* o) {
   return t;
 }
 
-// The stream of a call: the current one, or one that the caller gives. That one is
-// current while this lives, so that outputs and workspaces come from its own memory:
-// a block goes to the stream that allocated it when it is dropped, and to its next
-// user on that stream only behind the kernels of this call.
-class OnStream {
+// The stream of a call and what it allocates: the current stream, or one that the
+// caller gives. That one is made current for the allocations, so that outputs and
+// workspaces come from its own memory: a block goes to the stream that allocated it
+// when it is dropped, and to its next user on that stream only behind the kernels of
+// this call.
+class Call {
  public:
-  OnStream(PyObject* o, const Tensor& like) {
-    if (o == Py_None) {
-      raw_ = c10::cuda::getCurrentCUDAStream().stream();
-      return;
-    }
-    PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
+  Call(PyObject* stream, const Tensor& first) : device_(first.device()) {
+    if (stream == Py_None) return;
+    PyObject* h = PyObject_GetAttrString(stream, "cuda_stream");
     if (!h) throw Error();
-    raw_ = PyLong_AsVoidPtr(h);
+    given_ = static_cast<cudaStream_t>(PyLong_AsVoidPtr(h));
     Py_DECREF(h);
     if (PyErr_Occurred()) throw Error();
-    guard_.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(raw_), like.device().index()));
+    has_stream_ = true;
   }
-  void* raw() const { return raw_; }
+  Tensor empty(at::IntArrayRef shape, ScalarType type) const {
+    c10::cuda::OptionalCUDAStreamGuard guard;
+    if (has_stream_) guard.reset_stream(c10::cuda::getStreamFromExternal(given_, device_.index()));
+    return Tensor(at::detail::empty_cuda(shape, type, device_, std::nullopt));
+  }
+  // `out` checked, or a new tensor where it is None.
+  Tensor output(PyObject* out, at::IntArrayRef shape, ScalarType type, Types types, const char* name,
+                const Tensor& first) const {
+    return out == Py_None ? empty(shape, type) : need(out, types, name, shape, first);
+  }
+  // The stream, for a launch; launches go to the current device.
+  void* stream() const {
+    const int current = c10::cuda::current_device();
+    if (current != device_.index())
+      fail("the operands are on " + device_.str() + ", the current device is cuda:" + std::to_string(current));
+    return has_stream_ ? given_ : c10::cuda::getCurrentCUDAStream(device_.index()).stream();
+  }
 
  private:
-  c10::cuda::OptionalCUDAStreamGuard guard_;
-  void* raw_;
+  at::Device device_;
+  cudaStream_t given_ = nullptr;
+  bool has_stream_ = false;
 };
 
 int64_t integer(PyObject* o) {
@@ -197,26 +210,26 @@ PyObject* rms_norm_s8(PyObject* const* a) {
   const auto shape = x.sizes();
   const int64_t M = shape[0], H = shape[1];
   const ScalarType t = x.scalar_type();
-  const Tensor& w = need(a[1], FLOATS, "weight", {H});
+  const Tensor& w = need(a[1], FLOATS, "weight", {H}, x);
   const bool res = a[2] != Py_None;
   const double eps = PyFloat_AsDouble(a[3]);
   if (PyErr_Occurred()) throw Error();
   const bool save = truth(a[6]);
-  const void *xp = ptr(x), *wp = ptr(w), *rp = res ? ptr(need_rows(a[2], {t}, "residual", ldr, shape)) : nullptr;
-  const OnStream on(a[7], x);
-  const Tensor q = output(a[4], shape, S8, {S8}, "out", x);
+  const void *xp = ptr(x), *wp = ptr(w), *rp = res ? ptr(need_rows(a[2], {t}, "residual", ldr, shape, x)) : nullptr;
+  const Call call(a[7], x);
+  const Tensor q = call.output(a[4], shape, S8, {S8}, "out", x);
   Tensor h = x;
   if (res) {
-    h = output(a[5], shape, t, {t}, "h_out", x);
+    h = call.output(a[5], shape, t, {t}, "h_out", x);
   } else if (a[5] != Py_None) {
     fail("h_out without a residual: h is x");
   }
-  const Tensor scale = empty({M}, F32, x);
+  const Tensor scale = call.empty({M}, F32);
   Tensor rstd;
-  if (save) rstd = empty({M}, F32, x);
+  if (save) rstd = call.empty({M}, F32);
   const qmm_status st =
       unlocked(qmm_rms_norm_s8, xp, qmm_type(t), M, H, ldx, rp, ldr, wp, qmm_type(w.scalar_type()), eps,
-               res ? ptr(h) : nullptr, ptr(q), ptr(scale), save ? ptr(rstd) : nullptr, on.raw());
+               res ? ptr(h) : nullptr, ptr(q), ptr(scale), save ? ptr(rstd) : nullptr, call.stream());
   if (st != QMM_OK) return PyLong_FromLong(st);
   PyObject* r = PyTuple_New(4);
   PyTuple_SET_ITEM(r, 0, wrap(q));
@@ -241,12 +254,12 @@ PyObject* s8_dequantize_rows(PyObject* const* a) {
   const Tensor& q = need(a[0], {S8}, "q");
   if (q.dim() != 2) fail("q must be 2-D");
   const int64_t M = q.size(0), H = q.size(1);
-  const Tensor& scale = need(a[1], {F32}, "scale", {M});
+  const Tensor& scale = need(a[1], {F32}, "scale", {M}, q);
   const void *qp = ptr(q), *sp = ptr(scale);
-  const OnStream on(a[4], q);
-  const Tensor y = output(a[2], q.sizes(), float_type(a[3]), FLOATS, "out", q);
+  const Call call(a[4], q);
+  const Tensor y = call.output(a[2], q.sizes(), float_type(a[3]), FLOATS, "out", q);
   const qmm_status st =
-      unlocked(qmm_s8_dequantize_rows, qp, sp, M, H, ptr(y), qmm_type(y.scalar_type()), on.raw());
+      unlocked(qmm_s8_dequantize_rows, qp, sp, M, H, ptr(y), qmm_type(y.scalar_type()), call.stream());
   return st != QMM_OK ? PyLong_FromLong(st) : wrap(y);
 }
 
@@ -257,36 +270,40 @@ PyObject* rms_norm_backward(PyObject* const* a) {
   const auto shape = h.sizes();
   const int64_t M = shape[0], H = shape[1];
   const ScalarType t = h.scalar_type();
-  const Tensor& dy = need_rows(a[0], {t}, "dy", lddy, shape);
-  const Tensor& w = need(a[2], FLOATS, "weight", {H});
-  const Tensor& rstd = need(a[3], {F32}, "rstd", {M});
-  const void* dh = a[4] == Py_None ? nullptr : ptr(need_rows(a[4], {t}, "dh", lddh, shape));
+  const Tensor& dy = need_rows(a[0], {t}, "dy", lddy, shape, h);
+  const Tensor& w = need(a[2], FLOATS, "weight", {H}, h);
+  const Tensor& rstd = need(a[3], {F32}, "rstd", {M}, h);
+  const void* dh = a[4] == Py_None ? nullptr : ptr(need_rows(a[4], {t}, "dh", lddh, shape, h));
   const void *dyp = ptr(dy), *hp = ptr(h), *wp = ptr(w), *rp = ptr(rstd);
-  const OnStream on(a[7], h);
-  const Tensor dx = output(a[5], shape, t, {t}, "out", h);
-  const Tensor dw = output(a[6], {H}, F32, {F32}, "dweight", h);
+  const Call call(a[7], h);
+  const Tensor dx = call.output(a[5], shape, t, {t}, "out", h);
+  const Tensor dw = call.output(a[6], {H}, F32, {F32}, "dweight", h);
   const size_t bytes = qmm_rms_norm_backward_workspace_bytes(M, H);
   Tensor ws;
   size_t have = 0;
   if (THPVariable_Check(a[8])) {
     ws = tensor(a[8], "workspace");
     if (!ws.is_cuda()) fail("workspace must be a CUDA tensor");
+    check_device(ws, "workspace", h);
     have = ws.nbytes();
   } else if (bytes) {
     if (!PyUnicode_Check(a[8]) || PyUnicode_CompareWithASCIIString(a[8], "auto") != 0)
       fail("workspace must be 'auto' or a device tensor");
-    ws = empty({(int64_t)bytes}, U8, h);
+    ws = call.empty({(int64_t)bytes}, U8);
     have = bytes;
   }
   const qmm_status st =
       unlocked(qmm_rms_norm_backward, dyp, lddy, hp, ldh, dh, lddh, qmm_type(t), M, H, wp, qmm_type(w.scalar_type()),
-               rp, ptr(dx), ptr(dw), ws.defined() ? ptr(ws) : nullptr, have, on.raw());
+               rp, ptr(dx), ptr(dw), ws.defined() ? ptr(ws) : nullptr, have, call.stream());
   return st != QMM_OK ? PyLong_FromLong(st) : pair(wrap(dx), wrap(dw));
 }
 
-Tensor packed(PyObject* out, int64_t rows, int64_t cols, int block, const char* name, const Tensor& like) {
-  if (out != Py_None) return need(out, {U8}, name);
-  return empty({(int64_t)qmm_fp4_bytes(rows, cols, block)}, U8, like);
+Tensor packed(const Call& call, PyObject* out, int64_t rows, int64_t cols, int block, const char* name,
+              const Tensor& first) {
+  if (out == Py_None) return call.empty({(int64_t)qmm_fp4_bytes(rows, cols, block)}, U8);
+  const Tensor& t = need(out, {U8}, name);
+  check_device(t, name, first);
+  return t;
 }
 
 // x, block, transpose, out, stream -> buffer
@@ -297,10 +314,10 @@ PyObject* fp4_quantize(PyObject* const* a) {
   const int trans = truth(a[2]);
   const int64_t rows = x.size(trans ? 1 : 0), cols = x.size(trans ? 0 : 1);
   const void* xp = ptr(x);
-  const OnStream on(a[4], x);
-  const Tensor b = packed(a[3], rows, cols, block, "out", x);
+  const Call call(a[4], x);
+  const Tensor b = packed(call, a[3], rows, cols, block, "out", x);
   const qmm_status st = unlocked(qmm_fp4_quantize, xp, qmm_type(x.scalar_type()), rows, cols, ld, trans, block, ptr(b),
-                                 b.nbytes(), on.raw());
+                                 b.nbytes(), call.stream());
   return st != QMM_OK ? PyLong_FromLong(st) : wrap(b);
 }
 
@@ -311,10 +328,10 @@ PyObject* fp4_quantize_both(PyObject* const* a) {
   const int block = block_size(a[1]);
   const int64_t R = x.size(0), C = x.size(1);
   const void* xp = ptr(x);
-  const OnStream on(a[4], x);
-  const Tensor b = packed(a[2], R, C, block, "out", x), bt = packed(a[3], C, R, block, "out_t", x);
+  const Call call(a[4], x);
+  const Tensor b = packed(call, a[2], R, C, block, "out", x), bt = packed(call, a[3], C, R, block, "out_t", x);
   const qmm_status st = unlocked(qmm_fp4_quantize_both, xp, qmm_type(x.scalar_type()), R, C, ld, block, ptr(b),
-                                 b.nbytes(), ptr(bt), bt.nbytes(), on.raw());
+                                 b.nbytes(), ptr(bt), bt.nbytes(), call.stream());
   return st != QMM_OK ? PyLong_FromLong(st) : pair(wrap(b), wrap(bt));
 }
 
@@ -324,23 +341,24 @@ PyObject* fp4_dequantize(PyObject* const* a) {
   const int64_t rows = integer(a[1]), cols = integer(a[2]);
   const int block = block_size(a[3]);
   const void* bp = ptr(b);
-  const OnStream on(a[6], b);
-  const Tensor y = output(a[4], {rows, cols}, float_type(a[5]), FLOATS, "out", b);
+  const Call call(a[6], b);
+  const Tensor y = call.output(a[4], {rows, cols}, float_type(a[5]), FLOATS, "out", b);
   const qmm_status st =
-      unlocked(qmm_fp4_dequantize, bp, b.nbytes(), rows, cols, block, ptr(y), qmm_type(y.scalar_type()), on.raw());
+      unlocked(qmm_fp4_dequantize, bp, b.nbytes(), rows, cols, block, ptr(y), qmm_type(y.scalar_type()), call.stream());
   return st != QMM_OK ? PyLong_FromLong(st) : wrap(y);
 }
 
 // a, M, b, N, K, block, out, out_dtype, stream -> out
 PyObject* fp4_matmul(PyObject* const* a) {
   const Tensor &A = need(a[0], {U8}, "a"), &B = need(a[2], {U8}, "b");
+  check_device(B, "b", A);
   const int64_t M = integer(a[1]), N = integer(a[3]), K = integer(a[4]);
   const int block = block_size(a[5]);
   const void *ap = ptr(A), *bp = ptr(B);
-  const OnStream on(a[8], A);
-  const Tensor y = output(a[6], {M, N}, float_type(a[7]), FLOATS, "out", A);
+  const Call call(a[8], A);
+  const Tensor y = call.output(a[6], {M, N}, float_type(a[7]), FLOATS, "out", A);
   const qmm_status st = unlocked(qmm_fp4_matmul, ap, A.nbytes(), M, bp, B.nbytes(), N, K, block, ptr(y),
-                                 qmm_type(y.scalar_type()), on.raw());
+                                 qmm_type(y.scalar_type()), call.stream());
   return st != QMM_OK ? PyLong_FromLong(st) : wrap(y);
 }
 

@@ -88,3 +88,38 @@ def test_errors_inside_arguments_are_raised():
     """)
     assert lines[0] == "ZeroDivisionError: no truth value"
     assert len(lines) == 4 and all(line == "ValueError: block must be 16 or 32" for line in lines[1:]), lines
+
+
+def test_operands_on_two_devices_are_refused():
+    lines = child("""
+    M, N, H = 4, 5, 64
+    a, b = (lambda *s, **k: fake(*s, device="cuda:0", **k)), (lambda *s, **k: fake(*s, device="cuda:1", **k))
+    x, w, rows, scale = a(M, H), a(H), a(M, H, dtype=S8), a(M)
+    p = q.Fp4Matrix(a(q.qmm_fp4_bytes(M, H, 16), dtype=U8), M, H, 16)
+    far = q.Fp4Matrix(b(q.qmm_fp4_bytes(N, H, 16), dtype=U8), N, H, 16)
+    ws = a(q.qmm_rms_norm_backward_workspace_bytes(M, H), dtype=U8)
+    calls = [
+        lambda: q.qmm_rms_norm_s8(x, b(H), stream=S),
+        lambda: q.qmm_rms_norm_s8(x, w, residual=b(M, H), stream=S),
+        lambda: q.qmm_rms_norm_s8(x, w, out=b(M, H, dtype=S8), stream=S),
+        lambda: q.qmm_s8_dequantize_rows(rows, b(M), stream=S),
+        lambda: q.qmm_s8_dequantize_rows(rows, scale, out=b(M, H), stream=S),
+        lambda: q.qmm_rms_norm_backward(b(M, H), x, w, scale, stream=S),
+        lambda: q.qmm_rms_norm_backward(x, x, b(H), scale, stream=S),
+        lambda: q.qmm_rms_norm_backward(x, x, w, b(M), stream=S),
+        lambda: q.qmm_rms_norm_backward(x, x, w, scale, dh=b(M, H), stream=S),
+        lambda: q.qmm_rms_norm_backward(x, x, w, scale, out=b(M, H), dweight=a(H), workspace=ws, stream=S),
+        lambda: q.qmm_rms_norm_backward(x, x, w, scale, out=a(M, H), dweight=b(H), workspace=ws, stream=S),
+        lambda: q.qmm_rms_norm_backward(x, x, w, scale, out=a(M, H), dweight=a(H), stream=S,
+                                        workspace=b(ws.numel(), dtype=U8)),
+        lambda: q.qmm_fp4_quantize(x, out=q.Fp4Matrix(b(p.buf.numel(), dtype=U8), M, H, 16), stream=S),
+        lambda: q.qmm_fp4_dequantize(p, out=b(M, H), stream=S),
+        lambda: q.qmm_fp4_matmul(p, far, stream=S),
+        lambda: q.qmm_fp4_matmul(p, p, out=b(M, M), stream=S),
+    ]
+    for f in calls:
+        print(outcome(f))
+    """)
+    assert len(lines) == 16
+    for i, line in enumerate(lines):
+        assert line.startswith("ValueError: ") and "cuda:1" in line and "cuda:0" in line, (i, line)
