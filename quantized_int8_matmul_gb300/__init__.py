@@ -186,6 +186,8 @@ def _check(fn: str, status: int):
 def _need(t, dtypes, name):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != torch._C._cuda_getDevice():   # where the call's kernels run
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch._C._cuda_getDevice()}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {t.dtype} not in {dtypes}")
     if not t.is_contiguous():

@@ -123,3 +123,27 @@ def test_operands_on_two_devices_are_refused():
     assert len(lines) == 16
     for i, line in enumerate(lines):
         assert line.startswith("ValueError: ") and "cuda:1" in line and "cuda:0" in line, (i, line)
+
+
+def test_int8_operands_off_the_current_device_are_refused():
+    lines = child("""
+    torch._C._cuda_getDevice = lambda: 0        # (there is no driver to ask)
+    far = lambda *s, **k: fake(*s, device="cuda:1", **k)
+    A, B, near = fake(4, 64, dtype=S8), fake(64, 32, dtype=S8), fake(1)
+    x = fake(4, 64)
+    calls = [
+        lambda: q.qmm_a8w8(far(4, 64, dtype=S8), B, near, near, stream=S),
+        lambda: q.qmm_a8w8(A, B, near, far(1), stream=S),
+        lambda: q.qmm_a8w8(A, B, near, near, out=far(4, 32), stream=S),
+        lambda: q.qmm_a8w8_acc(A, far(64, 32, dtype=S8), near, near, stream=S),
+        lambda: q.qmm_w8_dequant(x, B, far(1), stream=S),
+        lambda: q.matmul_integer(A, far(64, 32, dtype=S8), stream=S),
+        lambda: q.dynamic_quantize_linear(far(4, 64), stream=S),
+        lambda: q.dynamic_quantize_matmul(x, far(64, 32, dtype=S8), near, stream=S),
+    ]
+    for f in calls:
+        print(outcome(f))
+    """)
+    assert len(lines) == 8
+    for i, line in enumerate(lines):
+        assert line.startswith("ValueError: ") and "cuda:1" in line and "cuda:0" in line, (i, line)
