@@ -755,7 +755,8 @@ def qmm_rms_norm_s8(x, weight, residual=None, eps=1e-6, out=None, h_out=None, sa
     x (and residual) float32 or bfloat16 [M, H], rows contiguous at any stride;
     weight float32 or bfloat16 [H]. out: int8 [M, H]; h_out: [M, H] of x's type,
     may be x or residual itself. save_rstd: return rstd [M] for the gradient. A row
-    that holds a NaN or an infinity gets a NaN scale."""
+    whose v holds a NaN or an infinity gets a NaN scale; a row of zeros, or of no
+    elements, gets scale 1."""
     r = _binding.rms_norm_s8(x, weight, residual, eps, out, h_out, save_rstd, stream)
     if type(r) is int:
         raise QmmError("qmm_rms_norm_s8", r)

@@ -18,6 +18,7 @@
 
 #include <exception>
 #include <initializer_list>
+#include <limits>
 #include <optional>
 #include <string>
 
@@ -130,9 +131,12 @@ class Call {
     has_stream_ = true;
   }
   Tensor empty(at::IntArrayRef shape, ScalarType type) const {
-    c10::cuda::OptionalCUDAStreamGuard guard;
-    if (has_stream_) guard.reset_stream(c10::cuda::getStreamFromExternal(given_, device_.index()));
+    const auto guard = on_stream();
     return Tensor(at::detail::empty_cuda(shape, type, device_, std::nullopt));
+  }
+  void fill(Tensor& t, double value) const {
+    const auto guard = on_stream();
+    t.fill_(value);
   }
   // `out` checked, or a new tensor where it is None.
   Tensor output(PyObject* out, at::IntArrayRef shape, ScalarType type, Types types, const char* name,
@@ -148,6 +152,12 @@ class Call {
   }
 
  private:
+  c10::cuda::OptionalCUDAStreamGuard on_stream() const {
+    std::optional<c10::Stream> s;
+    if (has_stream_) s = c10::cuda::getStreamFromExternal(given_, device_.index()).unwrap();
+    return c10::cuda::OptionalCUDAStreamGuard(s);
+  }
+
   at::Device device_;
   cudaStream_t given_ = nullptr;
   bool has_stream_ = false;
@@ -224,9 +234,13 @@ PyObject* rms_norm_s8(PyObject* const* a) {
   } else if (a[5] != Py_None) {
     fail("h_out without a residual: h is x");
   }
-  const Tensor scale = call.empty({M}, F32);
+  Tensor scale = call.empty({M}, F32);
   Tensor rstd;
   if (save) rstd = call.empty({M}, F32);
+  if (H == 0 && M > 0) {   // nothing is launched: rows of zeros, and the mean of no squares
+    call.fill(scale, 1.0);
+    if (save) call.fill(rstd, std::numeric_limits<double>::quiet_NaN());
+  }
   const qmm_status st =
       unlocked(qmm_rms_norm_s8, xp, qmm_type(t), M, H, ldx, rp, ldr, wp, qmm_type(w.scalar_type()), eps,
                res ? ptr(h) : nullptr, ptr(q), ptr(scale), save ? ptr(rstd) : nullptr, call.stream());
