@@ -298,6 +298,7 @@ PyObject* rms_norm_backward(PyObject* const* a) {
   if (THPVariable_Check(a[8])) {
     ws = tensor(a[8], "workspace");
     if (!ws.is_cuda()) fail("workspace must be a CUDA tensor");
+    if (!ws.is_contiguous()) fail("workspace must be contiguous");   // an expanded one has fewer bytes than elements
     check_device(ws, "workspace", h);
     have = ws.nbytes();
   } else if (bytes) {

@@ -147,3 +147,15 @@ def test_int8_operands_off_the_current_device_are_refused():
     assert len(lines) == 8
     for i, line in enumerate(lines):
         assert line.startswith("ValueError: ") and "cuda:1" in line and "cuda:0" in line, (i, line)
+
+
+def test_a_workspace_that_repeats_its_memory_is_refused():
+    """An expanded tensor has fewer bytes behind it than elements."""
+    lines = child("""
+    x, w, r = fake(4, 64), fake(64), fake(4)
+    n = q.qmm_rms_norm_backward_workspace_bytes(4, 64)
+    for ws in (fake(1, dtype=U8).expand(n), fake(n, 2, dtype=U8)[:, 0]):
+        print(outcome(lambda: q.qmm_rms_norm_backward(x, x, w, r, out=fake(4, 64), dweight=fake(64), stream=S,
+                                                      workspace=ws)))
+    """)
+    assert lines == ["ValueError: workspace must be contiguous"] * 2, lines
