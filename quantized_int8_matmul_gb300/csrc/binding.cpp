@@ -131,12 +131,10 @@ class Call {
     has_stream_ = true;
   }
   Tensor empty(at::IntArrayRef shape, ScalarType type) const {
-    const auto guard = on_stream();
-    return Tensor(at::detail::empty_cuda(shape, type, device_, std::nullopt));
+    return on_stream([&] { return Tensor(at::detail::empty_cuda(shape, type, device_, std::nullopt)); });
   }
   void fill(Tensor& t, double value) const {
-    const auto guard = on_stream();
-    t.fill_(value);
+    on_stream([&] { t.fill_(value); });
   }
   // `out` checked, or a new tensor where it is None.
   Tensor output(PyObject* out, at::IntArrayRef shape, ScalarType type, Types types, const char* name,
@@ -152,10 +150,12 @@ class Call {
   }
 
  private:
-  c10::cuda::OptionalCUDAStreamGuard on_stream() const {
-    std::optional<c10::Stream> s;
-    if (has_stream_) s = c10::cuda::getStreamFromExternal(given_, device_.index()).unwrap();
-    return c10::cuda::OptionalCUDAStreamGuard(s);
+  // f() with a given stream as the current one
+  template <typename F>
+  auto on_stream(F f) const -> decltype(f()) {
+    if (!has_stream_) return f();
+    const c10::cuda::CUDAStreamGuard guard(c10::cuda::getStreamFromExternal(given_, device_.index()));
+    return f();
   }
 
   at::Device device_;
