@@ -593,8 +593,8 @@ qmm_status qmm_rms_norm_backward(const void* dy, int64_t lddy, const void* h, in
  *                         [rows,cols]; with trans = 1, x is stored as [cols]
  *                         rows of `rows` elements (its transpose is packed, the
  *                         blocks running down x's columns)
- *  qmm_fp4_quantize_both  one read of x [rows,cols] to packed [rows,cols] and
- *                         packed_t [cols,rows]
+ *  qmm_fp4_quantize_both  x [rows,cols] to packed [rows,cols] and packed_t
+ *                         [cols,rows]; with block 32 x is read once
  *  qmm_fp4_dequantize     y [rows,cols] contiguous, y_dtype QMM_F32 or QMM_BF16:
  *                         y_dtype((code * s) * g)
  *  qmm_fp4_matmul         C[m,n] = c_dtype(((sum_k a*sa * b*sb) * ga[m]) * gb[n]),

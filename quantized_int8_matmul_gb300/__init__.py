@@ -832,7 +832,8 @@ def qmm_fp4_quantize(x, block=16, transpose=False, out=None, stream=None) -> Fp4
 
 
 def qmm_fp4_quantize_both(x, block=16, out=None, out_t=None, stream=None):
-    """(qmm_fp4_quantize(x), qmm_fp4_quantize(x, transpose=True)) from one read of x."""
+    """(qmm_fp4_quantize(x), qmm_fp4_quantize(x, transpose=True)) in one call; with block
+    32 x is read once."""
     R, C = _fp4_extents(x, block)
     buf = None if out is None else _fp4_buf(out, R, C, block, "out")
     buf_t = None if out_t is None else _fp4_buf(out_t, C, R, block, "out_t")

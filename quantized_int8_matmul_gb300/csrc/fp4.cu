@@ -1,5 +1,5 @@
 // Quantisation of a float matrix to 4-bit floats (e2m1) with block scales,
-// along its rows, its columns, or both from one read; and reading back.
+// along its rows, its columns, or both; and reading back.
 //
 // block 32 (a power of two per 32 elements, as in the OCP Microscaling Formats
 // specification, MXFP4): with b the block's largest magnitude, the scale is
@@ -13,7 +13,12 @@
 // settles it; the product applies it in its epilogue.
 // A block (32) or row (16) that holds a NaN or an infinity gets a NaN scale.
 //
-// Bound by HBM: x is read once, 0.53 or 0.56 bytes an element are written.
+// Bound by HBM: 0.53 or 0.56 bytes an element and direction are written, and x is read
+// once with block 32, both ways too. With block 16 a row or column has to be whole
+// before its first code: rows are read once where a CTA holds them, in registers (up to
+// four steps a warp of bf16, two of float32) or in shared memory, else twice; columns
+// once for up to 1024 rows (a cluster holds them), else twice, for their maxima and for
+// their codes; both ways twice at least. A second reading comes from L2 as far as x fits.
 #include "chain.cuh"
 #include "common.cuh"
 #include "fp4.cuh"
@@ -530,7 +535,7 @@ __global__ void __launch_bounds__(256) zero_kernel(unsigned* a, long long na, un
 // ---------------------------------------------------------------------------
 // Largest magnitudes of the columns (and the rows) into the packed buffers' max
 // words: 64 rows x 256 columns a CTA, eight columns a lane. 8192 x 4096 bf16: 11 of
-// the 27.0 us that block 16 takes along the columns (the second reading of x is
+// the 26.7 us that block 16 takes along the columns (the second reading of x is
 // largely from L2).
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256, VEC ? 4 : 2) absmax_kernel(const Fp4QuantArgs p, unsigned* colmax,
@@ -612,7 +617,7 @@ __global__ void __launch_bounds__(256, VEC ? 4 : 2) absmax_kernel(const Fp4Quant
 // columns' maxima are taken over it -- one launch in place of a fill, a pass for
 // the maxima and this. 8192 x 4096 bf16: block 32 both ways 19.6 us (5.3 TB/s, 79 %
 // of a copy's rate; issue slots 56 % busy), columns alone 15.1; block 16 with its
-// maxima 36.4 and 27.0. 4099 x 1021 float32, block 16, columns: 8.6 us.
+// maxima 36.2 and 26.7. 4099 x 1021 float32, block 16, columns: 8.4 us.
 template <typename T>
 struct TileSmem {
   static constexpr int PITCH = 128 * (int)sizeof(T) + 16;   // bytes; 16 more keep row accesses off each other's banks

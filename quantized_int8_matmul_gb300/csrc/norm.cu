@@ -10,9 +10,9 @@
 // squares, the maximum) run side by side in one pass.
 // Backward, one row, the quantiser passed straight through: n = h * rstd,
 //   g = dy * w;  dx = rstd * (g - n * mean(g * n)) (+ dh);  dw = sum over rows of dy * n.
-// Sums and statistics are fp32. Both are bound by HBM: every tensor is read or
-// written once, the row held in registers between its reduction and its output
-// (rows too long for that are read twice).
+// Sums and statistics are fp32 (rows whose squares leave its range: rescaled_row). Both
+// are bound by HBM: every tensor is read or written once, the row held in registers
+// between its reduction and its output (rows too long for that are read twice).
 #include "chain.cuh"
 #include "common.cuh"
 #include "kernels.h"
@@ -693,9 +693,9 @@ __global__ void __launch_bounds__(1024)
 // are on their way through the whole of this one's work. No copy reaches past the last
 // row of a tensor (4096 x 4095 bf16 with dh 49.1 us; 47.2 if the last one might). Rows of one vector a
 // thread go in pairs (RB = 2): one barrier and one reduction for both (8192 x 1024
-// bf16 21.1 -> 19.8 us). With sum_partials: 4096 x 4096 bf16 with dh 30.7 us (4.4
-// TB/s, 65 %), 4096 x 8192 49.6 (81 %), 1531 x 11008 float32 44.0 (69 %; 1531 rows
-// on 152 CTAs are eleven rounds for the longest and ten for the others). Of the 30.7
+// bf16 21.1 -> 19.8 us). With sum_partials: 4096 x 4096 bf16 with dh 30.1 us (4.5
+// TB/s, 67 %), 4096 x 8192 49.9 (80 %), 1531 x 11008 float32 43.5 (69 %; 1531 rows
+// on 152 CTAs are eleven rounds for the longest and ten for the others). Of the 30.1
 // the ring takes 26, the rest is the partial sums' own launch and pass. Waits are
 // bounded (common.cuh).
 constexpr int RING_MAX = 8;
@@ -1008,7 +1008,9 @@ cudaError_t launch_dequantize(const int8_t* q, const float* scale, long long M, 
 // 64 registers hold one vector of each tensor with its weight and sums, or two, or
 // three of float32; longer rows are read twice. CTAs are as many as fit at once
 // (1024 threads and the rings' two slots or more an SM, at most 8 an SM), no more
-// than rows, or a multiple of 8 (row_shift).
+// than rows, or a multiple of 8 (row_shift). They are counted for the 152 SMs of a GB300
+// and not the device's own, as the size of the workspace has to come out the same on a
+// host without one.
 struct BwdShape {
   int nv, G, R, parts, slots, tensors;
   size_t slot;   // bytes: a row of each of `tensors`
