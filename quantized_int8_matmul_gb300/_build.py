@@ -25,7 +25,7 @@ BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libqmm.so")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 BINDING_PATH = os.path.join(PKG_DIR, "_binding.so")
-BINDING_TAG = os.path.join(BUILD_DIR, "binding.tag")   # what BINDING_PATH was built for
+BINDING_TAG = os.path.join(PKG_DIR, "_binding.tag")   # beside it: what it was built for
 HEADERS = [os.path.join(REPO_DIR, "include", "qmm.h")]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]

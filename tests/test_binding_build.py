@@ -52,3 +52,10 @@ for f in (lambda: q.qmm_rms_norm_s8(torch.zeros(2, 8), torch.zeros(8)), lambda: 
     assert r.returncode == 0, r.stderr[-2000:]
     assert r.stdout.splitlines() == [f"True {q.qmm_fp4_bytes(128, 128, 16)}", "A must be a CUDA tensor",
                                      "RuntimeError True", "RuntimeError True"]
+
+
+def test_the_module_goes_without_the_build_folder(monkeypatch, tmp_path):
+    """A tree shipped with its two libraries and not the objects is not stale."""
+    assert os.path.dirname(_build.BINDING_TAG) == os.path.dirname(_build.BINDING_PATH)
+    monkeypatch.setattr(_build, "BUILD_DIR", str(tmp_path / "none"))
+    assert not _build.needs_build()
