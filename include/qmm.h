@@ -13,6 +13,8 @@
  *                            root-mean-square norm to int8 rows, its gradient
  *   qmm_fp4_quantize, qmm_fp4_quantize_both, qmm_fp4_dequantize, qmm_fp4_matmul
  *                            4-bit floats with block scales, and their product
+ *   qmm_kv_append, qmm_kv_read, qmm_kv_attention
+ *                            attention over a paged key-value cache of int8
  *
  * Conventions for every entry point:
  *  - Tensors are caller-owned DEVICE pointers, row-major and contiguous in the
@@ -618,6 +620,89 @@ qmm_status qmm_fp4_dequantize(const void* packed, size_t packed_bytes, int64_t r
                               int y_dtype, void* stream);
 qmm_status qmm_fp4_matmul(const void* a_packed, size_t a_bytes, int64_t M, const void* b_packed, size_t b_bytes,
                           int64_t N, int64_t K, int block, void* C, int c_dtype, void* stream);
+
+/*
+ * Attention over a paged key-value cache held in 8 bits.
+ *
+ * The cache (qmm_kv_cache): keys and values as int8 pages [pages, kv_heads, page,
+ * head_dim], contiguous and 16-byte aligned, and one byte for every 16 tokens of a
+ * page and head, k_exp and v_exp [pages, kv_heads, page / 16]: the 16 x head_dim
+ * numbers of such a block stand for int8 * 2^(byte - 127). page a multiple of 16,
+ * head_dim 64 or 128. A power of two, because a block fills token by token: when a
+ * new token needs a larger one, what the block already holds is shifted, each time
+ * by a factor of two or more, so that all its roundings together stay below one
+ * step; and int8 * 2^n is exact in bfloat16.
+ *
+ * The sequences of a call (qmm_kv_batch): their rows (tokens) are packed, sequence b
+ * owns rows starts[b] .. starts[b + 1] - 1 of `rows` (starts ascending; NULL: one row
+ * each, row b). lengths[b] counts the tokens of sequence b in the cache, the call's
+ * own n = starts[b + 1] - starts[b] as the last of them: row i is the token at position
+ * lengths[b] - n + i. table[b][p] names the page that holds positions p * page .. .
+ * All three are device memory, so a captured call follows them. Rows behind the last
+ * sequence's are left as they were. Nothing is read or written for a position below
+ * 0, for one beyond the table's row, or on a page outside [0, pages): such tokens are
+ * not stored, not seen by the attention, and read back as zeros. Page numbers may
+ * repeat where pages are only read; a block that two sequences append to in one call
+ * is undefined.
+ *
+ *  qmm_kv_append     stores the call's tokens: k and v [rows, kv_heads, head_dim] of
+ *                    `dtype` (QMM_F32 or QMM_BF16), elements of a head contiguous, rows
+ *                    and heads at any stride (k_row, k_head, ... in elements). The first
+ *                    `rotated` elements (a multiple of 16, 0: none) of each key head are
+ *                    rotated to the token's position first: pairs (i, i + rotated / 2),
+ *                    or neighbours (2 i, 2 i + 1) with interleaved = 1, become
+ *                    (a c - b s, b c + a s), c and s from cos and sin float[positions,
+ *                    rotated / 2], every operation rounded to float32. A block's byte is
+ *                    the smallest for which its largest magnitude rounds to 127 or
+ *                    less, and no smaller than it was while the block holds earlier
+ *                    tokens of the sequence; numbers are rounded to nearest even. A NaN
+ *                    is stored as 0, an infinity as the largest float32. q [rows,
+ *                    q_heads, head_dim], where not NULL, is rotated the same way into
+ *                    q_out (contiguous, dtype; may be q where that is contiguous). At a
+ *                    position without a row of cos and sin what is rotated is NaN.
+ *  qmm_kv_read       the tokens that the rows name, as dtype(int8 * 2^(byte - 127)) to k
+ *                    and v [rows, kv_heads, head_dim] contiguous; either may be NULL
+ *  qmm_kv_attention  out[t, h] = sum_j p_j v_j / sum_j p_j, p_j = exp(scale * q[t, h] .
+ *                    k_j), over the cached tokens j of the row's sequence: up to its own
+ *                    position with causal = 1, all lengths[b] with causal = 0 (states of
+ *                    an encoder, whose number has nothing to do with the rows). Query
+ *                    head h reads key head h / (q_heads / kv_heads). Sums and maxima in
+ *                    float32. A row that sees nothing gets zeros, one whose q holds a
+ *                    NaN or an infinity NaN. out [rows, q_heads, head_dim] contiguous,
+ *                    of q's dtype. max_tokens: no sequence has more rows, as far as the
+ *                    caller knows; it chooses kernels and splits, never results'
+ *                    validity (rows: always true).
+ *  workspace         qmm_kv_attention_workspace_bytes of the same arguments, 16-byte
+ *                    aligned; nothing in it has to survive a call, or to be zero
+ * rows = 0 or batch = 0 launches nothing. QMM_ERR_UNSUPPORTED for another head_dim, page
+ * or `rotated`; QMM_ERR_INVALID_ARG for a bad dtype, stride, null or unaligned pointer,
+ * short workspace, q_heads that kv_heads does not divide, starts = NULL with rows !=
+ * batch, width * page or rows * q_heads beyond 2^31 - 1.
+ */
+typedef struct {
+  int8_t* k;
+  int8_t* v;
+  uint8_t* k_exp;
+  uint8_t* v_exp;
+  int64_t pages, kv_heads, page, head_dim;
+} qmm_kv_cache;
+typedef struct {
+  const int32_t* table;   /* [batch, width] */
+  const int32_t* lengths; /* [batch] */
+  const int32_t* starts;  /* [batch + 1] or NULL */
+  int64_t batch, width, rows;
+} qmm_kv_batch;
+qmm_status qmm_kv_append(const qmm_kv_cache* cache, const qmm_kv_batch* batch, int dtype, const void* k,
+                         int64_t k_row, int64_t k_head, const void* v, int64_t v_row, int64_t v_head, const void* q,
+                         int64_t q_row, int64_t q_head, int64_t q_heads, void* q_out, const float* cos,
+                         const float* sin, int64_t positions, int64_t rotated, int interleaved, void* stream);
+qmm_status qmm_kv_read(const qmm_kv_cache* cache, const qmm_kv_batch* batch, void* k, void* v, int dtype,
+                       void* stream);
+size_t qmm_kv_attention_workspace_bytes(int64_t rows, int64_t batch, int64_t q_heads, int64_t kv_heads,
+                                        int64_t head_dim, int dtype, int64_t max_tokens);
+qmm_status qmm_kv_attention(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const void* q, int dtype,
+                            int64_t q_row, int64_t q_head, int64_t q_heads, float scale, int causal,
+                            int64_t max_tokens, void* out, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Human-readable name of a status. Never NULL. */
 const char* qmm_status_string(int status);

@@ -7,7 +7,7 @@ status. Every step of the computation runs in the library's CUDA kernels;
 there is no CPU or PyTorch fallback. Output tensors are allocated with torch
 when the caller does not pass one (device memory is PyTorch's job here). The
 marshalling of the calls that are often shorter than their marshalling (the norm,
-4-bit floats) is native, in the ``_binding`` module; the others use ctypes.
+4-bit floats, the key-value cache) is native, in the ``_binding`` module; the others use ctypes.
 
 ``stream``: a call that is given one runs on it and allocates device memory from its
 memory, as under ``torch.cuda.stream(stream)``: what it returns is ready, and its
@@ -117,6 +117,8 @@ def _load() -> ctypes.CDLL:
     lib.qmm_rms_norm_backward_workspace_bytes.restype = sz
     lib.qmm_fp4_bytes.argtypes = [i64, i64, ci]
     lib.qmm_fp4_bytes.restype = sz
+    lib.qmm_kv_attention_workspace_bytes.argtypes = [i64, i64, i64, i64, i64, ci, i64]
+    lib.qmm_kv_attention_workspace_bytes.restype = sz
     lib.qmm_int8_mma_peak_launch.argtypes = [ci, ctypes.POINTER(ctypes.c_double), vp]
     lib.qmm_int8_mma_peak_launch.restype = ci
     return lib
@@ -867,6 +869,94 @@ def qmm_fp4_matmul(a: Fp4Matrix, b: Fp4Matrix, out=None, out_dtype=torch.bfloat1
     return r
 
 
+class KvCache(NamedTuple):
+    """A paged key-value cache in 8 bits: keys and values int8 [pages, kv_heads, page,
+    head_dim], contiguous, and a byte for every 16 tokens of a page and head, uint8
+    [pages, kv_heads, page // 16]: a block's numbers stand for int8 * 2^(byte - 127).
+    page is a multiple of 16, head_dim 64 or 128. The tensors need no first values."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_exp: torch.Tensor
+    v_exp: torch.Tensor
+
+
+def qmm_kv_cache(pages: int, kv_heads: int, head_dim: int, page: int = 64, device="cuda") -> KvCache:
+    """The tensors of a cache of `pages` pages of `page` tokens, zeros."""
+    if head_dim not in (64, 128):
+        raise ValueError("head_dim must be 64 or 128")
+    if page < 16 or page % 16:
+        raise ValueError("page must be a multiple of 16")
+    kv = [torch.zeros((pages, kv_heads, page, head_dim), dtype=torch.int8, device=device) for _ in range(2)]
+    exps = [torch.zeros((pages, kv_heads, page // 16), dtype=torch.uint8, device=device) for _ in range(2)]
+    return KvCache(*kv, *exps)
+
+
+def qmm_kv_append(cache: KvCache, k, v, table, lengths, starts=None, q=None, cos=None, sin=None, interleaved=False,
+                  q_out=None, stream=None):
+    """Store the tokens k, v [rows, kv_heads, head_dim] (float32 or bfloat16, heads
+    contiguous at any strides) in the cache, and rotate keys and queries to their
+    positions on the way. Returns q rotated (q_out, or a new tensor), None without q.
+
+    Rows are packed: sequence b owns rows starts[b] to starts[b + 1] (int32 [batch + 1]
+    on the device; None: one row a sequence), its tokens at positions lengths[b] - n to
+    lengths[b] - 1: lengths (int32 [batch]) counts the new tokens in. table (int32
+    [batch, width]) names each sequence's pages in order. cos, sin: float32 [positions,
+    rotated / 2], or None for no rotation; the first `rotated` elements of a head (a
+    multiple of 16) turn in pairs (i, i + rotated / 2), with interleaved (2 i, 2 i + 1).
+
+    A block's scale is that of its largest number and grows with it, the tokens that it
+    holds following; a block whose first token is new starts afresh. Tokens on pages
+    outside the cache, or beyond the table, are not stored; NaN is stored as 0. A
+    position without a row of cos and sin gives NaN queries (and zero keys)."""
+    r = _binding.kv_append(*cache, table, lengths, starts, k, v, q, cos, sin, interleaved, q_out, stream)
+    if type(r) is int:
+        raise QmmError("qmm_kv_append", r)
+    return r
+
+
+def qmm_kv_read(cache: KvCache, table, lengths, starts=None, rows=None, k_out=None, v_out=None,
+                out_dtype=torch.bfloat16, stream=None):
+    """Cached tokens read back, (k, v) [rows, kv_heads, head_dim] float32 or bfloat16:
+    row starts[b] + i is the token at position lengths[b] - n + i of sequence b, as in
+    qmm_kv_append. rows: how many there are in all (starts is on the device; default:
+    one a sequence). A token that the cache does not hold reads as zeros; rows behind
+    the last sequence's are left as they were."""
+    if rows is None:
+        if starts is not None:
+            raise ValueError("rows is needed with starts")
+        rows = table.shape[0]
+    r = _binding.kv_read(*cache, table, lengths, starts, rows, k_out, v_out, out_dtype, stream)
+    if type(r) is int:
+        raise QmmError("qmm_kv_read", r)
+    return r
+
+
+def qmm_kv_attention_workspace_bytes(rows: int, batch: int, q_heads: int, kv_heads: int, head_dim: int,
+                                     dtype=torch.bfloat16, max_tokens=None) -> int:
+    return int(_lib.qmm_kv_attention_workspace_bytes(rows, batch, q_heads, kv_heads, head_dim, _TORCH_TO_QMM[dtype],
+                                                     rows if max_tokens is None else max_tokens))
+
+
+def qmm_kv_attention(q, cache: KvCache, table, lengths, starts=None, scale=None, causal=True, max_tokens=None, out=None,
+                     stream=None, workspace="auto"):
+    """softmax(q k^T * scale) v of q [rows, q_heads, head_dim] (float32 or bfloat16,
+    heads contiguous at any strides) over the cache, [rows, q_heads, head_dim].
+
+    Sequences as in qmm_kv_append: row i of n sees the tokens up to its own position,
+    lengths[b] - n + i (causal), or all lengths[b] (causal=False: an encoder's states).
+    Query head h reads key head h // (q_heads // kv_heads). scale: head_dim ** -0.5 by
+    default. A row that sees nothing gets zeros, one whose q is not finite NaN.
+    max_tokens: the most rows a sequence has, where the host knows it (default: all
+    rows); it picks the kernels. workspace: "auto" or a device tensor of
+    qmm_kv_attention_workspace_bytes bytes, which calls that run at once must not share."""
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    r = _binding.kv_attention(*cache, table, lengths, starts, q, scale, causal, max_tokens, out, stream, workspace)
+    if type(r) is int:
+        raise QmmError("qmm_kv_attention", r)
+    return r
+
+
 def num_sms() -> int:
     return int(_lib.qmm_num_sms())
 
@@ -877,6 +967,7 @@ __all__ = [
     "dynamic_quantize_linear",
     "qmm_rms_norm_s8", "RmsNormS8", "qmm_s8_dequantize_rows", "qmm_rms_norm_backward", "qmm_fp4_quantize",
     "qmm_fp4_quantize_both", "qmm_fp4_dequantize", "qmm_fp4_matmul", "qmm_fp4_bytes", "Fp4Matrix",
+    "KvCache", "qmm_kv_cache", "qmm_kv_append", "qmm_kv_read", "qmm_kv_attention", "qmm_kv_attention_workspace_bytes",
     "dynamic_quantize_linear_workspace_bytes", "last_kernel", "check_device_error", "QmmError", "lib",
     "num_sms", "LIB_PATH",
 ]

@@ -104,7 +104,8 @@ const Tensor& need_rows(PyObject* o, Types types, const char* name, int64_t& ld,
   return t;
 }
 
-constexpr ScalarType F32 = ScalarType::Float, BF16 = ScalarType::BFloat16, S8 = ScalarType::Char, U8 = ScalarType::Byte;
+constexpr ScalarType F32 = ScalarType::Float, BF16 = ScalarType::BFloat16, S8 = ScalarType::Char, U8 = ScalarType::Byte,
+                     S32 = ScalarType::Int;
 #define FLOATS {F32, BF16}
 
 ScalarType float_type(PyObject* o) {
@@ -377,6 +378,162 @@ PyObject* fp4_matmul(PyObject* const* a) {
   return st != QMM_OK ? PyLong_FromLong(st) : wrap(y);
 }
 
+// The cache (k, v, k_exp, v_exp) and the sequences of a call (table, lengths, starts),
+// of `rows` packed rows; all on one device.
+void kv_arguments(PyObject* const* cache, PyObject* const* batch, const Tensor& first, int64_t rows, qmm_kv_cache& c,
+                  qmm_kv_batch& b) {
+  const Tensor& k = need(cache[0], {S8}, "cache.k");
+  if (k.dim() != 4) fail("cache.k must be [pages, kv_heads, page, head_dim]");
+  check_device(k, "cache.k", first);
+  const int64_t pages = k.size(0), heads = k.size(1), page = k.size(2);
+  const Tensor& v = need(cache[1], {S8}, "cache.v", k.sizes(), first);
+  const Tensor& ke = need(cache[2], {U8}, "cache.k_exp", {pages, heads, page / 16}, first);
+  const Tensor& ve = need(cache[3], {U8}, "cache.v_exp", {pages, heads, page / 16}, first);
+  c = {static_cast<int8_t*>(ptr(k)), static_cast<int8_t*>(ptr(v)), static_cast<uint8_t*>(ptr(ke)),
+       static_cast<uint8_t*>(ptr(ve)), pages, heads, page, k.size(3)};
+  const Tensor& table = need(batch[0], {S32}, "table");
+  if (table.dim() != 2) fail("table must be 2-D");
+  check_device(table, "table", first);
+  const int64_t n = table.size(0);
+  const Tensor& lengths = need(batch[1], {S32}, "lengths", {n}, first);
+  const void* starts = nullptr;
+  if (batch[2] != Py_None) {
+    starts = ptr(need(batch[2], {S32}, "starts", {n + 1}, first));
+  } else if (rows != n) {
+    fail("without starts there is one row a sequence");
+  }
+  b = {static_cast<const int32_t*>(ptr(table)), static_cast<const int32_t*>(ptr(lengths)),
+       static_cast<const int32_t*>(starts), n, table.size(1), rows};
+}
+
+// A 3-D tensor [rows, heads, dim] whose heads are contiguous, at any strides of rows
+// and heads.
+const Tensor& need_heads(PyObject* o, Types types, const char* name, int64_t& row, int64_t& head) {
+  const Tensor& t = tensor(o, name);
+  check_type(t, types, name);
+  if (t.dim() != 3) fail(std::string(name) + " must be [rows, heads, head_dim]");
+  if (t.size(2) > 1 && t.stride(2) != 1) fail(std::string(name) + ": heads must be contiguous");
+  row = t.size(0) > 1 ? t.stride(0) : 0;
+  head = t.size(1) > 1 ? t.stride(1) : 0;
+  return t;
+}
+const Tensor& need_heads(PyObject* o, Types types, const char* name, int64_t& row, int64_t& head,
+                         at::IntArrayRef shape, const Tensor& first) {
+  const Tensor& t = need_heads(o, types, name, row, head);
+  if (t.sizes() != shape) fail(std::string(name) + " must be " + shape_text(shape));
+  check_device(t, name, first);
+  return t;
+}
+
+// cache (4), table, lengths, starts, k, v, q, cos, sin, interleaved, q_out, stream -> q_out or None
+PyObject* kv_append(PyObject* const* a) {
+  int64_t k_row, k_head, v_row, v_head, q_row = 0, q_head = 0;
+  const Tensor& k = need_heads(a[7], FLOATS, "k", k_row, k_head);
+  const ScalarType t = k.scalar_type();
+  const int64_t rows = k.size(0), dim = k.size(2);
+  const Tensor& v = need_heads(a[8], {t}, "v", v_row, v_head, k.sizes(), k);
+  qmm_kv_cache cache;
+  qmm_kv_batch batch;
+  kv_arguments(a, a + 4, k, rows, cache, batch);
+  if (cache.kv_heads != k.size(1) || cache.head_dim != dim) fail("k and v must have the cache's heads");
+  const bool turn = a[10] != Py_None;
+  if (turn != (a[11] != Py_None)) fail("cos and sin go together");
+  const void *cos = nullptr, *sin = nullptr;
+  int64_t positions = 0, rotated = 0;
+  if (turn) {
+    const Tensor& c = need(a[10], {F32}, "cos");
+    if (c.dim() != 2) fail("cos must be [positions, rotated / 2]");
+    check_device(c, "cos", k);
+    sin = ptr(need(a[11], {F32}, "sin", c.sizes(), k));
+    cos = ptr(c);
+    positions = c.size(0);
+    rotated = 2 * c.size(1);
+  }
+  const int interleaved = truth(a[12]);
+  const Call call(a[14], k);
+  const void* qp = nullptr;
+  int64_t q_heads = 0;
+  Tensor out;
+  if (a[9] != Py_None) {
+    const Tensor& q = need_heads(a[9], {t}, "q", q_row, q_head);
+    check_device(q, "q", k);
+    if (q.size(0) != rows || q.size(2) != dim) fail("q must have k's rows and head_dim");
+    q_heads = q.size(1);
+    if (q_heads < 1) fail("q has no heads");
+    // a stride that the extent leaves open is the one of a contiguous tensor
+    if (rows <= 1) q_row = q_heads * dim;
+    if (q_heads <= 1) q_head = dim;
+    qp = ptr(q);
+    out = call.output(a[13], q.sizes(), t, {t}, "q_out", k);
+  } else if (a[13] != Py_None) {
+    fail("q_out without q");
+  }
+  const qmm_status st = unlocked(
+      qmm_kv_append, &cache, &batch, qmm_type(t), ptr(k), k_row, k_head, ptr(v), v_row, v_head, qp, q_row, q_head,
+      q_heads, out.defined() ? ptr(out) : nullptr, static_cast<const float*>(cos), static_cast<const float*>(sin),
+      positions, rotated, interleaved, call.stream());
+  if (st != QMM_OK) return PyLong_FromLong(st);
+  if (out.defined()) return wrap(out);
+  Py_RETURN_NONE;
+}
+
+// cache (4), table, lengths, starts, rows, k_out, v_out, out_dtype, stream -> (k, v)
+PyObject* kv_read(PyObject* const* a) {
+  const Tensor& first = need(a[0], {S8}, "cache.k");
+  const int64_t rows = integer(a[7]);
+  if (rows < 0) fail("rows must not be negative");
+  qmm_kv_cache cache;
+  qmm_kv_batch batch;
+  kv_arguments(a, a + 4, first, rows, cache, batch);
+  ScalarType t = float_type(a[10]);
+  const Call call(a[11], first);
+  const int64_t shape[3] = {rows, cache.kv_heads, cache.head_dim};
+  const Tensor k = call.output(a[8], shape, t, FLOATS, "k_out", first);
+  if (a[8] != Py_None) t = k.scalar_type();
+  const Tensor v = call.output(a[9], shape, t, {t}, "v_out", first);
+  const qmm_status st = unlocked(qmm_kv_read, &cache, &batch, ptr(k), ptr(v), qmm_type(t), call.stream());
+  return st != QMM_OK ? PyLong_FromLong(st) : pair(wrap(k), wrap(v));
+}
+
+// cache (4), table, lengths, starts, q, scale, causal, max_tokens, out, stream, workspace -> out
+PyObject* kv_attention(PyObject* const* a) {
+  int64_t q_row, q_head;
+  const Tensor& q = need_heads(a[7], FLOATS, "q", q_row, q_head);
+  const ScalarType t = q.scalar_type();
+  const int64_t rows = q.size(0), q_heads = q.size(1), dim = q.size(2);
+  qmm_kv_cache cache;
+  qmm_kv_batch batch;
+  kv_arguments(a, a + 4, q, rows, cache, batch);
+  if (cache.head_dim != dim) fail("q must have the cache's head_dim");
+  const double scale = PyFloat_AsDouble(a[8]);
+  if (PyErr_Occurred()) throw Error();
+  const int causal = truth(a[9]);
+  const int64_t max_tokens = a[10] == Py_None ? (rows > 1 ? rows : 1) : integer(a[10]);
+  const void* qp = ptr(q);
+  const Call call(a[12], q);
+  const Tensor out = call.output(a[11], q.sizes(), t, {t}, "out", q);
+  const size_t bytes = qmm_kv_attention_workspace_bytes(rows, batch.batch, q_heads, cache.kv_heads, dim, qmm_type(t),
+                                                        max_tokens);
+  Tensor ws;
+  size_t have = 0;
+  if (THPVariable_Check(a[13])) {
+    ws = tensor(a[13], "workspace");
+    if (!ws.is_cuda()) fail("workspace must be a CUDA tensor");
+    if (!ws.is_contiguous()) fail("workspace must be contiguous");
+    check_device(ws, "workspace", q);
+    have = ws.nbytes();
+  } else {
+    if (!PyUnicode_Check(a[13]) || PyUnicode_CompareWithASCIIString(a[13], "auto") != 0)
+      fail("workspace must be 'auto' or a device tensor");
+    if (bytes) ws = call.empty({(int64_t)bytes}, U8);
+    have = bytes;
+  }
+  const qmm_status st = unlocked(qmm_kv_attention, &cache, &batch, qp, qmm_type(t), q_row, q_head, q_heads,
+                                 (float)scale, causal, max_tokens, ptr(out), ws.defined() ? ptr(ws) : nullptr, have,
+                                 call.stream());
+  return st != QMM_OK ? PyLong_FromLong(st) : wrap(out);
+}
+
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != N) {
@@ -397,7 +554,8 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   { #f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<f, n>)), METH_FASTCALL, nullptr }
 PyMethodDef methods[] = {ENTRY(rms_norm_s8, 8),   ENTRY(s8_dequantize_rows, 5), ENTRY(rms_norm_backward, 9),
                          ENTRY(fp4_quantize, 5),  ENTRY(fp4_quantize_both, 5),  ENTRY(fp4_dequantize, 7),
-                         ENTRY(fp4_matmul, 9),    {nullptr, nullptr, 0, nullptr}};
+                         ENTRY(fp4_matmul, 9),    ENTRY(kv_append, 15),         ENTRY(kv_read, 12),
+                         ENTRY(kv_attention, 14), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "Argument marshalling of the C ABI.", -1, methods};
 
 }  // namespace

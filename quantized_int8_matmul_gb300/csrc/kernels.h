@@ -353,6 +353,58 @@ struct GemmFp4Args {
 cudaError_t launch_gemm_fp4_pair(const GemmFp4Args& a, int block, cudaStream_t s);
 cudaError_t launch_gemm_fp4(const GemmFp4Args& a, int block, cudaStream_t s, const char** kernel_name);
 
+// ---------------------------------------------------------------------------
+// 8-bit key-value cache (kv_cache.cu) and attention over it (kv_attention.cu).
+// ---------------------------------------------------------------------------
+struct KvCacheArgs {
+  int8_t *k, *v;               // [pages][heads][bpp * 16][head_dim]
+  uint8_t *ke, *ve;            // [pages][heads][bpp]
+  int pages, heads, bpp;       // bpp: blocks of 16 tokens a page
+};
+struct KvBatchArgs {
+  const int* table;            // [batch][width] page numbers
+  const int* lengths;          // [batch]
+  const int* starts;           // [batch + 1], or null: row b is sequence b
+  int width, batch, rows;
+  int capacity;                // width * page: tokens that a sequence's row of the table has room for
+};
+struct KvAppendArgs {
+  KvCacheArgs cache;
+  KvBatchArgs batch;
+  const void *k, *v, *q;       // f32 or bf16; q may be null
+  long long k_row, k_head, v_row, v_head, q_row, q_head;   // elements between rows and heads
+  void* q_out;                 // [rows][q_heads][head_dim]
+  const float *cos, *sin;      // [positions][half]
+  int positions, half, interleaved, q_heads;
+  int slots, slot_ctas;        // set by the launch
+};
+// vec: every row and head of k, v and q starts on 16 bytes
+cudaError_t launch_kv_append(const KvAppendArgs& a, int head_dim, bool bf16, bool vec, cudaStream_t s,
+                             const char** kernel_name);
+struct KvReadArgs {
+  KvCacheArgs cache;
+  KvBatchArgs batch;
+  void *k, *v;                 // [rows][heads][head_dim], either may be null
+};
+cudaError_t launch_kv_read(const KvReadArgs& a, int head_dim, bool bf16, cudaStream_t s, const char** kernel_name);
+struct KvAttentionArgs {
+  KvCacheArgs cache;
+  KvBatchArgs batch;
+  const void* q;               // f32 or bf16
+  long long q_row, q_head;
+  void* out;                   // [rows][heads * group][head_dim]
+  int group;                   // query heads a key head
+  int causal;
+  float scale;
+  int max_tokens;              // the longest sequence's rows, as the caller knows it (a hint)
+  void* workspace;
+  unsigned* err;               // device error word
+};
+size_t kv_attention_workspace(int rows, int batch, int heads, int group, int head_dim, int max_tokens, bool bf16);
+// vec: every row and head of q starts on 16 bytes
+cudaError_t launch_kv_attention(const KvAttentionArgs& a, int head_dim, bool bf16, bool vec, cudaStream_t s,
+                                const char** kernel_name);
+
 int num_sms();
 // The unique id of the calling thread's current CUDA context; false when no
 // context is current (or the driver offers no such query).

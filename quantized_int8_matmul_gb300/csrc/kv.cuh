@@ -1,0 +1,113 @@
+// The 8-bit key-value cache as the kernels see it (format: include/qmm.h), and the
+// packed sequences of a call.
+#pragma once
+
+#include <climits>
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "kernels.h"
+
+namespace qmm {
+
+constexpr int kKvBlock = 16;   // tokens that share a scale
+
+// One sequence of a call: its packed rows and its tokens in the cache. What the
+// device finds in starts and lengths is clamped to the call's rows and to the table,
+// so that no index derived from them leaves either.
+struct KvSeq {
+  int start;   // first packed row
+  int n;       // rows
+  int len;     // tokens, the rows' own among them, as given (0 where negative)
+  int seen;    // of those, the ones that the table has room for
+};
+
+__device__ __forceinline__ KvSeq kv_sequence(const KvBatchArgs& a, int b) {
+  KvSeq s;
+  int s0 = b, s1 = b + 1;
+  if (a.starts) {
+    s0 = __ldg(a.starts + b);
+    s1 = __ldg(a.starts + b + 1);
+  }
+  s.start = min(max(s0, 0), a.rows);
+  s.n = max(min(s1, a.rows) - s.start, 0);
+  s.len = max(__ldg(a.lengths + b), 0);
+  s.seen = min(s.len, a.capacity);
+  return s;
+}
+
+// How many tokens row token i of a sequence sees.
+__device__ __forceinline__ int kv_visible(const KvSeq& s, int i, int causal) {
+  return causal ? min(max(s.len - s.n + i + 1, 0), s.seen) : s.seen;
+}
+
+// The sequence that packed row t belongs to, or -1; a whole warp asks for one row.
+__device__ __forceinline__ int kv_sequence_of_row(const KvBatchArgs& a, int t) {
+  if (!a.starts) return t < a.batch ? t : -1;
+  const int lane = threadIdx.x & 31;
+  int count = 0;   // starts[1 ..] that are <= t
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    const int b = b0 + lane;
+    count += __popc(__ballot_sync(~0u, b < a.batch && __ldg(a.starts + b + 1) <= t));
+  }
+  return count < a.batch ? count : -1;
+}
+
+// 2^(byte - 127); the smallest one is below float32's normal range.
+__device__ __forceinline__ float kv_power(int byte) {
+  return __int_as_float(byte > 0 ? byte << 23 : 0x00400000);
+}
+// The byte of a block with the largest magnitude amax (finite): the smallest power of
+// two under which amax rounds to 127 or less (amax / step < 127.5, that is a mantissa
+// below 0x7f0000 at a step six binades down).
+__device__ __forceinline__ int kv_exponent(float amax) {
+  return max(((__float_as_int(amax) + 0x10000) >> 23) - 6, 0);
+}
+
+__device__ __forceinline__ float kv_float(float x) { return x; }
+__device__ __forceinline__ float kv_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// Eight consecutive elements as float32; kVec: on a 16-byte boundary.
+template <bool kVec>
+__device__ __forceinline__ void kv_load8(const __nv_bfloat16* p, float (&x)[8]) {
+  if constexpr (kVec) {
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(u[i] << 16);
+      x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __bfloat162float(p[i]);
+  }
+}
+template <bool kVec>
+__device__ __forceinline__ void kv_load8(const float* p, float (&x)[8]) {
+  if constexpr (kVec) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = p[i];
+  }
+}
+// Eight elements to a 16-byte boundary.
+__device__ __forceinline__ void kv_store8(__nv_bfloat16* p, const float (&x)[8]) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    u[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+__device__ __forceinline__ void kv_store8(float* p, const float (&x)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+}  // namespace qmm

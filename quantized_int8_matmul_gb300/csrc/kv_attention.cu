@@ -1,0 +1,737 @@
+// Attention over the 8-bit key-value cache for few rows: a token, or a few drafted
+// ones, of each sequence (and every length of float32 rows).
+//
+//   o = sum_j p_j v_j / sum_j p_j,   p_j = exp2(c q.k_j - m),   c = scale * log2(e)
+//
+// What bounds it is the cache: every byte of it is read once, and 2 * group * 2
+// operations are made of each. So the work is cut by bytes. All (sequence, key head,
+// tile of rows) items are laid end to end in blocks of 16 tokens, and every warp of
+// the GPU takes the same number of consecutive blocks, wherever items begin and end:
+// long and short sequences balance, and one long sequence spreads over all SMs. Where
+// an item's blocks fall to several warps, the warps of a CTA join their parts through
+// shared memory, and a second kernel joins what several CTAs hold, both in the order
+// of the blocks.
+//
+// Inside a warp, tokens are the rows (M = 16: one block, one scale) and query rows the
+// columns (N = 8) of mma m16n8k16 in fp16: S^T = K Q^T, O^T = V^T P^T. A group of up to
+// 8 query heads then costs one MMA where rows of queries would pad to 16. int8 is exact
+// in fp16. bfloat16 rows of Q are scaled by a power of two each, under which fp16
+// holds them exactly down to 2^-24 of the row's largest value; float32 rows are split
+// in two fp16 parts (22 bits), and so are their P. The order of a sum's terms is free,
+// so a lane's 16 consecutive bytes of K serve four k-steps as they come, and its bytes
+// of V are interleaved by token pairs; each lane copies by cp.async exactly the bytes
+// that it will read, into its own slots of a ring, so that the loop has no barrier.
+//
+// The running maximum moves only when some score is 8 (a factor of 256) above it,
+// which a vote finds out: P keeps six more bits below fp16's largest value and 30 bits
+// to its smallest. V's power of two goes into P the same way.
+#include "chain.cuh"
+#include "common.cuh"
+#include "kv.cuh"
+
+namespace qmm {
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr float kNone = -1e30f;      // a running maximum that has seen nothing
+constexpr float kSlack = 8.f;        // how far a score may pass the running maximum
+constexpr int kLift = 6;             // P is held times 2^kLift
+constexpr int kMinBlocks = 4;        // blocks a warp, at least
+
+// A part of an item that one warp (in shared memory) or one CTA (in the workspace) holds.
+enum { kPartNone = 0, kPartHeld = 1, kPartBegins = 2, kPartEnds = 4 };
+struct Part {
+  int b, r, h, flags;
+};
+
+template <int D, int NT>
+struct Shape {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kStages = D == 64 ? 8 : NT == 1 ? 5 : 4;
+  static constexpr int kChunk = 2 * kKvBlock * D;                 // K and V of one block
+  static constexpr int kStage = kChunk + 128;                     // and a word a lane
+  static constexpr int kRing = kStages * kStage;                  // a warp's
+  static constexpr int kPartBytes = kRows * D * 4 + kRows * 8;    // rows of O, then (m, l) each
+  static_assert(kRing >= kPartBytes, "a warp's last part takes the place of its ring");
+  static constexpr int kSmem = kWarps * (kRing + kPartBytes) + 2 * kWarps * (int)sizeof(Part);
+  static_assert(kSmem <= 227 * 1024, "one CTA an SM");
+  static constexpr int kWsPart = kPartBytes;                      // in the workspace
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t half_pair(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float half_low(uint32_t u) { return __half2float(__ushort_as_half((unsigned short)u)); }
+__device__ __forceinline__ float half_high(uint32_t u) {
+  return __half2float(__ushort_as_half((unsigned short)(u >> 16)));
+}
+__device__ __forceinline__ uint32_t bytes_low(uint32_t u) {   // bytes 0, 1 (biased by 128) to two fp16
+  const uint32_t l = prmt(u, 0x64646464u, 0x4140u);
+  __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&l), __half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480)));
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t bytes_high(uint32_t u) {  // bytes 2, 3
+  const uint32_t l = prmt(u, 0x64646464u, 0x4342u);
+  __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&l), __half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480)));
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+struct Work {
+  KvAttentionArgs a;
+  int rows_limit;        // sequences with more rows a key head than this are not this kernel's (0: no limit)
+  Part* parts;           // [ctas][2]
+  uint8_t* ws;           // [ctas][2] parts
+  int ctas;
+};
+
+// The blocks of one row tile: at least one, so that rows that see nothing are written.
+template <int NT>
+__device__ __forceinline__ int tile_blocks(const Work& w, const KvSeq& s, int r) {
+  const int last = min(((r + 1) * 8 * NT - 1) / w.a.group, s.n - 1);
+  return max((kv_visible(s, last, w.a.causal) + kKvBlock - 1) / kKvBlock, 1);
+}
+template <int NT>
+__device__ __forceinline__ int tile_count(const Work& w, const KvSeq& s) {
+  const long long rows = (long long)s.n * w.a.group;
+  if (w.rows_limit && rows > w.rows_limit) return 0;
+  return (int)((rows + 8 * NT - 1) / (8 * NT));
+}
+template <int NT>
+__device__ __forceinline__ long long sequence_blocks(const Work& w, int b) {
+  const KvSeq s = kv_sequence(w.a.batch, b);
+  const int tiles = tile_count<NT>(w, s);
+  long long sum = 0;
+  for (int r = 0; r < tiles; ++r) sum += tile_blocks<NT>(w, s, r);
+  return sum * w.a.cache.heads;
+}
+
+// A place in the line of blocks.
+template <int NT>
+struct Cursor {
+  int b, r, h, blk, blocks, tiles;
+  KvSeq s;
+
+  __device__ void open(const Work& w) { blocks = tile_blocks<NT>(w, s, r); }
+  // To block `at` of sequence b.
+  __device__ void seek(const Work& w, int seq, long long at) {
+    b = seq;
+    s = kv_sequence(w.a.batch, b);
+    tiles = tile_count<NT>(w, s);
+    for (r = 0;; ++r) {
+      open(w);
+      const long long tile = (long long)blocks * w.a.cache.heads;
+      if (at < tile || r + 1 >= tiles) break;
+      at -= tile;
+    }
+    h = (int)(at / blocks);
+    blk = (int)(at % blocks);
+  }
+  // To the next item's first block.
+  __device__ void next_item(const Work& w) {
+    blk = 0;
+    if (++h < w.a.cache.heads) return;
+    h = 0;
+    if (++r < tiles) {
+      open(w);
+      return;
+    }
+    r = 0;
+    do {
+      if (++b >= w.a.batch.batch) return;
+      s = kv_sequence(w.a.batch, b);
+      tiles = tile_count<NT>(w, s);
+    } while (tiles == 0);
+    open(w);
+  }
+};
+
+// Where rows of an item go: rows are (token, query head of the group), token major.
+__device__ __forceinline__ long long out_row(const KvAttentionArgs& a, const KvSeq& s, int h, int row) {
+  return (long long)(s.start + row / a.group) * ((long long)a.cache.heads * a.group) + (long long)h * a.group +
+         row % a.group;
+}
+
+// Parts [first, first + count) of one item joined, one row by one warp: rows of O that
+// are already divided by their own sums l, with their maxima m. part(i) gives the
+// i-th part's bytes. The joined row is written to `out` (T, row index given) where it
+// is the whole item's, else as a part again.
+template <int D, typename T, typename F>
+__device__ __forceinline__ void join_row(int count, int rows, int row, F part, bool whole, T* out, uint8_t* into) {
+  constexpr int kE = D / 32;
+  const int lane = threadIdx.x & 31;
+  float top = kNone;
+  for (int i = lane; i < count; i += 32)
+    top = fmaxf(top, reinterpret_cast<const float2*>(part(i) + rows * D * 4)[row].x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+  float sum = 0.f, acc[kE] = {};
+#pragma unroll 4
+  for (int i = 0; i < count; ++i) {
+    const uint8_t* p = part(i);
+    const float2 ml = reinterpret_cast<const float2*>(p + rows * D * 4)[row];
+    const float weight = ml.y * exp2f(ml.x - top);
+    sum += weight;
+    if constexpr (kE == 4) {
+      const float4 x = reinterpret_cast<const float4*>(p)[row * 32 + lane];
+      acc[0] += weight * x.x; acc[1] += weight * x.y; acc[2] += weight * x.z; acc[3] += weight * x.w;
+    } else {
+      const float2 x = reinterpret_cast<const float2*>(p)[row * 32 + lane];
+      acc[0] += weight * x.x; acc[1] += weight * x.y;
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int e = 0; e < kE; ++e) acc[e] *= inv;
+  if (!whole) {
+    float* o = reinterpret_cast<float*>(into) + row * D + lane * kE;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) o[e] = acc[e];
+    if (lane == 0) reinterpret_cast<float2*>(into + rows * D * 4)[row] = make_float2(top, sum);
+  } else if (out) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int e = 0; e < kE; ++e) out[lane * kE + e] = acc[e];
+    } else {
+      uint32_t u[kE / 2];
+#pragma unroll
+      for (int e = 0; e < kE / 2; ++e) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(acc[2 * e], acc[2 * e + 1]);
+        u[e] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+      if constexpr (kE == 4) {
+        *reinterpret_cast<uint2*>(out + lane * 4) = make_uint2(u[0], u[1]);
+      } else {
+        *reinterpret_cast<uint32_t*>(out + lane * 2) = u[0];
+      }
+    }
+  }
+}
+
+template <int D, int NT, typename T, bool kVec>
+__global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const Work w) {
+  using S = Shape<D, NT>;
+  constexpr bool kSplit = sizeof(T) == 4;   // float32: two fp16 parts
+  constexpr int kParts = kSplit ? 2 : 1;
+  constexpr int kKI = D / 64;               // 16-byte pieces of a K row a lane
+  constexpr int kVW = D / 32;               // words of a V row a lane
+  constexpr int kMT = D / 16;               // tiles of O^T
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  uint8_t* const ring = smem + warp * S::kRing;
+  uint8_t* const first_part = smem + kWarps * S::kRing + warp * S::kPartBytes;
+  Part* const parts = reinterpret_cast<Part*>(smem + kWarps * (S::kRing + S::kPartBytes));
+  if (lane < 2) parts[2 * warp + lane] = Part{0, 0, 0, kPartNone};
+  chain_wait();
+
+  const KvBatchArgs& batch = w.a.batch;
+  const int heads = w.a.cache.heads, bpp = w.a.cache.bpp;
+
+  // the line's length, this warp's blocks of it, and the sequence they begin in
+  long long total = 0;
+  for (int b = lane; b < batch.batch; b += 32) total += sequence_blocks<NT>(w, b);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
+  const long long warps = (long long)w.ctas * kWarps;
+  const long long share = max((total + warps - 1) / warps, (long long)kMinBlocks);
+  const long long begin = ((long long)blockIdx.x * kWarps + warp) * share;
+  const int count = (int)min(max(total - begin, 0ll), share);
+
+  if (count > 0) {
+    Cursor<NT> at;   // of the block that is computed
+    {
+      long long before = 0;
+      int seq = 0;
+      for (int b0 = 0; b0 < batch.batch; b0 += 32) {
+        const long long mine = b0 + lane < batch.batch ? sequence_blocks<NT>(w, b0 + lane) : 0;
+        long long incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long up = __shfl_up_sync(~0u, incl, o);
+          if (lane >= o) incl += up;
+        }
+        const unsigned past = __ballot_sync(~0u, before + incl > begin);
+        if (past) {
+          const int l = __ffs(past) - 1;
+          seq = b0 + l;
+          before += __shfl_sync(~0u, incl - mine, l);
+          break;
+        }
+        before += __shfl_sync(~0u, incl, 31);
+      }
+      at.seek(w, seq, begin - before);
+    }
+    Cursor<NT> ahead = at;   // of the block that is fetched
+    int pages = 0, page0 = 0, page_at = 0, off = 0;   // 32 entries of the table from page0, a lane each
+    auto open_pages = [&](int pg) {
+      page0 = pg;
+      pages = pg + lane < batch.width ? __ldg(batch.table + (size_t)ahead.b * batch.width + pg + lane) : -1;
+    };
+    auto start_item = [&] {
+      page_at = ahead.blk / bpp;
+      off = ahead.blk - page_at * bpp;
+      open_pages(page_at);
+    };
+    start_item();
+    uint32_t tag = 0;        // what is in flight of the last fetched block's scales
+    int tag_stage = -1;
+    const uint32_t ring_addr = smem_u32(ring);
+
+    auto fetch = [&](int stage) {
+      if (page_at - page0 >= 32) open_pages(page_at);
+      const int page = __shfl_sync(~0u, pages, page_at - page0);
+      const bool there = page >= 0 && page < w.a.cache.pages && ahead.blk * kKvBlock < ahead.s.seen;
+      if (tag_stage >= 0) reinterpret_cast<uint32_t*>(ring + tag_stage * S::kStage + S::kChunk)[lane] = tag;
+      tag = 0;
+      if (there) {
+        const size_t block = ((size_t)page * heads + ahead.h) * bpp + off;
+        const int8_t* k = w.a.cache.k + block * (kKvBlock * D);
+        const int8_t* v = w.a.cache.v + block * (kKvBlock * D);
+        const uint32_t dst = ring_addr + stage * S::kStage;
+#pragma unroll
+        for (int i = 0; i < 2 * kKI; ++i)
+          cp_async16(dst + i * 512 + lane * 16, k + (g + 8 * (i & 1)) * D + (i >> 1) * 64 + t * 16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int8_t* src = v + (2 * t + (j & 1) + 8 * (j >> 1)) * D + g * (D / 8);
+          if constexpr (D == 128) {
+            cp_async16(dst + kKvBlock * D + j * 512 + lane * 16, src);
+          } else {
+            cp_async8(dst + kKvBlock * D + j * 256 + lane * 8, src);
+          }
+        }
+        tag = 0x10000u | __ldg(w.a.cache.ke + block) | ((uint32_t)__ldg(w.a.cache.ve + block) << 8);
+      }
+      tag_stage = stage;
+      cp_commit();
+      // on to the next block
+      if (++ahead.blk < ahead.blocks) {
+        if (++off == bpp) {
+          off = 0;
+          ++page_at;
+        }
+      } else {
+        ahead.next_item(w);
+        if (ahead.b < batch.batch) start_item();
+      }
+    };
+
+    int fetched = 0;
+#pragma unroll 1
+    for (; fetched < S::kStages - 1; ++fetched) {
+      if (fetched < count) fetch(fetched);
+      else cp_commit();
+    }
+
+    uint32_t qf[kParts][NT][D / 16][2];
+    float coef[NT][2];          // of columns 2t, 2t + 1
+    int lim[NT][2];
+    float m[NT][2], l[NT][2];
+    float o[kMT][NT][4];
+    int vref = 0, least = 0;
+    bool fresh = true, begins = at.blk == 0;
+    int stage = 0;
+#pragma unroll 1
+    for (int done = 0; done < count; ++done) {
+      if (fresh) {
+        fresh = false;
+        // the item's rows: lane (g, t) holds elements 64 i + 16 t .. of row 8 nt + g
+        least = INT_MAX;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int row = at.r * S::kRows + 8 * nt + g;
+          const bool there = row < at.s.n * w.a.group;
+          float x[kKI][2][8];
+          float top = 0.f;
+          const T* q = static_cast<const T*>(w.a.q) +
+                       (there ? (long long)(at.s.start + row / w.a.group) * w.a.q_row +
+                                    (long long)(at.h * w.a.group + row % w.a.group) * w.a.q_head
+                              : 0);
+#pragma unroll
+          for (int i = 0; i < kKI; ++i)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              if (there) {
+                kv_load8<kVec>(q + 64 * i + 16 * t + 8 * u, x[i][u]);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[i][u][e] = 0.f;
+              }
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                // a NaN counts as an infinity here: fp16 then holds infinities, and the row's scores are not numbers
+                top = fmaxf(top, x[i][u][e] == x[i][u][e] ? fabsf(x[i][u][e]) : __int_as_float(0x7f800000));
+              }
+            }
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+          // the largest magnitude to [2^14, 2^15)
+          const int e = min(max(__float_as_int(top) >> 23, 27), 254);
+          const float up = __int_as_float((127 + 14 + 127 - e) << 23);
+          const bool bad = top > 3.402823466e38f;
+          float cf = bad ? __int_as_float(0x7fc00000) : w.a.scale * 1.4426950408889634f * __int_as_float((e - 14) << 23);
+#pragma unroll
+          for (int i = 0; i < kKI; ++i)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int p2 = 0; p2 < 4; ++p2) {
+                const float a0 = bad ? 0.f : x[i][u][2 * p2] * up, a1 = bad ? 0.f : x[i][u][2 * p2 + 1] * up;
+                const uint32_t hi = half_pair(a0, a1);
+                const int step = i * 4 + 2 * u + (p2 >> 1);
+                qf[0][nt][step][p2 & 1] = hi;
+                if constexpr (kSplit) qf[1][nt][step][p2 & 1] = half_pair(a0 - half_low(hi), a1 - half_high(hi));
+              }
+          const int seen = there ? kv_visible(at.s, row / w.a.group, w.a.causal) : 0;
+          least = min(least, there ? seen : INT_MAX);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            coef[nt][c] = __shfl_sync(~0u, cf, 4 * (2 * t + c));
+            lim[nt][c] = __shfl_sync(~0u, seen, 4 * (2 * t + c));
+            m[nt][c] = kNone;
+            l[nt][c] = 0.f;
+          }
+#pragma unroll
+          for (int i = 0; i < kMT; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[i][nt][c] = 0.f;
+        }
+#pragma unroll
+        for (int d = 16; d >= 4; d >>= 1) least = min(least, __shfl_xor_sync(~0u, least, d));
+        vref = 0;
+      }
+
+      // fetch the block kStages - 1 ahead, then wait for this one
+      if (fetched < count) fetch(fetched % S::kStages);
+      else {
+        if (tag_stage >= 0) {
+          reinterpret_cast<uint32_t*>(ring + tag_stage * S::kStage + S::kChunk)[lane] = tag;
+          tag_stage = -1;
+        }
+        cp_commit();
+      }
+      ++fetched;
+      cp_wait<S::kStages - 1>();
+      const uint32_t src = ring_addr + stage * S::kStage;
+      const uint32_t word = reinterpret_cast<const uint32_t*>(ring + stage * S::kStage + S::kChunk)[lane];
+      if (word) {
+        // S^T
+        float sc[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) sc[nt][c] = 0.f;
+#pragma unroll
+        for (int i = 0; i < kKI; ++i) {
+          const uint4 k0 = ld_shared_v4(src + (2 * i) * 512 + lane * 16);
+          const uint4 k1 = ld_shared_v4(src + (2 * i + 1) * 512 + lane * 16);
+          const uint32_t r0[4] = {k0.x, k0.y, k0.z, k0.w}, r1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t u0 = r0[j] ^ 0x80808080u, u1 = r1[j] ^ 0x80808080u;
+            const uint32_t a0 = bytes_low(u0), a1 = bytes_low(u1), a2 = bytes_high(u0), a3 = bytes_high(u1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int p = 0; p < kParts; ++p)
+                mma16816(sc[nt], a0, a1, a2, a3, qf[p][nt][4 * i + j][0], qf[p][nt][4 * i + j][1]);
+          }
+        }
+        const float kpow = kv_power(word & 255);
+        const int ve = (word >> 8) & 255;
+        bool over = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) sc[nt][c] *= coef[nt][c & 1] * kpow;
+        const int token = at.blk * kKvBlock + g;
+        if (at.blk * kKvBlock + kKvBlock > least) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (token + 8 * (c >> 1) >= lim[nt][c & 1]) sc[nt][c] = -INFINITY;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) over |= sc[nt][c] > m[nt][c & 1] + kSlack;
+        over |= ve > vref;
+        if (__any_sync(~0u, over)) {
+          const float vdown = ve > vref ? exp2f((float)(vref - ve)) : 1.f;
+          vref = max(vref, ve);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float top = fmaxf(sc[nt][c], sc[nt][c + 2]);
+#pragma unroll
+              for (int d = 16; d >= 4; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+              top = fmaxf(top, m[nt][c]);
+              const float down = exp2_approx(m[nt][c] - top);
+              m[nt][c] = top;
+              l[nt][c] *= down;
+#pragma unroll
+              for (int i = 0; i < kMT; ++i) {
+                o[i][nt][c] *= down * vdown;
+                o[i][nt][c + 2] *= down * vdown;
+              }
+            }
+        }
+        const float vpow = __int_as_float(max(127 + kLift + ve - vref, 0) << 23);
+        uint32_t pf[kParts][NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float p0 = exp2_approx(sc[nt][2 * r] - m[nt][0]), p1 = exp2_approx(sc[nt][2 * r + 1] - m[nt][1]);
+            l[nt][0] += p0;
+            l[nt][1] += p1;
+            const float w0 = p0 * vpow, w1 = p1 * vpow;
+            const uint32_t hi = half_pair(w0, w1);
+            pf[0][nt][r] = transpose8(hi);
+            if constexpr (kSplit) pf[1][nt][r] = transpose8(half_pair(w0 - half_low(hi), w1 - half_high(hi)));
+          }
+        // O^T
+        uint32_t vw[4][kVW];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (D == 128) {
+            const uint4 x = ld_shared_v4(src + kKvBlock * D + j * 512 + lane * 16);
+            vw[j][0] = x.x; vw[j][1] = x.y; vw[j][2] = x.z; vw[j][3] = x.w;
+          } else {
+            const uint2 x = ld_shared_v2(src + kKvBlock * D + j * 256 + lane * 8);
+            vw[j][0] = x.x; vw[j][1] = x.y;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kVW; ++j) {
+          // bytes of tokens (2t, 2t + 1) and (2t + 8, 2t + 9), side by side
+          const uint32_t a = vw[0][j] ^ 0x80808080u, b = vw[1][j] ^ 0x80808080u;
+          const uint32_t c = vw[2][j] ^ 0x80808080u, d = vw[3][j] ^ 0x80808080u;
+          const uint32_t ab[2] = {prmt(a, b, 0x5140u), prmt(a, b, 0x7362u)};
+          const uint32_t cd[2] = {prmt(c, d, 0x5140u), prmt(c, d, 0x7362u)};
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t a0 = bytes_low(ab[e]), a1 = bytes_high(ab[e]), a2 = bytes_low(cd[e]), a3 = bytes_high(cd[e]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int p = 0; p < kParts; ++p)
+                mma16816(o[2 * j + e][nt], a0, a1, a2, a3, pf[p][nt][0], pf[p][nt][1]);
+          }
+        }
+      }
+      if (++stage == S::kStages) stage = 0;
+
+      // the end of the item, or of this warp's share of it
+      const bool ends = at.blk + 1 == at.blocks;
+      if (ends || done + 1 == count) {
+        const float vscale = kv_power(vref);
+        uint8_t* into = nullptr;
+        if (!(begins && ends)) {
+          // a part: the one at the share's beginning to its own place, one at its end to the ring's, which
+          // nothing is fetched to any more
+          const int slot = done + 1 == count && begins ? 1 : 0;
+          into = slot ? ring : first_part;
+          if (slot) cp_wait<0>();
+          __syncwarp();
+          if (lane == 0)
+            parts[2 * warp + slot] =
+                Part{at.b, at.r, at.h, kPartHeld | (begins ? kPartBegins : 0) | (ends ? kPartEnds : 0)};
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float sum = l[nt][c];
+#pragma unroll
+            for (int d = 16; d >= 4; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const int col = 8 * nt + 2 * t + c;
+            float y[kMT][2];
+#pragma unroll
+            for (int i = 0; i < kMT; ++i) {
+              y[i][0] = o[i][nt][c] * inv * (1.f / (1 << kLift)) * vscale;
+              y[i][1] = o[i][nt][c + 2] * inv * (1.f / (1 << kLift)) * vscale;
+            }
+            if (into) {
+              float* dst = reinterpret_cast<float*>(into) + col * D + g * (D / 8);
+#pragma unroll
+              for (int i = 0; i < kMT; i += 2)
+                *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(y[i][0], y[i][1], y[i + 1][0], y[i + 1][1]);
+              if (g == 0) reinterpret_cast<float2*>(into + S::kRows * D * 4)[col] = make_float2(m[nt][c], sum);
+            } else {
+              const int row = at.r * S::kRows + col;
+              if (row < at.s.n * w.a.group) {
+                T* dst = static_cast<T*>(w.a.out) + out_row(w.a, at.s, at.h, row) * D + g * (D / 8);
+#pragma unroll
+                for (int i = 0; i < kMT; i += 4) {
+                  const float z[8] = {y[i][0],     y[i][1],     y[i + 1][0], y[i + 1][1],
+                                      y[i + 2][0], y[i + 2][1], y[i + 3][0], y[i + 3][1]};
+                  kv_store8(dst + 2 * i, z);
+                }
+              }
+            }
+          }
+        fresh = begins = true;
+      }
+      if (ends) at.next_item(w);
+      else ++at.blk;
+    }
+    cp_wait<0>();
+  }
+
+  // the parts of the CTA's warps, joined: every warp takes some of the rows
+  __syncthreads();
+  auto part_bytes = [&](int i) -> const uint8_t* {
+    return i & 1 ? smem + (i >> 1) * S::kRing : smem + kWarps * S::kRing + (i >> 1) * S::kPartBytes;
+  };
+  Part left[2] = {{0, 0, 0, kPartNone}, {0, 0, 0, kPartNone}};   // what goes to the workspace
+  int list[2 * kWarps], n = 0;
+#pragma unroll 1
+  for (int i = 0; i <= 2 * kWarps; ++i) {
+    const Part p = i < 2 * kWarps ? parts[i] : Part{0, 0, 0, kPartNone};
+    if (i < 2 * kWarps && !(p.flags & kPartHeld)) continue;
+    // the run before this one ends where a part begins an item
+    if (n > 0 && (i == 2 * kWarps || (p.flags & kPartBegins))) {
+      const Part a = parts[list[0]], z = parts[list[n - 1]];
+      const bool whole = (a.flags & kPartBegins) && (z.flags & kPartEnds);
+      const int slot = (a.flags & kPartBegins) ? 1 : 0;
+      uint8_t* into = w.ws + (size_t)(2 * blockIdx.x + slot) * S::kWsPart;
+      if (!whole) left[slot] = Part{a.b, a.r, a.h, kPartHeld | (a.flags & kPartBegins) | (z.flags & kPartEnds)};
+      KvSeq s{};
+      if (whole) s = kv_sequence(batch, a.b);
+      for (int row = warp; row < S::kRows; row += kWarps) {
+        T* out = nullptr;
+        if (whole && a.r * S::kRows + row < s.n * w.a.group)
+          out = static_cast<T*>(w.a.out) + out_row(w.a, s, a.h, a.r * S::kRows + row) * D;
+        join_row<D, T>(n, S::kRows, row, [&](int j) { return part_bytes(list[j]); }, whole, out, into);
+      }
+      n = 0;
+    }
+    if (i < 2 * kWarps) list[n++] = i;
+  }
+  if (threadIdx.x < 2) w.parts[2 * blockIdx.x + threadIdx.x] = left[threadIdx.x];
+  chain_release();
+}
+
+// What several CTAs hold of an item, joined by the CTA with the number of the one that
+// holds its beginning.
+template <int D, int NT, typename T>
+__global__ void __launch_bounds__(kThreads) kv_attention_join_kernel(const Work w) {
+  using S = Shape<D, NT>;
+  chain_wait();
+  const Part a = w.parts[2 * blockIdx.x + 1];
+  if (!(a.flags & kPartHeld)) {
+    chain_release();
+    return;
+  }
+  // the following CTAs' first parts belong to the item, up to the one that ends it
+  const int lane = threadIdx.x & 31;
+  int n = 1;
+  for (int c0 = blockIdx.x + 1; c0 < w.ctas; c0 += 32) {
+    const int c = c0 + lane;
+    const unsigned ends = __ballot_sync(~0u, c < w.ctas && (w.parts[2 * c].flags & kPartEnds));
+    if (ends) {
+      n += __ffs(ends);
+      break;
+    }
+    n += 32;
+  }
+  n = min(n, w.ctas - (int)blockIdx.x);
+  const KvSeq s = kv_sequence(w.a.batch, a.b);
+  chain_release();
+  auto part = [&](int j) -> const uint8_t* {
+    return w.ws + (size_t)(j == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + j)) * S::kWsPart;
+  };
+  for (int row = threadIdx.x >> 5; row < S::kRows; row += kWarps) {
+    if (a.r * S::kRows + row >= s.n * w.a.group) break;
+    T* out = static_cast<T*>(w.a.out) + out_row(w.a, s, a.h, a.r * S::kRows + row) * D;
+    join_row<D, T>(n, S::kRows, row, part, true, out, nullptr);
+  }
+}
+
+// Two tiles of eight rows where one tile would not hold a sequence's rows.
+int row_tiles(int group, int max_tokens) { return (long long)group * max_tokens <= 8 ? 1 : 2; }
+
+// CTAs: one an SM, but no more than the work can fill.
+int rows_ctas(int sms, long long bound) {
+  return (int)std::max(1ll, std::min((long long)sms, (bound + kWarps * kMinBlocks - 1) / (kWarps * kMinBlocks)));
+}
+
+template <int D, int NT, typename T>
+cudaError_t rows_typed(const KvAttentionArgs& a, bool vec, cudaStream_t s) {
+  using S = Shape<D, NT>;
+  const int sms = num_sms();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  const long long tiles = ((long long)a.batch.rows * a.group + S::kRows - 1) / S::kRows + a.batch.batch;
+  const long long blocks = std::max(1, (a.batch.capacity + kKvBlock - 1) / kKvBlock);
+  Work w{};
+  w.a = a;
+  w.ctas = rows_ctas(sms, std::min(tiles * a.cache.heads, 1ll << 30) * blocks);
+  w.parts = static_cast<Part*>(a.workspace);
+  w.ws = static_cast<uint8_t*>(a.workspace) + (size_t)sms * 2 * sizeof(Part);
+  auto kern = vec ? &kv_attention_rows_kernel<D, NT, T, true> : &kv_attention_rows_kernel<D, NT, T, false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_chained(kern, dim3(w.ctas), dim3(kThreads), S::kSmem, 1, s, w);
+  if (e != cudaSuccess) return e;
+  return launch_chained(&kv_attention_join_kernel<D, NT, T>, dim3(w.ctas), dim3(kThreads), 0, 1, s, w);
+}
+
+template <int D>
+cudaError_t rows_sized(const KvAttentionArgs& a, bool bf16, bool vec, cudaStream_t s) {
+  if (row_tiles(a.group, a.max_tokens) == 1)
+    return bf16 ? rows_typed<D, 1, __nv_bfloat16>(a, vec, s) : rows_typed<D, 1, float>(a, vec, s);
+  return bf16 ? rows_typed<D, 2, __nv_bfloat16>(a, vec, s) : rows_typed<D, 2, float>(a, vec, s);
+}
+
+}  // namespace
+
+size_t kv_attention_workspace(int rows, int batch, int heads, int group, int head_dim, int max_tokens, bool bf16) {
+  const int sms = num_sms();
+  if (sms <= 0) return 0;
+  const size_t part = head_dim == 64 ? (row_tiles(group, max_tokens) == 1 ? Shape<64, 1>::kWsPart : Shape<64, 2>::kWsPart)
+                                     : (row_tiles(group, max_tokens) == 1 ? Shape<128, 1>::kWsPart
+                                                                          : Shape<128, 2>::kWsPart);
+  return (size_t)sms * 2 * (sizeof(Part) + part);
+}
+
+cudaError_t launch_kv_attention(const KvAttentionArgs& a, int head_dim, bool bf16, bool vec, cudaStream_t s,
+                                const char** kernel_name) {
+  *kernel_name = "kv_attention_rows+join";
+  return head_dim == 64 ? rows_sized<64>(a, bf16, vec, s) : rows_sized<128>(a, bf16, vec, s);
+}
+
+}  // namespace qmm

@@ -1828,4 +1828,160 @@ qmm_status qmm_fp4_matmul(const void* a_packed, size_t a_bytes, int64_t M, const
   return finish_launch(launch_gemm_fp4(a, block, s, &name), name);
 }
 
+// ---------------------------------------------------------------------------
+// 8-bit key-value cache
+// ---------------------------------------------------------------------------
+namespace {
+
+// The cache and the sequences of a call, checked; `empty`: nothing to do.
+qmm_status kv_arguments(const qmm_kv_cache* c, const qmm_kv_batch* b, KvCacheArgs* ca, KvBatchArgs* ba, bool* empty) {
+  if (!c || !b) return QMM_ERR_INVALID_ARG;
+  if (!dim_ok(c->pages) || !dim_ok(c->kv_heads) || !dim_ok(c->page) || !dim_ok(c->head_dim) || c->kv_heads < 1)
+    return QMM_ERR_INVALID_ARG;
+  if (!dim_ok(b->batch) || !dim_ok(b->width) || !dim_ok(b->rows)) return QMM_ERR_INVALID_ARG;
+  if ((c->head_dim != 64 && c->head_dim != 128) || c->page < 16 || c->page % 16) return QMM_ERR_UNSUPPORTED;
+  if (b->width > INT_MAX / c->page || b->rows > INT_MAX / c->kv_heads) return QMM_ERR_INVALID_ARG;
+  if (!b->starts && b->rows != b->batch) return QMM_ERR_INVALID_ARG;
+  *empty = b->rows == 0 || b->batch == 0;
+  if (*empty) return QMM_OK;
+  if (c->pages > 0 && (!c->k || !c->v || !c->k_exp || !c->v_exp || !aligned16(c->k) || !aligned16(c->v)))
+    return QMM_ERR_INVALID_ARG;
+  if (!b->lengths || (b->width > 0 && !b->table)) return QMM_ERR_INVALID_ARG;
+  ca->k = c->k;
+  ca->v = c->v;
+  ca->ke = c->k_exp;
+  ca->ve = c->v_exp;
+  ca->pages = (int)c->pages;
+  ca->heads = (int)c->kv_heads;
+  ca->bpp = (int)(c->page / 16);
+  ba->table = b->table;
+  ba->lengths = b->lengths;
+  ba->starts = b->starts;
+  ba->width = (int)b->width;
+  ba->batch = (int)b->batch;
+  ba->rows = (int)b->rows;
+  ba->capacity = (int)(b->width * c->page);
+  return QMM_OK;
+}
+
+// Rows and heads of a strided operand on 16 bytes.
+bool kv_vector(const void* p, int64_t row, int64_t head, int dtype) {
+  const int64_t n = dtype == QMM_BF16 ? 8 : 4;
+  return aligned16(p) && row % n == 0 && head % n == 0;
+}
+
+}  // namespace
+
+qmm_status qmm_kv_append(const qmm_kv_cache* cache, const qmm_kv_batch* batch, int dtype, const void* k,
+                         int64_t k_row, int64_t k_head, const void* v, int64_t v_row, int64_t v_head, const void* q,
+                         int64_t q_row, int64_t q_head, int64_t q_heads, void* q_out, const float* cos,
+                         const float* sin, int64_t positions, int64_t rotated, int interleaved, void* stream) {
+  KvAppendArgs a{};
+  bool empty = false;
+  if (!float_type(dtype)) return QMM_ERR_INVALID_ARG;
+  const qmm_status st = kv_arguments(cache, batch, &a.cache, &a.batch, &empty);
+  if (st != QMM_OK) return st;
+  if (!dim_ok(rotated) || !dim_ok(positions) || (interleaved != 0 && interleaved != 1)) return QMM_ERR_INVALID_ARG;
+  if (rotated > cache->head_dim || rotated % 16) return QMM_ERR_UNSUPPORTED;
+  if (k_row < 0 || k_head < 0 || v_row < 0 || v_head < 0) return QMM_ERR_INVALID_ARG;
+  if (q && (q_row < 0 || q_head < 0 || q_heads < 1 || q_heads > INT_MAX / std::max<int64_t>(batch->rows, 1)))
+    return QMM_ERR_INVALID_ARG;
+  if (empty) {
+    t_last_kernel = "none";
+    return QMM_OK;
+  }
+  if (!k || !v || (q && (!q_out || !aligned16(q_out)))) return QMM_ERR_INVALID_ARG;
+  if (rotated && positions > 0 && (!cos || !sin || !aligned16(cos) || !aligned16(sin))) return QMM_ERR_INVALID_ARG;
+  if (q && q == q_out && (q_row != q_heads * cache->head_dim || q_head != cache->head_dim)) return QMM_ERR_INVALID_ARG;
+  a.k = k;
+  a.v = v;
+  a.q = q;
+  a.k_row = k_row;
+  a.k_head = k_head;
+  a.v_row = v_row;
+  a.v_head = v_head;
+  a.q_row = q_row;
+  a.q_head = q_head;
+  a.q_out = q_out;
+  a.cos = cos;
+  a.sin = sin;
+  a.positions = (int)positions;
+  a.half = (int)rotated / 2;
+  a.interleaved = interleaved;
+  a.q_heads = q ? (int)q_heads : 0;
+  const bool vec = kv_vector(k, k_row, k_head, dtype) && kv_vector(v, v_row, v_head, dtype) &&
+                   (!q || kv_vector(q, q_row, q_head, dtype));
+  cudaGetLastError();
+  const char* name = "none";
+  return finish_launch(launch_kv_append(a, (int)cache->head_dim, dtype == QMM_BF16, vec,
+                                        static_cast<cudaStream_t>(stream), &name), name);
+}
+
+qmm_status qmm_kv_read(const qmm_kv_cache* cache, const qmm_kv_batch* batch, void* k, void* v, int dtype,
+                       void* stream) {
+  KvReadArgs a{};
+  bool empty = false;
+  if (!float_type(dtype)) return QMM_ERR_INVALID_ARG;
+  const qmm_status st = kv_arguments(cache, batch, &a.cache, &a.batch, &empty);
+  if (st != QMM_OK) return st;
+  if (empty || (!k && !v)) {
+    t_last_kernel = "none";
+    return QMM_OK;
+  }
+  if ((k && !aligned16(k)) || (v && !aligned16(v))) return QMM_ERR_INVALID_ARG;
+  a.k = k;
+  a.v = v;
+  cudaGetLastError();
+  const char* name = "none";
+  return finish_launch(launch_kv_read(a, (int)cache->head_dim, dtype == QMM_BF16, static_cast<cudaStream_t>(stream),
+                                      &name), name);
+}
+
+size_t qmm_kv_attention_workspace_bytes(int64_t rows, int64_t batch, int64_t q_heads, int64_t kv_heads,
+                                        int64_t head_dim, int dtype, int64_t max_tokens) {
+  if (!float_type(dtype) || !dim_ok(rows) || !dim_ok(batch) || !dim_ok(q_heads) || !dim_ok(kv_heads)) return 0;
+  if (kv_heads < 1 || q_heads < 1 || q_heads % kv_heads || (head_dim != 64 && head_dim != 128)) return 0;
+  if (rows == 0 || batch == 0 || max_tokens < 1) return 0;
+  return kv_attention_workspace((int)rows, (int)batch, (int)kv_heads, (int)(q_heads / kv_heads), (int)head_dim,
+                                (int)std::min(max_tokens, rows), dtype == QMM_BF16);
+}
+
+qmm_status qmm_kv_attention(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const void* q, int dtype,
+                            int64_t q_row, int64_t q_head, int64_t q_heads, float scale, int causal,
+                            int64_t max_tokens, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  KvAttentionArgs a{};
+  bool empty = false;
+  if (!float_type(dtype)) return QMM_ERR_INVALID_ARG;
+  const qmm_status st = kv_arguments(cache, batch, &a.cache, &a.batch, &empty);
+  if (st != QMM_OK) return st;
+  if ((causal != 0 && causal != 1) || q_row < 0 || q_head < 0 || max_tokens < 1) return QMM_ERR_INVALID_ARG;
+  if (q_heads < 1 || q_heads % cache->kv_heads || !(scale - scale == 0.f)) return QMM_ERR_INVALID_ARG;
+  if (q_heads > INT_MAX / std::max<int64_t>(batch->rows, 1)) return QMM_ERR_INVALID_ARG;
+  if (empty) {
+    t_last_kernel = "none";
+    return QMM_OK;
+  }
+  if (!q || !out || !aligned16(out)) return QMM_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) ||
+      workspace_bytes < qmm_kv_attention_workspace_bytes(batch->rows, batch->batch, q_heads, cache->kv_heads,
+                                                         cache->head_dim, dtype, max_tokens))
+    return QMM_ERR_INVALID_ARG;
+  a.err = err_word();
+  if (!a.err) return QMM_ERR_CUDA;
+  a.q = q;
+  a.q_row = q_row;
+  a.q_head = q_head;
+  a.out = out;
+  a.group = (int)(q_heads / cache->kv_heads);
+  a.causal = causal;
+  a.scale = scale;
+  a.max_tokens = (int)std::min(max_tokens, batch->rows);
+  a.workspace = workspace;
+  cudaGetLastError();
+  const char* name = "none";
+  return finish_launch(launch_kv_attention(a, (int)cache->head_dim, dtype == QMM_BF16,
+                                           kv_vector(q, q_row, q_head, dtype), static_cast<cudaStream_t>(stream),
+                                           &name), name);
+}
+
 }  // extern "C"
