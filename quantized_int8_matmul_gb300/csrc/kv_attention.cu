@@ -25,9 +25,7 @@
 // The running maximum moves only when some score is 8 (a factor of 256) above it,
 // which a vote finds out: P keeps six more bits below fp16's largest value and 30 bits
 // to its smallest. V's power of two goes into P the same way.
-#include "chain.cuh"
-#include "common.cuh"
-#include "kv.cuh"
+#include "kv_attention.cuh"
 
 namespace qmm {
 
@@ -35,16 +33,8 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr float kNone = -1e30f;      // a running maximum that has seen nothing
-constexpr float kSlack = 8.f;        // how far a score may pass the running maximum
 constexpr int kLift = 6;             // P is held times 2^kLift
 constexpr int kMinBlocks = 4;        // blocks a warp, at least
-
-// A part of an item that one warp (in shared memory) or one CTA (in the workspace) holds.
-enum { kPartNone = 0, kPartHeld = 1, kPartBegins = 2, kPartEnds = 4 };
-struct Part {
-  int b, r, h, flags;
-};
 
 template <int D, int NT>
 struct Shape {
@@ -53,11 +43,10 @@ struct Shape {
   static constexpr int kChunk = 2 * kKvBlock * D;                 // K and V of one block
   static constexpr int kStage = kChunk + 128;                     // and a word a lane
   static constexpr int kRing = kStages * kStage;                  // a warp's
-  static constexpr int kPartBytes = kRows * D * 4 + kRows * 8;    // rows of O, then (m, l) each
+  static constexpr int kPartBytes = (int)kv_part_bytes(D, kRows);   // rows of O, then (m, l) each
   static_assert(kRing >= kPartBytes, "a warp's last part takes the place of its ring");
-  static constexpr int kSmem = kWarps * (kRing + kPartBytes) + 2 * kWarps * (int)sizeof(Part);
+  static constexpr int kSmem = kWarps * (kRing + kPartBytes) + 2 * kWarps * (int)sizeof(KvPart);
   static_assert(kSmem <= 227 * 1024, "one CTA an SM");
-  static constexpr int kWsPart = kPartBytes;                      // in the workspace
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -82,163 +71,12 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
-__device__ __forceinline__ float exp2_approx(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ uint32_t half_pair(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 __device__ __forceinline__ float half_low(uint32_t u) { return __half2float(__ushort_as_half((unsigned short)u)); }
 __device__ __forceinline__ float half_high(uint32_t u) {
   return __half2float(__ushort_as_half((unsigned short)(u >> 16)));
 }
-__device__ __forceinline__ uint32_t bytes_low(uint32_t u) {   // bytes 0, 1 (biased by 128) to two fp16
-  const uint32_t l = prmt(u, 0x64646464u, 0x4140u);
-  __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&l), __half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480)));
-  return *reinterpret_cast<uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t bytes_high(uint32_t u) {  // bytes 2, 3
-  const uint32_t l = prmt(u, 0x64646464u, 0x4342u);
-  __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&l), __half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480)));
-  return *reinterpret_cast<uint32_t*>(&h);
-}
-
-struct Work {
-  KvAttentionArgs a;
-  int rows_limit;        // sequences with more rows a key head than this are not this kernel's (0: no limit)
-  Part* parts;           // [ctas][2]
-  uint8_t* ws;           // [ctas][2] parts
-  int ctas;
-};
-
-// The blocks of one row tile: at least one, so that rows that see nothing are written.
-template <int NT>
-__device__ __forceinline__ int tile_blocks(const Work& w, const KvSeq& s, int r) {
-  const int last = min(((r + 1) * 8 * NT - 1) / w.a.group, s.n - 1);
-  return max((kv_visible(s, last, w.a.causal) + kKvBlock - 1) / kKvBlock, 1);
-}
-template <int NT>
-__device__ __forceinline__ int tile_count(const Work& w, const KvSeq& s) {
-  const long long rows = (long long)s.n * w.a.group;
-  if (w.rows_limit && rows > w.rows_limit) return 0;
-  return (int)((rows + 8 * NT - 1) / (8 * NT));
-}
-template <int NT>
-__device__ __forceinline__ long long sequence_blocks(const Work& w, int b) {
-  const KvSeq s = kv_sequence(w.a.batch, b);
-  const int tiles = tile_count<NT>(w, s);
-  long long sum = 0;
-  for (int r = 0; r < tiles; ++r) sum += tile_blocks<NT>(w, s, r);
-  return sum * w.a.cache.heads;
-}
-
-// A place in the line of blocks.
-template <int NT>
-struct Cursor {
-  int b, r, h, blk, blocks, tiles;
-  KvSeq s;
-
-  __device__ void open(const Work& w) { blocks = tile_blocks<NT>(w, s, r); }
-  // To block `at` of sequence b.
-  __device__ void seek(const Work& w, int seq, long long at) {
-    b = seq;
-    s = kv_sequence(w.a.batch, b);
-    tiles = tile_count<NT>(w, s);
-    for (r = 0;; ++r) {
-      open(w);
-      const long long tile = (long long)blocks * w.a.cache.heads;
-      if (at < tile || r + 1 >= tiles) break;
-      at -= tile;
-    }
-    h = (int)(at / blocks);
-    blk = (int)(at % blocks);
-  }
-  // To the next item's first block.
-  __device__ void next_item(const Work& w) {
-    blk = 0;
-    if (++h < w.a.cache.heads) return;
-    h = 0;
-    if (++r < tiles) {
-      open(w);
-      return;
-    }
-    r = 0;
-    do {
-      if (++b >= w.a.batch.batch) return;
-      s = kv_sequence(w.a.batch, b);
-      tiles = tile_count<NT>(w, s);
-    } while (tiles == 0);
-    open(w);
-  }
-};
-
-// Where rows of an item go: rows are (token, query head of the group), token major.
-__device__ __forceinline__ long long out_row(const KvAttentionArgs& a, const KvSeq& s, int h, int row) {
-  return (long long)(s.start + row / a.group) * ((long long)a.cache.heads * a.group) + (long long)h * a.group +
-         row % a.group;
-}
-
-// Parts [first, first + count) of one item joined, one row by one warp: rows of O that
-// are already divided by their own sums l, with their maxima m. part(i) gives the
-// i-th part's bytes. The joined row is written to `out` (T, row index given) where it
-// is the whole item's, else as a part again.
-template <int D, typename T, typename F>
-__device__ __forceinline__ void join_row(int count, int rows, int row, F part, bool whole, T* out, uint8_t* into) {
-  constexpr int kE = D / 32;
-  const int lane = threadIdx.x & 31;
-  float top = kNone;
-  for (int i = lane; i < count; i += 32)
-    top = fmaxf(top, reinterpret_cast<const float2*>(part(i) + rows * D * 4)[row].x);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-  float sum = 0.f, acc[kE] = {};
-#pragma unroll 4
-  for (int i = 0; i < count; ++i) {
-    const uint8_t* p = part(i);
-    const float2 ml = reinterpret_cast<const float2*>(p + rows * D * 4)[row];
-    const float weight = ml.y * exp2f(ml.x - top);
-    sum += weight;
-    if constexpr (kE == 4) {
-      const float4 x = reinterpret_cast<const float4*>(p)[row * 32 + lane];
-      acc[0] += weight * x.x; acc[1] += weight * x.y; acc[2] += weight * x.z; acc[3] += weight * x.w;
-    } else {
-      const float2 x = reinterpret_cast<const float2*>(p)[row * 32 + lane];
-      acc[0] += weight * x.x; acc[1] += weight * x.y;
-    }
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-  for (int e = 0; e < kE; ++e) acc[e] *= inv;
-  if (!whole) {
-    float* o = reinterpret_cast<float*>(into) + row * D + lane * kE;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) o[e] = acc[e];
-    if (lane == 0) reinterpret_cast<float2*>(into + rows * D * 4)[row] = make_float2(top, sum);
-  } else if (out) {
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-      for (int e = 0; e < kE; ++e) out[lane * kE + e] = acc[e];
-    } else {
-      uint32_t u[kE / 2];
-#pragma unroll
-      for (int e = 0; e < kE / 2; ++e) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(acc[2 * e], acc[2 * e + 1]);
-        u[e] = *reinterpret_cast<const uint32_t*>(&v);
-      }
-      if constexpr (kE == 4) {
-        *reinterpret_cast<uint2*>(out + lane * 4) = make_uint2(u[0], u[1]);
-      } else {
-        *reinterpret_cast<uint32_t*>(out + lane * 2) = u[0];
-      }
-    }
-  }
-}
-
 template <int D, int NT, typename T, bool kVec>
-__global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const Work w) {
+__global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const KvWork w) {
   using S = Shape<D, NT>;
   constexpr bool kSplit = sizeof(T) == 4;   // float32: two fp16 parts
   constexpr int kParts = kSplit ? 2 : 1;
@@ -250,56 +88,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const Wo
   const int g = lane >> 2, t = lane & 3;
   uint8_t* const ring = smem + warp * S::kRing;
   uint8_t* const first_part = smem + kWarps * S::kRing + warp * S::kPartBytes;
-  Part* const parts = reinterpret_cast<Part*>(smem + kWarps * (S::kRing + S::kPartBytes));
-  if (lane < 2) parts[2 * warp + lane] = Part{0, 0, 0, kPartNone};
+  KvPart* const parts = reinterpret_cast<KvPart*>(smem + kWarps * (S::kRing + S::kPartBytes));
+  if (lane < 2) parts[2 * warp + lane] = KvPart{0, 0, 0, kPartNone};
   chain_wait();
 
   const KvBatchArgs& batch = w.a.batch;
   const int heads = w.a.cache.heads, bpp = w.a.cache.bpp;
 
-  // the line's length, this warp's blocks of it, and the sequence they begin in
-  long long total = 0;
-  for (int b = lane; b < batch.batch; b += 32) total += sequence_blocks<NT>(w, b);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
+  // the line's length and this warp's blocks of it
+  const long long total = kv_total_units<S::kRows, kKvBlock>(w);
   const long long warps = (long long)w.ctas * kWarps;
   const long long share = max((total + warps - 1) / warps, (long long)kMinBlocks);
   const long long begin = ((long long)blockIdx.x * kWarps + warp) * share;
   const int count = (int)min(max(total - begin, 0ll), share);
 
   if (count > 0) {
-    Cursor<NT> at;   // of the block that is computed
-    {
-      long long before = 0;
-      int seq = 0;
-      for (int b0 = 0; b0 < batch.batch; b0 += 32) {
-        const long long mine = b0 + lane < batch.batch ? sequence_blocks<NT>(w, b0 + lane) : 0;
-        long long incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long up = __shfl_up_sync(~0u, incl, o);
-          if (lane >= o) incl += up;
-        }
-        const unsigned past = __ballot_sync(~0u, before + incl > begin);
-        if (past) {
-          const int l = __ffs(past) - 1;
-          seq = b0 + l;
-          before += __shfl_sync(~0u, incl - mine, l);
-          break;
-        }
-        before += __shfl_sync(~0u, incl, 31);
-      }
-      at.seek(w, seq, begin - before);
-    }
-    Cursor<NT> ahead = at;   // of the block that is fetched
+    KvCursor<S::kRows, kKvBlock> at;   // of the block that is computed
+    at.seek(w, begin);
+    KvCursor<S::kRows, kKvBlock> ahead = at;   // of the block that is fetched
     int pages = 0, page0 = 0, page_at = 0, off = 0;   // 32 entries of the table from page0, a lane each
     auto open_pages = [&](int pg) {
       page0 = pg;
       pages = pg + lane < batch.width ? __ldg(batch.table + (size_t)ahead.b * batch.width + pg + lane) : -1;
     };
     auto start_item = [&] {
-      page_at = ahead.blk / bpp;
-      off = ahead.blk - page_at * bpp;
+      page_at = ahead.at / bpp;
+      off = ahead.at - page_at * bpp;
       open_pages(page_at);
     };
     start_item();
@@ -310,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const Wo
     auto fetch = [&](int stage) {
       if (page_at - page0 >= 32) open_pages(page_at);
       const int page = __shfl_sync(~0u, pages, page_at - page0);
-      const bool there = page >= 0 && page < w.a.cache.pages && ahead.blk * kKvBlock < ahead.s.seen;
+      const bool there = page >= 0 && page < w.a.cache.pages && ahead.at * kKvBlock < ahead.s.seen;
       if (tag_stage >= 0) reinterpret_cast<uint32_t*>(ring + tag_stage * S::kStage + S::kChunk)[lane] = tag;
       tag = 0;
       if (there) {
@@ -335,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const Wo
       tag_stage = stage;
       cp_commit();
       // on to the next block
-      if (++ahead.blk < ahead.blocks) {
+      if (++ahead.at < ahead.units) {
         if (++off == bpp) {
           off = 0;
           ++page_at;
@@ -359,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const Wo
     float m[NT][2], l[NT][2];
     float o[kMT][NT][4];
     int vref = 0, least = 0;
-    bool fresh = true, begins = at.blk == 0;
+    bool fresh = true, begins = at.at == 0;
     int stage = 0;
 #pragma unroll 1
     for (int done = 0; done < count; ++done) {
@@ -418,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const Wo
           for (int c = 0; c < 2; ++c) {
             coef[nt][c] = __shfl_sync(~0u, cf, 4 * (2 * t + c));
             lim[nt][c] = __shfl_sync(~0u, seen, 4 * (2 * t + c));
-            m[nt][c] = kNone;
+            m[nt][c] = kKvNone;
             l[nt][c] = 0.f;
           }
 #pragma unroll
@@ -474,8 +288,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const Wo
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 4; ++c) sc[nt][c] *= coef[nt][c & 1] * kpow;
-        const int token = at.blk * kKvBlock + g;
-        if (at.blk * kKvBlock + kKvBlock > least) {
+        const int token = at.at * kKvBlock + g;
+        if (at.at * kKvBlock + kKvBlock > least) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -485,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const Wo
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) over |= sc[nt][c] > m[nt][c & 1] + kSlack;
+          for (int c = 0; c < 4; ++c) over |= sc[nt][c] > m[nt][c & 1] + kKvSlack;
         over |= ve > vref;
         if (__any_sync(~0u, over)) {
           const float vdown = ve > vref ? exp2f((float)(vref - ve)) : 1.f;
@@ -555,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const Wo
       if (++stage == S::kStages) stage = 0;
 
       // the end of the item, or of this warp's share of it
-      const bool ends = at.blk + 1 == at.blocks;
+      const bool ends = at.at + 1 == at.units;
       if (ends || done + 1 == count) {
         const float vscale = kv_power(vref);
         uint8_t* into = nullptr;
@@ -568,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const Wo
           __syncwarp();
           if (lane == 0)
             parts[2 * warp + slot] =
-                Part{at.b, at.r, at.h, kPartHeld | (begins ? kPartBegins : 0) | (ends ? kPartEnds : 0)};
+                KvPart{at.b, at.r, at.h, kPartHeld | (begins ? kPartBegins : 0) | (ends ? kPartEnds : 0)};
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -594,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const Wo
             } else {
               const int row = at.r * S::kRows + col;
               if (row < at.s.n * w.a.group) {
-                T* dst = static_cast<T*>(w.a.out) + out_row(w.a, at.s, at.h, row) * D + g * (D / 8);
+                T* dst = static_cast<T*>(w.a.out) + kv_out_row(w.a, at.s, at.h, row) * D + g * (D / 8);
 #pragma unroll
                 for (int i = 0; i < kMT; i += 4) {
                   const float z[8] = {y[i][0],     y[i][1],     y[i + 1][0], y[i + 1][1],
@@ -607,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const Wo
         fresh = begins = true;
       }
       if (ends) at.next_item(w);
-      else ++at.blk;
+      else ++at.at;
     }
     cp_wait<0>();
   }
@@ -617,26 +431,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const Wo
   auto part_bytes = [&](int i) -> const uint8_t* {
     return i & 1 ? smem + (i >> 1) * S::kRing : smem + kWarps * S::kRing + (i >> 1) * S::kPartBytes;
   };
-  Part left[2] = {{0, 0, 0, kPartNone}, {0, 0, 0, kPartNone}};   // what goes to the workspace
+  KvPart left[2] = {{0, 0, 0, kPartNone}, {0, 0, 0, kPartNone}};   // what goes to the workspace
   int list[2 * kWarps], n = 0;
 #pragma unroll 1
   for (int i = 0; i <= 2 * kWarps; ++i) {
-    const Part p = i < 2 * kWarps ? parts[i] : Part{0, 0, 0, kPartNone};
+    const KvPart p = i < 2 * kWarps ? parts[i] : KvPart{0, 0, 0, kPartNone};
     if (i < 2 * kWarps && !(p.flags & kPartHeld)) continue;
     // the run before this one ends where a part begins an item
     if (n > 0 && (i == 2 * kWarps || (p.flags & kPartBegins))) {
-      const Part a = parts[list[0]], z = parts[list[n - 1]];
+      const KvPart a = parts[list[0]], z = parts[list[n - 1]];
       const bool whole = (a.flags & kPartBegins) && (z.flags & kPartEnds);
       const int slot = (a.flags & kPartBegins) ? 1 : 0;
-      uint8_t* into = w.ws + (size_t)(2 * blockIdx.x + slot) * S::kWsPart;
-      if (!whole) left[slot] = Part{a.b, a.r, a.h, kPartHeld | (a.flags & kPartBegins) | (z.flags & kPartEnds)};
+      uint8_t* into = w.ws + (size_t)(2 * blockIdx.x + slot) * kv_part_bytes(D, S::kRows);
+      if (!whole) left[slot] = KvPart{a.b, a.r, a.h, kPartHeld | (a.flags & kPartBegins) | (z.flags & kPartEnds)};
       KvSeq s{};
       if (whole) s = kv_sequence(batch, a.b);
       for (int row = warp; row < S::kRows; row += kWarps) {
         T* out = nullptr;
         if (whole && a.r * S::kRows + row < s.n * w.a.group)
-          out = static_cast<T*>(w.a.out) + out_row(w.a, s, a.h, a.r * S::kRows + row) * D;
-        join_row<D, T>(n, S::kRows, row, [&](int j) { return part_bytes(list[j]); }, whole, out, into);
+          out = static_cast<T*>(w.a.out) + kv_out_row(w.a, s, a.h, a.r * S::kRows + row) * D;
+        kv_join_row<D, T>(n, S::kRows, row, [&](int j) { return part_bytes(list[j]); }, whole, out, into);
       }
       n = 0;
     }
@@ -646,92 +460,82 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const Wo
   chain_release();
 }
 
-// What several CTAs hold of an item, joined by the CTA with the number of the one that
-// holds its beginning.
-template <int D, int NT, typename T>
-__global__ void __launch_bounds__(kThreads) kv_attention_join_kernel(const Work w) {
-  using S = Shape<D, NT>;
-  chain_wait();
-  const Part a = w.parts[2 * blockIdx.x + 1];
-  if (!(a.flags & kPartHeld)) {
-    chain_release();
-    return;
-  }
-  // the following CTAs' first parts belong to the item, up to the one that ends it
-  const int lane = threadIdx.x & 31;
-  int n = 1;
-  for (int c0 = blockIdx.x + 1; c0 < w.ctas; c0 += 32) {
-    const int c = c0 + lane;
-    const unsigned ends = __ballot_sync(~0u, c < w.ctas && (w.parts[2 * c].flags & kPartEnds));
-    if (ends) {
-      n += __ffs(ends);
-      break;
-    }
-    n += 32;
-  }
-  n = min(n, w.ctas - (int)blockIdx.x);
-  const KvSeq s = kv_sequence(w.a.batch, a.b);
-  chain_release();
-  auto part = [&](int j) -> const uint8_t* {
-    return w.ws + (size_t)(j == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + j)) * S::kWsPart;
-  };
-  for (int row = threadIdx.x >> 5; row < S::kRows; row += kWarps) {
-    if (a.r * S::kRows + row >= s.n * w.a.group) break;
-    T* out = static_cast<T*>(w.a.out) + out_row(w.a, s, a.h, a.r * S::kRows + row) * D;
-    join_row<D, T>(n, S::kRows, row, part, true, out, nullptr);
-  }
-}
-
 // Two tiles of eight rows where one tile would not hold a sequence's rows.
 int row_tiles(int group, int max_tokens) { return (long long)group * max_tokens <= 8 ? 1 : 2; }
 
-// CTAs: one an SM, but no more than the work can fill.
-int rows_ctas(int sms, long long bound) {
-  return (int)std::max(1ll, std::min((long long)sms, (bound + kWarps * kMinBlocks - 1) / (kWarps * kMinBlocks)));
+// Which kernels a call needs. Sequences with up to kFewRows rows a key head are this
+// file's, and float32 rows of any number; more bfloat16 rows are the tensor cores'. A
+// call whose sequences all have max_tokens rows needs one kernel.
+constexpr long long kFewRows = 16;
+struct Plan {
+  bool few, many;
+  size_t few_bytes, bytes;   // the workspace: `few` first
+};
+Plan plan_of(int rows, int batch, int group, int head_dim, int max_tokens, bool bf16) {
+  Plan p{};
+  p.many = bf16 && (long long)group * max_tokens > kFewRows;
+  p.few = !p.many || (long long)max_tokens * batch != rows;
+  const int part_rows = p.many ? 16 : 8 * row_tiles(group, max_tokens);
+  if (p.few) p.few_bytes = (size_t)num_sms() * 2 * (sizeof(KvPart) + kv_part_bytes(head_dim, part_rows));
+  p.bytes = p.few_bytes + (p.many ? kv_tiles_workspace(head_dim) : 0);
+  return p;
 }
 
 template <int D, int NT, typename T>
-cudaError_t rows_typed(const KvAttentionArgs& a, bool vec, cudaStream_t s) {
+cudaError_t rows_typed(const KvAttentionArgs& a, long long rows_to, bool vec, cudaStream_t s) {
   using S = Shape<D, NT>;
   const int sms = num_sms();
   if (sms <= 0) return cudaErrorInvalidDevice;
+  // one CTA an SM, but no more than the work can fill
   const long long tiles = ((long long)a.batch.rows * a.group + S::kRows - 1) / S::kRows + a.batch.batch;
   const long long blocks = std::max(1, (a.batch.capacity + kKvBlock - 1) / kKvBlock);
-  Work w{};
+  const long long bound = std::min(tiles * a.cache.heads, 1ll << 30) * blocks;
+  constexpr int kLeast = kWarps * kMinBlocks;
+  KvWork w{};
   w.a = a;
-  w.ctas = rows_ctas(sms, std::min(tiles * a.cache.heads, 1ll << 30) * blocks);
-  w.parts = static_cast<Part*>(a.workspace);
-  w.ws = static_cast<uint8_t*>(a.workspace) + (size_t)sms * 2 * sizeof(Part);
+  w.rows_to = rows_to;
+  w.ctas = (int)std::min<long long>(sms, (bound + kLeast - 1) / kLeast);
+  w.parts = static_cast<KvPart*>(a.workspace);
+  w.ws = static_cast<uint8_t*>(a.workspace) + (size_t)sms * 2 * sizeof(KvPart);
   auto kern = vec ? &kv_attention_rows_kernel<D, NT, T, true> : &kv_attention_rows_kernel<D, NT, T, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
   e = launch_chained(kern, dim3(w.ctas), dim3(kThreads), S::kSmem, 1, s, w);
   if (e != cudaSuccess) return e;
-  return launch_chained(&kv_attention_join_kernel<D, NT, T>, dim3(w.ctas), dim3(kThreads), 0, 1, s, w);
+  return launch_chained(&kv_attention_join_kernel<D, S::kRows, T>, dim3(w.ctas), dim3(256), 0, 1, s, w);
 }
 
 template <int D>
-cudaError_t rows_sized(const KvAttentionArgs& a, bool bf16, bool vec, cudaStream_t s) {
-  if (row_tiles(a.group, a.max_tokens) == 1)
-    return bf16 ? rows_typed<D, 1, __nv_bfloat16>(a, vec, s) : rows_typed<D, 1, float>(a, vec, s);
-  return bf16 ? rows_typed<D, 2, __nv_bfloat16>(a, vec, s) : rows_typed<D, 2, float>(a, vec, s);
+cudaError_t rows_sized(const KvAttentionArgs& a, bool one, long long rows_to, bool bf16, bool vec, cudaStream_t s) {
+  if (one)
+    return bf16 ? rows_typed<D, 1, __nv_bfloat16>(a, rows_to, vec, s) : rows_typed<D, 1, float>(a, rows_to, vec, s);
+  return bf16 ? rows_typed<D, 2, __nv_bfloat16>(a, rows_to, vec, s) : rows_typed<D, 2, float>(a, rows_to, vec, s);
 }
 
 }  // namespace
 
 size_t kv_attention_workspace(int rows, int batch, int heads, int group, int head_dim, int max_tokens, bool bf16) {
-  const int sms = num_sms();
-  if (sms <= 0) return 0;
-  const size_t part = head_dim == 64 ? (row_tiles(group, max_tokens) == 1 ? Shape<64, 1>::kWsPart : Shape<64, 2>::kWsPart)
-                                     : (row_tiles(group, max_tokens) == 1 ? Shape<128, 1>::kWsPart
-                                                                          : Shape<128, 2>::kWsPart);
-  return (size_t)sms * 2 * (sizeof(Part) + part);
+  return plan_of(rows, batch, group, head_dim, max_tokens, bf16).bytes;
 }
 
 cudaError_t launch_kv_attention(const KvAttentionArgs& a, int head_dim, bool bf16, bool vec, cudaStream_t s,
                                 const char** kernel_name) {
-  *kernel_name = "kv_attention_rows+join";
-  return head_dim == 64 ? rows_sized<64>(a, bf16, vec, s) : rows_sized<128>(a, bf16, vec, s);
+  const Plan p = plan_of(a.batch.rows, a.batch.batch, a.group, head_dim, a.max_tokens, bf16);
+  if (p.few) {
+    const bool one = !p.many && row_tiles(a.group, a.max_tokens) == 1;
+    const long long rows_to = p.many ? kFewRows : LLONG_MAX;
+    const cudaError_t e = head_dim == 64 ? rows_sized<64>(a, one, rows_to, bf16, vec, s)
+                                         : rows_sized<128>(a, one, rows_to, bf16, vec, s);
+    if (e != cudaSuccess) return e;
+    *kernel_name = "kv_attention_rows";
+  }
+  if (p.many) {
+    const cudaError_t e = launch_kv_attention_tiles(a, p.few ? kFewRows + 1 : 0,
+                                                    static_cast<uint8_t*>(a.workspace) + p.few_bytes, head_dim, vec, s);
+    if (e != cudaSuccess) return e;
+    *kernel_name = p.few ? "kv_attention_rows+tiles" : "kv_attention_tiles";
+  }
+  return cudaSuccess;
 }
 
 }  // namespace qmm

@@ -1,0 +1,282 @@
+// What the kernels of attention over the 8-bit key-value cache share: how the work is
+// cut and how its parts are joined.
+#pragma once
+
+#include "chain.cuh"
+#include "common.cuh"
+#include "kv.cuh"
+
+namespace qmm {
+
+constexpr float kKvNone = -1e30f;      // a running maximum that has seen nothing
+constexpr float kKvSlack = 8.f;        // how far a score may pass the running maximum (a factor of 256)
+
+// A part of an item that one warp (in shared memory) or one CTA (in the workspace) holds.
+enum { kPartNone = 0, kPartHeld = 1, kPartBegins = 2, kPartEnds = 4 };
+struct KvPart {
+  int b, r, h, flags;
+};
+
+__host__ __device__ constexpr size_t kv_part_bytes(int dim, int rows) { return (size_t)rows * (dim + 2) * 4; }
+
+// The kernel for many rows (kv_attention_tiles.cu), of the sequences with at least
+// rows_from rows a key head.
+size_t kv_tiles_workspace(int head_dim);
+cudaError_t launch_kv_attention_tiles(const KvAttentionArgs& a, long long rows_from, void* workspace, int head_dim,
+                                      bool vec, cudaStream_t s);
+
+struct KvWork {
+  KvAttentionArgs a;
+  long long rows_from, rows_to;   // this kernel takes the sequences with so many rows a key head
+  KvPart* parts;                  // [ctas][2]
+  uint8_t* ws;                    // [ctas][2] parts of kRows * (D + 2) floats
+  int ctas;
+};
+
+// The kernels cut the work of a call alike: all (sequence, tile of R rows, key head)
+// items end to end in units of TK tokens, and to each worker the same number of
+// consecutive units, wherever items begin and end.
+
+// The units of one row tile: at least one, so that rows that see nothing are written.
+template <int R, int TK>
+__device__ __forceinline__ int kv_tile_units(const KvWork& w, const KvSeq& s, int r) {
+  const int last = min((int)(((long long)(r + 1) * R - 1) / w.a.group), s.n - 1);
+  return max((int)(((long long)kv_visible(s, last, w.a.causal) + TK - 1) / TK), 1);
+}
+template <int R>
+__device__ __forceinline__ int kv_tile_count(const KvWork& w, const KvSeq& s) {
+  const long long rows = (long long)s.n * w.a.group;
+  return rows < w.rows_from || rows > w.rows_to ? 0 : (int)((rows + R - 1) / R);
+}
+
+// The units of sequence b, another one in each lane; a whole warp calls. A sequence of
+// many row tiles is summed by all lanes.
+template <int R, int TK>
+__device__ __forceinline__ long long kv_sequence_units(const KvWork& w, int b) {
+  const int lane = threadIdx.x & 31;
+  KvSeq s{};
+  int tiles = 0;
+  if (b < w.a.batch.batch) {
+    s = kv_sequence(w.a.batch, b);
+    tiles = kv_tile_count<R>(w, s);
+  }
+  long long sum = 0;
+  if (tiles <= 2)
+    for (int r = 0; r < tiles; ++r) sum += kv_tile_units<R, TK>(w, s, r);
+  for (unsigned many = __ballot_sync(~0u, tiles > 2); many; many &= many - 1) {
+    const int l = __ffs(many) - 1;
+    KvSeq o{};
+    o.n = __shfl_sync(~0u, s.n, l);
+    o.len = __shfl_sync(~0u, s.len, l);
+    o.seen = __shfl_sync(~0u, s.seen, l);
+    const int count = __shfl_sync(~0u, tiles, l);
+    long long all = 0;
+    for (int r = lane; r < count; r += 32) all += kv_tile_units<R, TK>(w, o, r);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) all += __shfl_xor_sync(~0u, all, d);
+    if (lane == l) sum = all;
+  }
+  return sum * w.a.cache.heads;
+}
+template <int R, int TK>
+__device__ __forceinline__ long long kv_total_units(const KvWork& w) {
+  const int lane = threadIdx.x & 31;
+  long long total = 0;
+  for (int b0 = 0; b0 < w.a.batch.batch; b0 += 32) total += kv_sequence_units<R, TK>(w, b0 + lane);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
+  return total;
+}
+
+// The lane whose inclusive prefix sum over `mine` first passes `at`, or -1; `before`
+// receives the sum before that lane, or of all lanes.
+__device__ __forceinline__ int kv_prefix_find(long long mine, long long at, long long& before) {
+  const int lane = threadIdx.x & 31;
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long up = __shfl_up_sync(~0u, incl, o);
+    if (lane >= o) incl += up;
+  }
+  const unsigned past = __ballot_sync(~0u, incl > at);
+  const int l = past ? __ffs(past) - 1 : -1;
+  before = past ? __shfl_sync(~0u, incl - mine, l) : __shfl_sync(~0u, incl, 31);
+  return l;
+}
+
+// A place in the line of units.
+template <int R, int TK>
+struct KvCursor {
+  int b, r, h, at, units, tiles;   // unit `at` of `units` of the item (b, r, h)
+  KvSeq s;
+
+  // To unit `place` of the line (which has more); a whole warp calls.
+  __device__ void seek(const KvWork& w, long long place) {
+    const int lane = threadIdx.x & 31;
+    b = 0;
+    for (int b0 = 0; b0 < w.a.batch.batch; b0 += 32) {
+      long long before;
+      const int l = kv_prefix_find(kv_sequence_units<R, TK>(w, b0 + lane), place, before);
+      place -= before;
+      if (l >= 0) {
+        b = b0 + l;
+        break;
+      }
+    }
+    s = kv_sequence(w.a.batch, b);
+    tiles = kv_tile_count<R>(w, s);
+    r = 0;
+    for (int r0 = 0; r0 < tiles; r0 += 32) {
+      long long before;
+      const long long mine = r0 + lane < tiles ? (long long)kv_tile_units<R, TK>(w, s, r0 + lane) * w.a.cache.heads : 0;
+      const int l = kv_prefix_find(mine, place, before);
+      place -= before;
+      if (l >= 0) {
+        r = r0 + l;
+        break;
+      }
+    }
+    units = kv_tile_units<R, TK>(w, s, r);
+    h = (int)(place / units);
+    at = (int)(place % units);
+  }
+  // To the next item's first unit.
+  __device__ void next_item(const KvWork& w) {
+    at = 0;
+    if (++h < w.a.cache.heads) return;
+    h = 0;
+    if (++r >= tiles) {
+      r = 0;
+      do {
+        if (++b >= w.a.batch.batch) return;
+        s = kv_sequence(w.a.batch, b);
+        tiles = kv_tile_count<R>(w, s);
+      } while (tiles == 0);
+    }
+    units = kv_tile_units<R, TK>(w, s, r);
+  }
+};
+
+// Where rows of an item go: rows are (token, query head of the group), token major.
+__device__ __forceinline__ long long kv_out_row(const KvAttentionArgs& a, const KvSeq& s, int h, int row) {
+  return (long long)(s.start + row / a.group) * ((long long)a.cache.heads * a.group) + (long long)h * a.group +
+         row % a.group;
+}
+
+// Parts [first, first + count) of one item joined, one row by one warp: rows of O that
+// are already divided by their own sums l, with their maxima m. part(i) gives the
+// i-th part's bytes. The joined row is written to `out` (T, row index given) where it
+// is the whole item's, else as a part again.
+template <int D, typename T, typename F>
+__device__ __forceinline__ void kv_join_row(int count, int rows, int row, F part, bool whole, T* out, uint8_t* into) {
+  constexpr int kE = D / 32;
+  const int lane = threadIdx.x & 31;
+  float top = kKvNone;
+  for (int i = lane; i < count; i += 32)
+    top = fmaxf(top, reinterpret_cast<const float2*>(part(i) + rows * D * 4)[row].x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+  float sum = 0.f, acc[kE] = {};
+#pragma unroll 4
+  for (int i = 0; i < count; ++i) {
+    const uint8_t* p = part(i);
+    const float2 ml = reinterpret_cast<const float2*>(p + rows * D * 4)[row];
+    const float weight = ml.y * exp2f(ml.x - top);
+    sum += weight;
+    if constexpr (kE == 4) {
+      const float4 x = reinterpret_cast<const float4*>(p)[row * 32 + lane];
+      acc[0] += weight * x.x; acc[1] += weight * x.y; acc[2] += weight * x.z; acc[3] += weight * x.w;
+    } else {
+      const float2 x = reinterpret_cast<const float2*>(p)[row * 32 + lane];
+      acc[0] += weight * x.x; acc[1] += weight * x.y;
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int e = 0; e < kE; ++e) acc[e] *= inv;
+  if (!whole) {
+    float* o = reinterpret_cast<float*>(into) + row * D + lane * kE;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) o[e] = acc[e];
+    if (lane == 0) reinterpret_cast<float2*>(into + rows * D * 4)[row] = make_float2(top, sum);
+  } else if (out) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int e = 0; e < kE; ++e) out[lane * kE + e] = acc[e];
+    } else {
+      uint32_t u[kE / 2];
+#pragma unroll
+      for (int e = 0; e < kE / 2; ++e) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(acc[2 * e], acc[2 * e + 1]);
+        u[e] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+      if constexpr (kE == 4) {
+        *reinterpret_cast<uint2*>(out + lane * 4) = make_uint2(u[0], u[1]);
+      } else {
+        *reinterpret_cast<uint32_t*>(out + lane * 2) = u[0];
+      }
+    }
+  }
+}
+
+// What several CTAs hold of an item, joined by the CTA with the number of the one that
+// holds its beginning.
+template <int D, int R, typename T>
+__global__ void __launch_bounds__(256) kv_attention_join_kernel(const KvWork w) {
+  chain_wait();
+  const KvPart a = w.parts[2 * blockIdx.x + 1];
+  if (!(a.flags & kPartHeld)) {
+    chain_release();
+    return;
+  }
+  // the following CTAs' first parts belong to the item, up to the one that ends it
+  const int lane = threadIdx.x & 31;
+  int n = 1;
+  for (int c0 = blockIdx.x + 1; c0 < w.ctas; c0 += 32) {
+    const int c = c0 + lane;
+    const unsigned ends = __ballot_sync(~0u, c < w.ctas && (w.parts[2 * c].flags & kPartEnds));
+    if (ends) {
+      n += __ffs(ends);
+      break;
+    }
+    n += 32;
+  }
+  n = min(n, w.ctas - (int)blockIdx.x);
+  const KvSeq s = kv_sequence(w.a.batch, a.b);
+  chain_release();
+  auto part = [&](int j) -> const uint8_t* {
+    return w.ws + (size_t)(j == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + j)) * kv_part_bytes(D, R);
+  };
+  for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < R; row += 8 * gridDim.y) {
+    if (a.r * R + row >= s.n * w.a.group) break;
+    T* out = static_cast<T*>(w.a.out) + kv_out_row(w.a, s, a.h, a.r * R + row) * D;
+    kv_join_row<D, T>(n, R, row, part, true, out, nullptr);
+  }
+}
+
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t half_pair(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Two int8, biased by 128, to two fp16: bytes 0 and 1 of u, or 2 and 3. The byte becomes
+// the low mantissa bits of 1024, whose ulp is 1, and 1024 + 128 is taken off, exactly.
+__device__ __forceinline__ uint32_t bytes_low(uint32_t u) {
+  const uint32_t l = prmt(u, 0x64646464u, 0x4140u);
+  const __half2 bias(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&l), bias);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t bytes_high(uint32_t u) {
+  const uint32_t l = prmt(u, 0x64646464u, 0x4342u);
+  const __half2 bias(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&l), bias);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+}  // namespace qmm
