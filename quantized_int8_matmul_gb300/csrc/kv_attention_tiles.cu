@@ -27,41 +27,88 @@ namespace qmm {
 namespace {
 
 constexpr int kRows = 256, kTokens = 128;
-constexpr int kThreads = 448;
-constexpr int kStages = 4;                 // operands (K or V tiles) in the ring
+constexpr int kThreads = 512;
+// Registers a thread of the softmax, of the converters and of the rest: the launch has 128 each.
+constexpr int kSoftmaxRegs = 192, kConvertRegs = 80, kRestRegs = 48;
+static_assert(256 * kSoftmaxRegs + 128 * kConvertRegs + 128 * kRestRegs <= 512 * 128, "registers of the launch");
+constexpr int kStages = 3;                 // operands (K or V tiles) in the ring of fp16
+constexpr int kRaw = 4;                    // and in the ring of int8 before it
 constexpr int kInfo = 4;                   // tiles whose scales are kept
 constexpr int kBlocks = kTokens / kKvBlock;
 constexpr int kMinTiles = 2;               // a CTA's share, at least
 constexpr float kLift = 7.f;               // P is held times 2^7: at most 2^15
 
-struct Info {
-  float kpow[kBlocks];     // 2^(byte - 127) of the tile's key blocks
-  int ve[kBlocks];         // bytes of its value blocks
-  int vmax;                // the largest of them
+// What the softmax needs to know of a tile's blocks.
+struct alignas(16) Info {
+  float kpow[kBlocks];     // 2^(byte - 127) of the key blocks
+  float vdown[kBlocks];    // byte - vmax of the value blocks, no less than -100
+  float vup[kBlocks];      // 2^(vmax - byte), the same
+  int vmax;                // the largest byte
   int missing;             // blocks on pages that are not there, a bit each
+  int pad[2];
 };
+
+// A CTA's consecutive units of one item, as one warp works them out for all.
+struct alignas(16) Run {
+  int b, r, h, flags;          // as in a part; kRunStop: there is none
+  int at, tiles, rows, start;  // first unit, units, rows of the tile pair, first packed row
+  int n, len, seen, pad;       // the sequence's
+};
+enum { kRunStop = 8 };
+constexpr int kRuns = 4;       // kept
 
 template <int D>
 struct Smem {
   static constexpr int kQTile = 128 * D * 2;
   static constexpr int kStage = kTokens * D * 2;
+  static constexpr int kRawStage = kTokens * D;
   alignas(1024) uint8_t q[2 * kQTile];
   alignas(1024) uint8_t stage[kStages][kStage];
+  alignas(128) uint8_t raw[kRaw][kRawStage];
   Info info[kInfo];
-  uint64_t full[kStages], empty[kStages];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drained;
+  Run run[kRuns];
+  uint64_t full[kStages], empty[kStages], raw_full[kRaw], raw_empty[kRaw];
+  uint64_t run_full[kRuns], run_empty[kRuns];
+  uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], drained;   // p_full: of either half of the columns
   uint32_t tmem;
   int abort;
 };
 
-__device__ __forceinline__ void mma_f16_tmem(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                             uint32_t accumulate) {
+// MMAs by the one lane of a converged warp for which `lead` is not 0: predicated, so
+// that the warp's descriptors stay in uniform registers, where the instruction takes
+// them from. A from shared memory, then A from tensor memory.
+__device__ __forceinline__ void mma_one(uint32_t lead, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
       : "memory");
+}
+__device__ __forceinline__ void mma_one(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void commit_one(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
 }
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 r;
@@ -80,29 +127,44 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return r;
 }
 
-using Cursor = KvCursor<kRows, kTokens>;
-
-// A CTA's consecutive units of one item.
-struct Run {
-  Cursor c;
-  int tiles;         // units of the run
-  long long left;    // units of the CTA's share from the run's beginning on
-
-  __device__ bool begins() const { return c.at == 0; }
-  __device__ bool ends() const { return c.at + tiles == c.units; }
-  // Whether the second tile has rows.
-  __device__ bool second(const KvWork& w) const {
-    return (long long)c.s.n * w.a.group - (long long)c.r * kRows > kRows / 2;
+// A wait of a whole warp, or of one lane of it, whose outcome is the same for all that
+// wait. Bounded by its tries, 2^22 of some tens of cycles, where the other kernels read
+// a clock: the waits here are short and many, and little code in each of them keeps the
+// roles, which share the instruction cache, from waiting for it.
+constexpr int kTries = 1 << 22;
+template <bool kWarp>
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* err,
+                                         unsigned site) {
+#pragma unroll 1
+  for (int i = 0;; ++i) {
+    const bool ok = mbar_try_wait(bar, parity);
+    if (kWarp ? __all_sync(~0u, ok) : ok) return true;
+    const bool end = i > kTries || *abort;
+    if (kWarp ? __any_sync(~0u, end) : end) break;
   }
-  __device__ void open() { tiles = (int)min(left, (long long)(c.units - c.at)); }
-  __device__ bool next(const KvWork& w) {
-    left -= tiles;
-    if (left <= 0) return false;
-    c.next_item(w);
-    open();
-    return true;
-  }
-};
+  if (!*abort) record_error(err, site);
+  *abort = 1;
+  return false;
+}
+
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// 128 columns of this warp's lanes.
+__device__ __forceinline__ void tmem_ld128(uint32_t t, uint32_t (&r)[128]) {
+  auto& a = *reinterpret_cast<uint32_t(*)[32]>(&r[0]);
+  auto& b = *reinterpret_cast<uint32_t(*)[32]>(&r[32]);
+  auto& c = *reinterpret_cast<uint32_t(*)[32]>(&r[64]);
+  auto& d = *reinterpret_cast<uint32_t(*)[32]>(&r[96]);
+  tmem_ld32x2(t, a, t + 32, b);
+  tmem_ld32x2(t + 64, c, t + 96, d);
+}
 
 // The row of Q that a softmax thread owns: scaled by a power of two that puts its
 // largest magnitude into [2^14, 2^15), where fp16 holds bfloat16 exactly down to 2^-24
@@ -112,9 +174,9 @@ struct Row {
   int limit;     // tokens that the row sees; INT_MAX for a row that is not there
 };
 template <int D, bool kVec>
-__device__ __forceinline__ Row load_row(const KvWork& w, const Cursor& c, int tile, int row, uint8_t* q) {
-  const int rr = c.r * kRows + tile * 128 + row;
-  const bool there = rr < c.s.n * w.a.group;
+__device__ __forceinline__ Row load_row(const KvWork& w, const Run& run, int tile, int row, uint8_t* q) {
+  const int rr = run.r * kRows + tile * 128 + row;
+  const bool there = tile * 128 + row < run.rows;
   Row out{1.f, INT_MAX};
   const uint32_t dst = smem_u32(q) + (uint32_t)row * 128u;
   const int swz = row & 7;
@@ -124,8 +186,8 @@ __device__ __forceinline__ Row load_row(const KvWork& w, const Cursor& c, int ti
     return out;
   }
   const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(w.a.q) +
-                             (long long)(c.s.start + rr / w.a.group) * w.a.q_row +
-                             (long long)(c.h * w.a.group + rr % w.a.group) * w.a.q_head;
+                             (long long)(run.start + rr / w.a.group) * w.a.q_row +
+                             (long long)(run.h * w.a.group + rr % w.a.group) * w.a.q_head;
   uint32_t x[D / 2];
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) {
@@ -148,7 +210,7 @@ __device__ __forceinline__ Row load_row(const KvWork& w, const Cursor& c, int ti
   if (scale < 0.f) up = -up;
   if (scale == 0.f) up = 0.f;
   if (scale != 0.f) out.coef = fabsf(scale) * 1.4426950408889634f * __int_as_float((e - 14) << 23);
-  out.limit = kv_visible(c.s, rr / w.a.group, w.a.causal);
+  out.limit = kv_visible(KvSeq{0, run.n, run.len, run.seen}, rr / w.a.group, w.a.causal);
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) {
     uint32_t u[4];
@@ -175,10 +237,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
       mbar_init(&sm.full[i], 4);
       mbar_init(&sm.empty[i], 1);
     }
+    for (int i = 0; i < kRaw; ++i) {
+      mbar_init(&sm.raw_full[i], 1);
+      mbar_init(&sm.raw_empty[i], 4);
+    }
+    for (int i = 0; i < kRuns; ++i) {
+      mbar_init(&sm.run_full[i], 1);
+      mbar_init(&sm.run_empty[i], 14);   // 8 warps of the softmax, 4 converters, the MMAs' and the copies'
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.q_full[i], 4);
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i], 4);
+      mbar_init(&sm.p_full[i][0], 4);
+      mbar_init(&sm.p_full[i][1], 4);
       mbar_init(&sm.o_full[i], 1);
     }
     mbar_init(&sm.drained, 1);
@@ -192,85 +263,80 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
-  const uint32_t s_col[2] = {0, 128}, o_col[2] = {256, 384};
   chain_wait();
 
-  // a wait whose outcome is the same for the whole warp
   auto wait = [&](uint64_t* bar, uint32_t parity, unsigned site) -> bool {
-    return __all_sync(~0u, mbar_wait(bar, parity, &sm.abort, w.a.err, site));
+    return wait_for<true>(bar, parity, &sm.abort, w.a.err, site);
   };
-
-  const long long total = kv_total_units<kRows, kTokens>(w);
-  const long long share = max((total + w.ctas - 1) / w.ctas, (long long)kMinTiles);
-  const long long begin = (long long)blockIdx.x * share;
-  Run run;
-  run.left = min(max(total - begin, 0ll), share);
-  const bool work = run.left > 0;
-  if (work) {
-    run.c.seek(w, begin);
-    run.open();
-  }
+  // the CTA's runs in turn
+  int run_slot = 0;
+  uint32_t run_phase = 0;
+  auto next_run = [&](Run& to) -> bool {
+    if (!wait(&sm.run_full[run_slot], run_phase, 0x50a)) return false;
+    to = sm.run[run_slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.run_empty[run_slot]);
+    if (++run_slot == kRuns) {
+      run_slot = 0;
+      run_phase ^= 1;
+    }
+    return !(to.flags & kRunStop);
+  };
 
   if (warp < 8) {
     // ---------------- softmax: a row a thread ----------------
+    more_registers<kSoftmaxRegs>();
     const int x = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;     // 32 lanes a warp, in bits 16 and up
-    const uint32_t s_tmem = tmem + lanes + s_col[x], o_tmem = tmem + lanes + o_col[x];
-    KvPart left[2] = {{0, 0, 0, kPartNone}, {0, 0, 0, kPartNone}};
+    // scores (and P) of the two tiles in columns 0 and 128, O in 256 and 384
+    const uint32_t s_tmem = tmem + lanes + x * 128, o_tmem = s_tmem + 256;
+    KvPart left0{0, 0, 0, kPartNone}, left1{0, 0, 0, kPartNone};
     uint32_t s_phase = 0, o_phase = 0;
     int tile = 0;            // tiles of the CTA before the run
-    bool more = work, ok = true;
-    Row r{1.f, INT_MAX};
+    bool ok = true;
+    Run now{};
+    Row me{1.f, INT_MAX};
     auto put_row = [&] {
-      if (x && !run.second(w)) return;
-      r = load_row<D, kVec>(w, run.c, x, row, sm.q + x * kQTile);
+      if (x && now.rows <= 128) return;
+      me = load_row<D, kVec>(w, now, x, row, sm.q + x * kQTile);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.q_full[x]);
     };
+    bool more = next_run(now);
     if (more) put_row();
-    while (more && ok) {
-      const Run now = run;
-      const bool mine = !x || now.second(w);
+    while (more) {
+      const bool mine = !x || now.rows > 128;
       float m = kKvNone, l = 0.f;
       int vref = 0;
-      const Row me = r;
       if (mine) {
-        for (int j = 0; j < now.tiles; ++j) {
+        const float coef = me.coef;
+        int cut = me.limit - now.at * kTokens;   // columns of the tile that the row sees
+        for (int j = 0; j < now.tiles; ++j, cut -= kTokens) {
           if (!(ok = wait(&sm.s_full[x], s_phase, 0x501))) break;
           s_phase ^= 1;
           tc_fence_after();
           const Info& info = sm.info[(tile + j) % kInfo];
-          const int cut = me.limit - (now.c.at + j) * kTokens;   // columns that the row sees
-          const int missing = info.missing;
-          const bool mask = __any_sync(~0u, cut < kTokens) || missing;
-          uint32_t a[32], b[32];
-          // columns of the half from `from` on that are masked, to -inf
-          auto masked = [&](int from) {
+          uint32_t s[128];
+          tmem_ld128(s_tmem, s);
+          const int missing = info.missing, vmax = info.vmax;
+          if (__any_sync(~0u, cut < kTokens) || missing) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              if (from + i >= cut || (missing >> ((from + i) / kKvBlock) & 1)) a[i] = 0xff800000u;
-              if (from + 32 + i >= cut || (missing >> ((from + 32 + i) / kKvBlock) & 1)) b[i] = 0xff800000u;
-            }
-          };
-          auto factor = [&](int block) { return fmaxf(me.coef * info.kpow[block], 1.17549435e-38f); };
-          auto top16 = [&](const uint32_t* v) {
-            float t = fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]));
+            for (int i = 0; i < kTokens; ++i)
+              if (i >= cut || (missing >> (i / kKvBlock) & 1)) s[i] = 0xff800000u;
+          }
+          // the blocks' factors, and the largest score
+          float f[kBlocks], top = -INFINITY;
 #pragma unroll
-            for (int i = 2; i < 16; i += 2) t = fmaxf(t, fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
-            return t;
-          };
-          auto top_half = [&](int first) {
-            return fmaxf(fmaxf(top16(a) * factor(first), top16(a + 16) * factor(first + 1)),
-                         fmaxf(top16(b) * factor(first + 2), top16(b + 16) * factor(first + 3)));
-          };
-          tmem_ld32x2(s_tmem + 64, a, s_tmem + 96, b);
-          if (mask) masked(64);
-          float top = top_half(4);
-          tmem_ld32x2(s_tmem, a, s_tmem + 32, b);
-          if (mask) masked(0);
-          top = fmaxf(top, top_half(0));
-          const int vmax = info.vmax;
+          for (int k = 0; k < kBlocks; ++k) {
+            f[k] = fmaxf(coef * info.kpow[k], 1.17549435e-38f);
+            float t = __uint_as_float(s[16 * k]);
+#pragma unroll
+            for (int i = 1; i < 15; i += 2)
+              t = fmaxf(fmaxf(t, __uint_as_float(s[16 * k + i])), __uint_as_float(s[16 * k + i + 1]));
+            t = fmaxf(t, __uint_as_float(s[16 * k + 15]));
+            top = fmaxf(top, t * f[k]);
+          }
           if (__any_sync(~0u, top > m + kKvSlack) || vmax > vref) {
             const float up = fmaxf(m, top);
             float down = exp2_approx(m - up);
@@ -282,71 +348,67 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
             }
             if (j > 0) {
 #pragma unroll 1
-              for (int i = 0; i < D; i += 32) {
-                uint32_t o[32];
-                tmem_ld32(o_tmem + i, o);
+              for (int i = 0; i < D; i += 16) {
+                uint32_t o[16];
+                tmem_ld16(o_tmem + i, o);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * down);
-                tmem_st32(o_tmem + i, o);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * down);
+                tmem_st16(o_tmem + i, o);
               }
             }
           }
-          // 16 columns: P, packed in pairs, and its sum
-          auto exp16 = [&](const uint32_t* v, int block, uint32_t* p) {
-            const float f = factor(block);
-            const int d = max(info.ve[block] - vref, -100);
-            const float add = (float)d + kLift - m;
-            const float2 f2 = make_float2(f, f), add2v = make_float2(add, add);
-            float2 sum = make_float2(0.f, 0.f);
+          // P = exp2(score - m) * 2^(byte - vref), held times 2^kLift; the sum without the powers
+          const int behind = max(vmax - vref, -100);
+          const float base = (float)behind + kLift - m;
+          float sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2 y = fma2(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2, add2v);
-              const float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-              sum = add2(sum, e);
-              p[i] = half_pair(e.x, e.y);
-            }
-            l += (sum.x + sum.y) * __int_as_float((127 - d) << 23);
-          };
-          auto exp_half = [&](int first, uint32_t p_tmem) {
+          for (int half = 0; half < 2; ++half) {
             uint32_t p[32];
-            exp16(a, first, p);
-            exp16(a + 16, first + 1, p + 8);
-            exp16(b, first + 2, p + 16);
-            exp16(b + 16, first + 3, p + 24);
-            tmem_st32_async(p_tmem, p);
-          };
-          exp_half(0, s_tmem);
-          tmem_ld32x2(s_tmem + 64, a, s_tmem + 96, b);
-          if (mask) masked(64);
-          exp_half(4, s_tmem + 32);
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.p_full[x]);
+#pragma unroll
+            for (int k = 4 * half; k < 4 * half + 4; ++k) {
+              const float add = info.vdown[k] + base;
+              const float2 f2 = make_float2(f[k], f[k]), a2 = make_float2(add, add);
+              float2 part = make_float2(0.f, 0.f);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float2 y = fma2(
+                    make_float2(__uint_as_float(s[16 * k + 2 * i]), __uint_as_float(s[16 * k + 2 * i + 1])), f2, a2);
+                const float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                part = i ? add2(part, e) : e;
+                p[8 * (k & 3) + i] = half_pair(e.x, e.y);
+              }
+              sum += (part.x + part.y) * info.vup[k];
+            }
+            tmem_st32_async(s_tmem + 32 * half, p);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.p_full[x][half]);
+          }
+          l += sum * __int_as_float((127 - behind) << 23);
         }
       }
       tile += now.tiles;
       if (!ok) break;
       // the next run's rows, under the last products of this one
-      more = run.next(w);
+      const Run was = now;
+      more = next_run(now);
       if (more) put_row();
-      const bool whole = now.begins() && now.ends();
-      const int slot = now.begins() ? 1 : 0;
-      if (!whole)
-        left[slot] = KvPart{now.c.b, now.c.r, now.c.h,
-                            kPartHeld | (now.begins() ? kPartBegins : 0) | (now.ends() ? kPartEnds : 0)};
+      const bool whole = (was.flags & kPartBegins) && (was.flags & kPartEnds);
+      const int slot = was.flags & kPartBegins ? 1 : 0;
+      if (!whole) (slot ? left1 : left0) = KvPart{was.b, was.r, was.h, was.flags};
       if (mine) {
         if (!(ok = wait(&sm.o_full[x], o_phase, 0x502))) break;
         o_phase ^= 1;
         tc_fence_after();
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const float vscale = kv_power(vref);
-        const int rr = now.c.r * kRows + x * 128 + row;
-        const bool there = rr < now.c.s.n * w.a.group;
         __nv_bfloat16* dst = nullptr;
         float* into = nullptr;
         if (whole) {
-          if (there) dst = static_cast<__nv_bfloat16*>(w.a.out) + kv_out_row(w.a, now.c.s, now.c.h, rr) * D;
+          if (x * 128 + row < was.rows)
+            dst = static_cast<__nv_bfloat16*>(w.a.out) +
+                  kv_out_row(w.a, KvSeq{was.start, was.n, was.len, was.seen}, was.h, was.r * kRows + x * 128 + row) * D;
         } else {
           into = reinterpret_cast<float*>(w.ws + (size_t)(2 * blockIdx.x + slot) * kv_part_bytes(D, kRows));
           reinterpret_cast<float2*>(into + kRows * D)[x * 128 + row] = make_float2(m, l);
@@ -374,184 +436,239 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
         tc_fence_before();
       }
     }
-    if (threadIdx.x < 2) w.parts[2 * blockIdx.x + threadIdx.x] = left[threadIdx.x];
+    if (threadIdx.x == 0) {
+      w.parts[2 * blockIdx.x] = left0;
+      w.parts[2 * blockIdx.x + 1] = left1;
+    }
   } else if (warp < 12) {
-    // ---------------- keys and values: pages to fp16 operands ----------------
+    // ---------------- int8 to fp16 operands ----------------
+    fewer_registers<kConvertRegs>();
     const int c = threadIdx.x - 256;
-    // a thread takes 16 bytes of a row; four neighbours and the same of the next token lie in different banks
+    // A thread takes 16 bytes of a token's row. Of eight neighbours four read the first half of one token and
+    // four the second half of the next (D = 128), so that neither their loads nor their swizzled stores meet
+    // in a bank.
     constexpr int kChunks = D / 16;                    // of a row
-    constexpr int kPer = kChunks * kKvBlock / 128;     // rounds of 128 threads a block (2 blocks a round for D = 64)
-    constexpr int kRounds = kBlocks * kChunks * kKvBlock / 128;
-    const int chunk = (c & 3) + (kChunks == 8 ? (c >> 3 & 1) * 4 : 0);
-    const int token0 = kChunks == 8 ? ((c >> 4) * 2 + (c >> 2 & 1)) : (c >> 2);   // of a round's 16 or 32
     constexpr int kRoundTokens = 128 / kChunks;
-    static_assert(kPer <= 1, "a round holds whole blocks");
+    constexpr int kRounds = kTokens / kRoundTokens;
+    const int odd = c >> 2 & 1;
+    const int chunk = (c & 3) + (kChunks == 8 ? ((c >> 3 & 1) ^ odd) * 4 : 0);
+    const int token0 = kChunks == 8 ? (c >> 4) * 2 + odd : c >> 2;
+    const uint32_t src0 = (uint32_t)(token0 * D + chunk * 16);
     const uint32_t dst0 = (uint32_t)(chunk >> 2) * 16384u + (uint32_t)token0 * 128u;
     const uint32_t piece = (uint32_t)(chunk & 3) * 2u, swz = (uint32_t)token0 & 7u;
-    long long blocks = -1;      // lane i: place in the cache of block i of the tile that is fetched, -1: not there
-    uint4 k[kRounds], v[kRounds];
-    uint32_t stage = 0, phase = 1;
-    int tile = 0;
+    const uint32_t at0 = dst0 + ((piece ^ swz) << 4), at1 = dst0 + (((piece + 1) ^ swz) << 4);
+    uint32_t stage = 0, phase = 1, from = 0, from_phase = 0;
     bool ok = true;
-
-    // the tile's blocks, and their bytes for the softmax (by the first of the four warps)
-    int ke = 0, ve = 0;
-    auto find = [&](const Cursor& cur, int unit) {
-      blocks = -1;
-      if (lane < kBlocks) {
-        const int blk = unit * kBlocks + lane;
-        if ((long long)blk * kKvBlock < cur.s.seen) {
-          const int page = __ldg(w.a.batch.table + (size_t)cur.b * w.a.batch.width + blk / w.a.cache.bpp);
-          if (page >= 0 && page < w.a.cache.pages)
-            blocks = ((long long)page * w.a.cache.heads + cur.h) * w.a.cache.bpp + blk % w.a.cache.bpp;
-        }
-        if (warp == 8 && blocks >= 0) {
-          ke = __ldg(w.a.cache.ke + blocks);
-          ve = __ldg(w.a.cache.ve + blocks);
-        }
-      }
-    };
-    auto fetch = [&](uint4 (&into)[kRounds], const int8_t* from) {
+    Run run{};
+    while (ok && next_run(run)) {
+      for (int i = 2 * run.tiles; i > 0; --i) {
+        if (!(ok = wait(&sm.raw_full[from], from_phase, 0x503))) break;
+        const uint32_t src = smem_u32(sm.raw[from]) + src0;
+        uint4 x[kRounds];
 #pragma unroll
-      for (int i = 0; i < kRounds; ++i) {
-        const long long block = __shfl_sync(~0u, blocks, i * (kRoundTokens / kKvBlock) + token0 / kKvBlock);
-        into[i] = block < 0 ? make_uint4(0, 0, 0, 0)
-                            : ldg_nc_v4(from + block * (kKvBlock * D) + (token0 % kKvBlock) * D + chunk * 16);
-      }
-    };
-    auto put = [&](const uint4 (&from)[kRounds]) -> bool {
-      if (!wait(&sm.empty[stage], phase, 0x503)) return false;
-      const uint32_t base = smem_u32(sm.stage[stage]) + dst0;
+        for (int r = 0; r < kRounds; ++r) x[r] = ld_shared_v4(src + r * (kRoundTokens * D));
+        if (!(ok = wait(&sm.empty[stage], phase, 0x50c))) break;
+        const uint32_t dst = smem_u32(sm.stage[stage]);
 #pragma unroll
-      for (int i = 0; i < kRounds; ++i) {
-        const uint32_t u[4] = {from[i].x ^ 0x80808080u, from[i].y ^ 0x80808080u, from[i].z ^ 0x80808080u,
-                               from[i].w ^ 0x80808080u};
-        const uint32_t at = base + (uint32_t)(i * kRoundTokens) * 128u;
-        st_shared_v4(at + ((piece ^ swz) << 4), bytes_low(u[0]), bytes_high(u[0]), bytes_low(u[1]), bytes_high(u[1]));
-        st_shared_v4(at + (((piece + 1) ^ swz) << 4), bytes_low(u[2]), bytes_high(u[2]), bytes_low(u[3]),
-                     bytes_high(u[3]));
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.full[stage]);
-      if (++stage == kStages) {
-        stage = 0;
-        phase ^= 1;
-      }
-      return true;
-    };
-    bool more = work;
-    if (more) {
-      find(run.c, run.c.at);
-      fetch(k, w.a.cache.k);
-    }
-    while (more && ok) {
-      const int tiles = run.tiles;
-      for (int j = 0; j < tiles && ok; ++j, ++tile) {
-        fetch(v, w.a.cache.v);
-        if (warp == 8) {
-          const unsigned absent = __ballot_sync(~0u, lane < kBlocks && blocks < 0);
-          int vmax = blocks >= 0 ? ve : 0;
-#pragma unroll
-          for (int o = 4; o; o >>= 1) vmax = max(vmax, __shfl_xor_sync(~0u, vmax, o));
-          Info& info = sm.info[tile % kInfo];
-          if (lane < kBlocks) {
-            info.kpow[lane] = blocks >= 0 ? kv_power(ke) : 0.f;
-            info.ve[lane] = blocks >= 0 ? ve : vmax;
-          }
-          if (lane == 0) {
-            info.vmax = vmax;
-            info.missing = (int)absent;
-          }
+        for (int r = 0; r < kRounds; ++r) {
+          const uint32_t u[4] = {x[r].x ^ 0x80808080u, x[r].y ^ 0x80808080u, x[r].z ^ 0x80808080u,
+                                 x[r].w ^ 0x80808080u};
+          const uint32_t at = dst + (uint32_t)(r * kRoundTokens) * 128u;
+          st_shared_v4(at + at0, bytes_low(u[0]), bytes_high(u[0]), bytes_low(u[1]), bytes_high(u[1]));
+          st_shared_v4(at + at1, bytes_low(u[2]), bytes_high(u[2]), bytes_low(u[3]), bytes_high(u[3]));
         }
-        if (!(ok = put(k))) break;
-        // the next tile's blocks and keys, before this one's values are put
-        if (j + 1 < tiles) {
-          find(run.c, run.c.at + j + 1);
-          fetch(k, w.a.cache.k);
-        } else if ((more = run.next(w))) {
-          find(run.c, run.c.at);
-          fetch(k, w.a.cache.k);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sm.full[stage]);
+          mbar_arrive(&sm.raw_empty[from]);
         }
-        if (!(ok = put(v))) break;
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
+        if (++from == kRaw) {
+          from = 0;
+          from_phase ^= 1;
+        }
       }
     }
-  } else if (warp == 12) {
-    // ---------------- one thread issues the MMAs ----------------
-    if (lane == 0 && work) {
+  } else {
+    fewer_registers<kRestRegs>();
+    if (warp == 12) {
+      // ---------------- the MMAs, by one lane of a converged warp ----------------
       constexpr uint32_t s_desc = idesc_f16_f32(128, kTokens, false, false);
       constexpr uint32_t o_desc = idesc_f16_f32(128, D, false, true);
+      const uint32_t lead = elect();
+      const uint32_t tm = __shfl_sync(~0u, tmem, 0);
+      // descriptors of the first k-step; the others' differ in the start address alone, the low word
+      const uint64_t q_first = sdesc_sw128(smem_u32(sm.q), 16u, 1024u);
+      const uint64_t k_first = sdesc_sw128(smem_u32(sm.stage[0]), 16u, 1024u);
+      const uint64_t v_first = sdesc_sw128(smem_u32(sm.stage[0]), 16384u, 1024u);
       uint32_t stage = 0, phase = 0;       // of the ring
-      uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
-      bool ok = true, more = true;
-      auto wait1 = [&](uint64_t* bar, uint32_t parity, unsigned site) {
-        return mbar_wait(bar, parity, &sm.abort, w.a.err, site);
+      uint32_t q_phase = 0, p_phase = 0;   // a bit for either tile
+      bool ok = true;
+      // the next operand of the ring, waited for
+      auto operand = [&](unsigned site) -> uint32_t {
+        const uint32_t got = stage;
+        ok = wait(&sm.full[got], phase, site);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
+        return got;
       };
-      auto scores = [&](int x, uint32_t k_stage) {
-        const uint32_t q = smem_u32(sm.q) + x * kQTile, k = smem_u32(sm.stage[k_stage]);
+      Run run{};
+      while (ok && next_run(run)) {
+        const int tiles = __shfl_sync(~0u, run.tiles, 0), pair = __shfl_sync(~0u, run.rows, 0) > 128 ? 2 : 1;
+        // scores of tile 0; then, tile by tile, the products of one and the scores of the next
+        uint32_t v_stage = 0;
+#pragma unroll 1
+        for (int j = -1; j < tiles && ok; ++j) {
+          const bool more = j + 1 < tiles;
+          uint32_t k_stage = 0;
+          if (j >= 0) v_stage = operand(0x506);
+#pragma unroll 1
+          for (int x = 0; x < pair && ok; ++x) {
+            if (j >= 0) {
+              const uint64_t v = v_first + v_stage * (Smem<D>::kStage / 16);
+              const uint32_t o = tm + 256u + (uint32_t)x * 128u, p = tm + (uint32_t)x * 128u;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint32_t at = (uint32_t)(i >> 2) * 16384u + (uint32_t)(i & 3) * 32u;
-          tc_mma_f16(tmem + s_col[x], sdesc_sw128(q + at, 16u, 1024u), sdesc_sw128(k + at, 16u, 1024u), s_desc, i > 0);
-        }
-        tc_commit(&sm.s_full[x]);
-      };
-      auto step = [&](uint32_t& st, uint32_t& ph) {
-        if (++st == kStages) {
-          st = 0;
-          ph ^= 1;
-        }
-      };
-      while (more && ok) {
-        const int heads = run.second(w) ? 2 : 1;   // row tiles
-        uint32_t k_stage = stage;
-        if (!(ok = wait1(&sm.full[stage], phase, 0x504))) break;
-        step(stage, phase);
-        for (int x = 0; x < heads && ok; ++x) {
-          if (!(ok = wait1(&sm.q_full[x], q_phase[x], 0x505))) break;
-          q_phase[x] ^= 1;
-          tc_fence_after();
-          scores(x, k_stage);
-        }
-        if (!ok) break;
-        tc_commit(&sm.empty[k_stage]);
-        for (int j = 0; j < run.tiles && ok; ++j) {
-          const bool last = j + 1 == run.tiles;
-          const uint32_t v_stage = stage;
-          if (!(ok = wait1(&sm.full[stage], phase, 0x506))) break;
-          step(stage, phase);
-          for (int x = 0; x < heads; ++x) {
-            if (!(ok = wait1(&sm.p_full[x], p_phase[x], 0x507))) break;
-            p_phase[x] ^= 1;
-            tc_fence_after();
-            const uint32_t v = smem_u32(sm.stage[v_stage]);
-#pragma unroll
-            for (int i = 0; i < kBlocks; ++i)
-              mma_f16_tmem(tmem + o_col[x], tmem + s_col[x] + 8 * i, sdesc_sw128(v + 2048u * i, 16384u, 1024u), o_desc,
-                           j > 0 || i > 0);
-            if (last) {
-              tc_commit(&sm.o_full[x]);
-            } else {
-              if (x == 0) {
-                k_stage = stage;
-                if (!(ok = wait1(&sm.full[stage], phase, 0x508))) break;
-                step(stage, phase);
+              for (int half = 0; half < 2; ++half) {
+                if (!(ok = wait(&sm.p_full[x][half], p_phase >> x & 1, 0x507))) break;
                 tc_fence_after();
+#pragma unroll
+                for (int i = half * (kBlocks / 2); i < (half + 1) * (kBlocks / 2); ++i)
+                  mma_one(lead, o, p + 8 * i, v + 128u * i, o_desc, j > 0 || i > 0);
               }
-              scores(x, k_stage);
+              if (!ok) break;
+              p_phase ^= 1u << x;
+              if (!more) commit_one(lead, &sm.o_full[x]);
+            } else {
+              if (!(ok = wait(&sm.q_full[x], q_phase >> x & 1, 0x505))) break;
+              q_phase ^= 1u << x;
+            }
+            if (more) {
+              if (x == 0) {
+                k_stage = operand(0x508);
+                if (!ok) break;
+              }
+              tc_fence_after();
+              const uint64_t q = q_first + (uint32_t)x * (kQTile / 16), k = k_first + k_stage * (Smem<D>::kStage / 16);
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                const uint32_t step = (uint32_t)((i >> 2) * 16384 + (i & 3) * 32) / 16;
+                mma_one(lead, tm + (uint32_t)x * 128u, q + step, k + step, s_desc, i > 0);
+              }
+              commit_one(lead, &sm.s_full[x]);
             }
           }
           if (!ok) break;
-          tc_commit(&sm.empty[v_stage]);
-          if (!last) tc_commit(&sm.empty[k_stage]);
+          if (j >= 0) commit_one(lead, &sm.empty[v_stage]);
+          if (more) commit_one(lead, &sm.empty[k_stage]);
         }
-        if (ok) more = run.next(w);
       }
       // what was issued has to end before tensor memory is given back
-      tc_commit(&sm.drained);
+      commit_one(lead, &sm.drained);
       mbar_wait(&sm.drained, 0, nullptr, w.a.err, 0x509);
+      __syncwarp();
+    } else if (warp == 14) {
+      // ---------------- int8 keys and values from their pages, and what the softmax needs of their blocks ----------
+      uint32_t stage = 0, phase = 1, copies = 0;
+      int tile = 0;
+      bool ok = true;
+      Run run{};
+      while (ok && next_run(run)) {
+        // four tiles at a time, a lane each block: the table and the scales are two loads that follow each other
+#pragma unroll 1
+        for (int j0 = 0; j0 < run.tiles && ok; j0 += 32 / kBlocks) {
+          const int blk = (run.at + j0) * kBlocks + lane;
+          long long block = -1;
+          int ke = 0, ve = 0;
+          if (j0 + lane / kBlocks < run.tiles && (long long)blk * kKvBlock < run.seen) {
+            const int page = __ldg(w.a.batch.table + (size_t)run.b * w.a.batch.width + blk / w.a.cache.bpp);
+            if (page >= 0 && page < w.a.cache.pages) {
+              block = ((long long)page * w.a.cache.heads + run.h) * w.a.cache.bpp + blk % w.a.cache.bpp;
+              ke = __ldg(w.a.cache.ke + block);
+              ve = __ldg(w.a.cache.ve + block);
+            }
+          }
+          const unsigned there = __ballot_sync(~0u, block >= 0);
+          int vmax = ve;
+#pragma unroll
+          for (int o = kBlocks / 2; o; o >>= 1) vmax = max(vmax, __shfl_xor_sync(~0u, vmax, o));
+#pragma unroll 1
+          for (int j = j0; j < min(j0 + 32 / kBlocks, run.tiles) && ok; ++j, ++tile) {
+            const bool mine = lane / kBlocks == j - j0;
+            const unsigned here = there >> ((j - j0) * kBlocks) & ((1u << kBlocks) - 1);
+#pragma unroll 1
+            for (int kind = 0; kind < 2; ++kind) {
+              if (!(ok = wait(&sm.raw_empty[stage], phase, 0x50d))) break;
+              if (kind == 0 && mine) {
+                Info& info = sm.info[tile % kInfo];
+                const int i = lane % kBlocks, down = block >= 0 ? min(vmax - ve, 100) : 0;
+                info.kpow[i] = block >= 0 ? kv_power(ke) : 0.f;
+                info.vdown[i] = (float)-down;
+                info.vup[i] = __int_as_float((127 + down) << 23);
+                if (i == 0) {
+                  info.vmax = vmax;
+                  info.missing = (int)(here ^ ((1u << kBlocks) - 1));
+                }
+              }
+              __syncwarp();
+              if (lane == 0)
+                mbar_arrive_expect_tx(&sm.raw_full[stage], (uint32_t)__popc(here) * (kKvBlock * D));
+              __syncwarp();
+              if (mine && block >= 0)
+                bulk_load(smem_u32(sm.raw[stage]) + (lane % kBlocks) * (kKvBlock * D),
+                          (kind ? w.a.cache.v : w.a.cache.k) + block * (kKvBlock * D), kKvBlock * D,
+                          &sm.raw_full[stage]);
+              ++copies;
+              if (++stage == kRaw) {
+                stage = 0;
+                phase ^= 1;
+              }
+            }
+          }
+        }
+      }
+      // copies in flight end before the CTA does, whatever ended the loop
+      for (uint32_t i = copies > kRaw ? copies - kRaw : 0; i < copies; ++i)
+        mbar_wait(&sm.raw_full[i % kRaw], (i / kRaw) & 1, nullptr, w.a.err, 0x50e);
+      __syncwarp();
+    } else if (warp == 13) {
+      // ---------------- the CTA's share of the work, run by run ----------------
+      const long long total = kv_total_units<kRows, kTokens>(w);
+      const long long share = max((total + w.ctas - 1) / w.ctas, (long long)kMinTiles);
+      const long long begin = (long long)blockIdx.x * share;
+      long long left = min(max(total - begin, 0ll), share);
+      KvCursor<kRows, kTokens> c;
+      if (left > 0) c.seek(w, begin);
+      uint32_t slot = 0, phase = 1;
+      for (bool ok = true; ok;) {
+        if (!wait(&sm.run_empty[slot], phase, 0x50b)) break;
+        const int tiles = left > 0 ? (int)min(left, (long long)(c.units - c.at)) : 0;
+        Run run{};
+        run.flags = kRunStop;
+        if (left > 0) {
+          run = Run{c.b, c.r, c.h, kPartHeld | (c.at == 0 ? kPartBegins : 0) | (c.at + tiles == c.units ? kPartEnds : 0),
+                    c.at, tiles, (int)min((long long)c.s.n * w.a.group - (long long)c.r * kRows, (long long)kRows),
+                    c.s.start, c.s.n, c.s.len, c.s.seen, 0};
+        }
+        if (lane == 0) {
+          sm.run[slot] = run;
+          mbar_arrive(&sm.run_full[slot]);
+        }
+        __syncwarp();
+        if (++slot == kRuns) {
+          slot = 0;
+          phase ^= 1;
+        }
+        ok = left > 0;
+        left -= tiles;
+        if (left > 0) c.next_item(w);
+      }
     }
-    __syncwarp();
   }
   chain_release();
   tc_fence_before();
