@@ -89,23 +89,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const Kv
   uint8_t* const ring = smem + warp * S::kRing;
   uint8_t* const first_part = smem + kWarps * S::kRing + warp * S::kPartBytes;
   KvPart* const parts = reinterpret_cast<KvPart*>(smem + kWarps * (S::kRing + S::kPartBytes));
-  if (lane < 2) parts[2 * warp + lane] = KvPart{0, 0, 0, kPartNone};
+  if (lane < 2) parts[2 * warp + lane] = KvPart{};
   chain_wait();
 
   const KvBatchArgs& batch = w.a.batch;
   const int heads = w.a.cache.heads, bpp = w.a.cache.bpp;
 
   // the line's length and this warp's blocks of it
-  const long long total = kv_total_units<S::kRows, kKvBlock>(w);
+  const long long total = kv_total_units<S::kRows, kKvBlock, 0>(w);
   const long long warps = (long long)w.ctas * kWarps;
   const long long share = max((total + warps - 1) / warps, (long long)kMinBlocks);
   const long long begin = ((long long)blockIdx.x * kWarps + warp) * share;
   const int count = (int)min(max(total - begin, 0ll), share);
 
   if (count > 0) {
-    KvCursor<S::kRows, kKvBlock> at;   // of the block that is computed
+    KvCursor<S::kRows, kKvBlock, 0> at;   // of the block that is computed
     at.seek(w, begin);
-    KvCursor<S::kRows, kKvBlock> ahead = at;   // of the block that is fetched
+    KvCursor<S::kRows, kKvBlock, 0> ahead = at;   // of the block that is fetched
     int pages = 0, page0 = 0, page_at = 0, off = 0;   // 32 entries of the table from page0, a lane each
     auto open_pages = [&](int pg) {
       page0 = pg;
@@ -382,7 +382,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const Kv
           __syncwarp();
           if (lane == 0)
             parts[2 * warp + slot] =
-                KvPart{at.b, at.r, at.h, kPartHeld | (begins ? kPartBegins : 0) | (ends ? kPartEnds : 0)};
+                KvPart{at.s.start, at.h, at.r * S::kRows, min(at.s.n * w.a.group - at.r * S::kRows, S::kRows),
+                       kPartHeld | (begins ? kPartBegins : 0) | (ends ? kPartEnds : 0)};
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -408,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const Kv
             } else {
               const int row = at.r * S::kRows + col;
               if (row < at.s.n * w.a.group) {
-                T* dst = static_cast<T*>(w.a.out) + kv_out_row(w.a, at.s, at.h, row) * D + g * (D / 8);
+                T* dst = static_cast<T*>(w.a.out) + kv_out_row(w.a, at.s.start, at.h, row) * D + g * (D / 8);
 #pragma unroll
                 for (int i = 0; i < kMT; i += 4) {
                   const float z[8] = {y[i][0],     y[i][1],     y[i + 1][0], y[i + 1][1],
@@ -431,11 +432,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const Kv
   auto part_bytes = [&](int i) -> const uint8_t* {
     return i & 1 ? smem + (i >> 1) * S::kRing : smem + kWarps * S::kRing + (i >> 1) * S::kPartBytes;
   };
-  KvPart left[2] = {{0, 0, 0, kPartNone}, {0, 0, 0, kPartNone}};   // what goes to the workspace
+  KvPart left[2] = {};   // what goes to the workspace
   int list[2 * kWarps], n = 0;
 #pragma unroll 1
   for (int i = 0; i <= 2 * kWarps; ++i) {
-    const KvPart p = i < 2 * kWarps ? parts[i] : KvPart{0, 0, 0, kPartNone};
+    const KvPart p = i < 2 * kWarps ? parts[i] : KvPart{};
     if (i < 2 * kWarps && !(p.flags & kPartHeld)) continue;
     // the run before this one ends where a part begins an item
     if (n > 0 && (i == 2 * kWarps || (p.flags & kPartBegins))) {
@@ -443,13 +444,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const Kv
       const bool whole = (a.flags & kPartBegins) && (z.flags & kPartEnds);
       const int slot = (a.flags & kPartBegins) ? 1 : 0;
       uint8_t* into = w.ws + (size_t)(2 * blockIdx.x + slot) * kv_part_bytes(D, S::kRows);
-      if (!whole) left[slot] = KvPart{a.b, a.r, a.h, kPartHeld | (a.flags & kPartBegins) | (z.flags & kPartEnds)};
-      KvSeq s{};
-      if (whole) s = kv_sequence(batch, a.b);
-      for (int row = warp; row < S::kRows; row += kWarps) {
+      if (!whole) {
+        left[slot] = a;
+        left[slot].flags = kPartHeld | (a.flags & kPartBegins) | (z.flags & kPartEnds);
+      }
+      for (int row = warp; row < a.rows; row += kWarps) {
         T* out = nullptr;
-        if (whole && a.r * S::kRows + row < s.n * w.a.group)
-          out = static_cast<T*>(w.a.out) + kv_out_row(w.a, s, a.h, a.r * S::kRows + row) * D;
+        if (whole) out = static_cast<T*>(w.a.out) + kv_out_row(w.a, a.start, a.h, a.first + row) * D;
         kv_join_row<D, T>(n, S::kRows, row, [&](int j) { return part_bytes(list[j]); }, whole, out, into);
       }
       n = 0;

@@ -13,8 +13,10 @@ constexpr float kKvSlack = 8.f;        // how far a score may pass the running m
 
 // A part of an item that one warp (in shared memory) or one CTA (in the workspace) holds.
 enum { kPartNone = 0, kPartHeld = 1, kPartBegins = 2, kPartEnds = 4 };
-struct KvPart {
-  int b, r, h, flags;
+struct alignas(16) KvPart {
+  int start, h;       // the sequence's first packed row, the key head
+  int first, rows;    // the tile's first row (of those of one key head) and how many it has
+  int flags, pad[3];
 };
 
 __host__ __device__ constexpr size_t kv_part_bytes(int dim, int rows) { return (size_t)rows * (dim + 2) * 4; }
@@ -35,13 +37,15 @@ struct KvWork {
 
 // The kernels cut the work of a call alike: all (sequence, tile of R rows, key head)
 // items end to end in units of TK tokens, and to each worker the same number of
-// consecutive units, wherever items begin and end.
+// consecutive units, wherever items begin and end. The first E units of an item stand
+// for what an item costs beside its tokens, and hold none.
 
-// The units of one row tile: at least one, so that rows that see nothing are written.
-template <int R, int TK>
+// The units of one row tile: at least one of tokens, so that rows that see nothing are
+// written.
+template <int R, int TK, int E>
 __device__ __forceinline__ int kv_tile_units(const KvWork& w, const KvSeq& s, int r) {
-  const int last = min((int)(((long long)(r + 1) * R - 1) / w.a.group), s.n - 1);
-  return max((int)(((long long)kv_visible(s, last, w.a.causal) + TK - 1) / TK), 1);
+  const int last = min((int)(((unsigned)(r + 1) * R - 1) / (unsigned)w.a.group), s.n - 1);
+  return max((kv_visible(s, last, w.a.causal) + (TK - 1u)) / TK, 1u) + E;
 }
 template <int R>
 __device__ __forceinline__ int kv_tile_count(const KvWork& w, const KvSeq& s) {
@@ -51,7 +55,7 @@ __device__ __forceinline__ int kv_tile_count(const KvWork& w, const KvSeq& s) {
 
 // The units of sequence b, another one in each lane; a whole warp calls. A sequence of
 // many row tiles is summed by all lanes.
-template <int R, int TK>
+template <int R, int TK, int E>
 __device__ __forceinline__ long long kv_sequence_units(const KvWork& w, int b) {
   const int lane = threadIdx.x & 31;
   KvSeq s{};
@@ -62,7 +66,7 @@ __device__ __forceinline__ long long kv_sequence_units(const KvWork& w, int b) {
   }
   long long sum = 0;
   if (tiles <= 2)
-    for (int r = 0; r < tiles; ++r) sum += kv_tile_units<R, TK>(w, s, r);
+    for (int r = 0; r < tiles; ++r) sum += kv_tile_units<R, TK, E>(w, s, r);
   for (unsigned many = __ballot_sync(~0u, tiles > 2); many; many &= many - 1) {
     const int l = __ffs(many) - 1;
     KvSeq o{};
@@ -71,18 +75,18 @@ __device__ __forceinline__ long long kv_sequence_units(const KvWork& w, int b) {
     o.seen = __shfl_sync(~0u, s.seen, l);
     const int count = __shfl_sync(~0u, tiles, l);
     long long all = 0;
-    for (int r = lane; r < count; r += 32) all += kv_tile_units<R, TK>(w, o, r);
+    for (int r = lane; r < count; r += 32) all += kv_tile_units<R, TK, E>(w, o, r);
 #pragma unroll
     for (int d = 16; d; d >>= 1) all += __shfl_xor_sync(~0u, all, d);
     if (lane == l) sum = all;
   }
   return sum * w.a.cache.heads;
 }
-template <int R, int TK>
+template <int R, int TK, int E>
 __device__ __forceinline__ long long kv_total_units(const KvWork& w) {
   const int lane = threadIdx.x & 31;
   long long total = 0;
-  for (int b0 = 0; b0 < w.a.batch.batch; b0 += 32) total += kv_sequence_units<R, TK>(w, b0 + lane);
+  for (int b0 = 0; b0 < w.a.batch.batch; b0 += 32) total += kv_sequence_units<R, TK, E>(w, b0 + lane);
 #pragma unroll
   for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
   return total;
@@ -105,7 +109,7 @@ __device__ __forceinline__ int kv_prefix_find(long long mine, long long at, long
 }
 
 // A place in the line of units.
-template <int R, int TK>
+template <int R, int TK, int E>
 struct KvCursor {
   int b, r, h, at, units, tiles;   // unit `at` of `units` of the item (b, r, h)
   KvSeq s;
@@ -116,7 +120,7 @@ struct KvCursor {
     b = 0;
     for (int b0 = 0; b0 < w.a.batch.batch; b0 += 32) {
       long long before;
-      const int l = kv_prefix_find(kv_sequence_units<R, TK>(w, b0 + lane), place, before);
+      const int l = kv_prefix_find(kv_sequence_units<R, TK, E>(w, b0 + lane), place, before);
       place -= before;
       if (l >= 0) {
         b = b0 + l;
@@ -128,7 +132,7 @@ struct KvCursor {
     r = 0;
     for (int r0 = 0; r0 < tiles; r0 += 32) {
       long long before;
-      const long long mine = r0 + lane < tiles ? (long long)kv_tile_units<R, TK>(w, s, r0 + lane) * w.a.cache.heads : 0;
+      const long long mine = r0 + lane < tiles ? (long long)kv_tile_units<R, TK, E>(w, s, r0 + lane) * w.a.cache.heads : 0;
       const int l = kv_prefix_find(mine, place, before);
       place -= before;
       if (l >= 0) {
@@ -136,9 +140,9 @@ struct KvCursor {
         break;
       }
     }
-    units = kv_tile_units<R, TK>(w, s, r);
-    h = (int)(place / units);
-    at = (int)(place % units);
+    units = kv_tile_units<R, TK, E>(w, s, r);
+    h = place >> 32 ? (int)(place / units) : (int)((unsigned)place / (unsigned)units);
+    at = (int)(place - (long long)h * units);
   }
   // To the next item's first unit.
   __device__ void next_item(const KvWork& w) {
@@ -153,14 +157,16 @@ struct KvCursor {
         tiles = kv_tile_count<R>(w, s);
       } while (tiles == 0);
     }
-    units = kv_tile_units<R, TK>(w, s, r);
+    units = kv_tile_units<R, TK, E>(w, s, r);
   }
 };
 
-// Where rows of an item go: rows are (token, query head of the group), token major.
-__device__ __forceinline__ long long kv_out_row(const KvAttentionArgs& a, const KvSeq& s, int h, int row) {
-  return (long long)(s.start + row / a.group) * ((long long)a.cache.heads * a.group) + (long long)h * a.group +
-         row % a.group;
+// Where a row goes: a sequence's rows of a key head are (token, query head of the
+// group), token major.
+__device__ __forceinline__ long long kv_out_row(const KvAttentionArgs& a, int start, int h, int row) {
+  const int token = (unsigned)row / (unsigned)a.group;
+  return (long long)(start + token) * ((long long)a.cache.heads * a.group) + (long long)h * a.group +
+         (row - token * a.group);
 }
 
 // Parts [first, first + count) of one item joined, one row by one warp: rows of O that
@@ -171,24 +177,43 @@ template <int D, typename T, typename F>
 __device__ __forceinline__ void kv_join_row(int count, int rows, int row, F part, bool whole, T* out, uint8_t* into) {
   constexpr int kE = D / 32;
   const int lane = threadIdx.x & 31;
-  float top = kKvNone;
-  for (int i = lane; i < count; i += 32)
-    top = fmaxf(top, reinterpret_cast<const float2*>(part(i) + rows * D * 4)[row].x);
+  float top = kKvNone, sum = 0.f, acc[kE] = {};
+  constexpr int kAhead = 4;   // parts loaded together
+#pragma unroll 1
+  for (int i0 = 0; i0 < count; i0 += kAhead) {
+    float2 ml[kAhead];
+    float x[kAhead][kE];
 #pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-  float sum = 0.f, acc[kE] = {};
-#pragma unroll 4
-  for (int i = 0; i < count; ++i) {
-    const uint8_t* p = part(i);
-    const float2 ml = reinterpret_cast<const float2*>(p + rows * D * 4)[row];
-    const float weight = ml.y * exp2f(ml.x - top);
-    sum += weight;
-    if constexpr (kE == 4) {
-      const float4 x = reinterpret_cast<const float4*>(p)[row * 32 + lane];
-      acc[0] += weight * x.x; acc[1] += weight * x.y; acc[2] += weight * x.z; acc[3] += weight * x.w;
-    } else {
-      const float2 x = reinterpret_cast<const float2*>(p)[row * 32 + lane];
-      acc[0] += weight * x.x; acc[1] += weight * x.y;
+    for (int j = 0; j < kAhead; ++j) {
+      ml[j] = make_float2(kKvNone, 0.f);
+#pragma unroll
+      for (int e = 0; e < kE; ++e) x[j][e] = 0.f;
+      if (i0 + j < count) {
+        const uint8_t* p = part(i0 + j);
+        ml[j] = reinterpret_cast<const float2*>(p + rows * D * 4)[row];
+        if constexpr (kE == 4) {
+          const float4 v = reinterpret_cast<const float4*>(p)[row * 32 + lane];
+          x[j][0] = v.x; x[j][1] = v.y; x[j][2] = v.z; x[j][3] = v.w;
+        } else {
+          const float2 v = reinterpret_cast<const float2*>(p)[row * 32 + lane];
+          x[j][0] = v.x; x[j][1] = v.y;
+        }
+      }
+    }
+    float up = top;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) up = fmaxf(up, ml[j].x);
+    const float down = exp2f(top - up);
+    top = up;
+    sum *= down;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) acc[e] *= down;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const float weight = ml[j].y * exp2f(ml[j].x - top);
+      sum += weight;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) acc[e] += weight * x[j][e];
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -242,18 +267,15 @@ __global__ void __launch_bounds__(256) kv_attention_join_kernel(const KvWork w) 
     n += 32;
   }
   n = min(n, w.ctas - (int)blockIdx.x);
-  const KvSeq s = kv_sequence(w.a.batch, a.b);
   chain_release();
   auto part = [&](int j) -> const uint8_t* {
     return w.ws + (size_t)(j == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + j)) * kv_part_bytes(D, R);
   };
-  for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < R; row += 8 * gridDim.y) {
-    if (a.r * R + row >= s.n * w.a.group) break;
-    T* out = static_cast<T*>(w.a.out) + kv_out_row(w.a, s, a.h, a.r * R + row) * D;
+  for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < a.rows; row += 8 * gridDim.y) {
+    T* out = static_cast<T*>(w.a.out) + kv_out_row(w.a, a.start, a.h, a.first + row) * D;
     kv_join_row<D, T>(n, R, row, part, true, out, nullptr);
   }
 }
-
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float r;

@@ -35,7 +35,8 @@ constexpr int kStages = 3;                 // operands (K or V tiles) in the rin
 constexpr int kRaw = 4;                    // and in the ring of int8 before it
 constexpr int kInfo = 4;                   // tiles whose scales are kept
 constexpr int kBlocks = kTokens / kKvBlock;
-constexpr int kMinTiles = 2;               // a CTA's share, at least
+constexpr int kSetup = 8;                  // units that stand for what an item costs beside its tiles
+constexpr int kMinUnits = kSetup + 2;      // a CTA's share, at least
 constexpr float kLift = 7.f;               // P is held times 2^7: at most 2^15
 
 // What the softmax needs to know of a tile's blocks.
@@ -166,61 +167,85 @@ __device__ __forceinline__ void tmem_ld128(uint32_t t, uint32_t (&r)[128]) {
   tmem_ld32x2(t + 64, c, t + 96, d);
 }
 
-// The row of Q that a softmax thread owns: scaled by a power of two that puts its
-// largest magnitude into [2^14, 2^15), where fp16 holds bfloat16 exactly down to 2^-24
-// of it, and by the sign of the scale; into the thread's row of shared memory.
+// The rows of Q of a softmax warp's 32 threads, a row each. They are fetched with
+// neighbouring lanes on neighbouring 16 bytes (a lane a row would ask for 32 lines at a
+// time, and take 8000 cycles of the L1 cache for the CTA's 64 KB) and stored into the
+// operand's rows, scaled by a power of two each that puts a row's largest magnitude
+// into [2^14, 2^15), where fp16 holds bfloat16 exactly down to 2^-24 of it, and by the
+// sign of the scale.
 struct Row {
   float coef;    // scores: coef * 2^(byte - 127) * S
   int limit;     // tokens that the row sees; INT_MAX for a row that is not there
 };
+template <int D>
+struct Fetched {
+  static constexpr int kLanes = D / 8;           // of a row
+  static constexpr int kAtOnce = 32 / kLanes;    // rows
+  static constexpr int kLoads = D / 8;
+  uint4 x[kLoads];
+};
 template <int D, bool kVec>
-__device__ __forceinline__ Row load_row(const KvWork& w, const Run& run, int tile, int row, uint8_t* q) {
-  const int rr = run.r * kRows + tile * 128 + row;
-  const bool there = tile * 128 + row < run.rows;
-  Row out{1.f, INT_MAX};
-  const uint32_t dst = smem_u32(q) + (uint32_t)row * 128u;
-  const int swz = row & 7;
-  if (!there) {
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) st_shared_v4(dst + (i >> 3) * 16384 + (((i & 7) ^ swz) << 4), 0, 0, 0, 0);
-    return out;
+__device__ __forceinline__ void fetch_rows(const KvWork& w, const Run& run, int first, Fetched<D>& f) {
+  using F = Fetched<D>;
+  const int lane = threadIdx.x & 31;
+  // this lane's own row
+  long long mine = -1;
+  if (first + lane < run.rows) {
+    const int rr = run.r * kRows + first + lane, token = (unsigned)rr / (unsigned)w.a.group;
+    mine = (long long)(run.start + token) * w.a.q_row +
+           ((long long)run.h * w.a.group + (rr - token * w.a.group)) * w.a.q_head;
   }
-  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(w.a.q) +
-                             (long long)(run.start + rr / w.a.group) * w.a.q_row +
-                             (long long)(run.h * w.a.group + rr % w.a.group) * w.a.q_head;
-  uint32_t x[D / 2];
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) {
-    if constexpr (kVec) {
-      const uint4 u = reinterpret_cast<const uint4*>(src)[i];
-      x[4 * i] = u.x; x[4 * i + 1] = u.y; x[4 * i + 2] = u.z; x[4 * i + 3] = u.w;
-    } else {
-      const unsigned short* p = reinterpret_cast<const unsigned short*>(src) + 8 * i;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[4 * i + e] = p[2 * e] | ((uint32_t)p[2 * e + 1] << 16);
+  for (int i = 0; i < F::kLoads; ++i) {
+    const long long at = __shfl_sync(~0u, mine, i * F::kAtOnce + lane / F::kLanes);
+    f.x[i] = make_uint4(0, 0, 0, 0);
+    if (at >= 0) {
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(w.a.q) + at + lane % F::kLanes * 8;
+      if constexpr (kVec) {
+        f.x[i] = *reinterpret_cast<const uint4*>(src);
+      } else {
+        const unsigned short* p = reinterpret_cast<const unsigned short*>(src);
+        f.x[i] = make_uint4(p[0] | ((uint32_t)p[1] << 16), p[2] | ((uint32_t)p[3] << 16), p[4] | ((uint32_t)p[5] << 16),
+                            p[6] | ((uint32_t)p[7] << 16));
+      }
     }
   }
-  uint32_t top = 0;   // magnitudes compare as integers; a NaN is above an infinity
-#pragma unroll
-  for (int i = 0; i < D / 2; ++i) top = max(top, max(x[i] << 16 & 0x7fff0000u, x[i] & 0x7fff0000u));
-  const bool bad = top >= 0x7f800000u;
-  const int e = min(max((int)(top >> 23), 27), 254);
+}
+// `q`: the operand's first row of the warp.
+template <int D>
+__device__ __forceinline__ Row store_rows(const KvWork& w, const Run& run, int first, const Fetched<D>& f, uint32_t q) {
+  using F = Fetched<D>;
+  const int lane = threadIdx.x & 31, piece = lane % F::kLanes;
+  Row out{1.f, INT_MAX};
   const float scale = w.a.scale;
-  float up = __int_as_float((127 + 14 + 127 - e) << 23);
-  if (scale < 0.f) up = -up;
-  if (scale == 0.f) up = 0.f;
-  if (scale != 0.f) out.coef = fabsf(scale) * 1.4426950408889634f * __int_as_float((e - 14) << 23);
-  out.limit = kv_visible(KvSeq{0, run.n, run.len, run.seen}, rr / w.a.group, w.a.causal);
+  uint32_t own = 0;   // the largest magnitude of this lane's row
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) {
+  for (int i = 0; i < F::kLoads; ++i) {
+    const uint32_t x[4] = {f.x[i].x, f.x[i].y, f.x[i].z, f.x[i].w};
+    uint32_t top = 0;   // magnitudes compare as integers; a NaN is above an infinity
+#pragma unroll
+    for (int e = 0; e < 4; ++e) top = max(top, max(x[e] << 16 & 0x7fff0000u, x[e] & 0x7fff0000u));
+#pragma unroll
+    for (int o = F::kLanes / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
+    const uint32_t theirs = __shfl_sync(~0u, top, lane % F::kAtOnce * F::kLanes);
+    if (lane / F::kAtOnce == i) own = theirs;
+    const bool bad = top >= 0x7f800000u;
+    const int e2 = min(max((int)(top >> 23), 27), 254);
+    float up = __int_as_float((127 + 14 + 127 - e2) << 23);
+    up = scale < 0.f ? -up : scale == 0.f ? 0.f : up;
     uint32_t u[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t v = x[4 * i + k];
-      u[k] = bad ? 0x7e007e00u : half_pair(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up);
-    }
-    st_shared_v4(dst + (i >> 3) * 16384 + (((i & 7) ^ swz) << 4), u[0], u[1], u[2], u[3]);
+    for (int e = 0; e < 4; ++e)
+      u[e] = bad ? 0x7e007e00u : half_pair(__uint_as_float(x[e] << 16) * up, __uint_as_float(x[e] & 0xffff0000u) * up);
+    const int row = i * F::kAtOnce + lane / F::kLanes;
+    st_shared_v4(q + (uint32_t)(piece >> 3) * 16384u + (uint32_t)row * 128u + (((piece & 7) ^ (row & 7)) << 4), u[0],
+                 u[1], u[2], u[3]);
   }
+  if (scale != 0.f)
+    out.coef = fabsf(scale) * 1.4426950408889634f * __int_as_float((min(max((int)(own >> 23), 27), 254) - 14) << 23);
+  if (first + lane < run.rows)
+    out.limit = kv_visible(KvSeq{0, run.n, run.len, run.seen},
+                           (unsigned)(run.r * kRows + first + lane) / (unsigned)w.a.group, w.a.causal);
   return out;
 }
 
@@ -286,25 +311,30 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
   if (warp < 8) {
     // ---------------- softmax: a row a thread ----------------
     more_registers<kSoftmaxRegs>();
-    const int x = warp >> 2, row = threadIdx.x & 127;
+    const int x = warp >> 2;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;     // 32 lanes a warp, in bits 16 and up
     // scores (and P) of the two tiles in columns 0 and 128, O in 256 and 384
     const uint32_t s_tmem = tmem + lanes + x * 128, o_tmem = s_tmem + 256;
-    KvPart left0{0, 0, 0, kPartNone}, left1{0, 0, 0, kPartNone};
+    KvPart left0{}, left1{};
     uint32_t s_phase = 0, o_phase = 0;
     int tile = 0;            // tiles of the CTA before the run
     bool ok = true;
     Run now{};
     Row me{1.f, INT_MAX};
-    auto put_row = [&] {
-      if (x && now.rows <= 128) return;
-      me = load_row<D, kVec>(w, now, x, row, sm.q + x * kQTile);
+    const int first = x * 128 + (warp & 3) * 32;   // the warp's first row
+    const uint32_t q_rows = smem_u32(sm.q) + x * kQTile + (warp & 3) * 32 * 128;
+    Fetched<D> rows;
+    auto put_rows = [&] {
+      me = store_rows<D>(w, now, first, rows, q_rows);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.q_full[x]);
     };
     bool more = next_run(now);
-    if (more) put_row();
+    if (more && (!x || now.rows > 128)) {
+      fetch_rows<D, kVec>(w, now, first, rows);
+      put_rows();
+    }
     while (more) {
       const bool mine = !x || now.rows > 128;
       float m = kKvNone, l = 0.f;
@@ -390,51 +420,76 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
       }
       tile += now.tiles;
       if (!ok) break;
-      // the next run's rows, under the last products of this one
+      // the next run's rows come under the last products of this one
       const Run was = now;
       more = next_run(now);
-      if (more) put_row();
+      const bool next = more && (!x || now.rows > 128);
+      fetch_rows<D, kVec>(w, now, next ? first : kRows, rows);   // none: so that nothing is kept through a run
       const bool whole = (was.flags & kPartBegins) && (was.flags & kPartEnds);
       const int slot = was.flags & kPartBegins ? 1 : 0;
-      if (!whole) (slot ? left1 : left0) = KvPart{was.b, was.r, was.h, was.flags};
+      if (!whole) (slot ? left1 : left0) = KvPart{was.start, was.h, was.r * kRows, was.rows, was.flags};
       if (mine) {
         if (!(ok = wait(&sm.o_full[x], o_phase, 0x502))) break;
         o_phase ^= 1;
         tc_fence_after();
+        // O by way of this warp's rows of Q, whose last use is over, so that neighbouring lanes write neighbouring
+        // bytes: 256 bytes of each row at a time, as bfloat16 or, of a part, as float32
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const float vscale = kv_power(vref);
-        __nv_bfloat16* dst = nullptr;
-        float* into = nullptr;
-        if (whole) {
-          if (x * 128 + row < was.rows)
-            dst = static_cast<__nv_bfloat16*>(w.a.out) +
-                  kv_out_row(w.a, KvSeq{was.start, was.n, was.len, was.seen}, was.h, was.r * kRows + x * 128 + row) * D;
-        } else {
-          into = reinterpret_cast<float*>(w.ws + (size_t)(2 * blockIdx.x + slot) * kv_part_bytes(D, kRows));
-          reinterpret_cast<float2*>(into + kRows * D)[x * 128 + row] = make_float2(m, l);
-          into += (x * 128 + row) * D;
-        }
+        uint8_t* const part = w.ws + (size_t)(2 * blockIdx.x + slot) * kv_part_bytes(D, kRows);
+        if (!whole) reinterpret_cast<float2*>(part + kRows * D * 4)[first + lane] = make_float2(m, l);
+        const int step = whole ? D : D / 2;                // columns at a time: 2 D bytes of a row
+        long long to = -1;                                 // where this lane's row goes, in elements of 2 D bytes
+        if (first + lane < was.rows)
+          to = whole ? kv_out_row(w.a, was.start, was.h, was.r * kRows + first + lane) : 2 * (first + lane);
+        uint8_t* const base = whole ? static_cast<uint8_t*>(w.a.out) : part;
+        constexpr int kPieces = D / 8;                     // of 16 bytes, of 2 D bytes
+        const uint32_t mine_at = q_rows + (uint32_t)lane * 128u;
 #pragma unroll 1
-        for (int i = 0; i < D; i += 32) {
-          uint32_t o[32];
-          tmem_ld32(o_tmem + i, o);
-          float y[32];
+        for (int col = 0; col < D; col += step) {
+#pragma unroll 1
+          for (int i = 0; i < step; i += 16) {
+            uint32_t o[16];
+            tmem_ld16(o_tmem + col + i, o);
+            float y[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(o[e]) * inv * vscale;
-          if (dst) {
+            for (int e = 0; e < 16; ++e) y[e] = __uint_as_float(o[e]) * inv * vscale;
+            // piece p of the row: panel p / 8, place p % 8 exchanged by the row
+            auto put = [&](int p, uint32_t u0, uint32_t u1, uint32_t u2, uint32_t u3) {
+              st_shared_v4(mine_at + (uint32_t)(p >> 3) * 16384u + (((p & 7) ^ (lane & 7)) << 4), u0, u1, u2, u3);
+            };
+            if (whole) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              const float z[8] = {y[e], y[e + 1], y[e + 2], y[e + 3], y[e + 4], y[e + 5], y[e + 6], y[e + 7]};
-              kv_store8(dst + i + e, z);
+              for (int e = 0; e < 16; e += 8) {
+                uint32_t u[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const __nv_bfloat162 h = __floats2bfloat162_rn(y[e + 2 * k], y[e + 2 * k + 1]);
+                  u[k] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+                put((i + e) / 8, u[0], u[1], u[2], u[3]);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; e += 4)
+                put((i + e) / 4, __float_as_uint(y[e]), __float_as_uint(y[e + 1]), __float_as_uint(y[e + 2]),
+                    __float_as_uint(y[e + 3]));
             }
-          } else if (into) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(into + i + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
           }
+          __syncwarp();
+#pragma unroll 4
+          for (int i = 0; i < kPieces; ++i) {
+            const int row = i * (32 / kPieces) + lane / kPieces, p = lane % kPieces;
+            const long long at = __shfl_sync(~0u, to, row);
+            const uint4 v = ld_shared_v4(q_rows + (uint32_t)(p >> 3) * 16384u + (uint32_t)row * 128u +
+                                         (((p & 7) ^ (row & 7)) << 4));
+            if (at >= 0) *reinterpret_cast<uint4*>(base + (at + (col > 0)) * (2 * D) + p * 16) = v;
+          }
+          __syncwarp();
         }
         tc_fence_before();
       }
+      if (next) put_rows();
     }
     if (threadIdx.x == 0) {
       w.parts[2 * blockIdx.x] = left0;
@@ -638,34 +693,39 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
       __syncwarp();
     } else if (warp == 13) {
       // ---------------- the CTA's share of the work, run by run ----------------
-      const long long total = kv_total_units<kRows, kTokens>(w);
-      const long long share = max((total + w.ctas - 1) / w.ctas, (long long)kMinTiles);
+      const long long total = kv_total_units<kRows, kTokens, kSetup>(w);
+      const long long share = max((total + w.ctas - 1) / w.ctas, (long long)kMinUnits);
       const long long begin = (long long)blockIdx.x * share;
       long long left = min(max(total - begin, 0ll), share);
-      KvCursor<kRows, kTokens> c;
+      KvCursor<kRows, kTokens, kSetup> c{};
       if (left > 0) c.seek(w, begin);
       uint32_t slot = 0, phase = 1;
-      for (bool ok = true; ok;) {
-        if (!wait(&sm.run_empty[slot], phase, 0x50b)) break;
-        const int tiles = left > 0 ? (int)min(left, (long long)(c.units - c.at)) : 0;
-        Run run{};
-        run.flags = kRunStop;
-        if (left > 0) {
-          run = Run{c.b, c.r, c.h, kPartHeld | (c.at == 0 ? kPartBegins : 0) | (c.at + tiles == c.units ? kPartEnds : 0),
-                    c.at, tiles, (int)min((long long)c.s.n * w.a.group - (long long)c.r * kRows, (long long)kRows),
-                    c.s.start, c.s.n, c.s.len, c.s.seen, 0};
+      for (;;) {
+        // the tiles of this stretch of units, if it has any
+        const int units = left > 0 ? (int)min(left, (long long)(c.units - c.at)) : 0;
+        const int from = max(c.at - kSetup, 0), tiles = max(c.at + units - kSetup, 0) - from;
+        const bool end = left <= 0;
+        if (end || tiles > 0) {
+          if (!wait(&sm.run_empty[slot], phase, 0x50b)) break;
+          if (lane == 0) {
+            Run run{};
+            run.flags = kRunStop;
+            if (!end) {
+              run = Run{c.b, c.r, c.h,
+                        kPartHeld | (from == 0 ? kPartBegins : 0) | (c.at + units == c.units ? kPartEnds : 0), from, tiles,
+                        min(c.s.n * w.a.group - c.r * kRows, kRows), c.s.start, c.s.n, c.s.len, c.s.seen, 0};
+            }
+            sm.run[slot] = run;
+            mbar_arrive(&sm.run_full[slot]);
+          }
+          __syncwarp();
+          if (++slot == kRuns) {
+            slot = 0;
+            phase ^= 1;
+          }
+          if (end) break;
         }
-        if (lane == 0) {
-          sm.run[slot] = run;
-          mbar_arrive(&sm.run_full[slot]);
-        }
-        __syncwarp();
-        if (++slot == kRuns) {
-          slot = 0;
-          phase ^= 1;
-        }
-        ok = left > 0;
-        left -= tiles;
+        left -= units;
         if (left > 0) c.next_item(w);
       }
     }
@@ -686,7 +746,7 @@ cudaError_t tiles_sized(const KvWork& w, bool vec, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = launch_chained(kern, dim3(w.ctas), dim3(kThreads), bytes, 1, s, w);
   if (e != cudaSuccess) return e;
-  return launch_chained(&kv_attention_join_kernel<D, kRows, __nv_bfloat16>, dim3(w.ctas, 8), dim3(256), 0, 1, s, w);
+  return launch_chained(&kv_attention_join_kernel<D, kRows, __nv_bfloat16>, dim3(w.ctas, 16), dim3(256), 0, 1, s, w);
 }
 
 }  // namespace
