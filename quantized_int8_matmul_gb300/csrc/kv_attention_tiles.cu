@@ -35,7 +35,7 @@ constexpr int kStages = 3;                 // operands (K or V tiles) in the rin
 constexpr int kRaw = 4;                    // and in the ring of int8 before it
 constexpr int kInfo = 4;                   // tiles whose scales are kept
 constexpr int kBlocks = kTokens / kKvBlock;
-constexpr int kSetup = 8;                  // units that stand for what an item costs beside its tiles
+constexpr int kSetup = 5;                  // units that stand for what an item costs beside its tiles
 constexpr int kMinUnits = kSetup + 2;      // a CTA's share, at least
 constexpr float kLift = 7.f;               // P is held times 2^7: at most 2^15
 
@@ -167,82 +167,90 @@ __device__ __forceinline__ void tmem_ld128(uint32_t t, uint32_t (&r)[128]) {
   tmem_ld32x2(t + 64, c, t + 96, d);
 }
 
-// The rows of Q of a softmax warp's 32 threads, a row each. They are fetched with
-// neighbouring lanes on neighbouring 16 bytes (a lane a row would ask for 32 lines at a
-// time, and take 8000 cycles of the L1 cache for the CTA's 64 KB) and stored into the
-// operand's rows, scaled by a power of two each that puts a row's largest magnitude
-// into [2^14, 2^15), where fp16 holds bfloat16 exactly down to 2^-24 of it, and by the
-// sign of the scale.
+// Rows of a tile in steps: row rr is query head rr % group of token rr / group.
+struct Walk {
+  int token, head;
+  int tokens, heads, group;   // a step
+  __device__ Walk(int rr, int step, int g) : group(g) {
+    token = (unsigned)rr / (unsigned)g;
+    head = rr - token * g;
+    tokens = (unsigned)step / (unsigned)g;
+    heads = step - tokens * g;
+  }
+  __device__ void next() {
+    token += tokens;
+    head += heads;
+    if (head >= group) {
+      head -= group;
+      ++token;
+    }
+  }
+};
+
+// The rows of Q of a softmax warp's 32 threads, a row each. They come with neighbouring
+// lanes on neighbouring 16 bytes (a lane a row would ask for 32 lines at a time, and
+// take 8000 cycles of the L1 cache for the CTA's 64 KB), straight into the operand's
+// rows (`q`: the warp's first), and are converted there: scaled by a power of two each
+// that puts a row's largest magnitude into [2^14, 2^15), where fp16 holds bfloat16
+// exactly down to 2^-24 of it, and by the sign of the scale.
 struct Row {
   float coef;    // scores: coef * 2^(byte - 127) * S
   int limit;     // tokens that the row sees; INT_MAX for a row that is not there
 };
-template <int D>
-struct Fetched {
-  static constexpr int kLanes = D / 8;           // of a row
-  static constexpr int kAtOnce = 32 / kLanes;    // rows
-  static constexpr int kLoads = D / 8;
-  uint4 x[kLoads];
-};
 template <int D, bool kVec>
-__device__ __forceinline__ void fetch_rows(const KvWork& w, const Run& run, int first, Fetched<D>& f) {
-  using F = Fetched<D>;
+__device__ __forceinline__ Row load_rows(const KvWork& w, const Run& run, int first, uint32_t q) {
   const int lane = threadIdx.x & 31;
-  // this lane's own row
-  long long mine = -1;
-  if (first + lane < run.rows) {
-    const int rr = run.r * kRows + first + lane, token = (unsigned)rr / (unsigned)w.a.group;
-    mine = (long long)(run.start + token) * w.a.q_row +
-           ((long long)run.h * w.a.group + (rr - token * w.a.group)) * w.a.q_head;
-  }
-#pragma unroll
-  for (int i = 0; i < F::kLoads; ++i) {
-    const long long at = __shfl_sync(~0u, mine, i * F::kAtOnce + lane / F::kLanes);
-    f.x[i] = make_uint4(0, 0, 0, 0);
-    if (at >= 0) {
-      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(w.a.q) + at + lane % F::kLanes * 8;
-      if constexpr (kVec) {
-        f.x[i] = *reinterpret_cast<const uint4*>(src);
+  constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;   // of a row; rows
+  const int piece = lane % kLanes;
+  {
+    int row = lane / kLanes;
+    Walk walk(run.r * kRows + first + row, kAtOnce, w.a.group);
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(w.a.q) + (long long)run.start * w.a.q_row +
+                               (long long)run.h * w.a.group * w.a.q_head + piece * 8;
+#pragma unroll 4
+    for (int i = 0; i < 32 / kAtOnce; ++i, row += kAtOnce, walk.next()) {
+      const uint32_t dst = q + (uint32_t)(piece >> 3) * 16384u + (uint32_t)row * 128u + (((piece & 7) ^ (row & 7)) << 4);
+      const __nv_bfloat16* at = src + walk.token * w.a.q_row + walk.head * w.a.q_head;
+      if (first + row >= run.rows) {
+        st_shared_v4(dst, 0, 0, 0, 0);
+      } else if constexpr (kVec) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(at) : "memory");
       } else {
-        const unsigned short* p = reinterpret_cast<const unsigned short*>(src);
-        f.x[i] = make_uint4(p[0] | ((uint32_t)p[1] << 16), p[2] | ((uint32_t)p[3] << 16), p[4] | ((uint32_t)p[5] << 16),
-                            p[6] | ((uint32_t)p[7] << 16));
+        const unsigned short* p = reinterpret_cast<const unsigned short*>(at);
+        st_shared_v4(dst, p[0] | ((uint32_t)p[1] << 16), p[2] | ((uint32_t)p[3] << 16), p[4] | ((uint32_t)p[5] << 16),
+                     p[6] | ((uint32_t)p[7] << 16));
       }
     }
+    if constexpr (kVec) asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
   }
-}
-// `q`: the operand's first row of the warp.
-template <int D>
-__device__ __forceinline__ Row store_rows(const KvWork& w, const Run& run, int first, const Fetched<D>& f, uint32_t q) {
-  using F = Fetched<D>;
-  const int lane = threadIdx.x & 31, piece = lane % F::kLanes;
-  Row out{1.f, INT_MAX};
+  const uint32_t mine = q + (uint32_t)lane * 128u, swz = (uint32_t)(lane & 7) << 4;
+  auto place = [&](int i) { return mine + (uint32_t)(i >> 3) * 16384u + (((uint32_t)(i & 7) << 4) ^ swz); };
+  uint32_t tops = 0;   // magnitudes compare as integers, two at a time; a NaN is above an infinity
+#pragma unroll 4
+  for (int i = 0; i < D / 8; ++i) {
+    const uint4 x = ld_shared_v4(place(i));
+    tops = __vmaxu2(__vmaxu2(tops, __vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu)),
+                    __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+  }
+  const uint32_t top = max(tops & 0xffffu, tops >> 16) << 16;
+  const bool bad = top >= 0x7f800000u;
+  const int e = min(max((int)(top >> 23), 27), 254);
   const float scale = w.a.scale;
-  uint32_t own = 0;   // the largest magnitude of this lane's row
+  float up = __int_as_float((127 + 14 + 127 - e) << 23);
+  up = scale < 0.f ? -up : scale == 0.f ? 0.f : up;
+#pragma unroll 4
+  for (int i = 0; i < D / 8; ++i) {
+    const uint4 x = ld_shared_v4(place(i));
+    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+    uint32_t y[4];
 #pragma unroll
-  for (int i = 0; i < F::kLoads; ++i) {
-    const uint32_t x[4] = {f.x[i].x, f.x[i].y, f.x[i].z, f.x[i].w};
-    uint32_t top = 0;   // magnitudes compare as integers; a NaN is above an infinity
-#pragma unroll
-    for (int e = 0; e < 4; ++e) top = max(top, max(x[e] << 16 & 0x7fff0000u, x[e] & 0x7fff0000u));
-#pragma unroll
-    for (int o = F::kLanes / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
-    const uint32_t theirs = __shfl_sync(~0u, top, lane % F::kAtOnce * F::kLanes);
-    if (lane / F::kAtOnce == i) own = theirs;
-    const bool bad = top >= 0x7f800000u;
-    const int e2 = min(max((int)(top >> 23), 27), 254);
-    float up = __int_as_float((127 + 14 + 127 - e2) << 23);
-    up = scale < 0.f ? -up : scale == 0.f ? 0.f : up;
-    uint32_t u[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      u[e] = bad ? 0x7e007e00u : half_pair(__uint_as_float(x[e] << 16) * up, __uint_as_float(x[e] & 0xffff0000u) * up);
-    const int row = i * F::kAtOnce + lane / F::kLanes;
-    st_shared_v4(q + (uint32_t)(piece >> 3) * 16384u + (uint32_t)row * 128u + (((piece & 7) ^ (row & 7)) << 4), u[0],
-                 u[1], u[2], u[3]);
+    for (int k = 0; k < 4; ++k)
+      y[k] = bad ? 0x7e007e00u : half_pair(__uint_as_float(u[k] << 16) * up, __uint_as_float(u[k] & 0xffff0000u) * up);
+    st_shared_v4(place(i), y[0], y[1], y[2], y[3]);
   }
-  if (scale != 0.f)
-    out.coef = fabsf(scale) * 1.4426950408889634f * __int_as_float((min(max((int)(own >> 23), 27), 254) - 14) << 23);
+  Row out{1.f, INT_MAX};
+  if (scale != 0.f) out.coef = fabsf(scale) * 1.4426950408889634f * __int_as_float((e - 14) << 23);
   if (first + lane < run.rows)
     out.limit = kv_visible(KvSeq{0, run.n, run.len, run.seen},
                            (unsigned)(run.r * kRows + first + lane) / (unsigned)w.a.group, w.a.causal);
@@ -323,18 +331,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
     Row me{1.f, INT_MAX};
     const int first = x * 128 + (warp & 3) * 32;   // the warp's first row
     const uint32_t q_rows = smem_u32(sm.q) + x * kQTile + (warp & 3) * 32 * 128;
-    Fetched<D> rows;
     auto put_rows = [&] {
-      me = store_rows<D>(w, now, first, rows, q_rows);
+      me = load_rows<D, kVec>(w, now, first, q_rows);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.q_full[x]);
     };
     bool more = next_run(now);
-    if (more && (!x || now.rows > 128)) {
-      fetch_rows<D, kVec>(w, now, first, rows);
-      put_rows();
-    }
+    if (more && (!x || now.rows > 128)) put_rows();
     while (more) {
       const bool mine = !x || now.rows > 128;
       float m = kKvNone, l = 0.f;
@@ -420,11 +424,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
       }
       tile += now.tiles;
       if (!ok) break;
-      // the next run's rows come under the last products of this one
       const Run was = now;
       more = next_run(now);
-      const bool next = more && (!x || now.rows > 128);
-      fetch_rows<D, kVec>(w, now, next ? first : kRows, rows);   // none: so that nothing is kept through a run
       const bool whole = (was.flags & kPartBegins) && (was.flags & kPartEnds);
       const int slot = was.flags & kPartBegins ? 1 : 0;
       if (!whole) (slot ? left1 : left0) = KvPart{was.start, was.h, was.r * kRows, was.rows, was.flags};
@@ -439,28 +440,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
         uint8_t* const part = w.ws + (size_t)(2 * blockIdx.x + slot) * kv_part_bytes(D, kRows);
         if (!whole) reinterpret_cast<float2*>(part + kRows * D * 4)[first + lane] = make_float2(m, l);
         const int step = whole ? D : D / 2;                // columns at a time: 2 D bytes of a row
-        long long to = -1;                                 // where this lane's row goes, in elements of 2 D bytes
-        if (first + lane < was.rows)
-          to = whole ? kv_out_row(w.a, was.start, was.h, was.r * kRows + first + lane) : 2 * (first + lane);
-        uint8_t* const base = whole ? static_cast<uint8_t*>(w.a.out) : part;
-        constexpr int kPieces = D / 8;                     // of 16 bytes, of 2 D bytes
-        const uint32_t mine_at = q_rows + (uint32_t)lane * 128u;
+        constexpr int kPieces = D / 8, kAtOnce = 32 / kPieces;   // pieces of 16 bytes of them; rows
+        const int piece = lane % kPieces;
+        const uint32_t mine_at = q_rows + (uint32_t)lane * 128u, swz = (uint32_t)(lane & 7) << 4;
 #pragma unroll 1
         for (int col = 0; col < D; col += step) {
 #pragma unroll 1
-          for (int i = 0; i < step; i += 16) {
-            uint32_t o[16];
-            tmem_ld16(o_tmem + col + i, o);
-            float y[16];
+          for (int i = 0; i < step; i += 32) {
+            uint32_t o[32];
+            tmem_ld32(o_tmem + col + i, o);
+            float y[32];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) y[e] = __uint_as_float(o[e]) * inv * vscale;
+            for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(o[e]) * inv * vscale;
             // piece p of the row: panel p / 8, place p % 8 exchanged by the row
             auto put = [&](int p, uint32_t u0, uint32_t u1, uint32_t u2, uint32_t u3) {
-              st_shared_v4(mine_at + (uint32_t)(p >> 3) * 16384u + (((p & 7) ^ (lane & 7)) << 4), u0, u1, u2, u3);
+              st_shared_v4(mine_at + (uint32_t)(p >> 3) * 16384u + (((uint32_t)(p & 7) << 4) ^ swz), u0, u1, u2, u3);
             };
             if (whole) {
 #pragma unroll
-              for (int e = 0; e < 16; e += 8) {
+              for (int e = 0; e < 32; e += 8) {
                 uint32_t u[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -471,25 +469,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
               }
             } else {
 #pragma unroll
-              for (int e = 0; e < 16; e += 4)
+              for (int e = 0; e < 32; e += 4)
                 put((i + e) / 4, __float_as_uint(y[e]), __float_as_uint(y[e + 1]), __float_as_uint(y[e + 2]),
                     __float_as_uint(y[e + 3]));
             }
           }
           __syncwarp();
+          int row = lane / kPieces;
+          Walk walk(was.r * kRows + first + row, kAtOnce, w.a.group);
+          uint8_t* const out = static_cast<uint8_t*>(w.a.out) + piece * 16;
 #pragma unroll 4
-          for (int i = 0; i < kPieces; ++i) {
-            const int row = i * (32 / kPieces) + lane / kPieces, p = lane % kPieces;
-            const long long at = __shfl_sync(~0u, to, row);
-            const uint4 v = ld_shared_v4(q_rows + (uint32_t)(p >> 3) * 16384u + (uint32_t)row * 128u +
-                                         (((p & 7) ^ (row & 7)) << 4));
-            if (at >= 0) *reinterpret_cast<uint4*>(base + (at + (col > 0)) * (2 * D) + p * 16) = v;
+          for (int i = 0; i < 32 / kAtOnce; ++i, row += kAtOnce, walk.next()) {
+            const uint4 v = ld_shared_v4(q_rows + (uint32_t)(piece >> 3) * 16384u + (uint32_t)row * 128u +
+                                         (((piece & 7) ^ (row & 7)) << 4));
+            if (first + row >= was.rows) continue;
+            const long long at = ((long long)(was.start + walk.token) * w.a.cache.heads + was.h) * w.a.group + walk.head;
+            uint8_t* to = whole ? out + at * (2 * D) : part + (first + row) * (4 * D) + 4 * col + piece * 16;
+            *reinterpret_cast<uint4*>(to) = v;
           }
           __syncwarp();
         }
         tc_fence_before();
       }
-      if (next) put_rows();
+      if (more && (!x || now.rows > 128)) put_rows();
     }
     if (threadIdx.x == 0) {
       w.parts[2 * blockIdx.x] = left0;
