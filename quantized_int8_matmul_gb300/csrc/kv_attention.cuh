@@ -82,30 +82,23 @@ __device__ __forceinline__ long long kv_sequence_units(const KvWork& w, int b) {
   }
   return sum * w.a.cache.heads;
 }
-template <int R, int TK, int E>
-__device__ __forceinline__ long long kv_total_units(const KvWork& w) {
+// Inclusive prefix sums over the lanes.
+__device__ __forceinline__ long long kv_prefix(long long mine) {
   const int lane = threadIdx.x & 31;
-  long long total = 0;
-  for (int b0 = 0; b0 < w.a.batch.batch; b0 += 32) total += kv_sequence_units<R, TK, E>(w, b0 + lane);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
-  return total;
-}
-
-// The lane whose inclusive prefix sum over `mine` first passes `at`, or -1; `before`
-// receives the sum before that lane, or of all lanes.
-__device__ __forceinline__ int kv_prefix_find(long long mine, long long at, long long& before) {
-  const int lane = threadIdx.x & 31;
-  long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long up = __shfl_up_sync(~0u, incl, o);
-    if (lane >= o) incl += up;
+    const long long up = __shfl_up_sync(~0u, mine, o);
+    if (lane >= o) mine += up;
   }
-  const unsigned past = __ballot_sync(~0u, incl > at);
-  const int l = past ? __ffs(past) - 1 : -1;
-  before = past ? __shfl_sync(~0u, incl - mine, l) : __shfl_sync(~0u, incl, 31);
-  return l;
+  return mine;
+}
+// The first lane whose prefix sum passes `place`, or -1; `place` counts from that lane's
+// own beginning, or from the end of them all.
+__device__ __forceinline__ int kv_find(long long mine, long long incl, long long& place) {
+  const unsigned past = __ballot_sync(~0u, incl > place);
+  const int l = past ? __ffs(past) - 1 : 31;
+  place -= __shfl_sync(~0u, past ? incl - mine : incl, l);
+  return past ? l : -1;
 }
 
 // A place in the line of units.
@@ -114,27 +107,37 @@ struct KvCursor {
   int b, r, h, at, units, tiles;   // unit `at` of `units` of the item (b, r, h)
   KvSeq s;
 
-  // To unit `place` of the line (which has more); a whole warp calls.
-  __device__ void seek(const KvWork& w, long long place) {
-    const int lane = threadIdx.x & 31;
-    b = 0;
-    for (int b0 = 0; b0 < w.a.batch.batch; b0 += 32) {
-      long long before;
-      const int l = kv_prefix_find(kv_sequence_units<R, TK, E>(w, b0 + lane), place, before);
-      place -= before;
-      if (l >= 0) {
-        b = b0 + l;
-        break;
-      }
+  // The line cut for `workers`, shares of no less than `least` units: to the beginning of
+  // the index-th share, whose length is returned (0: there is none). A whole warp calls.
+  __device__ long long open(const KvWork& w, int workers, int least, int index) {
+    const int lane = threadIdx.x & 31, batch = w.a.batch.batch;
+    const long long mine = kv_sequence_units<R, TK, E>(w, lane), incl = kv_prefix(mine);
+    long long total = 0;
+    for (int b0 = 32; b0 < batch; b0 += 32) total += kv_sequence_units<R, TK, E>(w, b0 + lane);
+    if (batch > 32) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
+    }
+    total += __shfl_sync(~0u, incl, 31);
+    const long long more = total + workers - 1;
+    const long long share = max(more >> 32 ? more / workers : (long long)((unsigned)more / (unsigned)workers),
+                                (long long)least);
+    long long place = share * index;
+    const long long count = min(total - place, share);
+    if (count <= 0) return 0;
+    b = kv_find(mine, incl, place);
+    for (int b0 = 32; b < 0 && b0 < batch; b0 += 32) {
+      const long long u = kv_sequence_units<R, TK, E>(w, b0 + lane);
+      const int l = kv_find(u, kv_prefix(u), place);
+      if (l >= 0) b = b0 + l;
     }
     s = kv_sequence(w.a.batch, b);
     tiles = kv_tile_count<R>(w, s);
     r = 0;
-    for (int r0 = 0; r0 < tiles; r0 += 32) {
-      long long before;
-      const long long mine = r0 + lane < tiles ? (long long)kv_tile_units<R, TK, E>(w, s, r0 + lane) * w.a.cache.heads : 0;
-      const int l = kv_prefix_find(mine, place, before);
-      place -= before;
+    for (int r0 = 0; tiles > 1 && r0 < tiles; r0 += 32) {
+      const long long u =
+          r0 + lane < tiles ? (long long)kv_tile_units<R, TK, E>(w, s, r0 + lane) * w.a.cache.heads : 0;
+      const int l = kv_find(u, kv_prefix(u), place);
       if (l >= 0) {
         r = r0 + l;
         break;
@@ -143,6 +146,7 @@ struct KvCursor {
     units = kv_tile_units<R, TK, E>(w, s, r);
     h = place >> 32 ? (int)(place / units) : (int)((unsigned)place / (unsigned)units);
     at = (int)(place - (long long)h * units);
+    return count;
   }
   // To the next item's first unit.
   __device__ void next_item(const KvWork& w) {
@@ -188,8 +192,8 @@ __device__ __forceinline__ void kv_join_row(int count, int rows, int row, F part
       ml[j] = make_float2(kKvNone, 0.f);
 #pragma unroll
       for (int e = 0; e < kE; ++e) x[j][e] = 0.f;
+      const uint8_t* p = part(min(i0 + j, count - 1));
       if (i0 + j < count) {
-        const uint8_t* p = part(i0 + j);
         ml[j] = reinterpret_cast<const float2*>(p + rows * D * 4)[row];
         if constexpr (kE == 4) {
           const float4 v = reinterpret_cast<const float4*>(p)[row * 32 + lane];

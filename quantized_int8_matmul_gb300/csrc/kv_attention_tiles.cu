@@ -695,12 +695,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
       __syncwarp();
     } else if (warp == 13) {
       // ---------------- the CTA's share of the work, run by run ----------------
-      const long long total = kv_total_units<kRows, kTokens, kSetup>(w);
-      const long long share = max((total + w.ctas - 1) / w.ctas, (long long)kMinUnits);
-      const long long begin = (long long)blockIdx.x * share;
-      long long left = min(max(total - begin, 0ll), share);
       KvCursor<kRows, kTokens, kSetup> c{};
-      if (left > 0) c.seek(w, begin);
+      long long left = c.open(w, w.ctas, kMinUnits, blockIdx.x);
       uint32_t slot = 0, phase = 1;
       for (;;) {
         // the tiles of this stretch of units, if it has any
