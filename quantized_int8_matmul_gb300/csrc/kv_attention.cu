@@ -177,6 +177,15 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_rows_kernel(const
     int stage = 0;
 #pragma unroll 1
     for (int done = 0; done < count; ++done) {
+      if (done == 0) {
+        // the first blocks, ahead of the rows of Q
+        locate();
+#pragma unroll 1
+        for (; fetched < S::kStages - 1; ++fetched) {
+          if (fetched < count) fetch(fetched, fetched);
+          else cp_commit();
+        }
+      }
       if (fresh) {
         fresh = false;
         // the item's rows: lane (g, t) holds elements 64 i + 16 t .. of row 8 nt + g
@@ -245,15 +254,6 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_rows_kernel(const
         vref = 0;
       }
 
-      if (done == 0) {
-        // the first blocks; the table's entries came beside the rows of Q
-        locate();
-#pragma unroll 1
-        for (; fetched < S::kStages - 1; ++fetched) {
-          if (fetched < count) fetch(fetched, fetched);
-          else cp_commit();
-        }
-      }
       // fetch the block kStages - 1 ahead, over the one that all lanes have read, then wait for this one's copies
       __syncwarp();
       if (fetched < count) fetch(fetched, stage == 0 ? S::kStages - 1 : stage - 1);
@@ -499,10 +499,11 @@ Plan plan_of(int rows, int batch, int group, int head_dim, int max_tokens, bool 
 template <int D, int NT, int kWarps, typename T>
 cudaError_t rows_launch(const KvWork& w, bool vec, cudaStream_t s) {
   using S = Shape<D, NT, kWarps>;
-  auto kern = vec ? &kv_attention_rows_kernel<D, NT, kWarps, T, true> : &kv_attention_rows_kernel<D, NT, kWarps, T, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  constexpr auto kVector = &kv_attention_rows_kernel<D, NT, kWarps, T, true>;
+  constexpr auto kScalar = &kv_attention_rows_kernel<D, NT, kWarps, T, false>;
+  cudaError_t e = vec ? kv_allow_smem<kVector>(S::kSmem) : kv_allow_smem<kScalar>(S::kSmem);
   if (e != cudaSuccess) return e;
-  e = launch_chained(kern, dim3(w.ctas), dim3(32 * kWarps), S::kSmem, 1, s, w);
+  e = launch_chained(vec ? kVector : kScalar, dim3(w.ctas), dim3(32 * kWarps), S::kSmem, 1, s, w);
   if (e != cudaSuccess) return e;
   return launch_chained(&kv_attention_join_kernel<D, S::kRows, T>, dim3(w.ctas), dim3(256), 0, 1, s, w);
 }

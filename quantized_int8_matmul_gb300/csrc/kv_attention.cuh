@@ -2,6 +2,8 @@
 // cut and how its parts are joined.
 #pragma once
 
+#include <atomic>
+
 #include "chain.cuh"
 #include "common.cuh"
 #include "kv.cuh"
@@ -279,6 +281,20 @@ __global__ void __launch_bounds__(256) kv_attention_join_kernel(const KvWork w) 
     T* out = static_cast<T*>(w.a.out) + kv_out_row(w.a, a.start, a.h, a.first + row) * D;
     kv_join_row<D, T>(n, R, row, part, true, out, nullptr);
   }
+}
+
+// The opt-in to a kernel's shared memory, once a device.
+template <auto kern>
+cudaError_t kv_allow_smem(int bytes) {
+  static std::atomic<bool> done[64];
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
+  if (done[device].load(std::memory_order_relaxed)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done[device].store(true, std::memory_order_relaxed);
+  return e;
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {

@@ -737,12 +737,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
 
 template <int D>
 cudaError_t tiles_sized(const KvWork& w, bool vec, cudaStream_t s) {
-  auto kern = vec ? &kv_attention_tiles_kernel<D, true> : &kv_attention_tiles_kernel<D, false>;
+  constexpr auto kVector = &kv_attention_tiles_kernel<D, true>, kScalar = &kv_attention_tiles_kernel<D, false>;
   constexpr int bytes = (int)sizeof(Smem<D>);
   static_assert(bytes <= 227 * 1024, "one CTA an SM");
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  cudaError_t e = vec ? kv_allow_smem<kVector>(bytes) : kv_allow_smem<kScalar>(bytes);
   if (e != cudaSuccess) return e;
-  e = launch_chained(kern, dim3(w.ctas), dim3(kThreads), bytes, 1, s, w);
+  e = launch_chained(vec ? kVector : kScalar, dim3(w.ctas), dim3(kThreads), bytes, 1, s, w);
   if (e != cudaSuccess) return e;
   return launch_chained(&kv_attention_join_kernel<D, kRows, __nv_bfloat16>, dim3(w.ctas, 16), dim3(256), 0, 1, s, w);
 }

@@ -15,6 +15,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kPasses = 4;               // of heads, by a warp that rotates queries
 
 // Where a lane's two groups of eight begin in a head: li = 0 .. dim / 16 - 1.
 struct Groups {
@@ -100,13 +101,13 @@ __device__ __forceinline__ void append_block(const KvAppendArgs& p, const KvSeq&
                                              uint8_t* exps, bool rotate) {
   constexpr int kLanes = D / 16;          // lanes of a token
   constexpr int kTokens = 32 / kLanes;    // tokens a pass
-  constexpr int kPasses = kKvBlock / kTokens;
+  constexpr int kSteps = kKvBlock / kTokens;
   const int lane = threadIdx.x & 31;
   const int li = lane % kLanes, ti = lane / kLanes;
   const Groups g = groups_of(li, rotate ? p.half : 0, rotate && p.interleaved);
-  float a[kPasses][8], b[kPasses][8];
+  float a[kSteps][8], b[kSteps][8];
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
+  for (int i = 0; i < kSteps; ++i) {
     const int pos = base + i * kTokens + ti;
     if (pos >= from && pos < to) {
       const T* r = x + (long long)(s.start + pos - (s.len - s.n)) * row_stride;
@@ -119,7 +120,7 @@ __device__ __forceinline__ void append_block(const KvAppendArgs& p, const KvSeq&
   }
   float top = 0.f;
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
+  for (int i = 0; i < kSteps; ++i) {
     const int pos = base + i * kTokens + ti;
     if (pos >= from && pos < to) {
       if (rotate && g.turn >= 0) {
@@ -149,7 +150,7 @@ __device__ __forceinline__ void append_block(const KvAppendArgs& p, const KvSeq&
   int8_t* c = cache + block * (size_t)(kKvBlock * D);
   __syncwarp();   // every lane has read the byte
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
+  for (int i = 0; i < kSteps; ++i) {
     const int pos = base + i * kTokens + ti;
     int8_t* r = c + (i * kTokens + ti) * D;
     if (pos >= from && pos < to) {
@@ -169,7 +170,8 @@ __device__ __forceinline__ void append_block(const KvAppendArgs& p, const KvSeq&
 // sequence b owns the slots from floor(starts[b] / 16) + 2 b on, which leaves room for
 // the floor(n / 16) + 2 blocks that n tokens can touch, so that the slot count follows
 // from the rows and the batch alone. The slot's warps are its heads, keys first. The
-// CTAs behind those rotate queries: a warp takes one token and up to two passes of heads.
+// CTAs behind those rotate queries: a warp takes one token and up to four passes of heads,
+// whose loads go out before it looks for the token's position.
 template <int D, typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendArgs p) {
   chain_wait();
@@ -221,33 +223,33 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendArgs 
     return;
   }
   constexpr int kLanes = D / 16, kHeads = 32 / kLanes;   // heads a pass
-  const int chunks = (p.q_heads + 2 * kHeads - 1) / (2 * kHeads);
+  const int chunks = (p.q_heads + kPasses * kHeads - 1) / (kPasses * kHeads);
   const long long task = ((long long)blockIdx.x - cache_ctas) * kWarps + warp;
   if (task < (long long)p.batch.rows * chunks) {
-    const int t = (int)(task / chunks), chunk = (int)(task % chunks);
+    const int t = (int)((unsigned long long)task / (unsigned)chunks), chunk = (int)(task - (long long)t * chunks);
+    const int li = lane % kLanes;
+    const Groups g = groups_of(li, p.half, p.interleaved);
+    const int h0 = chunk * kPasses * kHeads + lane / kLanes;
+    // the rows first, which need no position
+    float a[kPasses][8], e[kPasses][8];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int h = h0 + i * kHeads;
+      if (h < p.q_heads) {
+        const T* r = static_cast<const T*>(p.q) + (long long)t * p.q_row + (long long)h * p.q_head;
+        kv_load8<kVec>(r + g.a, a[i]);
+        kv_load8<kVec>(r + g.b, e[i]);
+      }
+    }
     const int b = kv_sequence_of_row(p.batch, t);
     if (b >= 0) {
       const KvSeq s = kv_sequence(p.batch, b);
       if (t >= s.start && t < s.start + s.n) {
-        const int pos = s.len - s.n + t - s.start;
-        const int li = lane % kLanes;
-        const Groups g = groups_of(li, p.half, p.interleaved);
         float c[8], sn[8];
-        if (g.turn >= 0) load_turn(p, pos, g.turn, c, sn);
-        float a[2][8], e[2][8];
-        const int h0 = chunk * 2 * kHeads + lane / kLanes;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int h = h0 + i * kHeads;
-          if (h < p.q_heads) {
-            const T* r = static_cast<const T*>(p.q) + (long long)t * p.q_row + (long long)h * p.q_head;
-            kv_load8<kVec>(r + g.a, a[i]);
-            kv_load8<kVec>(r + g.b, e[i]);
-          }
-        }
+        if (g.turn >= 0) load_turn(p, s.len - s.n + t - s.start, g.turn, c, sn);
         chain_release();
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kPasses; ++i) {
           const int h = h0 + i * kHeads;
           if (h < p.q_heads) {
             if (g.turn >= 0) turn_groups(a[i], e[i], c, sn, p.interleaved);
@@ -316,7 +318,7 @@ cudaError_t append_typed(KvAppendArgs a, bool vec, cudaStream_t s) {
   a.slots = a.batch.starts ? a.batch.rows / kKvBlock + 2 * a.batch.batch : a.batch.batch;
   a.slot_ctas = (2 * a.cache.heads + kWarps - 1) / kWarps;
   constexpr int kHeads = 32 / (D / 16);
-  const long long chunks = (a.q_heads + 2 * kHeads - 1) / (2 * kHeads);
+  const long long chunks = (a.q_heads + kPasses * kHeads - 1) / (kPasses * kHeads);
   const long long q_ctas = a.q ? (a.batch.rows * chunks + kWarps - 1) / kWarps : 0;
   const long long grid = (long long)a.slots * a.slot_ctas + q_ctas;
   if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
