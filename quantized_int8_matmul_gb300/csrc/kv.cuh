@@ -65,35 +65,54 @@ __device__ __forceinline__ int kv_exponent(float amax) {
   return max(((__float_as_int(amax) + 0x10000) >> 23) - 6, 0);
 }
 
-__device__ __forceinline__ float kv_float(float x) { return x; }
-__device__ __forceinline__ float kv_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-
-// Eight consecutive elements as float32; kVec: on a 16-byte boundary.
-template <bool kVec>
-__device__ __forceinline__ void kv_load8(const __nv_bfloat16* p, float (&x)[8]) {
-  if constexpr (kVec) {
-    const uint4 w = *reinterpret_cast<const uint4*>(p);
+// Eight consecutive elements as they lie, and as float32. kVec: on a 16-byte boundary.
+template <typename T>
+struct KvRaw;
+template <>
+struct KvRaw<__nv_bfloat16> {
+  uint4 w = make_uint4(0, 0, 0, 0);
+  template <bool kVec>
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    if constexpr (kVec) {
+      w = *reinterpret_cast<const uint4*>(p);
+    } else {
+      const unsigned short* s = reinterpret_cast<const unsigned short*>(p);
+      w = make_uint4(s[0] | (uint32_t)s[1] << 16, s[2] | (uint32_t)s[3] << 16, s[4] | (uint32_t)s[5] << 16,
+                     s[6] | (uint32_t)s[7] << 16);
+    }
+  }
+  __device__ __forceinline__ void floats(float (&x)[8]) const {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       x[2 * i] = __uint_as_float(u[i] << 16);
       x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __bfloat162float(p[i]);
   }
-}
-template <bool kVec>
-__device__ __forceinline__ void kv_load8(const float* p, float (&x)[8]) {
-  if constexpr (kVec) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+};
+template <>
+struct KvRaw<float> {
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = make_float4(0.f, 0.f, 0.f, 0.f);
+  template <bool kVec>
+  __device__ __forceinline__ void load(const float* p) {
+    if constexpr (kVec) {
+      a = reinterpret_cast<const float4*>(p)[0];
+      b = reinterpret_cast<const float4*>(p)[1];
+    } else {
+      a = make_float4(p[0], p[1], p[2], p[3]);
+      b = make_float4(p[4], p[5], p[6], p[7]);
+    }
+  }
+  __device__ __forceinline__ void floats(float (&x)[8]) const {
     x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
     x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = p[i];
   }
+};
+template <bool kVec, typename T>
+__device__ __forceinline__ void kv_load8(const T* p, float (&x)[8]) {
+  KvRaw<T> r;
+  r.template load<kVec>(p);
+  r.floats(x);
 }
 // Eight elements to a 16-byte boundary.
 __device__ __forceinline__ void kv_store8(__nv_bfloat16* p, const float (&x)[8]) {

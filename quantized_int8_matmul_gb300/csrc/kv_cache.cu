@@ -105,35 +105,41 @@ __device__ __forceinline__ void append_block(const KvAppendArgs& p, const KvSeq&
   const int lane = threadIdx.x & 31;
   const int li = lane % kLanes, ti = lane / kLanes;
   const Groups g = groups_of(li, rotate ? p.half : 0, rotate && p.interleaved);
-  float a[kSteps][8], b[kSteps][8];
+  // The block stays as it was read: it is rotated once for its largest magnitude and once more to be stored, which
+  // costs less than the registers of 64 numbers a lane would (a third fewer warps on an SM).
+  KvRaw<T> ra[kSteps], rb[kSteps];
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
     const int pos = base + i * kTokens + ti;
     if (pos >= from && pos < to) {
       const T* r = x + (long long)(s.start + pos - (s.len - s.n)) * row_stride;
-      kv_load8<kVec>(r + g.a, a[i]);
-      kv_load8<kVec>(r + g.b, b[i]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) a[i][e] = b[i][e] = 0.f;
+      ra[i].template load<kVec>(r + g.a);
+      rb[i].template load<kVec>(r + g.b);
     }
   }
+  auto step = [&](int i, float (&a)[8], float (&b)[8]) {
+    ra[i].floats(a);
+    rb[i].floats(b);
+    if (rotate && g.turn >= 0) {
+      float c[8], sn[8];
+      load_turn(p, base + i * kTokens + ti, g.turn, c, sn);
+      turn_groups(a, b, c, sn, p.interleaved);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      a[e] = storable(a[e]);
+      b[e] = storable(b[e]);
+    }
+  };
   float top = 0.f;
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
     const int pos = base + i * kTokens + ti;
     if (pos >= from && pos < to) {
-      if (rotate && g.turn >= 0) {
-        float c[8], sn[8];
-        load_turn(p, pos, g.turn, c, sn);
-        turn_groups(a[i], b[i], c, sn, p.interleaved);
-      }
+      float a[8], b[8];
+      step(i, a, b);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        a[i][e] = storable(a[i][e]);
-        b[i][e] = storable(b[i][e]);
-        top = fmaxf(top, fmaxf(fabsf(a[i][e]), fabsf(b[i][e])));
-      }
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, fmaxf(fabsf(a[e]), fabsf(b[e])));
     }
   }
 #pragma unroll
@@ -154,8 +160,10 @@ __device__ __forceinline__ void append_block(const KvAppendArgs& p, const KvSeq&
     const int pos = base + i * kTokens + ti;
     int8_t* r = c + (i * kTokens + ti) * D;
     if (pos >= from && pos < to) {
-      *reinterpret_cast<uint2*>(r + g.a) = make_uint2(pack4(a[i], up), pack4(a[i] + 4, up));
-      *reinterpret_cast<uint2*>(r + g.b) = make_uint2(pack4(b[i], up), pack4(b[i] + 4, up));
+      float a[8], b[8];
+      step(i, a, b);
+      *reinterpret_cast<uint2*>(r + g.a) = make_uint2(pack4(a, up), pack4(a + 4, up));
+      *reinterpret_cast<uint2*>(r + g.b) = make_uint2(pack4(b, up), pack4(b + 4, up));
     } else if (pos < from && byte > held) {
       // the block's scale grows: the tokens that are there follow it
       uint2 u = *reinterpret_cast<const uint2*>(r + g.a), w = *reinterpret_cast<const uint2*>(r + g.b);
@@ -173,7 +181,7 @@ __device__ __forceinline__ void append_block(const KvAppendArgs& p, const KvSeq&
 // CTAs behind those rotate queries: a warp takes one token and up to four passes of heads,
 // whose loads go out before it looks for the token's position.
 template <int D, typename T, bool kVec>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendArgs p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) kv_append_kernel(const KvAppendArgs p) {
   chain_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int heads = p.cache.heads;
@@ -231,14 +239,14 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendArgs 
     const Groups g = groups_of(li, p.half, p.interleaved);
     const int h0 = chunk * kPasses * kHeads + lane / kLanes;
     // the rows first, which need no position
-    float a[kPasses][8], e[kPasses][8];
+    KvRaw<T> ra[kPasses], rb[kPasses];
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
       const int h = h0 + i * kHeads;
       if (h < p.q_heads) {
         const T* r = static_cast<const T*>(p.q) + (long long)t * p.q_row + (long long)h * p.q_head;
-        kv_load8<kVec>(r + g.a, a[i]);
-        kv_load8<kVec>(r + g.b, e[i]);
+        ra[i].template load<kVec>(r + g.a);
+        rb[i].template load<kVec>(r + g.b);
       }
     }
     const int b = kv_sequence_of_row(p.batch, t);
@@ -252,10 +260,13 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendArgs 
         for (int i = 0; i < kPasses; ++i) {
           const int h = h0 + i * kHeads;
           if (h < p.q_heads) {
-            if (g.turn >= 0) turn_groups(a[i], e[i], c, sn, p.interleaved);
+            float a[8], e[8];
+            ra[i].floats(a);
+            rb[i].floats(e);
+            if (g.turn >= 0) turn_groups(a, e, c, sn, p.interleaved);
             T* r = static_cast<T*>(p.q_out) + ((size_t)t * p.q_heads + h) * D;
-            kv_store8(r + g.a, a[i]);
-            kv_store8(r + g.b, e[i]);
+            kv_store8(r + g.a, a);
+            kv_store8(r + g.b, e);
           }
         }
         return;
