@@ -119,6 +119,14 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return r;
 }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   float2 r;
   asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
@@ -167,22 +175,26 @@ __device__ __forceinline__ void tmem_ld128(uint32_t t, uint32_t (&r)[128]) {
   tmem_ld32x2(t + 64, c, t + 96, d);
 }
 
-// Rows of a tile in steps: row rr is query head rr % group of token rr / group.
+// Where rows of a tile lie, in steps: row rr is query head rr % group of token rr / group,
+// of a tensor with `row` elements between tokens and `head` between heads.
 struct Walk {
-  int token, head;
-  int tokens, heads, group;   // a step
-  __device__ Walk(int rr, int step, int g) : group(g) {
-    token = (unsigned)rr / (unsigned)g;
+  long long at;            // elements from the sequence's first row and the key head's first query head
+  long long step, wrap;    // a step, and what is added where it passes a token's last head
+  int head, heads, group;
+  __device__ Walk(int rr, int rows, int g, long long row, long long head_stride) : group(g) {
+    const int token = (unsigned)rr / (unsigned)g, tokens = (unsigned)rows / (unsigned)g;
     head = rr - token * g;
-    tokens = (unsigned)step / (unsigned)g;
-    heads = step - tokens * g;
+    heads = rows - tokens * g;
+    at = token * row + head * head_stride;
+    step = tokens * row + heads * head_stride;
+    wrap = row - g * head_stride;
   }
   __device__ void next() {
-    token += tokens;
     head += heads;
+    at += step;
     if (head >= group) {
       head -= group;
-      ++token;
+      at += wrap;
     }
   }
 };
@@ -204,13 +216,13 @@ __device__ __forceinline__ Row load_rows(const KvWork& w, const Run& run, int fi
   const int piece = lane % kLanes;
   {
     int row = lane / kLanes;
-    Walk walk(run.r * kRows + first + row, kAtOnce, w.a.group);
+    Walk walk(run.r * kRows + first + row, kAtOnce, w.a.group, w.a.q_row, w.a.q_head);
     const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(w.a.q) + (long long)run.start * w.a.q_row +
                                (long long)run.h * w.a.group * w.a.q_head + piece * 8;
 #pragma unroll 4
     for (int i = 0; i < 32 / kAtOnce; ++i, row += kAtOnce, walk.next()) {
       const uint32_t dst = q + (uint32_t)(piece >> 3) * 16384u + (uint32_t)row * 128u + (((piece & 7) ^ (row & 7)) << 4);
-      const __nv_bfloat16* at = src + walk.token * w.a.q_row + walk.head * w.a.q_head;
+      const __nv_bfloat16* at = src + walk.at;
       if (first + row >= run.rows) {
         st_shared_v4(dst, 0, 0, 0, 0);
       } else if constexpr (kVec) {
@@ -435,8 +447,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
         tc_fence_after();
         // O by way of this warp's rows of Q, whose last use is over, so that neighbouring lanes write neighbouring
         // bytes: 256 bytes of each row at a time, as bfloat16 or, of a part, as float32
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const float vscale = kv_power(vref);
+        // 1 / l and V's power in one factor where that is a normal number, else one after the other
+        const float inv = l == 0.f ? 0.f : 1.f / l, vscale = kv_power(vref), both = inv * vscale;
+        const bool small = __any_sync(~0u, both < 1.17549435e-38f);
+        const float2 factor = small ? make_float2(inv, inv) : make_float2(both, both);
         uint8_t* const part = w.ws + (size_t)(2 * blockIdx.x + slot) * kv_part_bytes(D, kRows);
         if (!whole) reinterpret_cast<float2*>(part + kRows * D * 4)[first + lane] = make_float2(m, l);
         const int step = whole ? D : D / 2;                // columns at a time: 2 D bytes of a row
@@ -451,7 +465,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
             tmem_ld32(o_tmem + col + i, o);
             float y[32];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(o[e]) * inv * vscale;
+            for (int e = 0; e < 32; e += 2) {
+              const float2 v = mul2(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), factor);
+              y[e] = v.x;
+              y[e + 1] = v.y;
+            }
+            if (small) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) y[e] *= vscale;
+            }
             // piece p of the row: panel p / 8, place p % 8 exchanged by the row
             auto put = [&](int p, uint32_t u0, uint32_t u1, uint32_t u2, uint32_t u3) {
               st_shared_v4(mine_at + (uint32_t)(p >> 3) * 16384u + (((uint32_t)(p & 7) << 4) ^ swz), u0, u1, u2, u3);
@@ -476,16 +498,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
           }
           __syncwarp();
           int row = lane / kPieces;
-          Walk walk(was.r * kRows + first + row, kAtOnce, w.a.group);
-          uint8_t* const out = static_cast<uint8_t*>(w.a.out) + piece * 16;
+          // in bytes; a part's rows follow each other
+          const long long out_heads = (long long)w.a.cache.heads * w.a.group;
+          Walk walk(was.r * kRows + first + row, kAtOnce, w.a.group, out_heads * (2 * D), 2 * D);
+          uint8_t* to = static_cast<uint8_t*>(w.a.out) + (was.start * out_heads + was.h * w.a.group) * (2 * D) + piece * 16;
+          if (!whole) {
+            walk = Walk(first + row, kAtOnce, 1, 4 * D, 0);
+            to = part + 4 * col + piece * 16;
+          }
 #pragma unroll 4
           for (int i = 0; i < 32 / kAtOnce; ++i, row += kAtOnce, walk.next()) {
             const uint4 v = ld_shared_v4(q_rows + (uint32_t)(piece >> 3) * 16384u + (uint32_t)row * 128u +
                                          (((piece & 7) ^ (row & 7)) << 4));
-            if (first + row >= was.rows) continue;
-            const long long at = ((long long)(was.start + walk.token) * w.a.cache.heads + was.h) * w.a.group + walk.head;
-            uint8_t* to = whole ? out + at * (2 * D) : part + (first + row) * (4 * D) + 4 * col + piece * 16;
-            *reinterpret_cast<uint4*>(to) = v;
+            if (first + row < was.rows) *reinterpret_cast<uint4*>(to + walk.at) = v;
           }
           __syncwarp();
         }
