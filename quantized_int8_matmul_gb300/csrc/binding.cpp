@@ -450,8 +450,8 @@ PyObject* kv_append(PyObject* const* a) {
     rotated = 2 * c.size(1);
   }
   const int interleaved = truth(a[12]);
+  const void *kp = ptr(k), *vp = ptr(v), *qp = nullptr;
   const Call call(a[14], k);
-  const void* qp = nullptr;
   int64_t q_heads = 0;
   Tensor out;
   if (a[9] != Py_None) {
@@ -469,9 +469,9 @@ PyObject* kv_append(PyObject* const* a) {
     fail("q_out without q");
   }
   const qmm_status st = unlocked(
-      qmm_kv_append, &cache, &batch, qmm_type(t), ptr(k), k_row, k_head, ptr(v), v_row, v_head, qp, q_row, q_head,
-      q_heads, out.defined() ? ptr(out) : nullptr, static_cast<const float*>(cos), static_cast<const float*>(sin),
-      positions, rotated, interleaved, call.stream());
+      qmm_kv_append, &cache, &batch, qmm_type(t), kp, k_row, k_head, vp, v_row, v_head, qp, q_row, q_head, q_heads,
+      out.defined() ? ptr(out) : nullptr, static_cast<const float*>(cos), static_cast<const float*>(sin), positions,
+      rotated, interleaved, call.stream());
   if (st != QMM_OK) return PyLong_FromLong(st);
   if (out.defined()) return wrap(out);
   Py_RETURN_NONE;
@@ -491,7 +491,8 @@ PyObject* kv_read(PyObject* const* a) {
   const Tensor k = call.output(a[8], shape, t, FLOATS, "k_out", first);
   if (a[8] != Py_None) t = k.scalar_type();
   const Tensor v = call.output(a[9], shape, t, {t}, "v_out", first);
-  const qmm_status st = unlocked(qmm_kv_read, &cache, &batch, ptr(k), ptr(v), qmm_type(t), call.stream());
+  void *kp = ptr(k), *vp = ptr(v);
+  const qmm_status st = unlocked(qmm_kv_read, &cache, &batch, kp, vp, qmm_type(t), call.stream());
   return st != QMM_OK ? PyLong_FromLong(st) : pair(wrap(k), wrap(v));
 }
 
@@ -528,8 +529,9 @@ PyObject* kv_attention(PyObject* const* a) {
     if (bytes) ws = call.empty({(int64_t)bytes}, U8);
     have = bytes;
   }
+  void* op = ptr(out);
   const qmm_status st = unlocked(qmm_kv_attention, &cache, &batch, qp, qmm_type(t), q_row, q_head, q_heads,
-                                 (float)scale, causal, max_tokens, ptr(out), ws.defined() ? ptr(ws) : nullptr, have,
+                                 (float)scale, causal, max_tokens, op, ws.defined() ? ptr(ws) : nullptr, have,
                                  call.stream());
   return st != QMM_OK ? PyLong_FromLong(st) : wrap(out);
 }

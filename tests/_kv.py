@@ -2,8 +2,6 @@
 import numpy as np
 import torch
 
-from oracle import kv_oracle as ko
-
 TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
 
 

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from oracle import kv_oracle as ko
-from tests._kv import TYPES, Batch, assert_attention, attention_bound, rounded
+from _kv import TYPES, Batch, assert_attention, attention_bound, rounded
 
 pytestmark = pytest.mark.gpu
 

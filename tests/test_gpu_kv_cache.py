@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from oracle import kv_oracle as ko
-from tests._kv import TYPES, Batch, rounded, turns
+from _kv import TYPES, Batch, rounded, turns
 
 pytestmark = pytest.mark.gpu
 
