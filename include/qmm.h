@@ -31,7 +31,7 @@
  *    it; a launch failure returns QMM_ERR_CUDA (qmm_last_cuda_error() gives
  *    the cudaError_t value).
  *  - Kernels never trap or spin without bound. A device-side wait that runs
- *    out (about one second) records a code in a device error word and the
+ *    out (after about one second, or some millions of tries) records a code in a device error word and the
  *    kernel returns; qmm_check_device_error() reports it as QMM_ERR_TIMEOUT.
  *  - Integer results wrap modulo 2^32 (two's complement); nothing saturates
  *    except the uint8 outputs of dynamic_quantize_linear.

@@ -26,6 +26,10 @@
 // The running maximum moves only when some score is 8 (a factor of 256) above it,
 // which a vote finds out: P keeps six more bits below fp16's largest value and 30 bits
 // to its smallest. V's power of two goes into P the same way.
+//
+// Measured, with the join: 64 sequences of up to 16384 tokens, 64 query heads on 8 of
+// 128, 114 us (6.0 TB/s, 89 % of a copy; the copies without arithmetic take as long); one
+// of 131072 54 us; one of 1021 9.8 us, a chain of latencies.
 #include "kv_attention.cuh"
 
 namespace qmm {

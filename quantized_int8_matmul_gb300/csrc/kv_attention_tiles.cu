@@ -11,16 +11,24 @@
 //   O += P V    B = V as it lies, tokens in rows (its other major order), fp32
 //
 // The two tiles alternate: while the tensor cores work for one, the softmax of the
-// other runs. Warps 0-3 and 4-7 hold a row a thread (its maximum and sum need no
-// exchange), warps 8-11 bring int8 keys and values from their pages through registers,
-// widen them to fp16, exactly, into a ring of four operands, and one thread issues the
-// MMAs. A block's power of two is not multiplied into K or V: a key block's goes into
-// the factor of its 16 columns of S, a value block's into the exponent of its 16 columns
-// of P. The running maximum moves only past a score 8 above it (rescaling O is then
-// rare); scores are masked only in tiles that some row's limit cuts.
+// other runs. Its roles: warps 0-3 and 4-7 hold a row a thread (its maximum and sum need
+// no exchange); one warp copies int8 keys and values from their pages (bulk copies of a
+// block each), warps 8-11 widen them to fp16, exactly, into a ring of three operands;
+// one warp issues the MMAs, another works out the CTA's share of the work. A block's
+// power of two is not multiplied into K or V: a key block's goes into the factor of its 16
+// columns of S, a value block's into the exponent of its 16 columns of P. The running
+// maximum moves only past a score 8 above it (rescaling O is then rare); scores are
+// masked only in tiles that some row's limit cuts.
 //
 // The work is cut like that of the other kernel (kv_attention.cuh), a unit being a tile
 // of 128 tokens, so that short and long rows of causal prompts balance.
+//
+// Measured: a prompt of 8192 tokens, 32 query heads on 8 of 128, 450 us (1220 TFLOP/s);
+// 8192 x 8192 not causal 800 us (1375); 500 tokens over 32000 206 us (1262). A tile of 256
+// x 128 takes about 3300 cycles: its MMAs 2080, its traffic in shared memory (320 KB: Q
+// and K 128, V 64, copies and conversion 128) 2560, one tile's softmax 1500. Sixteen
+// softmax warps with half a row each, and taking half of P before the maximum is known,
+// were slower (853 and 889 us for the 800).
 #include "kv_attention.cuh"
 
 namespace qmm {

@@ -7,6 +7,10 @@
 // magnitude, which decides its power of two, is then a warp's reduction, and nobody
 // else writes that block. A lane holds two groups of eight elements that a rotation
 // pairs (element i with i + half, or neighbours), so that the pair meets in one lane.
+//
+// Measured: 8192 tokens of 64 query and 8 + 8 key and value heads of 128, bfloat16, 60 us
+// (319 MB: 79 % of a copy's rate) and 14 us for reading them back (50 MB, 53 %); one token
+// of each of 256 sequences about 8 and 7 us, most of it loads that follow each other.
 #include "chain.cuh"
 #include "kv.cuh"
 
