@@ -31,7 +31,7 @@
  *    it; a launch failure returns QMM_ERR_CUDA (qmm_last_cuda_error() gives
  *    the cudaError_t value).
  *  - Kernels never trap or spin without bound. A device-side wait that runs
- *    out (after about one second, or some millions of tries) records a code in a device error word and the
+ *    out (about one second) records a code in a device error word and the
  *    kernel returns; qmm_check_device_error() reports it as QMM_ERR_TIMEOUT.
  *  - Integer results wrap modulo 2^32 (two's complement); nothing saturates
  *    except the uint8 outputs of dynamic_quantize_linear.
@@ -669,7 +669,7 @@ qmm_status qmm_fp4_matmul(const void* a_packed, size_t a_bytes, int64_t M, const
  *                    head h reads key head h / (q_heads / kv_heads). Sums and maxima in
  *                    float32. A row that sees nothing gets zeros, one whose q holds a
  *                    NaN or an infinity NaN. out [rows, q_heads, head_dim] contiguous,
- *                    of q's dtype. max_tokens: no sequence has more rows, as far as the
+ *                    of q's dtype, not overlapping q. max_tokens: no sequence has more rows, as far as the
  *                    caller knows; it chooses kernels and splits, never results'
  *                    validity (rows: always true).
  *  workspace         qmm_kv_attention_workspace_bytes of the same arguments, 16-byte
@@ -677,7 +677,7 @@ qmm_status qmm_fp4_matmul(const void* a_packed, size_t a_bytes, int64_t M, const
  * rows = 0 or batch = 0 launches nothing. QMM_ERR_UNSUPPORTED for another head_dim, page
  * or `rotated`; QMM_ERR_INVALID_ARG for a bad dtype, stride, null or unaligned pointer,
  * short workspace, q_heads that kv_heads does not divide, starts = NULL with rows !=
- * batch, width * page or rows * q_heads beyond 2^31 - 1.
+ * batch, width * page or rows * q_heads beyond 2^31 - 1, batch beyond 2^29 - 1.
  */
 typedef struct {
   int8_t* k;

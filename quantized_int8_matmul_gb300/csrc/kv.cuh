@@ -47,9 +47,16 @@ __device__ __forceinline__ int kv_sequence_of_row(const KvBatchArgs& a, int t) {
   if (!a.starts) return t < a.batch ? t : -1;
   const int lane = threadIdx.x & 31;
   int count = 0;   // starts[1 ..] that are <= t
-  for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    const int b = b0 + lane;
-    count += __popc(__ballot_sync(~0u, b < a.batch && __ldg(a.starts + b + 1) <= t));
+#pragma unroll 1
+  for (int b0 = 0; b0 < a.batch; b0 += 128) {
+    int ends[4];   // four loads in flight
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int b = b0 + 32 * e + lane;
+      ends[e] = b < a.batch ? __ldg(a.starts + b + 1) : INT_MAX;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) count += __popc(__ballot_sync(~0u, ends[e] <= t));
   }
   return count < a.batch ? count : -1;
 }

@@ -482,17 +482,16 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_rows_kernel(const
 // Two tiles of eight rows where one tile would not hold a sequence's rows.
 int row_tiles(int group, int max_tokens) { return (long long)group * max_tokens <= 8 ? 1 : 2; }
 
-// Which kernels a call needs. Sequences with up to kFewRows rows a key head are this
+// Which kernels a call needs. Sequences with up to kKvFewRows rows a key head are this
 // file's, and float32 rows of any number; more bfloat16 rows are the tensor cores'. A
 // call whose sequences all have max_tokens rows needs one kernel.
-constexpr long long kFewRows = 16;
 struct Plan {
   bool few, many;
   size_t few_bytes, bytes;   // the workspace: `few` first
 };
 Plan plan_of(int rows, int batch, int group, int head_dim, int max_tokens, bool bf16) {
   Plan p{};
-  p.many = bf16 && (long long)group * max_tokens > kFewRows;
+  p.many = bf16 && (long long)group * max_tokens > kKvFewRows;
   p.few = !p.many || (long long)max_tokens * batch != rows;
   const int part_rows = p.many ? 16 : 8 * row_tiles(group, max_tokens);
   if (p.few) p.few_bytes = (size_t)num_sms() * 2 * (sizeof(KvPart) + kv_part_bytes(head_dim, part_rows));
@@ -501,24 +500,23 @@ Plan plan_of(int rows, int batch, int group, int head_dim, int max_tokens, bool 
 }
 
 template <int D, int NT, int kWarps, typename T>
-cudaError_t rows_launch(const KvWork& w, bool vec, cudaStream_t s) {
+cudaError_t rows_launch(const KvWork& w, bool vec, bool join, cudaStream_t s) {
   using S = Shape<D, NT, kWarps>;
   constexpr auto kVector = &kv_attention_rows_kernel<D, NT, kWarps, T, true>;
   constexpr auto kScalar = &kv_attention_rows_kernel<D, NT, kWarps, T, false>;
   cudaError_t e = vec ? kv_allow_smem<kVector>(S::kSmem) : kv_allow_smem<kScalar>(S::kSmem);
   if (e != cudaSuccess) return e;
   e = launch_chained(vec ? kVector : kScalar, dim3(w.ctas), dim3(32 * kWarps), S::kSmem, 1, s, w);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || !join) return e;
   return launch_chained(&kv_attention_join_kernel<D, S::kRows, T>, dim3(w.ctas), dim3(256), 0, 1, s, w);
 }
 
 template <int D, int NT, typename T>
-cudaError_t rows_typed(const KvAttentionArgs& a, long long rows_to, bool vec, cudaStream_t s) {
+cudaError_t rows_typed(const KvAttentionArgs& a, bool with_tiles, bool vec, cudaStream_t s, KvWork& w) {
   const int sms = num_sms();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  KvWork w{};
   w.a = a;
-  w.rows_to = rows_to;
+  w.rows_to = with_tiles ? kKvFewRows : LLONG_MAX;
   w.parts = static_cast<KvPart*>(a.workspace);
   w.ws = static_cast<uint8_t*>(a.workspace) + (size_t)sms * 2 * sizeof(KvPart);
   // one CTA an SM, but no more than the work can fill, as far as the table's width says
@@ -533,18 +531,18 @@ cudaError_t rows_typed(const KvAttentionArgs& a, long long rows_to, bool vec, cu
   if constexpr (NT == 1) {
     if (bound > 2ll * 8 * sms) {
       w.ctas = ctas(12);
-      return rows_launch<D, NT, 12, T>(w, vec, s);
+      return rows_launch<D, NT, 12, T>(w, vec, !with_tiles, s);
     }
   }
   w.ctas = ctas(8);
-  return rows_launch<D, NT, 8, T>(w, vec, s);
+  return rows_launch<D, NT, 8, T>(w, vec, !with_tiles, s);
 }
 
 template <int D>
-cudaError_t rows_sized(const KvAttentionArgs& a, bool one, long long rows_to, bool bf16, bool vec, cudaStream_t s) {
-  if (one)
-    return bf16 ? rows_typed<D, 1, __nv_bfloat16>(a, rows_to, vec, s) : rows_typed<D, 1, float>(a, rows_to, vec, s);
-  return bf16 ? rows_typed<D, 2, __nv_bfloat16>(a, rows_to, vec, s) : rows_typed<D, 2, float>(a, rows_to, vec, s);
+cudaError_t rows_sized(const KvAttentionArgs& a, bool with_tiles, bool bf16, bool vec, cudaStream_t s, KvWork& w) {
+  if (!with_tiles && row_tiles(a.group, a.max_tokens) == 1)
+    return bf16 ? rows_typed<D, 1, __nv_bfloat16>(a, false, vec, s, w) : rows_typed<D, 1, float>(a, false, vec, s, w);
+  return bf16 ? rows_typed<D, 2, __nv_bfloat16>(a, with_tiles, vec, s, w) : rows_typed<D, 2, float>(a, false, vec, s, w);
 }
 
 }  // namespace
@@ -556,16 +554,15 @@ size_t kv_attention_workspace(int rows, int batch, int heads, int group, int hea
 cudaError_t launch_kv_attention(const KvAttentionArgs& a, int head_dim, bool bf16, bool vec, cudaStream_t s,
                                 const char** kernel_name) {
   const Plan p = plan_of(a.batch.rows, a.batch.batch, a.group, head_dim, a.max_tokens, bf16);
+  KvWork few{};
   if (p.few) {
-    const bool one = !p.many && row_tiles(a.group, a.max_tokens) == 1;
-    const long long rows_to = p.many ? kFewRows : LLONG_MAX;
-    const cudaError_t e = head_dim == 64 ? rows_sized<64>(a, one, rows_to, bf16, vec, s)
-                                         : rows_sized<128>(a, one, rows_to, bf16, vec, s);
+    const cudaError_t e = head_dim == 64 ? rows_sized<64>(a, p.many, bf16, vec, s, few)
+                                         : rows_sized<128>(a, p.many, bf16, vec, s, few);
     if (e != cudaSuccess) return e;
     *kernel_name = "kv_attention_rows";
   }
   if (p.many) {
-    const cudaError_t e = launch_kv_attention_tiles(a, p.few ? kFewRows + 1 : 0,
+    const cudaError_t e = launch_kv_attention_tiles(a, p.few ? &few : nullptr,
                                                     static_cast<uint8_t*>(a.workspace) + p.few_bytes, head_dim, vec, s);
     if (e != cudaSuccess) return e;
     *kernel_name = p.few ? "kv_attention_rows+tiles" : "kv_attention_tiles";

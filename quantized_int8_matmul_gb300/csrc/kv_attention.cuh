@@ -23,12 +23,6 @@ struct alignas(16) KvPart {
 
 __host__ __device__ constexpr size_t kv_part_bytes(int dim, int rows) { return (size_t)rows * (dim + 2) * 4; }
 
-// The kernel for many rows (kv_attention_tiles.cu), of the sequences with at least
-// rows_from rows a key head.
-size_t kv_tiles_workspace(int head_dim);
-cudaError_t launch_kv_attention_tiles(const KvAttentionArgs& a, long long rows_from, void* workspace, int head_dim,
-                                      bool vec, cudaStream_t s);
-
 struct KvWork {
   KvAttentionArgs a;
   long long rows_from, rows_to;   // this kernel takes the sequences with so many rows a key head
@@ -36,6 +30,15 @@ struct KvWork {
   uint8_t* ws;                    // [ctas][2] parts of kRows * (D + 2) floats
   int ctas;
 };
+
+// Rows a key head up to which a sequence is the rows kernel's where a call launches both.
+constexpr int kKvFewRows = 16;
+// The kernel for many rows (kv_attention_tiles.cu), of the sequences with more than
+// kKvFewRows where `few` is the work that the rows kernel has done of the same call (its
+// parts are joined with this kernel's), of all where it is null.
+size_t kv_tiles_workspace(int head_dim);
+cudaError_t launch_kv_attention_tiles(const KvAttentionArgs& a, const KvWork* few, void* workspace, int head_dim, bool vec,
+                                      cudaStream_t s);
 
 // The kernels cut the work of a call alike: all (sequence, tile of R rows, key head)
 // items end to end in units of TK tokens, and to each worker the same number of
@@ -250,16 +253,13 @@ __device__ __forceinline__ void kv_join_row(int count, int rows, int row, F part
   }
 }
 
-// What several CTAs hold of an item, joined by the CTA with the number of the one that
-// holds its beginning.
+// What several CTAs hold of an item, joined by the CTAs with the number of the one that
+// holds its beginning: slice `slice` of `slices` of its rows.
 template <int D, int R, typename T>
-__global__ void __launch_bounds__(256) kv_attention_join_kernel(const KvWork w) {
-  chain_wait();
+__device__ __forceinline__ void kv_join_parts(const KvWork& w, int slice, int slices) {
+  if ((int)blockIdx.x >= w.ctas) return;
   const KvPart a = w.parts[2 * blockIdx.x + 1];
-  if (!(a.flags & kPartHeld)) {
-    chain_release();
-    return;
-  }
+  if (!(a.flags & kPartHeld)) return;
   // the following CTAs' first parts belong to the item, up to the one that ends it
   const int lane = threadIdx.x & 31;
   int n = 1;
@@ -273,14 +273,30 @@ __global__ void __launch_bounds__(256) kv_attention_join_kernel(const KvWork w) 
     n += 32;
   }
   n = min(n, w.ctas - (int)blockIdx.x);
-  chain_release();
   auto part = [&](int j) -> const uint8_t* {
     return w.ws + (size_t)(j == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + j)) * kv_part_bytes(D, R);
   };
-  for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < a.rows; row += 8 * gridDim.y) {
+  for (int row = slice * 8 + (threadIdx.x >> 5); row < a.rows; row += 8 * slices) {
     T* out = static_cast<T*>(w.a.out) + kv_out_row(w.a, a.start, a.h, a.first + row) * D;
     kv_join_row<D, T>(n, R, row, part, true, out, nullptr);
   }
+}
+template <int D, int R, typename T>
+__global__ void __launch_bounds__(256) kv_attention_join_kernel(const KvWork w) {
+  chain_wait();
+  kv_join_parts<D, R, T>(w, blockIdx.y, gridDim.y);
+  chain_release();
+}
+// The parts of both kernels in one launch: `few` by the last slice of the grid.
+template <int D, int RFew, int RMany, typename T>
+__global__ void __launch_bounds__(256) kv_attention_join_both_kernel(const KvWork few, const KvWork many) {
+  chain_wait();
+  if (blockIdx.y + 1 == gridDim.y) {
+    kv_join_parts<D, RFew, T>(few, 0, 1);
+  } else {
+    kv_join_parts<D, RMany, T>(many, blockIdx.y, gridDim.y - 1);
+  }
+  chain_release();
 }
 
 // The opt-in to a kernel's shared memory, once a device.

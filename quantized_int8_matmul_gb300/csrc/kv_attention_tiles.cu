@@ -144,24 +144,26 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return r;
 }
 
-// A wait of a whole warp, or of one lane of it, whose outcome is the same for all that
-// wait. Bounded by its tries, 2^22 of some tens of cycles, where the other kernels read
-// a clock: the waits here are short and many, and little code in each of them keeps the
-// roles, which share the instruction cache, from waiting for it.
-constexpr int kTries = 1 << 22;
-template <bool kWarp>
+// A wait of a whole warp, whose outcome is the same for all its lanes. Bounded by the
+// clock like the other kernels', which is read only every 65536 tries: the waits here are
+// many and mostly shorter than its reading. (A role may wait for as long as one item
+// takes, about 14 ms a million tokens.)
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* err,
                                          unsigned site) {
+  uint64_t t0 = 0;
 #pragma unroll 1
-  for (int i = 0;; ++i) {
-    const bool ok = mbar_try_wait(bar, parity);
-    if (kWarp ? __all_sync(~0u, ok) : ok) return true;
-    const bool end = i > kTries || *abort;
-    if (kWarp ? __any_sync(~0u, end) : end) break;
+  for (uint32_t i = 1;; ++i) {
+    if (__all_sync(~0u, mbar_try_wait(bar, parity))) return true;
+    if ((i & 0xffff) == 0) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (__any_sync(~0u, now - t0 > kWaitLimitNs)) {
+        record_error(err, site);
+        *abort = 1;
+      }
+    }
+    if ((i & 255) == 0 && __any_sync(~0u, *abort != 0)) return false;
   }
-  if (!*abort) record_error(err, site);
-  *abort = 1;
-  return false;
 }
 
 template <int N>
@@ -319,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
   chain_wait();
 
   auto wait = [&](uint64_t* bar, uint32_t parity, unsigned site) -> bool {
-    return wait_for<true>(bar, parity, &sm.abort, w.a.err, site);
+    return wait_for(bar, parity, &sm.abort, w.a.err, site);
   };
   // the CTA's runs in turn
   int run_slot = 0;
@@ -769,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
 }
 
 template <int D>
-cudaError_t tiles_sized(const KvWork& w, bool vec, cudaStream_t s) {
+cudaError_t tiles_sized(const KvWork& w, const KvWork* few, bool vec, cudaStream_t s) {
   constexpr auto kVector = &kv_attention_tiles_kernel<D, true>, kScalar = &kv_attention_tiles_kernel<D, false>;
   constexpr int bytes = (int)sizeof(Smem<D>);
   static_assert(bytes <= 227 * 1024, "one CTA an SM");
@@ -777,24 +779,28 @@ cudaError_t tiles_sized(const KvWork& w, bool vec, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = launch_chained(vec ? kVector : kScalar, dim3(w.ctas), dim3(kThreads), bytes, 1, s, w);
   if (e != cudaSuccess) return e;
-  return launch_chained(&kv_attention_join_kernel<D, kRows, __nv_bfloat16>, dim3(w.ctas, 16), dim3(256), 0, 1, s, w);
+  constexpr int kSlices = 16;
+  if (few)
+    return launch_chained(&kv_attention_join_both_kernel<D, kKvFewRows, kRows, __nv_bfloat16>, dim3(w.ctas, kSlices + 1),
+                          dim3(256), 0, 1, s, *few, w);
+  return launch_chained(&kv_attention_join_kernel<D, kRows, __nv_bfloat16>, dim3(w.ctas, kSlices), dim3(256), 0, 1, s, w);
 }
 
 }  // namespace
 
 size_t kv_tiles_workspace(int head_dim) { return (size_t)num_sms() * 2 * (sizeof(KvPart) + kv_part_bytes(head_dim, kRows)); }
 
-cudaError_t launch_kv_attention_tiles(const KvAttentionArgs& a, long long rows_from, void* workspace, int head_dim,
-                                      bool vec, cudaStream_t s) {
+cudaError_t launch_kv_attention_tiles(const KvAttentionArgs& a, const KvWork* few, void* workspace, int head_dim, bool vec,
+                                      cudaStream_t s) {
   KvWork w{};
   w.a = a;
-  w.rows_from = rows_from;
+  w.rows_from = few ? kKvFewRows + 1 : 0;
   w.rows_to = LLONG_MAX;
   w.ctas = num_sms();
   if (w.ctas <= 0) return cudaErrorInvalidDevice;
   w.parts = static_cast<KvPart*>(workspace);
   w.ws = static_cast<uint8_t*>(workspace) + (size_t)w.ctas * 2 * sizeof(KvPart);
-  return head_dim == 64 ? tiles_sized<64>(w, vec, s) : tiles_sized<128>(w, vec, s);
+  return head_dim == 64 ? tiles_sized<64>(w, few, vec, s) : tiles_sized<128>(w, few, vec, s);
 }
 
 }  // namespace qmm

@@ -198,10 +198,16 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) kv_append_ke
       if (p.batch.starts) {
         // the last sequence whose slots begin at w or before
         int count = 0;
-        for (int b0 = 0; b0 < p.batch.batch; b0 += 32) {
-          const int i = b0 + lane;
-          count += __popc(__ballot_sync(
-              ~0u, i < p.batch.batch && (max(__ldg(p.batch.starts + i), 0) >> 4) + 2 * i <= w));
+#pragma unroll 1
+        for (int b0 = 0; b0 < p.batch.batch; b0 += 128) {
+          int begins[4];   // four loads in flight
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = b0 + 32 * e + lane;
+            begins[e] = i < p.batch.batch ? (max(__ldg(p.batch.starts + i), 0) >> 4) + 2 * i : INT_MAX;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) count += __popc(__ballot_sync(~0u, begins[e] <= w));
         }
         b = count - 1;
         if (b >= 0) first = w - ((max(__ldg(p.batch.starts + b), 0) >> 4) + 2 * b);

@@ -1839,6 +1839,7 @@ qmm_status kv_arguments(const qmm_kv_cache* c, const qmm_kv_batch* b, KvCacheArg
   if (!dim_ok(c->pages) || !dim_ok(c->kv_heads) || !dim_ok(c->page) || !dim_ok(c->head_dim) || c->kv_heads < 1)
     return QMM_ERR_INVALID_ARG;
   if (!dim_ok(b->batch) || !dim_ok(b->width) || !dim_ok(b->rows)) return QMM_ERR_INVALID_ARG;
+  if (b->batch > INT_MAX / 4) return QMM_ERR_INVALID_ARG;   // the append's slots, two a sequence, are counted in ints
   if ((c->head_dim != 64 && c->head_dim != 128) || c->page < 16 || c->page % 16) return QMM_ERR_UNSUPPORTED;
   if (b->width > INT_MAX / c->page || b->rows > INT_MAX / c->kv_heads) return QMM_ERR_INVALID_ARG;
   if (!b->starts && b->rows != b->batch) return QMM_ERR_INVALID_ARG;

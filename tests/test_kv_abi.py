@@ -23,7 +23,7 @@ BAD_CACHE = [dict(k=None), dict(v=None), dict(k_exp=None), dict(v_exp=None), dic
              dict(kv_heads=0), dict(kv_heads=-1), dict(kv_heads=2 ** 31), dict(pages=2 ** 31)]
 ODD_CACHE = [dict(head_dim=96), dict(head_dim=256), dict(head_dim=0), dict(page=8), dict(page=24), dict(page=0)]
 BAD_BATCH = [dict(table=None), dict(lengths=None), dict(starts=None), dict(batch=-1), dict(width=-1), dict(rows=-1),
-             dict(width=2 ** 31 // 32), dict(rows=2 ** 30), dict(batch=2 ** 31)]
+             dict(width=2 ** 31 // 32), dict(rows=2 ** 30), dict(batch=2 ** 31), dict(batch=2 ** 29)]
 
 
 @pytest.fixture(scope="module")
