@@ -1,5 +1,5 @@
 // Attention over the 8-bit key-value cache for few rows: a token, or a few drafted
-// ones, of each sequence (and every length of float32 rows).
+// ones, of each sequence.
 //
 //   o = sum_j p_j v_j / sum_j p_j,   p_j = exp2(c q.k_j - m),   c = scale * log2(e)
 //
@@ -71,10 +71,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
-}
-__device__ __forceinline__ float half_low(uint32_t u) { return __half2float(__ushort_as_half((unsigned short)u)); }
-__device__ __forceinline__ float half_high(uint32_t u) {
-  return __half2float(__ushort_as_half((unsigned short)(u >> 16)));
 }
 template <int D, int NT, int kWarps, typename T, bool kVec>
 __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_rows_kernel(const KvWork w) {
@@ -237,7 +233,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_rows_kernel(const
                 const uint32_t hi = half_pair(a0, a1);
                 const int step = i * 4 + 2 * u + (p2 >> 1);
                 qf[0][nt][step][p2 & 1] = hi;
-                if constexpr (kSplit) qf[1][nt][step][p2 & 1] = half_pair(a0 - half_low(hi), a1 - half_high(hi));
+                if constexpr (kSplit) qf[1][nt][step][p2 & 1] = half_rest(a0, a1, hi);
               }
           const int seen = there ? kv_visible(at.s, row / w.a.group, w.a.causal) : 0;
           least = min(least, there ? seen : INT_MAX);
@@ -343,7 +339,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_rows_kernel(const
             const float w0 = p0 * vpow, w1 = p1 * vpow;
             const uint32_t hi = half_pair(w0, w1);
             pf[0][nt][r] = transpose8(hi);
-            if constexpr (kSplit) pf[1][nt][r] = transpose8(half_pair(w0 - half_low(hi), w1 - half_high(hi)));
+            if constexpr (kSplit) pf[1][nt][r] = transpose8(half_rest(w0, w1, hi));
           }
         // O^T
         uint32_t vw[4][kVW];
@@ -482,20 +478,22 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_rows_kernel(const
 // Two tiles of eight rows where one tile would not hold a sequence's rows.
 int row_tiles(int group, int max_tokens) { return (long long)group * max_tokens <= 8 ? 1 : 2; }
 
-// Which kernels a call needs. Sequences with up to kKvFewRows rows a key head are this
-// file's, and float32 rows of any number; more bfloat16 rows are the tensor cores'. A
-// call whose sequences all have max_tokens rows needs one kernel.
+// Which kernels a call needs. Sequences with up to few_rows rows a key head are this
+// file's, those with more the tensor cores' (tcgen05): a tile there is 128 rows, filled
+// or not, and one of float32, alone on its SM, takes as long as about two of the rows
+// kernel's of 16. A call whose sequences all have max_tokens rows needs one kernel.
+int few_rows(bool bf16) { return bf16 ? 16 : 32; }
 struct Plan {
   bool few, many;
   size_t few_bytes, bytes;   // the workspace: `few` first
 };
 Plan plan_of(int rows, int batch, int group, int head_dim, int max_tokens, bool bf16) {
   Plan p{};
-  p.many = bf16 && (long long)group * max_tokens > kKvFewRows;
+  p.many = (long long)group * max_tokens > few_rows(bf16);
   p.few = !p.many || (long long)max_tokens * batch != rows;
   const int part_rows = p.many ? 16 : 8 * row_tiles(group, max_tokens);
   if (p.few) p.few_bytes = (size_t)num_sms() * 2 * (sizeof(KvPart) + kv_part_bytes(head_dim, part_rows));
-  p.bytes = p.few_bytes + (p.many ? kv_tiles_workspace(head_dim) : 0);
+  p.bytes = p.few_bytes + (p.many ? kv_tiles_workspace(head_dim, bf16) : 0);
   return p;
 }
 
@@ -516,7 +514,7 @@ cudaError_t rows_typed(const KvAttentionArgs& a, bool with_tiles, bool vec, cuda
   const int sms = num_sms();
   if (sms <= 0) return cudaErrorInvalidDevice;
   w.a = a;
-  w.rows_to = with_tiles ? kKvFewRows : LLONG_MAX;
+  w.rows_to = with_tiles ? few_rows(sizeof(T) == 2) : LLONG_MAX;
   w.parts = static_cast<KvPart*>(a.workspace);
   w.ws = static_cast<uint8_t*>(a.workspace) + (size_t)sms * 2 * sizeof(KvPart);
   // one CTA an SM, but no more than the work can fill, as far as the table's width says
@@ -542,7 +540,7 @@ template <int D>
 cudaError_t rows_sized(const KvAttentionArgs& a, bool with_tiles, bool bf16, bool vec, cudaStream_t s, KvWork& w) {
   if (!with_tiles && row_tiles(a.group, a.max_tokens) == 1)
     return bf16 ? rows_typed<D, 1, __nv_bfloat16>(a, false, vec, s, w) : rows_typed<D, 1, float>(a, false, vec, s, w);
-  return bf16 ? rows_typed<D, 2, __nv_bfloat16>(a, with_tiles, vec, s, w) : rows_typed<D, 2, float>(a, false, vec, s, w);
+  return bf16 ? rows_typed<D, 2, __nv_bfloat16>(a, with_tiles, vec, s, w) : rows_typed<D, 2, float>(a, with_tiles, vec, s, w);
 }
 
 }  // namespace
@@ -563,7 +561,8 @@ cudaError_t launch_kv_attention(const KvAttentionArgs& a, int head_dim, bool bf1
   }
   if (p.many) {
     const cudaError_t e = launch_kv_attention_tiles(a, p.few ? &few : nullptr,
-                                                    static_cast<uint8_t*>(a.workspace) + p.few_bytes, head_dim, vec, s);
+                                                    static_cast<uint8_t*>(a.workspace) + p.few_bytes, head_dim, bf16,
+                                                    vec, s);
     if (e != cudaSuccess) return e;
     *kernel_name = p.few ? "kv_attention_rows+tiles" : "kv_attention_tiles";
   }

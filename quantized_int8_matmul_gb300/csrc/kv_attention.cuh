@@ -31,14 +31,12 @@ struct KvWork {
   int ctas;
 };
 
-// Rows a key head up to which a sequence is the rows kernel's where a call launches both.
-constexpr int kKvFewRows = 16;
-// The kernel for many rows (kv_attention_tiles.cu), of the sequences with more than
-// kKvFewRows where `few` is the work that the rows kernel has done of the same call (its
-// parts are joined with this kernel's), of all where it is null.
-size_t kv_tiles_workspace(int head_dim);
-cudaError_t launch_kv_attention_tiles(const KvAttentionArgs& a, const KvWork* few, void* workspace, int head_dim, bool vec,
-                                      cudaStream_t s);
+// The kernel for many rows (kv_attention_tiles.cu): of all sequences, or, where `few` is
+// the work that the rows kernel has done of the same call, of those with more rows than
+// it takes (whose parts are then joined with this kernel's).
+size_t kv_tiles_workspace(int head_dim, bool bf16);
+cudaError_t launch_kv_attention_tiles(const KvAttentionArgs& a, const KvWork* few, void* workspace, int head_dim, bool bf16,
+                                      bool vec, cudaStream_t s);
 
 // The kernels cut the work of a call alike: all (sequence, tile of R rows, key head)
 // items end to end in units of TK tokens, and to each worker the same number of
@@ -321,6 +319,11 @@ __device__ __forceinline__ float exp2_approx(float x) {
 __device__ __forceinline__ uint32_t half_pair(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+// What is left of a and b beside their fp16 pair, in fp16.
+__device__ __forceinline__ uint32_t half_rest(float a, float b, uint32_t pair) {
+  const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&pair));
+  return half_pair(a - h.x, b - h.y);
 }
 // Two int8, biased by 128, to two fp16: bytes 0 and 1 of u, or 2 and 3. The byte becomes
 // the low mantissa bits of 1024, whose ulp is 1, and 1024 + 128 is taken off, exactly.

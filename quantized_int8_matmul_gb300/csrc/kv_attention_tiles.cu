@@ -1,5 +1,5 @@
 // Attention over the 8-bit key-value cache for many rows: prompts, pieces of them, an
-// encoder's states, on the tensor cores (tcgen05), bfloat16 queries.
+// encoder's states, on the tensor cores (tcgen05).
 //
 // What bounds it is arithmetic: 4 D operations a pair of a query row and a token, on the
 // tensor cores, and one exponential. A CTA takes 256 rows of one sequence and key head
@@ -23,18 +23,25 @@
 // The work is cut like that of the other kernel (kv_attention.cuh), a unit being a tile
 // of 128 tokens, so that short and long rows of causal prompts balance.
 //
-// Measured: a prompt of 8192 tokens, 32 query heads on 8 of 128, 450 us (1220 TFLOP/s);
-// 8192 x 8192 not causal 800 us (1375); 500 tokens over 32000 206 us (1262). A tile of 256
-// x 128 takes about 3300 cycles: its MMAs 2080, its traffic in shared memory (320 KB: Q
-// and K 128, V 64, copies and conversion 128) 2560, one tile's softmax 1500. Sixteen
-// softmax warps with half a row each, and taking half of P before the maximum is known,
-// were slower (853 and 889 us for the 800).
+// Float32 queries take one tile of 128 rows: Q in two fp16 parts (22 bits) fills both
+// tiles' places, P in two parts all the columns of S, and either product runs twice.
+//
+// Measured: a prompt of 8192 tokens, 32 query heads on 8 of 128, 435 us (1263 TFLOP/s),
+// float32 1247 us; 8192 x 8192 not causal 775 us (1420); 500 tokens over 32000 200 us
+// (1300). A tile of 256 x 128 takes about 3200 cycles: its MMAs 2080, its traffic in shared
+// memory (320 KB: Q and K 128, V 64, copies and conversion 128) 2560, one tile's softmax
+// 1500. Sixteen softmax warps with half a row each, and taking half of P before the maximum
+// is known, were slower (853 and 889 us where this took 798).
 #include "kv_attention.cuh"
 
 namespace qmm {
 namespace {
 
-constexpr int kRows = 256, kTokens = 128;
+constexpr int kTokens = 128;
+// Rows of an item: two tiles of 128, or one of float32, whose two fp16 parts take the
+// places of both.
+template <typename T>
+constexpr int kTileRows = sizeof(T) == 4 ? 128 : 256;
 constexpr int kThreads = 512;
 // Registers a thread of the softmax, of the converters and of the rest: the launch has 128 each.
 constexpr int kSoftmaxRegs = 192, kConvertRegs = 80, kRestRegs = 48;
@@ -219,9 +226,78 @@ struct Row {
   float coef;    // scores: coef * 2^(byte - 127) * S
   int limit;     // tokens that the row sees; INT_MAX for a row that is not there
 };
-template <int D, bool kVec>
+template <int D, typename T, bool kVec>
 __device__ __forceinline__ Row load_rows(const KvWork& w, const Run& run, int first, uint32_t q) {
+  constexpr int kRows = kTileRows<T>;
   const int lane = threadIdx.x & 31;
+  if constexpr (sizeof(T) == 4) {
+    // Float32: the first half of a row comes into its place in one operand, the second half into that in the other;
+    // what they become, the row's two fp16 parts, is held until both have been read.
+    constexpr uint32_t kOther = 128 * D * 2;
+    constexpr int kHalf = D / 8, kLanes = 2 * kHalf, kAtOnce = 32 / kLanes;   // pieces of half a row, of a row; rows
+    const int piece = lane % kLanes;
+    {
+      int row = lane / kLanes;
+      Walk walk(run.r * kRows + first + row, kAtOnce, w.a.group, w.a.q_row, w.a.q_head);
+      const float* src = static_cast<const float*>(w.a.q) + (long long)run.start * w.a.q_row +
+                         (long long)run.h * w.a.group * w.a.q_head + piece * 4;
+      const int within = piece % kHalf;
+      const uint32_t to = q + (uint32_t)(piece / kHalf) * kOther + (uint32_t)(within >> 3) * 16384u;
+#pragma unroll 4
+      for (int i = 0; i < 32 / kAtOnce; ++i, row += kAtOnce, walk.next()) {
+        const uint32_t dst = to + (uint32_t)row * 128u + (((within & 7) ^ (row & 7)) << 4);
+        const float* at = src + walk.at;
+        if (first + row >= run.rows) {
+          st_shared_v4(dst, 0, 0, 0, 0);
+        } else if constexpr (kVec) {
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(at) : "memory");
+        } else {
+          st_shared_v4(dst, __float_as_uint(at[0]), __float_as_uint(at[1]), __float_as_uint(at[2]), __float_as_uint(at[3]));
+        }
+      }
+      if constexpr (kVec) asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+    }
+    const uint32_t mine = q + (uint32_t)lane * 128u, swz = (uint32_t)(lane & 7) << 4;
+    auto place = [&](int i) {   // piece i of the row in one operand
+      return mine + (uint32_t)(i >> 3) * 16384u + (((uint32_t)(i & 7) << 4) ^ swz);
+    };
+    auto from = [&](int i) { return place(i % kHalf) + (i >= kHalf ? kOther : 0u); };   // of the row as it came
+    uint32_t top = 0;   // magnitudes compare as integers; a NaN is above an infinity
+#pragma unroll 4
+    for (int i = 0; i < kLanes; ++i) {
+      const uint4 x = ld_shared_v4(from(i));
+      top = max(max(max(top, x.x & 0x7fffffffu), max(x.y & 0x7fffffffu, x.z & 0x7fffffffu)), x.w & 0x7fffffffu);
+    }
+    const bool bad = top >= 0x7f800000u;
+    const int e = min(max((int)(top >> 23), 27), 254);
+    const float scale = w.a.scale;
+    float up = __int_as_float((127 + 14 + 127 - e) << 23);
+    up = scale < 0.f ? -up : scale == 0.f ? 0.f : up;
+    uint32_t hi[D / 2], lo[D / 2];
+#pragma unroll
+    for (int i = 0; i < kLanes; ++i) {
+      const uint4 x = ld_shared_v4(from(i));
+      const float y[4] = {__uint_as_float(x.x) * up, __uint_as_float(x.y) * up, __uint_as_float(x.z) * up,
+                          __uint_as_float(x.w) * up};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        hi[2 * i + k] = bad ? 0x7e007e00u : half_pair(y[2 * k], y[2 * k + 1]);
+        lo[2 * i + k] = bad ? 0u : half_rest(y[2 * k], y[2 * k + 1], hi[2 * i + k]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i) {
+      st_shared_v4(place(i), hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+      st_shared_v4(place(i) + kOther, lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+    }
+    Row out{1.f, INT_MAX};
+    if (scale != 0.f) out.coef = fabsf(scale) * 1.4426950408889634f * __int_as_float((e - 14) << 23);
+    if (first + lane < run.rows)
+      out.limit = kv_visible(KvSeq{0, run.n, run.len, run.seen},
+                             (unsigned)(run.r * kRows + first + lane) / (unsigned)w.a.group, w.a.causal);
+    return out;
+  } else {
   constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;   // of a row; rows
   const int piece = lane % kLanes;
   {
@@ -277,10 +353,13 @@ __device__ __forceinline__ Row load_rows(const KvWork& w, const Run& run, int fi
     out.limit = kv_visible(KvSeq{0, run.n, run.len, run.seen},
                            (unsigned)(run.r * kRows + first + lane) / (unsigned)w.a.group, w.a.causal);
   return out;
+  }
 }
 
-template <int D, bool kVec>
+template <int D, typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const KvWork w) {
+  constexpr int kRows = kTileRows<T>;
+  constexpr bool kSplit = sizeof(T) == 4;   // float32: Q and P in two fp16 parts each
   extern __shared__ __align__(1024) uint8_t raw[];
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
   constexpr int kQTile = Smem<D>::kQTile;
@@ -354,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
     const int first = x * 128 + (warp & 3) * 32;   // the warp's first row
     const uint32_t q_rows = smem_u32(sm.q) + x * kQTile + (warp & 3) * 32 * 128;
     auto put_rows = [&] {
-      me = load_rows<D, kVec>(w, now, first, q_rows);
+      me = load_rows<D, T, kVec>(w, now, first, q_rows);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.q_full[x]);
@@ -419,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
           float sum = 0.f;
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            uint32_t p[32];
+            uint32_t p[32], rest[kSplit ? 32 : 1];
 #pragma unroll
             for (int k = 4 * half; k < 4 * half + 4; ++k) {
               const float add = info.vdown[k] + base;
@@ -432,10 +511,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
                 const float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
                 part = i ? add2(part, e) : e;
                 p[8 * (k & 3) + i] = half_pair(e.x, e.y);
+                if constexpr (kSplit) rest[8 * (k & 3) + i] = half_rest(e.x, e.y, p[8 * (k & 3) + i]);
               }
               sum += (part.x + part.y) * info.vup[k];
             }
             tmem_st32_async(s_tmem + 32 * half, p);
+            if constexpr (kSplit) tmem_st32_async(s_tmem + 64 + 32 * half, rest);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -463,7 +544,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
         const float2 factor = small ? make_float2(inv, inv) : make_float2(both, both);
         uint8_t* const part = w.ws + (size_t)(2 * blockIdx.x + slot) * kv_part_bytes(D, kRows);
         if (!whole) reinterpret_cast<float2*>(part + kRows * D * 4)[first + lane] = make_float2(m, l);
-        const int step = whole ? D : D / 2;                // columns at a time: 2 D bytes of a row
+        const bool narrow = whole && !kSplit;              // to bfloat16
+        const int step = narrow ? D : D / 2;               // columns at a time: 2 D bytes of a row
         constexpr int kPieces = D / 8, kAtOnce = 32 / kPieces;   // pieces of 16 bytes of them; rows
         const int piece = lane % kPieces;
         const uint32_t mine_at = q_rows + (uint32_t)lane * 128u, swz = (uint32_t)(lane & 7) << 4;
@@ -488,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
             auto put = [&](int p, uint32_t u0, uint32_t u1, uint32_t u2, uint32_t u3) {
               st_shared_v4(mine_at + (uint32_t)(p >> 3) * 16384u + (((uint32_t)(p & 7) << 4) ^ swz), u0, u1, u2, u3);
             };
-            if (whole) {
+            if (narrow) {
 #pragma unroll
               for (int e = 0; e < 32; e += 8) {
                 uint32_t u[4];
@@ -510,8 +592,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
           int row = lane / kPieces;
           // in bytes; a part's rows follow each other
           const long long out_heads = (long long)w.a.cache.heads * w.a.group;
-          Walk walk(was.r * kRows + first + row, kAtOnce, w.a.group, out_heads * (2 * D), 2 * D);
-          uint8_t* to = static_cast<uint8_t*>(w.a.out) + (was.start * out_heads + was.h * w.a.group) * (2 * D) + piece * 16;
+          constexpr int kHead = D * (int)sizeof(T);
+          Walk walk(was.r * kRows + first + row, kAtOnce, w.a.group, out_heads * kHead, kHead);
+          uint8_t* to = static_cast<uint8_t*>(w.a.out) + (was.start * out_heads + was.h * w.a.group) * kHead +
+                        (narrow ? 0 : 4 * col) + piece * 16;
           if (!whole) {
             walk = Walk(first + row, kAtOnce, 1, 4 * D, 0);
             to = part + 4 * col + piece * 16;
@@ -632,6 +716,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
 #pragma unroll
                 for (int i = half * (kBlocks / 2); i < (half + 1) * (kBlocks / 2); ++i)
                   mma_one(lead, o, p + 8 * i, v + 128u * i, o_desc, j > 0 || i > 0);
+                if constexpr (kSplit) {
+#pragma unroll
+                  for (int i = half * (kBlocks / 2); i < (half + 1) * (kBlocks / 2); ++i)
+                    mma_one(lead, o, p + 64 + 8 * i, v + 128u * i, o_desc, 1);
+                }
               }
               if (!ok) break;
               p_phase ^= 1u << x;
@@ -651,6 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
               for (int i = 0; i < D / 16; ++i) {
                 const uint32_t step = (uint32_t)((i >> 2) * 16384 + (i & 3) * 32) / 16;
                 mma_one(lead, tm + (uint32_t)x * 128u, q + step, k + step, s_desc, i > 0);
+                if constexpr (kSplit) mma_one(lead, tm, q + kQTile / 16 + step, k + step, s_desc, 1);
               }
               commit_one(lead, &sm.s_full[x]);
             }
@@ -770,37 +860,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
   if (warp == 12) tmem_dealloc(tmem, 512);
 }
 
-template <int D>
+template <int D, typename T>
 cudaError_t tiles_sized(const KvWork& w, const KvWork* few, bool vec, cudaStream_t s) {
-  constexpr auto kVector = &kv_attention_tiles_kernel<D, true>, kScalar = &kv_attention_tiles_kernel<D, false>;
-  constexpr int bytes = (int)sizeof(Smem<D>);
+  constexpr auto kVector = &kv_attention_tiles_kernel<D, T, true>, kScalar = &kv_attention_tiles_kernel<D, T, false>;
+  constexpr int bytes = (int)sizeof(Smem<D>), kRows = kTileRows<T>, kSlices = 16;
   static_assert(bytes <= 227 * 1024, "one CTA an SM");
   cudaError_t e = vec ? kv_allow_smem<kVector>(bytes) : kv_allow_smem<kScalar>(bytes);
   if (e != cudaSuccess) return e;
   e = launch_chained(vec ? kVector : kScalar, dim3(w.ctas), dim3(kThreads), bytes, 1, s, w);
   if (e != cudaSuccess) return e;
-  constexpr int kSlices = 16;
   if (few)
-    return launch_chained(&kv_attention_join_both_kernel<D, kKvFewRows, kRows, __nv_bfloat16>, dim3(w.ctas, kSlices + 1),
-                          dim3(256), 0, 1, s, *few, w);
-  return launch_chained(&kv_attention_join_kernel<D, kRows, __nv_bfloat16>, dim3(w.ctas, kSlices), dim3(256), 0, 1, s, w);
+    return launch_chained(&kv_attention_join_both_kernel<D, 16, kRows, T>, dim3(w.ctas, kSlices + 1), dim3(256), 0, 1, s,
+                          *few, w);
+  return launch_chained(&kv_attention_join_kernel<D, kRows, T>, dim3(w.ctas, kSlices), dim3(256), 0, 1, s, w);
 }
 
 }  // namespace
 
-size_t kv_tiles_workspace(int head_dim) { return (size_t)num_sms() * 2 * (sizeof(KvPart) + kv_part_bytes(head_dim, kRows)); }
+size_t kv_tiles_workspace(int head_dim, bool bf16) {
+  return (size_t)num_sms() * 2 * (sizeof(KvPart) + kv_part_bytes(head_dim, bf16 ? kTileRows<__nv_bfloat16> : kTileRows<float>));
+}
 
-cudaError_t launch_kv_attention_tiles(const KvAttentionArgs& a, const KvWork* few, void* workspace, int head_dim, bool vec,
-                                      cudaStream_t s) {
+cudaError_t launch_kv_attention_tiles(const KvAttentionArgs& a, const KvWork* few, void* workspace, int head_dim, bool bf16,
+                                      bool vec, cudaStream_t s) {
   KvWork w{};
   w.a = a;
-  w.rows_from = few ? kKvFewRows + 1 : 0;
+  w.rows_from = few ? few->rows_to + 1 : 0;
   w.rows_to = LLONG_MAX;
   w.ctas = num_sms();
   if (w.ctas <= 0) return cudaErrorInvalidDevice;
   w.parts = static_cast<KvPart*>(workspace);
   w.ws = static_cast<uint8_t*>(workspace) + (size_t)w.ctas * 2 * sizeof(KvPart);
-  return head_dim == 64 ? tiles_sized<64>(w, few, vec, s) : tiles_sized<128>(w, few, vec, s);
+  if (head_dim == 64)
+    return bf16 ? tiles_sized<64, __nv_bfloat16>(w, few, vec, s) : tiles_sized<64, float>(w, few, vec, s);
+  return bf16 ? tiles_sized<128, __nv_bfloat16>(w, few, vec, s) : tiles_sized<128, float>(w, few, vec, s);
 }
 
 }  // namespace qmm

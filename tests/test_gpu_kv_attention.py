@@ -137,61 +137,70 @@ def test_same_call_same_bits(q):
 @pytest.mark.parametrize("dim,page,heads,group", [(64, 16, 2, 1), (128, 64, 1, 4), (64, 48, 1, 3), (128, 16, 2, 8),
                                                   (128, 128, 1, 1)])
 @pytest.mark.parametrize("causal", [True, False])
-def test_prompts(q, dim, page, heads, group, causal):
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_prompts(q, kind, dim, page, heads, group, causal):
     """Sequences of many rows, alone and among short ones; ends inside tiles of rows and of tokens."""
     for seqs in ([(200, 200)], [(17, 17), (129, 300), (1, 400), (0, 3), (64, 64), (2, 1), (70, 40)],
                  [(128, 128), (128, 257)]):
-        run(q, Batch(seqs, heads, dim, page, seed=dim), "bf16", group, causal)
+        run(q, Batch(seqs, heads, dim, page, seed=dim), kind, group, causal)
 
 
 def test_prompts_of_equal_length_take_one_kernel(q):
-    run(q, Batch([(40, 300), (40, 40), (40, 39)], 2, 64, 16), "bf16", 4, max_tokens=40, kernel="kv_attention_tiles")
-    run(q, Batch([(40, 300), (3, 40)], 2, 64, 16), "bf16", 4, max_tokens=40, kernel="kv_attention_rows+tiles")
-    run(q, Batch([(4, 300), (3, 40)], 2, 64, 16), "bf16", 4, max_tokens=4, kernel="kv_attention_rows")
+    for kind, few in (("bf16", 4), ("f32", 8)):
+        run(q, Batch([(40, 300), (40, 40), (40, 39)], 2, 64, 16), kind, 4, max_tokens=40, kernel="kv_attention_tiles")
+        run(q, Batch([(40, 300), (3, 40)], 2, 64, 16), kind, 4, max_tokens=40, kernel="kv_attention_rows+tiles")
+        run(q, Batch([(few, 300), (3, 40)], 2, 64, 16), kind, 4, max_tokens=few, kernel="kv_attention_rows")
 
 
 def test_a_wrong_hint_costs_time_only(q):
-    for hint in (1, 3, 1000):
-        run(q, Batch([(40, 300), (3, 40), (17, 60)], 2, 128, 16), "bf16", 4, max_tokens=hint)
+    for kind in ("bf16", "f32"):
+        for hint in (1, 3, 1000):
+            run(q, Batch([(40, 300), (3, 40), (17, 60)], 2, 128, 16), kind, 4, max_tokens=hint)
 
 
 def test_prompt_pieces_are_split_over_tokens(q):
     """Few items, many tokens: parts of one item from several CTAs."""
-    run(q, Batch([(33, 6000)], 1, 128, 64, seed=3), "bf16", 4)
-    run(q, Batch([(20, 3000), (5, 9)], 1, 64, 16, seed=3), "bf16", 8)
+    for kind in ("bf16", "f32"):
+        run(q, Batch([(33, 6000)], 1, 128, 64, seed=3), kind, 4)
+        run(q, Batch([(20, 3000), (5, 9)], 1, 64, 16, seed=3), kind, 8)
 
 
 def test_prompts_with_bad_pages_and_short_tables(q):
     seqs = [(40, 100), (30, 300), (33, 33)]
-    run(q, Batch(seqs, 2, 64, 16, bad=((0, 0, -1), (0, 3, 1 << 30), (1, 1, 500), (1, 8, -2), (2, 0, -5))), "bf16", 2)
-    run(q, Batch(seqs, 2, 128, 16, width=7), "bf16", 3)
-    run(q, Batch(seqs, 2, 64, 48, width=0), "bf16", 2)
+    bad = ((0, 0, -1), (0, 3, 1 << 30), (1, 1, 500), (1, 8, -2), (2, 0, -5))
+    for kind in ("bf16", "f32"):
+        run(q, Batch(seqs, 2, 64, 16, bad=bad), kind, 2)
+        run(q, Batch(seqs, 2, 128, 16, width=7), kind, 3)
+        run(q, Batch(seqs, 2, 64, 48, width=0), kind, 2)
 
 
-def test_prompt_scales_queries_and_strides(q):
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_prompt_scales_queries_and_strides(q, kind):
     for order in (1, -1):
         b = Batch([(40, 700), (20, 90)], 2, 64, 16, seed=4)
         b.ve[:] = np.linspace(100, 140, b.ve.size).astype(np.uint8).reshape(b.ve.shape)[::order]
         b.ke[:] = b.rng.integers(100, 122, b.ke.shape)
-        run(q, b, "bf16", 2, stride=1)
+        run(q, b, kind, 2, stride=1)
     b = Batch([(24, 200)], 1, 128, 16, seed=5)
     mags = np.resize([1e-38, 1e-20, 1e-3, 1, 3, 0], 24)[:, None, None]
-    run(q, b, "bf16", 2, x=rounded(b.rng.standard_normal((24, 2, 128)) * mags, "bf16"), stride=8, extra=5)
+    run(q, b, kind, 2, x=rounded(b.rng.standard_normal((24, 2, 128)) * mags, kind), stride=8, extra=5)
+    run(q, Batch([(50, 200)], 1, 128, 16, seed=5), kind, 2, stride=1)
     for scale in (0.0, -0.3, 2.0):
-        run(q, Batch([(40, 150), (18, 17)], 2, 64, 16, seed=7), "bf16", 2, scale=scale)
+        run(q, Batch([(40, 150), (18, 17)], 2, 64, 16, seed=7), kind, 2, scale=scale)
 
 
-def test_prompt_rows_that_are_not_finite(q):
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_prompt_rows_that_are_not_finite(q, kind):
     b = Batch([(40, 200)], 1, 64, 16, seed=6)
-    x = rounded(b.rng.standard_normal((40, 4, 64)) * 0.2, "bf16")
+    x = rounded(b.rng.standard_normal((40, 4, 64)) * 0.2, kind)
     bad = np.zeros((40, 4), bool)
     for i, (t, h) in enumerate(((0, 0), (17, 3), (39, 1))):
         x[t, h, 5 * i], bad[t, h] = (np.nan, np.inf, -np.inf)[i], True
     cache, table, lengths, starts = b.device(q)
-    y = q.qmm_kv_attention(torch.from_numpy(x).bfloat16().cuda(), cache, table, lengths, starts).double().cpu().numpy()
+    y = q.qmm_kv_attention(torch.from_numpy(x).to(TYPES[kind]).cuda(), cache, table, lengths, starts).double().cpu().numpy()
     assert np.isnan(y[bad]).all()
     x[bad] = 0
     exact, mag, top, seen = ko.attention(x.astype(np.float64), *b.cache_arrays(), b.table, b.lengths, b.starts,
                                          64 ** -0.5, True, detail=True)
-    bound = attention_bound(exact, mag, top, seen, "bf16", 64)
+    bound = attention_bound(exact, mag, top, seen, kind, 64)
     assert_attention(y[~bad], exact[~bad], bound[~bad])
