@@ -481,7 +481,10 @@ int row_tiles(int group, int max_tokens) { return (long long)group * max_tokens 
 // Which kernels a call needs. Sequences with up to few_rows rows a key head are this
 // file's, those with more the tensor cores' (tcgen05): a tile there is 128 rows, filled
 // or not, and one of float32, alone on its SM, takes as long as about two of the rows
-// kernel's of 16. A call whose sequences all have max_tokens rows needs one kernel.
+// kernel's of 16 (8 tokens of 4 heads over 32000 there, 12 here: 51 us both). For
+// bfloat16 two tiles of 16 rows are slower on long caches (64 sequences of up to 16384
+// with 24 rows each: 277 us, 247 here), if faster on short ones (one of 1021: 13 us, 23).
+// A call whose sequences all have max_tokens rows needs one kernel.
 int few_rows(bool bf16) { return bf16 ? 16 : 32; }
 struct Plan {
   bool few, many;
