@@ -31,7 +31,7 @@ __device__ __forceinline__ KvSeq kv_sequence(const KvBatchArgs& a, int b) {
     s1 = __ldg(a.starts + b + 1);
   }
   s.start = min(max(s0, 0), a.rows);
-  s.n = max(min(s1, a.rows) - s.start, 0);
+  s.n = max(min(max(s1, 0), a.rows) - s.start, 0);   // (a difference from -2^31 would wrap)
   s.len = max(__ldg(a.lengths + b), 0);
   s.seen = min(s.len, a.capacity);
   return s;

@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_rows_kernel(const
 #pragma unroll
           for (int c = 0; c < 4; ++c) sc[nt][c] *= coef[nt][c & 1] * kpow;
         const int token = at.at * kKvBlock + g;
-        if (at.at * kKvBlock + kKvBlock > least) {
+        if (at.at * kKvBlock > least - kKvBlock) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

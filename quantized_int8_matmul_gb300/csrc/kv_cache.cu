@@ -116,7 +116,7 @@ __device__ __forceinline__ void append_block(const KvAppendArgs& p, const KvSeq&
   for (int i = 0; i < kSteps; ++i) {
     const int pos = base + i * kTokens + ti;
     if (pos >= from && pos < to) {
-      const T* r = x + (long long)(s.start + pos - (s.len - s.n)) * row_stride;
+      const T* r = x + (long long)(s.start + (pos - (s.len - s.n))) * row_stride;
       ra[i].template load<kVec>(r + g.a);
       rb[i].template load<kVec>(r + g.b);
     }
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) kv_append_ke
             const bool key = task < heads;
             const int h = key ? task : task - heads;
             const size_t block = ((size_t)page * heads + h) * p.cache.bpp + blk % p.cache.bpp;
-            const int from = max(p0, base), to = min(s.seen, base + kKvBlock);
+            const int from = max(p0, base), to = base + min(s.seen - base, kKvBlock);
             if (key) {
               append_block<D, T, kVec>(p, s, base, from, to, block,
                                        static_cast<const T*>(p.k) + (long long)h * p.k_head, p.k_row, p.cache.k,
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) kv_append_ke
       const KvSeq s = kv_sequence(p.batch, b);
       if (t >= s.start && t < s.start + s.n) {
         float c[8], sn[8];
-        if (g.turn >= 0) load_turn(p, s.len - s.n + t - s.start, g.turn, c, sn);
+        if (g.turn >= 0) load_turn(p, s.len - s.n + (t - s.start), g.turn, c, sn);
         chain_release();
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadArgs p) {
     if (b >= 0) {
       const KvSeq s = kv_sequence(p.batch, b);
       if (t >= s.start && t < s.start + s.n) {
-        const int pos = s.len - s.n + t - s.start;
+        const int pos = s.len - s.n + (t - s.start);
         int page = -1, blk = 0;
         if (pos >= 0 && pos < s.seen) {
           blk = pos / kKvBlock;

@@ -228,3 +228,39 @@ def test_empty_calls():
     y = q.qmm_kv_attention(torch.ones(40, 4, 64, device="cuda").bfloat16(), empty, ints(0, 1).view(1, 2), ints(30),
                            starts=ints(0, 40))
     assert not y.any()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_sequences_that_make_no_sense_touch_nothing_else(kind):
+    """Starts out of order, negative or past the rows, lengths from -5 to 2^31 - 1: what comes out of them is not
+    defined, but nothing outside the outputs, the workspace and the named pages is written."""
+    t, heads, dim, page = TYPES[kind], 2, 64, 16
+    b = Batch([(9, 40)] * 5, heads, dim, page, seed=9, spare=6)
+    g = Guards()
+    cache = q.KvCache(*(g(a.shape, torch.from_numpy(a).dtype) for a in b.cache_arrays()))
+    for c, a in zip(cache, b.cache_arrays()):
+        c.copy_(torch.from_numpy(a))
+    table = torch.from_numpy(b.table).cuda()
+    rows = 45
+    x, k, v = (torch.randn(rows, h, dim, device="cuda").to(t) for h in (8, 2, 2))
+    cos, sin = (torch.from_numpy(a).cuda() for a in turns(64, 32))
+    used = set(b.table[b.table >= 0].tolist())
+    for starts in ([5, 2, 100, -3, 7, 45], [0, 2 ** 31 - 1, -2 ** 31, 30, 3, 1], [45, 0, 45, 0, 45, 0]):
+        for lengths in ([2 ** 31 - 1, -5, 40, 7, 0], [-2 ** 31, 1, 2 ** 30, 48, 49]):
+            for most in (1, 9, 45):
+                qo, out, kr, vr = (g((rows, h, dim), t) for h in (8, 8, 2, 2))
+                ws = g((q.qmm_kv_attention_workspace_bytes(rows, 5, 8, heads, dim, t, most),), torch.uint8)
+                s, n = ints(*starts), ints(*lengths)
+                q.qmm_kv_append(cache, k, v, table, n, starts=s, q=x, cos=cos, sin=sin, q_out=qo)
+                q.qmm_kv_read(cache, table, n, s, rows=rows, k_out=kr, v_out=vr)
+                for causal in (True, False):
+                    q.qmm_kv_attention(x, cache, table, n, starts=s, out=out, workspace=ws, causal=causal, max_tokens=most)
+    g.check()
+    q.check_device_error()
+    for c, a in zip(cache, b.cache_arrays()):
+        c = c.cpu().numpy()
+        for p in set(range(b.pages)) - used:
+            assert np.array_equal(c[p], a[p])
+    good = Batch([(1, 30), (40, 70)], heads, dim, page, seed=10)
+    y = rounded(good.rng.standard_normal((41, 4, dim)), kind)
+    check(good, y, q.qmm_kv_attention(torch.from_numpy(y).to(t).cuda(), *good.device(q)), kind)
