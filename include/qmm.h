@@ -669,13 +669,13 @@ qmm_status qmm_fp4_matmul(const void* a_packed, size_t a_bytes, int64_t M, const
  *                    head h reads key head h / (q_heads / kv_heads). Sums and maxima in
  *                    float32. A row that sees nothing gets zeros, one whose q holds a
  *                    NaN or an infinity NaN. out [rows, q_heads, head_dim] contiguous,
- *                    of q's dtype, not overlapping q. max_tokens: no sequence has more rows, as far as the
- *                    caller knows; it chooses kernels and splits, never results'
- *                    validity (rows: always true).
+ *                    of q's dtype, not overlapping q (out = q is refused). max_tokens:
+ *                    no sequence has more rows, as far as the caller knows; it chooses
+ *                    kernels and splits, never results' validity (rows: always true).
  *  workspace         qmm_kv_attention_workspace_bytes of the same arguments, 16-byte
  *                    aligned; nothing in it has to survive a call, or to be zero
  * rows = 0 or batch = 0 launches nothing. QMM_ERR_UNSUPPORTED for another head_dim, page
- * or `rotated`; QMM_ERR_INVALID_ARG for a bad dtype, stride, null or unaligned pointer,
+ * or `rotated`; QMM_ERR_INVALID_ARG for a bad dtype, stride, null or unaligned pointer, out = q,
  * short workspace, q_heads that kv_heads does not divide, starts = NULL with rows !=
  * batch, width * page or rows * q_heads beyond 2^31 - 1, batch beyond 2^29 - 1.
  */

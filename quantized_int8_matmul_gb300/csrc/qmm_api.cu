@@ -1962,7 +1962,8 @@ qmm_status qmm_kv_attention(const qmm_kv_cache* cache, const qmm_kv_batch* batch
     t_last_kernel = "none";
     return QMM_OK;
   }
-  if (!q || !out || !aligned16(out)) return QMM_ERR_INVALID_ARG;
+  // (a row of q is read by several CTAs, some of which are done before others begin)
+  if (!q || !out || out == q || !aligned16(out)) return QMM_ERR_INVALID_ARG;
   if (!workspace || !aligned16(workspace) ||
       workspace_bytes < qmm_kv_attention_workspace_bytes(batch->rows, batch->batch, q_heads, cache->kv_heads,
                                                          cache->head_dim, dtype, max_tokens))

@@ -52,8 +52,8 @@ def read(q, cache=None, batch=None, k=P, v=P, dt=None):
     return q.lib().qmm_kv_read(ctypes.byref(c), ctypes.byref(b), k, v, q.QMM_F32 if dt is None else dt, None)
 
 
-def attention(q, cache=None, batch=None, qp=P, dt=None, qr=256, qh=64, heads=4, scale=0.1, causal=1, most=5, out=P, ws=P,
-              wb=2 ** 40):
+def attention(q, cache=None, batch=None, qp=P, dt=None, qr=256, qh=64, heads=4, scale=0.1, causal=1, most=5,
+              out=ctypes.c_void_p(512), ws=P, wb=2 ** 40):
     c, b = structs(cache or {}, batch or {})
     return q.lib().qmm_kv_attention(ctypes.byref(c), ctypes.byref(b), qp, q.QMM_F32 if dt is None else dt, qr, qh, heads,
                                     scale, causal, most, out, ws, wb, None)
@@ -97,7 +97,7 @@ def test_read_refusals(qmm):
 
 def test_attention_refusals(qmm):
     bad = qmm.QMM_ERR_INVALID_ARG
-    for kw in (dict(qp=None), dict(out=None), dict(out=ODD), dict(qr=-1), dict(qh=-1), dict(heads=0), dict(heads=3),
+    for kw in (dict(qp=None), dict(out=None), dict(out=ODD), dict(out=P), dict(qr=-1), dict(qh=-1), dict(heads=0), dict(heads=3),
                dict(heads=2 ** 30), dict(scale=float("nan")), dict(scale=float("inf")), dict(causal=2), dict(most=0),
                dict(ws=None), dict(ws=ODD)):
         assert attention(qmm, **kw) == bad, kw
