@@ -402,11 +402,12 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_rows_kernel(const
             for (int d = 16; d >= 4; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             const int col = 8 * nt + 2 * t + c;
+            const float unlift = (into ? kKvPartScale : 1.f) / (1 << kLift);
             float y[kMT][2];
 #pragma unroll
             for (int i = 0; i < kMT; ++i) {
-              y[i][0] = o[i][nt][c] * inv * (1.f / (1 << kLift)) * vscale;
-              y[i][1] = o[i][nt][c + 2] * inv * (1.f / (1 << kLift)) * vscale;
+              y[i][0] = o[i][nt][c] * inv * unlift * vscale;
+              y[i][1] = o[i][nt][c + 2] * inv * unlift * vscale;
             }
             if (into) {
               float* dst = reinterpret_cast<float*>(into) + col * D + g * (D / 8);

@@ -176,10 +176,14 @@ __device__ __forceinline__ long long kv_out_row(const KvAttentionArgs& a, int st
          (row - token * a.group);
 }
 
-// Parts [first, first + count) of one item joined, one row by one warp: rows of O that
-// are already divided by their own sums l, with their maxima m. part(i) gives the
+// Parts [first, first + count) of one item joined, one row by one warp: halves of rows of
+// O that are already divided by their own sums l, with their maxima m. part(i) gives the
 // i-th part's bytes. The joined row is written to `out` (T, row index given) where it
 // is the whole item's, else as a part again.
+// Every sum is a mean, weights that add up to 1, and the parts are halved, because values
+// reach up to the end of float32's range: one that is stored as 64 * 2^122 lies just past
+// it, and is a row's own only where it is all that the row sees.
+constexpr float kKvPartScale = 0.5f;
 template <int D, typename T, typename F>
 __device__ __forceinline__ void kv_join_row(int count, int rows, int row, F part, bool whole, T* out, uint8_t* into) {
   constexpr int kE = D / 32;
@@ -212,20 +216,27 @@ __device__ __forceinline__ void kv_join_row(int count, int rows, int row, F part
     for (int j = 0; j < kAhead; ++j) up = fmaxf(up, ml[j].x);
     const float down = exp2f(top - up);
     top = up;
-    sum *= down;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) acc[e] *= down;
+    const float before = sum * down;
+    sum = before;
+    float weight[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      const float weight = ml[j].y * exp2f(ml[j].x - top);
-      sum += weight;
+      weight[j] = ml[j].y * exp2f(ml[j].x - top);
+      sum += weight[j];
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum, keep = before * inv;
 #pragma unroll
-      for (int e = 0; e < kE; ++e) acc[e] += weight * x[j][e];
+    for (int e = 0; e < kE; ++e) acc[e] *= keep;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+#pragma unroll
+      for (int e = 0; e < kE; ++e) acc[e] += weight[j] * inv * x[j][e];
     }
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  if (whole) {
 #pragma unroll
-  for (int e = 0; e < kE; ++e) acc[e] *= inv;
+    for (int e = 0; e < kE; ++e) acc[e] *= 1.f / kKvPartScale;
+  }
   if (!whole) {
     float* o = reinterpret_cast<float*>(into) + row * D + lane * kE;
 #pragma unroll

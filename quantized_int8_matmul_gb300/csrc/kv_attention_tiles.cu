@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
         // O by way of this warp's rows of Q, whose last use is over, so that neighbouring lanes write neighbouring
         // bytes: 256 bytes of each row at a time, as bfloat16 or, of a part, as float32
         // 1 / l and V's power in one factor where that is a normal number, else one after the other
-        const float inv = l == 0.f ? 0.f : 1.f / l, vscale = kv_power(vref), both = inv * vscale;
+        const float inv = l == 0.f ? 0.f : (whole ? 1.f : kKvPartScale) / l, vscale = kv_power(vref), both = inv * vscale;
         const bool small = __any_sync(~0u, both < 1.17549435e-38f);
         const float2 factor = small ? make_float2(inv, inv) : make_float2(both, both);
         uint8_t* const part = w.ws + (size_t)(2 * blockIdx.x + slot) * kv_part_bytes(D, kRows);
