@@ -25,7 +25,7 @@
 //
 // The running maximum moves only when some score is 8 (a factor of 256) above it,
 // which a vote finds out: P keeps six more bits below fp16's largest value and 30 bits
-// to its smallest. V's power of two goes into P the same way.
+// to its smallest. V's powers of two go into its fp16 (kv_attention.cuh).
 //
 // Measured, with the join: 64 sequences of up to 16384 tokens, 64 query heads on 8 of
 // 128, 114 us (6.0 TB/s, 89 % of a copy; the copies without arithmetic take as long); one
@@ -49,7 +49,9 @@ struct Shape {
   static constexpr int kRing = kStages * kStage;                  // a warp's
   static constexpr int kPartBytes = (int)kv_part_bytes(D, kRows);   // rows of O, then (m, l) each
   static_assert(kRing >= kPartBytes, "a warp's last part takes the place of its ring");
-  static constexpr int kSmem = kWarps * (kRing + kPartBytes) + 2 * kWarps * (int)sizeof(KvPart);
+  static constexpr int kParts = kWarps * (kRing + kPartBytes);      // where the parts' descriptions are
+  static constexpr int kState = kParts + 2 * kWarps * (int)sizeof(KvPart);
+  static constexpr int kSmem = kState + kWarps * kRows * (int)sizeof(float2);
   static_assert(kSmem <= 227 * 1024, "one CTA an SM");
 };
 
@@ -85,7 +87,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_rows_kernel(const
   const int g = lane >> 2, t = lane & 3;
   uint8_t* const ring = smem + warp * S::kRing;
   uint8_t* const first_part = smem + kWarps * S::kRing + warp * S::kPartBytes;
-  KvPart* const parts = reinterpret_cast<KvPart*>(smem + kWarps * (S::kRing + S::kPartBytes));
+  KvPart* const parts = reinterpret_cast<KvPart*>(smem + S::kParts);
+  float2* const state = reinterpret_cast<float2*>(smem + S::kState) + warp * S::kRows;   // of each row: below
   if (lane < 2) parts[2 * warp + lane] = KvPart{};
   chain_wait();
 
@@ -172,7 +175,11 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_rows_kernel(const
     int lim[NT][2];
     float m[NT][2], l[NT][2];
     float o[kMT][NT][4];
-    int vref = 0, least = 0;
+    int least = 0;
+    // `settled`: all rows that have seen anything have O in the present window, and l in units of 2^m; else `state`
+    // holds what the two are, (behind, window), for each row.
+    int window = kKvNoWindow;
+    bool settled = true;
     bool fresh = true, begins = at.at == 0;
     int stage = 0;
 #pragma unroll 1
@@ -251,7 +258,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_rows_kernel(const
         }
 #pragma unroll
         for (int d = 16; d >= 4; d >>= 1) least = min(least, __shfl_xor_sync(~0u, least, d));
-        vref = 0;
+        window = kKvNoWindow;
+        settled = true;
       }
 
       // fetch the block kStages - 1 ahead, over the one that all lanes have read, then wait for this one's copies
@@ -305,10 +313,42 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_rows_kernel(const
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 4; ++c) over |= sc[nt][c] > m[nt][c & 1] + kKvSlack;
-        over |= ve > vref;
-        if (__any_sync(~0u, over)) {
-          const float vdown = ve > vref ? exp2f((float)(vref - ve)) : 1.f;
-          vref = max(vref, ve);
+        const bool moved = !kv_in_window(ve, window);
+        const bool first = window == kKvNoWindow;
+        const int was = window;
+        if (moved) window = kv_window(ve, ve);
+        if (!first && (moved || !settled)) {
+          bool now_settled = true;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float top = fmaxf(sc[nt][c], sc[nt][c + 2]), largest = 0.f;
+#pragma unroll
+              for (int i = 0; i < kMT; ++i) largest = fmaxf(largest, fmaxf(fabsf(o[i][nt][c]), fabsf(o[i][nt][c + 2])));
+#pragma unroll
+              for (int d = 16; d >= 4; d >>= 1) {
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+                largest = fmaxf(largest, __shfl_xor_sync(~0u, largest, d));
+              }
+              float2* const mine = state + 8 * nt + 2 * t + c;
+              const float2 held = *mine;
+              KvUnit u{m[nt][c], settled ? 0.f : held.x, settled ? was : __float_as_int(held.y)};
+              const float scale = exp2_approx(kv_change_units(u, l[nt][c], top, largest, window));
+              m[nt][c] = u.m;
+#pragma unroll
+              for (int i = 0; i < kMT; ++i) {
+                o[i][nt][c] *= scale;
+                o[i][nt][c + 2] *= scale;
+              }
+              now_settled &= u.m == kKvNone || (u.window == window && u.behind == 0.f);
+              sc[nt][c] += fmaxf(u.behind - kKvFar, 0.f);
+              sc[nt][c + 2] += fmaxf(u.behind - kKvFar, 0.f);
+              __syncwarp();   // the column's lanes have all read it
+              *mine = make_float2(u.behind, __int_as_float(u.window));
+            }
+          settled = __all_sync(~0u, now_settled);
+        } else if (__any_sync(~0u, over)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -322,26 +362,31 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_rows_kernel(const
               l[nt][c] *= down;
 #pragma unroll
               for (int i = 0; i < kMT; ++i) {
-                o[i][nt][c] *= down * vdown;
-                o[i][nt][c + 2] *= down * vdown;
+                o[i][nt][c] *= down;
+                o[i][nt][c + 2] *= down;
               }
             }
         }
-        const float vpow = __int_as_float(max(127 + kLift + ve - vref, 0) << 23);
         uint32_t pf[kParts][NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+          float sum[2] = {};
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             const float p0 = exp2_approx(sc[nt][2 * r] - m[nt][0]), p1 = exp2_approx(sc[nt][2 * r + 1] - m[nt][1]);
-            l[nt][0] += p0;
-            l[nt][1] += p1;
-            const float w0 = p0 * vpow, w1 = p1 * vpow;
+            sum[0] += p0;
+            sum[1] += p1;
+            const float w0 = p0 * (1 << kLift), w1 = p1 * (1 << kLift);
             const uint32_t hi = half_pair(w0, w1);
             pf[0][nt][r] = transpose8(hi);
             if constexpr (kSplit) pf[1][nt][r] = transpose8(half_rest(w0, w1, hi));
           }
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            l[nt][c] += settled ? sum[c] : sum[c] * exp2_approx(fminf(state[8 * nt + 2 * t + c].x, kKvFar));
+        }
         // O^T
+        const KvScale vscale = kv_scale(ve - window);
         uint32_t vw[4][kVW];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -365,7 +410,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_rows_kernel(const
           const uint32_t cd[2] = {prmt(c, d, 0x5140u), prmt(c, d, 0x7362u)};
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const uint32_t a0 = bytes_low(ab[e]), a1 = bytes_high(ab[e]), a2 = bytes_low(cd[e]), a3 = bytes_high(cd[e]);
+            const uint32_t a0 = bytes_low(ab[e], vscale), a1 = bytes_high(ab[e], vscale);
+            const uint32_t a2 = bytes_low(cd[e], vscale), a3 = bytes_high(cd[e], vscale);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -379,7 +425,6 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_rows_kernel(const
       // the end of the item, or of this warp's share of it
       const bool ends = at.at + 1 == at.units;
       if (ends || done + 1 == count) {
-        const float vscale = kv_power(vref);
         uint8_t* into = nullptr;
         if (!(begins && ends)) {
           // a part: the one at the share's beginning to its own place, one at its end to the ring's, which
@@ -403,18 +448,25 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_rows_kernel(const
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             const int col = 8 * nt + 2 * t + c;
             const float unlift = (into ? kKvPartScale : 1.f) / (1 << kLift);
+            // O's power of two over that of l; by two factors where one might leave float32's range
+            float unit = m[nt][c], scale = kv_power(window), again = 1.f;
+            if (!settled) {
+              const float2 held = state[col];
+              unit -= held.x;
+              scale = again = exp2f(0.5f * (held.x + (float)(__float_as_int(held.y) - 127)));
+            }
             float y[kMT][2];
 #pragma unroll
             for (int i = 0; i < kMT; ++i) {
-              y[i][0] = o[i][nt][c] * inv * unlift * vscale;
-              y[i][1] = o[i][nt][c + 2] * inv * unlift * vscale;
+              y[i][0] = o[i][nt][c] * inv * unlift * scale * again;
+              y[i][1] = o[i][nt][c + 2] * inv * unlift * scale * again;
             }
             if (into) {
               float* dst = reinterpret_cast<float*>(into) + col * D + g * (D / 8);
 #pragma unroll
               for (int i = 0; i < kMT; i += 2)
                 *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(y[i][0], y[i][1], y[i + 1][0], y[i + 1][1]);
-              if (g == 0) reinterpret_cast<float2*>(into + S::kRows * D * 4)[col] = make_float2(m[nt][c], sum);
+              if (g == 0) reinterpret_cast<float2*>(into + S::kRows * D * 4)[col] = make_float2(unit, sum);
             } else {
               const int row = at.r * S::kRows + col;
               if (row < at.s.n * w.a.group) {

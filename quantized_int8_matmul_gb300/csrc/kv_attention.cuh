@@ -336,6 +336,65 @@ __device__ __forceinline__ uint32_t half_rest(float a, float b, uint32_t pair) {
   const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&pair));
   return half_pair(a - h.x, b - h.y);
 }
+// The values' powers of two. P, in fp16, has no digits to spare for them: times 2^30 for a
+// block that a row hardly sees, or does not see, the P of all that it does see would be
+// zeros. The fp16 that an int8 of V becomes has: int8 * 2^(byte - window) is exact for
+// bytes from 24 below the window's to 5 above, and costs nothing (kv_widen). A window
+// holds for as long as the bytes stay within; blocks within 2^29 of each other can all be
+// in one. Where they are not, the window moves, and a row that takes part in a block of
+// another window has its O rescaled from unit to unit. Rows that see nothing of the block
+// are left alone: what they add, 0 * V, is 0 in any unit.
+constexpr int kKvBelow = 24, kKvAbove = 5, kKvNoWindow = -1000;
+__host__ __device__ constexpr bool kv_in_window(int byte, int window) {
+  return byte >= window - kKvBelow && byte <= window + kKvAbove;
+}
+// The window around bytes lo .. hi, which are no further apart than it holds. (Between 24 and 250, 2^(window - 127) is
+// a normal number, and bytes 0 and 255 are still within.)
+__host__ __device__ constexpr int kv_window(int lo, int hi) {
+  const int w = (lo + hi + kKvBelow - kKvAbove + 1) / 2;
+  return w < 24 ? 24 : w > 250 ? 250 : w;
+}
+static_assert(kv_in_window(0, kv_window(0, 0)) && kv_in_window(255, kv_window(255, 255)) &&
+                  kv_in_window(100, kv_window(100, 129)) && kv_in_window(129, kv_window(100, 129)) &&
+                  kv_in_window(226, kv_window(226, 255)) && kv_in_window(29, kv_window(0, 29)),
+              "a window holds what it was made for");
+
+// A row's units: P is held in 2^m, O in 2^(m + window), the sum l in 2^(m - behind), that
+// is by the largest score so far. behind is 0 but where windows moved: below 0 for a block
+// with low scores, whose P has to be held by its own, above 0 for a block so far below
+// the last ones that O could not follow.
+struct KvUnit {
+  float m, behind;
+  int window;
+};
+// P and l of a row far above its scores: P is 0 in fp16 2^40 above them; no further than this, so that float32 still
+// holds what l takes from it.
+constexpr float kKvFar = 100.f;
+// The row comes to scores of which the largest is top (-inf: it sees none of them), with
+// values in `window`. `largest`: of its O, in magnitude. Returns log2 of the factor to O;
+// l is taken to its unit here.
+__device__ __forceinline__ float kv_change_units(KvUnit& u, float& l, float top, float largest, int window) {
+  const float most = u.m - u.behind, unit = fmaxf(most, top);   // of l: before, after
+  if (top > most) l *= exp2_approx(most - top);
+  float up = fmaxf(u.m, top), shift = u.m - up;
+  if (top > -INFINITY && u.window != window) {
+    up = top > unit - 16.f ? unit : top;
+    shift = 0.f;
+    if (largest > 0.f) {
+      const float moves = (float)(u.window - window);
+      const float room = fminf(251.f - (float)(__float_as_int(largest) >> 23), 126.f);   // O stays below 2^125
+      up = fmaxf(up, u.m + moves - room);
+      shift = u.m - up + moves;
+    }
+    u.window = window;
+    u.behind = up - unit;
+  } else if (top > most || up > u.m) {
+    u.behind = up - unit;
+  }
+  u.m = up;
+  return shift;
+}
+
 // Two int8, biased by 128, to two fp16: bytes 0 and 1 of u, or 2 and 3. The byte becomes
 // the low mantissa bits of 1024, whose ulp is 1, and 1024 + 128 is taken off, exactly.
 __device__ __forceinline__ uint32_t bytes_low(uint32_t u) {
@@ -350,5 +409,20 @@ __device__ __forceinline__ uint32_t bytes_high(uint32_t u) {
   const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&l), bias);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// The same times 2^s, s from -kKvBelow to kKvAbove, exactly: (1152 + int8) * 2^s - 1152 * 2^s in one operation.
+struct KvScale {
+  uint32_t factor, bias;   // fp16 pairs: 2^s, -1152 * 2^s
+};
+__device__ __forceinline__ KvScale kv_scale(int s) {
+  const uint32_t f = s >= -14 ? (uint32_t)(s + 15) << 10 : 1u << (s + 24);   // (subnormal below 2^-14)
+  return {f * 0x10001u, (0x8080u + ((uint32_t)(s + 25) << 10)) * 0x10001u};
+}
+__device__ __forceinline__ uint32_t kv_widen(uint32_t biased, KvScale k) {
+  const __half2 h = __hfma2(*reinterpret_cast<const __half2*>(&biased), *reinterpret_cast<const __half2*>(&k.factor),
+                            *reinterpret_cast<const __half2*>(&k.bias));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t bytes_low(uint32_t u, KvScale k) { return kv_widen(prmt(u, 0x64646464u, 0x4140u), k); }
+__device__ __forceinline__ uint32_t bytes_high(uint32_t u, KvScale k) { return kv_widen(prmt(u, 0x64646464u, 0x4342u), k); }
 
 }  // namespace qmm
