@@ -410,7 +410,7 @@ __device__ __forceinline__ uint32_t bytes_high(uint32_t u) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 // The same times 2^s, s from -kKvBelow to kKvAbove, exactly: (1152 + int8) * 2^s - 1152 * 2^s in one operation.
-struct KvScale {
+struct alignas(8) KvScale {
   uint32_t factor, bias;   // fp16 pairs: 2^s, -1152 * 2^s
 };
 __device__ __forceinline__ KvScale kv_scale(int s) {

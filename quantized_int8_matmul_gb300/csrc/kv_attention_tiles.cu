@@ -14,11 +14,12 @@
 // other runs. Its roles: warps 0-3 and 4-7 hold a row a thread (its maximum and sum need
 // no exchange); one warp copies int8 keys and values from their pages (bulk copies of a
 // block each), warps 8-11 widen them to fp16, exactly, into a ring of three operands;
-// one warp issues the MMAs, another works out the CTA's share of the work. A block's
-// power of two is not multiplied into K or V: a key block's goes into the factor of its 16
-// columns of S, a value block's into the exponent of its 16 columns of P. The running
-// maximum moves only past a score 8 above it (rescaling O is then rare); scores are
-// masked only in tiles that some row's limit cuts.
+// one warp issues the MMAs, another works out the CTA's share of the work. A key block's
+// power of two goes into the factor of its 16 columns of S, a value block's into its fp16
+// (the windows of kv_attention.cuh). A tile with blocks that no one window holds is passed
+// several times, each time for the blocks of one window. The running maximum moves only
+// past a score 8 above it (rescaling O is then rare); scores are masked only in tiles that
+// some row's limit cuts.
 //
 // The work is cut like that of the other kernel (kv_attention.cuh), a unit being a tile
 // of 128 tokens, so that short and long rows of causal prompts balance.
@@ -48,27 +49,28 @@ constexpr int kSoftmaxRegs = 192, kConvertRegs = 80, kRestRegs = 48;
 static_assert(256 * kSoftmaxRegs + 128 * kConvertRegs + 128 * kRestRegs <= 512 * 128, "registers of the launch");
 constexpr int kStages = 3;                 // operands (K or V tiles) in the ring of fp16
 constexpr int kRaw = 4;                    // and in the ring of int8 before it
-constexpr int kInfo = 4;                   // tiles whose scales are kept
+constexpr int kInfo = 4;                   // passes whose scales are kept
 constexpr int kBlocks = kTokens / kKvBlock;
 constexpr int kSetup = 5;                  // units that stand for what an item costs beside its tiles
 constexpr int kMinUnits = kSetup + 2;      // a CTA's share, at least
 constexpr float kLift = 7.f;               // P is held times 2^7: at most 2^15
 
-// What the softmax needs to know of a tile's blocks.
+// A pass over a tile, as the softmax, the converters and the MMAs' warp need to know it.
 struct alignas(16) Info {
   float kpow[kBlocks];     // 2^(byte - 127) of the key blocks
-  float vdown[kBlocks];    // byte - vmax of the value blocks, no less than -100
-  float vup[kBlocks];      // 2^(vmax - byte), the same
-  int vmax;                // the largest byte
-  int missing;             // blocks on pages that are not there, a bit each
-  int pad[2];
+  KvScale v[kBlocks];      // the value blocks' powers of two over the window's
+  int window;
+  int missing;             // blocks on pages that are not there, or of other passes, a bit each
+  int first;               // the tile's first token
+  int last;                // the last pass of the run
 };
 
 // A CTA's consecutive units of one item, as one warp works them out for all.
 struct alignas(16) Run {
   int b, r, h, flags;          // as in a part; kRunStop: there is none
   int at, tiles, rows, start;  // first unit, units, rows of the tile pair, first packed row
-  int n, len, seen, pad;       // the sequence's
+  int n, len, seen;            // the sequence's
+  int slot;                    // of this record
 };
 enum { kRunStop = 8 };
 constexpr int kRuns = 4;       // kept
@@ -83,6 +85,7 @@ struct Smem {
   alignas(128) uint8_t raw[kRaw][kRawStage];
   Info info[kInfo];
   Run run[kRuns];
+  int run_pass[kRuns];     // the number of each run's first pass
   uint64_t full[kStages], empty[kStages], raw_full[kRaw], raw_empty[kRaw];
   uint64_t run_full[kRuns], run_empty[kRuns];
   uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], drained;   // p_full: of either half of the columns
@@ -426,7 +429,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
     const uint32_t s_tmem = tmem + lanes + x * 128, o_tmem = s_tmem + 256;
     KvPart left0{}, left1{};
     uint32_t s_phase = 0, o_phase = 0;
-    int tile = 0;            // tiles of the CTA before the run
     bool ok = true;
     Run now{};
     Row me{1.f, INT_MAX};
@@ -442,19 +444,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
     if (more && (!x || now.rows > 128)) put_rows();
     while (more) {
       const bool mine = !x || now.rows > 128;
-      float m = kKvNone, l = 0.f;
-      int vref = 0;
+      KvUnit unit{kKvNone, 0.f, kKvNoWindow};
+      float l = 0.f;
       if (mine) {
         const float coef = me.coef;
-        int cut = me.limit - now.at * kTokens;   // columns of the tile that the row sees
-        for (int j = 0; j < now.tiles; ++j, cut -= kTokens) {
+        int pass = 0, last = 0;
+        for (int j = 0; !last; ++j, ++pass) {
           if (!(ok = wait(&sm.s_full[x], s_phase, 0x501))) break;
           s_phase ^= 1;
           tc_fence_after();
-          const Info& info = sm.info[(tile + j) % kInfo];
+          if (j == 0) pass = sm.run_pass[now.slot];
+          const Info& info = sm.info[pass % kInfo];
           uint32_t s[128];
           tmem_ld128(s_tmem, s);
-          const int missing = info.missing, vmax = info.vmax;
+          const int missing = info.missing, window = info.window;
+          const int cut = me.limit - info.first;   // columns of the tile that the row sees
+          last = info.last;
           if (__any_sync(~0u, cut < kTokens) || missing) {
 #pragma unroll
             for (int i = 0; i < kTokens; ++i)
@@ -472,37 +477,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
             t = fmaxf(t, __uint_as_float(s[16 * k + 15]));
             top = fmaxf(top, t * f[k]);
           }
-          if (__any_sync(~0u, top > m + kKvSlack) || vmax > vref) {
-            const float up = fmaxf(m, top);
-            float down = exp2_approx(m - up);
-            m = up;
-            l *= down;
-            if (vmax > vref) {
-              down *= exp2_approx((float)(vref - vmax));
-              vref = vmax;
+          if (__any_sync(~0u, top > unit.m - fmaxf(unit.behind, 0.f) + kKvSlack ||
+                                  (top > -INFINITY && unit.window != window))) {
+            float largest = 0.f;
+            if (j > 0 && __any_sync(~0u, unit.m != kKvNone && top > -INFINITY && unit.window != window)) {
+#pragma unroll 1
+              for (int i = 0; i < D; i += 16) {
+                uint32_t o[16];
+                tmem_ld16(o_tmem + i, o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) largest = fmaxf(largest, fabsf(__uint_as_float(o[e])));
+              }
             }
+            const float scale = exp2_approx(kv_change_units(unit, l, top, largest, window));
             if (j > 0) {
 #pragma unroll 1
               for (int i = 0; i < D; i += 16) {
                 uint32_t o[16];
                 tmem_ld16(o_tmem + i, o);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * down);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scale);
                 tmem_st16(o_tmem + i, o);
               }
             }
           }
-          // P = exp2(score - m) * 2^(byte - vref), held times 2^kLift; the sum without the powers
-          const int behind = max(vmax - vref, -100);
-          const float base = (float)behind + kLift - m;
+          // P = exp2(score - m), held times 2^kLift, and its sum (a row far above its scores: see kKvFar)
+          const float behind = fminf(unit.behind, kKvFar);
+          const float base = kLift - (unit.m - (unit.behind - behind));
           float sum = 0.f;
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             uint32_t p[32], rest[kSplit ? 32 : 1];
 #pragma unroll
             for (int k = 4 * half; k < 4 * half + 4; ++k) {
-              const float add = info.vdown[k] + base;
-              const float2 f2 = make_float2(f[k], f[k]), a2 = make_float2(add, add);
+              const float2 f2 = make_float2(f[k], f[k]), a2 = make_float2(base, base);
               float2 part = make_float2(0.f, 0.f);
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
@@ -513,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
                 p[8 * (k & 3) + i] = half_pair(e.x, e.y);
                 if constexpr (kSplit) rest[8 * (k & 3) + i] = half_rest(e.x, e.y, p[8 * (k & 3) + i]);
               }
-              sum += (part.x + part.y) * info.vup[k];
+              sum += part.x + part.y;
             }
             tmem_st32_async(s_tmem + 32 * half, p);
             if constexpr (kSplit) tmem_st32_async(s_tmem + 64 + 32 * half, rest);
@@ -522,10 +530,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.p_full[x][half]);
           }
-          l += sum * __int_as_float((127 - behind) << 23);
+          l = fmaf(sum, exp2_approx(behind), l);
         }
       }
-      tile += now.tiles;
       if (!ok) break;
       const Run was = now;
       more = next_run(now);
@@ -538,12 +545,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
         tc_fence_after();
         // O by way of this warp's rows of Q, whose last use is over, so that neighbouring lanes write neighbouring
         // bytes: 256 bytes of each row at a time, as bfloat16 or, of a part, as float32
-        // 1 / l and V's power in one factor where that is a normal number, else one after the other
-        const float inv = l == 0.f ? 0.f : (whole ? 1.f : kKvPartScale) / l, vscale = kv_power(vref), both = inv * vscale;
+        // 1 / l and O's power of two over that of l in one factor where that is a normal number, else in three
+        const float inv = l == 0.f ? 0.f : (whole ? 1.f : kKvPartScale) / l;
+        const float vscale = exp2f(0.5f * (unit.behind + (float)(unit.window - 127)));
+        const float both = unit.behind == 0.f ? inv * kv_power(unit.window) : 0.f;
         const bool small = __any_sync(~0u, both < 1.17549435e-38f);
         const float2 factor = small ? make_float2(inv, inv) : make_float2(both, both);
         uint8_t* const part = w.ws + (size_t)(2 * blockIdx.x + slot) * kv_part_bytes(D, kRows);
-        if (!whole) reinterpret_cast<float2*>(part + kRows * D * 4)[first + lane] = make_float2(m, l);
+        if (!whole) reinterpret_cast<float2*>(part + kRows * D * 4)[first + lane] = make_float2(unit.m - unit.behind, l);
         const bool narrow = whole && !kSplit;              // to bfloat16
         const int step = narrow ? D : D / 2;               // columns at a time: 2 D bytes of a row
         constexpr int kPieces = D / 8, kAtOnce = 32 / kPieces;   // pieces of 16 bytes of them; rows
@@ -564,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
             }
             if (small) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) y[e] *= vscale;
+              for (int e = 0; e < 32; ++e) y[e] = y[e] * vscale * vscale;
             }
             // piece p of the row: panel p / 8, place p % 8 exchanged by the row
             auto put = [&](int p, uint32_t u0, uint32_t u1, uint32_t u2, uint32_t u3) {
@@ -636,9 +645,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
     uint32_t stage = 0, phase = 1, from = 0, from_phase = 0;
     bool ok = true;
     Run run{};
+    int pass = 0, last = 0;
+    bool value = false;   // K and V in turn
     while (ok && next_run(run)) {
-      for (int i = 2 * run.tiles; i > 0; --i) {
+#pragma unroll 1
+      do {
         if (!(ok = wait(&sm.raw_full[from], from_phase, 0x503))) break;
+        const Info& info = sm.info[pass % kInfo];
+        last = info.last;
         const uint32_t src = smem_u32(sm.raw[from]) + src0;
         uint4 x[kRounds];
 #pragma unroll
@@ -650,8 +664,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
           const uint32_t u[4] = {x[r].x ^ 0x80808080u, x[r].y ^ 0x80808080u, x[r].z ^ 0x80808080u,
                                  x[r].w ^ 0x80808080u};
           const uint32_t at = dst + (uint32_t)(r * kRoundTokens) * 128u;
-          st_shared_v4(at + at0, bytes_low(u[0]), bytes_high(u[0]), bytes_low(u[1]), bytes_high(u[1]));
-          st_shared_v4(at + at1, bytes_low(u[2]), bytes_high(u[2]), bytes_low(u[3]), bytes_high(u[3]));
+          KvScale k = kv_scale(0);
+          if (value) k = info.v[(r * kRoundTokens + token0) / kKvBlock];
+          st_shared_v4(at + at0, bytes_low(u[0], k), bytes_high(u[0], k), bytes_low(u[1], k), bytes_high(u[1], k));
+          st_shared_v4(at + at1, bytes_low(u[2], k), bytes_high(u[2], k), bytes_low(u[3], k), bytes_high(u[3], k));
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -667,7 +683,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
           from = 0;
           from_phase ^= 1;
         }
-      }
+        pass += value;
+        value = !value;
+      } while (value || !last);
     }
   } else {
     fewer_registers<kRestRegs>();
@@ -695,15 +713,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
         return got;
       };
       Run run{};
+      int pass = 0;
       while (ok && next_run(run)) {
-        const int tiles = __shfl_sync(~0u, run.tiles, 0), pair = __shfl_sync(~0u, run.rows, 0) > 128 ? 2 : 1;
-        // scores of tile 0; then, tile by tile, the products of one and the scores of the next
+        const int pair = __shfl_sync(~0u, run.rows, 0) > 128 ? 2 : 1;
+        // scores of pass 0; then, pass by pass, the products of one and the scores of the next
         uint32_t v_stage = 0;
+        bool more = true;
 #pragma unroll 1
-        for (int j = -1; j < tiles && ok; ++j) {
-          const bool more = j + 1 < tiles;
+        for (int j = -1; more && ok; ++j) {
           uint32_t k_stage = 0;
-          if (j >= 0) v_stage = operand(0x506);
+          if (j >= 0) {
+            v_stage = operand(0x506);
+            more = !__shfl_sync(~0u, sm.info[pass++ % kInfo].last, 0);
+          }
 #pragma unroll 1
           for (int x = 0; x < pair && ok; ++x) {
             if (j >= 0) {
@@ -757,10 +779,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
     } else if (warp == 14) {
       // ---------------- int8 keys and values from their pages, and what the softmax needs of their blocks ----------
       uint32_t stage = 0, phase = 1, copies = 0;
-      int tile = 0;
+      int pass = 0;
       bool ok = true;
       Run run{};
       while (ok && next_run(run)) {
+        int window = kKvNoWindow;
+        bool opens = true;   // the run's first pass
         // four tiles at a time, a lane each block: the table and the scales are two loads that follow each other
 #pragma unroll 1
         for (int j0 = 0; j0 < run.tiles && ok; j0 += 32 / kBlocks) {
@@ -776,41 +800,52 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
             }
           }
           const unsigned there = __ballot_sync(~0u, block >= 0);
-          int vmax = ve;
-#pragma unroll
-          for (int o = kBlocks / 2; o; o >>= 1) vmax = max(vmax, __shfl_xor_sync(~0u, vmax, o));
 #pragma unroll 1
-          for (int j = j0; j < min(j0 + 32 / kBlocks, run.tiles) && ok; ++j, ++tile) {
-            const bool mine = lane / kBlocks == j - j0;
-            const unsigned here = there >> ((j - j0) * kBlocks) & ((1u << kBlocks) - 1);
+          for (int j = j0; j < min(j0 + 32 / kBlocks, run.tiles) && ok; ++j) {
+            unsigned pending = there & (((1u << kBlocks) - 1) << ((j - j0) * kBlocks));   // the tile's lanes
+            do {
+              unsigned here = __ballot_sync(~0u, kv_in_window(ve, window)) & pending;
+              if (!here && pending) {
+                const bool open = pending >> lane & 1;
+                const int lo = __reduce_min_sync(~0u, open ? ve : INT_MAX), hi = __reduce_max_sync(~0u, open ? ve : 0);
+                window = kv_window(lo, min(hi, lo + kKvBelow + kKvAbove));
+                here = __ballot_sync(~0u, kv_in_window(ve, window)) & pending;
+              }
+              pending &= ~here;
+              const bool mine = here >> lane & 1;
 #pragma unroll 1
-            for (int kind = 0; kind < 2; ++kind) {
-              if (!(ok = wait(&sm.raw_empty[stage], phase, 0x50d))) break;
-              if (kind == 0 && mine) {
-                Info& info = sm.info[tile % kInfo];
-                const int i = lane % kBlocks, down = block >= 0 ? min(vmax - ve, 100) : 0;
-                info.kpow[i] = block >= 0 ? kv_power(ke) : 0.f;
-                info.vdown[i] = (float)-down;
-                info.vup[i] = __int_as_float((127 + down) << 23);
-                if (i == 0) {
-                  info.vmax = vmax;
-                  info.missing = (int)(here ^ ((1u << kBlocks) - 1));
+              for (int kind = 0; kind < 2; ++kind) {
+                if (!(ok = wait(&sm.raw_empty[stage], phase, 0x50d))) break;
+                if (kind == 0 && lane / kBlocks == j - j0) {
+                  Info& info = sm.info[pass % kInfo];
+                  const int i = lane % kBlocks;
+                  info.kpow[i] = mine ? kv_power(ke) : 0.f;
+                  info.v[i] = kv_scale(mine ? ve - window : 0);
+                  if (i == 0) {
+                    info.window = window;
+                    info.missing = (int)(~here >> ((j - j0) * kBlocks) & ((1u << kBlocks) - 1));
+                    info.first = (run.at + j) * kTokens;
+                    info.last = !pending && j + 1 == run.tiles;
+                    if (opens) sm.run_pass[run.slot] = pass;
+                  }
+                }
+                __syncwarp();
+                if (lane == 0)
+                  mbar_arrive_expect_tx(&sm.raw_full[stage], (uint32_t)__popc(here) * (kKvBlock * D));
+                __syncwarp();
+                if (mine)
+                  bulk_load(smem_u32(sm.raw[stage]) + (lane % kBlocks) * (kKvBlock * D),
+                            (kind ? w.a.cache.v : w.a.cache.k) + block * (kKvBlock * D), kKvBlock * D,
+                            &sm.raw_full[stage]);
+                ++copies;
+                if (++stage == kRaw) {
+                  stage = 0;
+                  phase ^= 1;
                 }
               }
-              __syncwarp();
-              if (lane == 0)
-                mbar_arrive_expect_tx(&sm.raw_full[stage], (uint32_t)__popc(here) * (kKvBlock * D));
-              __syncwarp();
-              if (mine && block >= 0)
-                bulk_load(smem_u32(sm.raw[stage]) + (lane % kBlocks) * (kKvBlock * D),
-                          (kind ? w.a.cache.v : w.a.cache.k) + block * (kKvBlock * D), kKvBlock * D,
-                          &sm.raw_full[stage]);
-              ++copies;
-              if (++stage == kRaw) {
-                stage = 0;
-                phase ^= 1;
-              }
-            }
+              ++pass;
+              opens = false;
+            } while (pending && ok);
           }
         }
       }
@@ -836,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
             if (!end) {
               run = Run{c.b, c.r, c.h,
                         kPartHeld | (from == 0 ? kPartBegins : 0) | (c.at + units == c.units ? kPartEnds : 0), from, tiles,
-                        min(c.s.n * w.a.group - c.r * kRows, kRows), c.s.start, c.s.n, c.s.len, c.s.seen, 0};
+                        min(c.s.n * w.a.group - c.r * kRows, kRows), c.s.start, c.s.n, c.s.len, c.s.seen, (int)slot};
             }
             sm.run[slot] = run;
             mbar_arrive(&sm.run_full[slot]);

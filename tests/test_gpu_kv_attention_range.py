@@ -12,6 +12,7 @@ pytestmark = pytest.mark.gpu
 
 GAPS = [12, 24, 29, 31, 40, 60, 100, 120]
 FEW = [(8, 69), (3, 130), (1, 70)]   # the kernel for single tokens
+MANY = [(128, 128), (100, 260)]      # the tensor cores'
 
 
 def set_bytes(b, exps, rule):
@@ -33,7 +34,8 @@ def check(q, seqs, kind, rule, group=2, causal=True, dim=64, kernel=None, x=None
 
 
 def each(f):
-    for name, params in (("kind", ["bf16", "f32"]), ("seqs,group,kernel", [(FEW, 2, "kv_attention_rows")])):
+    for name, params in (("kind", ["bf16", "f32"]), ("seqs,group,kernel", [(FEW, 2, "kv_attention_rows"),
+                                                                          (MANY, 4, None)])):
         f = pytest.mark.parametrize(name, params)(f)
     return f
 
