@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_rows_kernel(const
           // the largest magnitude to [2^14, 2^15)
           const int e = min(max(__float_as_int(top) >> 23, 27), 254);
           const float up = __int_as_float((127 + 14 + 127 - e) << 23);
-          const bool bad = top > 3.402823466e38f;
+          const bool bad = top > kKvMax;
           float cf = bad ? __int_as_float(0x7fc00000) : w.a.scale * 1.4426950408889634f * __int_as_float((e - 14) << 23);
 #pragma unroll
           for (int i = 0; i < kKI; ++i)
@@ -300,7 +300,12 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_rows_kernel(const
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) sc[nt][c] *= coef[nt][c & 1] * kpow;
+          for (int c = 0; c < 2; ++c) {
+            float f = coef[nt][c] * kpow;
+            if (fabsf(f) > kKvMax) f = copysignf(kKvMax, f);   // (0 times it is a score; a NaN stays one)
+            sc[nt][c] *= f;
+            sc[nt][c + 2] *= f;
+          }
         const int token = at.at * kKvBlock + g;
         if (at.at * kKvBlock > least - kKvBlock) {
 #pragma unroll

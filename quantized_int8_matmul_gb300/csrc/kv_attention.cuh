@@ -10,7 +10,8 @@
 
 namespace qmm {
 
-constexpr float kKvNone = -1e30f;      // a running maximum that has seen nothing
+constexpr float kKvMax = 3.402823466e38f;   // the largest float32
+constexpr float kKvNone = -kKvMax;     // a running maximum that has seen nothing: no score may lie below it
 constexpr float kKvSlack = 8.f;        // how far a score may pass the running maximum (a factor of 256)
 
 // A part of an item that one warp (in shared memory) or one CTA (in the workspace) holds.

@@ -54,6 +54,9 @@ constexpr int kBlocks = kTokens / kKvBlock;
 constexpr int kSetup = 5;                  // units that stand for what an item costs beside its tiles
 constexpr int kMinUnits = kSetup + 2;      // a CTA's share, at least
 constexpr float kLift = 7.f;               // P is held times 2^7: at most 2^15
+// Sums of D <= 128 products of fp16 below 2^15 and int8 are below 2^29: with factors up to this scores stay below 2^20,
+// where the rounding of one is 2^-4 at most.
+constexpr float kPlainFactor = 1.f / 512;
 
 // A pass over a tile, as the softmax, the converters and the MMAs' warp need to know it.
 struct alignas(16) Info {
@@ -63,6 +66,8 @@ struct alignas(16) Info {
   int missing;             // blocks on pages that are not there, or of other passes, a bit each
   int first;               // the tile's first token
   int last;                // the last pass of the run
+  float kmax;              // of kpow
+  int pad[3];
 };
 
 // A CTA's consecutive units of one item, as one warp works them out for all.
@@ -86,6 +91,7 @@ struct Smem {
   Info info[kInfo];
   Run run[kRuns];
   int run_pass[kRuns];     // the number of each run's first pass
+  KvScale plain[kBlocks];  // 1, for K
   uint64_t full[kStages], empty[kStages], raw_full[kRaw], raw_empty[kRaw];
   uint64_t run_full[kRuns], run_empty[kRuns];
   uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], drained;   // p_full: of either half of the columns
@@ -141,6 +147,14 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 r;
   asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
       "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "sub.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
       : "=f"(r.x), "=f"(r.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;
@@ -294,7 +308,7 @@ __device__ __forceinline__ Row load_rows(const KvWork& w, const Run& run, int fi
       st_shared_v4(place(i), hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
       st_shared_v4(place(i) + kOther, lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
     }
-    Row out{1.f, INT_MAX};
+    Row out{0.f, INT_MAX};
     if (scale != 0.f) out.coef = fabsf(scale) * 1.4426950408889634f * __int_as_float((e - 14) << 23);
     if (first + lane < run.rows)
       out.limit = kv_visible(KvSeq{0, run.n, run.len, run.seen},
@@ -350,7 +364,7 @@ __device__ __forceinline__ Row load_rows(const KvWork& w, const Run& run, int fi
       y[k] = bad ? 0x7e007e00u : half_pair(__uint_as_float(u[k] << 16) * up, __uint_as_float(u[k] & 0xffff0000u) * up);
     st_shared_v4(place(i), y[0], y[1], y[2], y[3]);
   }
-  Row out{1.f, INT_MAX};
+  Row out{0.f, INT_MAX};
   if (scale != 0.f) out.coef = fabsf(scale) * 1.4426950408889634f * __int_as_float((e - 14) << 23);
   if (first + lane < run.rows)
     out.limit = kv_visible(KvSeq{0, run.n, run.len, run.seen},
@@ -370,6 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
 
   if (threadIdx.x == 0) {
     sm.abort = 0;
+    for (int i = 0; i < kBlocks; ++i) sm.plain[i] = kv_scale(0);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&sm.full[i], 4);
       mbar_init(&sm.empty[i], 1);
@@ -427,25 +442,35 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;     // 32 lanes a warp, in bits 16 and up
     // scores (and P) of the two tiles in columns 0 and 128, O in 256 and 384
     const uint32_t s_tmem = tmem + lanes + x * 128, o_tmem = s_tmem + 256;
-    KvPart left0{}, left1{};
     uint32_t s_phase = 0, o_phase = 0;
     bool ok = true;
-    Run now{};
-    Row me{1.f, INT_MAX};
+    // the run, which stays in its place until it is done with: this role has no registers for it
+    const Run* now = nullptr;
+    auto hold_run = [&]() -> bool {
+      if (!wait(&sm.run_full[run_slot], run_phase, 0x50a)) return false;
+      now = &sm.run[run_slot];
+      if (++run_slot == kRuns) {
+        run_slot = 0;
+        run_phase ^= 1;
+      }
+      return !(now->flags & kRunStop);
+    };
+    Row me{0.f, INT_MAX};
     const int first = x * 128 + (warp & 3) * 32;   // the warp's first row
     const uint32_t q_rows = smem_u32(sm.q) + x * kQTile + (warp & 3) * 32 * 128;
     auto put_rows = [&] {
-      me = load_rows<D, T, kVec>(w, now, first, q_rows);
+      me = load_rows<D, T, kVec>(w, *now, first, q_rows);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.q_full[x]);
     };
-    bool more = next_run(now);
-    if (more && (!x || now.rows > 128)) put_rows();
+    if (threadIdx.x == 0) w.parts[2 * blockIdx.x] = w.parts[2 * blockIdx.x + 1] = KvPart{};
+    bool more = hold_run();
+    if (more && (!x || now->rows > 128)) put_rows();
     while (more) {
-      const bool mine = !x || now.rows > 128;
+      const bool mine = !x || now->rows > 128;
       KvUnit unit{kKvNone, 0.f, kKvNoWindow};
-      float l = 0.f;
+      float l = 0.f, above = -kKvMax;   // a score above it moves the maximum
       if (mine) {
         const float coef = me.coef;
         int pass = 0, last = 0;
@@ -453,14 +478,45 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
           if (!(ok = wait(&sm.s_full[x], s_phase, 0x501))) break;
           s_phase ^= 1;
           tc_fence_after();
-          if (j == 0) pass = sm.run_pass[now.slot];
+          if (j == 0) pass = sm.run_pass[now->slot];
           const Info& info = sm.info[pass % kInfo];
           uint32_t s[128];
           tmem_ld128(s_tmem, s);
           const int missing = info.missing, window = info.window;
           const int cut = me.limit - info.first;   // columns of the tile that the row sees
           last = info.last;
-          if (__any_sync(~0u, cut < kTokens) || missing) {
+          float by = coef, origin = 0.f;           // origin: what has been taken off the scores
+          auto factor = [&](int k) { return fmaxf(by * info.kpow[k], 1.17549435e-38f); };
+          const bool masked = cut < kTokens || missing, large = coef * info.kmax > kPlainFactor;
+          if (__any_sync(~0u, masked || large)) {
+            if (__any_sync(~0u, large)) {
+              // Scores may be so large that what their rounding leaves out of the maximum, and the sum below would bring
+              // back, is too much for P: they are counted from the largest of them, which makes that one 0. (Where they
+              // lie, in a short loop: done in registers, it took the prompt of 8192 from 435 to 500 us without being
+              // reached. The kernel's loops are as long as the instruction cache holds; the converters' is cut for it.)
+              by = fminf(by, kKvMax / info.kmax);
+              float most = -kKvMax;
+#pragma unroll 1
+              for (int k = 0; k < 2 * kBlocks; ++k) {
+                uint32_t r[kKvBlock];
+                const int block = k % kBlocks, seen = missing >> block & 1 ? 0 : cut - kKvBlock * block;
+                tmem_ld16(s_tmem + kKvBlock * block, r);
+                const float f = factor(block);
+                if (k < kBlocks) {
+#pragma unroll
+                  for (int i = 0; i < kKvBlock; ++i)
+                    if (i < seen) most = fmaxf(most, __uint_as_float(r[i]) * f);
+                } else {
+                  const float inverse = 1.f / f;
+#pragma unroll
+                  for (int i = 0; i < kKvBlock; ++i)
+                    r[i] = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(r[i]), f), most) * inverse);
+                  tmem_st16(s_tmem + kKvBlock * block, r);
+                }
+              }
+              origin = most;
+              tmem_ld128(s_tmem, s);
+            }
 #pragma unroll
             for (int i = 0; i < kTokens; ++i)
               if (i >= cut || (missing >> (i / kKvBlock) & 1)) s[i] = 0xff800000u;
@@ -469,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
           float f[kBlocks], top = -INFINITY;
 #pragma unroll
           for (int k = 0; k < kBlocks; ++k) {
-            f[k] = fmaxf(coef * info.kpow[k], 1.17549435e-38f);
+            f[k] = factor(k);
             float t = __uint_as_float(s[16 * k]);
 #pragma unroll
             for (int i = 1; i < 15; i += 2)
@@ -477,8 +533,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
             t = fmaxf(t, __uint_as_float(s[16 * k + 15]));
             top = fmaxf(top, t * f[k]);
           }
-          if (__any_sync(~0u, top > unit.m - fmaxf(unit.behind, 0.f) + kKvSlack ||
-                                  (top > -INFINITY && unit.window != window))) {
+          top += origin;
+          if (__any_sync(~0u, top > above || window != unit.window)) {
             float largest = 0.f;
             if (j > 0 && __any_sync(~0u, unit.m != kKvNone && top > -INFINITY && unit.window != window)) {
 #pragma unroll 1
@@ -490,6 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
               }
             }
             const float scale = exp2_approx(kv_change_units(unit, l, top, largest, window));
+            above = unit.m - fmaxf(unit.behind, 0.f) + kKvSlack;
             if (j > 0) {
 #pragma unroll 1
               for (int i = 0; i < D; i += 16) {
@@ -503,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
           }
           // P = exp2(score - m), held times 2^kLift, and its sum (a row far above its scores: see kKvFar)
           const float behind = fminf(unit.behind, kKvFar);
-          const float base = kLift - (unit.m - (unit.behind - behind));
+          const float base = kLift - (unit.m - (unit.behind - behind) - origin);
           float sum = 0.f;
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
@@ -519,7 +576,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
                 const float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
                 part = i ? add2(part, e) : e;
                 p[8 * (k & 3) + i] = half_pair(e.x, e.y);
-                if constexpr (kSplit) rest[8 * (k & 3) + i] = half_rest(e.x, e.y, p[8 * (k & 3) + i]);
+                if constexpr (kSplit) {
+                  const float2 of = __half22float2(*reinterpret_cast<const __half2*>(&p[8 * (k & 3) + i]));
+                  const float2 left = sub2(e, of);
+                  rest[8 * (k & 3) + i] = half_pair(left.x, left.y);
+                }
               }
               sum += part.x + part.y;
             }
@@ -534,11 +595,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
         }
       }
       if (!ok) break;
-      const Run was = now;
-      more = next_run(now);
+      const Run& was = *now;
+      more = hold_run();
       const bool whole = (was.flags & kPartBegins) && (was.flags & kPartEnds);
       const int slot = was.flags & kPartBegins ? 1 : 0;
-      if (!whole) (slot ? left1 : left0) = KvPart{was.start, was.h, was.r * kRows, was.rows, was.flags};
+      if (!whole && threadIdx.x == 0)
+        w.parts[2 * blockIdx.x + slot] = KvPart{was.start, was.h, was.r * kRows, was.rows, was.flags};
       if (mine) {
         if (!(ok = wait(&sm.o_full[x], o_phase, 0x502))) break;
         o_phase ^= 1;
@@ -619,11 +681,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
         }
         tc_fence_before();
       }
-      if (more && (!x || now.rows > 128)) put_rows();
-    }
-    if (threadIdx.x == 0) {
-      w.parts[2 * blockIdx.x] = left0;
-      w.parts[2 * blockIdx.x + 1] = left1;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.run_empty[was.slot]);
+      if (more && (!x || now->rows > 128)) put_rows();
     }
   } else if (warp < 12) {
     // ---------------- int8 to fp16 operands ----------------
@@ -653,22 +713,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
         if (!(ok = wait(&sm.raw_full[from], from_phase, 0x503))) break;
         const Info& info = sm.info[pass % kInfo];
         last = info.last;
-        const uint32_t src = smem_u32(sm.raw[from]) + src0;
-        uint4 x[kRounds];
+        const KvScale* scales = (value ? info.v : sm.plain) + token0 / kKvBlock;
+        uint32_t src = smem_u32(sm.raw[from]) + src0, dst = smem_u32(sm.stage[stage]);
+#pragma unroll 1
+        for (int r0 = 0; r0 < kRounds; r0 += 4) {
+          uint4 x[4];
 #pragma unroll
-        for (int r = 0; r < kRounds; ++r) x[r] = ld_shared_v4(src + r * (kRoundTokens * D));
-        if (!(ok = wait(&sm.empty[stage], phase, 0x50c))) break;
-        const uint32_t dst = smem_u32(sm.stage[stage]);
+          for (int r = 0; r < 4; ++r) x[r] = ld_shared_v4(src + r * (kRoundTokens * D));
+          if (r0 == 0 && !(ok = wait(&sm.empty[stage], phase, 0x50c))) break;
 #pragma unroll
-        for (int r = 0; r < kRounds; ++r) {
-          const uint32_t u[4] = {x[r].x ^ 0x80808080u, x[r].y ^ 0x80808080u, x[r].z ^ 0x80808080u,
-                                 x[r].w ^ 0x80808080u};
-          const uint32_t at = dst + (uint32_t)(r * kRoundTokens) * 128u;
-          KvScale k = kv_scale(0);
-          if (value) k = info.v[(r * kRoundTokens + token0) / kKvBlock];
-          st_shared_v4(at + at0, bytes_low(u[0], k), bytes_high(u[0], k), bytes_low(u[1], k), bytes_high(u[1], k));
-          st_shared_v4(at + at1, bytes_low(u[2], k), bytes_high(u[2], k), bytes_low(u[3], k), bytes_high(u[3], k));
+          for (int r = 0; r < 4; ++r) {
+            const uint32_t u[4] = {x[r].x ^ 0x80808080u, x[r].y ^ 0x80808080u, x[r].z ^ 0x80808080u,
+                                   x[r].w ^ 0x80808080u};
+            const uint32_t at = dst + (uint32_t)(r * kRoundTokens) * 128u;
+            const KvScale k = scales[r * (kRoundTokens / kKvBlock)];
+            st_shared_v4(at + at0, bytes_low(u[0], k), bytes_high(u[0], k), bytes_low(u[1], k), bytes_high(u[1], k));
+            st_shared_v4(at + at1, bytes_low(u[2], k), bytes_high(u[2], k), bytes_low(u[3], k), bytes_high(u[3], k));
+          }
+          src += 4 * kRoundTokens * D;
+          dst += 4 * kRoundTokens * 128u;
+          scales += 4 * (kRoundTokens / kKvBlock);
         }
+        if (!ok) break;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -819,9 +885,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
                 if (kind == 0 && lane / kBlocks == j - j0) {
                   Info& info = sm.info[pass % kInfo];
                   const int i = lane % kBlocks;
-                  info.kpow[i] = mine ? kv_power(ke) : 0.f;
+                  const float power = mine ? kv_power(ke) : 0.f;
+                  float most = power;
+#pragma unroll
+                  for (int o = kBlocks / 2; o; o >>= 1)
+                    most = fmaxf(most, __shfl_xor_sync(((1u << kBlocks) - 1) << (lane & ~(kBlocks - 1)), most, o));
+                  info.kpow[i] = power;
                   info.v[i] = kv_scale(mine ? ve - window : 0);
                   if (i == 0) {
+                    info.kmax = most;
                     info.window = window;
                     info.missing = (int)(~here >> ((j - j0) * kBlocks) & ((1u << kBlocks) - 1));
                     info.first = (run.at + j) * kTokens;
