@@ -671,7 +671,8 @@ qmm_status qmm_fp4_matmul(const void* a_packed, size_t a_bytes, int64_t M, const
  *                    NaN or an infinity NaN. out [rows, q_heads, head_dim] contiguous,
  *                    of q's dtype, not overlapping q (out = q is refused). max_tokens:
  *                    no sequence has more rows, as far as the caller knows; it chooses
- *                    kernels and splits, never results' validity (rows: always true).
+ *                    kernels and splits, never results' validity (rows: always true;
+ *                    starts = NULL: taken as 1).
  *  workspace         qmm_kv_attention_workspace_bytes of the same arguments, 16-byte
  *                    aligned; nothing in it has to survive a call, or to be zero
  * rows = 0 or batch = 0 launches nothing. QMM_ERR_UNSUPPORTED for another head_dim, page

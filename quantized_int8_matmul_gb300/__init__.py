@@ -947,7 +947,7 @@ def qmm_kv_attention(q, cache: KvCache, table, lengths, starts=None, scale=None,
     Query head h reads key head h // (q_heads // kv_heads). scale: head_dim ** -0.5 by
     default. A row that sees nothing gets zeros, one whose q is not finite NaN.
     max_tokens: the most rows a sequence has, where the host knows it (default: all
-    rows); it picks the kernels. out must not overlap q. workspace: "auto" or a device tensor of
+    rows; without starts it is 1); it picks the kernels. out must not overlap q. workspace: "auto" or a device tensor of
     qmm_kv_attention_workspace_bytes bytes, which calls that run at once must not share."""
     if scale is None:
         scale = q.shape[-1] ** -0.5

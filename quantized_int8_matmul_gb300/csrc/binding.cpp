@@ -509,7 +509,9 @@ PyObject* kv_attention(PyObject* const* a) {
   const double scale = PyFloat_AsDouble(a[8]);
   if (PyErr_Occurred()) throw Error();
   const int causal = truth(a[9]);
-  const int64_t max_tokens = a[10] == Py_None ? (rows > 1 ? rows : 1) : integer(a[10]);
+  // the hint; without starts each sequence has one row
+  int64_t max_tokens = a[10] == Py_None ? (rows > 1 ? rows : 1) : integer(a[10]);
+  if (!batch.starts && max_tokens > 1) max_tokens = 1;
   const void* qp = ptr(q);
   const Call call(a[12], q);
   const Tensor out = call.output(a[11], q.sizes(), t, {t}, "out", q);

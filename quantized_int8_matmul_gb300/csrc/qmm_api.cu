@@ -1962,6 +1962,7 @@ qmm_status qmm_kv_attention(const qmm_kv_cache* cache, const qmm_kv_batch* batch
     t_last_kernel = "none";
     return QMM_OK;
   }
+  max_tokens = batch->starts ? std::min(max_tokens, batch->rows) : 1;   // (1 needs no more of the workspace than any other)
   // (a row of q is read by several CTAs, some of which are done before others begin)
   if (!q || !out || out == q || !aligned16(out)) return QMM_ERR_INVALID_ARG;
   if (!workspace || !aligned16(workspace) ||
@@ -1977,7 +1978,7 @@ qmm_status qmm_kv_attention(const qmm_kv_cache* cache, const qmm_kv_batch* batch
   a.group = (int)(q_heads / cache->kv_heads);
   a.causal = causal;
   a.scale = scale;
-  a.max_tokens = (int)std::min(max_tokens, batch->rows);
+  a.max_tokens = (int)max_tokens;
   a.workspace = workspace;
   cudaGetLastError();
   const char* name = "none";
