@@ -705,6 +705,21 @@ qmm_status qmm_kv_attention(const qmm_kv_cache* cache, const qmm_kv_batch* batch
                             int64_t q_row, int64_t q_head, int64_t q_heads, float scale, int causal,
                             int64_t max_tokens, void* out, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Failure-path test hook of the attention for prompts, like qmm_test_a8w8_packed_stall:
+ * qmm_kv_attention with one fault planted. The first block of the kernel for many rows
+ * does not copy its first keys, so that its converters wait for data that never comes.
+ * That wait runs out after wait_limit_ns (1 us .. 100 ms; the block's others after four
+ * times that). The block records site 0x503, lets go of its work, drains, frees its
+ * tensor memory and returns; what it should have computed is left as it was, the other
+ * blocks' rows are right, and the context stays usable. A call that needs the kernel for
+ * few rows alone runs as usual. QMM_ERR_INVALID_ARG for a limit outside the range.
+ */
+qmm_status qmm_test_kv_attention_stall(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const void* q, int dtype,
+                                       int64_t q_row, int64_t q_head, int64_t q_heads, float scale, int causal,
+                                       int64_t max_tokens, void* out, void* workspace, size_t workspace_bytes,
+                                       uint64_t wait_limit_ns, void* stream);
+
 /* Human-readable name of a status. Never NULL. */
 const char* qmm_status_string(int status);
 

@@ -399,6 +399,9 @@ struct KvAttentionArgs {
   int max_tokens;              // the longest sequence's rows, as the caller knows it (a hint)
   void* workspace;
   unsigned* err;               // device error word
+  // 0 but for the test of the waits: the kernel for many rows leaves CTA 0 without its first block of keys, whose
+  // converters' wait then runs out after wait_ns (the CTA's other waits after 4 * wait_ns)
+  unsigned long long wait_ns;
 };
 size_t kv_attention_workspace(int rows, int batch, int heads, int group, int head_dim, int max_tokens, bool bf16);
 // vec: every row and head of q starts on 16 bytes

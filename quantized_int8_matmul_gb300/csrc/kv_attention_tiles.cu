@@ -80,6 +80,11 @@ struct alignas(16) Run {
 enum { kRunStop = 8 };
 constexpr int kRuns = 4;       // kept
 
+// What bounds the waits, in shared memory: read only where one is long.
+struct Watch {
+  uint64_t limit, raw_limit;   // ns; of the wait at kSiteRaw
+  int abort;
+};
 template <int D>
 struct Smem {
   static constexpr int kQTile = 128 * D * 2;
@@ -96,7 +101,7 @@ struct Smem {
   uint64_t run_full[kRuns], run_empty[kRuns];
   uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], drained;   // p_full: of either half of the columns
   uint32_t tmem;
-  int abort;
+  Watch watch;
 };
 
 // MMAs by the one lane of a converged warp for which `lead` is not 0: predicated, so
@@ -169,24 +174,26 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 
 // A wait of a whole warp, whose outcome is the same for all its lanes. Bounded by the
-// clock like the other kernels', which is read only every 65536 tries: the waits here are
-// many and mostly shorter than its reading. (A role may wait for as long as one item
-// takes, about 14 ms a million tokens.)
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* err,
+// clock like the other kernels', which is read, with the abort flag, only every kLook
+// tries: the waits here are many and mostly shorter than the reading. (A role may wait for
+// as long as one item takes, about 14 ms a million tokens.)
+constexpr uint32_t kLook = 256;
+enum { kSiteRaw = 0x503 };   // the converters' wait for int8 keys or values
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile Watch* watch, unsigned* err,
                                          unsigned site) {
   uint64_t t0 = 0;
 #pragma unroll 1
   for (uint32_t i = 1;; ++i) {
     if (__all_sync(~0u, mbar_try_wait(bar, parity))) return true;
-    if ((i & 0xffff) == 0) {
+    if (i % kLook == 0) {
+      if (__any_sync(~0u, watch->abort != 0)) return false;
       const uint64_t now = globaltimer_ns();
       if (t0 == 0) t0 = now;
-      if (__any_sync(~0u, now - t0 > kWaitLimitNs)) {
+      if (__any_sync(~0u, now - t0 > (site == kSiteRaw ? watch->raw_limit : watch->limit))) {
         record_error(err, site);
-        *abort = 1;
+        watch->abort = 1;
       }
     }
-    if ((i & 255) == 0 && __any_sync(~0u, *abort != 0)) return false;
   }
 }
 
@@ -383,7 +390,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    sm.abort = 0;
+    const bool test = w.a.wait_ns && blockIdx.x == 0;
+    sm.watch = Watch{test ? 4 * w.a.wait_ns : kWaitLimitNs, test ? w.a.wait_ns : kWaitLimitNs, 0};
     for (int i = 0; i < kBlocks; ++i) sm.plain[i] = kv_scale(0);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&sm.full[i], 4);
@@ -418,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
   chain_wait();
 
   auto wait = [&](uint64_t* bar, uint32_t parity, unsigned site) -> bool {
-    return wait_for(bar, parity, &sm.abort, w.a.err, site);
+    return wait_for(bar, parity, &sm.watch, w.a.err, site);
   };
   // the CTA's runs in turn
   int run_slot = 0;
@@ -710,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
     while (ok && next_run(run)) {
 #pragma unroll 1
       do {
-        if (!(ok = wait(&sm.raw_full[from], from_phase, 0x503))) break;
+        if (!(ok = wait(&sm.raw_full[from], from_phase, kSiteRaw))) break;
         const Info& info = sm.info[pass % kInfo];
         last = info.last;
         const KvScale* scales = (value ? info.v : sm.plain) + token0 / kKvBlock;
@@ -902,10 +910,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
                   }
                 }
                 __syncwarp();
-                if (lane == 0)
+                const bool drop = w.a.wait_ns && blockIdx.x == 0 && copies == 0;   // (the test of the waits)
+                if (lane == 0 && !drop)
                   mbar_arrive_expect_tx(&sm.raw_full[stage], (uint32_t)__popc(here) * (kKvBlock * D));
                 __syncwarp();
-                if (mine)
+                if (mine && !drop)
                   bulk_load(smem_u32(sm.raw[stage]) + (lane % kBlocks) * (kKvBlock * D),
                             (kind ? w.a.cache.v : w.a.cache.k) + block * (kKvBlock * D), kKvBlock * D,
                             &sm.raw_full[stage]);
@@ -922,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
         }
       }
       // copies in flight end before the CTA does, whatever ended the loop
-      for (uint32_t i = copies > kRaw ? copies - kRaw : 0; i < copies; ++i)
+      for (uint32_t i = copies > kRaw ? copies - kRaw : w.a.wait_ns && blockIdx.x == 0; i < copies; ++i)
         mbar_wait(&sm.raw_full[i % kRaw], (i / kRaw) & 1, nullptr, w.a.err, 0x50e);
       __syncwarp();
     } else if (warp == 13) {

@@ -1947,9 +1947,10 @@ size_t qmm_kv_attention_workspace_bytes(int64_t rows, int64_t batch, int64_t q_h
                                 (int)std::min(max_tokens, rows), dtype == QMM_BF16);
 }
 
-qmm_status qmm_kv_attention(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const void* q, int dtype,
-                            int64_t q_row, int64_t q_head, int64_t q_heads, float scale, int causal,
-                            int64_t max_tokens, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+namespace {
+qmm_status kv_attention_impl(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const void* q, int dtype,
+                             int64_t q_row, int64_t q_head, int64_t q_heads, float scale, int causal, int64_t max_tokens,
+                             void* out, void* workspace, size_t workspace_bytes, void* stream, uint64_t wait_ns) {
   KvAttentionArgs a{};
   bool empty = false;
   if (!float_type(dtype)) return QMM_ERR_INVALID_ARG;
@@ -1980,11 +1981,29 @@ qmm_status qmm_kv_attention(const qmm_kv_cache* cache, const qmm_kv_batch* batch
   a.scale = scale;
   a.max_tokens = (int)max_tokens;
   a.workspace = workspace;
+  a.wait_ns = wait_ns;
   cudaGetLastError();
   const char* name = "none";
   return finish_launch(launch_kv_attention(a, (int)cache->head_dim, dtype == QMM_BF16,
                                            kv_vector(q, q_row, q_head, dtype), static_cast<cudaStream_t>(stream),
                                            &name), name);
+}
+}  // namespace
+
+qmm_status qmm_kv_attention(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const void* q, int dtype,
+                            int64_t q_row, int64_t q_head, int64_t q_heads, float scale, int causal,
+                            int64_t max_tokens, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  return kv_attention_impl(cache, batch, q, dtype, q_row, q_head, q_heads, scale, causal, max_tokens, out, workspace,
+                           workspace_bytes, stream, 0);
+}
+
+qmm_status qmm_test_kv_attention_stall(const qmm_kv_cache* cache, const qmm_kv_batch* batch, const void* q, int dtype,
+                                       int64_t q_row, int64_t q_head, int64_t q_heads, float scale, int causal,
+                                       int64_t max_tokens, void* out, void* workspace, size_t workspace_bytes,
+                                       uint64_t wait_limit_ns, void* stream) {
+  if (wait_limit_ns < 1000 || wait_limit_ns > 100000000ull) return QMM_ERR_INVALID_ARG;
+  return kv_attention_impl(cache, batch, q, dtype, q_row, q_head, q_heads, scale, causal, max_tokens, out, workspace,
+                           workspace_bytes, stream, wait_limit_ns);
 }
 
 }  // extern "C"
