@@ -676,7 +676,8 @@ qmm_status qmm_fp4_matmul(const void* a_packed, size_t a_bytes, int64_t M, const
  *  workspace         qmm_kv_attention_workspace_bytes of the same arguments, 16-byte
  *                    aligned; nothing in it has to survive a call, or to be zero
  * rows = 0 or batch = 0 launches nothing. QMM_ERR_UNSUPPORTED for another head_dim, page
- * or `rotated`; QMM_ERR_INVALID_ARG for a bad dtype, stride, null or unaligned pointer, out = q,
+ * or `rotated`; QMM_ERR_INVALID_ARG for a bad dtype, stride, null or unaligned pointer (k, v, q
+ * to an element, integers to 4 bytes), out = q,
  * short workspace, q_heads that kv_heads does not divide, starts = NULL with rows !=
  * batch, width * page or rows * q_heads beyond 2^31 - 1, batch beyond 2^29 - 1.
  */

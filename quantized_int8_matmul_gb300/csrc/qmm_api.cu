@@ -218,7 +218,8 @@ const char* kPackedMMI = "gemm_tc05_pair_f16ops_matmul_integer";
 const char* kTwoPassA8W8 = "f16_prepass+gemm_tc05_pair_f16ops_a8w8";
 const char* kTwoPassMMI = "f16_prepass+gemm_tc05_pair_f16ops_matmul_integer";
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) % 16) == 0; }
+bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+bool aligned16(const void* p) { return aligned(p, 16); }
 
 // Form (a) for large M on the SM-pair GEMM: the int8 weight converted once to
 // exact bf16 in a workspace, the activations' row sums (for a zero point), and
@@ -1848,6 +1849,7 @@ qmm_status kv_arguments(const qmm_kv_cache* c, const qmm_kv_batch* b, KvCacheArg
   if (c->pages > 0 && (!c->k || !c->v || !c->k_exp || !c->v_exp || !aligned16(c->k) || !aligned16(c->v)))
     return QMM_ERR_INVALID_ARG;
   if (!b->lengths || (b->width > 0 && !b->table)) return QMM_ERR_INVALID_ARG;
+  if (!aligned(b->table, 4) || !aligned(b->lengths, 4) || !aligned(b->starts, 4)) return QMM_ERR_INVALID_ARG;
   ca->k = c->k;
   ca->v = c->v;
   ca->ke = c->k_exp;
@@ -1865,6 +1867,7 @@ qmm_status kv_arguments(const qmm_kv_cache* c, const qmm_kv_batch* b, KvCacheArg
   return QMM_OK;
 }
 
+size_t kv_element(int dtype) { return dtype == QMM_BF16 ? 2 : 4; }
 // Rows and heads of a strided operand on 16 bytes.
 bool kv_vector(const void* p, int64_t row, int64_t head, int dtype) {
   const int64_t n = dtype == QMM_BF16 ? 8 : 4;
@@ -1892,6 +1895,8 @@ qmm_status qmm_kv_append(const qmm_kv_cache* cache, const qmm_kv_batch* batch, i
     return QMM_OK;
   }
   if (!k || !v || (q && (!q_out || !aligned16(q_out)))) return QMM_ERR_INVALID_ARG;
+  const size_t e = kv_element(dtype);
+  if (!aligned(k, e) || !aligned(v, e) || !aligned(q, e)) return QMM_ERR_INVALID_ARG;
   if (rotated && positions > 0 && (!cos || !sin || !aligned16(cos) || !aligned16(sin))) return QMM_ERR_INVALID_ARG;
   if (q && q == q_out && (q_row != q_heads * cache->head_dim || q_head != cache->head_dim)) return QMM_ERR_INVALID_ARG;
   a.k = k;
@@ -1965,7 +1970,7 @@ qmm_status kv_attention_impl(const qmm_kv_cache* cache, const qmm_kv_batch* batc
   }
   max_tokens = batch->starts ? std::min(max_tokens, batch->rows) : 1;   // (1 needs no more of the workspace than any other)
   // (a row of q is read by several CTAs, some of which are done before others begin)
-  if (!q || !out || out == q || !aligned16(out)) return QMM_ERR_INVALID_ARG;
+  if (!q || !out || out == q || !aligned16(out) || !aligned(q, kv_element(dtype))) return QMM_ERR_INVALID_ARG;
   if (!workspace || !aligned16(workspace) ||
       workspace_bytes < qmm_kv_attention_workspace_bytes(batch->rows, batch->batch, q_heads, cache->kv_heads,
                                                          cache->head_dim, dtype, max_tokens))
