@@ -339,12 +339,12 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_rows_kernel(const
               float2* const mine = state + 8 * nt + 2 * t + c;
               const float2 held = *mine;
               KvUnit u{m[nt][c], settled ? 0.f : held.x, settled ? was : __float_as_int(held.y)};
-              const float scale = exp2_approx(kv_change_units(u, l[nt][c], top, largest, window));
+              const KvFactor f = kv_change_units(u, l[nt][c], top, largest, window);
               m[nt][c] = u.m;
 #pragma unroll
               for (int i = 0; i < kMT; ++i) {
-                o[i][nt][c] *= scale;
-                o[i][nt][c + 2] *= scale;
+                o[i][nt][c] = o[i][nt][c] * f.a * f.b;
+                o[i][nt][c + 2] = o[i][nt][c + 2] * f.a * f.b;
               }
               now_settled &= u.m == kKvNone || (u.window == window && u.behind == 0.f);
               sc[nt][c] += fmaxf(u.behind - kKvFar, 0.f);

@@ -371,10 +371,14 @@ struct KvUnit {
 // P and l of a row far above its scores: P is 0 in fp16 2^40 above them; no further than this, so that float32 still
 // holds what l takes from it.
 constexpr float kKvFar = 100.f;
+// A factor to O, of which one float32 holds half the range.
+struct KvFactor {
+  float a, b;   // b: 1 but for factors below 2^-126
+};
 // The row comes to scores of which the largest is top (-inf: it sees none of them), with
-// values in `window`. `largest`: of its O, in magnitude. Returns log2 of the factor to O;
-// l is taken to its unit here.
-__device__ __forceinline__ float kv_change_units(KvUnit& u, float& l, float top, float largest, int window) {
+// values in `window`. `largest`: of its O, in magnitude. Returns the factor to O; l is
+// taken to its unit here.
+__device__ __forceinline__ KvFactor kv_change_units(KvUnit& u, float& l, float top, float largest, int window) {
   const float most = u.m - u.behind, unit = fmaxf(most, top);   // of l: before, after
   if (top > most) l *= exp2_approx(most - top);
   float up = fmaxf(u.m, top), shift = u.m - up;
@@ -393,7 +397,8 @@ __device__ __forceinline__ float kv_change_units(KvUnit& u, float& l, float top,
     u.behind = up - unit;
   }
   u.m = up;
-  return shift;
+  const float held = fmaxf(shift, -126.f);
+  return {exp2_approx(held), exp2_approx(shift - held)};
 }
 
 // Two int8, biased by 128, to two fp16: bytes 0 and 1 of u, or 2 and 3. The byte becomes

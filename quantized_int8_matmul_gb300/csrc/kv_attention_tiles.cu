@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
                 for (int e = 0; e < 16; ++e) largest = fmaxf(largest, fabsf(__uint_as_float(o[e])));
               }
             }
-            const float scale = exp2_approx(kv_change_units(unit, l, top, largest, window));
+            const KvFactor by_units = kv_change_units(unit, l, top, largest, window);
             above = unit.m - fmaxf(unit.behind, 0.f) + kKvSlack;
             if (j > 0) {
 #pragma unroll 1
@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
                 uint32_t o[16];
                 tmem_ld16(o_tmem + i, o);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scale);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * by_units.a * by_units.b);
                 tmem_st16(o_tmem + i, o);
               }
             }

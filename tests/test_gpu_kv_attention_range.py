@@ -113,3 +113,28 @@ def test_an_infinity_among_the_values(q, kind, seqs, group, kernel, dim):  # noq
         exact, mag, top, seen = ko.attention(x.astype(np.float64), *arrays, b.table, b.lengths, starts, dim ** -0.5, True,
                                              detail=True)
         assert_attention(y.double().cpu().numpy(), exact, attention_bound(exact, mag, top, seen, kind, dim))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("few", [True, False])
+@pytest.mark.parametrize("second", [4.0, 7.0, 8.0, 9.0])
+def test_windows_that_come_back(q, kind, few, second):  # noqa: F811
+    """Values, then blocks of zeros with scores 28 below, then values with scores above the first ones': what the first
+    ones leave has to come through both changes."""
+    size = 16 if few else 128                         # tokens of each of the three
+    seqs = [(1, 3 * size)] * 300 if few else [(96, 3 * size), (100, 3 * size)]
+    b = Batch(seqs, 8 if few else 2, 64, 16, seed=18)
+    b.ke[:], b.ve[:] = 120, 118
+    b.kc[..., 0] = 0
+    for s in range(len(seqs)):
+        for i in range(3 * size // 16):
+            part = i * 16 // size
+            b.kc[b.table[s, i], :, :, 0] = (0, -127, round(127 * second / 28))[part]
+            v = b.vc[b.table[s, i]]
+            v[:] = (np.abs(v) // 4 + 95, 0 * v, v // 16)[part]
+            if part == 1:
+                b.ve[b.table[s, i]] = 0
+    group = 1 if few else 4
+    x = b.rng.standard_normal((b.rows, b.heads * group, 64)) * 0.1
+    x[..., 0] = 28 * 8 * 128 / 127
+    run(q, b, kind, group, causal=False, x=rounded(x, kind), max_tokens=max(n for n, _ in seqs))
