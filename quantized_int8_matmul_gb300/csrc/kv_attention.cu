@@ -318,10 +318,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_rows_kernel(const
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 4; ++c) over |= sc[nt][c] > m[nt][c & 1] + kKvSlack;
-        const bool moved = !kv_in_window(ve, window);
+        const bool moved = !kv_in_window(ve, window, kKvBelow<T>);
         const bool first = window == kKvNoWindow;
         const int was = window;
-        if (moved) window = kv_window(ve, ve);
+        if (moved) window = kv_window(ve, ve, kKvBelow<T>);
         if (!first && (moved || !settled)) {
           bool now_settled = true;
 #pragma unroll

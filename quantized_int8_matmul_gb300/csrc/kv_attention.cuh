@@ -337,28 +337,39 @@ __device__ __forceinline__ uint32_t half_rest(float a, float b, uint32_t pair) {
   const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&pair));
   return half_pair(a - h.x, b - h.y);
 }
-// The values' powers of two. P, in fp16, has no digits to spare for them: times 2^30 for a
-// block that a row hardly sees, or does not see, the P of all that it does see would be
-// zeros. The fp16 that an int8 of V becomes has: int8 * 2^(byte - window) is exact for
-// bytes from 24 below the window's to 5 above, and costs nothing (kv_widen). A window
-// holds for as long as the bytes stay within; blocks within 2^29 of each other can all be
-// in one. Where they are not, the window moves, and a row that takes part in a block of
-// another window has its O rescaled from unit to unit. Rows that see nothing of the block
-// are left alone: what they add, 0 * V, is 0 in any unit.
-constexpr int kKvBelow = 24, kKvAbove = 5, kKvNoWindow = -1000;
-__host__ __device__ constexpr bool kv_in_window(int byte, int window) {
-  return byte >= window - kKvBelow && byte <= window + kKvAbove;
+// The values' powers of two. P, in fp16, has few digits to spare for them: times 2^30 for
+// a block that a row hardly sees, or does not see, the P of all that it does see would
+// be zeros. So they go into the fp16 that an int8 of V becomes, at no cost (kv_widen):
+// int8 * 2^(byte - window), exactly, for bytes from `below` under the window's to kKvAbove
+// over it. A window holds for as long as the bytes stay within. Where they do not, it
+// moves, and a row that takes part in a block of another window has its O rescaled from
+// unit to unit. Rows that see nothing of the block are left alone: what they add, 0 * V, is
+// 0 in any unit.
+// P is held by the row's largest score, not by its largest score * value, which may be as
+// much smaller as a window is wide: of the 31 binades that it has below 2^7, bfloat16's
+// leaves 13 to the digits of what weighs most, float32's 21.
+constexpr int kKvAbove = 5, kKvNoWindow = -1000;
+template <typename T>
+constexpr int kKvBelow = sizeof(T) == 4 ? 5 : 13;
+__host__ __device__ constexpr bool kv_in_window(int byte, int window, int below) {
+  return byte >= window - below && byte <= window + kKvAbove;
 }
-// The window around bytes lo .. hi, which are no further apart than it holds. (Between 24 and 250, 2^(window - 127) is
+// The window around bytes lo .. hi, which are no further apart than it holds. (Between 1 and 250, 2^(window - 127) is
 // a normal number, and bytes 0 and 255 are still within.)
-__host__ __device__ constexpr int kv_window(int lo, int hi) {
-  const int w = (lo + hi + kKvBelow - kKvAbove + 1) / 2;
-  return w < 24 ? 24 : w > 250 ? 250 : w;
+__host__ __device__ constexpr int kv_window(int lo, int hi, int below) {
+  const int w = (lo + hi + below - kKvAbove + 1) / 2;
+  return w < 1 ? 1 : w > 250 ? 250 : w;
 }
-static_assert(kv_in_window(0, kv_window(0, 0)) && kv_in_window(255, kv_window(255, 255)) &&
-                  kv_in_window(100, kv_window(100, 129)) && kv_in_window(129, kv_window(100, 129)) &&
-                  kv_in_window(226, kv_window(226, 255)) && kv_in_window(29, kv_window(0, 29)),
-              "a window holds what it was made for");
+template <int below>
+constexpr bool kKvWindowHolds = kv_in_window(0, kv_window(0, 0, below), below) &&
+                                kv_in_window(255, kv_window(255, 255, below), below) &&
+                                kv_in_window(0, kv_window(0, below + 5, below), below) &&
+                                kv_in_window(below + 5, kv_window(0, below + 5, below), below) &&
+                                kv_in_window(101, kv_window(101, 106 + below, below), below) &&
+                                kv_in_window(106 + below, kv_window(101, 106 + below, below), below) &&
+                                kv_in_window(250 - below, kv_window(250 - below, 255, below), below) &&
+                                kv_in_window(255, kv_window(250 - below, 255, below), below);
+static_assert(kKvWindowHolds<5> && kKvWindowHolds<13>, "a window holds what it was made for");
 
 // A row's units: P is held in 2^m, O in 2^(m + window), the sum l in 2^(m - behind), that
 // is by the largest score so far. behind is 0 but where windows moved: below 0 for a block
@@ -383,7 +394,7 @@ __device__ __forceinline__ KvFactor kv_change_units(KvUnit& u, float& l, float t
   if (top > most) l *= exp2_approx(most - top);
   float up = fmaxf(u.m, top), shift = u.m - up;
   if (top > -INFINITY && u.window != window) {
-    up = top > unit - 16.f ? unit : top;
+    up = top > unit - 2.f ? unit : top;
     shift = 0.f;
     if (largest > 0.f) {
       const float moves = (float)(u.window - window);
@@ -415,13 +426,12 @@ __device__ __forceinline__ uint32_t bytes_high(uint32_t u) {
   const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&l), bias);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// The same times 2^s, s from -kKvBelow to kKvAbove, exactly: (1152 + int8) * 2^s - 1152 * 2^s in one operation.
+// The same times 2^s, s from -14 to kKvAbove, exactly: (1152 + int8) * 2^s - 1152 * 2^s in one operation.
 struct alignas(8) KvScale {
   uint32_t factor, bias;   // fp16 pairs: 2^s, -1152 * 2^s
 };
 __device__ __forceinline__ KvScale kv_scale(int s) {
-  const uint32_t f = s >= -14 ? (uint32_t)(s + 15) << 10 : 1u << (s + 24);   // (subnormal below 2^-14)
-  return {f * 0x10001u, (0x8080u + ((uint32_t)(s + 25) << 10)) * 0x10001u};
+  return {((uint32_t)(s + 15) << 10) * 0x10001u, (0x8080u + ((uint32_t)(s + 25) << 10)) * 0x10001u};
 }
 __device__ __forceinline__ uint32_t kv_widen(uint32_t biased, KvScale k) {
   const __half2 h = __hfma2(*reinterpret_cast<const __half2*>(&biased), *reinterpret_cast<const __half2*>(&k.factor),

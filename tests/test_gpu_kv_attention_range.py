@@ -138,3 +138,40 @@ def test_windows_that_come_back(q, kind, few, second):  # noqa: F811
     x = b.rng.standard_normal((b.rows, b.heads * group, 64)) * 0.1
     x[..., 0] = 28 * 8 * 128 / 127
     run(q, b, kind, group, causal=False, x=rounded(x, kind), max_tokens=max(n for n, _ in seqs))
+
+@each
+@pytest.mark.parametrize("sharp", [3, 10])
+def test_blocks_of_zeros_among_sharp_scores(q, kind, seqs, group, kernel, sharp):  # noqa: F811
+    """Scores tens apart: what is left of a row where the zeros have most of its weight, and window after window of
+    values with next to none. (No other value is 0: an element has something of every block.)"""
+    for dim in (64, 128):
+        for often in (0.1, 0.5):
+            b = Batch(seqs, 2, dim, 32, seed=17)
+            b.ke[:] = 121
+            b.vc[b.vc == 0] = 1
+            b.ve[:] = b.rng.integers(117, 121, b.ve.shape)
+            zero = b.rng.random(b.ve.shape) < often
+            b.ve[zero] = 0
+            b.vc[np.repeat(zero, 16, axis=2)] = 0
+            x = rounded(b.rng.standard_normal((b.rows, 2 * group, dim)) * sharp, kind)
+            run(q, b, kind, group, kernel=kernel, x=x, max_tokens=max(n for n, _ in seqs))
+
+
+@each
+@pytest.mark.parametrize("drop", [4, 9, 14, 18, 22])
+def test_values_as_large_as_their_weights_are_small(q, kind, seqs, group, kernel, drop):  # noqa: F811
+    """One block's scores lie `drop` below the others', and its values above them by as much, by less and by more: what
+    weighs most in the row is held by digits of its own."""
+    for gap in sorted({round(drop * 1.4427) + d for d in (-8, -2, 0, 3, 7)}):
+        b = Batch(seqs, 2, 64, 32, seed=19)
+        b.ke[:] = 120
+        b.kc[..., 0] = 0
+        b.vc[b.vc == 0] = 1
+        per = b.page // 16
+        set_bytes(b, b.ve, lambda s, i: 118 + gap * (i == 2))
+        for s in range(len(seqs)):
+            o = 2 % per * 16
+            b.kc[b.table[s, 2 // per], :, o:o + 16, 0] = -round(127 * drop / 25)
+        x = b.rng.standard_normal((b.rows, 2 * group, 64)) * 0.2
+        x[..., 0] = 25 * 8 * 128 / 127
+        run(q, b, kind, group, kernel=kernel, x=rounded(x, kind), max_tokens=max(n for n, _ in seqs))
