@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_attention_rows_kernel(const
         const bool moved = !kv_in_window(ve, window, kKvBelow<T>);
         const bool first = window == kKvNoWindow;
         const int was = window;
-        if (moved) window = kv_window(ve, ve, kKvBelow<T>);
+        if (moved) window = kv_move_window(window, ve, ve, kKvBelow<T>);
         if (!first && (moved || !settled)) {
           bool now_settled = true;
 #pragma unroll

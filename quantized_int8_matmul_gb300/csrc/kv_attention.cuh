@@ -360,6 +360,13 @@ __host__ __device__ constexpr int kv_window(int lo, int hi, int below) {
   const int w = (lo + hi + below - kKvAbove + 1) / 2;
   return w < 1 ? 1 : w > 250 ? 250 : w;
 }
+// The window that holds lo .. hi and is next to the one that there is, so that windows of a sequence settle.
+__host__ __device__ constexpr int kv_move_window(int window, int lo, int hi, int below) {
+  return window == kKvNoWindow      ? kv_window(lo, hi, below)
+         : window < hi - kKvAbove   ? hi - kKvAbove
+         : window > lo + below      ? lo + below
+                                    : window;
+}
 template <int below>
 constexpr bool kKvWindowHolds = kv_in_window(0, kv_window(0, 0, below), below) &&
                                 kv_in_window(255, kv_window(255, 255, below), below) &&

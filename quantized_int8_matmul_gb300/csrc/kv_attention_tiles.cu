@@ -879,11 +879,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(const K
             unsigned pending = there & (((1u << kBlocks) - 1) << ((j - j0) * kBlocks));   // the tile's lanes
             do {
               unsigned here = __ballot_sync(~0u, kv_in_window(ve, window, kKvBelow<T>)) & pending;
-              if (!here && pending) {
+              if (here != pending) {
                 const bool open = pending >> lane & 1;
                 const int lo = __reduce_min_sync(~0u, open ? ve : INT_MAX), hi = __reduce_max_sync(~0u, open ? ve : 0);
-                window = kv_window(lo, min(hi, lo + kKvBelow<T> + kKvAbove), kKvBelow<T>);
-                here = __ballot_sync(~0u, kv_in_window(ve, window, kKvBelow<T>)) & pending;
+                constexpr int kWidth = kKvBelow<T> + kKvAbove;
+                if (hi - lo <= kWidth || !here) {
+                  window = kv_move_window(window, lo, min(hi, lo + kWidth), kKvBelow<T>);
+                  here = __ballot_sync(~0u, kv_in_window(ve, window, kKvBelow<T>)) & pending;
+                }
               }
               pending &= ~here;
               const bool mine = here >> lane & 1;
