@@ -656,7 +656,8 @@ qmm_status qmm_fp4_matmul(const void* a_packed, size_t a_bytes, int64_t M, const
  *                    the smallest for which its largest magnitude rounds to 127 or
  *                    less, and no smaller than it was while the block holds earlier
  *                    tokens of the sequence; numbers are rounded to nearest even. A NaN
- *                    is stored as 0, an infinity as the largest float32. q [rows,
+ *                    is stored as 0, an infinity as the largest float32 (64 * 2^122,
+ *                    which reads back as an infinity). q [rows,
  *                    q_heads, head_dim], where not NULL, is rotated the same way into
  *                    q_out (contiguous, dtype; may be q where that is contiguous). At a
  *                    position without a row of cos and sin what is rotated is NaN.
@@ -667,8 +668,13 @@ qmm_status qmm_fp4_matmul(const void* a_packed, size_t a_bytes, int64_t M, const
  *                    position with causal = 1, all lengths[b] with causal = 0 (states of
  *                    an encoder, whose number has nothing to do with the rows). Query
  *                    head h reads key head h / (q_heads / kv_heads). Sums and maxima in
- *                    float32. A row that sees nothing gets zeros, one whose q holds a
- *                    NaN or an infinity NaN. out [rows, q_heads, head_dim] contiguous,
+ *                    float32; a weight, p_j over the row's largest, in fp16 (for float32
+ *                    in two parts): off by 2^-11 (2^-21) of itself, or by 2^-31 where that
+ *                    is more. Values of very different scales in one sequence do not take
+ *                    from each other's weights; float32 rows that see values more than
+ *                    about 2^100 apart have fewer digits of the smaller. A row that sees
+ *                    nothing gets zeros, one whose q holds a NaN or an infinity, or whose
+ *                    scores leave float32's range, NaN. out [rows, q_heads, head_dim] contiguous,
  *                    of q's dtype, not overlapping q (out = q is refused). max_tokens:
  *                    no sequence has more rows, as far as the caller knows; it chooses
  *                    kernels and splits, never results' validity (rows: always true;

@@ -23,13 +23,16 @@
 // by cp.async 512 contiguous bytes at a time (where a lane copied just the bytes that it
 // reads itself, in runs of 64 and 128, the long sequence took 68 us in place of 58).
 //
-// The running maximum moves only when some score is 8 (a factor of 256) above it,
-// which a vote finds out: P keeps six more bits below fp16's largest value and 30 bits
-// to its smallest. V's powers of two go into its fp16 (kv_attention.cuh).
+// The running maximum moves only when some score is 8 (a factor of 256) above it, which a
+// vote finds out. P is held times 2^6, at most 2^14, and fp16 ends 30 binades below that 2^6.
+// V's powers of two go into V's own fp16 (the windows of kv_attention.cuh). A block outside
+// of the window takes a path of its own, which ends when all rows are in one unit again:
+// 64 sequences of 8192 tokens take 190 us with equal bytes or bytes within a window, 205 with
+// bytes anywhere in 40 binades (float32 203 and 244).
 //
 // Measured, with the join: 64 sequences of up to 16384 tokens, 64 query heads on 8 of
-// 128, 114 us (6.0 TB/s, 89 % of a copy; the copies without arithmetic take as long); one
-// of 131072 54 us; one of 1021 9.8 us, a chain of latencies.
+// 128, 117 us (5.9 TB/s, 87 % of a copy; the copies without arithmetic took 114); one of
+// 131072 54 us; one of 1021 9.7 us, a chain of latencies.
 #include "kv_attention.cuh"
 
 namespace qmm {
@@ -541,7 +544,8 @@ int row_tiles(int group, int max_tokens) { return (long long)group * max_tokens 
 // or not, and one of float32, alone on its SM, takes as long as about two of the rows
 // kernel's of 16 (8 tokens of 4 heads over 32000 there, 12 here: 51 us both). For
 // bfloat16 two tiles of 16 rows are slower on long caches (64 sequences of up to 16384
-// with 24 rows each: 277 us, 247 here), if faster on short ones (one of 1021: 13 us, 23).
+// with 24 rows each: 277 us, 247 there), if faster on short ones (one of 1021: 13 us, 23):
+// a choice by rows alone, because lengths are on the device.
 // A call whose sequences all have max_tokens rows needs one kernel.
 int few_rows(bool bf16) { return bf16 ? 16 : 32; }
 struct Plan {

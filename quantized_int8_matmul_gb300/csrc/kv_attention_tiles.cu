@@ -27,12 +27,14 @@
 // Float32 queries take one tile of 128 rows: Q in two fp16 parts (22 bits) fills both
 // tiles' places, P in two parts all the columns of S, and either product runs twice.
 //
-// Measured: a prompt of 8192 tokens, 32 query heads on 8 of 128, 435 us (1263 TFLOP/s),
-// float32 1247 us; 8192 x 8192 not causal 775 us (1420); 500 tokens over 32000 200 us
+// Measured: a prompt of 8192 tokens, 32 query heads on 8 of 128, 435 us (1264 TFLOP/s),
+// float32 1255 us; 8192 x 8192 not causal 772 us (1424); 500 tokens over 32000 200 us
 // (1300). A tile of 256 x 128 takes about 3200 cycles: its MMAs 2080, its traffic in shared
 // memory (320 KB: Q and K 128, V 64, copies and conversion 128) 2560, one tile's softmax
 // 1500. Sixteen softmax warps with half a row each, and taking half of P before the maximum
-// is known, were slower (853 and 889 us where this took 798).
+// is known, were slower (853 and 889 us where this took 798). Windows: a prompt of 4096 143
+// us with equal bytes, 145 with bytes within a window, 203 with a block of zeros in a
+// hundred, 492 with bytes anywhere in 40 binades (float32 369, 369, 442, 1608).
 #include "kv_attention.cuh"
 
 namespace qmm {
@@ -51,7 +53,9 @@ constexpr int kStages = 3;                 // operands (K or V tiles) in the rin
 constexpr int kRaw = 4;                    // and in the ring of int8 before it
 constexpr int kInfo = 4;                   // passes whose scales are kept
 constexpr int kBlocks = kTokens / kKvBlock;
-constexpr int kSetup = 5;                  // units that stand for what an item costs beside its tiles
+// Units that stand for what an item costs beside its tiles. Chosen on a prompt of bfloat16 and 128 columns; 64 columns
+// and float32, whose items and tiles cost others, have not been measured for it.
+constexpr int kSetup = 5;
 constexpr int kMinUnits = kSetup + 2;      // a CTA's share, at least
 constexpr float kLift = 7.f;               // P is held times 2^7: at most 2^15
 // Sums of D <= 128 products of fp16 below 2^15 and int8 are below 2^29: with factors up to this scores stay below 2^20,
