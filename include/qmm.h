@@ -671,8 +671,8 @@ qmm_status qmm_fp4_matmul(const void* a_packed, size_t a_bytes, int64_t M, const
  *                    float32; a weight, p_j over the row's largest, in fp16 (for float32
  *                    in two parts): off by 2^-11 (2^-21) of itself, or by 2^-31 where that
  *                    is more. Values of very different scales in one sequence do not take
- *                    from each other's weights; float32 rows that see values more than
- *                    about 2^100 apart have fewer digits of the smaller. A row that sees
+ *                    from each other's weights; rows that see values more than about
+ *                    2^100 apart have fewer digits of the smaller. A row that sees
  *                    nothing gets zeros, one whose q holds a NaN or an infinity, or whose
  *                    scores leave float32's range, NaN. out [rows, q_heads, head_dim] contiguous,
  *                    of q's dtype, not overlapping q (out = q is refused). max_tokens:
